@@ -422,7 +422,7 @@ def _plain_sample(s):
     before = ordered.cumsum(-1) - ordered
     # the shortest prefix that holds top_p of what is left
     goal = (ordered.sum(-1, keepdim=True).double() * s["top_p"].clamp(0, 1).double()[:, None]).long().clamp(min=1)
-    ordered = ordered * (before < goal)
+    ordered = ordered * ((before < goal) | (s["top_p"] >= 1)[:, None])
     ordered = ordered * (ordered.double() >= s["min_p"].double()[:, None] * UNIT)
     kept = torch.zeros_like(mass).scatter_(1, order, ordered)
     total = kept.sum(-1, keepdim=True)
