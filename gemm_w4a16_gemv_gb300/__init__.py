@@ -12,6 +12,7 @@ Tensors: packed codes are ``torch.uint8``; scales and zero points
 """
 from __future__ import annotations
 
+import collections
 import ctypes
 import os
 import threading
@@ -26,6 +27,8 @@ __all__ = [
     "w4a16_linear", "w4a16_linear_array", "w4a16_linear_sequence", "w4a16_graph_create", "w4a16_graph_launch",
     "w4a16_linear_chain", "w4a16_linear_chain_scratch_bytes", "chain_scratch", "w4a16_linear_chain_noalloc",
     "w4a16_graph_destroy", "W4A16Graph",
+    "kv4_plan", "kv4_plan_buffers", "KV4Plan", "w4a16_qk_norm_rope", "kv4_append", "kv4_gather", "kv4_cache",
+    "kv4_attention", "kv4_attention_scratch", "kv4_attention_scratch_bytes", "w4a16_sample",
     "library_path", "W4A16Error", "STATUS", "FMT_INT4", "FMT_FP4",
     "OUT_F32", "OUT_BF16",
 ]
@@ -54,6 +57,7 @@ class w4a16_linear(ctypes.Structure):
 
 
 _OPS = ctypes.POINTER(w4a16_linear)
+_F = ctypes.c_float
 SIGNATURES = {
     "w4a16_gemv": ([_P, _P, _P, _P, _P, _I64, _I64, _INT, _P], _INT),
     "w4a16_gemm": ([_P, _P, _P, _P, _P, _I64, _I64, _I64, _INT, _P], _INT),
@@ -71,6 +75,16 @@ SIGNATURES = {
     "w4a16_graph_create": ([_OPS, _INT, _INT, ctypes.POINTER(ctypes.c_void_p)], _INT),
     "w4a16_graph_launch": ([_P, _P], _INT),
     "w4a16_graph_destroy": ([_P], _INT),
+    "kv4_plan": ([_P, _P, _INT, _P, _I64, _P, _I64, _INT, _I64, _P, _P, _P, _P, _P, _P], _INT),
+    "w4a16_qk_norm_rope": ([_P, _I64, _P, _I64, _P, _P, _P, _I64, _INT, _P, _P, _P, _I64, _INT, _INT, _INT, _F, _F,
+                            _INT, _P], _INT),
+    "kv4_append": ([_P, _I64, _P, _I64, _P, _I64, _P, _P, _P, _I64, _INT, _P, _P, _P, _P, _I64, _INT, _I64, _INT,
+                    _INT, _INT, _F, _F, _INT, _P], _INT),
+    "kv4_gather": ([_P, _I64, _INT, _P, _P, _P, _I64, _INT, _INT, _P], _INT),
+    "kv4_attention_scratch_bytes": ([_INT, _INT, _INT], _I64),
+    "kv4_attention": ([_P, _I64, _P, _I64, _INT, _P, _I64, _P, _P, _INT, _P, _I64, _INT, _INT, _INT, _F, _I64, _I64,
+                       _I64, _P, _I64, _P], _INT),
+    "w4a16_sample": ([_P, _INT, _I64, _I64, _I64, _P, _P, _P, _P, _P, _P, _P], _INT),
     "w4a16_check_device_error": ([_P], _INT),
     "w4a16_debug_inject": ([ctypes.c_uint], _INT),
     "w4a16_last_error_string": ([], ctypes.c_char_p),
@@ -437,6 +451,245 @@ def w4a16_copy(dst: torch.Tensor, src: torch.Tensor, stream=None, device=None) -
         _check(lib().w4a16_copy(ctypes.c_void_p(dst.data_ptr()), ctypes.c_void_p(src.data_ptr()), nbytes,
                                 _stream(stream, dev)))
     return dst
+
+
+# --------------------------------------------- the step around the linears
+
+def _ptr(t, name, dtype, device, numel=None):
+    """Address of an optional contiguous tensor (None: a null pointer)."""
+    if t is None:
+        return None
+    if not isinstance(t, torch.Tensor):
+        raise TypeError("%s must be a torch.Tensor" % name)
+    if t.dtype != dtype:
+        raise TypeError("%s must be %s, got %s" % (name, dtype, t.dtype))
+    if t.device != device:
+        raise ValueError("%s is on %s, expected %s" % (name, t.device, device))
+    if not t.is_contiguous():
+        raise ValueError("%s must be contiguous" % name)
+    if numel is not None and t.numel() != numel:
+        raise ValueError("%s has %d elements, expected %d" % (name, t.numel(), numel))
+    return t.data_ptr()
+
+
+def _rows(t, name, device):
+    """Address and token stride of [T, heads, D] bfloat16 rows: heads and
+    elements contiguous, tokens any stride (a slice of a fused row)."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError("%s must be a torch.Tensor" % name)
+    if t.dtype != torch.bfloat16:
+        raise TypeError("%s must be torch.bfloat16, got %s" % (name, t.dtype))
+    if t.device != device:
+        raise ValueError("%s is on %s, expected %s" % (name, t.device, device))
+    if t.dim() != 3:
+        raise ValueError("%s must be [tokens, heads, D]" % name)
+    T, H, D = t.shape
+    a, b, c = t.stride()
+    if (c != 1 and D > 1) or (b != D and H > 1):
+        raise ValueError("%s: heads and elements must be contiguous" % name)
+    return t.data_ptr(), (a if T > 1 else H * D)
+
+
+def _on_device(device, fn, *args):
+    """Calls the library with `device` current (which it usually is)."""
+    if not device.type == "cuda":
+        raise ValueError("expected CUDA tensors, got %s" % device)
+    if torch.cuda.current_device() == device.index:
+        _check(fn(*args))
+    else:
+        with torch.cuda.device(device):
+            _check(fn(*args))
+
+
+KV4Plan = collections.namedtuple("KV4Plan", "seq_lens cu_new positions slots taken")
+
+
+def kv4_plan_buffers(requests: int, num_tokens: int, device=None) -> KV4Plan:
+    """Buffers for kv4_plan: `requests` requests, room for `num_tokens` new
+    tokens in a step."""
+    dev = torch.device(device if device is not None else "cuda")
+    i32 = dict(dtype=torch.int32, device=dev)
+    return KV4Plan(torch.empty(requests, **i32), torch.empty(requests + 1, **i32), torch.empty(num_tokens, **i32),
+                   torch.empty(num_tokens, dtype=torch.int64, device=dev), torch.empty(1, **i32))
+
+
+def kv4_plan(ctx_lens, new_lens, block_table, free_blocks, block_size: int, num_tokens=None, out=None, stream=None):
+    """Block tables and slot maps of a step: `ctx_lens` tokens held and
+    `new_lens` added by each request; `block_table` [requests, max_blocks]
+    gets the new blocks, from the front of `free_blocks`, written in.  Returns
+    KV4Plan(seq_lens, cu_new, positions, slots, taken), in `out` if given,
+    else new with room for `num_tokens` tokens."""
+    dev = ctx_lens.device
+    B = ctx_lens.numel()
+    if out is None:
+        if num_tokens is None:
+            raise ValueError("kv4_plan needs num_tokens or out")
+        out = kv4_plan_buffers(B, num_tokens, dev)
+    if block_table.dim() != 2 or block_table.shape[0] != B:
+        raise ValueError("block_table must be [%d, max_blocks]" % B)
+    T = out.positions.numel()
+    i32 = torch.int32
+    _on_device(dev, lib().kv4_plan, _ptr(ctx_lens, "ctx_lens", i32, dev), _ptr(new_lens, "new_lens", i32, dev, B), B,
+               _ptr(block_table, "block_table", i32, dev), block_table.shape[1],
+               _ptr(free_blocks, "free_blocks", i32, dev), free_blocks.numel(), block_size, T,
+               _ptr(out.seq_lens, "seq_lens", i32, dev, B), _ptr(out.cu_new, "cu_new", i32, dev, B + 1),
+               _ptr(out.positions, "positions", i32, dev), _ptr(out.slots, "slots", torch.int64, dev, T),
+               _ptr(out.taken, "taken", i32, dev, 1), _stream(stream, dev))
+    return out
+
+
+def _rope_args(dev, D, q_weight, k_weight, cos_sin, positions, T):
+    rows, rot = cos_sin.shape if cos_sin is not None else (0, 0)
+    if cos_sin is not None and positions is None:
+        raise ValueError("cos_sin needs positions")
+    return (_ptr(q_weight, "q_weight", torch.bfloat16, dev, D), _ptr(k_weight, "k_weight", torch.bfloat16, dev, D),
+            _ptr(cos_sin, "cos_sin", torch.float32, dev), rows, rot,
+            _ptr(positions, "positions", torch.int32, dev, T) if cos_sin is not None else None)
+
+
+def w4a16_qk_norm_rope(q, k, q_weight, k_weight, cos_sin, positions, q_out=None, k_out=None, eps: float = 1e-6,
+                       weight_offset: float = 0.0, interleaved: bool = False, stream=None):
+    """RMS norm and position rotation of every head of q [T, Hq, D] and
+    k [T, Hkv, D] (tokens may be strided) in one pass; weights [D] or None (no
+    norm), cos_sin float32 [positions, rot] or None (no rotation).  Returns
+    (q_out, k_out)."""
+    dev = q.device
+    T, Hq, D = q.shape
+    Hk = k.shape[1]
+    pq, sq = _rows(q, "q", dev)
+    pk, sk = _rows(k, "k", dev)
+    if k.shape[0] != T or k.shape[2] != D:
+        raise ValueError("k must be [%d, heads, %d]" % (T, D))
+    if q_out is None:
+        q_out = torch.empty(T, Hq, D, dtype=torch.bfloat16, device=dev)
+    if k_out is None:
+        k_out = torch.empty(T, Hk, D, dtype=torch.bfloat16, device=dev)
+    _on_device(dev, lib().w4a16_qk_norm_rope, pq, sq, pk, sk,
+               *_rope_args(dev, D, q_weight, k_weight, cos_sin, positions, T),
+               _ptr(q_out, "q_out", torch.bfloat16, dev, T * Hq * D),
+               _ptr(k_out, "k_out", torch.bfloat16, dev, T * Hk * D), T, Hq, Hk, D, eps, weight_offset,
+               1 if interleaved else 0, _stream(stream, dev))
+    return q_out, k_out
+
+
+def kv4_cache(num_blocks: int, Hkv: int, block_size: int, D: int, device=None) -> torch.Tensor:
+    """An empty 4-bit cache, uint8 [num_blocks, Hkv, block_size / 16, 18 D]."""
+    if block_size % 16 != 0:
+        raise ValueError("block_size %d is not a multiple of 16" % block_size)
+    return torch.zeros(num_blocks, Hkv, block_size // 16, 18 * D, dtype=torch.uint8,
+                       device=device if device is not None else "cuda")
+
+
+def _cache(cache, dev):
+    """Address, blocks, page size, heads and D of a cache tensor."""
+    p = _ptr(cache, "cache", torch.uint8, dev)
+    if cache.dim() != 4 or cache.shape[3] % 18 != 0:
+        raise ValueError("cache must be [num_blocks, Hkv, block_size / 16, 18 D]")
+    return p, cache.shape[0], cache.shape[2] * 16, cache.shape[1], cache.shape[3] // 18
+
+
+def kv4_append(k, v, cache, slots, q=None, q_weight=None, k_weight=None, cos_sin=None, positions=None, q_out=None,
+               eps: float = 1e-6, weight_offset: float = 0.0, interleaved: bool = False, stream=None):
+    """k and v [T, Hkv, D] quantised to 4 bits into `slots` of the cache; with
+    weights or cos_sin also norm and rotation of k, and of q [T, Hq, D] where
+    given, in the same pass.  Returns q_out (None without q)."""
+    dev = cache.device
+    pc, blocks, bs, Hkv, D = _cache(cache, dev)
+    T = k.shape[0]
+    pk, sk = _rows(k, "k", dev)
+    pv, sv = _rows(v, "v", dev)
+    for name, t in (("k", k), ("v", v)):
+        if tuple(t.shape) != (T, Hkv, D):
+            raise ValueError("%s must be [%d, %d, %d]" % (name, T, Hkv, D))
+    Hq, pq, sq, po = 0, None, 0, None
+    if q is not None:
+        Hq = q.shape[1]
+        pq, sq = _rows(q, "q", dev)
+        if q.shape[0] != T or q.shape[2] != D:
+            raise ValueError("q must be [%d, heads, %d]" % (T, D))
+        if q_out is None:
+            q_out = torch.empty(T, Hq, D, dtype=torch.bfloat16, device=dev)
+        po = _ptr(q_out, "q_out", torch.bfloat16, dev, T * Hq * D)
+    _on_device(dev, lib().kv4_append, pq, sq, pk, sk, pv, sv,
+               *_rope_args(dev, D, q_weight, k_weight, cos_sin, positions, T),
+               _ptr(slots, "slots", torch.int64, dev, T), po, pc, blocks, bs, T, Hq, Hkv, D, eps, weight_offset,
+               1 if interleaved else 0, _stream(stream, dev))
+    return q_out if q is not None else None
+
+
+def kv4_gather(cache, slots, k=None, v=None, stream=None):
+    """The values the cache holds at `slots`: (k, v) bfloat16 [T, Hkv, D]."""
+    dev = cache.device
+    pc, blocks, bs, Hkv, D = _cache(cache, dev)
+    T = slots.numel()
+    if k is None:
+        k = torch.empty(T, Hkv, D, dtype=torch.bfloat16, device=dev)
+    if v is None:
+        v = torch.empty(T, Hkv, D, dtype=torch.bfloat16, device=dev)
+    _on_device(dev, lib().kv4_gather, pc, blocks, bs, _ptr(slots, "slots", torch.int64, dev),
+               _ptr(k, "k", torch.bfloat16, dev, T * Hkv * D), _ptr(v, "v", torch.bfloat16, dev, T * Hkv * D), T, Hkv,
+               D, _stream(stream, dev))
+    return k, v
+
+
+def kv4_attention_scratch_bytes(Hq: int, Hkv: int, D: int) -> int:
+    """Bytes of scratch memory kv4_attention needs."""
+    return int(lib().kv4_attention_scratch_bytes(int(Hq), int(Hkv), int(D)))
+
+
+def kv4_attention_scratch(Hq: int, Hkv: int, D: int, device=None) -> torch.Tensor:
+    """A zeroed scratch buffer for kv4_attention, for calls on one stream."""
+    return torch.zeros(max(kv4_attention_scratch_bytes(Hq, Hkv, D), 1), dtype=torch.uint8,
+                       device=device if device is not None else "cuda")
+
+
+def kv4_attention(q, cache, block_table, seq_lens, cu_new, scratch, out=None, scale=None, window: int = 0,
+                  sinks: int = 0, max_new=None, stream=None):
+    """Attention of the new tokens q [T, Hq, D] over the 4-bit cache, causal
+    by position; window > 0: the last `window` tokens and the first `sinks`.
+    `max_new`: the most new tokens any request has (T when None); scale
+    1 / sqrt(D) when None; `scratch` from kv4_attention_scratch.  Returns
+    out bfloat16 [T, Hq, D]."""
+    dev = cache.device
+    pc, blocks, bs, Hkv, D = _cache(cache, dev)
+    pq, sq = _rows(q, "q", dev)
+    T, Hq, Dq = q.shape
+    if Dq != D:
+        raise ValueError("q has heads of %d, the cache of %d" % (Dq, D))
+    B = seq_lens.numel()
+    if block_table.dim() != 2 or block_table.shape[0] != B:
+        raise ValueError("block_table must be [%d, max_blocks]" % B)
+    if out is None:
+        out = torch.empty(T, Hq, D, dtype=torch.bfloat16, device=dev)
+    i32 = torch.int32
+    _on_device(dev, lib().kv4_attention, pq, sq, pc, blocks, bs, _ptr(block_table, "block_table", i32, dev),
+               block_table.shape[1], _ptr(seq_lens, "seq_lens", i32, dev), _ptr(cu_new, "cu_new", i32, dev, B + 1), B,
+               _ptr(out, "out", torch.bfloat16, dev, T * Hq * D), T, Hq, Hkv, D,
+               float(scale) if scale is not None else D ** -0.5, window, sinks,
+               int(max_new) if max_new is not None else max(T, 1), _ptr(scratch, "scratch", torch.uint8, dev),
+               scratch.numel(), _stream(stream, dev))
+    return out
+
+
+def w4a16_sample(logits, u, temperature=None, top_k=None, top_p=None, min_p=None, out=None, stream=None):
+    """One token (int32) for each row of logits [rows, vocab] (float32 or
+    bfloat16, rows may be strided) from the uniform numbers u [rows]; the
+    settings are per-row tensors or None (off)."""
+    dev = logits.device
+    if logits.dim() != 2 or (logits.stride(1) != 1 and logits.shape[1] > 1):
+        raise ValueError("logits must be [rows, vocab] with contiguous rows")
+    if logits.dtype not in (torch.float32, torch.bfloat16):
+        raise TypeError("logits must be torch.float32 or torch.bfloat16, got %s" % logits.dtype)
+    R, V = logits.shape
+    f32 = torch.float32
+    if out is None:
+        out = torch.empty(R, dtype=torch.int32, device=dev)
+    _on_device(dev, lib().w4a16_sample, logits.data_ptr(), OUT_F32 if logits.dtype == f32 else OUT_BF16,
+               logits.stride(0) if R > 1 else V, R, V, _ptr(u, "u", f32, dev, R),
+               _ptr(temperature, "temperature", f32, dev, R), _ptr(top_k, "top_k", torch.int32, dev, R),
+               _ptr(top_p, "top_p", f32, dev, R), _ptr(min_p, "min_p", f32, dev, R),
+               _ptr(out, "out", torch.int32, dev, R), _stream(stream, dev))
+    return out
 
 
 def w4a16_check_device_error(stream=None) -> int:

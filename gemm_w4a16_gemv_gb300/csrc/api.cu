@@ -10,8 +10,10 @@
 #include <new>
 
 #include "w4a16.h"
+#include "api_common.h"
 #include "common.cuh"
 #include "kernels.h"
+#include "kv4.cuh"
 
 namespace {
 
@@ -21,6 +23,10 @@ namespace {
 __device__ unsigned int g_status;
 
 thread_local char g_err[512] = "";
+
+}  // namespace
+
+namespace w4api {
 
 int fail(int code, const char *fmt, ...) {
     va_list ap;
@@ -35,7 +41,11 @@ int ok() {
     return W4A16_OK;
 }
 
-bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+}  // namespace w4api
+
+using namespace w4api;
+
+namespace {
 
 // Per-device state, filled once per device under a mutex (host threads may
 // make their first calls concurrently); after that it is read without a lock.
@@ -49,7 +59,7 @@ DevCache g_dev[64];
 std::mutex g_dev_mu;
 
 // Current device's info and status-word address (looked up once per device).
-int device_state(w4::DeviceInfo &info, unsigned int *&status, DevCache **cache = nullptr) {
+int device_cache(w4::DeviceInfo &info, unsigned int *&status, DevCache **cache) {
     int d = 0;
     cudaError_t e = cudaGetDevice(&d);
     if (e != cudaSuccess) return fail(W4A16_ERR_CUDA, "cudaGetDevice: %s", cudaGetErrorString(e));
@@ -77,6 +87,12 @@ int device_state(w4::DeviceInfo &info, unsigned int *&status, DevCache **cache =
     if (cache) *cache = &c;
     return W4A16_OK;
 }
+
+}  // namespace
+
+namespace w4api {
+
+int device_state(w4::DeviceInfo &info, unsigned int *&status) { return device_cache(info, status, nullptr); }
 
 // Every data pointer must be memory of the current device (the launches go
 // to the current device): device memory of that device, or managed memory.
@@ -107,6 +123,10 @@ int launched(cudaError_t e, const char *what) {
     if (e != cudaSuccess) return fail(W4A16_ERR_CUDA, "%s launch: %s", what, cudaGetErrorString(e));
     return ok();
 }
+
+}  // namespace w4api
+
+namespace {
 
 // Host checks of one INT4 linear, M = 1 (the GEMV's rules) or any M (the
 // GEMM's rules); `who` prefixes the message.
@@ -737,6 +757,8 @@ int w4a16_check_device_error(void *stream) {
     }
     if (v & w4::kDevTimeout) return fail(W4A16_ERR_TIMEOUT, "a device pipeline wait timed out");
     if (v & w4::kDevBadExpert) return fail(W4A16_ERR_DEVICE, "an expert id was outside [0, E)");
+    if (v & w4::kDevBadIndex)
+        return fail(W4A16_ERR_DEVICE, "a position, cache slot, block id or length was out of range");
     return ok();
 }
 
@@ -744,7 +766,7 @@ int w4a16_debug_inject(unsigned int flags) {
     w4::DeviceInfo dev;
     unsigned int *status;
     DevCache *c = nullptr;
-    if (int r = device_state(dev, status, &c)) return r;
+    if (int r = device_cache(dev, status, &c)) return r;
     if (flags & ~static_cast<unsigned int>(w4::kInjectStallPipeline | w4::kInjectStallConsumers))
         return fail(W4A16_ERR_INVALID_ARG, "unknown injection flags 0x%x", flags);
     // the flags travel as a kernel argument of later launches: the normal

@@ -117,4 +117,74 @@ cudaError_t launch_bf16_gemm(const uint16_t *X, const uint16_t *W, uint16_t *Y,
 // dereference, already translated and checked by the caller).
 cudaError_t launch_copy(void *dst, const void *src, int64_t bytes, cudaStream_t st, const DeviceInfo &dev);
 
+// ------------------------------------------- operators around the 4-bit cache
+// Sizes and layouts as the C header states them; block_size = 1 << bs_log2.
+
+struct Kv4PlanArgs {
+    const int32_t *ctx_lens, *new_lens;
+    int32_t *block_table;
+    const int32_t *free_blocks;
+    int32_t *seq_lens, *cu_new, *positions;
+    int64_t *slots;
+    int32_t *taken;
+    unsigned int *status;
+    int64_t max_blocks, num_free, num_tokens;
+    int requests, bs_log2;
+};
+cudaError_t launch_kv4_plan(const Kv4PlanArgs &a, cudaStream_t st, const DeviceInfo &dev);
+
+// Heads of q, k and v of every token in one pass; cache == nullptr: k goes to
+// k_out (and there is no v), else k and v go to the cache.
+struct Kv4RopeArgs {
+    const uint16_t *q, *k, *v;
+    int64_t q_stride, k_stride, v_stride;  // elements between tokens
+    const uint16_t *q_weight, *k_weight;
+    const float *cos_sin;
+    const int32_t *positions;
+    const int64_t *slots;
+    uint16_t *q_out, *k_out;
+    unsigned char *cache;
+    unsigned int *status;
+    int64_t T, num_slots, num_positions;
+    int Hq, Hk, Hv, rot, bs_log2, interleaved;
+    float eps, weight_offset;
+};
+cudaError_t launch_kv4_rope(const Kv4RopeArgs &a, int D, cudaStream_t st, const DeviceInfo &dev);
+
+struct Kv4GatherArgs {
+    const unsigned char *cache;
+    const int64_t *slots;
+    uint16_t *k, *v;
+    unsigned int *status;
+    int64_t T, num_slots;
+    int Hkv, bs_log2;
+};
+cudaError_t launch_kv4_gather(const Kv4GatherArgs &a, int D, cudaStream_t st, const DeviceInfo &dev);
+
+struct Kv4AttnArgs {
+    const uint16_t *q;
+    const unsigned char *cache;
+    const int32_t *block_table, *seq_lens, *cu_new;
+    uint16_t *out;
+    unsigned char *scratch;
+    unsigned int *status;
+    int64_t q_stride, num_blocks, max_blocks, T, window, sinks, max_new;
+    int requests, Hq, Hkv, bs_log2;
+    float scale;
+};
+int64_t kv4_attention_scratch(int Hq, int Hkv, int D);
+cudaError_t launch_kv4_attention(const Kv4AttnArgs &a, int D, cudaStream_t st, const DeviceInfo &dev);
+
+struct SampleArgs {
+    const void *logits;
+    const float *u, *temperature;
+    const int32_t *top_k;
+    const float *top_p, *min_p;
+    int32_t *tokens;
+    int64_t row_stride, rows;
+    int vocab;
+    bool bf16;
+};
+cudaError_t launch_sample(const SampleArgs &a, cudaStream_t st, const DeviceInfo &dev);
+
 }  // namespace w4

@@ -63,7 +63,7 @@ typedef enum {
     W4A16_ERR_MISALIGNED = 3,   /* a pointer is not 16-byte aligned           */
     W4A16_ERR_CUDA = 4,         /* a CUDA runtime call or launch failed       */
     W4A16_ERR_TIMEOUT = 5,      /* a device pipeline wait gave up             */
-    W4A16_ERR_DEVICE = 6        /* a device-side data error (bad expert id)   */
+    W4A16_ERR_DEVICE = 6        /* a device-side data error (bad id, slot...) */
 } w4a16_status;
 
 typedef enum { W4_FMT_INT4_ASYM = 0, W4_FMT_FP4_E2M1 = 1 } w4_format;
@@ -353,6 +353,185 @@ int w4a16_graph_create(const w4a16_linear *ops, int count, int group,
                        w4a16_graph_t *out);
 int w4a16_graph_launch(w4a16_graph_t graph, void *stream);
 int w4a16_graph_destroy(w4a16_graph_t graph);
+
+/*
+ * ---------------------------------------------------------------------------
+ * A decode step around the quantised linears: a paged key/value cache held in
+ * 4 bits, the attention that reads it, the head norms with the position
+ * rotation, and the choice of a token.
+ *
+ * The cache is one uint8 array [num_blocks, Hkv, block_size / 16, 18 * D]:
+ * each head's part of a page is a row of tiles of 16 tokens, a tile is
+ *   [0, 8 D)      codes of K [D / 64][16 tokens][32 bytes]: element 2 i of the
+ *                 64 in the low nibble of byte i, element 2 i + 1 in the high
+ *   [8 D, 16 D)   codes of V, the same
+ *   [16 D, 17 D)  binary16 pairs (scale, zero) of K [D / 64][16 tokens][2]
+ *   [17 D, 18 D)  the same of V
+ * and a value is (code - zero) * scale: one scale and zero per 64 elements of
+ * a token's head (D = 256: 288 bytes for a token's K and V of one head, where
+ * BF16 takes 1024).  A SLOT is block * block_size + offset: where a token
+ * lies.  block_size is 16, 32, 64, 128 or 256; D (head dimension) is 64, 128
+ * or 256.
+ *
+ * Values that cannot be checked on the host (lengths, block ids, slots,
+ * positions: device arrays) are checked by the kernels: what is out of range
+ * is neither read nor written through, and the device status is set
+ * (W4A16_ERR_DEVICE from w4a16_check_device_error).
+ * ---------------------------------------------------------------------------
+ */
+
+/*
+ * Block tables and slot maps of one step, from the requests' lengths.
+ * Request b holds ctx_lens[b] tokens in the cache and adds new_lens[b] (0: it
+ * sits the step out); its first ceil(ctx / block_size) table entries are
+ * valid.  The blocks that the requests still need are taken, in the order of
+ * the requests, from the front of free_blocks and entered in the table.
+ *   ctx_lens, new_lens : int32 [requests]
+ *   block_table : int32 [requests, max_blocks], only new entries are written
+ *   free_blocks : int32 [num_free] (may be NULL when num_free is 0)
+ *   seq_lens    : int32 [requests]      ctx + new
+ *   cu_new      : int32 [requests + 1]  running sum of new_lens
+ *   positions   : int32 [num_tokens]    position of each new token
+ *   slots       : int64 [num_tokens]    its slot in the cache
+ *   taken       : int32 [1]             blocks needed (the caller drops this
+ *                 many from the front of its free list)
+ * num_tokens is the capacity of positions and slots; entries past the step's
+ * tokens are -1 (kv4_append and w4a16_qk_norm_rope skip those), so a captured
+ * graph can be replayed with other lengths.  Too few free blocks: the missing
+ * entries and slots are -1 and the device status is set; so it is for a
+ * negative length, a request longer than its table row and more tokens than
+ * num_tokens.  One launch.  requests <= 8192, num_tokens <= 2^24.
+ */
+int kv4_plan(const int32_t *ctx_lens, const int32_t *new_lens, int requests,
+             int32_t *block_table, int64_t max_blocks,
+             const int32_t *free_blocks, int64_t num_free, int block_size,
+             int64_t num_tokens, int32_t *seq_lens, int32_t *cu_new,
+             int32_t *positions, int64_t *slots, int32_t *taken, void *stream);
+
+/*
+ * RMS norm of every query and key head with the position rotation in the same
+ * pass (binary32 inside, one rounding at the end):
+ *   y = x * rsqrt(mean(x^2) + eps) * (w + weight_offset)   over the D elements
+ *   (y_a, y_b) <- (y_a c - y_b s, y_b c + y_a s)           for rot / 2 pairs
+ * with pair i = (i, i + rot / 2), or (2 i, 2 i + 1) if `interleaved`; elements
+ * from rot on are not rotated.
+ *   q : bfloat16, T rows of Hq heads of D, q_stride elements apart (a slice of
+ *       a fused q|k|v row does); k : Hkv heads, k_stride apart.  Strides are
+ *       multiples of 8.  Hq or Hkv may be 0 (its pointers are not used).
+ *   q_weight, k_weight : bfloat16 [D], or NULL: no norm for those heads
+ *   cos_sin   : binary32 [num_positions, rot], rot / 2 cosines then rot / 2
+ *               sines, or NULL: no rotation (positions is not used)
+ *   positions : int32 [T]; a negative one marks a padding row: zeros are
+ *               written; one >= num_positions does the same and sets the
+ *               device status
+ *   q_out : bfloat16 [T, Hq, D];  k_out : bfloat16 [T, Hkv, D]
+ * rot: a multiple of 16, at most D.  T = 0 launches nothing.
+ * An output may be its own input's array when that is contiguous.
+ */
+int w4a16_qk_norm_rope(const uint16_t *q, int64_t q_stride, const uint16_t *k,
+                       int64_t k_stride, const uint16_t *q_weight,
+                       const uint16_t *k_weight, const float *cos_sin,
+                       int64_t num_positions, int rot,
+                       const int32_t *positions, uint16_t *q_out,
+                       uint16_t *k_out, int64_t T, int Hq, int Hkv, int D,
+                       float eps, float weight_offset, int interleaved,
+                       void *stream);
+
+/*
+ * Keys and values of T tokens into their slots of the cache, quantised to 4
+ * bits; with weights or cos_sin also the norm and the rotation of k, and of q
+ * where Hq > 0 (into q_out), in the same pass.  k enters the cache from its
+ * BF16 value, so this call equals w4a16_qk_norm_rope followed by a plain
+ * kv4_append bit for bit.  For each group of 64 elements x of a head:
+ *   s = fl16((max(x, 0) - min(x, 0)) / 15), at most 65504
+ *   z = rint(-min(x, 0) / s);  code = clamp(rint(x / s) + z, 0, 15)
+ * (s = 0: zero, code 0), divisions and sums in binary32, one by one.
+ *   v     : bfloat16, T rows of Hkv heads, v_stride elements apart
+ *   slots : int64 [T]; a negative one stores nothing; one past the cache
+ *           stores nothing and sets the device status.  Two tokens of a call
+ *           must not share a slot.
+ *   cache : uint8 [num_blocks, Hkv, block_size / 16, 18 D], 16-byte aligned
+ * The other arguments are those of w4a16_qk_norm_rope (Hq = 0: keys and
+ * values alone).
+ */
+int kv4_append(const uint16_t *q, int64_t q_stride, const uint16_t *k,
+               int64_t k_stride, const uint16_t *v, int64_t v_stride,
+               const uint16_t *q_weight, const uint16_t *k_weight,
+               const float *cos_sin, int64_t num_positions, int rot,
+               const int32_t *positions, const int64_t *slots, uint16_t *q_out,
+               uint8_t *cache, int64_t num_blocks, int block_size, int64_t T,
+               int Hq, int Hkv, int D, float eps, float weight_offset,
+               int interleaved, void *stream);
+
+/*
+ * The values that the cache holds at T slots: k, v bfloat16 [T, Hkv, D], each
+ * (code - zero) * scale rounded once.  A negative slot gives zeros; one past
+ * the cache gives zeros and sets the device status.
+ */
+int kv4_gather(const uint8_t *cache, int64_t num_blocks, int block_size,
+               const int64_t *slots, uint16_t *k, uint16_t *v, int64_t T,
+               int Hkv, int D, void *stream);
+
+/*
+ * Attention of the step's new tokens over the cache (their own keys and
+ * values are in it already).  Query token t of request b, that is cu_new[b]
+ * <= t < cu_new[b + 1], stands at position p = seq_lens[b] - cu_new[b + 1] + t
+ * and sees the keys at j <= p; with window > 0 of those only p - j < window
+ * or j < sinks (the first `sinks` tokens stay visible):
+ *   out[t, h] = sum_j softmax_j(scale * q[t, h] . K[j, h / (Hq / Hkv)]) V[j]
+ * A row that sees nothing (p < 0) is written as zeros.
+ *   q   : bfloat16, T rows of Hq heads of D, q_stride elements apart
+ *   out : bfloat16 [T, Hq, D];  rows past cu_new[requests] are zeros
+ *   block_table : int32 [requests, max_blocks]; a block id outside
+ *         [0, num_blocks) hides its tokens and sets the device status
+ *   max_new : an upper bound of the requests' new tokens that the caller
+ *         knows (1 in a decode step); it chooses between the kernels, and a
+ *         request with more is still answered
+ *   scratch : at least kv4_attention_scratch_bytes(Hq, Hkv, D) bytes, 256-byte
+ *         aligned, ALL ZERO before its first use; every call leaves it fit
+ *         for the next one.  Calls that may run at the same time need
+ *         separate scratch.
+ * K, V and the softmax's statistics and sums are binary32 or exact; the
+ * weights of the sum over V are rounded to binary16.
+ * Hq is a multiple of Hkv; requests <= 8192; T = 0 launches nothing.
+ */
+int64_t kv4_attention_scratch_bytes(int Hq, int Hkv, int D);
+int kv4_attention(const uint16_t *q, int64_t q_stride, const uint8_t *cache,
+                  int64_t num_blocks, int block_size,
+                  const int32_t *block_table, int64_t max_blocks,
+                  const int32_t *seq_lens, const int32_t *cu_new, int requests,
+                  uint16_t *out, int64_t T, int Hq, int Hkv, int D,
+                  float scale, int64_t window, int64_t sinks, int64_t max_new,
+                  void *scratch, int64_t scratch_bytes, void *stream);
+
+/*
+ * One token for each row of logits, from given uniform numbers.  Token i has
+ * the whole-number mass
+ *   m_i = rint(2^40 * exp(l_i / T - max_j(l_j / T)))     (exp in binary32)
+ * so that sums of masses are exact and a row's token depends neither on the
+ * order of summation nor on the other rows.  In this order:
+ *   top-k  keeps the k largest logits (equal ones by lower index);
+ *   top-p  keeps the shortest prefix, in falling order of logit, whose mass is
+ *          at least trunc(p * mass left) (at least one token);
+ *   min-p  keeps m_i >= min_p * 2^40;
+ *   the token is the first index at which the running mass of the kept tokens
+ *   exceeds trunc(u * their mass).
+ *   logits      : [rows, vocab] binary32 (W4_OUT_F32) or bfloat16
+ *                 (W4_OUT_BF16), rows row_stride elements apart
+ *   u           : binary32 [rows] in [0, 1)
+ *   temperature : binary32 [rows] or NULL (1); not above 0: the largest logit
+ *   top_k       : int32 [rows] or NULL; below 1: off
+ *   top_p       : binary32 [rows] or NULL; 1 or more: off
+ *   min_p       : binary32 [rows] or NULL; 0: off
+ *   tokens      : int32 [rows]; -1 for a row without a logit above -infinity
+ * NaN logits are never chosen.  A row whose largest logit / T is infinite
+ * gives that token (the first such).  rows <= 2^20, vocab <= 2^18.
+ */
+int w4a16_sample(const void *logits, int dtype, int64_t row_stride,
+                 int64_t rows, int64_t vocab, const float *u,
+                 const float *temperature, const int32_t *top_k,
+                 const float *top_p, const float *min_p, int32_t *tokens,
+                 void *stream);
 
 /*
  * Synchronises `stream`, then reads and clears the current device's sticky
