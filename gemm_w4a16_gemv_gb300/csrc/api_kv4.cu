@@ -259,7 +259,7 @@ int kv4_attention(const uint16_t *q, int64_t q_stride, const uint8_t *cache, int
         return fail(W4A16_ERR_INVALID_ARG, "%s: scale=%g must be finite", fn, static_cast<double>(scale));
     if (int r = check_head_dim(fn, D)) return r;
     if (int r = check_page(fn, block_size, num_blocks)) return r;
-    if (requests > 8192 || T > kMaxTokens || Hq > 1024 || max_blocks * block_size > 0x7fffffff)
+    if (requests > 4096 || T > kMaxTokens || Hq > 1024 || max_blocks * block_size > 0x7fffffff)
         return fail(W4A16_ERR_UNSUPPORTED, "%s: sizes too large", fn);
     if (T == 0) return ok();
     if (int r = check_rows(fn, "q", q, q_stride, Hq, D)) return r;

@@ -493,7 +493,7 @@ int kv4_gather(const uint8_t *cache, int64_t num_blocks, int block_size,
  *         separate scratch.
  * K, V and the softmax's statistics and sums are binary32 or exact; the
  * weights of the sum over V are rounded to binary16.
- * Hq is a multiple of Hkv; requests <= 8192; T = 0 launches nothing.
+ * Hq is a multiple of Hkv; requests <= 4096; T = 0 launches nothing.
  */
 int64_t kv4_attention_scratch_bytes(int Hq, int Hkv, int D);
 int kv4_attention(const uint16_t *q, int64_t q_stride, const uint8_t *cache,
