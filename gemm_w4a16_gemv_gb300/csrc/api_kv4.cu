@@ -275,7 +275,7 @@ int kv4_attention(const uint16_t *q, int64_t q_stride, const uint8_t *cache, int
         return fail(W4A16_ERR_INVALID_ARG, "%s: scratch of %lld bytes, %lld needed", fn, (long long)scratch_bytes,
                     (long long)need);
     w4::DeviceInfo dev;
-    w4::Kv4AttnArgs a;
+    w4::Kv4AttnArgs a = {};
     if (int r = device_state(dev, a.status)) return r;
     if (int r = check_device_ptrs(fn, dev.device, {q, cache, block_table, seq_lens, cu_new, out, scratch})) return r;
     a.q = q;

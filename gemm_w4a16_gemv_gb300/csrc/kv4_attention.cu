@@ -45,6 +45,7 @@ namespace {
 constexpr int MAX_CTAS = 160;         // scratch is sized for this many
 constexpr int MAX_ROWS = 16;          // rows of a segment
 constexpr int COUNTER_BYTES = 1024;   // arrival counters at the head of the scratch
+constexpr int PROMPT_ROWS = 48;       // requests with more rows go to the tensor cores
 constexpr float NEG_INF = -INFINITY;
 
 __device__ __forceinline__ float ex2(float x) {
@@ -94,6 +95,13 @@ __device__ __forceinline__ int key_of_row(int r) { return (0x57463120u >> (4 * r
 // Rows before request b; whatever the array holds, inside the tensors.
 __device__ __forceinline__ int rows_before(const Kv4AttnArgs &a, int b) {
     return static_cast<int>(min(max(static_cast<int64_t>(a.cu_new[b]), int64_t(0)), a.T));
+}
+
+// Rows of request b that this kernel answers: new tokens x query heads of a
+// key head, or none when the prompt kernel takes them.
+__device__ __forceinline__ int rows_of(const Kv4AttnArgs &a, int b, int G) {
+    const int rows = (rows_before(a, b + 1) - rows_before(a, b)) * G;
+    return rows > 0 && rows <= a.rows_most ? rows : 0;
 }
 
 // A segment: the rows [r0, r0 + rows) of (request b, key head h) and the cache
@@ -147,10 +155,10 @@ struct Cursor {
         if (++s.h < a.Hkv) return;
         s.h = 0;
         int b = s.b, r0 = s.r0 + R;
-        if (r0 >= (rows_before(a, b + 1) - rows_before(a, b)) * G) {
+        if (r0 >= rows_of(a, b, G)) {
             r0 = 0;
             do ++b;
-            while (b < a.requests && rows_before(a, b + 1) <= rows_before(a, b));
+            while (b < a.requests && rows_of(a, b, G) == 0);
             if (b >= a.requests) return;  // past the last segment: not used
         }
         shape_segment<R>(a, b, r0, G, s);
@@ -268,7 +276,7 @@ __global__ void __launch_bounds__(W * 32, 1) attn_stream_kernel(const Kv4AttnArg
         const int b0 = min(tid * per, a.requests), b1 = min(b0 + per, a.requests);
         long long sum = 0;
         for (int b = b0; b < b1; ++b) {
-            const int rows = (rows_before(a, b + 1) - rows_before(a, b)) * G;
+            const int rows = rows_of(a, b, G);
             long long n = 0;
             for (int r0 = 0; r0 < rows; r0 += R) {
                 Segment s;
@@ -296,8 +304,7 @@ __global__ void __launch_bounds__(W * 32, 1) attn_stream_kernel(const Kv4AttnArg
         }
         __syncthreads();
     }
-    // rows that belong to no request
-    {
+    if (a.zero_rest) {  // rows that belong to no request
         const int64_t from = static_cast<int64_t>(rows_before(a, a.requests)) * a.Hq * D / 8;
         const int64_t to = a.T * a.Hq * D / 8;
         for (int64_t i = from + static_cast<int64_t>(blockIdx.x) * W * 32 + tid; i < to;
@@ -743,9 +750,22 @@ int64_t kv4_attention_scratch(int, int, int D) {
     return (COUNTER_BYTES + int64_t(MAX_CTAS) * 2 * MAX_ROWS * (D + 2) * 4 + 255) / 256 * 256;
 }
 
-cudaError_t launch_kv4_attention(const Kv4AttnArgs &a, int D, cudaStream_t st, const DeviceInfo &dev) {
+cudaError_t launch_kv4_attention(const Kv4AttnArgs &args, int D, cudaStream_t st, const DeviceInfo &dev) {
+    Kv4AttnArgs a = args;
+    const int G = a.Hq / a.Hkv;
+    a.rows_most = 0x7fffffff;
+    a.zero_rest = 1;
+    if (a.max_new * G > PROMPT_ROWS) {
+        // requests of many rows to the tensor cores, the others of a mixed step
+        // to the streaming kernel
+        a.rows_above = a.requests > 1 ? PROMPT_ROWS : 0;
+        if (cudaError_t e = launch_kv4_prompt(a, D, st, dev)) return e;
+        if (a.requests == 1) return cudaSuccess;
+        a.rows_most = PROMPT_ROWS;
+        a.zero_rest = 0;
+    }
     // rows that share a read of the cache: 8 or 16 to a segment
-    const bool few = a.max_new * (a.Hq / a.Hkv) <= 8;
+    const bool few = a.max_new * G <= 8;
     if (D == 64) return few ? launch_stream<64, 1, 16>(a, st, dev) : launch_stream<64, 2, 16>(a, st, dev);
     if (D == 128) return few ? launch_stream<128, 1, 16>(a, st, dev) : launch_stream<128, 2, 12>(a, st, dev);
     return few ? launch_stream<256, 1, 12>(a, st, dev) : launch_stream<256, 2, 8>(a, st, dev);

@@ -1,0 +1,610 @@
+// Attention over the paged 4-bit cache for pieces of many new tokens, on the
+// tcgen05 tensor cores (kv4_attention in the C header; the streaming form for
+// few rows is kv4_attention.cu).
+//
+// An item is 128 rows (new tokens x the G query heads of one key head) of a
+// request; its keys are taken 128 at a time:
+//   S = Q K^T          M 128, N 128, K D      -> tensor memory (two buffers)
+//   P = exp2(S' - M)   128 threads, one row each, back into tensor memory
+//   O += P V           M 128, N D, K 128      P from tensor memory
+// Bound: at D = 256 the two products take 2 x 1024 cycles of the tensor pipe
+// per 128 x 128 tile; the same tile costs 2 x 32768 codes to be formed as
+// binary16 operands (1.6 instructions a code, 820 cycles of the SM's issue
+// slots) and 16384 exponentials with 7 instructions each (930 cycles), so
+// the instruction slots are nearly as full as the tensor pipe and all three
+// have to run at the same time.
+//
+// Roles: warps 0-3 softmax and epilogue (warp w owns the tensor memory lanes
+// 32 w ..), warps 4-11 form the operands (a warp per 16-token cache tile,
+// 16-byte loads of the codes one step ahead in registers), warp 12 issues the
+// products in the order Q K(i+1), P(i) V(i), so that the operands of one are
+// formed while the other runs.
+//
+// Operands.  (code - zero) is exact in binary16; times the scale it is rounded
+// once.  Scales are divided by a power of two per key (of the largest of its
+// groups) so that neither large nor small ones leave binary16's range; the
+// power of K's scale multiplies the key's score, that of V's enters the
+// exponent: P = exp2(x + e - M) and the sum of weights takes P 2^-e.  A row of
+// Q enters after a power-of-two scale of its own.  K and V lie in shared
+// memory as they come from the cache, a row of 64 dimensions per token and
+// group with the 128-byte swizzle: K-major for the first product, MN-major
+// (dimensions contiguous) for the second.  A word's codes leave in the order
+// 0 4 1 5 2 6 3 7; Q is stored in the same order and the epilogue undoes it.
+//
+// The running reference M of a row moves only when it would grow by more than
+// 2^8; then the softmax warps scale O in tensor memory themselves, between
+// two products.  Every wait is bounded; on a timeout the roles still go
+// through all their arrivals.
+#include "common.cuh"
+#include "kernels.h"
+#include "kv4.cuh"
+#include "tc_common.cuh"
+
+namespace w4 {
+namespace {
+
+constexpr int ROWS = 128;
+constexpr int KEYS = 128;
+constexpr int SOFT_THREADS = 128;
+constexpr int FORM_WARPS = 8;
+constexpr int FORM_THREADS = FORM_WARPS * 32;
+constexpr int THREADS = SOFT_THREADS + FORM_THREADS + 32;
+constexpr int VECS = 3;              // buffers of the per-key factors
+constexpr int SUB = KEYS * 128;      // bytes of 128 rows x 64 binary16
+
+struct Bars {
+    uint64_t qfull, kfull, kfree, vfull, vfree, sfull[2], pfull[2];
+    uint32_t tmem;
+};
+
+// MN-major operand with the 128-byte swizzle: 64 contiguous elements x 8 rows
+// of K per 1024 bytes; the next 64 elements `lead` bytes on, the next 8 rows
+// of K 1024 bytes on.
+__device__ __forceinline__ uint64_t desc_sw128_mn(uint32_t saddr, uint32_t lead) {
+    uint64_t d = 0;
+    d |= static_cast<uint64_t>((saddr >> 4) & 0x3FFFu);
+    d |= static_cast<uint64_t>((lead >> 4) & 0x3FFFu) << 16;
+    d |= static_cast<uint64_t>(1024u >> 4) << 32;
+    d |= static_cast<uint64_t>(1u) << 46;
+    d |= static_cast<uint64_t>(2u) << 61;
+    return d;
+}
+
+__device__ __forceinline__ float ex2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+__device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
+    const __half2 h = __floats2half2_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t *>(&h);
+}
+__device__ __forceinline__ uint32_t add_f16x2(uint32_t a, uint32_t b) {
+    uint32_t d;
+    asm("add.rn.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+    return d;
+}
+__device__ __forceinline__ uint32_t mul_f16x2(uint32_t a, uint32_t b) {
+    uint32_t d;
+    asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+    return d;
+}
+__device__ __forceinline__ uint32_t fma_f16x2(uint32_t a, uint32_t b, uint32_t c) {
+    uint32_t d;
+    asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(d) : "r"(a), "r"(b), "r"(c));
+    return d;
+}
+__device__ __forceinline__ float pow2(int e) { return __uint_as_float(static_cast<uint32_t>(127 + e) << 23); }
+
+__device__ __forceinline__ int rows_before(const Kv4AttnArgs &a, int b) {
+    return static_cast<int>(min(max(static_cast<int64_t>(a.cu_new[b]), int64_t(0)), a.T));
+}
+
+struct Item {
+    int b, h, tok0, r0, rows;   // rows [r0, r0 + rows) of the request; its first token
+    int base;                   // position of row r is base + r / G
+    int end;                    // keys at or past this are seen by no row
+    int n, ns, low;             // key tiles: the first ns, then from `low` on
+    __device__ __forceinline__ int key0(int i) const { return (i < ns ? i : i - ns + low) * KEYS; }
+};
+
+__device__ __forceinline__ bool taken(const Kv4AttnArgs &a, int rows) { return rows > a.rows_above; }
+
+__device__ __forceinline__ Item item_of(const Kv4AttnArgs &a, const int *cum, int index, int G) {
+    Item it;
+    int lo = 0, hi = a.requests;
+    while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (cum[mid] <= index) lo = mid;
+        else hi = mid;
+    }
+    it.b = lo;
+    it.tok0 = rows_before(a, lo);
+    const int n = rows_before(a, lo + 1) - it.tok0;
+    const int total = n * G, blocks = (total + ROWS - 1) / ROWS;
+    const int local = index - cum[lo];
+    it.h = local % a.Hkv;
+    it.r0 = (blocks - 1 - local / a.Hkv) * ROWS;  // the rows that see most first
+    it.rows = min(ROWS, total - it.r0);
+    const long long first = static_cast<long long>(a.seq_lens[lo]) - n;
+    it.base = static_cast<int>(first);
+    const long long cap = static_cast<long long>(a.max_blocks) << a.bs_log2;
+    const long long p_lo = first + it.r0 / G, p_hi = first + (it.r0 + it.rows - 1) / G;
+    long long end = p_hi + 1 < cap ? p_hi + 1 : cap;
+    if (end < 0) end = 0;
+    long long low = 0, ns = 0;
+    if (a.window > 0) {
+        low = p_lo - a.window + 1;
+        low = low > 0 ? low / KEYS : 0;
+        ns = ((a.sinks < end ? a.sinks : end) + KEYS - 1) / KEYS;
+        if (low < ns) low = ns;
+    }
+    const long long last = (end + KEYS - 1) / KEYS;
+    it.end = static_cast<int>(end);
+    it.ns = static_cast<int>(ns);
+    it.low = static_cast<int>(low);
+    it.n = static_cast<int>(ns + (last > low ? last - low : 0));
+    return it;
+}
+
+// A CTA's items: each round of gridDim.x items in turn, odd rounds backwards
+// (items get shorter within a request).
+__device__ __forceinline__ int index_of(int round) {
+    const int c = static_cast<int>(blockIdx.x), C = static_cast<int>(gridDim.x);
+    return round * C + (round & 1 ? C - 1 - c : c);
+}
+
+template <int D>
+struct PromptSmem {
+    static constexpr int G64 = D / 64;
+    static constexpr int q = 0, k = G64 * SUB, v = 2 * G64 * SUB;
+    static constexpr int vec = 3 * G64 * SUB;             // [VECS][3][KEYS] floats
+    static constexpr int bars = vec + VECS * 3 * KEYS * 4;
+    static constexpr int cum = bars + 128;                // [requests + 1] ints
+};
+
+// 16 bytes of codes of one token (32 dimensions of a group) to 64 bytes of
+// binary16 (code - zero) * scale in the swizzled row.
+__device__ __forceinline__ void form(const uint4 raw, uint32_t s2, uint32_t z1024, uint32_t z64, unsigned char *row, int x7,
+                                     int half) {
+    const uint32_t w[4] = {raw.x, raw.y, raw.z, raw.w};
+#pragma unroll
+    for (int c = 0; c < 4; ++c) {
+        const uint32_t lo = w[c], hi = w[c] >> 8;
+        uint4 o;
+        o.x = mul_f16x2(add_f16x2((lo & 0x000f000fu) | 0x64006400u, z1024), s2);
+        o.y = mul_f16x2(fma_f16x2((lo & 0x00f000f0u) | 0x64006400u, 0x2c002c00u, z64), s2);
+        o.z = mul_f16x2(add_f16x2((hi & 0x000f000fu) | 0x64006400u, z1024), s2);
+        o.w = mul_f16x2(fma_f16x2((hi & 0x00f000f0u) | 0x64006400u, 0x2c002c00u, z64), s2);
+        *reinterpret_cast<uint4 *>(row + (((half * 4 + c) ^ x7) << 4)) = o;
+    }
+}
+
+template <int D>
+__global__ void __launch_bounds__(THREADS, 1) attn_prompt_kernel(const Kv4AttnArgs a) {
+    using L = PromptSmem<D>;
+    constexpr int G64 = L::G64;
+    constexpr uint32_t COL_S = D, IDESC_QK = idesc_kind_f16(ROWS, KEYS, 0u),
+                       IDESC_PV = idesc_kind_f16(ROWS, D, 0u) | (1u << 16);
+    extern __shared__ unsigned char smem_raw[];
+    unsigned char *const smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+    Bars &bar = *reinterpret_cast<Bars *>(smem + L::bars);
+    int *const cum = reinterpret_cast<int *>(smem + L::cum);
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int G = a.Hq / a.Hkv;
+
+    if (tid == 0) {
+        mbar_init(&bar.qfull, SOFT_THREADS);
+        mbar_init(&bar.kfull, FORM_THREADS);
+        mbar_init(&bar.vfull, FORM_THREADS);
+        mbar_init(&bar.kfree, 1);
+        mbar_init(&bar.vfree, 1);
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&bar.sfull[i], 1);
+            mbar_init(&bar.pfull[i], SOFT_THREADS);
+        }
+        fence_barrier_init();
+    }
+    if (warp == 12) {
+        tmem_alloc(&bar.tmem, 512);
+        tmem_relinquish();
+    }
+    pdl_launch_dependents();
+    pdl_wait();
+    if (warp == 0) {  // items before each request
+        int at = 0;
+        for (int b0 = 0; b0 < a.requests; b0 += 32) {
+            const int b = b0 + lane;
+            int n = 0;
+            if (b < a.requests) {
+                const int rows = (rows_before(a, b + 1) - rows_before(a, b)) * G;
+                n = taken(a, rows) ? (rows + ROWS - 1) / ROWS * a.Hkv : 0;
+            }
+            int in = n;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const int v = __shfl_up_sync(0xffffffffu, in, o);
+                if (lane >= o) in += v;
+            }
+            if (b < a.requests) cum[b + 1] = at + in;
+            at += __shfl_sync(0xffffffffu, in, 31);
+        }
+        if (lane == 0) cum[0] = 0;
+    }
+    if (a.zero_rest) {  // rows that belong to no request
+        const int64_t from = static_cast<int64_t>(rows_before(a, a.requests)) * a.Hq * D / 8, to = a.T * a.Hq * D / 8;
+        for (int64_t i = from + static_cast<int64_t>(blockIdx.x) * THREADS + tid; i < to;
+             i += static_cast<int64_t>(gridDim.x) * THREADS)
+            reinterpret_cast<uint4 *>(a.out)[i] = make_uint4(0, 0, 0, 0);
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = bar.tmem;
+    const int items = cum[a.requests];
+
+    if (warp < 4) {
+        // ------------------------------------------------ softmax, epilogue
+        const int r = tid;
+        const uint32_t t_row = tmem + (static_cast<uint32_t>(warp * 32) << 16);
+        unsigned char *const qrow = smem + L::q + r * 128;
+        int g = 0;  // key tiles so far, over all items
+        // Q of an item: this thread's row; returns the factor of its scores
+        auto build = [&](const Item &it) -> float {
+            const bool on = r < it.rows;
+            const int row = it.r0 + (on ? r : 0);
+            const uint16_t *src = a.q + static_cast<int64_t>(it.tok0 + row / G) * a.q_stride +
+                                  static_cast<int64_t>(it.h * G + row % G) * D;
+            float big = 0.f;
+#pragma unroll 8
+            for (int c = 0; c < D / 8; ++c) {
+                const uint4 v = *reinterpret_cast<const uint4 *>(src + 8 * c);
+                const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    big = fmaxf(big, fmaxf(fabsf(__uint_as_float(w[j] << 16)), fabsf(__uint_as_float(w[j] & 0xffff0000u))));
+            }
+            int kappa = big > 0.f ? 13 - (static_cast<int>(__float_as_uint(big) >> 23) - 127) : 0;
+            kappa = min(max(kappa, -110), 110);
+            const float up = on ? pow2(kappa) : 0.f;
+#pragma unroll 8
+            for (int c = 0; c < D / 8; ++c) {
+                const uint4 v = *reinterpret_cast<const uint4 *>(src + 8 * c);
+                const float x0 = __uint_as_float(v.x << 16) * up, x1 = __uint_as_float(v.x & 0xffff0000u) * up;
+                const float x2 = __uint_as_float(v.y << 16) * up, x3 = __uint_as_float(v.y & 0xffff0000u) * up;
+                const float x4 = __uint_as_float(v.z << 16) * up, x5 = __uint_as_float(v.z & 0xffff0000u) * up;
+                const float x6 = __uint_as_float(v.w << 16) * up, x7 = __uint_as_float(v.w & 0xffff0000u) * up;
+                *reinterpret_cast<uint4 *>(qrow + (c >> 3) * SUB + (((c & 7) ^ (r & 7)) << 4)) =
+                    make_uint4(pack_f16(x0, x4), pack_f16(x1, x5), pack_f16(x2, x6), pack_f16(x3, x7));
+            }
+            fence_proxy_async_smem();
+            mbar_arrive(&bar.qfull);
+            return a.scale * 1.4426950408889634f * pow2(-kappa);
+        };
+        int round = 0;
+        Item it;
+        float F = 0.f;
+        bool have = false;
+        auto next_item = [&]() {  // the next item with keys; items without are answered at once
+            have = false;
+            while (true) {
+                const int index = index_of(round++);
+                if (round * static_cast<int>(gridDim.x) - static_cast<int>(gridDim.x) >= items) return;
+                if (index >= items) continue;
+                it = item_of(a, cum, index, G);
+                if (it.n > 0) break;
+                if (r < it.rows) {
+                    const int row = it.r0 + r;
+                    uint4 *dst = reinterpret_cast<uint4 *>(
+                        a.out + (static_cast<int64_t>(it.tok0 + row / G) * a.Hq + it.h * G + row % G) * D);
+                    for (int c = 0; c < D / 8; ++c) dst[c] = make_uint4(0, 0, 0, 0);
+                }
+            }
+            have = true;
+            F = build(it);
+        };
+        next_item();
+        while (have) {
+            const Item cur = it;
+            const float Fr = F;
+            float M = -INFINITY, l = 0.f;
+            const int p = cur.base + (cur.r0 + min(r, cur.rows - 1)) / G;
+            const int p_lo = cur.base + cur.r0 / G, p_hi = cur.base + (cur.r0 + cur.rows - 1) / G;
+            for (int i = 0; i < cur.n; ++i, ++g) {
+                const int j0 = cur.key0(i);
+                const float *const vec = reinterpret_cast<const float *>(smem + L::vec) + (g % VECS) * 3 * KEYS;
+                const bool free = j0 + KEYS <= p_lo + 1 && (a.window <= 0 || p_hi - j0 < a.window || j0 + KEYS <= a.sinks);
+                const uint32_t t_s = t_row + COL_S + (g & 1) * KEYS;
+                mbar_wait(&bar.sfull[g & 1], (g >> 1) & 1, a.status);
+                tc_fence_after();
+                uint32_t P[KEYS / 2];
+                float mx, sum;
+                // one pass over the row's scores against the reference m
+                auto pass = [&](float m) {
+                    mx = -INFINITY;
+                    sum = 0.f;
+#pragma unroll
+                    for (int c = 0; c < KEYS / 32; ++c) {
+                        uint32_t s[32];
+                        tmem_ld_32x32b_x32(t_s + 32 * c, s);
+                        tmem_ld_wait();
+#pragma unroll
+                        for (int e = 0; e < 32; e += 4) {
+                            const float4 fk = *reinterpret_cast<const float4 *>(vec + 32 * c + e);
+                            const float4 ev = *reinterpret_cast<const float4 *>(vec + KEYS + 32 * c + e);
+                            const float4 gv = *reinterpret_cast<const float4 *>(vec + 2 * KEYS + 32 * c + e);
+                            float u[4] = {fmaf(__uint_as_float(s[e]) * Fr, fk.x, ev.x),
+                                          fmaf(__uint_as_float(s[e + 1]) * Fr, fk.y, ev.y),
+                                          fmaf(__uint_as_float(s[e + 2]) * Fr, fk.z, ev.z),
+                                          fmaf(__uint_as_float(s[e + 3]) * Fr, fk.w, ev.w)};
+                            if (!free) {
+#pragma unroll
+                                for (int q = 0; q < 4; ++q) {
+                                    const int j = j0 + 32 * c + e + q;
+                                    const bool see = j <= p && (a.window <= 0 || p - j < a.window || j < a.sinks);
+                                    u[q] = see ? u[q] : -INFINITY;
+                                }
+                            }
+                            mx = fmaxf(fmaxf(mx, fmaxf(u[0], u[1])), fmaxf(u[2], u[3]));
+#pragma unroll
+                            for (int q = 0; q < 4; ++q) u[q] = ex2(u[q] - m);
+                            sum = fmaf(u[0], gv.x, sum);
+                            sum = fmaf(u[1], gv.y, sum);
+                            sum = fmaf(u[2], gv.z, sum);
+                            sum = fmaf(u[3], gv.w, sum);
+                            P[16 * c + e / 2] = pack_f16(u[0], u[1]);
+                            P[16 * c + e / 2 + 1] = pack_f16(u[2], u[3]);
+                        }
+                    }
+                };
+                pass(M == -INFINITY ? 0.f : M);
+                if (__any_sync(0xffffffffu, mx > M + 8.f)) {
+                    const float m = fmaxf(M, mx);
+                    const float f = m == -INFINITY ? 1.f : ex2(M - m);
+                    M = m;
+                    l *= f;
+                    pass(M == -INFINITY ? 0.f : M);
+                    if (i > 0) {  // O holds the earlier tiles once their product is done
+                        mbar_wait(&bar.vfree, (g - 1) & 1, a.status);
+                        tc_fence_after();
+#pragma unroll 1
+                        for (int c = 0; c < D / 32; ++c) {
+                            uint32_t o[32];
+                            tmem_ld_32x32b_x32(t_row + 32 * c, o);
+                            tmem_ld_wait();
+#pragma unroll
+                            for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
+                            tmem_st_32x32b_x32(t_row + 32 * c, o);
+                        }
+                    }
+                }
+                l += sum;
+                tmem_st_32x32b_x32(t_s, *reinterpret_cast<const uint32_t(*)[32]>(P));
+                tmem_st_32x32b_x32(t_s + 32, *reinterpret_cast<const uint32_t(*)[32]>(P + 32));
+                tmem_st_wait();
+                tc_fence_before();
+                mbar_arrive(&bar.pfull[g & 1]);
+            }
+            // every product Q K of this item is done: the next item's Q may be written
+            next_item();
+            mbar_wait(&bar.vfree, (g - 1) & 1, a.status);
+            tc_fence_after();
+            const float inv = l == 0.f ? 0.f : 1.f / l;
+            const int row = cur.r0 + r;
+            uint16_t *const dst = a.out + (static_cast<int64_t>(cur.tok0 + row / G) * a.Hq + cur.h * G + row % G) * D;
+#pragma unroll 1
+            for (int c = 0; c < D / 32; ++c) {
+                uint32_t o[32];
+                tmem_ld_32x32b_x32(t_row + 32 * c, o);
+                tmem_ld_wait();
+                if (r < cur.rows) {
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        uint32_t w[4];
+                        const uint32_t *x = o + 8 * e;  // dimensions 0 4 1 5 2 6 3 7
+                        const int at[8] = {0, 2, 4, 6, 1, 3, 5, 7};
+#pragma unroll
+                        for (int k = 0; k < 4; ++k)
+                            w[k] = static_cast<uint32_t>(f32_to_bf16_bits(__uint_as_float(x[at[2 * k]]) * inv)) |
+                                   static_cast<uint32_t>(f32_to_bf16_bits(__uint_as_float(x[at[2 * k + 1]]) * inv)) << 16;
+                        *reinterpret_cast<uint4 *>(dst + 32 * c + 8 * e) = make_uint4(w[0], w[1], w[2], w[3]);
+                    }
+                }
+            }
+            tc_fence_before();
+        }
+    } else if (warp < 4 + FORM_WARPS) {
+        // ------------------------------------------- operands from the cache
+        const int w = warp - 4, token = lane >> 1, half = lane & 1;
+        const int row = w * 16 + token;         // key row within the tile
+        unsigned char *const krow = smem + L::k + row * 128, *const vrow = smem + L::v + row * 128;
+        const int x7 = row & 7;
+        int g = 0;
+        bool bad = false;
+        for (int round = 0; round * static_cast<int>(gridDim.x) < items; ++round) {
+            const int index = index_of(round);
+            if (index >= items) continue;
+            const Item it = item_of(a, cum, index, G);
+            if (it.n == 0) continue;
+            // this warp's cache tile of key tile i (null: nothing there)
+            auto tile_of = [&](int i) -> const unsigned char * {
+                if (i >= it.n) return nullptr;
+                const int j = it.key0(i) + w * 16;
+                if (j >= it.end) return nullptr;
+                const int id = a.block_table[static_cast<int64_t>(it.b) * a.max_blocks + (j >> a.bs_log2)];
+                if (id < 0 || id >= a.num_blocks) {
+                    bad = true;
+                    return nullptr;
+                }
+                const int sub = (j & ((1 << a.bs_log2) - 1)) >> 4;
+                return a.cache + (((static_cast<size_t>(id) * a.Hkv + it.h) << (a.bs_log2 - 4)) + sub) *
+                                     static_cast<size_t>(kv4_tile_bytes(D));
+            };
+            uint4 kraw[G64], vraw[G64];
+            uint32_t kpar[G64], vpar[G64];
+            auto load_k = [&](const unsigned char *t, bool on) {
+#pragma unroll
+                for (int i = 0; i < G64; ++i) {
+                    kraw[i] = t ? *reinterpret_cast<const uint4 *>(t + (i * 16 + token) * 32 + half * 16) : make_uint4(0, 0, 0, 0);
+                    kpar[i] = on ? *reinterpret_cast<const uint32_t *>(t + 16 * D + (i * 16 + token) * 4) : 0u;
+                }
+            };
+            uint32_t vnext[G64];  // V's parameters of the tile whose K is in hand
+            auto load_vpar = [&](const unsigned char *t, bool on) {
+#pragma unroll
+                for (int i = 0; i < G64; ++i)
+                    vnext[i] = on ? *reinterpret_cast<const uint32_t *>(t + 17 * D + (i * 16 + token) * 4) : 0u;
+            };
+            auto load_v = [&](const unsigned char *t, bool on) {
+#pragma unroll
+                for (int i = 0; i < G64; ++i) {
+                    vraw[i] = t ? *reinterpret_cast<const uint4 *>(t + 8 * D + (i * 16 + token) * 32 + half * 16)
+                                : make_uint4(0, 0, 0, 0);
+                    vpar[i] = on ? *reinterpret_cast<const uint32_t *>(t + 17 * D + (i * 16 + token) * 4) : 0u;
+                }
+            };
+            auto valid = [&](int i, const unsigned char *t) { return t != nullptr && it.key0(i) + row < it.end; };
+            // exponent that brings the largest scale of the groups to [0.5, 1)
+            auto exponent = [](const uint32_t (&par)[G64]) -> int {
+                float top = 0.f;
+#pragma unroll
+                for (int i = 0; i < G64; ++i) top = fmaxf(top, fabsf(f16_lo(par[i])));
+                return top > 0.f ? static_cast<int>(__float_as_uint(top) >> 23) - 126 : 0;
+            };
+            auto put = [&](const uint4 (&raw)[G64], const uint32_t (&par)[G64], int e, unsigned char *rowp) {
+                const float down = pow2(-e);
+#pragma unroll
+                for (int i = 0; i < G64; ++i) {
+                    const float s = f16_lo(par[i]) * down, z = f16_hi(par[i]);
+                    form(raw[i], pack_f16(s, s), pack_f16(-1024.f - z, -1024.f - z), pack_f16(-64.f - z, -64.f - z),
+                         rowp + i * SUB, x7, half);
+                }
+            };
+            // K of tile number i (g + i over all items), with the key's factors
+            auto put_k = [&](int i, bool on) {
+                const int e = exponent(kpar), ev = exponent(vnext);
+                const int gi = g + i;
+                if (gi > 0) mbar_wait(&bar.kfree, (gi - 1) & 1, a.status);
+                put(kraw, kpar, e, krow);
+                if (half == 0) {
+                    float *const vec = reinterpret_cast<float *>(smem + L::vec) + (gi % VECS) * 3 * KEYS + row;
+                    vec[0] = on ? pow2(e) : 0.f;
+                    vec[KEYS] = on ? static_cast<float>(ev) : -INFINITY;
+                    vec[2 * KEYS] = on ? pow2(-ev) : 0.f;
+                }
+                fence_proxy_async_smem();
+                mbar_arrive(&bar.kfull);
+            };
+            auto put_v = [&](int i) {
+                const int e = exponent(vpar);
+                const int gi = g + i;
+                if (gi > 0) mbar_wait(&bar.vfree, (gi - 1) & 1, a.status);
+                put(vraw, vpar, e, vrow);
+                fence_proxy_async_smem();
+                mbar_arrive(&bar.vfull);
+            };
+            const unsigned char *t0 = tile_of(0), *t1 = tile_of(1);
+            load_k(t0, valid(0, t0));
+            load_vpar(t0, valid(0, t0));
+            load_v(t0, valid(0, t0));
+            put_k(0, valid(0, t0));
+            load_k(t1, valid(1, t1));
+            load_vpar(t1, valid(1, t1));
+            put_v(0);
+            load_v(t1, valid(1, t1));
+            for (int i = 1; i < it.n; ++i) {
+                // K(i), then V(i - 1) -- V(0) is there already; the loads run one tile ahead
+                const unsigned char *t2 = tile_of(i + 1);
+                put_k(i, valid(i, t1));
+                load_k(t2, valid(i + 1, t2));
+                load_vpar(t2, valid(i + 1, t2));
+                if (i > 1) {
+                    put_v(i - 1);
+                    load_v(t1, valid(i, t1));
+                }
+                t1 = t2;
+            }
+            if (it.n > 1) put_v(it.n - 1);
+            g += it.n;
+        }
+        if (__any_sync(0xffffffffu, bad) && lane == 0) atomicOr(a.status, kDevBadIndex);
+    } else {
+        // ------------------------------------------------------- products
+        const uint32_t qa = smem_u32(smem + L::q), ka = smem_u32(smem + L::k), va = smem_u32(smem + L::v);
+        int g = 0, done = 0;
+        auto qk = [&](int gi) {
+            mbar_wait(&bar.kfull, gi & 1, a.status);
+            tc_fence_after();
+#pragma unroll
+            for (int k = 0; k < D / 16; ++k) {
+                const uint32_t off = (k >> 2) * SUB + (k & 3) * 32;
+                umma_f16_w(tmem + COL_S + (gi & 1) * KEYS, smem_desc_sw128_kmajor(qa + off), smem_desc_sw128_kmajor(ka + off),
+                           IDESC_QK, k != 0);
+            }
+            umma_commit_w(&bar.sfull[gi & 1]);
+            umma_commit_w(&bar.kfree);
+        };
+        auto pv = [&](int gi, bool first) {
+            mbar_wait(&bar.pfull[gi & 1], (gi >> 1) & 1, a.status);
+            mbar_wait(&bar.vfull, gi & 1, a.status);
+            tc_fence_after();
+#pragma unroll
+            for (int k = 0; k < KEYS / 16; ++k)
+                umma_f16_tmem_a_w(tmem, tmem + COL_S + (gi & 1) * KEYS + 8 * k, desc_sw128_mn(va + k * 2048, SUB), IDESC_PV,
+                                  !(first && k == 0));
+            umma_commit_w(&bar.vfree);
+        };
+        for (int round = 0; round * static_cast<int>(gridDim.x) < items; ++round) {
+            const int index = index_of(round);
+            if (index >= items) continue;
+            const Item it = item_of(a, cum, index, G);
+            if (it.n == 0) continue;
+            mbar_wait(&bar.qfull, done & 1, a.status);
+            ++done;
+            qk(g);
+            for (int i = 1; i < it.n; ++i) {
+                qk(g + i);
+                pv(g + i - 1, i == 1);
+            }
+            pv(g + it.n - 1, it.n == 1);
+            g += it.n;
+        }
+        // tensor memory is released only when every product has completed
+        if (g > 0) mbar_wait(&bar.vfree, (g - 1) & 1, nullptr);
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 12) {
+        tc_fence_after();
+        tmem_dealloc(tmem, 512);
+    }
+}
+
+template <int D>
+cudaError_t launch(const Kv4AttnArgs &a, cudaStream_t st, const DeviceInfo &dev) {
+    const int smem = 1024 + PromptSmem<D>::cum + (a.requests + 1) * 4;
+    if (smem > dev.max_smem_optin) return cudaErrorNotSupported;
+    static SmemLimit limit;
+    if (cudaError_t e = limit.ensure(reinterpret_cast<const void *>(attn_prompt_kernel<D>), dev.device, smem)) return e;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned>(dev.num_sms));
+    cfg.blockDim = dim3(THREADS);
+    cfg.dynamicSmemBytes = static_cast<size_t>(smem);
+    cfg.stream = st;
+    cudaLaunchAttribute pdl[1];
+    pdl[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    pdl[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = pdl;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, attn_prompt_kernel<D>, a);
+}
+
+}  // namespace
+
+cudaError_t launch_kv4_prompt(const Kv4AttnArgs &a, int D, cudaStream_t st, const DeviceInfo &dev) {
+    if (D == 64) return launch<64>(a, st, dev);
+    if (D == 128) return launch<128>(a, st, dev);
+    return launch<256>(a, st, dev);
+}
+
+}  // namespace w4
