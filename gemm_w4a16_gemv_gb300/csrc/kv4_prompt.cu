@@ -49,6 +49,7 @@ constexpr int SOFT_THREADS = 128;
 constexpr int FORM_WARPS = 8;
 constexpr int FORM_THREADS = FORM_WARPS * 32;
 constexpr int THREADS = SOFT_THREADS + FORM_THREADS + 32;
+constexpr float NONE = -1e30f;       // reference of a row that has seen no key
 constexpr int VECS = 3;              // buffers of the per-key factors
 constexpr int SUB = KEYS * 128;      // bytes of 128 rows x 64 binary16
 
@@ -307,7 +308,7 @@ __global__ void __launch_bounds__(THREADS, 1) attn_prompt_kernel(const Kv4AttnAr
         while (have) {
             const Item cur = it;
             const float Fr = F;
-            float M = -INFINITY, l = 0.f;
+            float M = NONE, l = 0.f;
             const int p = cur.base + (cur.r0 + min(r, cur.rows - 1)) / G;
             const int p_lo = cur.base + cur.r0 / G, p_hi = cur.base + (cur.r0 + cur.rows - 1) / G;
             for (int i = 0; i < cur.n; ++i, ++g) {
@@ -317,53 +318,78 @@ __global__ void __launch_bounds__(THREADS, 1) attn_prompt_kernel(const Kv4AttnAr
                 const uint32_t t_s = t_row + COL_S + (g & 1) * KEYS;
                 mbar_wait(&bar.sfull[g & 1], (g >> 1) & 1, a.status);
                 tc_fence_after();
-                uint32_t P[KEYS / 2];
-                float mx, sum;
-                // one pass over the row's scores against the reference m
-                auto pass = [&](float m) {
-                    mx = -INFINITY;
-                    sum = 0.f;
+                // 32 keys at a time: scores in, weights out into the columns of
+                // scores already read (half as wide)
+                float m = M, sum = 0.f, scaled = 1.f;
+                uint32_t s[2][32];
+                tmem_ld_32x32b_x32(t_s, s[0]);
+#pragma unroll 1
+                for (int cc = 0; cc < KEYS / 32; cc += 2) {
 #pragma unroll
-                    for (int c = 0; c < KEYS / 32; ++c) {
-                        uint32_t s[32];
-                        tmem_ld_32x32b_x32(t_s + 32 * c, s);
+                    for (int half = 0; half < 2; ++half) {
+                        const int c = cc + half;
                         tmem_ld_wait();
+                        if (c + 1 < KEYS / 32) tmem_ld_32x32b_x32(t_s + 32 * (c + 1), s[half ^ 1]);
+                        float u[32];
+                        float mx = NONE;
 #pragma unroll
                         for (int e = 0; e < 32; e += 4) {
                             const float4 fk = *reinterpret_cast<const float4 *>(vec + 32 * c + e);
                             const float4 ev = *reinterpret_cast<const float4 *>(vec + KEYS + 32 * c + e);
-                            const float4 gv = *reinterpret_cast<const float4 *>(vec + 2 * KEYS + 32 * c + e);
-                            float u[4] = {fmaf(__uint_as_float(s[e]) * Fr, fk.x, ev.x),
-                                          fmaf(__uint_as_float(s[e + 1]) * Fr, fk.y, ev.y),
-                                          fmaf(__uint_as_float(s[e + 2]) * Fr, fk.z, ev.z),
-                                          fmaf(__uint_as_float(s[e + 3]) * Fr, fk.w, ev.w)};
-                            if (!free) {
-#pragma unroll
-                                for (int q = 0; q < 4; ++q) {
-                                    const int j = j0 + 32 * c + e + q;
-                                    const bool see = j <= p && (a.window <= 0 || p - j < a.window || j < a.sinks);
-                                    u[q] = see ? u[q] : -INFINITY;
-                                }
-                            }
-                            mx = fmaxf(fmaxf(mx, fmaxf(u[0], u[1])), fmaxf(u[2], u[3]));
-#pragma unroll
-                            for (int q = 0; q < 4; ++q) u[q] = ex2(u[q] - m);
-                            sum = fmaf(u[0], gv.x, sum);
-                            sum = fmaf(u[1], gv.y, sum);
-                            sum = fmaf(u[2], gv.z, sum);
-                            sum = fmaf(u[3], gv.w, sum);
-                            P[16 * c + e / 2] = pack_f16(u[0], u[1]);
-                            P[16 * c + e / 2 + 1] = pack_f16(u[2], u[3]);
+                            u[e] = fmaf(__uint_as_float(s[half][e]) * Fr, fk.x, ev.x);
+                            u[e + 1] = fmaf(__uint_as_float(s[half][e + 1]) * Fr, fk.y, ev.y);
+                            u[e + 2] = fmaf(__uint_as_float(s[half][e + 2]) * Fr, fk.z, ev.z);
+                            u[e + 3] = fmaf(__uint_as_float(s[half][e + 3]) * Fr, fk.w, ev.w);
                         }
+                        if (!free) {
+#pragma unroll
+                            for (int e = 0; e < 32; ++e) {
+                                const int j = j0 + 32 * c + e;
+                                const bool see = j <= p && (a.window <= 0 || p - j < a.window || j < a.sinks);
+                                u[e] = see ? u[e] : -INFINITY;
+                            }
+                        }
+#pragma unroll
+                        for (int e = 0; e < 32; ++e) mx = fmaxf(mx, u[e]);
+                        if (__any_sync(0xffffffffu, mx > m + 8.f)) {
+                            // the reference moves: what this tile has written so far, its
+                            // sum, and (below) what earlier tiles left shrink with it
+                            const float up = fmaxf(m, ceilf(mx)), f = ex2(m - up);  // whole numbers: f is a power of two
+                            m = up;
+                            sum *= f;
+                            scaled *= f;
+                            const uint32_t f2 = pack_f16(f, f);
+tmem_st_wait();
+#pragma unroll 1
+                            for (int q = 0; q < c; ++q) {
+                                uint32_t w[16];
+                                tmem_ld_32x32b_x16(t_s + 16 * q, w);
+                                tmem_ld_wait();
+#pragma unroll
+                                for (int e = 0; e < 16; ++e) w[e] = mul_f16x2(w[e], f2);
+                                tmem_st_32x32b_x16(t_s + 16 * q, w);
+                            }
+                        }
+                        float s0 = 0.f, s1 = 0.f, s2 = 0.f, s3 = 0.f;
+                        uint32_t w[16];
+#pragma unroll
+                        for (int e = 0; e < 32; e += 4) {
+                            const float4 gv = *reinterpret_cast<const float4 *>(vec + 2 * KEYS + 32 * c + e);
+                            const float p0 = ex2(u[e] - m), p1 = ex2(u[e + 1] - m), p2 = ex2(u[e + 2] - m),
+                                        p3 = ex2(u[e + 3] - m);
+                            s0 = fmaf(p0, gv.x, s0);
+                            s1 = fmaf(p1, gv.y, s1);
+                            s2 = fmaf(p2, gv.z, s2);
+                            s3 = fmaf(p3, gv.w, s3);
+                            w[e / 2] = pack_f16(p0, p1);
+                            w[e / 2 + 1] = pack_f16(p2, p3);
+                        }
+                        sum += (s0 + s1) + (s2 + s3);
+                        tmem_st_32x32b_x16(t_s + 16 * c, w);
                     }
-                };
-                pass(M == -INFINITY ? 0.f : M);
-                if (__any_sync(0xffffffffu, mx > M + 8.f)) {
-                    const float m = fmaxf(M, mx);
-                    const float f = m == -INFINITY ? 1.f : ex2(M - m);
-                    M = m;
-                    l *= f;
-                    pass(M == -INFINITY ? 0.f : M);
+                }
+                if (__any_sync(0xffffffffu, m != M)) {
+                    l *= scaled;
                     if (i > 0) {  // O holds the earlier tiles once their product is done
                         mbar_wait(&bar.vfree, (g - 1) & 1, a.status);
                         tc_fence_after();
@@ -373,14 +399,13 @@ __global__ void __launch_bounds__(THREADS, 1) attn_prompt_kernel(const Kv4AttnAr
                             tmem_ld_32x32b_x32(t_row + 32 * c, o);
                             tmem_ld_wait();
 #pragma unroll
-                            for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
+                            for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * scaled);
                             tmem_st_32x32b_x32(t_row + 32 * c, o);
                         }
                     }
+                    M = m;
                 }
                 l += sum;
-                tmem_st_32x32b_x32(t_s, *reinterpret_cast<const uint32_t(*)[32]>(P));
-                tmem_st_32x32b_x32(t_s + 32, *reinterpret_cast<const uint32_t(*)[32]>(P + 32));
                 tmem_st_wait();
                 tc_fence_before();
                 mbar_arrive(&bar.pfull[g & 1]);
@@ -503,28 +528,26 @@ __global__ void __launch_bounds__(THREADS, 1) attn_prompt_kernel(const Kv4AttnAr
                 fence_proxy_async_smem();
                 mbar_arrive(&bar.vfull);
             };
+            // K(i), then V(i - 1); the loads run one tile ahead
             const unsigned char *t0 = tile_of(0), *t1 = tile_of(1);
             load_k(t0, valid(0, t0));
             load_vpar(t0, valid(0, t0));
             load_v(t0, valid(0, t0));
-            put_k(0, valid(0, t0));
-            load_k(t1, valid(1, t1));
-            load_vpar(t1, valid(1, t1));
-            put_v(0);
-            load_v(t1, valid(1, t1));
-            for (int i = 1; i < it.n; ++i) {
-                // K(i), then V(i - 1) -- V(0) is there already; the loads run one tile ahead
-                const unsigned char *t2 = tile_of(i + 1);
-                put_k(i, valid(i, t1));
-                load_k(t2, valid(i + 1, t2));
-                load_vpar(t2, valid(i + 1, t2));
-                if (i > 1) {
-                    put_v(i - 1);
-                    load_v(t1, valid(i, t1));
+#pragma unroll 1
+            for (int i = 0; i <= it.n; ++i) {
+                const unsigned char *t2 = tile_of(i + 2);
+                if (i < it.n) {
+                    put_k(i, valid(i, t0));
+                    load_k(t1, valid(i + 1, t1));
+                    load_vpar(t1, valid(i + 1, t1));
                 }
+                if (i > 0) {
+                    put_v(i - 1);
+                    load_v(t0, valid(i, t0));
+                }
+                t0 = t1;
                 t1 = t2;
             }
-            if (it.n > 1) put_v(it.n - 1);
             g += it.n;
         }
         if (__any_sync(0xffffffffu, bad) && lane == 0) atomicOr(a.status, kDevBadIndex);
@@ -561,12 +584,11 @@ __global__ void __launch_bounds__(THREADS, 1) attn_prompt_kernel(const Kv4AttnAr
             if (it.n == 0) continue;
             mbar_wait(&bar.qfull, done & 1, a.status);
             ++done;
-            qk(g);
-            for (int i = 1; i < it.n; ++i) {
-                qk(g + i);
-                pv(g + i - 1, i == 1);
+#pragma unroll 1
+            for (int i = 0; i <= it.n; ++i) {
+                if (i < it.n) qk(g + i);
+                if (i > 0) pv(g + i - 1, i == 1);
             }
-            pv(g + it.n - 1, it.n == 1);
             g += it.n;
         }
         // tensor memory is released only when every product has completed
