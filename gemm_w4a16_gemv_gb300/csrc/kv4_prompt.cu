@@ -8,11 +8,14 @@
 //   P = exp2(S' - M)   128 threads, one row each, back into tensor memory
 //   O += P V           M 128, N D, K 128      P from tensor memory
 // Bound: at D = 256 the two products take 2 x 1024 cycles of the tensor pipe
-// per 128 x 128 tile; the same tile costs 2 x 32768 codes to be formed as
-// binary16 operands (1.6 instructions a code, 820 cycles of the SM's issue
-// slots) and 16384 exponentials with 7 instructions each (930 cycles), so
-// the instruction slots are nearly as full as the tensor pipe and all three
-// have to run at the same time.
+// per 128 x 128 tile.  The same tile costs 2 x 32768 codes to be formed as
+// binary16 operands (14 instructions per 8 codes and lane: 1300 cycles of the
+// SM's issue slots) and 16384 exponentials with 3 other instructions each (500
+// cycles; 1024 of the special-function units), all at the same time.
+//
+// Items are handed out by a counter in scratch, the longest first (requests
+// sorted by length, the last rows of a request first), and announced to the
+// roles through a small ring in shared memory.
 //
 // Roles: warps 0-3 softmax and epilogue (warp w owns the tensor memory lanes
 // 32 w ..), warps 4-11 form the operands (a warp per 16-token cache tile,
@@ -21,11 +24,11 @@
 // formed while the other runs.
 //
 // Operands.  (code - zero) is exact in binary16; times the scale it is rounded
-// once.  Scales are divided by a power of two per key (of the largest of its
-// groups) so that neither large nor small ones leave binary16's range; the
-// power of K's scale multiplies the key's score, that of V's enters the
-// exponent: P = exp2(x + e - M) and the sum of weights takes P 2^-e.  A row of
-// Q enters after a power-of-two scale of its own.  K and V lie in shared
+// once.  The scales of a tile are multiplied by a power of two that brings the
+// largest to [2^10, 2^11), so that scales 2^25 apart keep all their bits; the
+// power of K's goes into the factor of the scores, that of V's into the
+// exponent: P = exp2(x + e - M), and the sum of weights takes P 2^-e.  A row
+// of Q enters after a power-of-two scale of its own.  K and V lie in shared
 // memory as they come from the cache, a row of 64 dimensions per token and
 // group with the 128-byte swizzle: K-major for the first product, MN-major
 // (dimensions contiguous) for the second.  A word's codes leave in the order
@@ -50,12 +53,21 @@ constexpr int FORM_WARPS = 8;
 constexpr int FORM_THREADS = FORM_WARPS * 32;
 constexpr int THREADS = SOFT_THREADS + FORM_THREADS + 32;
 constexpr float NONE = -1e30f;       // reference of a row that has seen no key
-constexpr int VECS = 3;              // buffers of the per-key factors
+constexpr int METAS = 3;             // buffers of what the softmax needs to know of a key tile
+constexpr int QUEUE = 4;             // items announced ahead
+constexpr int SORT_MOST = 512;       // requests that are put in order of length
 constexpr int SUB = KEYS * 128;      // bytes of 128 rows x 64 binary16
 
 struct Bars {
-    uint64_t qfull, kfull, kfree, vfull, vfree, sfull[2], pfull[2];
+    uint64_t qfull, kfull, kfree, vfull, vfree, sfull[2], pfull[2], ifull[QUEUE];
     uint32_t tmem;
+    int item[QUEUE];
+};
+// Of a key tile, from the warps that form it: the exponents of its scales and
+// which of its cache tiles there are.
+struct alignas(8) Meta {
+    unsigned char there[8];
+    float k_factor, v_exponent, v_factor;
 };
 
 // MN-major operand with the 128-byte swizzle: 64 contiguous elements x 8 rows
@@ -95,6 +107,28 @@ __device__ __forceinline__ uint32_t fma_f16x2(uint32_t a, uint32_t b, uint32_t c
     asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(d) : "r"(a), "r"(b), "r"(c));
     return d;
 }
+__device__ __forceinline__ float max3(float a, float b, float c) {
+    float d;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+    return d;
+}
+// Two binary32 operations in one instruction.
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+    float2 d;
+    asm("{\n\t.reg .b64 x, y, z, w;\n\tmov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\tmov.b64 z, {%6, %7};\n\t"
+        "fma.rn.f32x2 w, x, y, z;\n\tmov.b64 {%0, %1}, w;\n\t}"
+        : "=f"(d.x), "=f"(d.y)
+        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+    return d;
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+    float2 d;
+    asm("{\n\t.reg .b64 x, y, w;\n\tmov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\tadd.rn.f32x2 w, x, y;\n\t"
+        "mov.b64 {%0, %1}, w;\n\t}"
+        : "=f"(d.x), "=f"(d.y)
+        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+    return d;
+}
 __device__ __forceinline__ float pow2(int e) { return __uint_as_float(static_cast<uint32_t>(127 + e) << 23); }
 
 __device__ __forceinline__ int rows_before(const Kv4AttnArgs &a, int b) {
@@ -111,7 +145,7 @@ struct Item {
 
 __device__ __forceinline__ bool taken(const Kv4AttnArgs &a, int rows) { return rows > a.rows_above; }
 
-__device__ __forceinline__ Item item_of(const Kv4AttnArgs &a, const int *cum, int index, int G) {
+__device__ __forceinline__ Item item_of(const Kv4AttnArgs &a, const int *cum, const int *order, int index, int G) {
     Item it;
     int lo = 0, hi = a.requests;
     while (hi - lo > 1) {
@@ -119,11 +153,12 @@ __device__ __forceinline__ Item item_of(const Kv4AttnArgs &a, const int *cum, in
         if (cum[mid] <= index) lo = mid;
         else hi = mid;
     }
+    const int local = index - cum[lo];
+    lo = order[lo];
     it.b = lo;
     it.tok0 = rows_before(a, lo);
     const int n = rows_before(a, lo + 1) - it.tok0;
     const int total = n * G, blocks = (total + ROWS - 1) / ROWS;
-    const int local = index - cum[lo];
     it.h = local % a.Hkv;
     it.r0 = (blocks - 1 - local / a.Hkv) * ROWS;  // the rows that see most first
     it.rows = min(ROWS, total - it.r0);
@@ -144,24 +179,19 @@ __device__ __forceinline__ Item item_of(const Kv4AttnArgs &a, const int *cum, in
     it.end = static_cast<int>(end);
     it.ns = static_cast<int>(ns);
     it.low = static_cast<int>(low);
-    it.n = static_cast<int>(ns + (last > low ? last - low : 0));
+    // (rows that see nothing take one empty tile and come out as zeros)
+    it.n = static_cast<int>(max(ns + (last > low ? last - low : 0), 1ll));
     return it;
-}
-
-// A CTA's items: each round of gridDim.x items in turn, odd rounds backwards
-// (items get shorter within a request).
-__device__ __forceinline__ int index_of(int round) {
-    const int c = static_cast<int>(blockIdx.x), C = static_cast<int>(gridDim.x);
-    return round * C + (round & 1 ? C - 1 - c : c);
 }
 
 template <int D>
 struct PromptSmem {
     static constexpr int G64 = D / 64;
     static constexpr int q = 0, k = G64 * SUB, v = 2 * G64 * SUB;
-    static constexpr int vec = 3 * G64 * SUB;             // [VECS][3][KEYS] floats
-    static constexpr int bars = vec + VECS * 3 * KEYS * 4;
-    static constexpr int cum = bars + 128;                // [requests + 1] ints
+    static constexpr int meta = 3 * G64 * SUB;            // [METAS] Meta
+    static constexpr int peak = meta + 128;               // [2][FORM_WARPS][2] largest scales of K and V
+    static constexpr int bars = peak + 128;
+    static constexpr int cum = bars + 256;                // [requests + 1] ints, then [requests] order
 };
 
 // 16 bytes of codes of one token (32 dimensions of a group) to 64 bytes of
@@ -204,6 +234,7 @@ __global__ void __launch_bounds__(THREADS, 1) attn_prompt_kernel(const Kv4AttnAr
             mbar_init(&bar.sfull[i], 1);
             mbar_init(&bar.pfull[i], SOFT_THREADS);
         }
+        for (int i = 0; i < QUEUE; ++i) mbar_init(&bar.ifull[i], 1);
         fence_barrier_init();
     }
     if (warp == 12) {
@@ -212,12 +243,29 @@ __global__ void __launch_bounds__(THREADS, 1) attn_prompt_kernel(const Kv4AttnAr
     }
     pdl_launch_dependents();
     pdl_wait();
-    if (warp == 0) {  // items before each request
+    int *const order = cum + a.requests + 1;
+    // requests by falling length (few enough to compare all pairs), then the
+    // items before each
+    for (int b = tid; b < a.requests; b += THREADS) {
+        int at = b;
+        if (a.requests <= SORT_MOST) {
+            const int mine = a.seq_lens[b];
+            at = 0;
+            for (int o = 0; o < a.requests; ++o) {
+                const int len = a.seq_lens[o];
+                at += len > mine || (len == mine && o < b);
+            }
+        }
+        order[at] = b;
+    }
+    __syncthreads();
+    if (warp == 0) {
         int at = 0;
         for (int b0 = 0; b0 < a.requests; b0 += 32) {
-            const int b = b0 + lane;
+            const int i = b0 + lane;
             int n = 0;
-            if (b < a.requests) {
+            if (i < a.requests) {
+                const int b = order[i];
                 const int rows = (rows_before(a, b + 1) - rows_before(a, b)) * G;
                 n = taken(a, rows) ? (rows + ROWS - 1) / ROWS * a.Hkv : 0;
             }
@@ -227,7 +275,7 @@ __global__ void __launch_bounds__(THREADS, 1) attn_prompt_kernel(const Kv4AttnAr
                 const int v = __shfl_up_sync(0xffffffffu, in, o);
                 if (lane >= o) in += v;
             }
-            if (b < a.requests) cum[b + 1] = at + in;
+            if (i < a.requests) cum[i + 1] = at + in;
             at += __shfl_sync(0xffffffffu, in, 31);
         }
         if (lane == 0) cum[0] = 0;
@@ -243,6 +291,12 @@ __global__ void __launch_bounds__(THREADS, 1) attn_prompt_kernel(const Kv4AttnAr
     tc_fence_after();
     const uint32_t tmem = bar.tmem;
     const int items = cum[a.requests];
+    unsigned int *const counter = reinterpret_cast<unsigned int *>(a.scratch + PROMPT_COUNTERS);
+    // the k-th item of this CTA (items or more: there is none)
+    auto item_at = [&](int k) -> int {
+        mbar_wait(&bar.ifull[k % QUEUE], (k / QUEUE) & 1, a.status);
+        return bar.item[k % QUEUE];
+    };
 
     if (warp < 4) {
         // ------------------------------------------------ softmax, epilogue
@@ -267,7 +321,7 @@ __global__ void __launch_bounds__(THREADS, 1) attn_prompt_kernel(const Kv4AttnAr
             }
             int kappa = big > 0.f ? 13 - (static_cast<int>(__float_as_uint(big) >> 23) - 127) : 0;
             kappa = min(max(kappa, -110), 110);
-            const float up = on ? pow2(kappa) : 0.f;
+            const float up = on ? (a.scale < 0.f ? -pow2(kappa) : pow2(kappa)) : 0.f;
 #pragma unroll 8
             for (int c = 0; c < D / 8; ++c) {
                 const uint4 v = *reinterpret_cast<const uint4 *>(src + 8 * c);
@@ -280,28 +334,17 @@ __global__ void __launch_bounds__(THREADS, 1) attn_prompt_kernel(const Kv4AttnAr
             }
             fence_proxy_async_smem();
             mbar_arrive(&bar.qfull);
-            return a.scale * 1.4426950408889634f * pow2(-kappa);
+            return fmaxf(fabsf(a.scale) * 1.4426950408889634f * pow2(-kappa), 1e-37f);
         };
-        int round = 0;
+        int k_item = 0;
         Item it;
         float F = 0.f;
         bool have = false;
-        auto next_item = [&]() {  // the next item with keys; items without are answered at once
-            have = false;
-            while (true) {
-                const int index = index_of(round++);
-                if (round * static_cast<int>(gridDim.x) - static_cast<int>(gridDim.x) >= items) return;
-                if (index >= items) continue;
-                it = item_of(a, cum, index, G);
-                if (it.n > 0) break;
-                if (r < it.rows) {
-                    const int row = it.r0 + r;
-                    uint4 *dst = reinterpret_cast<uint4 *>(
-                        a.out + (static_cast<int64_t>(it.tok0 + row / G) * a.Hq + it.h * G + row % G) * D);
-                    for (int c = 0; c < D / 8; ++c) dst[c] = make_uint4(0, 0, 0, 0);
-                }
-            }
-            have = true;
+        auto next_item = [&]() {
+            const int index = item_at(k_item++);
+            have = index < items;
+            if (!have) return;
+            it = item_of(a, cum, order, index, G);
             F = build(it);
         };
         next_item();
@@ -313,14 +356,18 @@ __global__ void __launch_bounds__(THREADS, 1) attn_prompt_kernel(const Kv4AttnAr
             const int p_lo = cur.base + cur.r0 / G, p_hi = cur.base + (cur.r0 + cur.rows - 1) / G;
             for (int i = 0; i < cur.n; ++i, ++g) {
                 const int j0 = cur.key0(i);
-                const float *const vec = reinterpret_cast<const float *>(smem + L::vec) + (g % VECS) * 3 * KEYS;
-                const bool free = j0 + KEYS <= p_lo + 1 && (a.window <= 0 || p_hi - j0 < a.window || j0 + KEYS <= a.sinks);
+                const Meta &meta = reinterpret_cast<const Meta *>(smem + L::meta)[g % METAS];
                 const uint32_t t_s = t_row + COL_S + (g & 1) * KEYS;
                 mbar_wait(&bar.sfull[g & 1], (g >> 1) & 1, a.status);
                 tc_fence_after();
+                const uint2 there = *reinterpret_cast<const uint2 *>(meta.there);
+                const bool free = (there.x & there.y) == 0x01010101u && j0 + KEYS <= p_lo + 1 &&
+                                  (a.window <= 0 || p_hi - j0 < a.window || j0 + KEYS <= a.sinks);
+                const float A = Fr * meta.k_factor, B = meta.v_exponent;
                 // 32 keys at a time: scores in, weights out into the columns of
                 // scores already read (half as wide)
-                float m = M, sum = 0.f, scaled = 1.f;
+                float m = M, scaled = 1.f;
+                float2 sum = make_float2(0.f, 0.f);
                 uint32_t s[2][32];
                 tmem_ld_32x32b_x32(t_s, s[0]);
 #pragma unroll 1
@@ -330,36 +377,34 @@ __global__ void __launch_bounds__(THREADS, 1) attn_prompt_kernel(const Kv4AttnAr
                         const int c = cc + half;
                         tmem_ld_wait();
                         if (c + 1 < KEYS / 32) tmem_ld_32x32b_x32(t_s + 32 * (c + 1), s[half ^ 1]);
-                        float u[32];
-                        float mx = NONE;
-#pragma unroll
-                        for (int e = 0; e < 32; e += 4) {
-                            const float4 fk = *reinterpret_cast<const float4 *>(vec + 32 * c + e);
-                            const float4 ev = *reinterpret_cast<const float4 *>(vec + KEYS + 32 * c + e);
-                            u[e] = fmaf(__uint_as_float(s[half][e]) * Fr, fk.x, ev.x);
-                            u[e + 1] = fmaf(__uint_as_float(s[half][e + 1]) * Fr, fk.y, ev.y);
-                            u[e + 2] = fmaf(__uint_as_float(s[half][e + 2]) * Fr, fk.z, ev.z);
-                            u[e + 3] = fmaf(__uint_as_float(s[half][e + 3]) * Fr, fk.w, ev.w);
-                        }
+                        uint32_t(&x)[32] = s[half];
                         if (!free) {
 #pragma unroll
                             for (int e = 0; e < 32; ++e) {
                                 const int j = j0 + 32 * c + e;
-                                const bool see = j <= p && (a.window <= 0 || p - j < a.window || j < a.sinks);
-                                u[e] = see ? u[e] : -INFINITY;
+                                const bool see = j <= p && j < cur.end && meta.there[2 * c + e / 16] &&
+                                                 (a.window <= 0 || p - j < a.window || j < a.sinks);
+                                x[e] = see ? x[e] : 0xff800000u;  // -infinity
                             }
                         }
+                        float top = __uint_as_float(x[0]), top1 = __uint_as_float(x[1]);
 #pragma unroll
-                        for (int e = 0; e < 32; ++e) mx = fmaxf(mx, u[e]);
+                        for (int e = 2; e < 30; e += 4) {
+                            top = max3(top, __uint_as_float(x[e]), __uint_as_float(x[e + 1]));
+                            top1 = max3(top1, __uint_as_float(x[e + 2]), __uint_as_float(x[e + 3]));
+                        }
+                        top = max3(top, __uint_as_float(x[30]), __uint_as_float(x[31]));
+                        const float mx = fmaf(fmaxf(top, top1), A, B);
                         if (__any_sync(0xffffffffu, mx > m + 8.f)) {
                             // the reference moves: what this tile has written so far, its
                             // sum, and (below) what earlier tiles left shrink with it
                             const float up = fmaxf(m, ceilf(mx)), f = ex2(m - up);  // whole numbers: f is a power of two
                             m = up;
-                            sum *= f;
+                            sum.x *= f;
+                            sum.y *= f;
                             scaled *= f;
                             const uint32_t f2 = pack_f16(f, f);
-tmem_st_wait();
+                            tmem_st_wait();
 #pragma unroll 1
                             for (int q = 0; q < c; ++q) {
                                 uint32_t w[16];
@@ -370,21 +415,16 @@ tmem_st_wait();
                                 tmem_st_32x32b_x16(t_s + 16 * q, w);
                             }
                         }
-                        float s0 = 0.f, s1 = 0.f, s2 = 0.f, s3 = 0.f;
+                        const float2 A2 = make_float2(A, A), B2 = make_float2(B - m, B - m);
                         uint32_t w[16];
 #pragma unroll
-                        for (int e = 0; e < 32; e += 4) {
-                            const float4 gv = *reinterpret_cast<const float4 *>(vec + 2 * KEYS + 32 * c + e);
-                            const float p0 = ex2(u[e] - m), p1 = ex2(u[e + 1] - m), p2 = ex2(u[e + 2] - m),
-                                        p3 = ex2(u[e + 3] - m);
-                            s0 = fmaf(p0, gv.x, s0);
-                            s1 = fmaf(p1, gv.y, s1);
-                            s2 = fmaf(p2, gv.z, s2);
-                            s3 = fmaf(p3, gv.w, s3);
-                            w[e / 2] = pack_f16(p0, p1);
-                            w[e / 2 + 1] = pack_f16(p2, p3);
+                        for (int e = 0; e < 32; e += 2) {
+                            float2 v = fma2(make_float2(__uint_as_float(x[e]), __uint_as_float(x[e + 1])), A2, B2);
+                            v.x = ex2(v.x);
+                            v.y = ex2(v.y);
+                            sum = add2(sum, v);
+                            w[e / 2] = pack_f16(v.x, v.y);
                         }
-                        sum += (s0 + s1) + (s2 + s3);
                         tmem_st_32x32b_x16(t_s + 16 * c, w);
                     }
                 }
@@ -405,7 +445,7 @@ tmem_st_wait();
                     }
                     M = m;
                 }
-                l += sum;
+                l = fmaf(sum.x + sum.y, meta.v_factor, l);
                 tmem_st_wait();
                 tc_fence_before();
                 mbar_arrive(&bar.pfull[g & 1]);
@@ -446,11 +486,10 @@ tmem_st_wait();
         const int x7 = row & 7;
         int g = 0;
         bool bad = false;
-        for (int round = 0; round * static_cast<int>(gridDim.x) < items; ++round) {
-            const int index = index_of(round);
-            if (index >= items) continue;
-            const Item it = item_of(a, cum, index, G);
-            if (it.n == 0) continue;
+        for (int k_item = 0;; ++k_item) {
+            const int index = item_at(k_item);
+            if (index >= items) break;
+            const Item it = item_of(a, cum, order, index, G);
             // this warp's cache tile of key tile i (null: nothing there)
             auto tile_of = [&](int i) -> const unsigned char * {
                 if (i >= it.n) return nullptr;
@@ -489,42 +528,64 @@ tmem_st_wait();
                 }
             };
             auto valid = [&](int i, const unsigned char *t) { return t != nullptr && it.key0(i) + row < it.end; };
-            // exponent that brings the largest scale of the groups to [0.5, 1)
-            auto exponent = [](const uint32_t (&par)[G64]) -> int {
-                float top = 0.f;
+            // largest scale of this lane's groups, as its bits
+            auto peak = [](const uint32_t (&par)[G64]) -> unsigned {
+                unsigned top = 0;
 #pragma unroll
-                for (int i = 0; i < G64; ++i) top = fmaxf(top, fabsf(f16_lo(par[i])));
-                return top > 0.f ? static_cast<int>(__float_as_uint(top) >> 23) - 126 : 0;
+                for (int i = 0; i < G64; ++i) top = max(top, par[i] & 0x7fffu);
+                return top;
             };
-            auto put = [&](const uint4 (&raw)[G64], const uint32_t (&par)[G64], int e, unsigned char *rowp) {
-                const float down = pow2(-e);
+            // e with scale < 2^e
+            auto exponent = [](unsigned bits) -> int {
+                return bits ? static_cast<int>(__float_as_uint(f16_lo(bits)) >> 23) - 126 : 0;
+            };
+            auto put = [&](const uint4 (&raw)[G64], const uint32_t (&par)[G64], float up, unsigned char *rowp) {
 #pragma unroll
                 for (int i = 0; i < G64; ++i) {
-                    const float s = f16_lo(par[i]) * down, z = f16_hi(par[i]);
+                    const float s = f16_lo(par[i]) * up, z = f16_hi(par[i]);
                     form(raw[i], pack_f16(s, s), pack_f16(-1024.f - z, -1024.f - z), pack_f16(-64.f - z, -64.f - z),
                          rowp + i * SUB, x7, half);
                 }
             };
-            // K of tile number i (g + i over all items), with the key's factors
-            auto put_k = [&](int i, bool on) {
-                const int e = exponent(kpar), ev = exponent(vnext);
+            float v_up = 0.f, v_up_next = 0.f;
+            // K of tile number i (g + i over all items), with what the softmax
+            // has to know of the tile
+            auto put_k = [&](int i, bool there) {
                 const int gi = g + i;
+                unsigned *const peaks = reinterpret_cast<unsigned *>(smem + L::peak) + (gi & 1) * 2 * FORM_WARPS;
+                const unsigned pk = __reduce_max_sync(0xffffffffu, peak(kpar)), pv = __reduce_max_sync(0xffffffffu, peak(vnext));
+                if (lane == 0) {
+                    peaks[w] = pk;
+                    peaks[FORM_WARPS + w] = pv;
+                }
+                named_bar_sync(1, FORM_THREADS);
+                unsigned tk = 0, tv = 0;
+#pragma unroll
+                for (int o = 0; o < FORM_WARPS; ++o) {
+                    tk = max(tk, peaks[o]);
+                    tv = max(tv, peaks[FORM_WARPS + o]);
+                }
+                const int ek = exponent(tk) - 11, ev = exponent(tv) - 11;
+                v_up = v_up_next;
+                v_up_next = pow2(-ev);
                 if (gi > 0) mbar_wait(&bar.kfree, (gi - 1) & 1, a.status);
-                put(kraw, kpar, e, krow);
-                if (half == 0) {
-                    float *const vec = reinterpret_cast<float *>(smem + L::vec) + (gi % VECS) * 3 * KEYS + row;
-                    vec[0] = on ? pow2(e) : 0.f;
-                    vec[KEYS] = on ? static_cast<float>(ev) : -INFINITY;
-                    vec[2 * KEYS] = on ? pow2(-ev) : 0.f;
+                put(kraw, kpar, pow2(-ek), krow);
+                if (lane == 0) {
+                    Meta &meta = reinterpret_cast<Meta *>(smem + L::meta)[gi % METAS];
+                    meta.there[w] = there;
+                    if (w == 0) {
+                        meta.k_factor = pow2(ek);
+                        meta.v_exponent = static_cast<float>(ev);
+                        meta.v_factor = pow2(-ev);
+                    }
                 }
                 fence_proxy_async_smem();
                 mbar_arrive(&bar.kfull);
             };
-            auto put_v = [&](int i) {
-                const int e = exponent(vpar);
+            auto put_v = [&](int i, float up) {
                 const int gi = g + i;
                 if (gi > 0) mbar_wait(&bar.vfree, (gi - 1) & 1, a.status);
-                put(vraw, vpar, e, vrow);
+                put(vraw, vpar, up, vrow);
                 fence_proxy_async_smem();
                 mbar_arrive(&bar.vfull);
             };
@@ -537,12 +598,12 @@ tmem_st_wait();
             for (int i = 0; i <= it.n; ++i) {
                 const unsigned char *t2 = tile_of(i + 2);
                 if (i < it.n) {
-                    put_k(i, valid(i, t0));
+                    put_k(i, t0 != nullptr);
                     load_k(t1, valid(i + 1, t1));
                     load_vpar(t1, valid(i + 1, t1));
                 }
                 if (i > 0) {
-                    put_v(i - 1);
+                    put_v(i - 1, i < it.n ? v_up : v_up_next);
                     load_v(t0, valid(i, t0));
                 }
                 t0 = t1;
@@ -554,7 +615,7 @@ tmem_st_wait();
     } else {
         // ------------------------------------------------------- products
         const uint32_t qa = smem_u32(smem + L::q), ka = smem_u32(smem + L::k), va = smem_u32(smem + L::v);
-        int g = 0, done = 0;
+        int g = 0;
         auto qk = [&](int gi) {
             mbar_wait(&bar.kfull, gi & 1, a.status);
             tc_fence_after();
@@ -577,19 +638,41 @@ tmem_st_wait();
                                   !(first && k == 0));
             umma_commit_w(&bar.vfree);
         };
-        for (int round = 0; round * static_cast<int>(gridDim.x) < items; ++round) {
-            const int index = index_of(round);
-            if (index >= items) continue;
-            const Item it = item_of(a, cum, index, G);
-            if (it.n == 0) continue;
-            mbar_wait(&bar.qfull, done & 1, a.status);
-            ++done;
+        auto announce = [&](int k, int index) {
+            if (lane == 0) {
+                bar.item[k % QUEUE] = index;
+                mbar_arrive(&bar.ifull[k % QUEUE]);
+            }
+            __syncwarp();
+        };
+        // the first item is the CTA's number, the others come from the counter;
+        // one is fetched ahead.  A slot of the ring is written again four items
+        // later, when every role has left it: the softmax is at most an item
+        // behind, and the forming warps are ahead.
+        int index = static_cast<int>(blockIdx.x);
+        announce(0, index);
+        for (int k = 0; index < items; ++k) {
+            int next = 0;
+            if (lane == 0) next = static_cast<int>(gridDim.x + atomicAdd(counter, 1u));
+            next = __shfl_sync(0xffffffffu, next, 0);
+            announce(k + 1, next);
+            const Item it = item_of(a, cum, order, index, G);
+            index = next;
+            mbar_wait(&bar.qfull, k & 1, a.status);
 #pragma unroll 1
             for (int i = 0; i <= it.n; ++i) {
                 if (i < it.n) qk(g + i);
                 if (i > 0) pv(g + i - 1, i == 1);
             }
             g += it.n;
+        }
+        // the last CTA to run out of items leaves the counters at zero
+        if (lane == 0) {
+            __threadfence();
+            if (atomicAdd(counter + 1, 1u) == gridDim.x - 1) {
+                counter[0] = 0;
+                counter[1] = 0;
+            }
         }
         // tensor memory is released only when every product has completed
         if (g > 0) mbar_wait(&bar.vfree, (g - 1) & 1, nullptr);
@@ -604,7 +687,7 @@ tmem_st_wait();
 
 template <int D>
 cudaError_t launch(const Kv4AttnArgs &a, cudaStream_t st, const DeviceInfo &dev) {
-    const int smem = 1024 + PromptSmem<D>::cum + (a.requests + 1) * 4;
+    const int smem = 1024 + PromptSmem<D>::cum + (2 * a.requests + 1) * 4;
     if (smem > dev.max_smem_optin) return cudaErrorNotSupported;
     static SmemLimit limit;
     if (cudaError_t e = limit.ensure(reinterpret_cast<const void *>(attn_prompt_kernel<D>), dev.device, smem)) return e;
