@@ -304,6 +304,8 @@ __global__ void __launch_bounds__(THREADS, 1) attn_prompt_kernel(const Kv4AttnAr
         const uint32_t t_row = tmem + (static_cast<uint32_t>(warp * 32) << 16);
         unsigned char *const qrow = smem + L::q + r * 128;
         int g = 0;  // key tiles so far, over all items
+        const int window = static_cast<int>(min(a.window, int64_t(0x7fffffff)));
+        const int sinks = a.window > 0 ? static_cast<int>(min(a.sinks, int64_t(0x7fffffff))) : 0;
         // Q of an item: this thread's row; returns the factor of its scores
         auto build = [&](const Item &it) -> float {
             const bool on = r < it.rows;
@@ -362,51 +364,53 @@ __global__ void __launch_bounds__(THREADS, 1) attn_prompt_kernel(const Kv4AttnAr
                 tc_fence_after();
                 const uint2 there = *reinterpret_cast<const uint2 *>(meta.there);
                 const bool free = (there.x & there.y) == 0x01010101u && j0 + KEYS <= p_lo + 1 &&
-                                  (a.window <= 0 || p_hi - j0 < a.window || j0 + KEYS <= a.sinks);
+                                  (window == 0 || p_hi - j0 < window || j0 + KEYS <= sinks);
                 const float A = Fr * meta.k_factor, B = meta.v_exponent;
-                // 32 keys at a time: scores in, weights out into the columns of
+                // 64 keys at a time: scores in, weights out into the columns of
                 // scores already read (half as wide)
                 float m = M, scaled = 1.f;
-                float2 sum = make_float2(0.f, 0.f);
-                uint32_t s[2][32];
-                tmem_ld_32x32b_x32(t_s, s[0]);
+                float2 sum = make_float2(0.f, 0.f), sum1 = sum;
 #pragma unroll 1
-                for (int cc = 0; cc < KEYS / 32; cc += 2) {
+                for (int c = 0; c < 2; ++c) {
+                    uint32_t x[2][32];
+                    tmem_ld_32x32b_x32(t_s + 64 * c, x[0]);
+                    tmem_ld_32x32b_x32(t_s + 64 * c + 32, x[1]);
+                    tmem_ld_wait();
+                    if (!free) {
+                        // keys from .. upto of these 64 are seen, and those before `first`
+                        const int at = j0 + 64 * c;
+                        const int upto = min(p + 1, cur.end) - at, from = window == 0 ? 0 : p - window + 1 - at, first = sinks - at;
+                        const uint32_t pages = c ? there.y : there.x;
 #pragma unroll
-                    for (int half = 0; half < 2; ++half) {
-                        const int c = cc + half;
-                        tmem_ld_wait();
-                        if (c + 1 < KEYS / 32) tmem_ld_32x32b_x32(t_s + 32 * (c + 1), s[half ^ 1]);
-                        uint32_t(&x)[32] = s[half];
-                        if (!free) {
-#pragma unroll
-                            for (int e = 0; e < 32; ++e) {
-                                const int j = j0 + 32 * c + e;
-                                const bool see = j <= p && j < cur.end && meta.there[2 * c + e / 16] &&
-                                                 (a.window <= 0 || p - j < a.window || j < a.sinks);
-                                x[e] = see ? x[e] : 0xff800000u;  // -infinity
-                            }
+                        for (int e = 0; e < 64; ++e) {
+                            const bool see = e < upto && (e >= from || e < first) && (pages >> (8 * (e / 16)) & 1u);
+                            x[e >> 5][e & 31] = see ? x[e >> 5][e & 31] : 0xff800000u;  // -infinity
                         }
-                        float top = __uint_as_float(x[0]), top1 = __uint_as_float(x[1]);
+                    }
+                    float top[4];
 #pragma unroll
-                        for (int e = 2; e < 30; e += 4) {
-                            top = max3(top, __uint_as_float(x[e]), __uint_as_float(x[e + 1]));
-                            top1 = max3(top1, __uint_as_float(x[e + 2]), __uint_as_float(x[e + 3]));
-                        }
-                        top = max3(top, __uint_as_float(x[30]), __uint_as_float(x[31]));
-                        const float mx = fmaf(fmaxf(top, top1), A, B);
-                        if (__any_sync(0xffffffffu, mx > m + 8.f)) {
-                            // the reference moves: what this tile has written so far, its
-                            // sum, and (below) what earlier tiles left shrink with it
-                            const float up = fmaxf(m, ceilf(mx)), f = ex2(m - up);  // whole numbers: f is a power of two
-                            m = up;
-                            sum.x *= f;
-                            sum.y *= f;
-                            scaled *= f;
+                    for (int q = 0; q < 4; ++q) {
+                        const uint32_t *const y = &x[q >> 1][(q & 1) * 16];
+                        top[q] = fmaxf(__uint_as_float(y[0]), __uint_as_float(y[1]));
+#pragma unroll
+                        for (int e = 2; e < 16; e += 2) top[q] = max3(top[q], __uint_as_float(y[e]), __uint_as_float(y[e + 1]));
+                    }
+                    const float mx = fmaf(max3(fmaxf(top[0], top[1]), top[2], top[3]), A, B);
+                    if (__any_sync(0xffffffffu, mx > m + 8.f)) {
+                        // the reference moves: what this tile has written so far, its
+                        // sum, and (below) what earlier tiles left shrink with it
+                        const float up = fmaxf(m, ceilf(mx)), f = ex2(m - up);  // whole numbers: f is a power of two
+                        m = up;
+                        sum.x *= f;
+                        sum.y *= f;
+                        sum1.x *= f;
+                        sum1.y *= f;
+                        scaled *= f;
+                        if (c > 0) {
                             const uint32_t f2 = pack_f16(f, f);
                             tmem_st_wait();
 #pragma unroll 1
-                            for (int q = 0; q < c; ++q) {
+                            for (int q = 0; q < 2; ++q) {
                                 uint32_t w[16];
                                 tmem_ld_32x32b_x16(t_s + 16 * q, w);
                                 tmem_ld_wait();
@@ -415,17 +419,21 @@ __global__ void __launch_bounds__(THREADS, 1) attn_prompt_kernel(const Kv4AttnAr
                                 tmem_st_32x32b_x16(t_s + 16 * q, w);
                             }
                         }
-                        const float2 A2 = make_float2(A, A), B2 = make_float2(B - m, B - m);
+                    }
+                    const float2 A2 = make_float2(A, A), B2 = make_float2(B - m, B - m);
+#pragma unroll
+                    for (int q = 0; q < 2; ++q) {
                         uint32_t w[16];
 #pragma unroll
                         for (int e = 0; e < 32; e += 2) {
-                            float2 v = fma2(make_float2(__uint_as_float(x[e]), __uint_as_float(x[e + 1])), A2, B2);
+                            float2 v = fma2(make_float2(__uint_as_float(x[q][e]), __uint_as_float(x[q][e + 1])), A2, B2);
                             v.x = ex2(v.x);
                             v.y = ex2(v.y);
-                            sum = add2(sum, v);
+                            if (e & 2) sum1 = add2(sum1, v);
+                            else sum = add2(sum, v);
                             w[e / 2] = pack_f16(v.x, v.y);
                         }
-                        tmem_st_32x32b_x16(t_s + 16 * c, w);
+                        tmem_st_32x32b_x16(t_s + 32 * c + 16 * q, w);
                     }
                 }
                 if (__any_sync(0xffffffffu, m != M)) {
@@ -445,7 +453,7 @@ __global__ void __launch_bounds__(THREADS, 1) attn_prompt_kernel(const Kv4AttnAr
                     }
                     M = m;
                 }
-                l = fmaf(sum.x + sum.y, meta.v_factor, l);
+                l = fmaf((sum.x + sum.y) + (sum1.x + sum1.y), meta.v_factor, l);
                 tmem_st_wait();
                 tc_fence_before();
                 mbar_arrive(&bar.pfull[g & 1]);
@@ -484,25 +492,31 @@ __global__ void __launch_bounds__(THREADS, 1) attn_prompt_kernel(const Kv4AttnAr
         const int row = w * 16 + token;         // key row within the tile
         unsigned char *const krow = smem + L::k + row * 128, *const vrow = smem + L::v + row * 128;
         const int x7 = row & 7;
+        const size_t page_bytes = (static_cast<size_t>(a.Hkv) << (a.bs_log2 - 4)) * kv4_tile_bytes(D);
         int g = 0;
         bool bad = false;
         for (int k_item = 0;; ++k_item) {
             const int index = item_at(k_item);
             if (index >= items) break;
             const Item it = item_of(a, cum, order, index, G);
-            // this warp's cache tile of key tile i (null: nothing there)
-            auto tile_of = [&](int i) -> const unsigned char * {
+            // this warp's cache tile of key tile i: the page is asked for a step
+            // before it is looked at (-1: nothing there)
+            const int32_t *const pages = a.block_table + static_cast<int64_t>(it.b) * a.max_blocks;
+            auto page_of = [&](int i) -> int {
+                if (i >= it.n) return -1;
+                const int j = it.key0(i) + w * 16;
+                return j < it.end ? pages[j >> a.bs_log2] : -1;
+            };
+            auto tile_of = [&](int i, int id) -> const unsigned char * {
                 if (i >= it.n) return nullptr;
                 const int j = it.key0(i) + w * 16;
                 if (j >= it.end) return nullptr;
-                const int id = a.block_table[static_cast<int64_t>(it.b) * a.max_blocks + (j >> a.bs_log2)];
                 if (id < 0 || id >= a.num_blocks) {
                     bad = true;
                     return nullptr;
                 }
-                const int sub = (j & ((1 << a.bs_log2) - 1)) >> 4;
-                return a.cache + (((static_cast<size_t>(id) * a.Hkv + it.h) << (a.bs_log2 - 4)) + sub) *
-                                     static_cast<size_t>(kv4_tile_bytes(D));
+                const int off = ((it.h << (a.bs_log2 - 4)) + ((j & ((1 << a.bs_log2) - 1)) >> 4)) * kv4_tile_bytes(D);
+                return a.cache + static_cast<size_t>(id) * page_bytes + off;
             };
             uint4 kraw[G64], vraw[G64];
             uint32_t kpar[G64], vpar[G64];
@@ -590,15 +604,17 @@ __global__ void __launch_bounds__(THREADS, 1) attn_prompt_kernel(const Kv4AttnAr
                 mbar_arrive(&bar.vfull);
             };
             // K(i), then V(i - 1); the loads run one tile ahead
-            const unsigned char *t0 = tile_of(0), *t1 = tile_of(1);
+            int id1 = page_of(1);
+            const unsigned char *t0 = tile_of(0, page_of(0)), *t1 = nullptr;
             load_k(t0, valid(0, t0));
             load_vpar(t0, valid(0, t0));
             load_v(t0, valid(0, t0));
 #pragma unroll 1
             for (int i = 0; i <= it.n; ++i) {
-                const unsigned char *t2 = tile_of(i + 2);
+                const int id2 = page_of(i + 2);
                 if (i < it.n) {
                     put_k(i, t0 != nullptr);
+                    t1 = tile_of(i + 1, id1);
                     load_k(t1, valid(i + 1, t1));
                     load_vpar(t1, valid(i + 1, t1));
                 }
@@ -607,7 +623,8 @@ __global__ void __launch_bounds__(THREADS, 1) attn_prompt_kernel(const Kv4AttnAr
                     load_v(t0, valid(i, t0));
                 }
                 t0 = t1;
-                t1 = t2;
+                t1 = nullptr;
+                id1 = id2;
             }
             g += it.n;
         }
