@@ -11,11 +11,17 @@
 // BF16 value, so the fused call stores bit for bit what the norm followed by
 // a plain append stores.
 //
-// All of it is bound by memory (a few operations per 2-byte element).  A head
-// is held by D / 8 lanes of a warp, 8 elements (one 16-byte load) per lane:
-// the norm's sum, the rotation's partner (a lane rot / 16 away, or the lane
-// itself for interleaved pairs) and a group's extremes are shuffles, and a
-// lane's 8 codes are one 32-bit word of the cache's 32-byte rows.
+// All of it is bound by memory once there are enough tokens (by the launch
+// before that).  A head is held by D / 8 lanes of a warp, 8 elements (one
+// 16-byte load) per lane: the norm's sum, the rotation's partner (a lane
+// rot / 16 away, or the lane itself for interleaved pairs) and a group's
+// extremes are shuffles, and a lane's 8 codes are one 32-bit word of the
+// cache's 32-byte rows.  A warp takes U x 256 / D heads of one token, all
+// loads first: with U = 4 each lane has 64 bytes under way and a token's
+// cosines and sines are read once for them; with few tokens U = 1 spreads the
+// heads over more warps.  Four CTAs of 256 threads per SM hold it best: 4099
+// tokens of 40 heads of 128 take 25.5 us, with registers for three or five
+// 28.4 and 39.7, with U = 2 27.7.
 #include "common.cuh"
 #include "kernels.h"
 #include "kv4.cuh"
@@ -44,9 +50,14 @@ __device__ __forceinline__ uint4 pack8(const float (&x)[8]) {
 }
 
 // Quantises this lane's 8 elements (8 lanes hold a group of 64) and stores
-// the code word and, from the group's first lane, the parameters.
-// Division, rounding and addition are the IEEE operations one by one (no
-// contraction), so that the codes are those of the formula in binary32.
+// the code word and, from the group's first lane, the parameters.  Quotients
+// are the correctly rounded ones of binary32, x / s by Markstein's correction
+// (P. Markstein, "Computation of elementary functions on the IBM RISC
+// System/6000 processor", 1990): y the rounded reciprocal, q = x y rounded,
+// the remainder x - q s exact in a fused multiply-add, q + r y rounded.  Adding
+// 1.5 2^23 rounds to the nearest whole number, ties to even, and leaves it in
+// the low bits.  A group whose scale is at its limit (values beyond 15 x
+// 65504, infinities) takes the plain division.
 template <int D>
 __device__ __forceinline__ void quantise_store(const float (&x)[8], unsigned char *tile, int part, int l, int row,
                                                bool store) {
@@ -65,13 +76,23 @@ __device__ __forceinline__ void quantise_store(const float (&x)[8], unsigned cha
     const float s = __half2float(sh);
     uint32_t word = 0;
     float z = 0.f;
-    if (s > 0.f) {
+    if (s >= 65504.f) {
         z = __fadd_rn(fminf(fmaxf(rintf(__fdiv_rn(-lo, s)), 0.f), 15.f), 0.f);  // never -0
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
             const float c = fminf(fmaxf(__fadd_rn(rintf(__fdiv_rn(x[i], s)), z), 0.f), 15.f);
             word |= static_cast<uint32_t>(c) << (4 * i);
         }
+    } else if (s > 0.f) {
+        const float inv = __frcp_rn(s);
+        auto whole = [&](float v) -> int {
+            const float q = v * inv;
+            return __float_as_int(__fadd_rn(fmaf(fmaf(-q, s, v), inv, q), 12582912.f)) - 0x4b400000;
+        };
+        const int zi = min(max(whole(-lo), 0), 15);
+        z = static_cast<float>(zi);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) word |= static_cast<uint32_t>(min(max(whole(x[i]) + zi, 0), 15)) << (4 * i);
     }
     if (!store) return;
     const int group = l >> 3;
@@ -82,150 +103,172 @@ __device__ __forceinline__ void quantise_store(const float (&x)[8], unsigned cha
             static_cast<uint32_t>(__half_as_ushort(__float2half_rn(z))) << 16;
 }
 
-// A unit is one head of one token; 32 / LPH units per warp, in the order
-// token, then q heads, k heads, v heads.
-template <int D>
-__global__ void __launch_bounds__(ROPE_THREADS) rope_kernel(const Kv4RopeArgs a) {
-    constexpr int LPH = D / 8;  // lanes per head
+// A task is U x 32 / LPH heads of one token, in the order q heads, k heads, v
+// heads; `tasks` of them per token.
+template <int D, int U>
+__global__ void __launch_bounds__(ROPE_THREADS, 4) rope_kernel(const Kv4RopeArgs a, const unsigned tasks) {
+    constexpr int LPH = D / 8;   // lanes per head
+    constexpr int HPS = 32 / LPH;
     pdl_launch_dependents();
     pdl_wait();
     const int lane = threadIdx.x & 31;
     const int l = lane % LPH;
-    const unsigned heads = a.Hq + a.Hk + a.Hv;
-    const unsigned units = static_cast<unsigned>(a.T) * heads;
-    const unsigned step = gridDim.x * (ROPE_THREADS / LPH);
-    const unsigned first = blockIdx.x * (ROPE_THREADS / LPH) + (threadIdx.x >> 5) * (32 / LPH);
+    const int heads = a.Hq + a.Hk + a.Hv;
+    const int half = a.rot >> 1, hl = half >> 3;  // lanes of half a rotation
     bool bad = false;
-    // the whole warp takes part in every shuffle: lanes without a unit go
-    // along on the last one and store nothing
-    for (unsigned u0 = first; u0 < units; u0 += step) {
-        const unsigned mine = u0 + lane / LPH;
-        const bool live = mine < units;
-        const unsigned u = live ? mine : units - 1;
-        const unsigned t = u / heads;
-        const int h = static_cast<int>(u - t * heads);
-        const bool is_q = h < a.Hq, is_v = h >= a.Hq + a.Hk;
-        const uint16_t *src = is_q   ? a.q + t * a.q_stride + h * D
-                              : is_v ? a.v + t * a.v_stride + (h - a.Hq - a.Hk) * D
-                                     : a.k + t * a.k_stride + (h - a.Hq) * D;
-        float x[8];
-        unpack8(*reinterpret_cast<const uint4 *>(src + 8 * l), x);
-        const uint16_t *w = is_q ? a.q_weight : is_v ? nullptr : a.k_weight;
-        float ss = 0.f;
+    for (unsigned task = blockIdx.x * (ROPE_THREADS / 32) + (threadIdx.x >> 5); task < static_cast<unsigned>(a.T) * tasks;
+         task += gridDim.x * (ROPE_THREADS / 32)) {
+        const unsigned t = task / tasks;
+        const int h0 = static_cast<int>(task - t * tasks) * (U * HPS) + lane / LPH;
+        // the whole warp takes part in every shuffle: lanes past the last head
+        // go along on it and store nothing
+        uint4 raw[U];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) ss = fmaf(x[i], x[i], ss);
-#pragma unroll
-        for (int o = 1; o < LPH; o <<= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-        if (w) {
-            const float r = rsqrtf(ss * (1.f / D) + a.eps);
-            float wv[8];
-            unpack8(*reinterpret_cast<const uint4 *>(w + 8 * l), wv);
-#pragma unroll
-            for (int i = 0; i < 8; ++i) x[i] = x[i] * r * (wv[i] + a.weight_offset);
+        for (int k = 0; k < U; ++k) {
+            const int h = min(h0 + k * HPS, heads - 1);
+            const uint16_t *src = h < a.Hq          ? a.q + t * a.q_stride + h * D
+                                  : h < a.Hq + a.Hk ? a.k + t * a.k_stride + (h - a.Hq) * D
+                                                    : a.v + t * a.v_stride + (h - a.Hq - a.Hk) * D;
+            raw[k] = *reinterpret_cast<const uint4 *>(src + 8 * l);
         }
+        int64_t slot = -1;
+        if (a.cache) slot = a.slots[t];
         bool skip = false;  // a row whose position names none: written as zeros
+        float cc[8], sn[8];
+        const bool low = l < hl;
         if (a.cos_sin) {
             const int pos = a.positions[t];
-            const bool in = pos >= 0 && pos < a.num_positions;
-            bad |= live && pos >= a.num_positions;
-            skip = !in;
-            const float *cs = a.cos_sin + static_cast<size_t>(in ? pos : 0) * a.rot;
-            const int half = a.rot >> 1;
-            if (a.interleaved) {
-                if (!is_v && 8 * l < a.rot) {
-                    const float4 c = *reinterpret_cast<const float4 *>(cs + 4 * l);
-                    const float4 s = *reinterpret_cast<const float4 *>(cs + half + 4 * l);
-                    const float cc[4] = {c.x, c.y, c.z, c.w}, sn[4] = {s.x, s.y, s.z, s.w};
+            skip = pos < 0 || pos >= a.num_positions;
+            bad |= pos >= a.num_positions;
+            const float *cs = a.cos_sin + static_cast<size_t>(skip ? 0 : pos) * a.rot;
+            const int at = a.interleaved ? 4 * l : 8 * (low ? l : l - hl);
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const float p = x[2 * i], q = x[2 * i + 1];
-                        x[2 * i] = p * cc[i] - q * sn[i];
-                        x[2 * i + 1] = q * cc[i] + p * sn[i];
-                    }
+            for (int i = 0; i < 2; ++i) {
+                float4 c = make_float4(1.f, 1.f, 1.f, 1.f), s = make_float4(0.f, 0.f, 0.f, 0.f);
+                if (l < 2 * hl && (i == 0 || !a.interleaved)) {
+                    c = *reinterpret_cast<const float4 *>(cs + at + 4 * i);
+                    s = *reinterpret_cast<const float4 *>(cs + half + at + 4 * i);
                 }
-            } else {
-                const int hl = half >> 3;  // lanes of half a rotation
-                const bool low = l < hl;
-                const int from = (lane - l) + (l < 2 * hl ? (low ? l + hl : l - hl) : l);
-                float y[8];
-#pragma unroll
-                for (int i = 0; i < 8; ++i) y[i] = __shfl_sync(0xffffffffu, x[i], from);
-                if (!is_v && l < 2 * hl) {
-                    const int at = 8 * (low ? l : l - hl);
-                    float cc[8], sn[8];
-#pragma unroll
-                    for (int i = 0; i < 2; ++i) {
-                        const float4 c = *reinterpret_cast<const float4 *>(cs + at + 4 * i);
-                        const float4 s = *reinterpret_cast<const float4 *>(cs + half + at + 4 * i);
-                        cc[4 * i] = c.x, cc[4 * i + 1] = c.y, cc[4 * i + 2] = c.z, cc[4 * i + 3] = c.w;
-                        sn[4 * i] = s.x, sn[4 * i + 1] = s.y, sn[4 * i + 2] = s.z, sn[4 * i + 3] = s.w;
-                    }
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) x[i] = low ? x[i] * cc[i] - y[i] * sn[i] : x[i] * cc[i] + y[i] * sn[i];
-                }
+                cc[4 * i] = c.x, cc[4 * i + 1] = c.y, cc[4 * i + 2] = c.z, cc[4 * i + 3] = c.w;
+                sn[4 * i] = s.x, sn[4 * i + 1] = s.y, sn[4 * i + 2] = s.z, sn[4 * i + 3] = s.w;
             }
         }
-        const uint4 packed = (skip && !is_v) ? make_uint4(0, 0, 0, 0) : pack8(x);
-        if (is_q) {
-            if (live)
-                *reinterpret_cast<uint4 *>(a.q_out + (static_cast<size_t>(t) * a.Hq + h) * D + 8 * l) = packed;
-        } else if (!a.cache) {
-            if (live)
-                *reinterpret_cast<uint4 *>(a.k_out + (static_cast<size_t>(t) * a.Hk + (h - a.Hq)) * D + 8 * l) = packed;
-        }
-        if (a.cache) {
+#pragma unroll
+        for (int k = 0; k < U; ++k) {
+            const bool live = h0 + k * HPS < heads;
+            const int h = min(h0 + k * HPS, heads - 1);
+            const bool is_q = h < a.Hq, is_v = h >= a.Hq + a.Hk;
+            uint4 packed = raw[k];
+            float x[8];
             unpack8(packed, x);
-            const int64_t slot = a.slots[t];
-            const bool in = slot >= 0 && slot < a.num_slots;
-            bad |= live && slot >= a.num_slots;
-            // all lanes form codes (the shuffles need the whole warp); heads of q and tokens without a slot
-            // point at the first tile and do not store
-            const int hk = is_q ? 0 : is_v ? h - a.Hq - a.Hk : h - a.Hq;
-            unsigned char *tile = a.cache + kv4_tile_offset(in ? slot : 0, hk, a.Hv, a.bs_log2, D);
-            quantise_store<D>(x, tile, is_v ? 1 : 0, l, static_cast<int>(slot & 15), live && in && !is_q);
+            const uint16_t *w = is_q ? a.q_weight : is_v ? nullptr : a.k_weight;
+            if (a.q_weight || a.k_weight) {
+                float ss = 0.f;
+#pragma unroll
+                for (int i = 0; i < 8; ++i) ss = fmaf(x[i], x[i], ss);
+#pragma unroll
+                for (int o = 1; o < LPH; o <<= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+                if (w) {
+                    const float r = rsqrtf(ss * (1.f / D) + a.eps);
+                    float wv[8];
+                    unpack8(*reinterpret_cast<const uint4 *>(w + 8 * l), wv);
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) x[i] = x[i] * r * (wv[i] + a.weight_offset);
+                }
+            }
+            if (a.cos_sin) {
+                if (a.interleaved) {
+                    if (!is_v && l < 2 * hl) {
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            const float p = x[2 * i], q = x[2 * i + 1];
+                            x[2 * i] = p * cc[i] - q * sn[i];
+                            x[2 * i + 1] = q * cc[i] + p * sn[i];
+                        }
+                    }
+                } else {
+                    const int from = (lane - l) + (l < 2 * hl ? (low ? l + hl : l - hl) : l);
+                    float y[8];
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) y[i] = __shfl_sync(0xffffffffu, x[i], from);
+                    if (!is_v && l < 2 * hl) {
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) x[i] = low ? x[i] * cc[i] - y[i] * sn[i] : x[i] * cc[i] + y[i] * sn[i];
+                    }
+                }
+            }
+            if (!is_v) packed = skip ? make_uint4(0, 0, 0, 0) : pack8(x);
+            if (is_q) {
+                if (live)
+                    *reinterpret_cast<uint4 *>(a.q_out + (static_cast<size_t>(t) * a.Hq + h) * D + 8 * l) = packed;
+            } else if (!a.cache) {
+                if (live)
+                    *reinterpret_cast<uint4 *>(a.k_out + (static_cast<size_t>(t) * a.Hk + (h - a.Hq)) * D + 8 * l) = packed;
+            }
+            if (a.cache) {
+                unpack8(packed, x);
+                const bool in = slot >= 0 && slot < a.num_slots;
+                bad |= slot >= a.num_slots;
+                // all lanes form codes (the shuffles need the whole warp); heads of q and tokens without a slot
+                // point at the first tile and do not store
+                const int hk = is_q ? 0 : is_v ? h - a.Hq - a.Hk : h - a.Hq;
+                unsigned char *tile = a.cache + kv4_tile_offset(in ? slot : 0, hk, a.Hv, a.bs_log2, D);
+                quantise_store<D>(x, tile, is_v ? 1 : 0, l, static_cast<int>(slot & 15), live && in && !is_q);
+            }
         }
     }
     if (__any_sync(0xffffffffu, bad) && lane == 0) atomicOr(a.status, kDevBadIndex);
 }
 
-// K and V of given slots as BF16 values (slots that name none: zeros).
-template <int D>
-__global__ void __launch_bounds__(ROPE_THREADS) gather_kernel(const Kv4GatherArgs a) {
-    constexpr int LPH = D / 8;
+// K and V of given slots as BF16 values (slots that name none: zeros); a task
+// is U x 32 / LPH of the 2 Hkv heads of one slot.
+template <int D, int U>
+__global__ void __launch_bounds__(ROPE_THREADS, 4) gather_kernel(const Kv4GatherArgs a, const unsigned tasks) {
+    constexpr int LPH = D / 8, HPS = 32 / LPH;
     pdl_launch_dependents();
     pdl_wait();
-    const int l = threadIdx.x % LPH;
-    const unsigned units = static_cast<unsigned>(a.T) * a.Hkv * 2;
+    const int lane = threadIdx.x & 31, l = lane % LPH;
     bool bad = false;
-    for (unsigned u = blockIdx.x * (ROPE_THREADS / LPH) + threadIdx.x / LPH; u < units;
-         u += gridDim.x * (ROPE_THREADS / LPH)) {
-        const unsigned t = u / (2 * a.Hkv);
-        const int r = static_cast<int>(u - t * 2 * a.Hkv);
-        const int part = r >= a.Hkv, h = part ? r - a.Hkv : r;
+    for (unsigned task = blockIdx.x * (ROPE_THREADS / 32) + (threadIdx.x >> 5); task < static_cast<unsigned>(a.T) * tasks;
+         task += gridDim.x * (ROPE_THREADS / 32)) {
+        const unsigned t = task / tasks;
+        const int h0 = static_cast<int>(task - t * tasks) * (U * HPS) + lane / LPH;
         const int64_t slot = a.slots[t];
-        uint4 out = make_uint4(0, 0, 0, 0);
-        if (slot >= 0 && slot < a.num_slots) {
-            const unsigned char *tile = a.cache + kv4_tile_offset(slot, h, a.Hkv, a.bs_log2, D);
-            const int at = (l >> 3) * KV4_TILE + static_cast<int>(slot & 15);
-            const uint32_t word = *reinterpret_cast<const uint32_t *>(tile + part * 8 * D + at * 32 + (l & 7) * 4);
-            const uint32_t sz = *reinterpret_cast<const uint32_t *>(tile + (16 + part) * D + at * 4);
-            const float s = f16_lo(sz), z = f16_hi(sz);
+        const bool in = slot >= 0 && slot < a.num_slots;
+        bad |= slot >= a.num_slots;
+        uint32_t word[U], sz[U];
+#pragma unroll
+        for (int k = 0; k < U; ++k) {
+            word[k] = sz[k] = 0;
+            const int r = h0 + k * HPS, part = r >= a.Hkv;
+            if (in && r < 2 * a.Hkv) {
+                const unsigned char *tile = a.cache + kv4_tile_offset(slot, part ? r - a.Hkv : r, a.Hkv, a.bs_log2, D);
+                const int at = (l >> 3) * KV4_TILE + static_cast<int>(slot & 15);
+                word[k] = *reinterpret_cast<const uint32_t *>(tile + part * 8 * D + at * 32 + (l & 7) * 4);
+                sz[k] = *reinterpret_cast<const uint32_t *>(tile + (16 + part) * D + at * 4);
+            }
+        }
+#pragma unroll
+        for (int k = 0; k < U; ++k) {
+            const int r = h0 + k * HPS, part = r >= a.Hkv;
+            if (r >= 2 * a.Hkv) continue;
+            const float s = f16_lo(sz[k]), z = f16_hi(sz[k]);
             float x[8];
 #pragma unroll
-            for (int i = 0; i < 8; ++i) x[i] = (static_cast<float>((word >> (4 * i)) & 15u) - z) * s;
-            out = pack8(x);
-        } else if (slot >= 0) bad = true;
-        *reinterpret_cast<uint4 *>((part ? a.v : a.k) + (static_cast<size_t>(t) * a.Hkv + h) * D + 8 * l) = out;
+            for (int i = 0; i < 8; ++i) x[i] = (static_cast<float>((word[k] >> (4 * i)) & 15u) - z) * s;
+            *reinterpret_cast<uint4 *>((part ? a.v : a.k) + (static_cast<size_t>(t) * a.Hkv + (part ? r - a.Hkv : r)) * D + 8 * l) =
+                pack8(x);
+        }
     }
     if (bad) atomicOr(a.status, kDevBadIndex);
 }
 
 template <typename Args>
-cudaError_t launch_units(void (*kern)(Args), const Args &a, int64_t units, int lph, cudaStream_t st,
-                         const DeviceInfo &dev) {
-    const int64_t per = ROPE_THREADS / lph;
-    int64_t grid = (units + per - 1) / per;
-    const int64_t most = 8 * static_cast<int64_t>(dev.num_sms);
+cudaError_t launch_tasks(void (*kern)(Args, unsigned), const Args &a, int64_t tokens, int64_t heads, int per_task,
+                         cudaStream_t st, const DeviceInfo &dev) {
+    const int64_t tasks = (heads + per_task - 1) / per_task;
+    int64_t grid = (tokens * tasks + ROPE_THREADS / 32 - 1) / (ROPE_THREADS / 32);
+    const int64_t most = 16 * static_cast<int64_t>(dev.num_sms);
     if (grid > most) grid = most;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(static_cast<unsigned>(grid));
@@ -236,23 +279,38 @@ cudaError_t launch_units(void (*kern)(Args), const Args &a, int64_t units, int l
     pdl[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = pdl;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, kern, a);
+    return cudaLaunchKernelEx(&cfg, kern, a, static_cast<unsigned>(tasks));
+}
+
+// Four 16-byte loads per lane once that still gives every SM a few warps.
+bool many(int64_t tokens, int64_t heads, int D, const DeviceInfo &dev) {
+    return tokens * heads * D >= int64_t(dev.num_sms) * 16 * 4 * 256;
 }
 
 }  // namespace
 
 cudaError_t launch_kv4_rope(const Kv4RopeArgs &a, int D, cudaStream_t st, const DeviceInfo &dev) {
-    const int64_t units = a.T * (a.Hq + a.Hk + a.Hv);
-    if (D == 64) return launch_units(rope_kernel<64>, a, units, 8, st, dev);
-    if (D == 128) return launch_units(rope_kernel<128>, a, units, 16, st, dev);
-    return launch_units(rope_kernel<256>, a, units, 32, st, dev);
+    const int64_t heads = a.Hq + a.Hk + a.Hv;
+    if (many(a.T, heads, D, dev)) {
+        if (D == 64) return launch_tasks(rope_kernel<64, 4>, a, a.T, heads, 16, st, dev);
+        if (D == 128) return launch_tasks(rope_kernel<128, 4>, a, a.T, heads, 8, st, dev);
+        return launch_tasks(rope_kernel<256, 4>, a, a.T, heads, 4, st, dev);
+    }
+    if (D == 64) return launch_tasks(rope_kernel<64, 1>, a, a.T, heads, 4, st, dev);
+    if (D == 128) return launch_tasks(rope_kernel<128, 1>, a, a.T, heads, 2, st, dev);
+    return launch_tasks(rope_kernel<256, 1>, a, a.T, heads, 1, st, dev);
 }
 
 cudaError_t launch_kv4_gather(const Kv4GatherArgs &a, int D, cudaStream_t st, const DeviceInfo &dev) {
-    const int64_t units = a.T * a.Hkv * 2;
-    if (D == 64) return launch_units(gather_kernel<64>, a, units, 8, st, dev);
-    if (D == 128) return launch_units(gather_kernel<128>, a, units, 16, st, dev);
-    return launch_units(gather_kernel<256>, a, units, 32, st, dev);
+    const int64_t heads = 2 * a.Hkv;
+    if (many(a.T, heads, D, dev)) {
+        if (D == 64) return launch_tasks(gather_kernel<64, 4>, a, a.T, heads, 16, st, dev);
+        if (D == 128) return launch_tasks(gather_kernel<128, 4>, a, a.T, heads, 8, st, dev);
+        return launch_tasks(gather_kernel<256, 4>, a, a.T, heads, 4, st, dev);
+    }
+    if (D == 64) return launch_tasks(gather_kernel<64, 1>, a, a.T, heads, 4, st, dev);
+    if (D == 128) return launch_tasks(gather_kernel<128, 1>, a, a.T, heads, 2, st, dev);
+    return launch_tasks(gather_kernel<256, 1>, a, a.T, heads, 1, st, dev);
 }
 
 }  // namespace w4
