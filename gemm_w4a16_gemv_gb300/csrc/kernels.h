@@ -177,7 +177,7 @@ struct Kv4AttnArgs {
     // no request
     int rows_most, rows_above, zero_rest;
 };
-constexpr int PROMPT_COUNTERS = 960;  // byte offset in the scratch of the prompt kernel's two counters
+constexpr int PROMPT_COUNTERS = 13056;  // byte offset in the scratch of the prompt kernel's two counters
 cudaError_t launch_kv4_prompt(const Kv4AttnArgs &a, int D, cudaStream_t st, const DeviceInfo &dev);
 int64_t kv4_attention_scratch(int Hq, int Hkv, int D);
 cudaError_t launch_kv4_attention(const Kv4AttnArgs &a, int D, cudaStream_t st, const DeviceInfo &dev);

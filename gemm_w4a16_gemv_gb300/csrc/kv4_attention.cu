@@ -10,28 +10,37 @@
 //
 // Work.  The unit is a cache tile (16 tokens of one head, one contiguous run
 // fetched by one bulk copy).  The visible tiles of all (request, row block,
-// head) segments are numbered in a row and split evenly over one CTA per SM,
-// so lengths of any raggedness, windows and one long request alike fill the
-// GPU.  Every CTA finds its share itself from the lengths (a prefix sum in
-// shared memory).  A segment that lies in one CTA is finished there; of one
-// that several CTAs share, each writes its partial result (maximum, sum,
-// weighted values) to scratch and the last to arrive joins them in the order
-// of the CTAs, so results do not depend on timing.  No CTA waits for another.
+// head) segments are numbered in a row and split evenly over teams, so lengths
+// of any raggedness, windows and one long request alike fill the GPU.  A team
+// is one warp where there are many segments (it joins nothing with its
+// neighbours but the segments at the ends of its share), a CTA's warps
+// together where there are few (joined in shared memory first, or one long
+// row would leave two thousand partial results).  Every team finds its share
+// itself from the lengths (a prefix sum in shared memory).  A segment inside
+// one share is finished there; of one that several share, each team writes its
+// partial result (maximum, sum, weighted values) to scratch and the last to
+// arrive joins them in the order of the teams, so results do not depend on
+// timing.  No team waits for another.
 //
-// A CTA's warps take its tiles in turn, each with its own ring of stages and
-// barriers: no producer warp and no barrier between warps inside a segment.
+// Each warp has its own ring of stages and barriers: no producer warp and no
+// barrier between warps inside a segment.
 //
 // Arithmetic per tile, all products on mma.m16n8k16 (binary16 in, binary32
 // out) with the CODES as the A operand: the low and high nibble pairs of a
 // word masked in place are binary16 subnormals c 2^-24 and 16 c 2^-24, exact,
 // so 8 codes cost 5 logic operations and no conversion.
-//   S^T = K Q^T (16 keys x 8 rows), a sum per group of 64 dimensions:
+//   S^T = K Q^T (16 keys x 8 columns), a sum per group of 64 dimensions:
 //     x += s (acc - z sum(q))                        binary32, exact products
 //     (q enters as binary16 after a power-of-two scale of its row)
-//   O^T += (V - z)^T P^T (16 dimensions x 8 rows), per group with P' = p s
+//   O^T += (V - z)^T P^T (16 dimensions x 8 columns), per group with P' = p s
 //     rounded to binary16.  Here code and zero are subtracted first (exact, a
 //     pair operation per two codes): summed apart, p c - p z would leave
 //     2^-24 of p z where a value is zero.
+// The 8 columns are rows of the segment, with accumulators for each group of
+// dimensions; or, where 8 / groups rows are enough (SPLIT), groups x rows: Q
+// and P' are zero outside their group, one set of accumulators serves all
+// groups (16 registers instead of 64 at D = 256), and each lane handles the
+// parameters of one group instead of all.
 // The reference of the exponentials is a running maximum of x + log2(s), so
 // that the largest P' is near 1 whatever the magnitude of V; it moves (and
 // the accumulators are scaled) only when it would grow by more than 2^8.
@@ -43,10 +52,15 @@ namespace w4 {
 namespace {
 
 constexpr int MAX_CTAS = 160;         // scratch is sized for this many
-constexpr int MAX_ROWS = 16;          // rows of a segment
-constexpr int COUNTER_BYTES = 1024;   // arrival counters at the head of the scratch
+constexpr int MAX_WARPS = 20;         // of a CTA
+constexpr int MAX_TEAMS = MAX_CTAS * MAX_WARPS;
+constexpr int COUNTER_BYTES = 13312;  // arrival counters and the prompt kernel's two
+static_assert(MAX_TEAMS * 4 <= PROMPT_COUNTERS && PROMPT_COUNTERS + 8 <= COUNTER_BYTES, "counters");
+// Partial results that two slots per team can need: warps x rows of an instance.
+constexpr int warp_rows(int D) { return D == 256 ? 128 : D == 128 ? 192 : 256; }
+constexpr int TEAM_RATIO = 8;         // warps to a segment up to which a warp is a team of its own
 constexpr int PROMPT_ROWS = 48;       // requests with more rows go to the tensor cores
-constexpr float NEG_INF = -INFINITY;
+constexpr float NONE = -1e30f;        // reference of a row that has seen no key
 
 __device__ __forceinline__ float ex2(float x) {
     float y;
@@ -79,6 +93,12 @@ __device__ __forceinline__ uint32_t mul_f16x2(uint32_t a, uint32_t b) {
 __device__ __forceinline__ uint32_t sub_f16x2(uint32_t a, uint32_t b) {
     uint32_t d;
     asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+    return d;
+}
+// The larger magnitude of each half, with some sign.
+__device__ __forceinline__ uint32_t maxabs_f16x2(uint32_t a, uint32_t b) {
+    uint32_t d;
+    asm("max.xorsign.abs.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
     return d;
 }
 __device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
@@ -169,41 +189,50 @@ struct Cursor {
     }
 };
 
-template <int D, int NT, int W>
-struct StreamSmem {
-    static constexpr int R = 8 * NT;
+// Shapes of an instance: D, columns' sets of 8, warps, warps of a team, and
+// whether the columns are split between groups and rows.
+template <int D, int NT, int W, int TEAM, bool SPLIT>
+struct Stream {
     static constexpr int G64 = D / 64;
-    static constexpr int MERGE_T = 2 * D + 4;                 // floats of a row pair
-    static constexpr int MERGE_WARP = NT * 4 * MERGE_T;       // floats of a warp
-    static constexpr int QFRAG = NT * G64 * 2 * 32 * 16;      // bytes: [NT][group][mma pair][lane] 4 words
-    // offsets in bytes
-    static constexpr int q = 0;                               // [2][QFRAG]
-    static constexpr int qs = q + 2 * QFRAG;                  // [2][G64][R] scaled row sums
-    static constexpr int fr = qs + 2 * G64 * R * 4;           // [2][R] factor of the scores
-    static constexpr int mx = fr + 2 * R * 4;                 // [2][W][R]
-    static constexpr int sm = mx + 2 * W * R * 4;             // [2][W][R]
-    static constexpr int misc = sm + 2 * W * R * 4;           // 64 bytes
-    static constexpr int bars = misc + 64;                    // [W][8] barriers
-    static constexpr int merge = (bars + W * 8 * 8 + 127) / 128 * 128;  // [W / 2][MERGE_WARP] floats
-    static constexpr int ring = (merge + W / 2 * MERGE_WARP * 4 + 127) / 128 * 128;
+    static constexpr int SETS = SPLIT ? 1 : G64;              // sets of accumulators
+    static constexpr int RPT = SPLIT ? 8 / G64 : 8;           // rows of 8 columns
+    static constexpr int R = RPT * NT;                        // rows of a segment
+    static constexpr int TEAMS = W / TEAM;                    // of a CTA
+    static constexpr int QBUF = TEAM == 1 ? 1 : 2;            // buffers of Q
+    static constexpr int QFRAG = NT * SETS * 2 * 32 * 16;     // bytes: [NT][set][mma pair][lane] 4 words
+    static constexpr int REGION = 2 * 64 + 4;                 // floats: two rows of 64 dimensions
+    static constexpr int MERGE_WARP = NT * SETS * 4 * REGION;
+    // per team, offsets in bytes
+    static constexpr int q = 0;                               // [QBUF][QFRAG]
+    static constexpr int qs = q + QBUF * QFRAG;               // [QBUF][SETS][8 NT] scaled row sums
+    static constexpr int fr = qs + QBUF * SETS * NT * 32;     // [QBUF][8 NT] factor of the scores
+    static constexpr int bars = fr + QBUF * NT * 32;          // [TEAM][8] barriers
+    static constexpr int team_bytes = (bars + TEAM * 64 + 15) / 16 * 16;
+    // of the CTA
+    static constexpr int teams = 128;                         // after 16 zero bytes and a word for the CTA
+    static constexpr int mx = teams + TEAMS * team_bytes;     // [2][W][R], or the prefix sum's W sums
+    static constexpr int sm = mx + (TEAM == 1 ? W * 8 : 2 * W * R * 4);
+    static constexpr int merge = (sm + (TEAM == 1 ? 0 : 2 * W * R * 4) + 127) / 128 * 128;  // [W / 2][MERGE_WARP] floats
+    static constexpr int ring = (merge + (TEAM == 1 ? 0 : W / 2 * MERGE_WARP * 4) + 127) / 128 * 128;
 };
 
-// Q of a segment as the MMA's B operand, by one warp per 8 rows: lane (g, t)
-// takes row g, 16 dimensions from 64 gi + 16 t on of each group.
-template <int D, int NT, int W>
-__device__ __forceinline__ void build_q(const Kv4AttnArgs &a, const Segment &s, int G, int nt, unsigned char *smem,
+// Q of 8 columns of a segment as the MMA's B operand, by one warp: lane (g, t)
+// takes column g, 16 dimensions from 64 i + 16 t on of its group(s).
+template <typename L, int D, bool SPLIT>
+__device__ __forceinline__ void build_q(const Kv4AttnArgs &a, const Segment &s, int G, int nt, int nts, unsigned char *team,
                                         int par, int lane) {
-    using L = StreamSmem<D, NT, W>;
     const int g = lane >> 2, t = lane & 3;
-    const int r = 8 * nt + g;
+    const int r = L::RPT * nt + g % L::RPT;
     const bool on = r < s.rows;
     const int row = s.r0 + (on ? r : 0);
     const int tok = rows_before(a, s.b) + row / G;
-    const uint16_t *src = a.q + static_cast<int64_t>(tok) * a.q_stride + static_cast<int64_t>(s.h * G + row % G) * D + 16 * t;
-    uint4 raw[L::G64][2];
+    const int own = SPLIT ? g / L::RPT : 0;  // group of the column
+    const uint16_t *src = a.q + static_cast<int64_t>(tok) * a.q_stride + static_cast<int64_t>(s.h * G + row % G) * D +
+                          64 * own + 16 * t;
+    uint4 raw[L::SETS][2];
     float big = 0.f;
 #pragma unroll
-    for (int i = 0; i < L::G64; ++i) {
+    for (int i = 0; i < L::SETS; ++i) {
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
             raw[i][k] = on ? *reinterpret_cast<const uint4 *>(src + 64 * i + 8 * k) : make_uint4(0, 0, 0, 0);
@@ -215,13 +244,17 @@ __device__ __forceinline__ void build_q(const Kv4AttnArgs &a, const Segment &s, 
     }
     big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, 1));
     big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, 2));
+    if (SPLIT) {  // the row's other groups are other columns
+        if (L::G64 == 4) big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, 8));
+        if (L::G64 >= 2) big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, 16));
+    }
     // the row's largest magnitude to [2^13, 2^14): the sums of the odd
     // dimensions' 1/16 stay exact down to 2^-33 of it
     int kappa = big > 0.f ? 13 - (static_cast<int>(__float_as_uint(big) >> 23) - 127) : 0;
     kappa = min(max(kappa, -110), 110);
     const float up = __uint_as_float(static_cast<uint32_t>(127 + kappa) << 23);
 #pragma unroll
-    for (int i = 0; i < L::G64; ++i) {
+    for (int i = 0; i < L::SETS; ++i) {
         float v[16], sum = 0.f;
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
@@ -236,8 +269,9 @@ __device__ __forceinline__ void build_q(const Kv4AttnArgs &a, const Segment &s, 
         sum += __shfl_xor_sync(0xffffffffu, sum, 1);
         sum += __shfl_xor_sync(0xffffffffu, sum, 2);
         if (t == 0)
-            reinterpret_cast<float *>(smem + L::qs)[(par * L::G64 + i) * L::R + r] = sum * 5.9604644775390625e-8f;  // 2^-24
-        uint4 *dst = reinterpret_cast<uint4 *>(smem + L::q + par * L::QFRAG) + (nt * L::G64 + i) * 2 * 32 + lane;
+            reinterpret_cast<float *>(team + L::qs)[(par * L::SETS + i) * 8 * nts + 8 * nt + g] =
+                sum * 5.9604644775390625e-8f;  // 2^-24
+        uint4 *dst = reinterpret_cast<uint4 *>(team + L::q + par * L::QFRAG) + (nt * L::SETS + i) * 2 * 32 + lane;
 #pragma unroll
         for (int k = 0; k < 2; ++k) {  // word k of the lane's two: dimensions 8 k .. 8 k + 7
             const float *x = v + 8 * k;
@@ -246,31 +280,38 @@ __device__ __forceinline__ void build_q(const Kv4AttnArgs &a, const Segment &s, 
         }
     }
     if (t == 0)
-        reinterpret_cast<float *>(smem + L::fr)[par * L::R + r] =
+        reinterpret_cast<float *>(team + L::fr)[par * 8 * nts + 8 * nt + g] =
             on ? a.scale * 1.4426950408889634f * (16777216.f * __uint_as_float(static_cast<uint32_t>(127 - kappa) << 23))
                : 0.f;
 }
 
-template <int D, int NT, int W>
+template <int D, int NT, int W, int TEAM, bool SPLIT>
 __global__ void __launch_bounds__(W * 32, 1) attn_stream_kernel(const Kv4AttnArgs a, const int depth) {
-    using L = StreamSmem<D, NT, W>;
-    constexpr int R = L::R, G64 = L::G64, TB = kv4_tile_bytes(D);
+    using L = Stream<D, NT, W, TEAM, SPLIT>;
+    constexpr int R = L::R, RPT = L::RPT, G64 = L::G64, SETS = L::SETS, TB = kv4_tile_bytes(D);
     extern __shared__ __align__(128) unsigned char smem[];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int g = lane >> 2, t = lane & 3;
     const int G = a.Hq / a.Hkv;
-    uint64_t *const bars = reinterpret_cast<uint64_t *>(smem + L::bars) + warp * 8;
+    const int tw = warp % TEAM;  // the warp's number in its team
+    unsigned char *const team = smem + L::teams + (warp / TEAM) * L::team_bytes;
+    uint64_t *const bars = reinterpret_cast<uint64_t *>(team + L::bars) + tw * 8;
     unsigned char *const ring = smem + L::ring + static_cast<size_t>(warp) * depth * TB;
     long long *const cum = reinterpret_cast<long long *>(smem + L::ring + static_cast<size_t>(W) * depth * TB);
-    volatile int *const misc = reinterpret_cast<volatile int *>(smem + L::misc);
+    volatile int *const misc = reinterpret_cast<volatile int *>(smem + 16);
+    auto team_sync = [&]() {
+        if (TEAM == 1) __syncwarp();
+        else __syncthreads();
+    };
 
+    if (tid < 4) reinterpret_cast<uint32_t *>(smem)[tid] = 0;
     if (lane == 0)
         for (int i = 0; i < depth; ++i) mbar_init(&bars[i], 1);
     fence_barrier_init();
     pdl_launch_dependents();
     pdl_wait();
 
-    // ---- this CTA's share: tiles of the requests, their running sum
+    // ---- tiles of the requests, their running sum
     {
         const int per = (a.requests + W * 32 - 1) / (W * 32);
         const int b0 = min(tid * per, a.requests), b1 = min(b0 + per, a.requests);
@@ -311,12 +352,15 @@ __global__ void __launch_bounds__(W * 32, 1) attn_stream_kernel(const Kv4AttnArg
              i += static_cast<int64_t>(gridDim.x) * W * 32)
             reinterpret_cast<uint4 *>(a.out)[i] = make_uint4(0, 0, 0, 0);
     }
-    // CTAs that take part: no more than there are tiles, so that none between
+    // teams that take part: no more than there are tiles, so that none between
     // the first and the last of a shared segment is without a part of it
-    const long long U = cum[a.requests], C = U < gridDim.x ? U : gridDim.x;
-    if (blockIdx.x >= C) return;
-    const long long u0 = U * blockIdx.x / C;
-    const int mine = static_cast<int>(U * (blockIdx.x + 1) / C - u0);
+    const long long U = cum[a.requests];
+    const long long all_teams = static_cast<long long>(gridDim.x) * L::TEAMS, C = U < all_teams ? U : all_teams;
+    // (neighbouring teams on different SMs: a small U fills them evenly)
+    const int me = static_cast<int>(blockIdx.x) + static_cast<int>(gridDim.x) * (warp / TEAM);
+    if (me >= C) return;
+    const long long u0 = U * me / C;
+    const int mine = static_cast<int>(U * (me + 1) / C - u0);
 
     // ---- the segment of the first tile
     Cursor<R> cur;
@@ -339,147 +383,174 @@ __global__ void __launch_bounds__(W * 32, 1) attn_stream_kernel(const Kv4AttnArg
         cur.first = -static_cast<int>(rest - static_cast<long long>(cur.s.h) * cur.s.nt);
     }
     Cursor<R> pre = cur;     // of the next tile to fetch
-    int pre_u = warp;        // its number in the CTA's share
+    int pre_u = tw;          // its number in the team's share
     bool bad = false;
-    // the page of a tile, or -1 where there is nothing to fetch; asked for one
-    // step before the copy is issued, so that its latency is not waited for
-    auto page_of = [&]() -> int {
-        if (pre_u >= mine) return -1;
-        while (pre_u >= pre.first + pre.s.nt) pre.next(a, G);
+    const int sub_log2 = a.bs_log2 - 4;
+    const size_t page_bytes = (static_cast<size_t>(a.Hkv) << sub_log2) * TB;
+    const int32_t *pages = a.block_table + static_cast<int64_t>(pre.s.b) * a.max_blocks;
+    // the next tile's page and place in it (-1: nothing to fetch); asked for a
+    // step before the copy is issued, so that the latency is not waited for
+    int page = -1, place = -1;
+    auto ask = [&]() {
+        page = place = -1;
+        if (pre_u >= mine) return;
+        if (pre_u >= pre.first + pre.s.nt) {
+            do pre.next(a, G);
+            while (pre_u >= pre.first + pre.s.nt);
+            pages = a.block_table + static_cast<int64_t>(pre.s.b) * a.max_blocks;
+        }
         const int tile = pre.tile(pre_u);
-        if (tile * 16 >= pre.s.end) return -1;
-        const int id = a.block_table[static_cast<int64_t>(pre.s.b) * a.max_blocks + (tile >> (a.bs_log2 - 4))];
-        return id;
+        if (tile * 16 >= pre.s.end) return;
+        page = pages[tile >> sub_log2];
+        place = ((pre.s.h << sub_log2) + (tile & ((1 << sub_log2) - 1))) * TB;
     };
     uint32_t live = 0;       // bit of a stage: it holds a tile
-    int page = page_of();
     auto fetch = [&](int stage) {
-        const bool in = page >= 0 && page < a.num_blocks;
-        if (pre_u < mine) {
-            const int tile = pre.tile(pre_u);
-            if (!in && tile * 16 < pre.s.end) bad = true;
-            if (in) {
-                if (lane == 0) {
-                    const int sub = tile & ((1 << (a.bs_log2 - 4)) - 1);
-                    const size_t at =
-                        (((static_cast<size_t>(page) * a.Hkv + pre.s.h) << (a.bs_log2 - 4)) + sub) * static_cast<size_t>(TB);
-                    mbar_arrive_expect_tx(&bars[stage], TB);
-                    asm volatile(
-                        "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
-                            smem_u32(ring + static_cast<size_t>(stage) * TB)),
-                        "l"(a.cache + at), "r"(TB), "r"(smem_u32(&bars[stage]))
-                        : "memory");
-                }
-            }
+        const bool in = place >= 0 && page >= 0 && page < a.num_blocks;
+        bad |= place >= 0 && !in;
+        if (in && lane == 0) {
+            mbar_arrive_expect_tx(&bars[stage], TB);
+            asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
+                             smem_u32(ring + static_cast<size_t>(stage) * TB)),
+                         "l"(a.cache + static_cast<size_t>(page) * page_bytes + place), "r"(TB), "r"(smem_u32(&bars[stage]))
+                         : "memory");
         }
-        live = in && pre_u < mine ? live | (1u << stage) : live & ~(1u << stage);
-        pre_u += W;
-        page = page_of();
+        live = in ? live | (1u << stage) : live & ~(1u << stage);
+        pre_u += TEAM;
+        ask();
     };
+    ask();
     for (int i = 0; i < depth; ++i) fetch(i);
 
     uint32_t parity = 0;  // bit per stage
     int stage = 0;
-    int u = warp;
+    int u = tw;
     int par = 0;          // of the per-segment buffers
     bool ok = true;
     const int kA = key_of_row(g), vA = key_of_row(2 * t), vB = key_of_row(2 * t + 1);
+    // SPLIT: group of this lane's two accumulator columns, and of its column of B
+    const int col_group = SPLIT ? 2 * t / RPT : 0, b_group = SPLIT ? g / RPT : 0;
 
-    if (warp >= W - NT) build_q<D, NT, W>(a, cur.s, G, W - 1 - warp, smem, 0, lane);
-    __syncthreads();
+    if (tw >= TEAM - NT || TEAM == 1) {
+        if (TEAM == 1) {
+            for (int n = 0; n < NT; ++n) build_q<L, D, SPLIT>(a, cur.s, G, n, NT, team, 0, lane);
+        } else build_q<L, D, SPLIT>(a, cur.s, G, TEAM - 1 - tw, NT, team, 0, lane);
+    }
+    team_sync();
 
     while (true) {
         const Segment s = cur.s;
         const int seg_end = min(cur.first + s.nt, mine);
-        float O[NT][G64][4][4], M[NT][2], Ls[NT][2], QS[NT][G64][2], F[NT][2];
+        float O[NT][SETS][4][4], M[NT][2], Ls[NT][2], QS[NT][SETS][2], F[NT][2];
         int P[NT][2];
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
 #pragma unroll
-            for (int i = 0; i < G64; ++i) {
+            for (int i = 0; i < SETS; ++i) {
 #pragma unroll
                 for (int k = 0; k < 4; ++k)
 #pragma unroll
                     for (int e = 0; e < 4; ++e) O[n][i][k][e] = 0.f;
-                const float2 v = *reinterpret_cast<const float2 *>(smem + L::qs + ((par * G64 + i) * R + 8 * n + 2 * t) * 4);
+                const float2 v = *reinterpret_cast<const float2 *>(team + L::qs + ((par * SETS + i) * 8 * NT + 8 * n + 2 * t) * 4);
                 QS[n][i][0] = v.x;
                 QS[n][i][1] = v.y;
             }
-            const float2 f = *reinterpret_cast<const float2 *>(smem + L::fr + (par * R + 8 * n + 2 * t) * 4);
+            const float2 f = *reinterpret_cast<const float2 *>(team + L::fr + (par * 8 * NT + 8 * n + 2 * t) * 4);
             F[n][0] = f.x;
             F[n][1] = f.y;
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
-                M[n][e] = NEG_INF;
+                M[n][e] = NONE;
                 Ls[n][e] = 0.f;
-                P[n][e] = s.base + (s.r0 + min(8 * n + 2 * t + e, s.rows - 1)) / G;
+                P[n][e] = s.base + (s.r0 + min(RPT * n + (2 * t + e) % RPT, s.rows - 1)) / G;
             }
         }
         const int p_lo = s.base + s.r0 / G, p_hi = s.base + (s.r0 + s.rows - 1) / G;
 
-        for (; u < seg_end; u += W) {
+        for (; u < seg_end; u += TEAM) {
             if (live >> stage & 1u) {
                 ok = mbar_wait(&bars[stage], parity >> stage & 1u, a.status) && ok;
                 parity ^= 1u << stage;
                 const unsigned char *tile = ring + static_cast<size_t>(stage) * TB;
                 const int j0 = cur.tile(u) * 16;
-                const uint4 *qf = reinterpret_cast<const uint4 *>(smem + L::q + par * L::QFRAG) + lane;
-                float x[NT][4];
+                const uint4 *qf = reinterpret_cast<const uint4 *>(team + L::q + par * L::QFRAG) + lane;
+                // ---- scores
+                float acc[NT][SETS][4];
 #pragma unroll
                 for (int n = 0; n < NT; ++n)
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) x[n][e] = 0.f;
-                // ---- scores
+                    for (int i = 0; i < SETS; ++i)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) acc[n][i][e] = 0.f;
 #pragma unroll
                 for (int i = 0; i < G64; ++i) {
                     const uint2 k0 = *reinterpret_cast<const uint2 *>(tile + (i * 16 + kA) * 32 + t * 8);
                     const uint2 k1 = *reinterpret_cast<const uint2 *>(tile + (i * 16 + kA + 8) * 32 + t * 8);
-                    const uint32_t sz0 = *reinterpret_cast<const uint32_t *>(tile + 16 * D + (i * 16 + kA) * 4);
-                    const uint32_t sz1 = *reinterpret_cast<const uint32_t *>(tile + 16 * D + (i * 16 + kA + 8) * 4);
-                    float acc[NT][4];
-#pragma unroll
-                    for (int n = 0; n < NT; ++n)
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) acc[n][e] = 0.f;
+                    // SPLIT: columns of other groups read the zeros at the start
+                    const bool zero = SPLIT && b_group != i;
 #pragma unroll
                     for (int k = 0; k < 2; ++k) {
                         const uint32_t w0 = k ? k0.y : k0.x, w1 = k ? k1.y : k1.x;
                         const uint32_t w0h = w0 >> 8, w1h = w1 >> 8;
 #pragma unroll
                         for (int n = 0; n < NT; ++n) {
-                            const uint4 b = qf[((n * G64 + i) * 2 + k) * 32];
-                            mma_f16(acc[n], w0 & 0x000f000fu, w1 & 0x000f000fu, w0 & 0x00f000f0u, w1 & 0x00f000f0u, b.x, b.y);
-                            mma_f16(acc[n], w0h & 0x000f000fu, w1h & 0x000f000fu, w0h & 0x00f000f0u, w1h & 0x00f000f0u, b.z,
-                                    b.w);
+                            const uint4 b = *(zero ? reinterpret_cast<const uint4 *>(smem)
+                                                   : qf + ((n * SETS + (SPLIT ? 0 : i)) * 2 + k) * 32);
+                            float(&c)[4] = acc[n][SPLIT ? 0 : i];
+                            mma_f16(c, w0 & 0x000f000fu, w1 & 0x000f000fu, w0 & 0x00f000f0u, w1 & 0x00f000f0u, b.x, b.y);
+                            mma_f16(c, w0h & 0x000f000fu, w1h & 0x000f000fu, w0h & 0x00f000f0u, w1h & 0x00f000f0u, b.z, b.w);
                         }
                     }
+                }
+                float x[NT][4];
+#pragma unroll
+                for (int n = 0; n < NT; ++n)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) x[n][e] = 0.f;
+#pragma unroll
+                for (int i = 0; i < SETS; ++i) {
+                    const int at = SPLIT ? col_group : i;
+                    const uint32_t sz0 = *reinterpret_cast<const uint32_t *>(tile + 16 * D + (at * 16 + kA) * 4);
+                    const uint32_t sz1 = *reinterpret_cast<const uint32_t *>(tile + 16 * D + (at * 16 + kA + 8) * 4);
                     const float s0 = f16_lo(sz0), z0 = f16_hi(sz0), s1 = f16_lo(sz1), z1 = f16_hi(sz1);
 #pragma unroll
                     for (int n = 0; n < NT; ++n) {
-                        x[n][0] = fmaf(s0, fmaf(-z0, QS[n][i][0], acc[n][0]), x[n][0]);
-                        x[n][1] = fmaf(s0, fmaf(-z0, QS[n][i][1], acc[n][1]), x[n][1]);
-                        x[n][2] = fmaf(s1, fmaf(-z1, QS[n][i][0], acc[n][2]), x[n][2]);
-                        x[n][3] = fmaf(s1, fmaf(-z1, QS[n][i][1], acc[n][3]), x[n][3]);
+                        x[n][0] = fmaf(s0, fmaf(-z0, QS[n][i][0], acc[n][i][0]), x[n][0]);
+                        x[n][1] = fmaf(s0, fmaf(-z0, QS[n][i][1], acc[n][i][1]), x[n][1]);
+                        x[n][2] = fmaf(s1, fmaf(-z1, QS[n][i][0], acc[n][i][2]), x[n][2]);
+                        x[n][3] = fmaf(s1, fmaf(-z1, QS[n][i][1], acc[n][i][3]), x[n][3]);
                     }
+                }
+                if (SPLIT && G64 > 1) {  // the groups are on neighbouring lanes
+#pragma unroll
+                    for (int n = 0; n < NT; ++n)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            x[n][e] += __shfl_xor_sync(0xffffffffu, x[n][e], 2);
+                            if (G64 == 4) x[n][e] += __shfl_xor_sync(0xffffffffu, x[n][e], 1);
+                        }
                 }
                 // ---- V's parameters; what lies past the last key of the
                 // cache may hold anything and counts as zeros
                 const int ja = j0 + kA, jb = ja + 8;
                 const bool whole = j0 + 16 <= s.end;
-                uint32_t vz0[G64], vz1[G64];  // (scale, zero) of keys kA, kA + 8
-                float top0 = 0.f, top1 = 0.f;
+                uint32_t vz0[SETS], vz1[SETS];  // (scale, zero) of keys kA, kA + 8
+                uint32_t top0 = 0, top1 = 0;
 #pragma unroll
-                for (int i = 0; i < G64; ++i) {
-                    vz0[i] = *reinterpret_cast<const uint32_t *>(tile + 17 * D + (i * 16 + kA) * 4);
-                    vz1[i] = *reinterpret_cast<const uint32_t *>(tile + 17 * D + (i * 16 + kA + 8) * 4);
+                for (int i = 0; i < SETS; ++i) {
+                    const int at = SPLIT ? col_group : i;
+                    vz0[i] = *reinterpret_cast<const uint32_t *>(tile + 17 * D + (at * 16 + kA) * 4);
+                    vz1[i] = *reinterpret_cast<const uint32_t *>(tile + 17 * D + (at * 16 + kA + 8) * 4);
                     if (!whole) {
                         vz0[i] = ja < s.end ? vz0[i] : 0u;
                         vz1[i] = jb < s.end ? vz1[i] : 0u;
                     }
-                    top0 = fmaxf(top0, fabsf(f16_lo(vz0[i])));
-                    top1 = fmaxf(top1, fabsf(f16_lo(vz1[i])));
+                    top0 = maxabs_f16x2(top0, vz0[i]);
+                    top1 = maxabs_f16x2(top1, vz1[i]);
                 }
-                const float l0 = lg2(fmaxf(top0, 5.9604644775390625e-8f)), l1 = lg2(fmaxf(top1, 5.9604644775390625e-8f));
+                // (SPLIT: each lane its own group's; the reference below takes the largest of the lanes)
+                const float l0 = lg2(fmaxf(fabsf(f16_lo(top0)), 5.9604644775390625e-8f));
+                const float l1 = lg2(fmaxf(fabsf(f16_lo(top1)), 5.9604644775390625e-8f));
                 // ---- mask and running reference
                 const bool free = j0 + 16 <= p_lo + 1 && (a.window <= 0 || p_hi - j0 < a.window || j0 + 16 <= a.sinks);
                 bool grow = false;
@@ -492,7 +563,7 @@ __global__ void __launch_bounds__(W * 32, 1) attn_stream_kernel(const Kv4AttnArg
                         for (int e = 0; e < 4; ++e) {
                             const int j = e < 2 ? ja : jb, p = P[n][e & 1];
                             const bool see = j <= p && j < s.end && (a.window <= 0 || p - j < a.window || j < a.sinks);
-                            x[n][e] = see ? x[n][e] : NEG_INF;
+                            x[n][e] = see ? x[n][e] : -INFINITY;
                         }
                     }
 #pragma unroll
@@ -508,12 +579,16 @@ __global__ void __launch_bounds__(W * 32, 1) attn_stream_kernel(const Kv4AttnArg
                             m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 4));
                             m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 8));
                             m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 16));
+                            if (SPLIT && G64 > 1) {
+                                m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 2));
+                                if (G64 == 4) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 1));
+                            }
                             m = fmaxf(m, M[n][e]);
-                            const float f = m == NEG_INF ? 1.f : ex2(M[n][e] - m);
+                            const float f = ex2(M[n][e] - m);
                             M[n][e] = m;
                             Ls[n][e] *= f;
 #pragma unroll
-                            for (int i = 0; i < G64; ++i)
+                            for (int i = 0; i < SETS; ++i)
 #pragma unroll
                                 for (int k = 0; k < 4; ++k) {
                                     O[n][i][k][e] *= f;
@@ -523,13 +598,25 @@ __global__ void __launch_bounds__(W * 32, 1) attn_stream_kernel(const Kv4AttnArg
                     }
                 }
 #pragma unroll
-                for (int n = 0; n < NT; ++n) {
+                for (int n = 0; n < NT; ++n)
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {
-                        const float m = M[n][e & 1];
-                        x[n][e] = ex2(x[n][e] - (m == NEG_INF ? 0.f : m));
+                        x[n][e] = ex2(x[n][e] - M[n][e & 1]);
                         Ls[n][e & 1] += x[n][e];
                     }
+                // ---- weights times scales as the B operand; zeros of this
+                // lane's four keys (SPLIT: of group b_group)
+                uint32_t b[SETS][NT][2], zab[SETS], zcd[SETS];
+#pragma unroll
+                for (int i = 0; i < SETS; ++i) {
+                    const float v0 = f16_lo(vz0[i]), v1 = f16_lo(vz1[i]);
+#pragma unroll
+                    for (int n = 0; n < NT; ++n) {
+                        b[i][n][0] = transpose8x8(pack_f16(x[n][0] * v0, x[n][1] * v0));
+                        b[i][n][1] = transpose8x8(pack_f16(x[n][2] * v1, x[n][3] * v1));
+                    }
+                    zab[i] = transpose8x8(__byte_perm(vz0[i], 0, 0x3232));
+                    zcd[i] = transpose8x8(__byte_perm(vz1[i], 0, 0x3232));
                 }
                 // ---- weighted values
 #pragma unroll
@@ -539,27 +626,30 @@ __global__ void __launch_bounds__(W * 32, 1) attn_stream_kernel(const Kv4AttnArg
                     const uint32_t wB = *reinterpret_cast<const uint32_t *>(vt + vB * 32);
                     const uint32_t wC = *reinterpret_cast<const uint32_t *>(vt + (vA + 8) * 32);
                     const uint32_t wD = *reinterpret_cast<const uint32_t *>(vt + (vB + 8) * 32);
-                    uint32_t b[NT][2];
+                    uint32_t za = zab[SPLIT ? 0 : i], zc = zcd[SPLIT ? 0 : i];
+                    if (SPLIT && G64 > 1) {  // from a lane whose column is of group i
+                        za = __shfl_sync(0xffffffffu, za, i * RPT * 4 + t);
+                        zc = __shfl_sync(0xffffffffu, zc, i * RPT * 4 + t);
+                    }
+                    // in the codes' units, 2^-24 and 2^-20
+                    const uint32_t za1 = mul_f16x2(za, 0x00010001u), za16 = mul_f16x2(za, 0x00100010u);
+                    const uint32_t zc1 = mul_f16x2(zc, 0x00010001u), zc16 = mul_f16x2(zc, 0x00100010u);
+                    uint32_t bi[NT][2];
 #pragma unroll
                     for (int n = 0; n < NT; ++n) {
-                        const float v0 = f16_lo(vz0[i]), v1 = f16_lo(vz1[i]);
-                        b[n][0] = transpose8x8(pack_f16(x[n][0] * v0, x[n][1] * v0));
-                        b[n][1] = transpose8x8(pack_f16(x[n][2] * v1, x[n][3] * v1));
+                        bi[n][0] = SPLIT ? (b_group == i ? b[0][n][0] : 0u) : b[SPLIT ? 0 : i][n][0];
+                        bi[n][1] = SPLIT ? (b_group == i ? b[0][n][1] : 0u) : b[SPLIT ? 0 : i][n][1];
                     }
-                    // zeros of this lane's four keys in the codes' units, 2^-24 and 2^-20
-                    const uint32_t zab = transpose8x8(__byte_perm(vz0[i], 0, 0x3232)), zcd = transpose8x8(__byte_perm(vz1[i], 0, 0x3232));
-                    const uint32_t zab1 = mul_f16x2(zab, 0x00010001u), zab16 = mul_f16x2(zab, 0x00100010u);
-                    const uint32_t zcd1 = mul_f16x2(zcd, 0x00010001u), zcd16 = mul_f16x2(zcd, 0x00100010u);
 #pragma unroll
                     for (int k = 0; k < 4; ++k) {
                         // dimensions 8 g + 2 k and 8 g + 2 k + 1 of keys A, B and C, D
                         const uint32_t sel = k < 2 ? 0x5410u : 0x7632u;
                         uint32_t ab = __byte_perm(wA, wB, sel), cd = __byte_perm(wC, wD, sel);
                         if (k & 1) ab >>= 8, cd >>= 8;
-                        const uint32_t a0 = sub_f16x2(ab & 0x000f000fu, zab1), a1 = sub_f16x2(ab & 0x00f000f0u, zab16);
-                        const uint32_t a2 = sub_f16x2(cd & 0x000f000fu, zcd1), a3 = sub_f16x2(cd & 0x00f000f0u, zcd16);
+                        const uint32_t a0 = sub_f16x2(ab & 0x000f000fu, za1), a1 = sub_f16x2(ab & 0x00f000f0u, za16);
+                        const uint32_t a2 = sub_f16x2(cd & 0x000f000fu, zc1), a3 = sub_f16x2(cd & 0x00f000f0u, zc16);
 #pragma unroll
-                        for (int n = 0; n < NT; ++n) mma_f16(O[n][i][k], a0, a1, a2, a3, b[n][0], b[n][1]);
+                        for (int n = 0; n < NT; ++n) mma_f16(O[n][SPLIT ? 0 : i][k], a0, a1, a2, a3, bi[n][0], bi[n][1]);
                     }
                 }
                 __syncwarp();
@@ -568,9 +658,28 @@ __global__ void __launch_bounds__(W * 32, 1) attn_stream_kernel(const Kv4AttnArg
             stage = stage + 1 == depth ? 0 : stage + 1;
         }
 
-        // ---- the segment's end: join the warps
-        float *const sM = reinterpret_cast<float *>(smem + L::mx) + par * W * R;
-        float *const sL = reinterpret_cast<float *>(smem + L::sm) + par * W * R;
+        // ---- the segment's end
+        const int seg_first = cur.first, seg_nt = s.nt;
+        const bool last = seg_first + seg_nt >= mine;  // no further segment in this share
+        const bool split = seg_first < 0 || seg_first + seg_nt > mine;
+        int c_first = 0, c_last = 0;
+        if (split) {
+            const long long seg_u0 = u0 + seg_first;
+            c_first = static_cast<int>(((seg_u0 + 1) * C - 1) / U);
+            c_last = static_cast<int>(((seg_u0 + seg_nt) * C - 1) / U);
+        }
+        // partial results: [team][2][R][D + 4], slot 1 where the segment begins in
+        // the share; of a row: maximum, sum, two unused, weighted values
+        constexpr int PART = R * (D + 4);
+        float *const parts = reinterpret_cast<float *>(a.scratch + COUNTER_BYTES);
+        float *const part = parts + (static_cast<size_t>(me) * 2 + (seg_first >= 0 ? 1 : 0)) * PART;
+        unsigned int *const count = reinterpret_cast<unsigned int *>(a.scratch) + c_first;
+        auto row_of = [&](int r) -> uint16_t * {  // out of row r
+            const int row = s.r0 + r, tok = rows_before(a, s.b) + row / G;
+            return a.out + (static_cast<int64_t>(tok) * a.Hq + s.h * G + row % G) * D;
+        };
+        // accumulators to their units (2^-24 for even dimensions, 2^-20 for odd
+        // ones), and the sums over the keys
 #pragma unroll
         for (int n = 0; n < NT; ++n)
 #pragma unroll
@@ -579,138 +688,183 @@ __global__ void __launch_bounds__(W * 32, 1) attn_stream_kernel(const Kv4AttnArg
                 l += __shfl_xor_sync(0xffffffffu, l, 4);
                 l += __shfl_xor_sync(0xffffffffu, l, 8);
                 l += __shfl_xor_sync(0xffffffffu, l, 16);
-                if (g == 0) {
-                    sM[warp * R + 8 * n + 2 * t + e] = M[n][e];
-                    sL[warp * R + 8 * n + 2 * t + e] = l;
-                }
+                Ls[n][e] = l;
             }
-        __syncthreads();
-        float *const buf = reinterpret_cast<float *>(smem + L::merge) + (warp >= W / 2 ? warp - W / 2 : warp) * L::MERGE_WARP;
-#pragma unroll
-        for (int n = 0; n < NT; ++n) {
-            float f[2];
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-                float m = NEG_INF;
-                for (int w = 0; w < W; ++w) m = fmaxf(m, sM[w * R + 8 * n + 2 * t + e]);
-                f[e] = M[n][e] == NEG_INF ? 0.f : ex2(M[n][e] - m);
-            }
-            // the codes' units: 2^-24 for even dimensions, 2^-20 for odd ones
-            const float e0 = f[0] * 16777216.f, e1 = f[1] * 16777216.f, d0 = f[0] * 1048576.f, d1 = f[1] * 1048576.f;
-#pragma unroll
-            for (int i = 0; i < G64; ++i)
-#pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    O[n][i][k][0] *= e0;
-                    O[n][i][k][1] *= e1;
-                    O[n][i][k][2] *= d0;
-                    O[n][i][k][3] *= d1;
-                    if (warp >= W / 2 && 8 * n + 2 * t < s.rows)
-                        *reinterpret_cast<float4 *>(buf + (n * 4 + t) * L::MERGE_T + (64 * i + 8 * g + 2 * k) * 2) =
-                            make_float4(O[n][i][k][0], O[n][i][k][1], O[n][i][k][2], O[n][i][k][3]);
-                }
-        }
-        __syncthreads();
-        const bool last = cur.first + s.nt >= mine;  // no further segment in this CTA
-        const int seg_first = cur.first, seg_nt = s.nt;
-        if (warp < W / 2) {
+        if constexpr (TEAM == 1) {
 #pragma unroll
             for (int n = 0; n < NT; ++n)
-                if (8 * n + 2 * t < s.rows)
 #pragma unroll
-                    for (int i = 0; i < G64; ++i)
+                for (int e = 0; e < 2; ++e) {
+                    const int r = RPT * n + (2 * t + e) % RPT;
+                    if (r < s.rows) {
+                        const float inv = Ls[n][e] == 0.f ? 0.f : 1.f / Ls[n][e];
 #pragma unroll
-                        for (int k = 0; k < 4; ++k) {
-                            float4 *const at =
-                                reinterpret_cast<float4 *>(buf + (n * 4 + t) * L::MERGE_T + (64 * i + 8 * g + 2 * k) * 2);
-                            const float4 o = *at;
-                            *at = make_float4(O[n][i][k][0] + o.x, O[n][i][k][1] + o.y, O[n][i][k][2] + o.z, O[n][i][k][3] + o.w);
+                        for (int i = 0; i < SETS; ++i) {
+                            const int d = 64 * (SPLIT ? col_group : i) + 8 * g;
+                            float v[8];
+#pragma unroll
+                            for (int k = 0; k < 4; ++k) {
+                                v[2 * k] = O[n][i][k][e] * 16777216.f;
+                                v[2 * k + 1] = O[n][i][k][e + 2] * 1048576.f;
+                            }
+                            if (!split) {
+                                uint32_t w[4];
+#pragma unroll
+                                for (int k = 0; k < 4; ++k)
+                                    w[k] = static_cast<uint32_t>(f32_to_bf16_bits(v[2 * k] * inv)) |
+                                           static_cast<uint32_t>(f32_to_bf16_bits(v[2 * k + 1] * inv)) << 16;
+                                *reinterpret_cast<uint4 *>(row_of(r) + d) = make_uint4(w[0], w[1], w[2], w[3]);
+                            } else {
+                                float *const to = part + r * (D + 4);
+                                __stcg(reinterpret_cast<float4 *>(to + 4 + d), make_float4(v[0], v[1], v[2], v[3]));
+                                __stcg(reinterpret_cast<float4 *>(to + 8 + d), make_float4(v[4], v[5], v[6], v[7]));
+                                if (d == 0) __stcg(reinterpret_cast<float2 *>(to), make_float2(M[n][e], Ls[n][e]));
+                            }
                         }
-        }
-        if (!last) {
-            cur.next(a, G);
-            if (warp >= W - NT) build_q<D, NT, W>(a, cur.s, G, W - 1 - warp, smem, par ^ 1, lane);
-        }
-        __syncthreads();
-        // ---- each thread two rows of a dimension
-        const bool split = seg_first < 0 || seg_first + seg_nt > mine;
-        const float *const all = reinterpret_cast<const float *>(smem + L::merge);
-        const long long seg_u0 = u0 + seg_first;
-        int c_first = 0, c_last = 0;
-        if (split) {
-            c_first = static_cast<int>(((seg_u0 + 1) * C - 1) / U);
-            c_last = static_cast<int>(((seg_u0 + seg_nt) * C - 1) / U);
-        }
-        // partial results: [CTA][2][MAX_ROWS][D + 2], slot 1 where the segment begins in the CTA
-        float *const parts = reinterpret_cast<float *>(a.scratch + COUNTER_BYTES);
-        constexpr int PART = MAX_ROWS * (D + 2);
-        float *const part = parts + (static_cast<size_t>(blockIdx.x) * 2 + (seg_first >= 0 ? 1 : 0)) * PART;
-        for (int i = tid; i < (s.rows + 1) / 2 * D; i += W * 32) {
-            const int pr = i / D, d = i % D;
-            float o0 = 0.f, o1 = 0.f;
-#pragma unroll
-            for (int w = 0; w < W / 2; ++w) {
-                const float2 v = *reinterpret_cast<const float2 *>(all + w * L::MERGE_WARP + pr * L::MERGE_T + d * 2);
-                o0 += v.x;
-                o1 += v.y;
-            }
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-                const int r = 2 * pr + e;
-                if (r >= s.rows) break;
-                float m = NEG_INF, l = 0.f;
-                for (int w = 0; w < W; ++w) m = fmaxf(m, sM[w * R + r]);
-                for (int w = 0; w < W; ++w) {
-                    const float mw = sM[w * R + r];
-                    l += mw == NEG_INF ? 0.f : sL[w * R + r] * ex2(mw - m);
+                    }
                 }
-                const float o = e ? o1 : o0;
-                if (!split) {
-                    const int row = s.r0 + r, tok = rows_before(a, s.b) + row / G;
-                    a.out[(static_cast<int64_t>(tok) * a.Hq + s.h * G + row % G) * D + d] =
-                        f32_to_bf16_bits(l == 0.f ? 0.f : o / l);
-                } else {
-                    __stcg(part + r * (D + 2) + 2 + d, o);
-                    if (d == 0) {
-                        __stcg(part + r * (D + 2), m);
-                        __stcg(part + r * (D + 2) + 1, l);
+        } else {
+            float *const sM = reinterpret_cast<float *>(smem + L::mx) + par * W * R;
+            float *const sL = reinterpret_cast<float *>(smem + L::sm) + par * W * R;
+            if (g == 0 && col_group == 0) {
+#pragma unroll
+                for (int n = 0; n < NT; ++n)
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        sM[warp * R + RPT * n + (2 * t + e) % RPT] = M[n][e];
+                        sL[warp * R + RPT * n + (2 * t + e) % RPT] = Ls[n][e];
+                    }
+            }
+            __syncthreads();
+            float *const buf = reinterpret_cast<float *>(smem + L::merge) + (warp >= W / 2 ? warp - W / 2 : warp) * L::MERGE_WARP;
+#pragma unroll
+            for (int n = 0; n < NT; ++n) {
+                float f[2];
+                const int r = RPT * n + 2 * t % RPT;
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    float m = NONE;
+                    for (int w = 0; w < W; ++w) m = fmaxf(m, sM[w * R + r + e]);
+                    f[e] = ex2(M[n][e] - m);
+                }
+                const float e0 = f[0] * 16777216.f, e1 = f[1] * 16777216.f, d0 = f[0] * 1048576.f, d1 = f[1] * 1048576.f;
+#pragma unroll
+                for (int i = 0; i < SETS; ++i)
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        O[n][i][k][0] *= e0;
+                        O[n][i][k][1] *= e1;
+                        O[n][i][k][2] *= d0;
+                        O[n][i][k][3] *= d1;
+                        if (warp >= W / 2 && r < s.rows)
+                            *reinterpret_cast<float4 *>(buf + ((n * SETS + i) * 4 + t) * L::REGION + (8 * g + 2 * k) * 2) =
+                                make_float4(O[n][i][k][0], O[n][i][k][1], O[n][i][k][2], O[n][i][k][3]);
+                    }
+            }
+            __syncthreads();
+            if (warp < W / 2) {
+#pragma unroll
+                for (int n = 0; n < NT; ++n)
+                    if (RPT * n + 2 * t % RPT < s.rows)
+#pragma unroll
+                        for (int i = 0; i < SETS; ++i)
+#pragma unroll
+                            for (int k = 0; k < 4; ++k) {
+                                float4 *const at =
+                                    reinterpret_cast<float4 *>(buf + ((n * SETS + i) * 4 + t) * L::REGION + (8 * g + 2 * k) * 2);
+                                const float4 o = *at;
+                                *at = make_float4(O[n][i][k][0] + o.x, O[n][i][k][1] + o.y, O[n][i][k][2] + o.z, O[n][i][k][3] + o.w);
+                            }
+            }
+            if (!last) {
+                Cursor<R> after = cur;
+                after.next(a, G);
+                if (tw >= TEAM - NT) build_q<L, D, SPLIT>(a, after.s, G, TEAM - 1 - tw, NT, team, par ^ 1, lane);
+            }
+            __syncthreads();
+            // each thread two rows of a dimension
+            const float *const all = reinterpret_cast<const float *>(smem + L::merge);
+            for (int i = tid; i < (s.rows + 1) / 2 * D; i += W * 32) {
+                const int pr = i / D, d = i % D;
+                constexpr int PPT = RPT / 2;  // row pairs of 8 columns
+                const int n = pr / PPT, set = SPLIT ? 0 : d >> 6, tt = SPLIT ? (d >> 6) * PPT + pr % PPT : pr % PPT;
+                float o[2] = {0.f, 0.f};
+#pragma unroll
+                for (int w = 0; w < W / 2; ++w) {
+                    const float2 v = *reinterpret_cast<const float2 *>(all + w * L::MERGE_WARP +
+                                                                       ((n * SETS + set) * 4 + tt) * L::REGION + (d & 63) * 2);
+                    o[0] += v.x;
+                    o[1] += v.y;
+                }
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    const int r = 2 * pr + e;
+                    if (r >= s.rows) break;
+                    float m = NONE, l = 0.f;
+                    for (int w = 0; w < W; ++w) m = fmaxf(m, sM[w * R + r]);
+                    for (int w = 0; w < W; ++w) l += sL[w * R + r] * ex2(sM[w * R + r] - m);
+                    if (!split) row_of(r)[d] = f32_to_bf16_bits(l == 0.f ? 0.f : o[e] / l);
+                    else {
+                        __stcg(part + r * (D + 4) + 4 + d, o[e]);
+                        if (d == 0) __stcg(reinterpret_cast<float2 *>(part + r * (D + 4)), make_float2(m, l));
                     }
                 }
             }
         }
         if (split) {
-            unsigned int *const count = reinterpret_cast<unsigned int *>(a.scratch) + c_first;
+            // the last team to arrive joins the parts, in the order of the teams
             __threadfence();
-            __syncthreads();
-            if (tid == 0) {
-                const bool done = atomicAdd(count, 1u) == static_cast<unsigned int>(c_last - c_first);
+            team_sync();
+            bool done = false;
+            if (TEAM == 1 ? lane == 0 : tid == 0) {
+                done = atomicAdd(count, 1u) == static_cast<unsigned int>(c_last - c_first);
                 if (done) *count = 0;  // for the next call
-                misc[0] = done;
+                if (TEAM > 1) misc[0] = done;
                 __threadfence();
             }
-            __syncthreads();
-            if (misc[0]) {
-                for (int i = tid; i < s.rows * D; i += W * 32) {
-                    const int r = i / D, d = i % D;
-                    float m = NEG_INF;
-                    for (int c = c_first; c <= c_last; ++c)
-                        m = fmaxf(m, __ldcg(parts + (static_cast<size_t>(c) * 2 + (c == c_first)) * PART + r * (D + 2)));
-                    float l = 0.f, o = 0.f;
+            if (TEAM == 1) done = __shfl_sync(0xffffffffu, done, 0);
+            else {
+                __syncthreads();
+                done = misc[0];
+            }
+            if (done) {
+                __threadfence();
+                const int step = TEAM == 1 ? 32 : W * 32;
+                for (int i = TEAM == 1 ? lane : tid; i < s.rows * (D / 4); i += step) {
+                    const int r = i / (D / 4), d = i % (D / 4) * 4;
+                    const float *const base = parts + r * (D + 4);
+                    auto slot = [&](int c) { return (static_cast<size_t>(c) * 2 + (c == c_first)) * PART; };
+                    float m = NONE;
+                    for (int c = c_first; c <= c_last; ++c) m = fmaxf(m, __ldcg(base + slot(c)));
+                    float l = 0.f;
+                    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
                     for (int c = c_first; c <= c_last; ++c) {
-                        const float *const q = parts + (static_cast<size_t>(c) * 2 + (c == c_first)) * PART + r * (D + 2);
-                        const float mc = __ldcg(q);
-                        const float f = mc == NEG_INF ? 0.f : ex2(mc - m);
-                        l += f * __ldcg(q + 1);
-                        o += f * __ldcg(q + 2 + d);
+                        const float2 ml = __ldcg(reinterpret_cast<const float2 *>(base + slot(c)));
+                        const float4 v = __ldcg(reinterpret_cast<const float4 *>(base + slot(c) + 4 + d));
+                        const float f = ex2(ml.x - m);
+                        l = fmaf(f, ml.y, l);
+                        o.x = fmaf(f, v.x, o.x);
+                        o.y = fmaf(f, v.y, o.y);
+                        o.z = fmaf(f, v.z, o.z);
+                        o.w = fmaf(f, v.w, o.w);
                     }
-                    const int row = s.r0 + r, tok = rows_before(a, s.b) + row / G;
-                    a.out[(static_cast<int64_t>(tok) * a.Hq + s.h * G + row % G) * D + d] =
-                        f32_to_bf16_bits(l == 0.f ? 0.f : o / l);
+                    const float inv = l == 0.f ? 0.f : 1.f / l;
+                    *reinterpret_cast<uint2 *>(row_of(r) + d) =
+                        make_uint2(static_cast<uint32_t>(f32_to_bf16_bits(o.x * inv)) |
+                                       static_cast<uint32_t>(f32_to_bf16_bits(o.y * inv)) << 16,
+                                   static_cast<uint32_t>(f32_to_bf16_bits(o.z * inv)) |
+                                       static_cast<uint32_t>(f32_to_bf16_bits(o.w * inv)) << 16);
                 }
             }
         }
         if (last) break;
-        par ^= 1;
+        cur.next(a, G);
+        if (TEAM == 1) {
+            __syncwarp();
+            for (int n = 0; n < NT; ++n) build_q<L, D, SPLIT>(a, cur.s, G, n, NT, team, 0, lane);
+            __syncwarp();
+        } else par ^= 1;
     }
     if (__any_sync(0xffffffffu, bad) && lane == 0) atomicOr(a.status, kDevBadIndex);
     // every copy of this warp has been waited for, unless a wait gave up: then
@@ -720,16 +874,17 @@ __global__ void __launch_bounds__(W * 32, 1) attn_stream_kernel(const Kv4AttnArg
             if (live >> i & 1u) mbar_wait(&bars[i], parity >> i & 1u, nullptr);
 }
 
-template <int D, int NT, int W>
+template <int D, int NT, int W, int TEAM, bool SPLIT>
 cudaError_t launch_stream(const Kv4AttnArgs &a, cudaStream_t st, const DeviceInfo &dev) {
-    using L = StreamSmem<D, NT, W>;
+    using L = Stream<D, NT, W, TEAM, SPLIT>;
+    static_assert(L::TEAMS * L::R <= warp_rows(D) && W <= MAX_WARPS, "scratch size");
     const int table = (a.requests + 1) * 8;
     int depth = (dev.max_smem_optin - L::ring - table) / (W * kv4_tile_bytes(D));
     if (depth > 8) depth = 8;
     if (depth < 1) return cudaErrorNotSupported;
     const int smem = L::ring + W * depth * kv4_tile_bytes(D) + table;
     static SmemLimit limit;
-    const void *kern = reinterpret_cast<const void *>(attn_stream_kernel<D, NT, W>);
+    const void *kern = reinterpret_cast<const void *>(attn_stream_kernel<D, NT, W, TEAM, SPLIT>);
     if (cudaError_t e = limit.ensure(kern, dev.device, smem)) return e;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(static_cast<unsigned>(dev.num_sms < MAX_CTAS ? dev.num_sms : MAX_CTAS));
@@ -741,21 +896,32 @@ cudaError_t launch_stream(const Kv4AttnArgs &a, cudaStream_t st, const DeviceInf
     pdl[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = pdl;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, attn_stream_kernel<D, NT, W>, a, depth);
+    return cudaLaunchKernelEx(&cfg, attn_stream_kernel<D, NT, W, TEAM, SPLIT>, a, depth);
+}
+
+// One warp to a team when there are segments enough for that (rows is the
+// most a request has).
+template <int D, int NT, int W, bool SPLIT>
+cudaError_t launch_teams(const Kv4AttnArgs &a, int64_t rows, cudaStream_t st, const DeviceInfo &dev) {
+    constexpr int R = Stream<D, NT, W, 1, SPLIT>::R;
+    const int64_t segments = a.requests * a.Hkv * ((rows + R - 1) / R);
+    if (segments * TEAM_RATIO >= static_cast<int64_t>(dev.num_sms) * W) return launch_stream<D, NT, W, 1, SPLIT>(a, st, dev);
+    return launch_stream<D, NT, W, W, SPLIT>(a, st, dev);
 }
 
 }  // namespace
 
 int64_t kv4_attention_scratch(int, int, int D) {
-    return (COUNTER_BYTES + int64_t(MAX_CTAS) * 2 * MAX_ROWS * (D + 2) * 4 + 255) / 256 * 256;
+    return (COUNTER_BYTES + int64_t(MAX_CTAS) * 2 * warp_rows(D) * (D + 4) * 4 + 255) / 256 * 256;
 }
 
 cudaError_t launch_kv4_attention(const Kv4AttnArgs &args, int D, cudaStream_t st, const DeviceInfo &dev) {
     Kv4AttnArgs a = args;
     const int G = a.Hq / a.Hkv;
+    int64_t rows = a.max_new * G;  // the most a request has
     a.rows_most = 0x7fffffff;
     a.zero_rest = 1;
-    if (a.max_new * G > PROMPT_ROWS) {
+    if (rows > PROMPT_ROWS) {
         // requests of many rows to the tensor cores, the others of a mixed step
         // to the streaming kernel
         a.rows_above = a.requests > 1 ? PROMPT_ROWS : 0;
@@ -763,12 +929,16 @@ cudaError_t launch_kv4_attention(const Kv4AttnArgs &args, int D, cudaStream_t st
         if (a.requests == 1) return cudaSuccess;
         a.rows_most = PROMPT_ROWS;
         a.zero_rest = 0;
+        rows = PROMPT_ROWS;
     }
-    // rows that share a read of the cache: 8 or 16 to a segment
-    const bool few = a.max_new * G <= 8;
-    if (D == 64) return few ? launch_stream<64, 1, 16>(a, st, dev) : launch_stream<64, 2, 16>(a, st, dev);
-    if (D == 128) return few ? launch_stream<128, 1, 16>(a, st, dev) : launch_stream<128, 2, 12>(a, st, dev);
-    return few ? launch_stream<256, 1, 12>(a, st, dev) : launch_stream<256, 2, 8>(a, st, dev);
+    if (D == 64) return rows <= 8 ? launch_teams<64, 1, 16, false>(a, rows, st, dev) : launch_teams<64, 2, 16, false>(a, rows, st, dev);
+    if (D == 128)
+        return rows <= 4   ? launch_teams<128, 1, 16, true>(a, rows, st, dev)
+               : rows <= 8 ? launch_teams<128, 1, 16, false>(a, rows, st, dev)
+                           : launch_teams<128, 2, 12, false>(a, rows, st, dev);
+    return rows <= 2   ? launch_teams<256, 1, 16, true>(a, rows, st, dev)
+           : rows <= 8 ? launch_teams<256, 1, 12, false>(a, rows, st, dev)
+                       : launch_teams<256, 2, 8, false>(a, rows, st, dev);
 }
 
 }  // namespace w4

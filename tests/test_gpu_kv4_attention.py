@@ -185,3 +185,38 @@ def test_strided_queries_other_stream_and_graph_replay(max_new):
     g.replay()
     torch.cuda.synchronize()
     _check(w4, out, (*host[:3], shorter, host[4]), 128 ** -0.5)
+
+
+@pytest.mark.parametrize("Hq,Hkv,D,new", [(2, 1, 256, 1), (1, 1, 256, 1), (4, 1, 128, 1), (3, 1, 128, 1), (8, 1, 256, 1),
+                                          (7, 1, 128, 1), (8, 1, 64, 1), (16, 1, 64, 1), (6, 1, 256, 2), (5, 1, 128, 3)])
+@pytest.mark.parametrize("window,sinks", [(0, 0), (20, 3)])
+def test_many_requests(Hq, Hkv, D, new, window, sinks):
+    # so many segments that each warp works alone; lengths that end and begin
+    # inside a share, and a few that several warps share
+    torch, w4 = cuda_or_skip()
+    rng = np.random.default_rng(D + Hq)
+    ends = rng.integers(1, 30, 320)
+    ends[[5, 100, 319]] = 700, 333, 512
+    ends[[6, 7, 200]] = 16, 17, 0
+    n = np.minimum(rng.integers(1, new + 1, 320), np.maximum(ends, 1))
+    n[[9, 10, 318]] = 0
+    dev, host = _problem(torch, [int(e) for e in ends], [int(v) for v in n], Hq, Hkv, D, 16, D)
+    scratch = w4.kv4_attention_scratch(Hq, Hkv, D)
+    out = w4.kv4_attention(**dev, scratch=scratch, window=window, sinks=sinks, max_new=new)
+    _check(w4, out, host, D ** -0.5, window, sinks)
+    assert torch.equal(out, w4.kv4_attention(**dev, scratch=scratch, window=window, sinks=sinks, max_new=new))
+
+
+@pytest.mark.parametrize("Hq,Hkv,D", [(2, 1, 256), (4, 1, 128), (16, 1, 64)])
+def test_mixed_step_of_decodes_and_prompts(Hq, Hkv, D):
+    # one call: requests for the prompt kernel beside many for the streaming one
+    torch, w4 = cuda_or_skip()
+    rng = np.random.default_rng(D)
+    new = np.ones(90, int)
+    new[[3, 50]] = 140, 61
+    ends = new + rng.integers(0, 60, 90)
+    ends[80] = 900
+    dev, host = _problem(torch, [int(e) for e in ends], [int(v) for v in new], Hq, Hkv, D, 32, D + 1, gap=2)
+    out = torch.full((int(new.sum()) + 2, Hq, D), float("nan"), dtype=torch.bfloat16, device="cuda")
+    w4.kv4_attention(**dev, scratch=w4.kv4_attention_scratch(Hq, Hkv, D), max_new=140, out=out)
+    _check(w4, out, host, D ** -0.5)
