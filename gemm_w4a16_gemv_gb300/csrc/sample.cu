@@ -34,6 +34,7 @@
 #include "kv4.cuh"
 
 #include <cooperative_groups.h>
+#include <type_traits>
 
 namespace cg = cooperative_groups;
 
@@ -50,6 +51,7 @@ constexpr int SMALL_K = 256;         // top-k that goes by candidates
 constexpr int CANDIDATES = 1024;
 constexpr float UNIT = 1099511627776.f;  // 2^40
 constexpr float BINS_PER_UNIT = 36.f;    // 28.4 units: beyond that a mass is 0
+constexpr float NO_MASS = 40.f * BINS_PER_UNIT;  // certainly (2^40 exp(-40) < 1 / 2), whatever was rounded
 
 // Unsigned key with the order of the logits (which hold no NaN and no -0).
 __device__ __forceinline__ uint32_t key_of(float v) {
@@ -80,39 +82,65 @@ struct Shared {
     int list_n, cand_n, bin;
 };
 
-// A row's exponentials.  The quotient l / T is the correctly rounded one: for
-// T and 1 / T well inside the exponent range by Markstein's correction (P.
-// Markstein, "Computation of elementary functions on the IBM RISC System/6000
-// processor", 1990): with y the rounded reciprocal and q = l y rounded, the
-// remainder l - q T is exact in a fused multiply-add and q + r y rounds to
-// the quotient.
+// A row's masses.  The quotient l / T is the correctly rounded one: for T = 1
+// the logit itself; for T well inside the exponent range by Markstein's
+// correction (P. Markstein, "Computation of elementary functions on the IBM
+// RISC System/6000 processor", 1990): with y the rounded reciprocal and q = l y
+// rounded, the remainder l - q T is exact in a fused multiply-add and q + r y
+// rounds to the quotient; else by division.
+enum { MODE_ONE, MODE_FUSED, MODE_DIVIDE };
 struct Masses {
-    float T, inv, top;
-    bool fused;
-    __device__ __forceinline__ Masses(float temperature, float top_l) : T(temperature) {
+    float T, inv, top, top_l, per_bin;
+    int mode;
+    __device__ __forceinline__ Masses(float temperature, float largest) : T(temperature), top_l(largest) {
         inv = __frcp_rn(T);
-        fused = T > 1e-20f && T < 1e20f;
         top = __fdiv_rn(top_l, T);
+        per_bin = fminf(__fdividef(BINS_PER_UNIT, T), 1e30f);
+        mode = T == 1.f ? MODE_ONE : T > 1e-15f && T < 1e15f && fabsf(top_l) < 1e15f ? MODE_FUSED : MODE_DIVIDE;
     }
-    __device__ __forceinline__ float quotient(float l) const {
-        if (!fused || !(fabsf(l) < 1e15f)) return __fdiv_rn(l, T);
-        const float q = l * inv;
-        return fmaf(fmaf(-q, T, l), inv, q);
-    }
-    // mass before rounding; logits of -infinity have none
+    // (max - l) / T in bins, not rounded to one; rises as l falls
+    __device__ __forceinline__ float depth(float l) const { return (top_l - l) * per_bin; }
+    // mass before rounding
+    template <int MODE>
     __device__ __forceinline__ float scaled(float l) const {
-        return l > -INFINITY ? expf(__fsub_rn(quotient(l), top)) * UNIT : 0.f;
+        float x = l;
+        if (MODE != MODE_ONE && !(depth(l) < NO_MASS)) return 0.f;  // (-infinity, or a quotient out of range)
+        if (MODE == MODE_FUSED) {
+            const float q = l * inv;
+            x = fmaf(fmaf(-q, T, l), inv, q);
+        } else if (MODE == MODE_DIVIDE) x = __fdiv_rn(l, T);
+        return expf(__fsub_rn(x, top)) * UNIT;
     }
-    __device__ __forceinline__ u64 of(float l) const { return static_cast<u64>(__float2ll_rn(scaled(l))); }
+    // The whole number nearest to t <= 2^40 (ties to even) as hi 2^20 + lo: the
+    // part above 2^20 cut off by adding 2^23 rounded down, the rest (exact)
+    // rounded by adding 2^23.  Sums of 64 of either part fit 32 bits.
+    static __device__ __forceinline__ void whole(float t, uint32_t &hi, uint32_t &lo) {
+        const float h = __fadd_rd(t * 9.5367431640625e-7f, 8388608.f);  // 2^-20
+        hi = __float_as_uint(h) - 0x4b000000u;
+        lo = __float_as_uint(__fadd_rn(fmaf(__fsub_rn(h, 8388608.f), -1048576.f, t), 8388608.f)) - 0x4b000000u;
+    }
+    static __device__ __forceinline__ u64 whole(float t) {
+        uint32_t hi, lo;
+        whole(t, hi, lo);
+        return (static_cast<u64>(hi) << 20) + lo;
+    }
+    template <int MODE>
+    __device__ __forceinline__ u64 mass(float l) const {
+        return whole(scaled<MODE>(l));
+    }
+    __device__ __forceinline__ u64 of(float l) const {
+        return mode == MODE_ONE ? mass<MODE_ONE>(l) : mode == MODE_FUSED ? mass<MODE_FUSED>(l) : mass<MODE_DIVIDE>(l);
+    }
 };
 
-// EPT neighbouring logits per thread (EPT / 2 words of two BF16, or EPT of
-// binary32): element e of the CTA's slice belongs to thread e / EPT.  The
-// threads of a warp read their words rotated against each other, so that they
-// fall into different banks.
+// EPT neighbouring logits per thread: element e of the CTA's slice belongs to
+// thread e / EPT.  They are read in units of 16 bytes (8 BF16 or 4 binary32),
+// the threads of a warp rotated against each other so that they fall into
+// different banks, and a unit's exponentials are formed together, without
+// branches between them.
 template <bool BF16, int EPT>
 __global__ void __launch_bounds__(THREADS) sample_kernel(const SampleArgs a) {
-    constexpr int WORDS = BF16 ? EPT / 2 : EPT;
+    constexpr int N = BF16 ? 8 : 4, UNITS = EPT / N;  // logits of a unit, units of a thread
     extern __shared__ __align__(16) unsigned char smem[];
     Shared &sh = *reinterpret_cast<Shared *>(smem);
     uint32_t *const row = reinterpret_cast<uint32_t *>(smem + (sizeof(Shared) + 127) / 128 * 128);
@@ -122,8 +150,8 @@ __global__ void __launch_bounds__(THREADS) sample_kernel(const SampleArgs a) {
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int V = a.vocab;
     const int slice = rank * EPT * THREADS;           // first index of the CTA
-    const int rot = WORDS >= 32 ? lane : (lane * WORDS) >> 5;
-    const uint32_t *const own = row + tid * WORDS;
+    const int rot = UNITS >= 8 ? lane : (lane * UNITS) >> 3;
+    const uint4 *const own = reinterpret_cast<const uint4 *>(row) + tid * UNITS;
     if (tid == 0) sh.list_n = sh.cand_n = 0;
     for (int i = tid; i < BINS; i += THREADS) sh.hist[i] = 0;
     // every CTA of the cluster has started (waited for before the first write
@@ -170,75 +198,100 @@ __global__ void __launch_bounds__(THREADS) sample_kernel(const SampleArgs a) {
         }
     }
 
-    // f(logit) of every own element, in no particular order
+    // f(N logits, element of the first) of every own unit, in no particular order
     auto each = [&](auto f) {
-#pragma unroll 4
-        for (int j = 0; j < WORDS; ++j) {
-            const uint32_t w = own[(j + rot) & (WORDS - 1)];
-            if (BF16) {
-                f(__uint_as_float(w << 16));
-                f(__uint_as_float(w & 0xffff0000u));
-            } else f(__uint_as_float(w));
+#pragma unroll 1
+        for (int j = 0; j < UNITS; ++j) {
+            const int q = (j + rot) & (UNITS - 1);
+            const uint4 w = own[q];
+            float l[N];
+            if constexpr (BF16) {
+                l[0] = __uint_as_float(w.x << 16), l[1] = __uint_as_float(w.x & 0xffff0000u);
+                l[2] = __uint_as_float(w.y << 16), l[3] = __uint_as_float(w.y & 0xffff0000u);
+                l[4] = __uint_as_float(w.z << 16), l[5] = __uint_as_float(w.z & 0xffff0000u);
+                l[6] = __uint_as_float(w.w << 16), l[7] = __uint_as_float(w.w & 0xffff0000u);
+            } else {
+                l[0] = __uint_as_float(w.x), l[1] = __uint_as_float(w.y);
+                l[2] = __uint_as_float(w.z), l[3] = __uint_as_float(w.w);
+            }
+            f(l, tid * EPT + q * N);
         }
     };
-    auto logit = [&](int e) -> float {  // own element e
-        if (BF16) return __uint_as_float(e & 1 ? own[e >> 1] & 0xffff0000u : own[e >> 1] << 16);
-        return __uint_as_float(own[e]);
+    auto logit = [&](int e) -> float {  // element e of the slice
+        if (BF16) return __uint_as_float(e & 1 ? row[e >> 1] & 0xffff0000u : row[e >> 1] << 16);
+        return __uint_as_float(row[e]);
     };
 
-    // ---- sums of three numbers, and a least and a largest key, over the cluster
+    // ---- COUNT sums, and with KEYS a least and a largest key, over the cluster
     int turn = 0;
-    auto reduce = [&](u64 &s0, u64 &s1, u64 &s2, uint32_t &lo, uint32_t &hi) {
+    auto reduce = [&](auto count, auto keys, u64 *sum, uint32_t &lo, uint32_t &hi) {
+        constexpr int COUNT = count.value;
+        constexpr bool KEYS = keys.value;
+        auto warps = [&](u64 *x, uint32_t &l, uint32_t &h) {
 #pragma unroll
-        for (int o = 16; o; o >>= 1) {
-            s0 += __shfl_xor_sync(0xffffffffu, s0, o);
-            s1 += __shfl_xor_sync(0xffffffffu, s1, o);
-            s2 += __shfl_xor_sync(0xffffffffu, s2, o);
-        }
-        lo = __reduce_min_sync(0xffffffffu, lo);
-        hi = __reduce_max_sync(0xffffffffu, hi);
+            for (int o = 16; o; o >>= 1)
+#pragma unroll
+                for (int i = 0; i < COUNT; ++i) x[i] += __shfl_xor_sync(0xffffffffu, x[i], o);
+            if (KEYS) {
+                l = __reduce_min_sync(0xffffffffu, l);
+                h = __reduce_max_sync(0xffffffffu, h);
+            }
+        };
+        warps(sum, lo, hi);
         if (lane == 0) {
-            sh.part[warp][0] = s0;
-            sh.part[warp][1] = s1;
-            sh.part[warp][2] = s2;
-            sh.plo[warp] = lo;
-            sh.phi[warp] = hi;
+#pragma unroll
+            for (int i = 0; i < COUNT; ++i) sh.part[warp][i] = sum[i];
+            if (KEYS) {
+                sh.plo[warp] = lo;
+                sh.phi[warp] = hi;
+            }
         }
         __syncthreads();
         if (warp == 0) {
-            const bool on = lane < WARPS;
-            s0 = on ? sh.part[lane & (WARPS - 1)][0] : 0;
-            s1 = on ? sh.part[lane & (WARPS - 1)][1] : 0;
-            s2 = on ? sh.part[lane & (WARPS - 1)][2] : 0;
+            const int from = lane & (WARPS - 1);
 #pragma unroll
-            for (int o = 16; o; o >>= 1) {
-                s0 += __shfl_xor_sync(0xffffffffu, s0, o);
-                s1 += __shfl_xor_sync(0xffffffffu, s1, o);
-                s2 += __shfl_xor_sync(0xffffffffu, s2, o);
+            for (int i = 0; i < COUNT; ++i) sum[i] = lane < WARPS ? sh.part[from][i] : 0;
+            if (KEYS) {
+                lo = sh.plo[from];
+                hi = sh.phi[from];
             }
-            lo = __reduce_min_sync(0xffffffffu, sh.plo[lane & (WARPS - 1)]);
-            hi = __reduce_max_sync(0xffffffffu, sh.phi[lane & (WARPS - 1)]);
+            warps(sum, lo, hi);
             if (lane < CS) {
                 Exchange &to = cluster.map_shared_rank(&sh, lane)->ex;
-                to.sums[turn][rank][0] = s0;
-                to.sums[turn][rank][1] = s1;
-                to.sums[turn][rank][2] = s2;
-                to.lo[turn][rank] = lo;
-                to.hi[turn][rank] = hi;
+#pragma unroll
+                for (int i = 0; i < COUNT; ++i) to.sums[turn][rank][i] = sum[i];
+                if (KEYS) {
+                    to.lo[turn][rank] = lo;
+                    to.hi[turn][rank] = hi;
+                }
             }
         }
         cluster.sync();
-        s0 = s1 = s2 = 0;
-        lo = 0xffffffffu;
-        hi = 0;
-        for (int c = 0; c < CS; ++c) {
-            s0 += sh.ex.sums[turn][c][0];
-            s1 += sh.ex.sums[turn][c][1];
-            s2 += sh.ex.sums[turn][c][2];
-            lo = min(lo, sh.ex.lo[turn][c]);
-            hi = max(hi, sh.ex.hi[turn][c]);
+#pragma unroll
+        for (int i = 0; i < COUNT; ++i) sum[i] = 0;
+        if (KEYS) {
+            lo = 0xffffffffu;
+            hi = 0;
         }
+#pragma unroll
+        for (int c = 0; c < 8; ++c)
+            if (c < CS) {
+#pragma unroll
+                for (int i = 0; i < COUNT; ++i) sum[i] += sh.ex.sums[turn][c][i];
+                if (KEYS) {
+                    lo = min(lo, sh.ex.lo[turn][c]);
+                    hi = max(hi, sh.ex.hi[turn][c]);
+                }
+            }
         turn ^= 1;
+    };
+    typedef std::integral_constant<int, 0> none;
+    typedef std::integral_constant<int, 1> one;
+    typedef std::integral_constant<int, 2> two;
+    typedef std::integral_constant<int, 3> three;
+    auto reduce_sum = [&](u64 &v) {
+        uint32_t lo = 0, hi = 0;
+        reduce(one(), none(), &v, lo, hi);
     };
     // Inclusive sum over the CTA's threads.
     auto block_scan = [&](u64 v) -> u64 {
@@ -254,25 +307,39 @@ __global__ void __launch_bounds__(THREADS) sample_kernel(const SampleArgs a) {
         return v;
     };
     // The first index at which the running sum of the threads' `mine` exceeds
-    // goal(total); inside the thread that holds it, of value(element).
+    // goal(total); inside the thread that holds it the warp looks at its
+    // elements, value(element of the slice), together.
     auto locate = [&](u64 mine, auto value, auto goal_of, auto hit) {
-        u64 all = mine, z1 = 0, z2 = 0;
-        uint32_t lo = 0, hi = 0;
+        u64 all = mine;
         const int t = turn;
-        reduce(all, z1, z2, lo, hi);
+        reduce_sum(all);
         const u64 goal = goal_of(all);
         u64 before = 0;
         for (int c = 0; c < rank; ++c) before += sh.ex.sums[t][c][0];
         if (goal < before || goal >= before + sh.ex.sums[t][rank][0]) return;
         const u64 upto = before + block_scan(mine);
-        if (goal >= upto || goal < upto - mine) return;
-        u64 at = upto - mine;
-        for (int e = 0; e < EPT; ++e) {
-            at += value(e);
-            if (at > goal) {
-                hit(slice + tid * EPT + e);
-                break;
-            }
+        const unsigned holds = __ballot_sync(0xffffffffu, goal < upto && goal >= upto - mine);
+        if (holds == 0) return;
+        const int src = __ffs(holds) - 1;
+        constexpr int PER = EPT >= 32 ? EPT / 32 : 1;
+        const int e0 = (warp * 32 + src) * EPT + lane * PER;
+        u64 v[PER], sum = 0;
+#pragma unroll
+        for (int q = 0; q < PER; ++q) {
+            v[q] = lane * PER < EPT ? value(e0 + q) : 0ull;
+            sum += v[q];
+        }
+        u64 at = sum;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const u64 x = __shfl_up_sync(0xffffffffu, at, o);
+            if (lane >= o) at += x;
+        }
+        at += __shfl_sync(0xffffffffu, upto - mine, src) - sum;
+#pragma unroll
+        for (int q = 0; q < PER; ++q) {
+            if (goal >= at && goal < at + v[q]) hit(slice + e0 + q);
+            at += v[q];
         }
     };
 
@@ -281,9 +348,8 @@ __global__ void __launch_bounds__(THREADS) sample_kernel(const SampleArgs a) {
     // ---- the largest logit
     float top_l;
     {
-        u64 z0 = 0, z1 = 0, z2 = 0;
         uint32_t lo = 0, hi = key_of(best);
-        reduce(z0, z1, z2, lo, hi);
+        reduce(none(), one(), nullptr, lo, hi);
         top_l = logit_of(hi);
     }
     if (top_l == -INFINITY) {  // nothing to choose from
@@ -295,18 +361,28 @@ __global__ void __launch_bounds__(THREADS) sample_kernel(const SampleArgs a) {
     if (!(T > 0.f) || !(fabsf(mass.top) < INFINITY)) {
         // the largest logit: the first index that holds it
         u64 n = 0;
-        each([&](float l) { n += l == top_l; });
+        each([&](const float(&l)[N], int) {
+#pragma unroll
+            for (int e = 0; e < N; ++e) n += l[e] == top_l;
+        });
         locate(n, [&](int e) -> u64 { return logit(e) == top_l; }, [](u64) -> u64 { return 0; },
                [&](int index) { a.tokens[r] = index; });
         return;
     }
-    const float per_bin = fminf(__fdividef(BINS_PER_UNIT, T), 1e30f);
-    auto bin_of = [&](float v) -> int { return static_cast<int>(fminf((top_l - v) * per_bin, static_cast<float>(BINS - 1))); };
+    auto bin_of = [&](float v) -> int { return static_cast<int>(fminf(mass.depth(v), static_cast<float>(BINS - 1))); };
+    // f(MODE) for the row's mode
+    auto in_mode = [&](auto f) {
+        if (mass.mode == MODE_ONE) f(std::integral_constant<int, MODE_ONE>());
+        else if (mass.mode == MODE_FUSED) f(std::integral_constant<int, MODE_FUSED>());
+        else f(std::integral_constant<int, MODE_DIVIDE>());
+    };
     // masses of bin b are below 2^(40 - 0.04 b): shortened to 15 bits
     auto shift_of = [](int b) -> int { return max(0, 26 - static_cast<int>(static_cast<float>(b) * 0.0400748f)); };
     const int k = a.top_k ? a.top_k[r] : 0;
     const float p = a.top_p ? a.top_p[r] : 1.f;
-    const double least = static_cast<double>(a.min_p ? fminf(a.min_p[r], 1.f) : 0.f) * static_cast<double>(UNIT);
+    // min_p 2^40, rounded up to a whole mass (NaN: off)
+    const double min_mass = static_cast<double>(a.min_p ? fminf(a.min_p[r], 1.f) : 0.f) * static_cast<double>(UNIT);
+    const u64 least = min_mass > 0. ? static_cast<u64>(__double2ll_ru(min_mass)) : 0ull;
     const float u = a.u[r];
     auto share_of = [](u64 total, float x) -> u64 {  // trunc(x of total), x in [0, 1]
         return static_cast<u64>(__double2ll_rz(static_cast<double>(total) * static_cast<double>(x)));
@@ -324,7 +400,9 @@ __global__ void __launch_bounds__(THREADS) sample_kernel(const SampleArgs a) {
 #pragma unroll
         for (int q = 0; q < PER; ++q) {
             u64 v = 0;
-            for (int c = 0; c < CS; ++c) v += cluster.map_shared_rank(&sh, c)->hist[tid * PER + q];
+#pragma unroll
+            for (int c = 0; c < 8; ++c)
+                if (c < CS) v += cluster.map_shared_rank(&sh, c)->hist[tid * PER + q];
             part[q] = shortened ? v << shift_of(tid * PER + q) : v;
             sum += part[q];
         }
@@ -353,20 +431,23 @@ __global__ void __launch_bounds__(THREADS) sample_kernel(const SampleArgs a) {
     if (k > 0 && k <= SMALL_K && k < V) {
         if (best > -INFINITY) atomicAdd(&sh.hist[bin_of(best)], 1u);
         cluster.sync();
-        const int bin = goal_bin(static_cast<u64>(k), false);
+        const float deepest = static_cast<float>(goal_bin(static_cast<u64>(k), false) + 1);
+        const bool all = deepest >= static_cast<float>(BINS);
         Shared *const head = cluster.map_shared_rank(&sh, 0);
-        for (int j = 0; j < WORDS; ++j) {
-            const int q = (j + rot) & (WORDS - 1);
+        each([&](const float(&l)[N], int e0) {
+            unsigned in = 0;
 #pragma unroll
-            for (int e = 0; e < (BF16 ? 2 : 1); ++e) {
-                const float l = BF16 ? __uint_as_float(e ? own[q] & 0xffff0000u : own[q] << 16) : __uint_as_float(own[q]);
-                if (l > -INFINITY && bin_of(l) <= bin) {
+            for (int e = 0; e < N; ++e)
+                in |= static_cast<unsigned>((mass.depth(l[e]) < deepest || all) && l[e] > -INFINITY) << e;
+            if (in == 0) return;
+#pragma unroll
+            for (int e = 0; e < N; ++e)
+                if (in >> e & 1u) {
                     const int at = atomicAdd(&head->cand_n, 1);
-                    const uint32_t index = static_cast<uint32_t>(slice + tid * EPT + (BF16 ? 2 * q + e : q));
-                    if (at < CANDIDATES) head->cand[at] = static_cast<u64>(key_of(l)) << 32 | (0xffffffffu - index);
+                    if (at < CANDIDATES)
+                        head->cand[at] = static_cast<u64>(key_of(l[e])) << 32 | (0xffffffffu - static_cast<uint32_t>(slice + e0 + e));
                 }
-            }
-        }
+        });
         cluster.sync();
         const int n = *static_cast<volatile int *>(&head->cand_n);
         // (nobody may leave, or clear the count, while another still reads it)
@@ -400,7 +481,7 @@ __global__ void __launch_bounds__(THREADS) sample_kernel(const SampleArgs a) {
                 const u64 goal = max(share_of(sh.ex.found_left, p > 0.f ? p : 0.f), 1ull);
                 if (upto - m >= goal) m = 0;
             }
-            if (static_cast<double>(m) < least) m = 0;
+            if (m < least) m = 0;
             if (tid < top) sh.cand_mass[tid] = m;
             const u64 kept = block_scan(m);
             if (tid == THREADS - 1) sh.ex.found_equal = kept;
@@ -425,43 +506,69 @@ __global__ void __launch_bounds__(THREADS) sample_kernel(const SampleArgs a) {
     auto select = [&](float floor_l, bool by_mass, u64 goal, float &cut, u64 &left, u64 &equal) {
         int bin = goal_bin(goal, by_mass);
         auto measure = [&](float l) -> u64 { return by_mass ? mass.of(l) : 1ull; };
-        u64 above, inside, count;
+        u64 found[3], &above = found[0], &inside = found[1], &count = found[2];
         uint32_t klo, khi;
         while (true) {
             above = inside = count = 0;
             klo = 0xffffffffu, khi = 0;
-            each([&](float l) {
-                if (l < floor_l || l == -INFINITY) return;
-                const int b = bin_of(l);
-                if (b > bin) return;
-                const u64 m = measure(l);
-                if (b < bin) above += m;
-                else {
-                    inside += m;
-                    ++count;
-                    klo = min(klo, key_of(l));
-                    khi = max(khi, key_of(l));
-                }
+            const float upper = static_cast<float>(bin), lower = bin == BINS - 1 ? INFINITY : static_cast<float>(bin + 1);
+            in_mode([&](auto mode) {
+                uint32_t his = 0, los = 0;
+                each([&](const float(&l)[N], int) {
+                    unsigned in = 0;
+#pragma unroll
+                    for (int e = 0; e < N; ++e) {
+                        const float d = mass.depth(l[e]);
+                        const bool here = d < lower && l[e] >= floor_l;
+                        in |= static_cast<unsigned>(here && d >= upper) << e;
+                        if (by_mass) {
+                            uint32_t hi, lo;
+                            Masses::whole(here && d < upper ? mass.template scaled<mode.value>(l[e]) : 0.f, hi, lo);
+                            his += hi;
+                            los += lo;
+                        } else los += here && d < upper;
+                    }
+                    if (in) {
+#pragma unroll
+                        for (int e = 0; e < N; ++e)
+                            if ((in >> e & 1u) && l[e] > -INFINITY) {
+                                inside += by_mass ? mass.template mass<mode.value>(l[e]) : 1ull;
+                                ++count;
+                                klo = min(klo, key_of(l[e]));
+                                khi = max(khi, key_of(l[e]));
+                            }
+                    }
+                });
+                above += (static_cast<u64>(his) << 20) + los;
             });
-            reduce(above, inside, count, klo, khi);
+            reduce(three(), one(), found, klo, khi);
             if (above >= goal && bin > 0) --bin;
             else if (above + inside < goal && bin < BINS - 1) ++bin;
             else break;
         }
         while (count > LIST && klo < khi) {
             const uint32_t mid = klo + (khi - klo) / 2;
-            u64 sum = 0, n = 0, none = 0;
+            u64 part[2] = {0, 0}, &sum = part[0], &n = part[1];
             uint32_t up = 0xffffffffu, down = 0;
-            each([&](float l) {
-                const uint32_t key = key_of(l);
-                if (key < klo || key > khi || l < floor_l) return;
-                if (key > mid) {
-                    sum += measure(l);
-                    ++n;
-                    up = min(up, key);
-                } else down = max(down, key);
+            const float flo = fmaxf(logit_of(klo), floor_l), fhi = logit_of(khi);
+            each([&](const float(&l)[N], int) {
+                unsigned in = 0;
+#pragma unroll
+                for (int e = 0; e < N; ++e) in |= static_cast<unsigned>(l[e] >= flo && l[e] <= fhi) << e;
+                if (in) {
+#pragma unroll
+                    for (int e = 0; e < N; ++e)
+                        if (in >> e & 1u) {
+                            const uint32_t key = key_of(l[e]);
+                            if (key > mid) {
+                                sum += measure(l[e]);
+                                ++n;
+                                up = min(up, key);
+                            } else down = max(down, key);
+                        }
+                }
             });
-            reduce(sum, n, none, up, down);
+            reduce(two(), one(), part, up, down);
             if (above + sum >= goal) {
                 klo = up;
                 count = n;
@@ -478,14 +585,17 @@ __global__ void __launch_bounds__(THREADS) sample_kernel(const SampleArgs a) {
             return;
         }
         Shared *const head = cluster.map_shared_rank(&sh, 0);
-        each([&](float l) {
-            const uint32_t key = key_of(l);
-            if (key < klo || key > khi || l < floor_l) return;
-            const int at = atomicAdd(&head->list_n, 1);
-            if (at < LIST) {
-                head->list_key[at] = key;
-                head->list_mass[at] = measure(l);
-            }
+        const float flo = fmaxf(logit_of(klo), floor_l), fhi = logit_of(khi);
+        each([&](const float(&l)[N], int) {
+#pragma unroll
+            for (int e = 0; e < N; ++e)
+                if (l[e] >= flo && l[e] <= fhi) {
+                    const int at = atomicAdd(&head->list_n, 1);
+                    if (at < LIST) {
+                        head->list_key[at] = key_of(l[e]);
+                        head->list_mass[at] = measure(l[e]);
+                    }
+                }
         });
         cluster.sync();
         if (rank == 0) {
@@ -524,15 +634,16 @@ __global__ void __launch_bounds__(THREADS) sample_kernel(const SampleArgs a) {
     float cut = -INFINITY;
     u64 ties = ~0ull, equal = 0;
     if (k > 0 && k < V) {
-        u64 finite = 0, z1 = 0, z2 = 0;
-        uint32_t lo = 0, hi = 0;
-        each([&](float l) {
-            if (l > -INFINITY) {
-                ++finite;
-                atomicAdd(&sh.hist[bin_of(l)], 1u);
-            }
+        u64 finite = 0;
+        each([&](const float(&l)[N], int) {
+#pragma unroll
+            for (int e = 0; e < N; ++e)
+                if (l[e] > -INFINITY) {
+                    ++finite;
+                    atomicAdd(&sh.hist[bin_of(l[e])], 1u);
+                }
         });
-        reduce(finite, z1, z2, lo, hi);
+        reduce_sum(finite);
         if (static_cast<u64>(k) < finite) select(-INFINITY, false, static_cast<u64>(k), cut, ties, equal);
         cluster.sync();  // the others have read this histogram
         for (int i = tid; i < BINS; i += THREADS) sh.hist[i] = 0;
@@ -540,26 +651,26 @@ __global__ void __launch_bounds__(THREADS) sample_kernel(const SampleArgs a) {
     }
     if (p < 1.f) {
         // the masses that are left: their sum and histogram
-        u64 sum = 0, z1 = 0, z2 = 0;
-        uint32_t lo = 0, hi = 0, small = 0;
-        each([&](float l) {
-            if (l < cut || l == -INFINITY) return;
-            const float t = mass.scaled(l);
-            const int b = bin_of(l);
-            uint32_t v;
-            if (t < 4194304.f) {  // below 2^22: rint by adding 2^23 (at most 2^6 such per thread)
-                const uint32_t m = __float_as_uint(__fadd_rn(t, 8388608.f)) & 0x7fffffu;
-                if (l > cut) small += m;
-                v = m >> shift_of(b);
-            } else {
-                const u64 m = static_cast<u64>(__float2ll_rn(t));
-                if (l > cut) sum += m;
-                v = static_cast<uint32_t>(m >> shift_of(b));
-            }
-            if (v) atomicAdd(&sh.hist[b], v);
+        u64 sum = 0;
+        in_mode([&](auto mode) {
+            uint32_t his = 0, los = 0;
+            each([&](const float(&l)[N], int) {
+#pragma unroll
+                for (int e = 0; e < N; ++e) {
+                    const float d = mass.depth(l[e]);
+                    const float t = l[e] >= cut ? mass.template scaled<mode.value>(l[e]) : 0.f;
+                    uint32_t hi, lo;
+                    Masses::whole(l[e] > cut ? t : 0.f, hi, lo);
+                    his += hi;
+                    los += lo;
+                    const int b = static_cast<int>(fminf(d, static_cast<float>(BINS - 1)));
+                    const uint32_t v = static_cast<uint32_t>(t * __uint_as_float(static_cast<uint32_t>(127 - shift_of(b)) << 23));
+                    if (v) atomicAdd(&sh.hist[b], v);
+                }
+            });
+            sum += (static_cast<u64>(his) << 20) + los;
         });
-        sum += small;
-        reduce(sum, z1, z2, lo, hi);
+        reduce_sum(sum);
         if (cut > -INFINITY) sum += (ties < equal ? ties : equal) * mass.of(cut);
         const u64 goal = max(share_of(sum, p > 0.f ? p : 0.f), 1ull);
         float cut2;
@@ -575,7 +686,10 @@ __global__ void __launch_bounds__(THREADS) sample_kernel(const SampleArgs a) {
     if (cut > -INFINITY && ties < equal) {
         const u64 n = ties;
         u64 mine = 0;
-        each([&](float l) { mine += l == cut; });
+        each([&](const float(&l)[N], int) {
+#pragma unroll
+            for (int e = 0; e < N; ++e) mine += l[e] == cut;
+        });
         locate(mine, [&](int e) -> u64 { return logit(e) == cut; }, [&](u64) -> u64 { return n - 1; },
                [&](int index) {
                    for (int c = 0; c < CS; ++c) cluster.map_shared_rank(&sh, c)->ex.found_index = index;
@@ -586,35 +700,43 @@ __global__ void __launch_bounds__(THREADS) sample_kernel(const SampleArgs a) {
     // logits below this have a mass under min_p's (or none): no exponential is
     // taken of them.  A little lower than the bound itself, which is rounded.
     float floor_l = cut;
-    if (least > 0.) {
+    if (least > 0) {
         const float reach = -logf(fminf(fmaxf(a.min_p[r], 1e-30f), 1.f)) * T;  // max - l at the bound
         const float lowest = top_l - reach * 1.0001f - 1e-4f * (fabsf(top_l) + T);
         floor_l = fmaxf(floor_l, lowest);
     }
     auto kept = [&](float l, int index) -> u64 {
-        if (l < floor_l || l == -INFINITY || (l == cut && index > last_tie)) return 0ull;
+        if (l < floor_l || (l == cut && index > last_tie)) return 0ull;
         const u64 m = mass.of(l);
-        return static_cast<double>(m) < least ? 0ull : m;
+        return m < least ? 0ull : m;
     };
+    // the least scaled mass that rounds to `least`: least - 1/2 if that ties to
+    // it, or the next above; from 2^23 on scaled masses are whole themselves
+    const float least_t = least == 0             ? -1.f
+                          : least < (1ull << 23) ? __uint_as_float(__float_as_uint(static_cast<float>(least) - 0.5f) + (least & 1u))
+                                                 : __ull2float_ru(least);
     u64 mine = 0;
-    if (cut == -INFINITY && least <= 0.) {  // everything
-        uint32_t small = 0;
-        each([&](float l) {
-            const float t = mass.scaled(l);
-            if (t < 4194304.f) small += __float_as_uint(__fadd_rn(t, 8388608.f)) & 0x7fffffu;
-            else mine += static_cast<u64>(__float2ll_rn(t));
+    in_mode([&](auto mode) {
+        uint32_t his = 0, los = 0;
+        each([&](const float(&l)[N], int e0) {
+            // (l > -infinity too: cut and floor_l may be that)
+            bool any = false;
+#pragma unroll
+            for (int e = 0; e < N; ++e) any |= l[e] >= floor_l;
+            if (!any) return;
+#pragma unroll
+            for (int e = 0; e < N; ++e) {
+                const bool in = l[e] >= floor_l && !(l[e] == cut && slice + e0 + e > last_tie);
+                const float t = in ? mass.template scaled<mode.value>(l[e]) : 0.f;
+                uint32_t hi, lo;
+                Masses::whole(t >= least_t ? t : 0.f, hi, lo);
+                his += hi;
+                los += lo;
+            }
         });
-        mine += small;
-    } else {
-        const bool tie_here = slice + tid * EPT <= last_tie && last_tie < slice + (tid + 1) * EPT;
-        if (tie_here) {
-            for (int e = 0; e < EPT; ++e) mine += kept(logit(e), slice + tid * EPT + e);
-        } else {
-            const int index = slice + tid * EPT;  // all of this thread's are on one side of the last tie
-            each([&](float l) { mine += kept(l, index); });
-        }
-    }
-    locate(mine, [&](int e) -> u64 { return kept(logit(e), slice + tid * EPT + e); }, draw,
+        mine += (static_cast<u64>(his) << 20) + los;
+    });
+    locate(mine, [&](int e) -> u64 { return kept(logit(e), slice + e); }, draw,
            [&](int index) { a.tokens[r] = index; });
 }
 
