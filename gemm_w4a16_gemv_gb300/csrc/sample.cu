@@ -70,8 +70,8 @@ struct Exchange {            // what a CTA's peers write into its shared memory
     u64 found_left, found_equal;
 };
 struct Shared {
+    alignas(16) uint32_t hist[BINS];
     Exchange ex;
-    uint32_t hist[BINS];
     u64 part[WARPS][3];
     uint32_t plo[WARPS], phi[WARPS];
     u64 scan[WARPS];
@@ -172,29 +172,46 @@ __global__ void __launch_bounds__(THREADS) sample_kernel(const SampleArgs a) {
         const unsigned char *p = static_cast<const unsigned char *>(a.logits) +
                                  (r * a.row_stride + slice) * (BF16 ? 2 : 4);
         const bool vec = (reinterpret_cast<uintptr_t>(p) & 15u) == 0;
-#pragma unroll 4
-        for (int i = tid; i < EPT * THREADS / PER; i += THREADS) {
-            const int left = V - slice - i * PER;  // logits from here on
-            uint4 w;
-            uint32_t *const x = reinterpret_cast<uint32_t *>(&w);
-            if (vec && left >= PER) w = *reinterpret_cast<const uint4 *>(p + 16 * static_cast<int64_t>(i));
-            else {
+        constexpr int COUNT = EPT / PER, BATCH = COUNT < 8 ? COUNT : 8;  // vectors a thread, and at a time
+        const bool inside = vec && V - slice >= EPT * THREADS;
+#pragma unroll 1
+        for (int i0 = 0; i0 < COUNT; i0 += BATCH) {
+            uint4 w[BATCH];
+            if (inside) {
 #pragma unroll
-                for (int e = 0; e < PER; ++e) {
-                    if (BF16) {
-                        const uint32_t h = e < left ? reinterpret_cast<const uint16_t *>(p)[i * PER + e] : 0xff80u;
-                        x[e / 2] = e & 1 ? x[e / 2] | h << 16 : h;
-                    } else x[e & 3] = e < left ? reinterpret_cast<const uint32_t *>(p)[i * PER + e] : 0xff800000u;
+                for (int q = 0; q < BATCH; ++q)
+                    w[q] = *reinterpret_cast<const uint4 *>(p + 16 * static_cast<int64_t>((i0 + q) * THREADS + tid));
+            } else {
+#pragma unroll
+                for (int q = 0; q < BATCH; ++q) {
+                    const int first = ((i0 + q) * THREADS + tid) * PER, left = V - slice - first;  // logits from here on
+                    uint32_t x[4];
+                    if (vec && left >= PER) {
+                        w[q] = *reinterpret_cast<const uint4 *>(p + 16 * static_cast<int64_t>((i0 + q) * THREADS + tid));
+                        continue;
+                    }
+#pragma unroll
+                    for (int e = 0; e < PER; ++e) {
+                        if (BF16) {
+                            const uint32_t h = e < left ? reinterpret_cast<const uint16_t *>(p)[first + e] : 0xff80u;
+                            x[e / 2] = e & 1 ? x[e / 2] | h << 16 : h;
+                        } else x[e & 3] = e < left ? reinterpret_cast<const uint32_t *>(p)[first + e] : 0xff800000u;
+                    }
+                    w[q] = make_uint4(x[0], x[1], x[2], x[3]);
                 }
             }
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                if (BF16) {
-                    const float lo = clean(__uint_as_float(x[e] << 16)), hi = clean(__uint_as_float(x[e] & 0xffff0000u));
-                    x[e] = __float_as_uint(lo) >> 16 | (__float_as_uint(hi) & 0xffff0000u);
-                } else x[e] = __float_as_uint(clean(__uint_as_float(x[e])));
+            for (int q = 0; q < BATCH; ++q) {
+                uint32_t x[4] = {w[q].x, w[q].y, w[q].z, w[q].w};
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    if (BF16) {
+                        const float lo = clean(__uint_as_float(x[e] << 16)), hi = clean(__uint_as_float(x[e] & 0xffff0000u));
+                        x[e] = __float_as_uint(lo) >> 16 | (__float_as_uint(hi) & 0xffff0000u);
+                    } else x[e] = __float_as_uint(clean(__uint_as_float(x[e])));
+                }
+                reinterpret_cast<uint4 *>(row)[(i0 + q) * THREADS + tid] = make_uint4(x[0], x[1], x[2], x[3]);
             }
-            reinterpret_cast<uint4 *>(row)[i] = w;
         }
     }
 
@@ -395,16 +412,26 @@ __global__ void __launch_bounds__(THREADS) sample_kernel(const SampleArgs a) {
     // goal: the same in every CTA.  If none does: the last bin, or where sums
     // are shortened the last one with anything.
     auto goal_bin = [&](u64 goal, bool shortened) -> int {
-        constexpr int PER = BINS / THREADS;
-        u64 part[PER], sum = 0;
-#pragma unroll
-        for (int q = 0; q < PER; ++q) {
-            u64 v = 0;
+        // four bins a thread (16 bytes of each CTA's histogram), half the threads
+        constexpr int PER = 4;
+        u64 part[PER] = {}, sum = 0;
+        if (tid < BINS / PER) {
+            uint4 v[8];
 #pragma unroll
             for (int c = 0; c < 8; ++c)
-                if (c < CS) v += cluster.map_shared_rank(&sh, c)->hist[tid * PER + q];
-            part[q] = shortened ? v << shift_of(tid * PER + q) : v;
-            sum += part[q];
+                v[c] = c < CS ? reinterpret_cast<const uint4 *>(cluster.map_shared_rank(&sh, c)->hist)[tid] : make_uint4(0, 0, 0, 0);
+#pragma unroll
+            for (int c = 0; c < 8; ++c) {
+                part[0] += v[c].x;
+                part[1] += v[c].y;
+                part[2] += v[c].z;
+                part[3] += v[c].w;
+            }
+#pragma unroll
+            for (int q = 0; q < PER; ++q) {
+                if (shortened) part[q] <<= shift_of(tid * PER + q);
+                sum += part[q];
+            }
         }
         if (tid == 0) sh.bin = -1;
         u64 upto = block_scan(sum);   // (its barriers order the line above)
@@ -454,23 +481,33 @@ __global__ void __launch_bounds__(THREADS) sample_kernel(const SampleArgs a) {
         cluster.sync();
         if (n <= CANDIDATES) {
             if (rank != 0) return;
-            int size = 2;
-            while (size < n) size <<= 1;
-            for (int i = n + tid; i < size; i += THREADS) sh.cand[i] = 0;
-            __syncthreads();
             // falling order of key, rising order of index
-            for (int s = 2; s <= size; s <<= 1)
-                for (int d = s >> 1; d; d >>= 1) {
-                    for (int i = tid; i < size / 2; i += THREADS) {
-                        const int x = 2 * i - (i & (d - 1)), y = x + d;
-                        const u64 A = sh.cand[x], B = sh.cand[y];
-                        if ((A < B) == ((x & s) == 0)) {
-                            sh.cand[x] = B;
-                            sh.cand[y] = A;
+            if (n <= THREADS / 2) {  // every candidate counts those ahead of it
+                const u64 own_cand = tid < n ? sh.cand[tid] : 0;
+                int ahead = 0;
+#pragma unroll 4
+                for (int j = 0; j < n; ++j) ahead += sh.cand[j] > own_cand;
+                __syncthreads();
+                if (tid < n) sh.cand[ahead] = own_cand;
+                __syncthreads();
+            } else {
+                int size = 2;
+                while (size < n) size <<= 1;
+                for (int i = n + tid; i < size; i += THREADS) sh.cand[i] = 0;
+                __syncthreads();
+                for (int s = 2; s <= size; s <<= 1)
+                    for (int d = s >> 1; d; d >>= 1) {
+                        for (int i = tid; i < size / 2; i += THREADS) {
+                            const int x = 2 * i - (i & (d - 1)), y = x + d;
+                            const u64 A = sh.cand[x], B = sh.cand[y];
+                            if ((A < B) == ((x & s) == 0)) {
+                                sh.cand[x] = B;
+                                sh.cand[y] = A;
+                            }
                         }
+                        __syncthreads();
                     }
-                    __syncthreads();
-                }
+            }
             const int top = min(k, n);
             u64 m = 0;
             if (tid < top) m = mass.of(logit_of(static_cast<uint32_t>(sh.cand[tid] >> 32)));
@@ -490,6 +527,7 @@ __global__ void __launch_bounds__(THREADS) sample_kernel(const SampleArgs a) {
                 const u64 goal = draw(sh.ex.found_equal);
                 const uint32_t me = static_cast<uint32_t>(sh.cand[tid]);  // falls as the index rises
                 u64 before = 0;
+#pragma unroll 4
                 for (int j = 0; j < top; ++j)
                     if (static_cast<uint32_t>(sh.cand[j]) > me) before += sh.cand_mass[j];
                 if (goal >= before && goal < before + m) a.tokens[r] = static_cast<int>(0xffffffffu - me);
