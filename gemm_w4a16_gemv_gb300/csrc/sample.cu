@@ -584,6 +584,59 @@ __global__ void __launch_bounds__(THREADS) sample_kernel(const SampleArgs a) {
             else if (above + inside < goal && bin < BINS - 1) ++bin;
             else break;
         }
+        // BF16: a count per distinct key of the bin says everything (equal keys
+        // have equal masses)
+        if (BF16 && count > LIST && klo < khi && (khi - klo) >> 16 < static_cast<uint32_t>(BINS) &&
+            (khi ^ klo) >> 31 == 0) {  // (of one sign: the keys are 2^16 apart)
+            // (every CTA has read the first histogram: the sums above were exchanged since)
+            for (int i = tid; i < BINS; i += THREADS) sh.hist[i] = 0;
+            __syncthreads();
+            const float flo = fmaxf(logit_of(klo), floor_l), fhi = logit_of(khi);
+            each([&](const float(&l)[N], int) {
+                unsigned in = 0;
+#pragma unroll
+                for (int e = 0; e < N; ++e) in |= static_cast<unsigned>(l[e] >= flo && l[e] <= fhi) << e;
+                if (in) {
+#pragma unroll
+                    for (int e = 0; e < N; ++e)
+                        if (in >> e & 1u) atomicAdd(&sh.hist[(khi - key_of(l[e])) >> 16], 1u);
+                }
+            });
+            cluster.sync();
+            u64 sum = 0, part[4] = {};
+            uint32_t counts[4] = {};
+            if (tid < BINS / 4) {
+#pragma unroll
+                for (int c = 0; c < 8; ++c)
+                    if (c < CS) {
+                        const uint4 v = reinterpret_cast<const uint4 *>(cluster.map_shared_rank(&sh, c)->hist)[tid];
+                        counts[0] += v.x;
+                        counts[1] += v.y;
+                        counts[2] += v.z;
+                        counts[3] += v.w;
+                    }
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                    if (counts[q]) part[q] = counts[q] * measure(logit_of(khi - (static_cast<uint32_t>(tid * 4 + q) << 16)));
+                    sum += part[q];
+                }
+            }
+            u64 at = above + block_scan(sum) - sum;
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                if (at < goal && at + part[q] >= goal) {
+                    sh.ex.found_key = khi - (static_cast<uint32_t>(tid * 4 + q) << 16);
+                    sh.ex.found_left = goal - at;
+                    sh.ex.found_equal = counts[q];
+                }
+                at += part[q];
+            }
+            cluster.sync();  // (the histogram may be written again, and nobody is still reading)
+            cut = logit_of(sh.ex.found_key);
+            left = sh.ex.found_left;
+            equal = sh.ex.found_equal;
+            return;
+        }
         while (count > LIST && klo < khi) {
             const uint32_t mid = klo + (khi - klo) / 2;
             u64 part[2] = {0, 0}, &sum = part[0], &n = part[1];
