@@ -14,6 +14,8 @@ from __future__ import annotations
 
 import collections
 import ctypes
+import importlib.machinery
+import importlib.util
 import os
 import threading
 
@@ -35,8 +37,10 @@ __all__ = [
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 _LIB_PATH = os.path.join(_HERE, "_lib", "libw4a16.so")
+_MARSHAL_PATH = os.path.join(_HERE, "_lib", "_marshal.so")
 _lock = threading.Lock()
 _lib = None
+_addresses = None  # the extension's check of a call's tensors
 
 STATUS = {0: "OK", 1: "INVALID_ARG", 2: "UNSUPPORTED", 3: "MISALIGNED",
           4: "CUDA", 5: "TIMEOUT", 6: "DEVICE"}
@@ -106,7 +110,7 @@ def library_path() -> str:
 
 def lib():
     """The loaded CUDA library (raises if it has not been built)."""
-    global _lib
+    global _lib, _addresses
     if _lib is not None:
         return _lib
     with _lock:
@@ -119,6 +123,11 @@ def lib():
                 fn = getattr(handle, name)
                 fn.argtypes = argtypes
                 fn.restype = restype
+            loader = importlib.machinery.ExtensionFileLoader("_marshal", _MARSHAL_PATH)
+            spec = importlib.util.spec_from_file_location("_marshal", _MARSHAL_PATH, loader=loader)
+            module = importlib.util.module_from_spec(spec)
+            loader.exec_module(module)
+            _addresses = module.addresses
             _lib = handle
         return _lib
 
@@ -505,20 +514,45 @@ def _rows(t, name, device):
     return t.data_ptr(), (a if T > 1 else H * D)
 
 
-def _on_device(device, fn, *args):
-    """Calls the library with `device` current (which it usually is)."""
+_TYPES = {"b": torch.uint8, "h": torch.bfloat16, "i": torch.int32, "l": torch.int64, "f": torch.float32}
+
+
+def _checked(device, spec, names, *tensors):
+    """Addresses of a call's tensors, given as tensor, count, tensor, count
+    ...: by the extension, or one by one to say what is wrong."""
+    if device.type == "cuda":
+        lib()
+        got = _addresses(device.index, spec, *tensors)
+        if got is not None:
+            return got
+    out = []
+    for c, name, t, n in zip(spec, names, tensors[0::2], tensors[1::2]):
+        if c == "r":
+            out += _rows(t, name, device) if t is not None else (None, 0)
+        else:
+            out.append(_ptr(t, name, _TYPES[c], device, n if n >= 0 else None))
     if device.type != "cuda":
         raise ValueError("expected CUDA tensors, got %s" % device)
+    return out
+
+
+def _launch(device, stream, fn, *args):
+    """Calls the library with `device` current (which it usually is)."""
+    if stream is None and _raw_stream is not None:
+        handle = _raw_stream(device.index)
+    else:
+        handle = _stream(stream, device)
     if torch.cuda.current_device() == device.index:
-        status = fn(*args)
+        status = fn(*args, handle)
     else:
         with torch.cuda.device(device):
-            status = fn(*args)
+            status = fn(*args, handle)
     if status != 0:
         _check(status)
 
 
 KV4Plan = collections.namedtuple("KV4Plan", "seq_lens cu_new positions slots taken")
+_PLAN_NAMES = ("ctx_lens", "new_lens", "block_table", "free_blocks", "seq_lens", "cu_new", "positions", "slots", "taken")
 
 
 def kv4_plan_buffers(requests: int, num_tokens: int, device=None) -> KV4Plan:
@@ -544,24 +578,26 @@ def kv4_plan(ctx_lens, new_lens, block_table, free_blocks, block_size: int, num_
         out = kv4_plan_buffers(B, num_tokens, dev)
     if block_table.dim() != 2 or block_table.shape[0] != B:
         raise ValueError("block_table must be [%d, max_blocks]" % B)
-    T = out.positions.numel()
-    i32 = torch.int32
-    _on_device(dev, lib().kv4_plan, _ptr(ctx_lens, "ctx_lens", i32, dev), _ptr(new_lens, "new_lens", i32, dev, B), B,
-               _ptr(block_table, "block_table", i32, dev), block_table.shape[1],
-               _ptr(free_blocks, "free_blocks", i32, dev), free_blocks.numel(), block_size, T,
-               _ptr(out.seq_lens, "seq_lens", i32, dev, B), _ptr(out.cu_new, "cu_new", i32, dev, B + 1),
-               _ptr(out.positions, "positions", i32, dev), _ptr(out.slots, "slots", torch.int64, dev, T),
-               _ptr(out.taken, "taken", i32, dev, 1), _stream(stream, dev))
+    seq, cu, pos, slots, taken = out
+    T = pos.numel()
+    a = _checked(dev, "iiiiiiili", _PLAN_NAMES, ctx_lens, B, new_lens, B, block_table, -1, free_blocks, -1, seq, B, cu,
+                 B + 1, pos, T, slots, T, taken, 1)
+    _launch(dev, stream, lib().kv4_plan, a[0], a[1], B, a[2], block_table.shape[1], a[3], free_blocks.numel(), block_size,
+            T, a[4], a[5], a[6], a[7], a[8])
     return out
 
 
-def _rope_args(dev, D, q_weight, k_weight, cos_sin, positions, T):
-    rows, rot = cos_sin.shape if cos_sin is not None else (0, 0)
-    if cos_sin is not None and positions is None:
+_ROPE_NAMES = ("q", "k", "q_weight", "k_weight", "cos_sin", "positions", "q_out", "k_out")
+
+
+def _table(cos_sin, positions):
+    """Rows and width of a cos_sin table (0, 0: no rotation)."""
+    if cos_sin is None:
+        return 0, 0
+    if positions is None:
         raise ValueError("cos_sin needs positions")
-    return (_ptr(q_weight, "q_weight", torch.bfloat16, dev, D), _ptr(k_weight, "k_weight", torch.bfloat16, dev, D),
-            _ptr(cos_sin, "cos_sin", torch.float32, dev), rows, rot,
-            _ptr(positions, "positions", torch.int32, dev, T) if cos_sin is not None else None)
+    rows, rot = cos_sin.shape
+    return rows, rot
 
 
 def w4a16_qk_norm_rope(q, k, q_weight, k_weight, cos_sin, positions, q_out=None, k_out=None, eps: float = 1e-6,
@@ -572,20 +608,18 @@ def w4a16_qk_norm_rope(q, k, q_weight, k_weight, cos_sin, positions, q_out=None,
     (q_out, k_out)."""
     dev = q.device
     T, Hq, D = q.shape
-    Hk = k.shape[1]
-    pq, sq = _rows(q, "q", dev)
-    pk, sk = _rows(k, "k", dev)
-    if k.shape[0] != T or k.shape[2] != D:
+    Tk, Hk, Dk = k.shape
+    if Tk != T or Dk != D:
         raise ValueError("k must be [%d, heads, %d]" % (T, D))
+    rows, rot = _table(cos_sin, positions)
     if q_out is None:
         q_out = torch.empty(T, Hq, D, dtype=torch.bfloat16, device=dev)
     if k_out is None:
         k_out = torch.empty(T, Hk, D, dtype=torch.bfloat16, device=dev)
-    _on_device(dev, lib().w4a16_qk_norm_rope, pq, sq, pk, sk,
-               *_rope_args(dev, D, q_weight, k_weight, cos_sin, positions, T),
-               _ptr(q_out, "q_out", torch.bfloat16, dev, T * Hq * D),
-               _ptr(k_out, "k_out", torch.bfloat16, dev, T * Hk * D), T, Hq, Hk, D, eps, weight_offset,
-               1 if interleaved else 0, _stream(stream, dev))
+    a = _checked(dev, "rrhhfihh", _ROPE_NAMES, q, 0, k, 0, q_weight, D, k_weight, D, cos_sin, -1,
+                 positions if rot else None, T, q_out, T * Hq * D, k_out, T * Hk * D)
+    _launch(dev, stream, lib().w4a16_qk_norm_rope, a[0], a[1], a[2], a[3], a[4], a[5], a[6], rows, rot, a[7], a[8], a[9],
+            T, Hq, Hk, D, eps, weight_offset, 1 if interleaved else 0)
     return q_out, k_out
 
 
@@ -597,12 +631,15 @@ def kv4_cache(num_blocks: int, Hkv: int, block_size: int, D: int, device=None) -
                        device=device if device is not None else "cuda")
 
 
-def _cache(cache, dev):
-    """Address, blocks, page size, heads and D of a cache tensor."""
-    p = _ptr(cache, "cache", torch.uint8, dev)
-    if cache.dim() != 4 or cache.shape[3] % 18 != 0:
+def _cache_shape(cache):
+    """Blocks, page size, heads and D of a cache tensor."""
+    shape = cache.shape
+    if len(shape) != 4 or shape[3] % 18 != 0:
         raise ValueError("cache must be [num_blocks, Hkv, block_size / 16, 18 D]")
-    return p, cache.shape[0], cache.shape[2] * 16, cache.shape[1], cache.shape[3] // 18
+    return shape[0], shape[2] * 16, shape[1], shape[3] // 18
+
+
+_APPEND_NAMES = ("q", "k", "v", "q_weight", "k_weight", "cos_sin", "positions", "slots", "q_out", "cache")
 
 
 def kv4_append(k, v, cache, slots, q=None, q_weight=None, k_weight=None, cos_sin=None, positions=None, q_out=None,
@@ -611,41 +648,38 @@ def kv4_append(k, v, cache, slots, q=None, q_weight=None, k_weight=None, cos_sin
     weights or cos_sin also norm and rotation of k, and of q [T, Hq, D] where
     given, in the same pass.  Returns q_out (None without q)."""
     dev = cache.device
-    pc, blocks, bs, Hkv, D = _cache(cache, dev)
+    blocks, bs, Hkv, D = _cache_shape(cache)
     T = k.shape[0]
-    pk, sk = _rows(k, "k", dev)
-    pv, sv = _rows(v, "v", dev)
     for name, t in (("k", k), ("v", v)):
-        if tuple(t.shape) != (T, Hkv, D):
+        if t.shape != (T, Hkv, D):
             raise ValueError("%s must be [%d, %d, %d]" % (name, T, Hkv, D))
-    Hq, pq, sq, po = 0, None, 0, None
+    rows, rot = _table(cos_sin, positions)
+    Hq = 0
     if q is not None:
-        Hq = q.shape[1]
-        pq, sq = _rows(q, "q", dev)
-        if q.shape[0] != T or q.shape[2] != D:
+        Tq, Hq, Dq = q.shape
+        if Tq != T or Dq != D:
             raise ValueError("q must be [%d, heads, %d]" % (T, D))
         if q_out is None:
             q_out = torch.empty(T, Hq, D, dtype=torch.bfloat16, device=dev)
-        po = _ptr(q_out, "q_out", torch.bfloat16, dev, T * Hq * D)
-    _on_device(dev, lib().kv4_append, pq, sq, pk, sk, pv, sv,
-               *_rope_args(dev, D, q_weight, k_weight, cos_sin, positions, T),
-               _ptr(slots, "slots", torch.int64, dev, T), po, pc, blocks, bs, T, Hq, Hkv, D, eps, weight_offset,
-               1 if interleaved else 0, _stream(stream, dev))
+    a = _checked(dev, "rrrhhfilhb", _APPEND_NAMES, q, 0, k, 0, v, 0, q_weight, D, k_weight, D, cos_sin, -1,
+                 positions if rot else None, T, slots, T, q_out if q is not None else None, T * Hq * D, cache, -1)
+    _launch(dev, stream, lib().kv4_append, a[0], a[1], a[2], a[3], a[4], a[5], a[6], a[7], a[8], rows, rot, a[9], a[10],
+            a[11], a[12], blocks, bs, T, Hq, Hkv, D, eps, weight_offset, 1 if interleaved else 0)
     return q_out if q is not None else None
 
 
 def kv4_gather(cache, slots, k=None, v=None, stream=None):
     """The values the cache holds at `slots`: (k, v) bfloat16 [T, Hkv, D]."""
     dev = cache.device
-    pc, blocks, bs, Hkv, D = _cache(cache, dev)
+    blocks, bs, Hkv, D = _cache_shape(cache)
     T = slots.numel()
     if k is None:
         k = torch.empty(T, Hkv, D, dtype=torch.bfloat16, device=dev)
     if v is None:
         v = torch.empty(T, Hkv, D, dtype=torch.bfloat16, device=dev)
-    _on_device(dev, lib().kv4_gather, pc, blocks, bs, _ptr(slots, "slots", torch.int64, dev),
-               _ptr(k, "k", torch.bfloat16, dev, T * Hkv * D), _ptr(v, "v", torch.bfloat16, dev, T * Hkv * D), T, Hkv,
-               D, _stream(stream, dev))
+    n = T * Hkv * D
+    a = _checked(dev, "blhh", ("cache", "slots", "k", "v"), cache, -1, slots, T, k, n, v, n)
+    _launch(dev, stream, lib().kv4_gather, a[0], blocks, bs, a[1], a[2], a[3], T, Hkv, D)
     return k, v
 
 
@@ -660,6 +694,9 @@ def kv4_attention_scratch(Hq: int, Hkv: int, D: int, device=None) -> torch.Tenso
                        device=device if device is not None else "cuda")
 
 
+_ATTENTION_NAMES = ("q", "cache", "block_table", "seq_lens", "cu_new", "out", "scratch")
+
+
 def kv4_attention(q, cache, block_table, seq_lens, cu_new, scratch, out=None, scale=None, window: int = 0,
                   sinks: int = 0, max_new=None, stream=None):
     """Attention of the new tokens q [T, Hq, D] over the 4-bit cache, causal
@@ -668,8 +705,7 @@ def kv4_attention(q, cache, block_table, seq_lens, cu_new, scratch, out=None, sc
     1 / sqrt(D) when None; `scratch` from kv4_attention_scratch.  Returns
     out bfloat16 [T, Hq, D]."""
     dev = cache.device
-    pc, blocks, bs, Hkv, D = _cache(cache, dev)
-    pq, sq = _rows(q, "q", dev)
+    blocks, bs, Hkv, D = _cache_shape(cache)
     T, Hq, Dq = q.shape
     if Dq != D:
         raise ValueError("q has heads of %d, the cache of %d" % (Dq, D))
@@ -678,14 +714,15 @@ def kv4_attention(q, cache, block_table, seq_lens, cu_new, scratch, out=None, sc
         raise ValueError("block_table must be [%d, max_blocks]" % B)
     if out is None:
         out = torch.empty(T, Hq, D, dtype=torch.bfloat16, device=dev)
-    i32 = torch.int32
-    _on_device(dev, lib().kv4_attention, pq, sq, pc, blocks, bs, _ptr(block_table, "block_table", i32, dev),
-               block_table.shape[1], _ptr(seq_lens, "seq_lens", i32, dev), _ptr(cu_new, "cu_new", i32, dev, B + 1), B,
-               _ptr(out, "out", torch.bfloat16, dev, T * Hq * D), T, Hq, Hkv, D,
-               float(scale) if scale is not None else D ** -0.5, window, sinks,
-               int(max_new) if max_new is not None else max(T, 1), _ptr(scratch, "scratch", torch.uint8, dev),
-               scratch.numel(), _stream(stream, dev))
+    a = _checked(dev, "rbiiihb", _ATTENTION_NAMES, q, 0, cache, -1, block_table, -1, seq_lens, B, cu_new, B + 1, out,
+                 T * Hq * D, scratch, -1)
+    _launch(dev, stream, lib().kv4_attention, a[0], a[1], a[2], blocks, bs, a[3], block_table.shape[1], a[4], a[5], B,
+            a[6], T, Hq, Hkv, D, D ** -0.5 if scale is None else scale, window, sinks,
+            max(T, 1) if max_new is None else max_new, a[7], scratch.numel())
     return out
+
+
+_SAMPLE_NAMES = ("u", "temperature", "top_k", "top_p", "min_p", "out")
 
 
 def w4a16_sample(logits, u, temperature=None, top_k=None, top_p=None, min_p=None, out=None, stream=None):
@@ -693,19 +730,17 @@ def w4a16_sample(logits, u, temperature=None, top_k=None, top_p=None, min_p=None
     bfloat16, rows may be strided) from the uniform numbers u [rows]; the
     settings are per-row tensors or None (off)."""
     dev = logits.device
-    if logits.dim() != 2 or (logits.stride(1) != 1 and logits.shape[1] > 1):
-        raise ValueError("logits must be [rows, vocab] with contiguous rows")
-    if logits.dtype not in (torch.float32, torch.bfloat16):
-        raise TypeError("logits must be torch.float32 or torch.bfloat16, got %s" % logits.dtype)
     R, V = logits.shape
-    f32 = torch.float32
+    if logits.stride(1) != 1 and V > 1:
+        raise ValueError("logits must be [rows, vocab] with contiguous rows")
+    dt = logits.dtype
+    if dt is not torch.float32 and dt is not torch.bfloat16:
+        raise TypeError("logits must be torch.float32 or torch.bfloat16, got %s" % dt)
     if out is None:
         out = torch.empty(R, dtype=torch.int32, device=dev)
-    _on_device(dev, lib().w4a16_sample, logits.data_ptr(), OUT_F32 if logits.dtype == f32 else OUT_BF16,
-               logits.stride(0) if R > 1 else V, R, V, _ptr(u, "u", f32, dev, R),
-               _ptr(temperature, "temperature", f32, dev, R), _ptr(top_k, "top_k", torch.int32, dev, R),
-               _ptr(top_p, "top_p", f32, dev, R), _ptr(min_p, "min_p", f32, dev, R),
-               _ptr(out, "out", torch.int32, dev, R), _stream(stream, dev))
+    a = _checked(dev, "ffiffi", _SAMPLE_NAMES, u, R, temperature, R, top_k, R, top_p, R, min_p, R, out, R)
+    _launch(dev, stream, lib().w4a16_sample, logits.data_ptr(), OUT_F32 if dt is torch.float32 else OUT_BF16,
+            logits.stride(0) if R > 1 else V, R, V, *a)
     return out
 
 

@@ -1,4 +1,5 @@
-"""In-tree build of the CUDA library libw4a16.so for sm_103a.
+"""In-tree build of the CUDA library libw4a16.so for sm_103a, and of the
+binding's small host extension.
 
 Each translation unit is compiled by nvcc in parallel, then linked into one
 shared library next to this file (``_lib/libw4a16.so``) with the CUDA runtime
@@ -14,6 +15,7 @@ HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
 OUT_DIR = os.path.join(HERE, "_lib")
 LIB = os.path.join(OUT_DIR, "libw4a16.so")
+MARSHAL = os.path.join(OUT_DIR, "_marshal.so")  # the binding's checks of tensors (csrc/marshal.cpp)
 SOURCES = ["api.cu", "dequant.cu", "gemv_int4.cu", "gemv_chain.cu", "moe_fp4.cu", "moe_fp4_gemm.cu",
            "gemm_int4_tc.cu", "gemm_int4_f16.cu", "gemm_bf16_tc.cu", "copy.cu",
            "api_kv4.cu", "kv4_plan.cu", "kv4_rope.cu", "kv4_attention.cu", "kv4_prompt.cu", "sample.cu"]
@@ -28,6 +30,26 @@ def nvcc() -> str:
     return cand if os.path.exists(cand) else (shutil.which("nvcc") or "nvcc")
 
 
+def build_marshal() -> str:
+    """The host extension that checks a call's tensors for the binding."""
+    import sysconfig
+
+    import torch
+    root = os.path.dirname(torch.__file__)
+    inc = [sysconfig.get_paths()["include"], os.path.join(root, "include"),
+           os.path.join(root, "include", "torch", "csrc", "api", "include")]
+    tmp = MARSHAL + ".tmp.%d" % os.getpid()
+    cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-shared",
+           "-D_GLIBCXX_USE_CXX11_ABI=%d" % int(torch._C._GLIBCXX_USE_CXX11_ABI), *["-I" + d for d in inc],
+           os.path.join(CSRC, "marshal.cpp"), "-o", tmp, "-L" + os.path.join(root, "lib"), "-lc10", "-ltorch_cpu",
+           "-ltorch_python"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError("g++ failed for marshal.cpp:\n%s%s" % (r.stdout, r.stderr))
+    os.replace(tmp, MARSHAL)
+    return MARSHAL
+
+
 def _stale(lib: str, deps) -> bool:
     if not os.path.exists(lib):
         return True
@@ -40,7 +62,7 @@ def build(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
     deps = [os.path.join(CSRC, f) for f in os.listdir(CSRC)]
     deps.append(os.path.join(os.path.dirname(HERE), "include", "w4a16.h"))
     deps.append(os.path.abspath(__file__))
-    if not force and not _stale(LIB, deps):
+    if not force and not _stale(LIB, deps) and not _stale(MARSHAL, deps):
         return LIB
     obj_dir = os.path.join(OUT_DIR, "obj")
     os.makedirs(obj_dir, exist_ok=True)
@@ -55,8 +77,10 @@ def build(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
             print(r.stdout + r.stderr)
         return obj
 
-    with cf.ThreadPoolExecutor(max_workers=len(SOURCES)) as ex:
+    with cf.ThreadPoolExecutor(max_workers=len(SOURCES) + 1) as ex:
+        marshal = ex.submit(build_marshal)
         objs = list(ex.map(compile_one, SOURCES))
+        marshal.result()
     tmp = LIB + ".tmp.%d" % os.getpid()
     cmd = [nvcc()] + ARCH + ["-shared", "-cudart", "static", "-o", tmp] + objs
     r = subprocess.run(cmd, capture_output=True, text=True)
