@@ -40,7 +40,7 @@ _LIB_PATH = os.path.join(_HERE, "_lib", "libw4a16.so")
 _MARSHAL_PATH = os.path.join(_HERE, "_lib", "_marshal.so")
 _lock = threading.Lock()
 _lib = None
-_addresses = None  # the extension's check of a call's tensors
+_fast = None  # the host extension: checks a call's tensors and makes it
 
 STATUS = {0: "OK", 1: "INVALID_ARG", 2: "UNSUPPORTED", 3: "MISALIGNED",
           4: "CUDA", 5: "TIMEOUT", 6: "DEVICE"}
@@ -110,7 +110,7 @@ def library_path() -> str:
 
 def lib():
     """The loaded CUDA library (raises if it has not been built)."""
-    global _lib, _addresses
+    global _lib, _fast
     if _lib is not None:
         return _lib
     with _lock:
@@ -127,7 +127,8 @@ def lib():
             spec = importlib.util.spec_from_file_location("_marshal", _MARSHAL_PATH, loader=loader)
             module = importlib.util.module_from_spec(spec)
             loader.exec_module(module)
-            _addresses = module.addresses
+            module.bind(_LIB_PATH)
+            _fast = module
             _lib = handle
         return _lib
 
@@ -517,14 +518,24 @@ def _rows(t, name, device):
 _TYPES = {"b": torch.uint8, "h": torch.bfloat16, "i": torch.int32, "l": torch.int64, "f": torch.float32}
 
 
+# The functions below make their call through the host extension.  Where that
+# finds an argument amiss (it returns None) they go through the same checks
+# here, to say what it is.
+
+def _extension():
+    if _fast is None:
+        lib()
+    return _fast
+
+
+def _handle(stream):
+    """The stream argument of the extension: None or a handle."""
+    return stream if stream is None else stream.cuda_stream if isinstance(stream, torch.cuda.Stream) else int(stream)
+
+
 def _checked(device, spec, names, *tensors):
     """Addresses of a call's tensors, given as tensor, count, tensor, count
-    ...: by the extension, or one by one to say what is wrong."""
-    if device.type == "cuda":
-        lib()
-        got = _addresses(device.index, spec, *tensors)
-        if got is not None:
-            return got
+    ... with a letter of `spec` each (r: rows, else the type)."""
     out = []
     for c, name, t, n in zip(spec, names, tensors[0::2], tensors[1::2]):
         if c == "r":
@@ -576,9 +587,15 @@ def kv4_plan(ctx_lens, new_lens, block_table, free_blocks, block_size: int, num_
         if num_tokens is None:
             raise ValueError("kv4_plan needs num_tokens or out")
         out = kv4_plan_buffers(B, num_tokens, dev)
+    seq, cu, pos, slots, taken = out
+    r = _extension().kv4_plan(ctx_lens, new_lens, block_table, free_blocks, block_size, seq, cu, pos, slots, taken,
+                              _handle(stream))
+    if r == 0:
+        return out
+    if r is not None:
+        _check(r)
     if block_table.dim() != 2 or block_table.shape[0] != B:
         raise ValueError("block_table must be [%d, max_blocks]" % B)
-    seq, cu, pos, slots, taken = out
     T = pos.numel()
     a = _checked(dev, "iiiiiiili", _PLAN_NAMES, ctx_lens, B, new_lens, B, block_table, -1, free_blocks, -1, seq, B, cu,
                  B + 1, pos, T, slots, T, taken, 1)
@@ -616,6 +633,12 @@ def w4a16_qk_norm_rope(q, k, q_weight, k_weight, cos_sin, positions, q_out=None,
         q_out = torch.empty(T, Hq, D, dtype=torch.bfloat16, device=dev)
     if k_out is None:
         k_out = torch.empty(T, Hk, D, dtype=torch.bfloat16, device=dev)
+    r = _extension().w4a16_qk_norm_rope(q, k, q_weight, k_weight, cos_sin, positions, q_out, k_out, float(eps),
+                                        float(weight_offset), interleaved, _handle(stream))
+    if r == 0:
+        return q_out, k_out
+    if r is not None:
+        _check(r)
     a = _checked(dev, "rrhhfihh", _ROPE_NAMES, q, 0, k, 0, q_weight, D, k_weight, D, cos_sin, -1,
                  positions if rot else None, T, q_out, T * Hq * D, k_out, T * Hk * D)
     _launch(dev, stream, lib().w4a16_qk_norm_rope, a[0], a[1], a[2], a[3], a[4], a[5], a[6], rows, rot, a[7], a[8], a[9],
@@ -661,6 +684,12 @@ def kv4_append(k, v, cache, slots, q=None, q_weight=None, k_weight=None, cos_sin
             raise ValueError("q must be [%d, heads, %d]" % (T, D))
         if q_out is None:
             q_out = torch.empty(T, Hq, D, dtype=torch.bfloat16, device=dev)
+    r = _extension().kv4_append(k, v, cache, slots, q, q_weight, k_weight, cos_sin, positions, q_out, float(eps),
+                                float(weight_offset), interleaved, _handle(stream))
+    if r == 0:
+        return q_out if q is not None else None
+    if r is not None:
+        _check(r)
     a = _checked(dev, "rrrhhfilhb", _APPEND_NAMES, q, 0, k, 0, v, 0, q_weight, D, k_weight, D, cos_sin, -1,
                  positions if rot else None, T, slots, T, q_out if q is not None else None, T * Hq * D, cache, -1)
     _launch(dev, stream, lib().kv4_append, a[0], a[1], a[2], a[3], a[4], a[5], a[6], a[7], a[8], rows, rot, a[9], a[10],
@@ -677,6 +706,11 @@ def kv4_gather(cache, slots, k=None, v=None, stream=None):
         k = torch.empty(T, Hkv, D, dtype=torch.bfloat16, device=dev)
     if v is None:
         v = torch.empty(T, Hkv, D, dtype=torch.bfloat16, device=dev)
+    r = _extension().kv4_gather(cache, slots, k, v, _handle(stream))
+    if r == 0:
+        return k, v
+    if r is not None:
+        _check(r)
     n = T * Hkv * D
     a = _checked(dev, "blhh", ("cache", "slots", "k", "v"), cache, -1, slots, T, k, n, v, n)
     _launch(dev, stream, lib().kv4_gather, a[0], blocks, bs, a[1], a[2], a[3], T, Hkv, D)
@@ -705,20 +739,27 @@ def kv4_attention(q, cache, block_table, seq_lens, cu_new, scratch, out=None, sc
     1 / sqrt(D) when None; `scratch` from kv4_attention_scratch.  Returns
     out bfloat16 [T, Hq, D]."""
     dev = cache.device
-    blocks, bs, Hkv, D = _cache_shape(cache)
-    T, Hq, Dq = q.shape
-    if Dq != D:
-        raise ValueError("q has heads of %d, the cache of %d" % (Dq, D))
+    T, Hq, D = q.shape
+    if out is None:
+        out = torch.empty(T, Hq, D, dtype=torch.bfloat16, device=dev)
+    scale = D ** -0.5 if scale is None else float(scale)
+    max_new = max(T, 1) if max_new is None else max_new
+    r = _extension().kv4_attention(q, cache, block_table, seq_lens, cu_new, scratch, out, scale, window, sinks, max_new,
+                                   _handle(stream))
+    if r == 0:
+        return out
+    if r is not None:
+        _check(r)
+    blocks, bs, Hkv, Dc = _cache_shape(cache)
+    if Dc != D:
+        raise ValueError("q has heads of %d, the cache of %d" % (D, Dc))
     B = seq_lens.numel()
     if block_table.dim() != 2 or block_table.shape[0] != B:
         raise ValueError("block_table must be [%d, max_blocks]" % B)
-    if out is None:
-        out = torch.empty(T, Hq, D, dtype=torch.bfloat16, device=dev)
     a = _checked(dev, "rbiiihb", _ATTENTION_NAMES, q, 0, cache, -1, block_table, -1, seq_lens, B, cu_new, B + 1, out,
                  T * Hq * D, scratch, -1)
     _launch(dev, stream, lib().kv4_attention, a[0], a[1], a[2], blocks, bs, a[3], block_table.shape[1], a[4], a[5], B,
-            a[6], T, Hq, Hkv, D, D ** -0.5 if scale is None else scale, window, sinks,
-            max(T, 1) if max_new is None else max_new, a[7], scratch.numel())
+            a[6], T, Hq, Hkv, D, scale, window, sinks, max_new, a[7], scratch.numel())
     return out
 
 
@@ -738,6 +779,11 @@ def w4a16_sample(logits, u, temperature=None, top_k=None, top_p=None, min_p=None
         raise TypeError("logits must be torch.float32 or torch.bfloat16, got %s" % dt)
     if out is None:
         out = torch.empty(R, dtype=torch.int32, device=dev)
+    r = _extension().w4a16_sample(logits, u, temperature, top_k, top_p, min_p, out, _handle(stream))
+    if r == 0:
+        return out
+    if r is not None:
+        _check(r)
     a = _checked(dev, "ffiffi", _SAMPLE_NAMES, u, R, temperature, R, top_k, R, top_p, R, min_p, R, out, R)
     _launch(dev, stream, lib().w4a16_sample, logits.data_ptr(), OUT_F32 if dt is torch.float32 else OUT_BF16,
             logits.stride(0) if R > 1 else V, R, V, *a)

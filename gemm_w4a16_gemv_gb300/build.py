@@ -15,7 +15,7 @@ HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
 OUT_DIR = os.path.join(HERE, "_lib")
 LIB = os.path.join(OUT_DIR, "libw4a16.so")
-MARSHAL = os.path.join(OUT_DIR, "_marshal.so")  # the binding's checks of tensors (csrc/marshal.cpp)
+MARSHAL = os.path.join(OUT_DIR, "_marshal.so")  # the binding's host extension (csrc/marshal.cpp)
 SOURCES = ["api.cu", "dequant.cu", "gemv_int4.cu", "gemv_chain.cu", "moe_fp4.cu", "moe_fp4_gemm.cu",
            "gemm_int4_tc.cu", "gemm_int4_f16.cu", "gemm_bf16_tc.cu", "copy.cu",
            "api_kv4.cu", "kv4_plan.cu", "kv4_rope.cu", "kv4_attention.cu", "kv4_prompt.cu", "sample.cu"]
@@ -31,18 +31,19 @@ def nvcc() -> str:
 
 
 def build_marshal() -> str:
-    """The host extension that checks a call's tensors for the binding."""
+    """The host extension that checks tensors and makes calls for the binding."""
     import sysconfig
 
     import torch
     root = os.path.dirname(torch.__file__)
     inc = [sysconfig.get_paths()["include"], os.path.join(root, "include"),
-           os.path.join(root, "include", "torch", "csrc", "api", "include")]
+           os.path.join(root, "include", "torch", "csrc", "api", "include"), INCLUDE,
+           os.path.join(os.path.dirname(os.path.dirname(nvcc())), "include")]
     tmp = MARSHAL + ".tmp.%d" % os.getpid()
     cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-shared",
            "-D_GLIBCXX_USE_CXX11_ABI=%d" % int(torch._C._GLIBCXX_USE_CXX11_ABI), *["-I" + d for d in inc],
-           os.path.join(CSRC, "marshal.cpp"), "-o", tmp, "-L" + os.path.join(root, "lib"), "-lc10", "-ltorch_cpu",
-           "-ltorch_python"]
+           os.path.join(CSRC, "marshal.cpp"), "-o", tmp, "-L" + os.path.join(root, "lib"), "-lc10", "-lc10_cuda",
+           "-ltorch_cpu", "-ltorch_python", "-ldl"]
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError("g++ failed for marshal.cpp:\n%s%s" % (r.stdout, r.stderr))
