@@ -59,6 +59,10 @@ constexpr int KEYS = 128;
 constexpr int SOFT_THREADS = 128;
 constexpr int FORM_WARPS = 4;         // of K, and as many of V
 constexpr int THREADS = SOFT_THREADS + 2 * FORM_WARPS * 32 + 32;
+// Registers: 128 a thread at launch (13 warps); of each SM quarter's three
+// warps of four-warp groups 144 + 2 x 120 = 3 x 128.  With 128 the softmax
+// spills, and the L1 left beside the operands does not hold what it spills.
+constexpr int SOFT_REGS = 144, FORM_REGS = 120;
 constexpr float NONE = -1e30f;       // reference of a row that has seen no key
 constexpr int METAS = 4;             // buffers of what the softmax needs to know of a key tile: it is at most
                                      // two tiles behind the one whose operands are free to be written, of two
@@ -214,6 +218,19 @@ template <bool PAIR>
 __device__ __forceinline__ void tmem_give(uint32_t taddr) {
     if (!PAIR) tmem_dealloc(taddr, 512);
     else asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(taddr), "r"(512u) : "memory");
+}
+
+// The loads from tensor memory are complete; no use of x moves before this.
+__device__ __forceinline__ void arrived(uint32_t (&x)[32]) {
+    asm volatile("tcgen05.wait::ld.sync.aligned;"
+                 : "+r"(x[0]), "+r"(x[1]), "+r"(x[2]), "+r"(x[3]), "+r"(x[4]), "+r"(x[5]),
+                   "+r"(x[6]), "+r"(x[7]), "+r"(x[8]), "+r"(x[9]), "+r"(x[10]), "+r"(x[11]),
+                   "+r"(x[12]), "+r"(x[13]), "+r"(x[14]), "+r"(x[15]), "+r"(x[16]), "+r"(x[17]),
+                   "+r"(x[18]), "+r"(x[19]), "+r"(x[20]), "+r"(x[21]), "+r"(x[22]), "+r"(x[23]),
+                   "+r"(x[24]), "+r"(x[25]), "+r"(x[26]), "+r"(x[27]), "+r"(x[28]), "+r"(x[29]),
+                   "+r"(x[30]), "+r"(x[31])
+                 :
+                 : "memory");
 }
 
 __device__ __forceinline__ float ex2(float x) {
@@ -446,6 +463,7 @@ __global__ void __launch_bounds__(THREADS, 1) attn_prompt_kernel(const Kv4AttnAr
 
     if (warp < 4) {
         // ------------------------------------------------ softmax, epilogue
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(SOFT_REGS));
         const int r = tid;
         const uint32_t t_row = tmem + (static_cast<uint32_t>(warp * 32) << 16);
         int g = 0;  // key tiles so far, over all items
@@ -466,45 +484,44 @@ __global__ void __launch_bounds__(THREADS, 1) attn_prompt_kernel(const Kv4AttnAr
                 const Meta &meta = reinterpret_cast<const Meta *>(smem + L::meta)[g % METAS];
                 const uint32_t t_s = t_row + COL_S + (g & 1) * KEYS;
                 wait_for(&bar.sfull[g & 1], (g >> 1) & 1, a.status);
-                wait_for(&bar.known[g % METAS], (g / METAS) & 1, a.status);
                 tc_fence_after();
+                uint32_t x0[32], x1[32];
+                tmem_ld_32x32b_x32(t_s, x0);
+                wait_for(&bar.known[g % METAS], (g / METAS) & 1, a.status);
                 if (i == 0) Fr = q_factor[(k_item & 1) * ROWS + r];
                 const uint2 there = *reinterpret_cast<const uint2 *>(meta.there);
                 const bool free = (there.x & there.y) == 0x01010101u && j0 + KEYS <= p_lo + 1 &&
                                   (window == 0 || p_hi - j0 < window || j0 + KEYS <= sinks);
-                // 64 keys at a time: scores in, weights out into the columns of
-                // scores already read (half as wide)
+                // 32 keys at a time: scores in (the next 32 on their way), weights out
+                // into the columns of scores already read (half as wide)
                 float m = M, scaled = 1.f, added = 0.f;
-#pragma unroll 1
-                for (int c = 0; c < 2; ++c) {
-                    uint32_t x[2][32];
-                    tmem_ld_32x32b_x32(t_s + 64 * c, x[0]);
-                    tmem_ld_32x32b_x32(t_s + 64 * c + 32, x[1]);
-                    tmem_ld_wait();
+                auto weigh = [&](uint32_t(&x)[32], int c) {
                     if (!free) {
-                        // keys from .. upto of these 64 are seen, and those before `first`
-                        const int at = j0 + 64 * c;
-                        const int upto = min(p + 1, cur.end) - at, from = window == 0 ? 0 : p - window + 1 - at, first = sinks - at;
-                        const uint32_t pages = c ? there.y : there.x;
+                        // keys from .. upto of these 32 are seen, and those before `first`
+                        const int at = j0 + 32 * c;
+                        auto below = [](int n) -> uint32_t { return n >= 32 ? 0xffffffffu : n > 0 ? (1u << n) - 1 : 0u; };
+                        const uint32_t pages = (c & 2 ? there.y : there.x) >> (16 * (c & 1));
+                        uint32_t see = window == 0 ? 0xffffffffu : ~below(p - window + 1 - at) | below(sinks - at);
+                        see &= below(min(p + 1, cur.end) - at) & ((pages & 1u) * 0xffffu | (pages >> 8 & 1u) * 0xffff0000u);
 #pragma unroll
-                        for (int e = 0; e < 64; ++e) {
-                            const bool see = e < upto && (e >= from || e < first) && (pages >> (8 * (e / 16)) & 1u);
-                            x[e >> 5][e & 31] = see ? x[e >> 5][e & 31] : 0xff800000u;  // -infinity
-                        }
+                        for (int e = 0; e < 32; ++e) x[e] = see >> e & 1u ? x[e] : 0xff800000u;  // -infinity
                     }
-                    float top[4];
+                    float top[2];
 #pragma unroll
-                    for (int q = 0; q < 4; ++q) {
-                        const uint32_t *const y = &x[q >> 1][(q & 1) * 16];
-                        top[q] = fmaxf(__uint_as_float(y[0]), __uint_as_float(y[1]));
+                    for (int q = 0; q < 2; ++q) {
+                        const uint32_t *const y = x + q * 16;
+                        float t[2] = {fmaxf(__uint_as_float(y[0]), __uint_as_float(y[1])),
+                                      fmaxf(__uint_as_float(y[2]), __uint_as_float(y[3]))};
 #pragma unroll
-                        for (int e = 2; e < 16; e += 2) top[q] = max3(top[q], __uint_as_float(y[e]), __uint_as_float(y[e + 1]));
+                        for (int e = 4; e < 16; e += 2)
+                            t[e / 2 & 1] = max3(t[e / 2 & 1], __uint_as_float(y[e]), __uint_as_float(y[e + 1]));
+                        top[q] = fmaxf(t[0], t[1]);
                     }
-                    const float4 kf = *reinterpret_cast<const float4 *>(meta.k_factor + 4 * c);
-                    const float4 B = *reinterpret_cast<const float4 *>(meta.v_exponent + 4 * c);
-                    const float A[4] = {factor(Fr, kf.x), factor(Fr, kf.y), factor(Fr, kf.z), factor(Fr, kf.w)};
-                    const float mx = max3(fmaxf(fmaf(top[0], A[0], B.x), fmaf(top[1], A[1], B.y)), fmaf(top[2], A[2], B.z),
-                                          fmaf(top[3], A[3], B.w));
+                    const float2 kf = *reinterpret_cast<const float2 *>(meta.k_factor + 2 * c);
+                    const float2 B = *reinterpret_cast<const float2 *>(meta.v_exponent + 2 * c);
+                    const float2 vf = *reinterpret_cast<const float2 *>(meta.v_factor + 2 * c);
+                    const float A[2] = {factor(Fr, kf.x), factor(Fr, kf.y)};
+                    const float mx = fmaxf(fmaf(top[0], A[0], B.x), fmaf(top[1], A[1], B.y));
                     if (__any_sync(0xffffffffu, mx > m + 8.f)) {
                         // the reference moves: what this tile has written so far, its
                         // sum, and (below) what earlier tiles left shrink with it
@@ -516,7 +533,7 @@ __global__ void __launch_bounds__(THREADS, 1) attn_prompt_kernel(const Kv4AttnAr
                             const uint32_t f2 = pack_f16(f, f);
                             tmem_st_wait();
 #pragma unroll 1
-                            for (int q = 0; q < 2; ++q) {
+                            for (int q = 0; q < c; ++q) {
                                 uint32_t w[16];
                                 tmem_ld_32x32b_x16(t_s + 16 * q, w);
                                 tmem_ld_wait();
@@ -526,13 +543,12 @@ __global__ void __launch_bounds__(THREADS, 1) attn_prompt_kernel(const Kv4AttnAr
                             }
                         }
                     }
-                    const float4 vf = *reinterpret_cast<const float4 *>(meta.v_factor + 4 * c);
-                    const float Bm[4] = {B.x - m, B.y - m, B.z - m, B.w - m}, of[4] = {vf.x, vf.y, vf.z, vf.w};
+                    const float Bm[2] = {B.x - m, B.y - m}, of[2] = {vf.x, vf.y};
+                    uint32_t w[16];
 #pragma unroll
-                    for (int q = 0; q < 4; ++q) {
-                        uint32_t w[8];
+                    for (int q = 0; q < 2; ++q) {
                         float2 sum[2];
-                        const uint32_t *const y = &x[q >> 1][(q & 1) * 16];
+                        const uint32_t *const y = x + q * 16;
 #pragma unroll
                         for (int e = 0; e < 16; e += 2) {
                             float2 v = fma2(make_float2(__uint_as_float(y[e]), __uint_as_float(y[e + 1])),
@@ -541,12 +557,21 @@ __global__ void __launch_bounds__(THREADS, 1) attn_prompt_kernel(const Kv4AttnAr
                             v.y = ex2(v.y);
                             if (e < 4) sum[e / 2] = v;
                             else sum[(e / 2) & 1] = add2(sum[(e / 2) & 1], v);
-                            w[e / 2] = pack_f16(v.x, v.y);
+                            w[8 * q + e / 2] = pack_f16(v.x, v.y);
                         }
                         sum[0] = add2(sum[0], sum[1]);
                         added = fmaf(sum[0].x + sum[0].y, of[q], added);
-                        tmem_st_32x32b_x8(t_s + 32 * c + 8 * q, w);
                     }
+                    tmem_st_32x32b_x16(t_s + 16 * c, w);
+                };
+#pragma unroll 1
+                for (int c = 0; c < 4; c += 2) {
+                    arrived(x0);
+                    tmem_ld_32x32b_x32(t_s + 32 * c + 32, x1);
+                    weigh(x0, c);
+                    arrived(x1);
+                    if (c == 0) tmem_ld_32x32b_x32(t_s + 64, x0);
+                    weigh(x1, c + 1);
                 }
                 if (__any_sync(0xffffffffu, m != M)) {
                     l *= scaled;
@@ -598,6 +623,7 @@ __global__ void __launch_bounds__(THREADS, 1) attn_prompt_kernel(const Kv4AttnAr
         }
     } else if (warp < 4 + 2 * FORM_WARPS) {
         // ------------------------------------------- operands from the cache
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(FORM_REGS));
         // Q of an item: 16 rows a warp, D / 8 lanes a row with 16 bytes each, and
         // the factors of their scores.
         auto build = [&](const Item &it, int k_item) {
@@ -682,38 +708,42 @@ __global__ void __launch_bounds__(THREADS, 1) attn_prompt_kernel(const Kv4AttnAr
                 const int at = (it.key0(i) >> 4) + c;
                 return ((static_cast<unsigned>(id) * a.Hkv + it.h) << shift) + (at & in_page);
             };
-            uint4 raw[2][HALF];
-            uint32_t par[2][HALF];  // (scale, zero) of this lane's token
-            uint2 all[2];           // of tokens 2 (lane % 8) and one more in group lane / 8, of both cache tiles
-            int n0 = 0, n1 = 0;     // tokens there are
-            auto load = [&](int i, int id) {
+            struct Tile {
+                uint4 raw[2][HALF];
+                uint32_t par[2][HALF];  // (scale, zero) of this lane's token
+                uint2 all[2];           // of tokens 2 (lane % 8) and one more in group lane / 8, of both cache tiles
+                int n0, n1;             // tokens there are
+            };
+            auto load = [&](int i, int id) -> Tile {
+                Tile t;
                 int n = tokens(i);
                 if (n > 0 && (id < 0 || id >= a.num_blocks)) {
                     bad = true;
                     n = 0;
                 }
                 const unsigned mine = number(i, id);
-                n0 = __shfl_sync(0xffffffffu, n, 0);
-                n1 = __shfl_sync(0xffffffffu, n, 1);
+                t.n0 = __shfl_sync(0xffffffffu, n, 0);
+                t.n1 = __shfl_sync(0xffffffffu, n, 1);
                 const size_t o0 = static_cast<size_t>(__shfl_sync(0xffffffffu, mine, 0)) * kv4_tile_bytes(D);
                 const size_t o1 = static_cast<size_t>(__shfl_sync(0xffffffffu, mine, 1)) * kv4_tile_bytes(D);
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
                     const size_t o = h && !shared ? o1 : o0;
-                    const int n_form = h && !shared ? n1 : n0, grp = h ? g1 : g0;
+                    const int n = h && !shared ? t.n1 : t.n0, grp = h ? g1 : g0;
 #pragma unroll
                     for (int q = 0; q < HALF; ++q) {
-                        raw[h][q] = make_uint4(0, 0, 0, 0);
-                        par[h][q] = 0;
-                        if (token < n_form) {
-                            raw[h][q] = *reinterpret_cast<const uint4 *>(codes + o + (grp + q) * 512);
-                            par[h][q] = *reinterpret_cast<const uint32_t *>(params + o + ((grp + q) * 16 + token) * 4);
+                        t.raw[h][q] = make_uint4(0, 0, 0, 0);
+                        t.par[h][q] = 0;
+                        if (token < n) {
+                            t.raw[h][q] = *reinterpret_cast<const uint4 *>(codes + o + (grp + q) * 512);
+                            t.par[h][q] = *reinterpret_cast<const uint32_t *>(params + o + ((grp + q) * 16 + token) * 4);
                         }
                     }
-                    all[h] = make_uint2(0, 0);
-                    if (2 * (lane & 7) < (h ? n1 : n0) && lane < 8 * G64)
-                        all[h] = *reinterpret_cast<const uint2 *>(params + (h ? o1 : o0) + lane * 8);
+                    t.all[h] = make_uint2(0, 0);
+                    if (2 * (lane & 7) < (h ? t.n1 : t.n0) && lane < 8 * G64)
+                        t.all[h] = *reinterpret_cast<const uint2 *>(params + (h ? o1 : o0) + lane * 8);
                 }
+                return t;
             };
             // e such that every scale of a cache tile < 2^(e + 11)
             auto exponent = [&](uint2 x, int n) -> int {
@@ -721,7 +751,7 @@ __global__ void __launch_bounds__(THREADS, 1) attn_prompt_kernel(const Kv4AttnAr
                 const unsigned bits = __reduce_max_sync(0xffffffffu, max(x.x & 0x7fffu, second));
                 return bits ? static_cast<int>(__float_as_uint(f16_lo(bits)) >> 23) - 137 : -11;
             };
-            load(0, page_of(0));
+            Tile tile = load(0, page_of(0));
             int id = page_of(1);
             // (Q's place is free when the last product Q K of the item before is done)
             if (g > 0) wait_for(&bar.kfree[(g - 1) % BUFS], ((g - 1) / BUFS) & 1, a.status);
@@ -729,8 +759,9 @@ __global__ void __launch_bounds__(THREADS, 1) attn_prompt_kernel(const Kv4AttnAr
 #pragma unroll 1
             for (int i = 0; i < it.n; ++i) {
                 const int gi = g + i, buf = gi % BUFS, id2 = page_of(i + 2);
+                const Tile next = load(i + 1, id);  // on its way while this one is formed
                 Meta &meta = reinterpret_cast<Meta *>(smem + L::meta)[gi % METAS];
-                const int e0 = exponent(all[0], n0), e1 = exponent(all[1], n1);
+                const int e0 = exponent(tile.all[0], tile.n0), e1 = exponent(tile.all[1], tile.n1);
                 if (is_v) {
                     // (that the operands of the tile before could be written shows that
                     // the softmax is past the tile that had this entry)
@@ -738,7 +769,7 @@ __global__ void __launch_bounds__(THREADS, 1) attn_prompt_kernel(const Kv4AttnAr
                         const int e = lane ? e1 : e0;
                         meta.v_exponent[c] = static_cast<float>(e);
                         meta.v_factor[c] = pow2(-e);
-                        meta.there[c] = (lane ? n1 : n0) > 0;
+                        meta.there[c] = (lane ? tile.n1 : tile.n0) > 0;
                     }
                 }
                 if (!is_v) {
@@ -754,14 +785,14 @@ __global__ void __launch_bounds__(THREADS, 1) attn_prompt_kernel(const Kv4AttnAr
                     const float up = pow2(-(h && !shared ? e1 : e0));
 #pragma unroll
                     for (int q = 0; q < HALF; ++q) {
-                        const float s = f16_lo(par[h][q]) * up, z = f16_hi(par[h][q]);
-                        form(raw[h][q], pack_f16(s, s), pack_f16(-1024.f - z, -1024.f - z), pack_f16(-64.f - z, -64.f - z),
+                        const float s = f16_lo(tile.par[h][q]) * up, z = f16_hi(tile.par[h][q]);
+                        form(tile.raw[h][q], pack_f16(s, s), pack_f16(-1024.f - z, -1024.f - z), pack_f16(-64.f - z, -64.f - z),
                              dst + buf * next_buf + h * part + q * step, x7, half);
                     }
                 }
                 fence_proxy_async_smem();
                 warp_arrive<PAIR>(&full[buf], lane);
-                load(i + 1, id);
+                tile = next;
                 id = id2;
             }
             g += it.n;
