@@ -10,14 +10,20 @@
 //
 // Bound.  At D = 256 the two products take 2 x 1024 cycles of an SM's tensor
 // pipe per 128 x 128 tile.  One CTA alone also has to form 2 x 32768 codes as
-// binary16 operands (14 instructions per 8 codes and lane, 1300 cycles of
-// issue slots), store them (128 KB at 128 bytes a cycle) and feed the products
-// from shared memory (192 KB): 2500 cycles of its bandwidth, and the stages
-// wait for one another.  So for D = 128 and 256 two CTAs work as a pair
-// (cta_group::2): each keeps its own 128 rows of Q, S, P and O, but only half
-// of K (64 of the 128 keys) and half of V (D / 2 of the dimensions), which
-// halves the forming and the stores per SM, and leaves room for two buffers of
-// each operand.  One CTA of the pair issues the products of both.
+// binary16 operands (14 instructions per 8 codes and lane), store them (128 KB
+// at 128 bytes a cycle) and feed the products from shared memory (192 KB):
+// 2500 cycles of its bandwidth, and the stages wait for one another.  So for
+// D = 128 and 256 two CTAs work as a pair (cta_group::2): each keeps its own
+// 128 rows of Q, S, P and O, but only half of K (64 of the 128 keys) and half
+// of V (D / 2 of the dimensions), which halves the forming and the stores per
+// SM, and leaves room for two buffers of each operand.  One CTA of the pair
+// issues the products of both.  Measured on 6491 new tokens in three requests
+// with up to 6000 tokens before them, 16 heads of 256 on 8: single CTAs 455 us,
+// pairs 297 us, 1130 TFLOP/s.  What bounds it now is the softmax: 2700 cycles a
+// tile (4 x 32 keys, each 170 until the scores are there, 190 for the
+// reference, 250 for the weights), of which the exponentials are 512 per SM
+// quarter; the code is kept short (rolled loops, masks as 32-bit words),
+// because its three roles share the instruction cache (341 -> 298 us).
 // (D = 64 stays with single CTAs: half of its 64 dimensions is no whole
 // swizzled row.)
 //
@@ -119,8 +125,8 @@ __device__ __forceinline__ void arrive_at(uint32_t bar) {
 // that it wrote: the tensor core of its own CTA reads them, and the fence of the
 // proxies (or of tensor memory) before this call orders them there.  So the
 // arrival releases nothing to the other CTA's threads, and must not: a release
-// of the cluster's scope waits for the warp's loads in flight (521 us instead
-// of ... for the whole kernel).
+// of the cluster's scope waits for the warp's loads in flight (the whole kernel
+// took 521 us with it and 410 without, at that step).
 template <bool PAIR>
 __device__ __forceinline__ void warp_arrive(uint64_t *bar, int lane) {
     __syncwarp();
@@ -485,15 +491,14 @@ __global__ void __launch_bounds__(THREADS, 1) attn_prompt_kernel(const Kv4AttnAr
                 const uint32_t t_s = t_row + COL_S + (g & 1) * KEYS;
                 wait_for(&bar.sfull[g & 1], (g >> 1) & 1, a.status);
                 tc_fence_after();
-                uint32_t x0[32], x1[32];
+                uint32_t x0[32];
                 tmem_ld_32x32b_x32(t_s, x0);
                 wait_for(&bar.known[g % METAS], (g / METAS) & 1, a.status);
                 if (i == 0) Fr = q_factor[(k_item & 1) * ROWS + r];
                 const uint2 there = *reinterpret_cast<const uint2 *>(meta.there);
                 const bool free = (there.x & there.y) == 0x01010101u && j0 + KEYS <= p_lo + 1 &&
                                   (window == 0 || p_hi - j0 < window || j0 + KEYS <= sinks);
-                // 32 keys at a time: scores in (the next 32 on their way), weights out
-                // into the columns of scores already read (half as wide)
+                // 32 keys at a time: scores in, weights out into the columns of scores already read (half as wide)
                 float m = M, scaled = 1.f, added = 0.f;
                 auto weigh = [&](uint32_t(&x)[32], int c) {
                     if (!free) {
@@ -565,13 +570,10 @@ __global__ void __launch_bounds__(THREADS, 1) attn_prompt_kernel(const Kv4AttnAr
                     tmem_st_32x32b_x16(t_s + 16 * c, w);
                 };
 #pragma unroll 1
-                for (int c = 0; c < 4; c += 2) {
+                for (int c = 0; c < 4; ++c) {
+                    if (c > 0) tmem_ld_32x32b_x32(t_s + 32 * c, x0);
                     arrived(x0);
-                    tmem_ld_32x32b_x32(t_s + 32 * c + 32, x1);
                     weigh(x0, c);
-                    arrived(x1);
-                    if (c == 0) tmem_ld_32x32b_x32(t_s + 64, x0);
-                    weigh(x1, c + 1);
                 }
                 if (__any_sync(0xffffffffu, m != M)) {
                     l *= scaled;
