@@ -171,11 +171,11 @@ struct Kv4AttnArgs {
     int64_t q_stride, num_blocks, max_blocks, T, window, sinks, max_new;
     int requests, Hq, Hkv, bs_log2;
     float scale;
-    // set by launch_kv4_attention: the streaming kernel takes requests of at
-    // most rows_most rows (new tokens x query heads per key head), the prompt
-    // kernel those of more than rows_above; one of the two zeroes the rows of
-    // no request
-    int rows_most, rows_above, zero_rest;
+    // set by launch_kv4_attention: the streaming kernel takes requests of
+    // rows_least to rows_most rows (new tokens x query heads per key head), the
+    // prompt kernel those of more than rows_above; the first launch of a call
+    // zeroes the rows of no request
+    int rows_least, rows_most, rows_above, zero_rest;
 };
 constexpr int PROMPT_COUNTERS = 13056;  // byte offset in the scratch of the prompt kernel's two counters
 cudaError_t launch_kv4_prompt(const Kv4AttnArgs &a, int D, cudaStream_t st, const DeviceInfo &dev);

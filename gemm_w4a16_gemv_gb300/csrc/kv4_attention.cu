@@ -41,9 +41,10 @@
 // and P' are zero outside their group, one set of accumulators serves all
 // groups (16 registers instead of 64 at D = 256), and each lane handles the
 // parameters of one group instead of all.
-// The reference of the exponentials is a running maximum of x + log2(s), so
-// that the largest P' is near 1 whatever the magnitude of V; it moves (and
-// the accumulators are scaled) only when it would grow by more than 2^8.
+// The reference of the exponentials follows the running maximum of x + log2(s),
+// so that the largest P' lies in [2^7, 2^15] whatever the magnitude of V (binary16
+// then keeps 11 bits of weights down to 2^-21 of it); it moves (and the
+// accumulators are scaled) only when P' would pass 2^15.
 #include "common.cuh"
 #include "kernels.h"
 #include "kv4.cuh"
@@ -58,8 +59,7 @@ constexpr int COUNTER_BYTES = 13312;  // arrival counters and the prompt kernel'
 static_assert(MAX_TEAMS * 4 <= PROMPT_COUNTERS && PROMPT_COUNTERS + 8 <= COUNTER_BYTES, "counters");
 // Partial results that two slots per team can need: warps x rows of an instance.
 constexpr int warp_rows(int D) { return D == 256 ? 128 : D == 128 ? 192 : 256; }
-constexpr int TEAM_RATIO = 8;         // warps to a segment up to which a warp is a team of its own
-constexpr int PROMPT_ROWS = 48;       // requests with more rows go to the tensor cores
+constexpr int TEAM_RATIO = 5;         // warps to a segment up to which a warp is a team of its own
 constexpr float NONE = -1e30f;        // reference of a row that has seen no key
 
 __device__ __forceinline__ float ex2(float x) {
@@ -121,7 +121,7 @@ __device__ __forceinline__ int rows_before(const Kv4AttnArgs &a, int b) {
 // key head, or none when the prompt kernel takes them.
 __device__ __forceinline__ int rows_of(const Kv4AttnArgs &a, int b, int G) {
     const int rows = (rows_before(a, b + 1) - rows_before(a, b)) * G;
-    return rows > 0 && rows <= a.rows_most ? rows : 0;
+    return rows >= a.rows_least && rows <= a.rows_most ? rows : 0;
 }
 
 // A segment: the rows [r0, r0 + rows) of (request b, key head h) and the cache
@@ -568,7 +568,7 @@ __global__ void __launch_bounds__(W * 32, 1) attn_stream_kernel(const Kv4AttnArg
                     }
 #pragma unroll
                     for (int e = 0; e < 2; ++e)
-                        grow |= fmaxf(x[n][e] + l0, x[n][e + 2] + l1) > M[n][e] + 8.f;
+                        grow |= fmaxf(x[n][e] + l0, x[n][e + 2] + l1) > M[n][e] + 15.f;
                 }
                 if (__any_sync(0xffffffffu, grow)) {
 #pragma unroll
@@ -583,7 +583,7 @@ __global__ void __launch_bounds__(W * 32, 1) attn_stream_kernel(const Kv4AttnArg
                                 m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 2));
                                 if (G64 == 4) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 1));
                             }
-                            m = fmaxf(m, M[n][e]);
+                            m = fmaxf(m - 7.f, M[n][e]);
                             const float f = ex2(M[n][e] - m);
                             M[n][e] = m;
                             Ls[n][e] *= f;
@@ -900,13 +900,54 @@ cudaError_t launch_stream(const Kv4AttnArgs &a, cudaStream_t st, const DeviceInf
 }
 
 // One warp to a team when there are segments enough for that (rows is the
-// most a request has).
+// most a request has).  Warps alone against a CTA's warps together, one new
+// token after 4000, 16 heads of 256 on 8 (32 of 128 on 8):
+//     requests   1         16       32       48        64       128
+//     alone     144 (149)  55 (50)  78 (64)  101 (79)  124 (95) 219 (159) us
+//     together   13 (13)   44 (35)  72 (56)  100 (75)  127 (95) 235 (171) us
 template <int D, int NT, int W, bool SPLIT>
 cudaError_t launch_teams(const Kv4AttnArgs &a, int64_t rows, cudaStream_t st, const DeviceInfo &dev) {
     constexpr int R = Stream<D, NT, W, 1, SPLIT>::R;
     const int64_t segments = a.requests * a.Hkv * ((rows + R - 1) / R);
     if (segments * TEAM_RATIO >= static_cast<int64_t>(dev.num_sms) * W) return launch_stream<D, NT, W, 1, SPLIT>(a, st, dev);
     return launch_stream<D, NT, W, W, SPLIT>(a, st, dev);
+}
+
+// Groups as columns (SPLIT) where the rows leave room for them, two blocks of
+// columns where one is too few.  64 requests, one token after 4000, 8 key
+// heads; us with SPLIT, one block, two blocks (- : not possible):
+//     D = 256   1 row  119 140 197   2 rows 124 143 201   4 - 151 208   8 - 167 222
+//     D = 128   1 row   86  89 116   2 rows  89  92 117   4 95 98 122   8 - 111 131
+//     D = 64                                              4 - 70  83    8 -  77  90
+cudaError_t stream(const Kv4AttnArgs &a, int D, int64_t rows, cudaStream_t st, const DeviceInfo &dev) {
+    if (D == 64) return rows <= 8 ? launch_teams<64, 1, 16, false>(a, rows, st, dev) : launch_teams<64, 2, 16, false>(a, rows, st, dev);
+    if (D == 128)
+        return rows <= 4   ? launch_teams<128, 1, 16, true>(a, rows, st, dev)
+               : rows <= 8 ? launch_teams<128, 1, 16, false>(a, rows, st, dev)
+                           : launch_teams<128, 2, 12, false>(a, rows, st, dev);
+    return rows <= 2   ? launch_teams<256, 1, 16, true>(a, rows, st, dev)
+           : rows <= 8 ? launch_teams<256, 1, 12, false>(a, rows, st, dev)
+                       : launch_teams<256, 2, 8, false>(a, rows, st, dev);
+}
+
+// Requests of up to this many rows are streamed.  A streamed block of 16 rows
+// costs its share of the GPU, an item of the prompt kernel (up to 256 rows, 128
+// at D = 64) a whole worker, and a round of items as long as one of them; in
+// units of a round, per key, a streamed block of one segment costs 1 / (ratio x
+// workers) with the measured ratio below.  So few segments stream more rows:
+//     8 segments, 8000 keys, rows     16   32   64  128     (us: streamed / prompt)
+//       D = 256                       33   41   51   70  / 113 for all
+//     128 segments, 4000 keys         16   24   32   64
+//       D = 256                       74  184  185  249  / 135
+//       D = 128                       49    -   97  147  / 108
+//     512 segments, 1000 keys         16   24   32   48   64
+//       D = 256                      118  163  163  214  260  / 143
+//       D = 128                       75    -   96  122  147  / 114
+//       D = 64                        57   65   66   83   99  / 58
+int64_t stream_rows(int64_t segments, int D, const DeviceInfo &dev) {
+    const int64_t workers = D == 64 ? dev.num_sms : dev.num_sms / 2, rounds = (segments + workers - 1) / workers;
+    const int64_t blocks = (D == 128 ? 8 : 5) * workers * rounds / (4 * segments);
+    return 16 * (blocks > 1 ? blocks : 1);
 }
 
 }  // namespace
@@ -919,26 +960,27 @@ cudaError_t launch_kv4_attention(const Kv4AttnArgs &args, int D, cudaStream_t st
     Kv4AttnArgs a = args;
     const int G = a.Hq / a.Hkv;
     int64_t rows = a.max_new * G;  // the most a request has
+    const int64_t few = stream_rows(a.requests * a.Hkv, D, dev);
+    a.rows_least = 1;
     a.rows_most = 0x7fffffff;
     a.zero_rest = 1;
-    if (rows > PROMPT_ROWS) {
-        // requests of many rows to the tensor cores, the others of a mixed step
-        // to the streaming kernel
-        a.rows_above = a.requests > 1 ? PROMPT_ROWS : 0;
+    if (rows > few) {
+        // requests of many rows to the tensor cores; the others of a mixed step to
+        // the streaming kernel, those of a token or so (most, as a rule) by the
+        // form for them: 64 requests, one of them a prompt, would take 201 us
+        // instead of 124 in the form for 16 rows
+        a.rows_above = a.requests > 1 ? static_cast<int>(few) : 0;
         if (cudaError_t e = launch_kv4_prompt(a, D, st, dev)) return e;
         if (a.requests == 1) return cudaSuccess;
-        a.rows_most = PROMPT_ROWS;
         a.zero_rest = 0;
-        rows = PROMPT_ROWS;
+        a.rows_most = D == 256 ? 2 : D == 128 ? 4 : 8;
+        if (G <= a.rows_most)
+            if (cudaError_t e = stream(a, D, a.rows_most, st, dev)) return e;
+        a.rows_least = a.rows_most + 1;
+        a.rows_most = static_cast<int>(few);
+        rows = few;
     }
-    if (D == 64) return rows <= 8 ? launch_teams<64, 1, 16, false>(a, rows, st, dev) : launch_teams<64, 2, 16, false>(a, rows, st, dev);
-    if (D == 128)
-        return rows <= 4   ? launch_teams<128, 1, 16, true>(a, rows, st, dev)
-               : rows <= 8 ? launch_teams<128, 1, 16, false>(a, rows, st, dev)
-                           : launch_teams<128, 2, 12, false>(a, rows, st, dev);
-    return rows <= 2   ? launch_teams<256, 1, 16, true>(a, rows, st, dev)
-           : rows <= 8 ? launch_teams<256, 1, 12, false>(a, rows, st, dev)
-                       : launch_teams<256, 2, 8, false>(a, rows, st, dev);
+    return stream(a, D, rows, st, dev);
 }
 
 }  // namespace w4

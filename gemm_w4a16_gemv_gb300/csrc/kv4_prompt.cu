@@ -33,14 +33,14 @@
 //
 // Roles: warps 0-3 softmax and epilogue (warp w owns the tensor memory lanes
 // 32 w ..), warps 4-7 form K and 8-11 V (16-byte loads of the codes one step
-// ahead in registers) and together Q of the next item, warp 12 issues the products in the
-// order Q K(i+1), P(i) V(i), so that the operands of one are formed while the
-// other runs.
+// ahead in registers) and together Q of the next item, warp 12 issues the
+// products in the order Q K(i+1), P(i) V(i), so that the operands of one are
+// formed while the other runs.
 //
 // Operands.  (code - zero) is exact in binary16; times the scale it is rounded
-// once.  The scales of a tile are multiplied by a power of two that brings the
-// largest to [2^10, 2^11), so that scales 2^25 apart keep all their bits; the
-// power of K's goes into the factor of the scores, that of V's into the
+// once.  The scales of a cache tile are multiplied by a power of two that brings
+// the largest to [2^10, 2^11), so that scales 2^25 apart keep all their bits; the
+// power of K's goes into the factor of its 16 scores, that of V's into the
 // exponent: P = exp2(x + e - M), and the sum of weights takes P 2^-e.  A row
 // of Q enters after a power-of-two scale of its own.  K and V lie in shared
 // memory as they come from the cache, a row of 64 dimensions per token and
@@ -48,8 +48,9 @@
 // (dimensions contiguous) for the second.  A word's codes leave in the order
 // 0 4 1 5 2 6 3 7; Q is stored in the same order and the epilogue undoes it.
 //
-// The running reference M of a row moves only when it would grow by more than
-// 2^8; then the softmax warps scale O in tensor memory themselves, between
+// The running reference M of a row puts its largest P into [2^6, 2^15] (binary16
+// then keeps 11 bits of weights down to 2^-20 of it) and moves only when P would
+// pass 2^15; then the softmax warps scale O in tensor memory themselves, between
 // two products.  Every wait is bounded; on a timeout the roles still go
 // through all their arrivals.
 #include "common.cuh"
@@ -527,10 +528,10 @@ __global__ void __launch_bounds__(THREADS, 1) attn_prompt_kernel(const Kv4AttnAr
                     const float2 vf = *reinterpret_cast<const float2 *>(meta.v_factor + 2 * c);
                     const float A[2] = {factor(Fr, kf.x), factor(Fr, kf.y)};
                     const float mx = fmaxf(fmaf(top[0], A[0], B.x), fmaf(top[1], A[1], B.y));
-                    if (__any_sync(0xffffffffu, mx > m + 8.f)) {
+                    if (__any_sync(0xffffffffu, mx > m + 15.f)) {
                         // the reference moves: what this tile has written so far, its
                         // sum, and (below) what earlier tiles left shrink with it
-                        const float up = fmaxf(m, ceilf(mx)), f = ex2(m - up);  // whole numbers: f is a power of two
+                        const float up = fmaxf(m, ceilf(mx) - 7.f), f = ex2(m - up);  // whole numbers: f is a power of two
                         m = up;
                         added *= f;
                         scaled *= f;

@@ -860,8 +860,13 @@ cudaError_t launch_typed(const SampleArgs &a, cudaStream_t st, const DeviceInfo 
         while (cs * ept * THREADS < a.vocab) cs *= 2;
         return cs;
     };
-    // few rows of a small vocabulary: spread thinner over more SMs
-    if (cluster(16) <= 8 && a.rows * cluster(16) <= dev.num_sms) return launch_rows<BF16, 16>(a, cluster(16), st, dev);
+    // A vocabulary that 8 CTAs hold at 16 logits a thread is spread thinner over
+    // more SMs, unless rows alone are enough.  16 against 64, us, BF16:
+    //     rows              1        16        64       128       256
+    //     4096 logits    9.7/14.3  13/24     17/29     18/32     22/40
+    //     32000         10.1/12.4  20/37     23/39     33/46     51/52
+    //     65536         10.5/12.1  23/37     35/45     55/52     98/67
+    if (cluster(16) <= 8 && a.rows * cluster(16) <= 6 * dev.num_sms) return launch_rows<BF16, 16>(a, cluster(16), st, dev);
     return launch_rows<BF16, 64>(a, cluster(64), st, dev);
 }
 

@@ -491,8 +491,11 @@ int kv4_gather(const uint8_t *cache, int64_t num_blocks, int block_size,
  *         aligned, ALL ZERO before its first use; every call leaves it fit
  *         for the next one.  Calls that may run at the same time need
  *         separate scratch.
- * K, V and the softmax's statistics and sums are binary32 or exact; the
- * weights of the sum over V are rounded to binary16.
+ * Queries, statistics and sums are exact or binary32.  The streaming kernel
+ * takes K and V as they are in the cache, the one for long pieces rounds each
+ * of their values once to binary16 (2^-12 of it at most).  The weights of the
+ * sum over V, times the scales of V, are rounded to binary16: to 2^-11, or to
+ * 2^-31 of the row's largest such product where that is more.
  * Hq is a multiple of Hkv; requests <= 4096; T = 0 launches nothing.
  */
 int64_t kv4_attention_scratch_bytes(int Hq, int Hkv, int D);
