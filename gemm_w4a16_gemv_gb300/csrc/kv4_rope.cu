@@ -104,8 +104,11 @@ __device__ __forceinline__ void quantise_store(const float (&x)[8], unsigned cha
 }
 
 // A task is U x 32 / LPH heads of one token, in the order q heads, k heads, v
-// heads; `tasks` of them per token.
-template <int D, int U>
+// heads; `tasks` of them per token.  TURN: with a norm or a rotation; KEEP:
+// with a cache (instances of their own need fewer registers, 4099 tokens of 40
+// heads of 128 TURN_US us and 8191 tokens of 8 heads of 256 KEEP_US us with
+// the read-back, where one for all took 24.9 and 59.2).
+template <int D, int U, bool TURN, bool KEEP>
 __global__ void __launch_bounds__(ROPE_THREADS, 4) rope_kernel(const Kv4RopeArgs a, const unsigned tasks) {
     constexpr int LPH = D / 8;   // lanes per head
     constexpr int HPS = 32 / LPH;
@@ -132,11 +135,11 @@ __global__ void __launch_bounds__(ROPE_THREADS, 4) rope_kernel(const Kv4RopeArgs
             raw[k] = *reinterpret_cast<const uint4 *>(src + 8 * l);
         }
         int64_t slot = -1;
-        if (a.cache) slot = a.slots[t];
+        if (KEEP) slot = a.slots[t];
         bool skip = false;  // a row whose position names none: written as zeros
         float cc[8], sn[8];
         const bool low = l < hl;
-        if (a.cos_sin) {
+        if (TURN && a.cos_sin) {
             const int pos = a.positions[t];
             skip = pos < 0 || pos >= a.num_positions;
             bad |= pos >= a.num_positions;
@@ -158,11 +161,14 @@ __global__ void __launch_bounds__(ROPE_THREADS, 4) rope_kernel(const Kv4RopeArgs
             const bool live = h0 + k * HPS < heads;
             const int h = min(h0 + k * HPS, heads - 1);
             const bool is_q = h < a.Hq, is_v = h >= a.Hq + a.Hk;
+            // of the whole warp: no head to rotate, or none to quantise
+            const int warp_h = h0 - lane / LPH + k * HPS;
+            const bool all_v = warp_h >= a.Hq + a.Hk, all_q = warp_h + HPS <= a.Hq;
             uint4 packed = raw[k];
             float x[8];
             unpack8(packed, x);
             const uint16_t *w = is_q ? a.q_weight : is_v ? nullptr : a.k_weight;
-            if (a.q_weight || a.k_weight) {
+            if (TURN && (a.q_weight || a.k_weight) && !all_v) {
                 float ss = 0.f;
 #pragma unroll
                 for (int i = 0; i < 8; ++i) ss = fmaf(x[i], x[i], ss);
@@ -176,7 +182,7 @@ __global__ void __launch_bounds__(ROPE_THREADS, 4) rope_kernel(const Kv4RopeArgs
                     for (int i = 0; i < 8; ++i) x[i] = x[i] * r * (wv[i] + a.weight_offset);
                 }
             }
-            if (a.cos_sin) {
+            if (TURN && a.cos_sin && !all_v) {
                 if (a.interleaved) {
                     if (!is_v && l < 2 * hl) {
 #pragma unroll
@@ -197,20 +203,20 @@ __global__ void __launch_bounds__(ROPE_THREADS, 4) rope_kernel(const Kv4RopeArgs
                     }
                 }
             }
-            if (!is_v) packed = skip ? make_uint4(0, 0, 0, 0) : pack8(x);
+            if (TURN && !is_v) packed = skip ? make_uint4(0, 0, 0, 0) : pack8(x);
             if (is_q) {
                 if (live)
                     *reinterpret_cast<uint4 *>(a.q_out + (static_cast<size_t>(t) * a.Hq + h) * D + 8 * l) = packed;
-            } else if (!a.cache) {
+            } else if (!KEEP) {
                 if (live)
                     *reinterpret_cast<uint4 *>(a.k_out + (static_cast<size_t>(t) * a.Hk + (h - a.Hq)) * D + 8 * l) = packed;
             }
-            if (a.cache) {
+            if (KEEP && !all_q) {
                 unpack8(packed, x);
                 const bool in = slot >= 0 && slot < a.num_slots;
                 bad |= slot >= a.num_slots;
-                // all lanes form codes (the shuffles need the whole warp); heads of q and tokens without a slot
-                // point at the first tile and do not store
+                // all lanes form codes (the shuffles need the whole warp); heads of q among them and tokens
+                // without a slot point at the first tile and do not store
                 const int hk = is_q ? 0 : is_v ? h - a.Hq - a.Hk : h - a.Hq;
                 unsigned char *tile = a.cache + kv4_tile_offset(in ? slot : 0, hk, a.Hv, a.bs_log2, D);
                 quantise_store<D>(x, tile, is_v ? 1 : 0, l, static_cast<int>(slot & 15), live && in && !is_q);
@@ -290,18 +296,27 @@ bool many(int64_t tokens, int64_t heads, int D, const DeviceInfo &dev) {
     return tokens * heads * D >= int64_t(dev.num_sms) * 32768;
 }
 
+template <int D, bool TURN, bool KEEP>
+cudaError_t launch_form(const Kv4RopeArgs &a, cudaStream_t st, const DeviceInfo &dev) {
+    const int64_t heads = a.Hq + a.Hk + a.Hv;
+    if (many(a.T, heads, D, dev)) return launch_tasks(rope_kernel<D, 4, TURN, KEEP>, a, a.T, heads, 1024 / D, st, dev);
+    return launch_tasks(rope_kernel<D, 1, TURN, KEEP>, a, a.T, heads, 256 / D, st, dev);
+}
+
+// (without a cache there is a norm or a rotation, or a plain copy of q and k)
+template <int D>
+cudaError_t launch_rope(const Kv4RopeArgs &a, bool turn, cudaStream_t st, const DeviceInfo &dev) {
+    if (!a.cache) return launch_form<D, true, false>(a, st, dev);
+    return turn ? launch_form<D, true, true>(a, st, dev) : launch_form<D, false, true>(a, st, dev);
+}
+
 }  // namespace
 
 cudaError_t launch_kv4_rope(const Kv4RopeArgs &a, int D, cudaStream_t st, const DeviceInfo &dev) {
-    const int64_t heads = a.Hq + a.Hk + a.Hv;
-    if (many(a.T, heads, D, dev)) {
-        if (D == 64) return launch_tasks(rope_kernel<64, 4>, a, a.T, heads, 16, st, dev);
-        if (D == 128) return launch_tasks(rope_kernel<128, 4>, a, a.T, heads, 8, st, dev);
-        return launch_tasks(rope_kernel<256, 4>, a, a.T, heads, 4, st, dev);
-    }
-    if (D == 64) return launch_tasks(rope_kernel<64, 1>, a, a.T, heads, 4, st, dev);
-    if (D == 128) return launch_tasks(rope_kernel<128, 1>, a, a.T, heads, 2, st, dev);
-    return launch_tasks(rope_kernel<256, 1>, a, a.T, heads, 1, st, dev);
+    const bool turn = a.q_weight || a.k_weight || a.cos_sin;
+    if (D == 64) return launch_rope<64>(a, turn, st, dev);
+    if (D == 128) return launch_rope<128>(a, turn, st, dev);
+    return launch_rope<256>(a, turn, st, dev);
 }
 
 cudaError_t launch_kv4_gather(const Kv4GatherArgs &a, int D, cudaStream_t st, const DeviceInfo &dev) {
