@@ -43,64 +43,80 @@ __device__ __forceinline__ void unpack8(const uint4 v, float (&x)[8]) {
 __device__ __forceinline__ uint4 pack8(const float (&x)[8]) {
     uint32_t w[4];
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
-        w[i] = static_cast<uint32_t>(f32_to_bf16_bits(x[2 * i])) |
-               static_cast<uint32_t>(f32_to_bf16_bits(x[2 * i + 1])) << 16;
+    for (int i = 0; i < 4; ++i) {
+        const __nv_bfloat162 p = __floats2bfloat162_rn(x[2 * i], x[2 * i + 1]);
+        w[i] = *reinterpret_cast<const uint32_t *>(&p);
+    }
     return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
-// Quantises this lane's 8 elements (8 lanes hold a group of 64) and stores
-// the code word and, from the group's first lane, the parameters.  Quotients
-// are the correctly rounded ones of binary32, x / s by Markstein's correction
-// (P. Markstein, "Computation of elementary functions on the IBM RISC
-// System/6000 processor", 1990): y the rounded reciprocal, q = x y rounded,
-// the remainder x - q s exact in a fused multiply-add, q + r y rounded.  Adding
-// 1.5 2^23 rounds to the nearest whole number, ties to even, and leaves it in
-// the low bits.  A group whose scale is at its limit (values beyond 15 x
-// 65504, infinities) takes the plain division.
-template <int D>
-__device__ __forceinline__ void quantise_store(const float (&x)[8], unsigned char *tile, int part, int l, int row,
+__device__ __forceinline__ uint32_t min_bf16x2(uint32_t a, uint32_t b) {
+    uint32_t d;
+    asm("min.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+    return d;
+}
+// 1 / s rounded, for every binary16 s > 0: one Newton step from the
+// approximate reciprocal, compared with __frcp_rn for all of them.
+__device__ __forceinline__ float reciprocal(float s) {
+    float y;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(s));
+    return fmaf(fmaf(-s, y, 1.f), y, y);
+}
+// x / b correctly rounded, with y the rounded reciprocal of b, by Markstein's
+// correction (P. Markstein, "Computation of elementary functions on the IBM
+// RISC System/6000 processor", 1990): q = x y rounded, the remainder x - q b
+// exact in a fused multiply-add, q + r y rounded.
+__device__ __forceinline__ float divided(float x, float b, float y) {
+    const float q = __fmul_rn(x, y);
+    return fmaf(fmaf(-q, b, x), y, q);
+}
+
+// Quantises this lane's 8 BF16 elements (8 lanes hold a group of 64) and
+// stores the code word and, from the group's first lane, the parameters, at
+// `words` and `params` of the row.  The extremes are found as BF16 pairs (a
+// minimum of x and one of -x).  Quotients are the correctly rounded ones of
+// binary32.  Adding 1.5 2^23 rounds to the nearest whole number, ties to even,
+// and leaves it in the low bits.  A group whose scale is at its limit (values
+// beyond 15 x 65504, infinities) takes the plain division.
+__device__ __forceinline__ void quantise_store(const uint4 raw, unsigned char *words, unsigned char *params, int l,
                                                bool store) {
-    float lo = 0.f, hi = 0.f;
+    const uint32_t low = min_bf16x2(min_bf16x2(raw.x, raw.y), min_bf16x2(raw.z, raw.w));
+    const uint32_t neg = min_bf16x2(min_bf16x2(raw.x ^ 0x80008000u, raw.y ^ 0x80008000u),
+                                    min_bf16x2(raw.z ^ 0x80008000u, raw.w ^ 0x80008000u));
+    uint32_t both = min_bf16x2(__byte_perm(low, neg, 0x5410), __byte_perm(low, neg, 0x7632));
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        lo = fminf(lo, x[i]);
-        hi = fmaxf(hi, x[i]);
-    }
-#pragma unroll
-    for (int o = 1; o < 8; o <<= 1) {
-        lo = fminf(lo, __shfl_xor_sync(0xffffffffu, lo, o));
-        hi = fmaxf(hi, __shfl_xor_sync(0xffffffffu, hi, o));
-    }
-    const __half sh = __float2half_rn(fminf(__fdiv_rn(__fsub_rn(hi, lo), 15.f), 65504.f));
+    for (int o = 1; o < 8; o <<= 1) both = min_bf16x2(both, __shfl_xor_sync(0xffffffffu, both, o));
+    const float lo = fminf(__uint_as_float(both << 16), 0.f), hi = fmaxf(-__uint_as_float(both & 0xffff0000u), 0.f);
+    const __half sh = __float2half_rn(fminf(divided(__fsub_rn(hi, lo), 15.f, 1.f / 15.f), 65504.f));
     const float s = __half2float(sh);
     uint32_t word = 0;
     float z = 0.f;
     if (s >= 65504.f) {
+        float x[8];
+        unpack8(raw, x);
         z = __fadd_rn(fminf(fmaxf(rintf(__fdiv_rn(-lo, s)), 0.f), 15.f), 0.f);  // never -0
-#pragma unroll
+#pragma unroll 1
         for (int i = 0; i < 8; ++i) {
-            const float c = fminf(fmaxf(__fadd_rn(rintf(__fdiv_rn(x[i], s)), z), 0.f), 15.f);
+            const float v = i < 4 ? (i < 2 ? (i ? x[1] : x[0]) : (i == 2 ? x[2] : x[3]))
+                                  : (i < 6 ? (i == 4 ? x[4] : x[5]) : (i == 6 ? x[6] : x[7]));
+            const float c = fminf(fmaxf(__fadd_rn(rintf(__fdiv_rn(v, s)), z), 0.f), 15.f);
             word |= static_cast<uint32_t>(c) << (4 * i);
         }
     } else if (s > 0.f) {
-        const float inv = __frcp_rn(s);
-        auto whole = [&](float v) -> int {
-            const float q = v * inv;
-            return __float_as_int(__fadd_rn(fmaf(fmaf(-q, s, v), inv, q), 12582912.f)) - 0x4b400000;
-        };
-        const int zi = min(max(whole(-lo), 0), 15);
+        float x[8];
+        unpack8(raw, x);
+        const float inv = reciprocal(s);
+        auto whole = [&](float v) -> int { return __float_as_int(__fadd_rn(divided(v, s, inv), 12582912.f)); };
+        const int zi = __vimin_s32_relu(whole(-lo) - 0x4b400000, 15);
         z = static_cast<float>(zi);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) word |= static_cast<uint32_t>(min(max(whole(x[i]) + zi, 0), 15)) << (4 * i);
+        for (int i = 7; i >= 0; --i) word = word * 16 + __vimin_s32_relu(whole(x[i]) + (zi - 0x4b400000), 15);
     }
     if (!store) return;
-    const int group = l >> 3;
-    *reinterpret_cast<uint32_t *>(tile + part * 8 * D + (group * KV4_TILE + row) * 32 + (l & 7) * 4) = word;
+    *reinterpret_cast<uint32_t *>(words) = word;
     if ((l & 7) == 0)
-        *reinterpret_cast<uint32_t *>(tile + (16 + part) * D + (group * KV4_TILE + row) * 4) =
-            static_cast<uint32_t>(__half_as_ushort(sh)) |
-            static_cast<uint32_t>(__half_as_ushort(__float2half_rn(z))) << 16;
+        *reinterpret_cast<uint32_t *>(params) = static_cast<uint32_t>(__half_as_ushort(sh)) |
+                                                static_cast<uint32_t>(__half_as_ushort(__float2half_rn(z))) << 16;
 }
 
 // A task is U x 32 / LPH heads of one token, in the order q heads, k heads, v
@@ -136,6 +152,15 @@ __global__ void __launch_bounds__(ROPE_THREADS, 4) rope_kernel(const Kv4RopeArgs
         }
         int64_t slot = -1;
         if (KEEP) slot = a.slots[t];
+        // this lane's word of the slot's row in head 0, and its group's parameters from there
+        const bool in = KEEP && slot >= 0 && slot < a.num_slots;
+        if (KEEP) bad |= slot >= a.num_slots;
+        unsigned char *row = nullptr;
+        const int place = static_cast<int>(slot & 15), params = 16 * D + (l >> 3) * (KV4_TILE * 4) + place * 4 -
+                                                               (((l >> 3) * KV4_TILE + place) * 32 + (l & 7) * 4);
+        const int head_bytes = kv4_tile_bytes(D) << (a.bs_log2 - 4);
+        if (KEEP)
+            row = a.cache + kv4_tile_offset(in ? slot : 0, 0, a.Hv, a.bs_log2, D) + ((l >> 3) * KV4_TILE + place) * 32 + (l & 7) * 4;
         bool skip = false;  // a row whose position names none: written as zeros
         float cc[8], sn[8];
         const bool low = l < hl;
@@ -212,14 +237,11 @@ __global__ void __launch_bounds__(ROPE_THREADS, 4) rope_kernel(const Kv4RopeArgs
                     *reinterpret_cast<uint4 *>(a.k_out + (static_cast<size_t>(t) * a.Hk + (h - a.Hq)) * D + 8 * l) = packed;
             }
             if (KEEP && !all_q) {
-                unpack8(packed, x);
-                const bool in = slot >= 0 && slot < a.num_slots;
-                bad |= slot >= a.num_slots;
                 // all lanes form codes (the shuffles need the whole warp); heads of q among them and tokens
-                // without a slot point at the first tile and do not store
+                // without a slot do not store
                 const int hk = is_q ? 0 : is_v ? h - a.Hq - a.Hk : h - a.Hq;
-                unsigned char *tile = a.cache + kv4_tile_offset(in ? slot : 0, hk, a.Hv, a.bs_log2, D);
-                quantise_store<D>(x, tile, is_v ? 1 : 0, l, static_cast<int>(slot & 15), live && in && !is_q);
+                unsigned char *const at = row + hk * head_bytes + (is_v ? 8 * D : 0);
+                quantise_store(packed, at, at + params + (is_v ? D - 8 * D : 0), l, live && in && !is_q);
             }
         }
     }
