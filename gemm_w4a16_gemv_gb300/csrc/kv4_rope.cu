@@ -11,17 +11,19 @@
 // BF16 value, so the fused call stores bit for bit what the norm followed by
 // a plain append stores.
 //
-// All of it is bound by memory once there are enough tokens (by the launch
-// before that).  A head is held by D / 8 lanes of a warp, 8 elements (one
-// 16-byte load) per lane: the norm's sum, the rotation's partner (a lane
+// All of it is bound by the launch for few tokens, and by its instructions and
+// memory together for many.  A head is held by D / 8 lanes of a warp, 8 elements
+// (one 16-byte load) per lane: the norm's sum, the rotation's partner (a lane
 // rot / 16 away, or the lane itself for interleaved pairs) and a group's
 // extremes are shuffles, and a lane's 8 codes are one 32-bit word of the
 // cache's 32-byte rows.  A warp takes U x 256 / D heads of one token, all
 // loads first: with U = 4 each lane has 64 bytes under way and a token's
-// cosines and sines are read once for them; with few tokens U = 1 spreads the
-// heads over more warps.  Four CTAs of 256 threads per SM hold it best: 4099
-// tokens of 40 heads of 128 take 25.5 us, with registers for three or five
-// 28.4 and 39.7, with U = 2 27.7.
+// cosines, sines and addresses are found once for them; with few tokens U = 1
+// spreads the heads over more warps.  Measured: 4099 tokens of 40 heads of 128,
+// norm and rotation, 23.2 us (3.7 TB/s, issue slots 65% busy; four CTAs of 256
+// threads per SM hold it best, with registers for three or five it was 28.4
+// and 39.7 when it was 25.5); 8191 tokens of 8 heads of 256 appended and read
+// back 42.0 us (4.1 TB/s, issue slots 75% busy).
 #include "common.cuh"
 #include "kernels.h"
 #include "kv4.cuh"
@@ -121,9 +123,9 @@ __device__ __forceinline__ void quantise_store(const uint4 raw, unsigned char *w
 
 // A task is U x 32 / LPH heads of one token, in the order q heads, k heads, v
 // heads; `tasks` of them per token.  TURN: with a norm or a rotation; KEEP:
-// with a cache (instances of their own need fewer registers, 4099 tokens of 40
-// heads of 128 TURN_US us and 8191 tokens of 8 heads of 256 KEEP_US us with
-// the read-back, where one for all took 24.9 and 59.2).
+// with a cache (instances of their own need fewer registers: 4099 tokens of 40
+// heads of 128 take 24.0 us, 8191 tokens of 8 heads of 256 with their read-back
+// 49.8, where one for all took 24.9 and 59.2).
 template <int D, int U, bool TURN, bool KEEP>
 __global__ void __launch_bounds__(ROPE_THREADS, 4) rope_kernel(const Kv4RopeArgs a, const unsigned tasks) {
     constexpr int LPH = D / 8;   // lanes per head
@@ -142,13 +144,13 @@ __global__ void __launch_bounds__(ROPE_THREADS, 4) rope_kernel(const Kv4RopeArgs
         // the whole warp takes part in every shuffle: lanes past the last head
         // go along on it and store nothing
         uint4 raw[U];
+        // (as if each tensor began with the heads before its own)
+        const uint16_t *const qt = a.q + (t * a.q_stride + 8 * l), *const kt = a.k + (t * a.k_stride - a.Hq * D + 8 * l),
+                       *const vt = a.v + (t * a.v_stride - (a.Hq + a.Hk) * D + 8 * l);
 #pragma unroll
         for (int k = 0; k < U; ++k) {
             const int h = min(h0 + k * HPS, heads - 1);
-            const uint16_t *src = h < a.Hq          ? a.q + t * a.q_stride + h * D
-                                  : h < a.Hq + a.Hk ? a.k + t * a.k_stride + (h - a.Hq) * D
-                                                    : a.v + t * a.v_stride + (h - a.Hq - a.Hk) * D;
-            raw[k] = *reinterpret_cast<const uint4 *>(src + 8 * l);
+            raw[k] = *reinterpret_cast<const uint4 *>((h < a.Hq ? qt : h < a.Hq + a.Hk ? kt : vt) + h * D);
         }
         int64_t slot = -1;
         if (KEEP) slot = a.slots[t];
@@ -264,28 +266,39 @@ __global__ void __launch_bounds__(ROPE_THREADS, 4) gather_kernel(const Kv4Gather
         const int64_t slot = a.slots[t];
         const bool in = slot >= 0 && slot < a.num_slots;
         bad |= slot >= a.num_slots;
+        // the slot's tile in head 0, this lane's word and parameters in a tile of K
+        const unsigned char *const tile = a.cache + kv4_tile_offset(in ? slot : 0, 0, a.Hkv, a.bs_log2, D);
+        const int place = (l >> 3) * KV4_TILE + static_cast<int>(slot & 15);
+        const int at = place * 32 + (l & 7) * 4, params = 16 * D + place * 4;
+        const int head_bytes = kv4_tile_bytes(D) << (a.bs_log2 - 4);
         uint32_t word[U], sz[U];
 #pragma unroll
         for (int k = 0; k < U; ++k) {
             word[k] = sz[k] = 0;
             const int r = h0 + k * HPS, part = r >= a.Hkv;
             if (in && r < 2 * a.Hkv) {
-                const unsigned char *tile = a.cache + kv4_tile_offset(slot, part ? r - a.Hkv : r, a.Hkv, a.bs_log2, D);
-                const int at = (l >> 3) * KV4_TILE + static_cast<int>(slot & 15);
-                word[k] = *reinterpret_cast<const uint32_t *>(tile + part * 8 * D + at * 32 + (l & 7) * 4);
-                sz[k] = *reinterpret_cast<const uint32_t *>(tile + (16 + part) * D + at * 4);
+                const int off = (part ? r - a.Hkv : r) * head_bytes;
+                word[k] = *reinterpret_cast<const uint32_t *>(tile + (off + at + part * 8 * D));
+                sz[k] = *reinterpret_cast<const uint32_t *>(tile + (off + params + part * D));
             }
         }
+        const int64_t to = static_cast<int64_t>(t) * a.Hkv * D + 8 * l;
+        uint16_t *const kt = a.k + to, *const vt = a.v + (to - static_cast<int64_t>(a.Hkv) * D);
 #pragma unroll
         for (int k = 0; k < U; ++k) {
             const int r = h0 + k * HPS, part = r >= a.Hkv;
             if (r >= 2 * a.Hkv) continue;
-            const float s = f16_lo(sz[k]), z = f16_hi(sz[k]);
+            // a code in place in the significand of 2^23 is 2^23 + 16^i code; all
+            // of it is exact (zero times scale has 15 bits)
+            const float s = f16_lo(sz[k]), zs = -f16_hi(sz[k]) * s;
             float x[8];
 #pragma unroll
-            for (int i = 0; i < 8; ++i) x[i] = (static_cast<float>((word[k] >> (4 * i)) & 15u) - z) * s;
-            *reinterpret_cast<uint4 *>((part ? a.v : a.k) + (static_cast<size_t>(t) * a.Hkv + (part ? r - a.Hkv : r)) * D + 8 * l) =
-                pack8(x);
+            for (int i = 0; i < 8; ++i) {
+                const uint32_t w = i < 4 ? word[k] : word[k] >> 16;
+                const float c = __fsub_rn(__uint_as_float((w & (15u << (4 * (i & 3)))) | 0x4b000000u), 8388608.f);
+                x[i] = fmaf(c, s * (1.f / (1 << (4 * (i & 3)))), zs);
+            }
+            *reinterpret_cast<uint4 *>((part ? vt : kt) + r * D) = pack8(x);
         }
     }
     if (bad) atomicOr(a.status, kDevBadIndex);

@@ -204,3 +204,16 @@ def test_sample_rows_alone_and_together(R, V, bf16):
     for r in list(range(0, R, max(1, R // 6))) + [R - 1]:
         s = slice(r, r + 1)
         assert torch.equal(got[s], w4.w4a16_sample(x[s], u[s], T[s], k[s], p[s], m[s]))
+
+
+@pytest.mark.parametrize("T", [3, 1400])
+def test_append_with_queries_and_nothing_to_turn(T):
+    # q comes out as it is, k and v are stored as without it
+    torch, w4 = cuda_or_skip()
+    (q, k, v), _ = _qkv(torch, T, 12, 4, 256, T)
+    a, b = (w4.kv4_cache(T // 16 + 1, 4, 16, 256) for _ in range(2))
+    slots = torch.arange(T, device="cuda")
+    out = w4.kv4_append(k, v, a, slots, q=q)
+    w4.kv4_append(k, v, b, slots)
+    assert torch.equal(out, q) and torch.equal(a, b)
+    assert w4.w4a16_check_device_error() == 0
