@@ -322,6 +322,7 @@ __global__ void __launch_bounds__(W * 32, 1) attn_stream_kernel(const Kv4AttnArg
         const int b0 = min(tid * per, a.requests), b1 = min(b0 + per, a.requests);
         long long sum = 0;
         for (int b = b0; b < b1; ++b) {
+            asm volatile("prefetch.global.L1 [%0];" ::"l"(a.seq_lens + b));  // asked for beside cu_new
             const int rows = rows_of(a, b, G);
             long long n = 0;
             for (int r0 = 0; r0 < rows; r0 += R) {
@@ -833,26 +834,42 @@ __global__ void __launch_bounds__(W * 32, 1) attn_stream_kernel(const Kv4AttnArg
                 done = misc[0];
             }
             if (done) {
-                __threadfence();
+                if (TEAM == 1) __threadfence();  // (otherwise the first thread's, and the barrier)
                 const int step = TEAM == 1 ? 32 : W * 32;
                 for (int i = TEAM == 1 ? lane : tid; i < s.rows * (D / 4); i += step) {
                     const int r = i / (D / 4), d = i % (D / 4) * 4;
                     const float *const base = parts + r * (D + 4);
                     auto slot = [&](int c) { return (static_cast<size_t>(c) * 2 + (c == c_first)) * PART; };
-                    float m = NONE;
-                    for (int c = c_first; c <= c_last; ++c) m = fmaxf(m, __ldcg(base + slot(c)));
-                    float l = 0.f;
+                    // JOIN parts at a time, all on their way together: their
+                    // latency is most of the join's time
+                    constexpr int JOIN = 8;
+                    float m = NONE, l = 0.f;
                     float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
-                    for (int c = c_first; c <= c_last; ++c) {
-                        const float2 ml = __ldcg(reinterpret_cast<const float2 *>(base + slot(c)));
-                        const float4 v = __ldcg(reinterpret_cast<const float4 *>(base + slot(c) + 4 + d));
-                        const float f = ex2(ml.x - m);
-                        l = fmaf(f, ml.y, l);
-                        o.x = fmaf(f, v.x, o.x);
-                        o.y = fmaf(f, v.y, o.y);
-                        o.z = fmaf(f, v.z, o.z);
-                        o.w = fmaf(f, v.w, o.w);
+                    for (int c0 = c_first; c0 <= c_last; c0 += JOIN) {
+                        float2 ml[JOIN];
+                        float4 v[JOIN];
+#pragma unroll
+                        for (int j = 0; j < JOIN; ++j) {
+                            const float *const from = base + slot(min(c0 + j, c_last));
+                            ml[j] = __ldcg(reinterpret_cast<const float2 *>(from));
+                            v[j] = __ldcg(reinterpret_cast<const float4 *>(from + 4 + d));
+                        }
+                        float up = m;
+#pragma unroll
+                        for (int j = 0; j < JOIN; ++j) up = fmaxf(up, ml[j].x);
+                        const float old = ex2(m - up);
+                        m = up;
+                        l *= old;
+                        o.x *= old, o.y *= old, o.z *= old, o.w *= old;
+#pragma unroll
+                        for (int j = 0; j < JOIN; ++j) {
+                            const float f = c0 + j <= c_last ? ex2(ml[j].x - m) : 0.f;
+                            l = fmaf(f, ml[j].y, l);
+                            o.x = fmaf(f, v[j].x, o.x);
+                            o.y = fmaf(f, v[j].y, o.y);
+                            o.z = fmaf(f, v[j].z, o.z);
+                            o.w = fmaf(f, v[j].w, o.w);
+                        }
                     }
                     const float inv = l == 0.f ? 0.f : 1.f / l;
                     *reinterpret_cast<uint2 *>(row_of(r) + d) =
