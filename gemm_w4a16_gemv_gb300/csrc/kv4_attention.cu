@@ -7,11 +7,14 @@
 // Bound: memory.  A token's K and V of one head are 18 D / 16 bytes and every
 // byte is read once; a row block of up to 8 NT rows (the G query heads of a
 // key head times the request's new tokens) shares the read.  Measured, 16 query
-// heads of 256 on 8: 64 requests of 255 to 32767 tokens 200 us, 5.07 TB/s or 75%
+// heads of 256 on 8: 64 requests of 255 to 32767 tokens 190 us, 5.3 TB/s or 78%
 // of the copy bandwidth (the ALU pipe 58% busy, issue slots 64%: the codes'
 // logic and parameters, then the memory); 128 requests with a window of 1024 and
-// 4 sinks 71 us, 4.06 TB/s; one request of 8200 tokens 15 us, of which the
-// memory would take 2.8: start, one round of copies, two joins.
+// 4 sinks 69 us, 4.2 TB/s; one request of 8200 tokens 13 us (the memory would take
+// 2.8: lengths, shares and pages 4, the copies 3.5, two tiles a warp that arrive
+// together 3, the join in the CTA 1.3, the one across CTAs the rest).  The parts
+// of a split row are read eight at a time: 14.9 -> 13.1 us, 200 -> 190, 71 -> 69;
+// spread over more threads of the CTA besides it was 13.1 still.
 //
 // Work.  The unit is a cache tile (16 tokens of one head, one contiguous run
 // fetched by one bulk copy).  The visible tiles of all (request, row block,
