@@ -90,6 +90,18 @@ struct Shared {
     int list_n, cand_n, bin;
 };
 
+// Pairs of BF16: the larger of each (a NaN gives way), and -0 as +0.
+__device__ __forceinline__ uint32_t max_bf16x2(uint32_t a, uint32_t b) {
+    uint32_t d;
+    asm("max.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+    return d;
+}
+__device__ __forceinline__ uint32_t plus_zero_bf16x2(uint32_t a) {
+    uint32_t d;
+    asm("add.rn.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(0u));
+    return d;
+}
+
 // A row's masses.  The quotient l / T is the correctly rounded one: for T = 1
 // the logit itself; for T well inside the exponent range by Markstein's
 // correction (P. Markstein, "Computation of elementary functions on the IBM
@@ -171,10 +183,17 @@ __global__ void __launch_bounds__(THREADS) sample_kernel(const SampleArgs a) {
     // ---- the row into shared memory, once; NaN as -infinity, -0 as +0
     float best = -INFINITY;
     {
-        auto clean = [&](float v) -> float {
+        uint32_t best2 = 0xff80ff80u;  // of a pair
+        auto clean = [&](uint32_t w) -> uint32_t {
+            if (BF16) {
+                w = plus_zero_bf16x2(max_bf16x2(w, 0xff80ff80u));
+                best2 = max_bf16x2(best2, w);
+                return w;
+            }
+            float v = __uint_as_float(w);
             v = v != v ? -INFINITY : v + 0.f;
             best = fmaxf(best, v);
-            return v;
+            return __float_as_uint(v);
         };
         constexpr int PER = BF16 ? 8 : 4;  // logits of 16 bytes
         const unsigned char *p = static_cast<const unsigned char *>(a.logits) +
@@ -210,17 +229,11 @@ __global__ void __launch_bounds__(THREADS) sample_kernel(const SampleArgs a) {
             }
 #pragma unroll
             for (int q = 0; q < BATCH; ++q) {
-                uint32_t x[4] = {w[q].x, w[q].y, w[q].z, w[q].w};
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    if (BF16) {
-                        const float lo = clean(__uint_as_float(x[e] << 16)), hi = clean(__uint_as_float(x[e] & 0xffff0000u));
-                        x[e] = __float_as_uint(lo) >> 16 | (__float_as_uint(hi) & 0xffff0000u);
-                    } else x[e] = __float_as_uint(clean(__uint_as_float(x[e])));
-                }
-                reinterpret_cast<uint4 *>(row)[(i0 + q) * THREADS + tid] = make_uint4(x[0], x[1], x[2], x[3]);
+                reinterpret_cast<uint4 *>(row)[(i0 + q) * THREADS + tid] =
+                    make_uint4(clean(w[q].x), clean(w[q].y), clean(w[q].z), clean(w[q].w));
             }
         }
+        if (BF16) best = fmaxf(__uint_as_float(best2 << 16), __uint_as_float(best2 & 0xffff0000u));
     }
 
     // f(N logits, element of the first) of every own unit, in no particular order
@@ -469,7 +482,14 @@ __global__ void __launch_bounds__(THREADS) sample_kernel(const SampleArgs a) {
         const float deepest = static_cast<float>(goal_bin(static_cast<u64>(k), false) + 1);
         const bool all = deepest >= static_cast<float>(BINS);
         Shared *const head = cluster.map_shared_rank(&sh, 0);
+        // (a bound that no logit as deep as that lies below, whatever was rounded:
+        // most units have none above it)
+        const float reach = top_l - deepest / mass.per_bin * 1.0001f;
+        const float bound = all ? -INFINITY : reach - 1e-5f * (fabsf(reach) + fabsf(top_l));
         each([&](const float(&l)[N], int e0) {
+            float most = fmaxf(fmaxf(l[0], l[1]), fmaxf(l[2], l[3]));
+            if (N == 8) most = fmaxf(most, fmaxf(fmaxf(l[N - 4], l[N - 3]), fmaxf(l[N - 2], l[N - 1])));
+            if (most < bound) return;
             unsigned in = 0;
 #pragma unroll
             for (int e = 0; e < N; ++e)
