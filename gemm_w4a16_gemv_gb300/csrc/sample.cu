@@ -15,17 +15,17 @@
 // histograms) goes through distributed shared memory, a cluster barrier per
 // exchange.  Nothing is sorted but short lists.  Rows past what is resident (38
 // clusters of 8 CTAs, two to an SM by registers and by shared memory) follow in
-// waves.  us for 262144 BF16 logits, one row and 128 rows: greedy 6.1 and 35,
-// top-k 40 with or without top-p 11.5 and 58, neither 12.2 and 69, top-p alone
-// 31 and 179 (the masses and the cut), a mixture of settings 12.6 and 110.
+// waves.  us for 262144 BF16 logits, one row and 128 rows: greedy 5.4 and 30,
+// top-k 40 with or without top-p 10 and 49, neither 11.7 and 65, top-p alone 31
+// and 174 (the masses and the cut), a mixture of settings 11.1 and 100.
 //
 // Small top-k (up to 256): a histogram of the threads' largest logits gives a
 // bin that at least k of them reach, so everything kept lies in the bins up
 // to it; those few candidates go to one CTA, which sorts them and does the
 // rest alone.  Exponentials are taken of the candidates only.  Against the
-// general way below: top-k 40 10.8 / 19.5 us (with top-p 11.5 / 33), 256 19.0 /
-// 20.3 (19.1 / 36) for one row of 262144; 128 rows 57 / 105 (58 / 197) and 73 /
-// 113 (73 / 204); 64 rows of 32000, 256 20.8 / 18.0 (20.5 / 28.4): beyond 256 the
+// general way below: top-k 40 9.7 / 19.0 us (with top-p 10.2 / 34), 256 18.4 /
+// 19.8 (18.5 / 35) for one row of 262144; 128 rows 48 / 100 (50 / 193) and 67 /
+// 108 (67 / 200); 64 rows of 32000, 256 21.0 / 17.9 (20.6 / 30.6): beyond 256 the
 // sort of the candidates costs what is saved.
 //
 // Otherwise one pass forms all masses, their sum and a histogram over
@@ -179,6 +179,10 @@ __global__ void __launch_bounds__(THREADS) sample_kernel(const SampleArgs a) {
     asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
     pdl_launch_dependents();
     pdl_wait();
+    // the row's settings, on their way beside the row
+    const float T = a.temperature ? a.temperature[r] : 1.f, p = a.top_p ? a.top_p[r] : 1.f, u = a.u[r];
+    const float wanted = a.min_p ? a.min_p[r] : 0.f, min_p = wanted > 0.f ? fminf(wanted, 1.f) : 0.f;
+    const int k = a.top_k ? a.top_k[r] : 0;
 
     // ---- the row into shared memory, once; NaN as -infinity, -0 as +0
     float best = -INFINITY;
@@ -196,9 +200,9 @@ __global__ void __launch_bounds__(THREADS) sample_kernel(const SampleArgs a) {
             return __float_as_uint(v);
         };
         constexpr int PER = BF16 ? 8 : 4;  // logits of 16 bytes
-        const unsigned char *p = static_cast<const unsigned char *>(a.logits) +
-                                 (r * a.row_stride + slice) * (BF16 ? 2 : 4);
-        const bool vec = (reinterpret_cast<uintptr_t>(p) & 15u) == 0;
+        const unsigned char *from = static_cast<const unsigned char *>(a.logits) +
+                                    (r * a.row_stride + slice) * (BF16 ? 2 : 4);
+        const bool vec = (reinterpret_cast<uintptr_t>(from) & 15u) == 0;
         constexpr int COUNT = EPT / PER, BATCH = COUNT < 8 ? COUNT : 8;  // vectors a thread, and at a time
         const bool inside = vec && V - slice >= EPT * THREADS;
 #pragma unroll 1
@@ -207,22 +211,22 @@ __global__ void __launch_bounds__(THREADS) sample_kernel(const SampleArgs a) {
             if (inside) {
 #pragma unroll
                 for (int q = 0; q < BATCH; ++q)
-                    w[q] = *reinterpret_cast<const uint4 *>(p + 16 * static_cast<int64_t>((i0 + q) * THREADS + tid));
+                    w[q] = *reinterpret_cast<const uint4 *>(from + 16 * static_cast<int64_t>((i0 + q) * THREADS + tid));
             } else {
 #pragma unroll
                 for (int q = 0; q < BATCH; ++q) {
                     const int first = ((i0 + q) * THREADS + tid) * PER, left = V - slice - first;  // logits from here on
                     uint32_t x[4];
                     if (vec && left >= PER) {
-                        w[q] = *reinterpret_cast<const uint4 *>(p + 16 * static_cast<int64_t>((i0 + q) * THREADS + tid));
+                        w[q] = *reinterpret_cast<const uint4 *>(from + 16 * static_cast<int64_t>((i0 + q) * THREADS + tid));
                         continue;
                     }
 #pragma unroll
                     for (int e = 0; e < PER; ++e) {
                         if (BF16) {
-                            const uint32_t h = e < left ? reinterpret_cast<const uint16_t *>(p)[first + e] : 0xff80u;
+                            const uint32_t h = e < left ? reinterpret_cast<const uint16_t *>(from)[first + e] : 0xff80u;
                             x[e / 2] = e & 1 ? x[e / 2] | h << 16 : h;
-                        } else x[e & 3] = e < left ? reinterpret_cast<const uint32_t *>(p)[first + e] : 0xff800000u;
+                        } else x[e & 3] = e < left ? reinterpret_cast<const uint32_t *>(from)[first + e] : 0xff800000u;
                     }
                     w[q] = make_uint4(x[0], x[1], x[2], x[3]);
                 }
@@ -394,7 +398,6 @@ __global__ void __launch_bounds__(THREADS) sample_kernel(const SampleArgs a) {
         if (rank == 0 && tid == 0) a.tokens[r] = -1;
         return;                // every CTA of the cluster is past its last access to the others
     }
-    const float T = a.temperature ? a.temperature[r] : 1.f;
     const Masses mass(T, top_l);
     if (!(T > 0.f) || !(fabsf(mass.top) < INFINITY)) {
         // the largest logit: the first index that holds it
@@ -416,12 +419,9 @@ __global__ void __launch_bounds__(THREADS) sample_kernel(const SampleArgs a) {
     };
     // masses of bin b are below 2^(40 - 0.04 b): shortened to 15 bits
     auto shift_of = [](int b) -> int { return max(0, 26 - static_cast<int>(static_cast<float>(b) * 0.0400748f)); };
-    const int k = a.top_k ? a.top_k[r] : 0;
-    const float p = a.top_p ? a.top_p[r] : 1.f;
     // min_p 2^40, rounded up to a whole mass (NaN: off)
-    const double min_mass = static_cast<double>(a.min_p ? fminf(a.min_p[r], 1.f) : 0.f) * static_cast<double>(UNIT);
+    const double min_mass = static_cast<double>(min_p) * static_cast<double>(UNIT);
     const u64 least = min_mass > 0. ? static_cast<u64>(__double2ll_ru(min_mass)) : 0ull;
-    const float u = a.u[r];
     auto share_of = [](u64 total, float x) -> u64 {  // trunc(x of total), x in [0, 1]
         return static_cast<u64>(__double2ll_rz(static_cast<double>(total) * static_cast<double>(x)));
     };
@@ -820,7 +820,7 @@ __global__ void __launch_bounds__(THREADS) sample_kernel(const SampleArgs a) {
     // taken of them.  A little lower than the bound itself, which is rounded.
     float floor_l = cut;
     if (least > 0) {
-        const float reach = -logf(fminf(fmaxf(a.min_p[r], 1e-30f), 1.f)) * T;  // max - l at the bound
+        const float reach = -logf(fmaxf(min_p, 1e-30f)) * T;  // max - l at the bound
         const float lowest = top_l - reach * 1.0001f - 1e-4f * (fabsf(top_l) + T);
         floor_l = fmaxf(floor_l, lowest);
     }

@@ -525,7 +525,7 @@ int kv4_attention(const uint16_t *q, int64_t q_stride, const uint8_t *cache,
  *   temperature : binary32 [rows] or NULL (1); not above 0: the largest logit
  *   top_k       : int32 [rows] or NULL; below 1: off
  *   top_p       : binary32 [rows] or NULL; 1 or more: off
- *   min_p       : binary32 [rows] or NULL; 0: off, 1 or more as 1
+ *   min_p       : binary32 [rows] or NULL; 0, less or NaN: off, 1 or more as 1
  *   tokens      : int32 [rows]; -1 for a row without a logit above -infinity
  * NaN logits are never chosen.  A row whose largest logit / T is infinite
  * gives that token (the first such).  rows <= 2^20, vocab <= 2^18.

@@ -217,3 +217,14 @@ def test_append_with_queries_and_nothing_to_turn(T):
     w4.kv4_append(k, v, b, slots)
     assert torch.equal(out, q) and torch.equal(a, b)
     assert w4.w4a16_check_device_error() == 0
+
+
+def test_sample_settings_that_are_no_numbers_are_off():
+    torch, w4 = cuda_or_skip()
+    x = torch.randn(6, 3000, device="cuda", generator=torch.Generator("cuda").manual_seed(3))
+    u = torch.linspace(0, 0.99, 6, device="cuda")
+    nan = torch.full((6,), float("nan"), device="cuda")
+    off = w4.w4a16_sample(x, u)
+    assert torch.equal(off, w4.w4a16_sample(x, u, min_p=nan))
+    assert torch.equal(off, w4.w4a16_sample(x, u, min_p=-torch.ones_like(u)))
+    assert torch.equal(off, w4.w4a16_sample(x, u, top_p=nan))
