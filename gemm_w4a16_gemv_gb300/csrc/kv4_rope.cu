@@ -20,7 +20,7 @@
 // loads first: with U = 4 each lane has 64 bytes under way and a token's
 // cosines, sines and addresses are found once for them; with few tokens U = 1
 // spreads the heads over more warps.  Measured: 4099 tokens of 40 heads of 128,
-// norm and rotation, 23.2 us (3.7 TB/s, issue slots 65% busy; four CTAs of 256
+// norm and rotation, 22.4 us (3.8 TB/s, issue slots 65% busy; four CTAs of 256
 // threads per SM hold it best, with registers for three or five it was 28.4
 // and 39.7 when it was 25.5); 8191 tokens of 8 heads of 256 appended and read
 // back 42.0 us (4.1 TB/s, issue slots 75% busy).
@@ -304,12 +304,15 @@ __global__ void __launch_bounds__(ROPE_THREADS, 4) gather_kernel(const Kv4Gather
     if (bad) atomicOr(a.status, kDevBadIndex);
 }
 
+// At most `per_sm` CTAs per SM: 4, one round of CTAs that go on with further
+// tasks, for the norm alone (4099 tokens 23.4 -> 22.4 us), 16 where codes are
+// formed or read (append and read-back of 8191 tokens 42.7 us, with 4 49.0).
 template <typename Args>
-cudaError_t launch_tasks(void (*kern)(Args, unsigned), const Args &a, int64_t tokens, int64_t heads, int per_task,
+cudaError_t launch_tasks(void (*kern)(Args, unsigned), const Args &a, int64_t tokens, int64_t heads, int per_task, int per_sm,
                          cudaStream_t st, const DeviceInfo &dev) {
     const int64_t tasks = (heads + per_task - 1) / per_task;
     int64_t grid = (tokens * tasks + ROPE_THREADS / 32 - 1) / (ROPE_THREADS / 32);
-    const int64_t most = 16 * static_cast<int64_t>(dev.num_sms);
+    const int64_t most = per_sm * static_cast<int64_t>(dev.num_sms);
     if (grid > most) grid = most;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(static_cast<unsigned>(grid));
@@ -334,8 +337,8 @@ bool many(int64_t tokens, int64_t heads, int D, const DeviceInfo &dev) {
 template <int D, bool TURN, bool KEEP>
 cudaError_t launch_form(const Kv4RopeArgs &a, cudaStream_t st, const DeviceInfo &dev) {
     const int64_t heads = a.Hq + a.Hk + a.Hv;
-    if (many(a.T, heads, D, dev)) return launch_tasks(rope_kernel<D, 4, TURN, KEEP>, a, a.T, heads, 1024 / D, st, dev);
-    return launch_tasks(rope_kernel<D, 1, TURN, KEEP>, a, a.T, heads, 256 / D, st, dev);
+    if (many(a.T, heads, D, dev)) return launch_tasks(rope_kernel<D, 4, TURN, KEEP>, a, a.T, heads, 1024 / D, KEEP ? 16 : 4, st, dev);
+    return launch_tasks(rope_kernel<D, 1, TURN, KEEP>, a, a.T, heads, 256 / D, 16, st, dev);
 }
 
 // (without a cache there is a norm or a rotation, or a plain copy of q and k)
@@ -357,13 +360,13 @@ cudaError_t launch_kv4_rope(const Kv4RopeArgs &a, int D, cudaStream_t st, const 
 cudaError_t launch_kv4_gather(const Kv4GatherArgs &a, int D, cudaStream_t st, const DeviceInfo &dev) {
     const int64_t heads = 2 * a.Hkv;
     if (many(a.T, heads, D, dev)) {
-        if (D == 64) return launch_tasks(gather_kernel<64, 4>, a, a.T, heads, 16, st, dev);
-        if (D == 128) return launch_tasks(gather_kernel<128, 4>, a, a.T, heads, 8, st, dev);
-        return launch_tasks(gather_kernel<256, 4>, a, a.T, heads, 4, st, dev);
+        if (D == 64) return launch_tasks(gather_kernel<64, 4>, a, a.T, heads, 16, 16, st, dev);
+        if (D == 128) return launch_tasks(gather_kernel<128, 4>, a, a.T, heads, 8, 16, st, dev);
+        return launch_tasks(gather_kernel<256, 4>, a, a.T, heads, 4, 16, st, dev);
     }
-    if (D == 64) return launch_tasks(gather_kernel<64, 1>, a, a.T, heads, 4, st, dev);
-    if (D == 128) return launch_tasks(gather_kernel<128, 1>, a, a.T, heads, 2, st, dev);
-    return launch_tasks(gather_kernel<256, 1>, a, a.T, heads, 1, st, dev);
+    if (D == 64) return launch_tasks(gather_kernel<64, 1>, a, a.T, heads, 4, 16, st, dev);
+    if (D == 128) return launch_tasks(gather_kernel<128, 1>, a, a.T, heads, 2, 16, st, dev);
+    return launch_tasks(gather_kernel<256, 1>, a, a.T, heads, 1, 16, st, dev);
 }
 
 }  // namespace w4
