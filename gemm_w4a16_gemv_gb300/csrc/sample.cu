@@ -13,8 +13,8 @@
 // Bound: latency.  A row is read once, by a cluster of up to 8 CTAs that keep
 // it in shared memory; what they need of one another (maxima, sums,
 // histograms) goes through distributed shared memory, a cluster barrier per
-// exchange.  Nothing is sorted but short lists.  Rows past what is resident (38
-// clusters of 8 CTAs, two to an SM by registers and by shared memory) follow in
+// exchange.  Nothing is sorted but short lists.  Rows past what is resident (at most
+// 38 clusters of 8 CTAs, two to an SM by registers and by shared memory) follow in
 // waves.  us for 262144 BF16 logits, one row and 128 rows: greedy 5.4 and 30,
 // top-k 40 with or without top-p 10 and 49, neither 11.7 and 65, top-p alone 31
 // and 174 (the masses and the cut), a mixture of settings 11.1 and 100.
