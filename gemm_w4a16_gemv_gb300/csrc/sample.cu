@@ -577,7 +577,9 @@ __global__ void __launch_bounds__(THREADS) sample_kernel(const SampleArgs a) {
         while (true) {
             above = inside = count = 0;
             klo = 0xffffffffu, khi = 0;
-            const float upper = static_cast<float>(bin), lower = bin == BINS - 1 ? INFINITY : static_cast<float>(bin + 1);
+            // the last bin has no lower end: a finite logit may lie infinitely deep
+            // (no comparison with NaN holds)
+            const float upper = static_cast<float>(bin), lower = bin == BINS - 1 ? NAN : static_cast<float>(bin + 1);
             in_mode([&](auto mode) {
                 uint32_t his = 0, los = 0;
                 each([&](const float(&l)[N], int) {
@@ -585,7 +587,7 @@ __global__ void __launch_bounds__(THREADS) sample_kernel(const SampleArgs a) {
 #pragma unroll
                     for (int e = 0; e < N; ++e) {
                         const float d = mass.depth(l[e]);
-                        const bool here = d < lower && l[e] >= floor_l;
+                        const bool here = !(d >= lower) && l[e] >= floor_l;
                         in |= static_cast<unsigned>(here && d >= upper) << e;
                         if (by_mass) {
                             uint32_t hi, lo;
