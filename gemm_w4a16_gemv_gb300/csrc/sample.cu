@@ -110,16 +110,19 @@ __device__ __forceinline__ uint32_t plus_zero_bf16x2(uint32_t a) {
 // rounds to the quotient; else by division.
 enum { MODE_ONE, MODE_FUSED, MODE_DIVIDE };
 struct Masses {
-    float T, inv, top, top_l, per_bin;
+    float T, inv, top, half_top, per_half;
     int mode;
-    __device__ __forceinline__ Masses(float temperature, float largest) : T(temperature), top_l(largest) {
+    __device__ __forceinline__ Masses(float temperature, float top_l) : T(temperature), half_top(0.5f * top_l) {
         inv = __frcp_rn(T);
         top = __fdiv_rn(top_l, T);
-        per_bin = fminf(__fdividef(BINS_PER_UNIT, T), 1e30f);
+        per_half = fminf(2.f * BINS_PER_UNIT * inv, 2e30f);
         mode = T == 1.f ? MODE_ONE : T > 1e-15f && T < 1e15f && fabsf(top_l) < 1e15f ? MODE_FUSED : MODE_DIVIDE;
     }
-    // (max - l) / T in bins, not rounded to one; rises as l falls
-    __device__ __forceinline__ float depth(float l) const { return (top_l - l) * per_bin; }
+    // (max - l) / T in bins, not rounded to one; rises as l falls.  From half the
+    // difference, which no two finite logits take past binary32's range.
+    __device__ __forceinline__ float depth(float l) const { return fmaf(-0.5f, l, half_top) * per_half; }
+    // max itself, but for the last bit of a subnormal
+    __device__ __forceinline__ float largest() const { return 2.f * half_top; }
     // mass before rounding
     template <int MODE>
     __device__ __forceinline__ float scaled(float l) const {
@@ -484,8 +487,8 @@ __global__ void __launch_bounds__(THREADS) sample_kernel(const SampleArgs a) {
         Shared *const head = cluster.map_shared_rank(&sh, 0);
         // (a bound that no logit as deep as that lies below, whatever was rounded:
         // most units have none above it)
-        const float reach = top_l - deepest / mass.per_bin * 1.0001f;
-        const float bound = all ? -INFINITY : reach - 1e-5f * (fabsf(reach) + fabsf(top_l));
+        const float reach = mass.largest() - 2.f * deepest / mass.per_half * 1.0001f;
+        const float bound = all ? -INFINITY : reach - 1e-5f * (fabsf(reach) + fabsf(mass.largest()));
         each([&](const float(&l)[N], int e0) {
             float most = fmaxf(fmaxf(l[0], l[1]), fmaxf(l[2], l[3]));
             if (N == 8) most = fmaxf(most, fmaxf(fmaxf(l[N - 4], l[N - 3]), fmaxf(l[N - 2], l[N - 1])));
@@ -823,7 +826,7 @@ __global__ void __launch_bounds__(THREADS) sample_kernel(const SampleArgs a) {
     float floor_l = cut;
     if (least > 0) {
         const float reach = -logf(fmaxf(min_p, 1e-30f)) * T;  // max - l at the bound
-        const float lowest = top_l - reach * 1.0001f - 1e-4f * (fabsf(top_l) + T);
+        const float lowest = mass.largest() - reach * 1.0001f - 1e-4f * (fabsf(mass.largest()) + T) - 1e-37f;
         floor_l = fmaxf(floor_l, lowest);
     }
     auto kept = [&](float l, int index) -> u64 {

@@ -65,3 +65,18 @@ def test_tiny_temperatures(T):
         x[2], x[7] = 0.0, 0.25
         for k in (3, 300):
             assert (_tokens(torch, w4, x, [0.0, 0.5, 0.99], T, k, 1.0) == 7).all()
+
+
+@pytest.mark.parametrize("k", [0, 2, 300])
+@pytest.mark.parametrize("T", [1e38, 2e38, 3.4e38, np.inf])
+def test_temperatures_as_large_as_the_logits(T, k):
+    # differences of logits past binary32's range, quotients of ordinary size
+    torch, w4 = cuda_or_skip()
+    x = np.zeros(1000)
+    x[3], x[900], x[500] = 3e38, -3e38, -1e38
+    x[1::2] = -np.inf
+    x[3] = 3e38
+    w = _kept(np.float32(x), float(np.float32(T)) if T < 1e39 else 1e300, k, 1.0, 0.0)
+    wide = np.flatnonzero(w > 1e-4)
+    got = _tokens(torch, w4, torch.tensor(x, dtype=torch.float32, device="cuda"), (w.cumsum() - w / 2)[wide], T, k, 1.0)
+    assert np.array_equal(got, wide)
