@@ -84,7 +84,7 @@ int kv4_plan(const int32_t *ctx_lens, const int32_t *new_lens, int requests, int
         return fail(W4A16_ERR_INVALID_ARG, "%s: null pointer", fn);
     if (page_log2(block_size) < 0)
         return fail(W4A16_ERR_UNSUPPORTED, "%s: block size %d (16, 32, 64, 128 or 256)", fn, block_size);
-    if (requests > 8192 || num_tokens > kMaxTokens || max_blocks * block_size > 0x7fffffff || num_free > 0x7fffffff)
+    if (requests > 8192 || num_tokens > kMaxTokens || max_blocks > 0x7fffffff / block_size || num_free > 0x7fffffff)
         return fail(W4A16_ERR_UNSUPPORTED, "%s: sizes too large", fn);
     if (!aligned(ctx_lens, 4) || !aligned(new_lens, 4) || !aligned(block_table, 4) || !aligned(free_blocks, 4) ||
         !aligned(seq_lens, 4) || !aligned(cu_new, 4) || !aligned(positions, 4) || !aligned(slots, 8) ||
@@ -259,7 +259,7 @@ int kv4_attention(const uint16_t *q, int64_t q_stride, const uint8_t *cache, int
         return fail(W4A16_ERR_INVALID_ARG, "%s: scale=%g must be finite", fn, static_cast<double>(scale));
     if (int r = check_head_dim(fn, D)) return r;
     if (int r = check_page(fn, block_size, num_blocks)) return r;
-    if (requests > 4096 || T > kMaxTokens || Hq > 1024 || max_blocks * block_size > 0x7fffffff)
+    if (requests > 4096 || T > kMaxTokens || Hq > 1024 || max_blocks > 0x7fffffff / block_size)
         return fail(W4A16_ERR_UNSUPPORTED, "%s: sizes too large", fn);
     if (T == 0) return ok();
     if (int r = check_rows(fn, "q", q, q_stride, Hq, D)) return r;
