@@ -176,6 +176,7 @@ struct Kv4AttnArgs {
     // prompt kernel those of more than rows_above; the first launch of a call
     // zeroes the rows of no request
     int rows_least, rows_most, rows_above, zero_rest;
+    unsigned int inject;  // test-only injection flags (0 normally)
 };
 constexpr int PROMPT_COUNTERS = 13056;  // byte offset in the scratch of the prompt kernel's two counters
 cudaError_t launch_kv4_prompt(const Kv4AttnArgs &a, int D, cudaStream_t st, const DeviceInfo &dev);

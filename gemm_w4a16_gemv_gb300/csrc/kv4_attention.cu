@@ -414,10 +414,13 @@ __global__ void __launch_bounds__(W * 32, 1) attn_stream_kernel(const Kv4AttnArg
         place = ((pre.s.h << sub_log2) + (tile & ((1 << sub_log2) - 1))) * TB;
     };
     uint32_t live = 0;       // bit of a stage: it holds a tile
+    // lane 0 issues the copies (test-only injection: none) until one of its waits
+    // runs out: a stage whose copy has not arrived must not be handed out again
+    bool issues = lane == 0 && !(a.inject & kInjectStallPipeline);
     auto fetch = [&](int stage) {
         const bool in = place >= 0 && page >= 0 && page < a.num_blocks;
         bad |= place >= 0 && !in;
-        if (in && lane == 0) {
+        if (in && issues) {
             mbar_arrive_expect_tx(&bars[stage], TB);
             asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
                              smem_u32(ring + static_cast<size_t>(stage) * TB)),
@@ -478,7 +481,17 @@ __global__ void __launch_bounds__(W * 32, 1) attn_stream_kernel(const Kv4AttnArg
 
         for (; u < seg_end; u += TEAM) {
             if (live >> stage & 1u) {
-                ok = mbar_wait(&bars[stage], parity >> stage & 1u, a.status) && ok;
+                if (!mbar_try_wait(smem_u32(&bars[stage]), parity >> stage & 1u) && ok) {
+                    ok = mbar_wait(&bars[stage], parity >> stage & 1u, a.status);
+                    if (!ok && issues) {
+                        // no copy may be under way when the CTA ends: wait (bounded)
+                        // for those issued and not waited for
+#pragma unroll 1
+                        for (int i = 0; live >> i; ++i)
+                            if (live >> i & 1u) mbar_wait(&bars[i], parity >> i & 1u, nullptr);
+                        issues = false;
+                    }
+                }
                 parity ^= 1u << stage;
                 const unsigned char *tile = ring + static_cast<size_t>(stage) * TB;
                 const int j0 = cur.tile(u) * 16;
@@ -892,11 +905,6 @@ __global__ void __launch_bounds__(W * 32, 1) attn_stream_kernel(const Kv4AttnArg
         } else par ^= 1;
     }
     if (__any_sync(0xffffffffu, bad) && lane == 0) atomicOr(a.status, kDevBadIndex);
-    // every copy of this warp has been waited for, unless a wait gave up: then
-    // wait (bounded) for what may still be under way before the CTA ends
-    if (!__all_sync(0xffffffffu, ok))
-        for (int i = 0; i < depth; ++i)
-            if (live >> i & 1u) mbar_wait(&bars[i], parity >> i & 1u, nullptr);
 }
 
 template <int D, int NT, int W, int TEAM, bool SPLIT>
@@ -989,6 +997,7 @@ cudaError_t launch_kv4_attention(const Kv4AttnArgs &args, int D, cudaStream_t st
     a.rows_least = 1;
     a.rows_most = 0x7fffffff;
     a.zero_rest = 1;
+    a.inject = dev.inject;
     if (rows > few) {
         // requests of many rows to the tensor cores; the others of a mixed step to
         // the streaming kernel, those of a token or so (most, as a rule) by the
