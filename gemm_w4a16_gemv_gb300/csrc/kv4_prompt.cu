@@ -51,8 +51,11 @@
 // The running reference M of a row puts its largest P into [2^6, 2^15] (binary16
 // then keeps 11 bits of weights down to 2^-20 of it) and moves only when P would
 // pass 2^15; then the softmax warps scale O in tensor memory themselves, between
-// two products.  Every wait is bounded; on a timeout the roles still go
-// through all their arrivals.
+// two products.
+//
+// Every wait is bounded.  On a timeout the roles still go through all their
+// arrivals, except that one which is not told of its next item leaves; tensor
+// memory is given back, and the CTAs end, when the products issued are done.
 #include "common.cuh"
 #include "kernels.h"
 #include "kv4.cuh"
@@ -81,12 +84,13 @@ struct Bars {
     uint64_t qfull, kfull[2], kfree[2], vfull[2], vfree[2], sfull[2], pfull[2], ifull[QUEUE], known[METAS];
     uint32_t tmem;
     int item[QUEUE];
+    int late;  // key tiles worked on, where some wait has run out; else 0
 };
 // Of a key tile, from the warps that form it: the factors of its cache tiles
 // and which of them there are.
 struct alignas(16) Meta {
     float k_factor[8], v_exponent[8], v_factor[8];
-    unsigned char there[8];
+    unsigned char held[8];
 };
 
 // MN-major operand with the 128-byte swizzle: 64 contiguous elements x 8 rows
@@ -407,6 +411,7 @@ __global__ void __launch_bounds__(THREADS, 1) attn_prompt_kernel(const Kv4AttnAr
         }
         for (int i = 0; i < QUEUE; ++i) mbar_init(&bar.ifull[i], 1);
         for (int i = 0; i < METAS; ++i) mbar_init(&bar.known[i], 2 * FORM_WARPS);
+        bar.late = 0;
         fence_barrier_init();
     }
     if (warp == 12) tmem_take<PAIR>(&bar.tmem);
@@ -462,10 +467,15 @@ __global__ void __launch_bounds__(THREADS, 1) attn_prompt_kernel(const Kv4AttnAr
     const uint32_t tmem = bar.tmem;
     const int items = cum[a.requests];
     unsigned int *const counter = reinterpret_cast<unsigned int *>(a.scratch + PROMPT_COUNTERS);
-    // the k-th item of this CTA or pair (items or more: there is none)
+    // the k-th item of this CTA or pair (items or more: there is none, or it was not announced in time)
     auto item_at = [&](int k) -> int {
-        wait_for<PAIR>(&bar.ifull[k % QUEUE], (k / QUEUE) & 1, a.status);
-        return *static_cast<volatile int *>(&bar.item[k % QUEUE]);
+        const bool told = wait_for<PAIR>(&bar.ifull[k % QUEUE], (k / QUEUE) & 1, a.status);
+        const int index = *static_cast<volatile int *>(&bar.item[k % QUEUE]);
+        return __all_sync(0xffffffffu, told) ? index : items;
+    };
+    // until the products of so many key tiles are done
+    auto finish = [&](int g) {
+        if (g > 0) wait_for(&bar.vfree[(g - 1) % BUFS], ((g - 1) / BUFS) & 1, nullptr);
     };
 
     if (warp < 4) {
@@ -496,8 +506,8 @@ __global__ void __launch_bounds__(THREADS, 1) attn_prompt_kernel(const Kv4AttnAr
                 tmem_ld_32x32b_x32(t_s, x0);
                 wait_for(&bar.known[g % METAS], (g / METAS) & 1, a.status);
                 if (i == 0) Fr = q_factor[(k_item & 1) * ROWS + r];
-                const uint2 there = *reinterpret_cast<const uint2 *>(meta.there);
-                const bool free = (there.x & there.y) == 0x01010101u && j0 + KEYS <= p_lo + 1 &&
+                const uint2 held = *reinterpret_cast<const uint2 *>(meta.held);
+                const bool free = (held.x & held.y) == 0x01010101u && j0 + KEYS <= p_lo + 1 &&
                                   (window == 0 || p_hi - j0 < window || j0 + KEYS <= sinks);
                 // 32 keys at a time: scores in, weights out into the columns of scores already read (half as wide)
                 float m = M, scaled = 1.f, added = 0.f;
@@ -506,7 +516,7 @@ __global__ void __launch_bounds__(THREADS, 1) attn_prompt_kernel(const Kv4AttnAr
                         // keys from .. upto of these 32 are seen, and those before `first`
                         const int at = j0 + 32 * c;
                         auto below = [](int n) -> uint32_t { return n >= 32 ? 0xffffffffu : n > 0 ? (1u << n) - 1 : 0u; };
-                        const uint32_t pages = (c & 2 ? there.y : there.x) >> (16 * (c & 1));
+                        const uint32_t pages = (c & 2 ? held.y : held.x) >> (16 * (c & 1));
                         uint32_t see = window == 0 ? 0xffffffffu : ~below(p - window + 1 - at) | below(sinks - at);
                         see &= below(min(p + 1, cur.end) - at) & ((pages & 1u) * 0xffffu | (pages >> 8 & 1u) * 0xffff0000u);
 #pragma unroll
@@ -772,7 +782,7 @@ __global__ void __launch_bounds__(THREADS, 1) attn_prompt_kernel(const Kv4AttnAr
                         const int e = lane ? e1 : e0;
                         meta.v_exponent[c] = static_cast<float>(e);
                         meta.v_factor[c] = pow2(-e);
-                        meta.there[c] = (lane ? tile.n1 : tile.n0) > 0;
+                        meta.held[c] = (lane ? tile.n1 : tile.n0) > 0;
                     }
                 }
                 if (!is_v) {
@@ -848,7 +858,8 @@ __global__ void __launch_bounds__(THREADS, 1) attn_prompt_kernel(const Kv4AttnAr
             // most an item behind, and the forming warps are ahead.
             const int workers = static_cast<int>(gridDim.x) / CTAS;
             int index = static_cast<int>(blockIdx.x) / CTAS;
-            announce(0, index);
+            if (!(a.inject & kInjectStallPipeline)) announce(0, index);
+            if (a.inject) index = items;  // test-only injection: no item announced, or none worked on
             for (int k = 0; index < items; ++k) {
                 int next = 0;
                 if (lane == 0) next = workers + static_cast<int>(atomicAdd(counter, 1u));
@@ -871,14 +882,27 @@ __global__ void __launch_bounds__(THREADS, 1) attn_prompt_kernel(const Kv4AttnAr
                     counter[0] = 0;
                     counter[1] = 0;
                 }
+                if (PAIR && (*reinterpret_cast<volatile unsigned int *>(a.status) & kDevTimeout)) {
+                    bar.late = g;
+                    asm volatile("st.shared::cluster.s32 [%0], %1;" ::"r"(peer(&bar.late, 1)), "r"(g) : "memory");
+                }
             }
+            __syncwarp();
         }
         // tensor memory is released only when every product has completed
-        if (g > 0) wait_for(&bar.vfree[(g - 1) % BUFS], ((g - 1) / BUFS) & 1, nullptr);
+        finish(g);
     }
     tc_fence_before();
     __syncthreads();
-    if (PAIR) cluster_sync();  // nothing of the other CTA's is in use any more
+    if (PAIR) {
+        cluster_sync();  // nothing of the other CTA's is in use any more
+        if (bar.late) {
+            // a role of the second CTA may have left early: it ends when it too has been
+            // told that the last products are done
+            if (rank == 1 && warp == 12) finish(bar.late);
+            cluster_sync();
+        }
+    }
     if (warp == 12) {
         tc_fence_after();
         tmem_give<PAIR>(tmem);
