@@ -546,7 +546,8 @@ __global__ void __launch_bounds__(THREADS, 1) attn_prompt_kernel(const Kv4AttnAr
                         added *= f;
                         scaled *= f;
                         if (c > 0) {
-                            const uint32_t f2 = pack_f16(f, f);
+                            // (in binary32: f may lie below binary16's smallest number
+                            // where its product with a weight does not)
                             tmem_st_wait();
 #pragma unroll 1
                             for (int q = 0; q < c; ++q) {
@@ -554,7 +555,7 @@ __global__ void __launch_bounds__(THREADS, 1) attn_prompt_kernel(const Kv4AttnAr
                                 tmem_ld_32x32b_x16(t_s + 16 * q, w);
                                 tmem_ld_wait();
 #pragma unroll
-                                for (int e = 0; e < 16; ++e) w[e] = mul_f16x2(w[e], f2);
+                                for (int e = 0; e < 16; ++e) w[e] = pack_f16(f16_lo(w[e]) * f, f16_hi(w[e]) * f);
                                 tmem_st_32x32b_x16(t_s + 16 * q, w);
                             }
                         }

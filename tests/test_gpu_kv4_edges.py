@@ -1,0 +1,55 @@
+"""Edges of the KV4 operators: what lies outside a window, lengths out of
+range, references that move far, values that are no numbers."""
+import numpy as np
+import pytest
+
+from tests import kv4_helpers as ref
+from tests.gpu_helpers import cuda_or_skip
+from tests.test_gpu_kv4_attention import _check, _problem
+from tests.test_gpu_kv4_cache import _i32
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.mark.parametrize("Hq,Hkv,D", [(32, 16, 256), (32, 16, 128), (48, 24, 64)])
+@pytest.mark.parametrize("new", [1, 140])
+@pytest.mark.parametrize("jump", [20, 26, 27, 32, 40])
+@pytest.mark.parametrize("at", [64, 97, 130])
+def test_weights_before_a_far_move_of_the_reference_count(Hq, Hkv, D, new, jump, at):
+    # Keys of log2 score 0, then 7, then one of `jump` whose values are all zero:
+    # the output is what the others add.  In the bound: the result's rounding
+    # (2^-8), weights and values rounded to binary16 (2^-11 each), the scores'
+    # binary32 steps (2^-16), and weights kept to 2^-30 of the largest.
+    torch, w4 = cuda_or_skip()
+    rng = np.random.default_rng(jump)
+    end, bs = 160, 16
+    c = ref.Cache(end // bs, Hkv, bs, D)
+    score = np.zeros(end)
+    score[32:64], score[at] = 7, jump
+    one, zero = np.full(D // 64, 1.0, np.float16), rng.integers(1, 15, (end, Hkv, D // 64))
+    V = np.zeros((end, Hkv, D))
+    for j in range(end):
+        for h in range(Hkv):
+            kc = np.zeros(D, np.uint8)
+            kc[0] = score[j] > 0
+            c.put(0, j, h, kc, one * max(score[j], 1), one * 0)
+            z = np.repeat(zero[j, h], 64)
+            codes = z if j == at else rng.integers(0, 16, D)
+            c.put(1, j, h, codes.astype(np.uint8), one, zero[j, h].astype(np.float16))
+            V[j, h] = codes - z
+    q = torch.zeros(new, Hq, D, dtype=torch.bfloat16, device="cuda")
+    q[..., 0] = 1
+    ln2 = float(np.float32(np.log(2)))
+    out = w4.kv4_attention(q, torch.tensor(c.raw, device="cuda"), _i32(torch, [list(range(end // bs))]),
+                           _i32(torch, [end]), _i32(torch, [0, new]), w4.kv4_attention_scratch(Hq, Hkv, D), scale=ln2,
+                           max_new=new).double().cpu().numpy()
+    for t in range(new):
+        see = end - new + t + 1
+        w = np.exp(ln2 * (score[:see] - score[:see].max()))
+        w /= w.sum()
+        o, size = np.einsum("j,jhd->hd", w, V[:see]), np.einsum("j,jhd->hd", w, np.abs(V[:see]))
+        tol = 2.0 ** -8 * np.abs(o) + (2.0 ** -10 + 2.0 ** -16) * (1 + 2.0 ** -8) * size + \
+            2.0 ** -30 * w.max() * np.abs(V[:see]).sum(0)
+        got = out[t].reshape(Hkv, Hq // Hkv, D)
+        assert (np.abs(got - o[:, None]) <= tol[:, None]).all(), t
+    assert w4.w4a16_check_device_error() == 0
