@@ -12,6 +12,26 @@ constexpr int64_t kMaxTokens = int64_t(1) << 24;
 
 bool aligned(const void *p, unsigned n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
 
+// An array of a call, for the check of overlap.
+struct Span {
+    const char *name;
+    const void *p;
+    int64_t bytes;
+};
+
+// None of the arrays from number `inputs` on, which are written, may share
+// bytes with another one.
+template <int N>
+int check_apart(const char *fn, int inputs, const Span (&x)[N]) {
+    for (int i = inputs; i < N; ++i)
+        for (int j = 0; j < i; ++j) {
+            const uintptr_t a = reinterpret_cast<uintptr_t>(x[i].p), b = reinterpret_cast<uintptr_t>(x[j].p);
+            if (a < b + x[j].bytes && b < a + x[i].bytes && x[i].bytes > 0 && x[j].bytes > 0)
+                return fail(W4A16_ERR_INVALID_ARG, "%s: %s and %s overlap", fn, x[i].name, x[j].name);
+        }
+    return W4A16_OK;
+}
+
 // log2 of a page size, or -1.
 int page_log2(int block_size) {
     for (int l = 4; l <= 8; ++l)
@@ -90,6 +110,12 @@ int kv4_plan(const int32_t *ctx_lens, const int32_t *new_lens, int requests, int
         !aligned(seq_lens, 4) || !aligned(cu_new, 4) || !aligned(positions, 4) || !aligned(slots, 8) ||
         !aligned(taken, 4))
         return fail(W4A16_ERR_MISALIGNED, "%s: arrays must be aligned to their elements", fn);
+    // every CTA reads the lengths again while the first one writes its results
+    const Span arrays[] = {{"ctx_lens", ctx_lens, 4 * int64_t(requests)}, {"new_lens", new_lens, 4 * int64_t(requests)},
+                           {"free_blocks", free_blocks, 4 * num_free}, {"block_table", block_table, 4 * requests * max_blocks},
+                           {"seq_lens", seq_lens, 4 * int64_t(requests)}, {"cu_new", cu_new, 4 * int64_t(requests) + 4},
+                           {"positions", positions, 4 * num_tokens}, {"slots", slots, 8 * num_tokens}, {"taken", taken, 4}};
+    if (int r = check_apart(fn, 3, arrays)) return r;
     w4::DeviceInfo dev;
     w4::Kv4PlanArgs a;
     if (int r = device_state(dev, a.status)) return r;

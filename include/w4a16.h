@@ -400,7 +400,9 @@ int w4a16_graph_destroy(w4a16_graph_t graph);
  * graph can be replayed with other lengths.  Too few free blocks: the missing
  * entries and slots are -1 and the device status is set; so it is for a
  * negative length, a request longer than its table row and more tokens than
- * num_tokens.  One launch.  requests <= 8192, num_tokens <= 2^24.
+ * num_tokens.  No output may share memory with another array of the call
+ * (INVALID_ARG): lengths are not advanced in place.  One launch.
+ * requests <= 8192, num_tokens <= 2^24.
  */
 int kv4_plan(const int32_t *ctx_lens, const int32_t *new_lens, int requests,
              int32_t *block_table, int64_t max_blocks,
