@@ -174,8 +174,8 @@ struct Kv4AttnArgs {
     // set by launch_kv4_attention: the streaming kernel takes requests of
     // rows_least to rows_most rows (new tokens x query heads per key head), the
     // prompt kernel those of more than rows_above; the first launch of a call
-    // zeroes the rows of no request
-    int rows_least, rows_most, rows_above, zero_rest;
+    // zeroes the rows of no request and looks for lengths out of range
+    int rows_least, rows_most, rows_above, first_launch;
     unsigned int inject;  // test-only injection flags (0 normally)
 };
 constexpr int PROMPT_COUNTERS = 13056;  // byte offset in the scratch of the prompt kernel's two counters

@@ -16,6 +16,7 @@
 #pragma once
 
 #include "common.cuh"
+#include "kernels.h"
 
 namespace w4 {
 
@@ -33,6 +34,20 @@ __device__ __forceinline__ size_t kv4_tile_offset(int64_t slot, int h, int Hkv, 
     const int64_t block = slot >> bs_log2;
     const int64_t tile = (slot & ((int64_t(1) << bs_log2) - 1)) >> 4;
     return static_cast<size_t>(((block * Hkv + h) << (bs_log2 - 4)) + tile) * static_cast<size_t>(kv4_tile_bytes(D));
+}
+
+// Rows before request b; whatever the array holds, inside the tensors.
+__device__ __forceinline__ int rows_before(const Kv4AttnArgs &a, int b) {
+    return static_cast<int>(min(max(static_cast<int64_t>(a.cu_new[b]), int64_t(0)), a.T));
+}
+
+// Sets the status if request b's rows lie outside the tensors, or its length
+// is negative or more than its row of the block table names (of a request
+// with new tokens: of others it is not used).
+__device__ __forceinline__ void check_lengths(const Kv4AttnArgs &a, int b) {
+    const int64_t from = a.cu_new[b], to = a.cu_new[b + 1], len = a.seq_lens[b];
+    if (from < 0 || to < from || to > a.T || (to > from && (len < 0 || len > a.max_blocks << a.bs_log2)))
+        atomicOr(a.status, kDevBadIndex);
 }
 
 __device__ __forceinline__ float f16_lo(uint32_t w) { return __half2float(__ushort_as_half(static_cast<uint16_t>(w))); }

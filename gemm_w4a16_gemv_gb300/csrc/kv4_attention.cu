@@ -120,11 +120,6 @@ __device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
 // rows 2 t + 1) fall into different banks.
 __device__ __forceinline__ int key_of_row(int r) { return (0x57463120u >> (4 * r)) & 15; }
 
-// Rows before request b; whatever the array holds, inside the tensors.
-__device__ __forceinline__ int rows_before(const Kv4AttnArgs &a, int b) {
-    return static_cast<int>(min(max(static_cast<int64_t>(a.cu_new[b]), int64_t(0)), a.T));
-}
-
 // Rows of request b that this kernel answers: new tokens x query heads of a
 // key head, or none when the prompt kernel takes them.
 __device__ __forceinline__ int rows_of(const Kv4AttnArgs &a, int b, int G) {
@@ -326,6 +321,7 @@ __global__ void __launch_bounds__(W * 32, 1) attn_stream_kernel(const Kv4AttnArg
         long long sum = 0;
         for (int b = b0; b < b1; ++b) {
             asm volatile("prefetch.global.L1 [%0];" ::"l"(a.seq_lens + b));  // asked for beside cu_new
+            if (a.first_launch && blockIdx.x == 0) check_lengths(a, b);
             const int rows = rows_of(a, b, G);
             long long n = 0;
             for (int r0 = 0; r0 < rows; r0 += R) {
@@ -354,7 +350,7 @@ __global__ void __launch_bounds__(W * 32, 1) attn_stream_kernel(const Kv4AttnArg
         }
         __syncthreads();
     }
-    if (a.zero_rest) {  // rows that belong to no request
+    if (a.first_launch) {  // rows that belong to no request
         const int64_t from = static_cast<int64_t>(rows_before(a, a.requests)) * a.Hq * D / 8;
         const int64_t to = a.T * a.Hq * D / 8;
         for (int64_t i = from + static_cast<int64_t>(blockIdx.x) * W * 32 + tid; i < to;
@@ -996,7 +992,7 @@ cudaError_t launch_kv4_attention(const Kv4AttnArgs &args, int D, cudaStream_t st
     const int64_t few = stream_rows(a.requests * a.Hkv, D, dev);
     a.rows_least = 1;
     a.rows_most = 0x7fffffff;
-    a.zero_rest = 1;
+    a.first_launch = 1;
     a.inject = dev.inject;
     if (rows > few) {
         // requests of many rows to the tensor cores; the others of a mixed step to
@@ -1006,7 +1002,7 @@ cudaError_t launch_kv4_attention(const Kv4AttnArgs &args, int D, cudaStream_t st
         a.rows_above = a.requests > 1 ? static_cast<int>(few) : 0;
         if (cudaError_t e = launch_kv4_prompt(a, D, st, dev)) return e;
         if (a.requests == 1) return cudaSuccess;
-        a.zero_rest = 0;
+        a.first_launch = 0;
         a.rows_most = D == 256 ? 2 : D == 128 ? 4 : 8;
         if (G <= a.rows_most)
             if (cudaError_t e = stream(a, D, a.rows_most, st, dev)) return e;

@@ -299,10 +299,6 @@ __device__ __forceinline__ float2 add2(float2 a, float2 b) {
 __device__ __forceinline__ float factor(float f, float k) { return fmaxf(f * k, 1.2e-38f); }
 __device__ __forceinline__ float pow2(int e) { return __uint_as_float(static_cast<uint32_t>(127 + e) << 23); }
 
-__device__ __forceinline__ int rows_before(const Kv4AttnArgs &a, int b) {
-    return static_cast<int>(min(max(static_cast<int64_t>(a.cu_new[b]), int64_t(0)), a.T));
-}
-
 struct Item {
     int b, h, tok0, r0, rows;   // rows [r0, r0 + rows) of the request; its first token
     int base;                   // position of row r is base + r / G
@@ -454,7 +450,9 @@ __global__ void __launch_bounds__(THREADS, 1) attn_prompt_kernel(const Kv4AttnAr
         }
         if (lane == 0) cum[0] = 0;
     }
-    if (a.zero_rest) {  // rows that belong to no request
+    if (blockIdx.x == 0)
+        for (int b = tid; b < a.requests; b += THREADS) check_lengths(a, b);
+    if (a.first_launch) {  // rows that belong to no request
         const int64_t from = static_cast<int64_t>(rows_before(a, a.requests)) * a.Hq * D / 8, to = a.T * a.Hq * D / 8;
         for (int64_t i = from + static_cast<int64_t>(blockIdx.x) * THREADS + tid; i < to;
              i += static_cast<int64_t>(gridDim.x) * THREADS)

@@ -482,6 +482,9 @@ int kv4_gather(const uint8_t *cache, int64_t num_blocks, int block_size,
  * or j < sinks (the first `sinks` tokens stay visible):
  *   out[t, h] = sum_j softmax_j(scale * q[t, h] . K[j, h / (Hq / Hkv)]) V[j]
  * A row that sees nothing (p < 0) is written as zeros.
+ * Lengths of a request with new tokens below 0 or past its row of the table,
+ * and a cu_new that falls or leaves 0 .. T, set the device status; what is
+ * outside is left out.
  *   q   : bfloat16, T rows of Hq heads of D, q_stride elements apart
  *   out : bfloat16 [T, Hq, D];  rows past cu_new[requests] are zeros
  *   block_table : int32 [requests, max_blocks]; a block id outside

@@ -53,3 +53,37 @@ def test_weights_before_a_far_move_of_the_reference_count(Hq, Hkv, D, new, jump,
         got = out[t].reshape(Hkv, Hq // Hkv, D)
         assert (np.abs(got - o[:, None]) <= tol[:, None]).all(), t
     assert w4.w4a16_check_device_error() == 0
+
+
+@pytest.mark.parametrize("Hq,Hkv,D", [(32, 16, 256), (4, 2, 128), (48, 24, 64)])
+@pytest.mark.parametrize("new", [1, 130])
+def test_lengths_out_of_range_are_reported(Hq, Hkv, D, new):
+    torch, w4 = cuda_or_skip()
+    ends, n = [170, 140, 135], [new] * 3
+    dev, host = _problem(torch, ends, n, Hq, Hkv, D, 16, D)
+    width = host[2].shape[1]
+    kw = dict(scratch=w4.kv4_attention_scratch(Hq, Hkv, D), max_new=new)
+    whole = w4.kv4_attention(**dev, **kw)
+    torch.cuda.synchronize()
+    assert w4.w4a16_check_device_error() == 0
+
+    def status(lens=ends, cu=(0, new, 2 * new, 3 * new), T=3 * new):
+        args = dict(dev, seq_lens=_i32(torch, lens), cu_new=_i32(torch, cu), q=dev["q"][:T])
+        out = w4.kv4_attention(**args, **kw)
+        torch.cuda.synchronize()
+        return w4.w4a16_check_device_error(), out
+
+    full = width * 16
+    assert status()[0] == 0
+    assert status([170, full + 1, 135])[0] == 6
+    assert status([170, 140, 2 ** 31 - 1])[0] == 6
+    assert status([-1, 140, 135])[0] == 6
+    # a request without new tokens is not looked at
+    for unused in (-5, 2 ** 31 - 1):
+        assert status([170, unused, 135], (0, new, new, 2 * new), 2 * new)[0] == 0
+    # fewer tokens in all than new ones: rows that see nothing, no error
+    assert status([0, 140, 135])[0] == 0
+    assert status(cu=(0, new, 2 * new, 3 * new + 1))[0] == 6
+    assert status(cu=(0, 2 * new, new, 3 * new))[0] == 6
+    assert status(cu=(-1, new, 2 * new, 3 * new))[0] == 6
+    assert status()[0] == 0 and torch.equal(status()[1], whole)
