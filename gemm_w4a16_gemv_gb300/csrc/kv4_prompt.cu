@@ -302,7 +302,8 @@ __device__ __forceinline__ float pow2(int e) { return __uint_as_float(static_cas
 struct Item {
     int b, h, tok0, r0, rows;   // rows [r0, r0 + rows) of the request; its first token
     int base;                   // position of row r is base + r / G
-    int end;                    // keys at or past this are seen by no row
+    int end;                    // keys at or past this are seen by no row,
+    int sink, first;            // nor are those from `sink` to before `first`
     int n, ns, low;             // key tiles: the first ns, then from `low` on
     __device__ __forceinline__ int key0(int i) const { return (i < ns ? i : i - ns + low) * KEYS; }
 };
@@ -333,10 +334,12 @@ __device__ __forceinline__ Item item_of(const Kv4AttnArgs &a, const int *cum, co
     const int p_lo = first + it.r0 / G, p_hi = first + (it.r0 + it.rows - 1) / G;
     const int end = max(min(p_hi + 1, cap), 0);
     int low = 0, ns = 0;
+    it.sink = it.first = 0;
     if (a.window > 0) {
-        low = static_cast<int>(max(p_lo - a.window + 1, int64_t(0))) / KEYS;
-        ns = (static_cast<int>(min(a.sinks, static_cast<int64_t>(end))) + KEYS - 1) / KEYS;
-        low = max(low, ns);
+        it.first = static_cast<int>(max(p_lo - a.window + 1, int64_t(0)));
+        it.sink = static_cast<int>(min(a.sinks, static_cast<int64_t>(end)));
+        ns = (it.sink + KEYS - 1) / KEYS;
+        low = max(it.first / KEYS, ns);
     }
     const int last = (end + KEYS - 1) / KEYS;
     it.end = end;
@@ -710,11 +713,16 @@ __global__ void __launch_bounds__(THREADS, 1) attn_prompt_kernel(const Kv4AttnAr
             const Item it = item_of<ITEM>(a, cum, order, index, G);
             const int32_t *const pages = a.block_table + static_cast<int64_t>(it.b) * a.max_blocks;
             // Lane 0 looks after cache tile c0, lane 1 after c1 (and so on): its
-            // tokens in key tile i, the page (asked for a step before it is looked
+            // tokens in key tile i (none if no row sees any of them: the caller may
+            // have given such a page back), the page (asked for a step before it is looked
             // at), its number among all cache tiles (of 18 D bytes: 32 bits are
             // enough for terabytes).
             const int c = lane & 1 ? c1 : c0;
-            auto tokens = [&](int i) -> int { return i < it.n ? min(max(it.end - it.key0(i) - c * 16, 0), 16) : 0; };
+            const int from = it.first - 15 - c * 16, upto = it.sink - c * 16, end = it.end - c * 16;  // of key0
+            auto tokens = [&](int i) -> int {
+                const int at = it.key0(i);
+                return i < it.n && (at >= from || at < upto) ? min(max(end - at, 0), 16) : 0;
+            };
             auto page_of = [&](int i) -> int { return tokens(i) > 0 ? pages[(it.key0(i) + c * 16) >> a.bs_log2] : -1; };
             auto number = [&](int i, int id) -> unsigned {
                 const int at = (it.key0(i) >> 4) + c;
