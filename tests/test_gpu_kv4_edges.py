@@ -16,26 +16,29 @@ pytestmark = pytest.mark.gpu
 @pytest.mark.parametrize("window,sinks", [(1, 0), (30, 0), (30, 5), (100, 20)])
 @pytest.mark.parametrize("new", [1, 20, 130])
 def test_pages_that_no_query_sees_may_be_gone(Hq, Hkv, D, bs, window, sinks, new):
-    # given back by the caller: the same bits, and no error
+    # given back by the caller, or given to somebody else (the spare pages hold NaN
+    # and infinite parameters): the same bits, and no error
     torch, w4 = cuda_or_skip()
     ends = [300, 190, 131, 20]
     n = [min(new, e) for e in ends]
     dev, host = _problem(torch, ends, n, Hq, Hkv, D, bs, D + window)
     kw = dict(scratch=w4.kv4_attention_scratch(Hq, Hkv, D), window=window, sinks=sinks, max_new=new)
     whole = w4.kv4_attention(**dev, **kw)
-    gone = 0
+    gone, spare = [], (set(range(host[1].blocks)) - set(host[2].ravel().tolist())).pop()
     for b, (e, m) in enumerate(zip(ends, n)):
         first = max(0, e - m - window + 1)            # the first key in the first query's window
         for i in range(host[2].shape[1]):
             if i * bs >= sinks and (i + 1) * bs <= first:
-                host[2][b, i] = -1
-                gone += 1
-    assert gone > 0
-    dev["block_table"] = _i32(torch, host[2])
-    out = w4.kv4_attention(**dev, **kw)
-    torch.cuda.synchronize()
-    assert w4.w4a16_check_device_error() == 0
-    assert torch.equal(out, whole)
+                gone.append((b, i))
+    assert gone
+    for page in (-1, spare):
+        for at in gone:
+            host[2][at] = page
+        dev["block_table"] = _i32(torch, host[2])
+        out = w4.kv4_attention(**dev, **kw)
+        torch.cuda.synchronize()
+        assert w4.w4a16_check_device_error() == 0
+        assert torch.equal(out, whole)
 
 
 @pytest.mark.parametrize("Hq,Hkv,D", [(32, 16, 256), (32, 16, 128), (48, 24, 64)])
