@@ -1,11 +1,14 @@
 """Python binding of the w4a16 CUDA library (include/w4a16.h).
 
 Argument marshalling only: every entry point checks tensor dtypes, shapes,
-devices and contiguity, then calls the C ABI of ``_lib/libw4a16.so`` through
-ctypes with raw device pointers and the current CUDA stream.  All arithmetic
-happens in the library's CUDA kernels; there is no fallback of any kind.  If
-the library has not been built, importing this package succeeds but every
-call raises ``RuntimeError`` (build it with ``__graft_entry__.build()``).
+devices and contiguity, then calls the C ABI of ``_lib/libw4a16.so`` with raw
+device pointers and the current CUDA stream: through ctypes, or, for the
+operators of a decode step (``kv4_*``, ``w4a16_qk_norm_rope``,
+``w4a16_sample``), through the small host extension ``_lib/_marshal.so``.  All
+arithmetic happens in the library's CUDA kernels; there is no fallback of any
+kind.  If the library (or for those operators the extension) has not been
+built, importing this package succeeds but every call raises ``RuntimeError``
+(build it with ``__graft_entry__.build()``).
 
 Tensors: packed codes are ``torch.uint8``; scales and zero points
 ``torch.float16``; activations and outputs ``torch.bfloat16``.
@@ -110,7 +113,7 @@ def library_path() -> str:
 
 def lib():
     """The loaded CUDA library (raises if it has not been built)."""
-    global _lib, _fast
+    global _lib
     if _lib is not None:
         return _lib
     with _lock:
@@ -123,12 +126,6 @@ def lib():
                 fn = getattr(handle, name)
                 fn.argtypes = argtypes
                 fn.restype = restype
-            loader = importlib.machinery.ExtensionFileLoader("_marshal", _MARSHAL_PATH)
-            spec = importlib.util.spec_from_file_location("_marshal", _MARSHAL_PATH, loader=loader)
-            module = importlib.util.module_from_spec(spec)
-            loader.exec_module(module)
-            module.bind(_LIB_PATH)
-            _fast = module
             _lib = handle
         return _lib
 
@@ -523,8 +520,23 @@ _TYPES = {"b": torch.uint8, "h": torch.bfloat16, "i": torch.int32, "l": torch.in
 # here, to say what it is.
 
 def _extension():
+    """The loaded host extension (raises if it has not been built, or was built
+    for another torch)."""
+    global _fast
     if _fast is None:
         lib()
+        with _lock:
+            if _fast is None:
+                loader = importlib.machinery.ExtensionFileLoader("_marshal", _MARSHAL_PATH)
+                spec = importlib.util.spec_from_file_location("_marshal", _MARSHAL_PATH, loader=loader)
+                try:
+                    module = importlib.util.module_from_spec(spec)
+                    loader.exec_module(module)
+                    module.bind(_LIB_PATH)
+                except (ImportError, RuntimeError) as e:
+                    raise RuntimeError("the host extension %s cannot be loaded (%s); run __graft_entry__.build()" %
+                                       (_MARSHAL_PATH, e)) from e
+                _fast = module
     return _fast
 
 

@@ -59,12 +59,24 @@ def _stale(lib: str, deps) -> bool:
 
 
 def build(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
-    """Compile the library if any source or header is newer; return its path."""
+    """Compile what is older than any source or header, the library and the
+    host extension; return the library's path.  The library does not need the
+    extension: it is in place where compiling that one fails (which raises)."""
     deps = [os.path.join(CSRC, f) for f in os.listdir(CSRC)]
     deps.append(os.path.join(os.path.dirname(HERE), "include", "w4a16.h"))
     deps.append(os.path.abspath(__file__))
-    if not force and not _stale(LIB, deps) and not _stale(MARSHAL, deps):
-        return LIB
+    os.makedirs(OUT_DIR, exist_ok=True)
+    with cf.ThreadPoolExecutor(max_workers=1) as ex:
+        marshal = ex.submit(build_marshal) if force or _stale(MARSHAL, deps) else None
+        if force or _stale(LIB, deps):
+            build_library(verbose, extra_flags)
+        if marshal:
+            marshal.result()
+    return LIB
+
+
+def build_library(verbose: bool = False, extra_flags=()) -> None:
+    """Compile and link libw4a16.so."""
     obj_dir = os.path.join(OUT_DIR, "obj")
     os.makedirs(obj_dir, exist_ok=True)
 
@@ -78,17 +90,14 @@ def build(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
             print(r.stdout + r.stderr)
         return obj
 
-    with cf.ThreadPoolExecutor(max_workers=len(SOURCES) + 1) as ex:
-        marshal = ex.submit(build_marshal)
+    with cf.ThreadPoolExecutor(max_workers=len(SOURCES)) as ex:
         objs = list(ex.map(compile_one, SOURCES))
-        marshal.result()
     tmp = LIB + ".tmp.%d" % os.getpid()
     cmd = [nvcc()] + ARCH + ["-shared", "-cudart", "static", "-o", tmp] + objs
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError("link failed:\n%s%s" % (r.stdout, r.stderr))
     os.replace(tmp, LIB)
-    return LIB
 
 
 if __name__ == "__main__":
