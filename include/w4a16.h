@@ -498,9 +498,10 @@ int kv4_gather(const uint8_t *cache, int64_t num_blocks, int block_size,
  *         separate scratch.
  * Queries, statistics and sums are exact or binary32.  The streaming kernel
  * takes K and V as they are in the cache, the one for long pieces rounds each
- * of their values once to binary16 (2^-12 of it at most).  The weights of the
- * sum over V, times the scales of V, are rounded to binary16: to 2^-11, or to
- * 2^-31 of the row's largest such product where that is more.
+ * of their values once to binary16 (2^-11 of it at most, so a score by up to
+ * 2^-11 of scale * sum |q K|).  The weights of the sum over V, times the scales
+ * of V, are rounded to binary16: to 2^-11, or to 2^-30 of the row's largest such
+ * product where that is more.
  * Hq is a multiple of Hkv; requests <= 4096; T = 0 launches nothing.
  */
 int64_t kv4_attention_scratch_bytes(int Hq, int Hkv, int D);

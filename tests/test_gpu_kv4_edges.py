@@ -85,6 +85,42 @@ def test_weights_before_a_far_move_of_the_reference_count(Hq, Hkv, D, new, jump,
     assert w4.w4a16_check_device_error() == 0
 
 
+@pytest.mark.parametrize("Hq,Hkv,D", [(32, 16, 256), (32, 16, 128), (48, 24, 64)])
+@pytest.mark.parametrize("new", [1, 90])
+def test_scores_of_keys_at_the_middle_between_two_numbers(Hq, Hkv, D, new):
+    # 3 * 1370 and 3 * 1374 lie half a unit of binary16 from its numbers, the first
+    # is rounded up and the second down: each by 2^-11 of itself, the most there is.
+    # Scores of 2055 and 2061, so the smaller weights grow by up to exp(2 * 2^-11 *
+    # 2061) where keys are rounded; the streaming kernel takes them as they are.
+    torch, w4 = cuda_or_skip()
+    end, bs = 100, 16
+    c = ref.Cache(-(-end // bs), Hkv, bs, D)
+    one, rng = np.ones(D // 64, np.float16), np.random.default_rng(D)
+    V = np.zeros((end, Hkv, D))
+    for j in range(end):
+        for h in range(Hkv):
+            kc = np.zeros(D, np.uint8)
+            kc[0] = 3
+            c.put(0, j, h, kc, one * np.float16((1374 if j % 2 else 1370) / 1024), one * 0)
+            V[j, h] = 0 if j % 2 else rng.integers(0, 16, D)
+            c.put(1, j, h, V[j, h].astype(np.uint8), one, one * 0)
+    score = 512.0 * 3 / 1024 * np.where(np.arange(end) % 2, 1374, 1370)
+    q = torch.zeros(new, Hq, D, dtype=torch.bfloat16, device="cuda")
+    q[..., 0] = 512
+    out = w4.kv4_attention(q, torch.tensor(c.raw, device="cuda"), _i32(torch, [list(range(-(-end // bs)))]),
+                           _i32(torch, [end]), _i32(torch, [0, new]), w4.kv4_attention_scratch(Hq, Hkv, D), scale=1.0,
+                           max_new=new).double().cpu().numpy()
+    e = ((2.0 ** -11 if new > 1 else 0) + 2.0 ** -20) * score.max()
+    for t in range(new):
+        see = end - new + t + 1
+        w = np.exp(score[:see] - score[:see].max())
+        o = np.einsum("j,jhd->hd", w / w.sum(), V[:see])[:, None]
+        got = out[t].reshape(Hkv, Hq // Hkv, D)
+        # (values and weights to binary16, the result to BF16)
+        assert (np.abs(got - o) <= (np.expm1(2 * e) + 2.0 ** -10 + 2.0 ** -8 * np.exp(2 * e)) * o + 1e-30).all()
+    assert w4.w4a16_check_device_error() == 0
+
+
 @pytest.mark.parametrize("Hq,Hkv,D", [(32, 16, 256), (4, 2, 128), (48, 24, 64)])
 @pytest.mark.parametrize("new", [1, 130])
 def test_lengths_out_of_range_are_reported(Hq, Hkv, D, new):
