@@ -52,9 +52,15 @@ __device__ __forceinline__ uint4 pack8(const float (&x)[8]) {
     return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
+// Of each pair of BF16 the smaller, or a NaN where there is one.
 __device__ __forceinline__ uint32_t min_bf16x2(uint32_t a, uint32_t b) {
     uint32_t d;
-    asm("min.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+    asm("min.NaN.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+    return d;
+}
+__device__ __forceinline__ float min_or_nan(float a, float b) {
+    float d;
+    asm("min.NaN.f32 %0, %1, %2;" : "=f"(d) : "f"(a), "f"(b));
     return d;
 }
 // 1 / s rounded, for every binary16 s > 0: one Newton step from the
@@ -73,52 +79,80 @@ __device__ __forceinline__ float divided(float x, float b, float y) {
     return fmaf(fmaf(-q, b, x), y, q);
 }
 
-// Quantises this lane's 8 BF16 elements (8 lanes hold a group of 64) and
-// stores the code word and, from the group's first lane, the parameters, at
-// `words` and `params` of the row.  The extremes are found as BF16 pairs (a
-// minimum of x and one of -x).  Quotients are the correctly rounded ones of
-// binary32.  Adding 1.5 2^23 rounds to the nearest whole number, ties to even,
-// and leaves it in the low bits.  A group whose scale is at its limit (values
-// beyond 15 x 65504, infinities) takes the plain division.
-__device__ __forceinline__ void quantise_store(const uint4 raw, unsigned char *words, unsigned char *params, int l,
-                                               bool store) {
+// The least element, at most 0, and the greatest, at least 0, of a group of
+// 64: 8 in each of the 8 lanes (`lanes` are those that take part).  They are
+// found as BF16 pairs (a minimum of x and one of -x), and are NaN if the group
+// holds one.
+__device__ __forceinline__ void extremes(const uint4 raw, unsigned lanes, float &lo, float &hi) {
     const uint32_t low = min_bf16x2(min_bf16x2(raw.x, raw.y), min_bf16x2(raw.z, raw.w));
     const uint32_t neg = min_bf16x2(min_bf16x2(raw.x ^ 0x80008000u, raw.y ^ 0x80008000u),
                                     min_bf16x2(raw.z ^ 0x80008000u, raw.w ^ 0x80008000u));
     uint32_t both = min_bf16x2(__byte_perm(low, neg, 0x5410), __byte_perm(low, neg, 0x7632));
 #pragma unroll
-    for (int o = 1; o < 8; o <<= 1) both = min_bf16x2(both, __shfl_xor_sync(0xffffffffu, both, o));
-    const float lo = fminf(__uint_as_float(both << 16), 0.f), hi = fmaxf(-__uint_as_float(both & 0xffff0000u), 0.f);
-    const __half sh = __float2half_rn(fminf(divided(__fsub_rn(hi, lo), 15.f, 1.f / 15.f), 65504.f));
+    for (int o = 1; o < 8; o <<= 1) both = min_bf16x2(both, __shfl_xor_sync(lanes, both, o));
+    lo = min_or_nan(__uint_as_float(both << 16), 0.f);
+    hi = -min_or_nan(__uint_as_float(both & 0xffff0000u), 0.f);
+}
+__device__ __forceinline__ __half scale_of(float lo, float hi) {  // of NaN: the limit
+    return __float2half_rn(fminf(divided(__fsub_rn(hi, lo), 15.f, 1.f / 15.f), 65504.f));
+}
+
+// The code word and the parameters of a group whose scale is at its limit
+// (values beyond 15 x 65504, infinities: the plain division) or that holds a
+// NaN (which counts as zero).  On its own: its registers are not the caller's.
+__device__ __noinline__ uint2 quantise_rare(uint4 raw, float lo, float hi) {
+    if (lo != lo) {  // (in all lanes of the group)
+        auto clean = [](uint32_t w) -> uint32_t { return w & ~__vcmpgtu2(w & 0x7fff7fffu, 0x7f807f80u); };
+        raw = make_uint4(clean(raw.x), clean(raw.y), clean(raw.z), clean(raw.w));
+        extremes(raw, 0xffu << (threadIdx.x & 24), lo, hi);
+    }
+    const __half sh = scale_of(lo, hi);
     const float s = __half2float(sh);
     uint32_t word = 0;
     float z = 0.f;
-    if (s >= 65504.f) {
+    if (s > 0.f) {
         float x[8];
         unpack8(raw, x);
         z = __fadd_rn(fminf(fmaxf(rintf(__fdiv_rn(-lo, s)), 0.f), 15.f), 0.f);  // never -0
-#pragma unroll 1
+#pragma unroll
         for (int i = 0; i < 8; ++i) {
-            const float v = i < 4 ? (i < 2 ? (i ? x[1] : x[0]) : (i == 2 ? x[2] : x[3]))
-                                  : (i < 6 ? (i == 4 ? x[4] : x[5]) : (i == 6 ? x[6] : x[7]));
-            const float c = fminf(fmaxf(__fadd_rn(rintf(__fdiv_rn(v, s)), z), 0.f), 15.f);
+            const float c = fminf(fmaxf(__fadd_rn(rintf(__fdiv_rn(x[i], s)), z), 0.f), 15.f);
             word |= static_cast<uint32_t>(c) << (4 * i);
         }
+    }
+    return make_uint2(word, static_cast<uint32_t>(__half_as_ushort(sh)) |
+                                static_cast<uint32_t>(__half_as_ushort(__float2half_rn(z))) << 16);
+}
+
+// Quantises this lane's 8 BF16 elements (8 lanes hold a group of 64) and
+// stores the code word and, from the group's first lane, the parameters, at
+// `words` and `params` of the row.  Quotients are the correctly rounded ones of
+// binary32.  Adding 1.5 2^23 rounds to the nearest whole number, ties to even,
+// and leaves it in the low bits.
+__device__ __forceinline__ void quantise_store(const uint4 raw, unsigned char *words, unsigned char *params, int l,
+                                               bool store) {
+    float lo, hi;
+    extremes(raw, 0xffffffffu, lo, hi);
+    const __half sh = scale_of(lo, hi);
+    const float s = __half2float(sh);
+    uint32_t word = 0, sz = __half_as_ushort(sh);
+    if (s >= 65504.f) {
+        const uint2 r = quantise_rare(raw, lo, hi);
+        word = r.x;
+        sz = r.y;
     } else if (s > 0.f) {
         float x[8];
         unpack8(raw, x);
         const float inv = reciprocal(s);
         auto whole = [&](float v) -> int { return __float_as_int(__fadd_rn(divided(v, s, inv), 12582912.f)); };
         const int zi = __vimin_s32_relu(whole(-lo) - 0x4b400000, 15);
-        z = static_cast<float>(zi);
+        sz |= static_cast<uint32_t>(__half_as_ushort(__float2half_rn(static_cast<float>(zi)))) << 16;
 #pragma unroll
         for (int i = 7; i >= 0; --i) word = word * 16 + __vimin_s32_relu(whole(x[i]) + (zi - 0x4b400000), 15);
     }
     if (!store) return;
     *reinterpret_cast<uint32_t *>(words) = word;
-    if ((l & 7) == 0)
-        *reinterpret_cast<uint32_t *>(params) = static_cast<uint32_t>(__half_as_ushort(sh)) |
-                                                static_cast<uint32_t>(__half_as_ushort(__float2half_rn(z))) << 16;
+    if ((l & 7) == 0) *reinterpret_cast<uint32_t *>(params) = sz;
 }
 
 // A task is U x 32 / LPH heads of one token, in the order q heads, k heads, v

@@ -448,6 +448,8 @@ int w4a16_qk_norm_rope(const uint16_t *q, int64_t q_stride, const uint16_t *k,
  *   s = fl16((max(x, 0) - min(x, 0)) / 15), at most 65504
  *   z = rint(-min(x, 0) / s);  code = clamp(rint(x / s) + z, 0, 15)
  * (s = 0: zero, code 0), divisions and sums in binary32, one by one.
+ * The cache holds no NaN: a NaN counts as 0, whether it is in k, in v or comes
+ * of the norm; infinities take the scale's limit.
  *   v     : bfloat16, T rows of Hkv heads, v_stride elements apart
  *   slots : int64 [T]; a negative one stores nothing; one past the cache
  *           stores nothing and sets the device status.  Two tokens of a call

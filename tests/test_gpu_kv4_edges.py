@@ -6,7 +6,7 @@ import pytest
 from tests import kv4_helpers as ref
 from tests.gpu_helpers import cuda_or_skip
 from tests.test_gpu_kv4_attention import _check, _problem
-from tests.test_gpu_kv4_cache import _i32
+from tests.test_gpu_kv4_cache import _i32, _qkv
 
 pytestmark = pytest.mark.gpu
 
@@ -153,3 +153,31 @@ def test_lengths_out_of_range_are_reported(Hq, Hkv, D, new):
     assert status(cu=(0, 2 * new, new, 3 * new))[0] == 6
     assert status(cu=(-1, new, 2 * new, 3 * new))[0] == 6
     assert status()[0] == 0 and torch.equal(status()[1], whole)
+
+
+@pytest.mark.parametrize("T,Hkv,D", [(5, 2, 128), (9, 1, 64), (3, 2, 256), (2000, 8, 256), (1200, 16, 128), (5000, 8, 64)])
+@pytest.mark.parametrize("norm", [False, True])
+def test_nan_keys_and_values_count_as_zero(T, Hkv, D, norm):
+    torch, w4 = cuda_or_skip()
+    (q, k, v), _ = _qkv(torch, T, Hkv, Hkv, D, T)
+    g = torch.Generator(device="cuda").manual_seed(D)
+    w = torch.ones(D, dtype=torch.bfloat16, device="cuda") if norm else None
+    slots = torch.arange(T, device="cuda")
+    a, b = (w4.kv4_cache(T // 16 + 1, Hkv, 16, D) for _ in range(2))
+    nan = torch.rand(v.shape, device="cuda", generator=g) < 0.02
+    nan[0, 0, :64] = True                                    # a whole group
+    v[1, 0, 3], v[2, 0, 5] = 3e38, float("inf")              # scales at their limit
+    nan[1, 0, 4] = nan[2, 0, 4] = True
+    sign = torch.where(torch.rand(v.shape, device="cuda", generator=g) < 0.5, -1.0, 1.0).to(torch.bfloat16)
+    bad = torch.full_like(sign, float("nan")).copysign(sign)
+    if norm:      # one NaN makes its head's norm NaN: all of it counts as zero
+        head = nan[..., :1] & (torch.arange(T, device="cuda") % 3 == 0)[:, None, None]
+        k1, k0 = torch.where(head & (torch.arange(D, device="cuda") == 7), bad, k), torch.where(head, 0, k)
+    else:
+        k1, k0 = torch.where(nan, bad, k), torch.where(nan, 0, k)
+    w4.kv4_append(k1, torch.where(nan, bad, v), a, slots, q=q if norm else None, k_weight=w)
+    w4.kv4_append(k0, torch.where(nan, 0, v), b, slots, q=q if norm else None, k_weight=w)
+    torch.cuda.synchronize()
+    assert torch.equal(a, b)
+    assert torch.isfinite(w4.kv4_gather(a, slots)[1].float()).all()
+    assert w4.w4a16_check_device_error() == 0
