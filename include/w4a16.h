@@ -368,10 +368,12 @@ int w4a16_graph_destroy(w4a16_graph_t graph);
  *   [16 D, 17 D)  binary16 pairs (scale, zero) of K [D / 64][16 tokens][2]
  *   [17 D, 18 D)  the same of V
  * and a value is (code - zero) * scale: one scale and zero per 64 elements of
- * a token's head (D = 256: 288 bytes for a token's K and V of one head, where
- * BF16 takes 1024).  A SLOT is block * block_size + offset: where a token
- * lies.  block_size is 16, 32, 64, 128 or 256; D (head dimension) is 64, 128
- * or 256.
+ * a token's head, the zero a whole number 0 .. 15 (D = 256: 288 bytes for a
+ * token's K and V of one head, where BF16 takes 1024).  A cache that another
+ * program fills has to keep to that: what the kernels read from a zero between
+ * whole numbers differs from one to the other.  A SLOT is block * block_size +
+ * offset: where a token lies.  block_size is 16, 32, 64, 128 or 256; D (head
+ * dimension) is 64, 128 or 256.
  *
  * Values that cannot be checked on the host (lengths, block ids, slots,
  * positions: device arrays) are checked by the kernels: what is out of range
