@@ -86,6 +86,15 @@ float real(PyObject *o) {
     return static_cast<float>(PyFloat_AS_DOUBLE(o));
 }
 
+int truth(PyObject *o) {
+    const int v = PyObject_IsTrue(o);
+    if (v < 0) {
+        PyErr_Clear();
+        throw Unfit();
+    }
+    return v;
+}
+
 // The stream to launch on, with its device current while this lives.
 struct Launch {
     std::optional<c10::cuda::CUDAGuard> guard;
@@ -153,9 +162,10 @@ int rope(PyObject *const *a) {
     const Table t(a[4], a[5], device, q.T);
     uint16_t *oq = address<uint16_t>(a[6], H, device, q.T * q.H * q.D), *ok = address<uint16_t>(a[7], H, device, k.T * k.H * k.D);
     const float eps = real(a[8]), offset = real(a[9]);
+    const int interleaved = truth(a[10]);
     const Launch l(device, a[11]);
     return p_rope(q.p, q.stride, k.p, k.stride, wq, wk, t.p, t.rows, small(t.rot), t.positions, oq, ok, q.T, small(q.H),
-                  small(k.H), small(q.D), eps, offset, PyObject_IsTrue(a[10]), l.stream);
+                  small(k.H), small(q.D), eps, offset, interleaved, l.stream);
 }
 
 // k, v, cache, slots, q, q_weight, k_weight, cos_sin, positions, q_out, eps, weight_offset, interleaved, stream
@@ -175,10 +185,10 @@ int append(PyObject *const *a) {
     const uint16_t *wq = address<uint16_t>(a[5], H, c.device, c.D), *wk = address<uint16_t>(a[6], H, c.device, c.D);
     const Table t(a[7], a[8], c.device, k.T);
     const float eps = real(a[10]), offset = real(a[11]);
+    const int interleaved = truth(a[12]);
     const Launch l(c.device, a[13]);
     return p_append(q.p, q.stride, k.p, k.stride, v.p, v.stride, wq, wk, t.p, t.rows, small(t.rot), t.positions, slots, out,
-                    c.p, c.blocks, c.bs, k.T, small(q.H), small(c.Hkv), small(c.D), eps, offset, PyObject_IsTrue(a[12]),
-                    l.stream);
+                    c.p, c.blocks, c.bs, k.T, small(q.H), small(c.Hkv), small(c.D), eps, offset, interleaved, l.stream);
 }
 
 // cache, slots, k, v, stream

@@ -181,3 +181,13 @@ def test_nan_keys_and_values_count_as_zero(T, Hkv, D, norm):
     assert torch.equal(a, b)
     assert torch.isfinite(w4.kv4_gather(a, slots)[1].float()).all()
     assert w4.w4a16_check_device_error() == 0
+
+
+def test_flags_that_have_no_truth_value_are_refused():
+    torch, w4 = cuda_or_skip()
+    (q, k, v), _ = _qkv(torch, 2, 2, 2, 64, 1)
+    two = np.array([True, False])
+    with pytest.raises(ValueError, match="truth value"):
+        w4.w4a16_qk_norm_rope(q, k, None, None, None, None, interleaved=two)
+    with pytest.raises(ValueError, match="truth value"):
+        w4.kv4_append(k, v, w4.kv4_cache(1, 2, 16, 64), torch.arange(2, device="cuda"), interleaved=two)
