@@ -988,7 +988,7 @@ int64_t kv4_attention_scratch(int, int, int D) {
 cudaError_t launch_kv4_attention(const Kv4AttnArgs &args, int D, cudaStream_t st, const DeviceInfo &dev) {
     Kv4AttnArgs a = args;
     const int G = a.Hq / a.Hkv;
-    int64_t rows = a.max_new * G;  // the most a request has
+    int64_t rows = (a.max_new < a.T ? a.max_new : a.T) * G;  // the most a request has
     const int64_t few = stream_rows(a.requests * a.Hkv, D, dev);
     a.rows_least = 1;
     a.rows_most = 0x7fffffff;

@@ -191,3 +191,14 @@ def test_flags_that_have_no_truth_value_are_refused():
         w4.w4a16_qk_norm_rope(q, k, None, None, None, None, interleaved=two)
     with pytest.raises(ValueError, match="truth value"):
         w4.kv4_append(k, v, w4.kv4_cache(1, 2, 16, 64), torch.arange(2, device="cuda"), interleaved=two)
+
+
+@pytest.mark.parametrize("Hq,Hkv,D", [(32, 16, 256), (32, 16, 128), (48, 24, 64)])
+def test_any_upper_bound_of_new_tokens_chooses_alike(Hq, Hkv, D):
+    # no more than there are rows of q: the same bits for bounds past that
+    torch, w4 = cuda_or_skip()
+    dev, host = _problem(torch, [140, 60], [130, 30], Hq, Hkv, D, 16, D)
+    kw = dict(scratch=w4.kv4_attention_scratch(Hq, Hkv, D))
+    want = w4.kv4_attention(**dev, **kw, max_new=160)
+    for most in (1 << 20, 1 << 31, 1 << 62, (1 << 63) - 1):
+        assert torch.equal(want, w4.kv4_attention(**dev, **kw, max_new=most))
