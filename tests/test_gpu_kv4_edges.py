@@ -202,3 +202,38 @@ def test_any_upper_bound_of_new_tokens_chooses_alike(Hq, Hkv, D):
     want = w4.kv4_attention(**dev, **kw, max_new=160)
     for most in (1 << 20, 1 << 31, 1 << 62, (1 << 63) - 1):
         assert torch.equal(want, w4.kv4_attention(**dev, **kw, max_new=most))
+
+
+@pytest.mark.parametrize("requests,Hq,Hkv,D", [(700, 4, 1, 256), (700, 4, 1, 128), (700, 4, 2, 64), (4096, 4, 1, 256),
+                                               (4096, 8, 1, 64)])
+@pytest.mark.parametrize("window,sinks", [(0, 0), (30, 2)])
+def test_pieces_of_many_requests(requests, Hq, Hkv, D, window, sinks):
+    # more than are put in order of their length, and as many as a call takes
+    torch, w4 = cuda_or_skip()
+    rng = np.random.default_rng(requests + D)
+    g = torch.Generator(device="cuda").manual_seed(D)
+    new = rng.integers(0, 9, requests)
+    new[[3, requests - 1]] = 150, 70
+    ends = new + rng.integers(0, 90, requests)
+    held = -(-ends // 16)
+    blocks = int(held.sum())
+    cache = torch.randint(0, 256, (blocks, Hkv, 1, 18 * D), device="cuda", generator=g, dtype=torch.uint8)
+    shape = (blocks, Hkv, 1, D // 2)
+    par = torch.stack([(0.05 + 0.2 * torch.rand(shape, device="cuda", generator=g)).half(),
+                       torch.randint(0, 16, shape, device="cuda", generator=g).half()], -1)
+    cache[..., 16 * D:] = par.flatten(-2).view(torch.uint8)
+    ids = rng.permutation(blocks)
+    table = np.full((requests, int(held.max())), -1)
+    table[np.arange(table.shape[1])[None] < held[:, None]] = ids
+    cu = np.concatenate([[0], np.cumsum(new)])
+    q = torch.randn(int(cu[-1]), Hq, D, device="cuda", generator=g).to(torch.bfloat16)
+    out = w4.kv4_attention(q, cache, _i32(torch, table), _i32(torch, ends), _i32(torch, cu),
+                           w4.kv4_attention_scratch(Hq, Hkv, D), window=window, sinks=sinks, max_new=150)
+    # some of them against the reference
+    pick = sorted({0, 1, 3, requests - 1, *rng.integers(0, requests, 25).tolist()})
+    c = ref.Cache(blocks, Hkv, 16, D)
+    c.raw = cache.cpu().numpy()
+    rows = np.concatenate([np.arange(cu[b], cu[b + 1]) for b in pick])
+    host = (q.double().cpu().numpy()[rows], c, table[pick], ends[pick], np.concatenate([[0], np.cumsum(new[pick])]))
+    _check(w4, out[torch.tensor(rows, device="cuda")], host, D ** -0.5, window, sinks)
+    assert torch.isfinite(out).all()
