@@ -70,6 +70,8 @@ constexpr int warp_rows(int D) { return D == 256 ? 128 : D == 128 ? 192 : 256; }
 constexpr int TEAM_RATIO = 5;         // warps to a segment up to which a warp is a team of its own
 constexpr float NONE = -1e30f;        // reference of a row that has seen no key
 
+// 2^x by the hardware's approximation (2 ulp): a weight is rounded to 11 bits
+// after it.
 __device__ __forceinline__ float ex2(float x) {
     float y;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));

@@ -244,6 +244,8 @@ __device__ __forceinline__ void arrived(uint32_t (&x)[32]) {
                  : "memory");
 }
 
+// 2^x by the hardware's approximation (2 ulp): a weight is rounded to 11 bits
+// after it.
 __device__ __forceinline__ float ex2(float x) {
     float y;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));

@@ -64,7 +64,8 @@ __device__ __forceinline__ float min_or_nan(float a, float b) {
     return d;
 }
 // 1 / s rounded, for every binary16 s > 0: one Newton step from the
-// approximate reciprocal, compared with __frcp_rn for all of them.
+// approximate reciprocal (the tests compare the codes of all scales with those
+// of the division).
 __device__ __forceinline__ float reciprocal(float s) {
     float y;
     asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(s));
