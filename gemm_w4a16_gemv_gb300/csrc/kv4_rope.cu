@@ -20,10 +20,12 @@
 // loads first: with U = 4 each lane has 64 bytes under way and a token's
 // cosines, sines and addresses are found once for them; with few tokens U = 1
 // spreads the heads over more warps.  Measured: 4099 tokens of 40 heads of 128,
-// norm and rotation, 22.4 us (3.8 TB/s, issue slots 65% busy; four CTAs of 256
+// norm and rotation, 22.2 us (3.9 TB/s, issue slots 65% busy; four CTAs of 256
 // threads per SM hold it best, with registers for three or five it was 28.4
 // and 39.7 when it was 25.5); 8191 tokens of 8 heads of 256 appended and read
-// back 42.0 us (4.1 TB/s, issue slots 75% busy).
+// back 41.5 us (4.1 TB/s, issue slots 78% busy); norm, rotation and write of
+// 8191 tokens of 16 query heads and 8 of k and v in one pass 82.8 us (2.8 TB/s;
+// its registers spill).
 #include "common.cuh"
 #include "kernels.h"
 #include "kv4.cuh"
@@ -100,7 +102,8 @@ __device__ __forceinline__ __half scale_of(float lo, float hi) {  // of NaN: the
 
 // The code word and the parameters of a group whose scale is at its limit
 // (values beyond 15 x 65504, infinities: the plain division) or that holds a
-// NaN (which counts as zero).  On its own: its registers are not the caller's.
+// NaN (which counts as zero).  A function of its own, whose registers are not
+// the caller's: append and read-back of 8191 tokens 41.5 us, inlined 42.6.
 __device__ __noinline__ uint2 quantise_rare(uint4 raw, float lo, float hi) {
     if (lo != lo) {  // (in all lanes of the group)
         auto clean = [](uint32_t w) -> uint32_t { return w & ~__vcmpgtu2(w & 0x7fff7fffu, 0x7f807f80u); };

@@ -15,9 +15,11 @@
 // histograms) goes through distributed shared memory, a cluster barrier per
 // exchange.  Nothing is sorted but short lists.  Rows past what is resident (at most
 // 38 clusters of 8 CTAs, two to an SM by registers and by shared memory) follow in
-// waves.  us for 262144 BF16 logits, one row and 128 rows: greedy 5.4 and 30,
-// top-k 40 with or without top-p 10 and 49, neither 11.7 and 65, top-p alone 31
-// and 174 (the masses and the cut), a mixture of settings 11.1 and 100.
+// waves.  us for 262144 BF16 logits (a bell and 40 that stand out), one row and
+// 128 rows: greedy 5.3 and 30, top-k 40 10.2 and 48 (with top-p 0.92 10.7 and
+// 50), top-k 300 22.5 and 122, min-p 0.02 6.9 and 35, none of them 10.7 and 58,
+// top-p alone 39 and 217 at 0.92, 31 and 166 at 0.5 (the masses and the cut), a
+// mixture of settings 11.4 and 102; of binary32 logits the mixture 12.8 and 174.
 //
 // Small top-k (up to 256): a histogram of the threads' largest logits gives a
 // bin that at least k of them reach, so everything kept lies in the bins up
