@@ -109,7 +109,8 @@ __device__ __forceinline__ uint32_t plus_zero_bf16x2(uint32_t a) {
 // correction (P. Markstein, "Computation of elementary functions on the IBM
 // RISC System/6000 processor", 1990): with y the rounded reciprocal and q = l y
 // rounded, the remainder l - q T is exact in a fused multiply-add and q + r y
-// rounds to the quotient; else by division.
+// rounds to the quotient; else, and for a largest quotient of 10^6 or more, whose
+// neighbours are no longer close on the scale of the exponential, by division.
 enum { MODE_ONE, MODE_FUSED, MODE_DIVIDE };
 struct Masses {
     float T, inv, top, half_top, per_half;
@@ -118,7 +119,8 @@ struct Masses {
         inv = __frcp_rn(T);
         top = __fdiv_rn(top_l, T);
         per_half = fminf(2.f * BINS_PER_UNIT * inv, 2e30f);
-        mode = T == 1.f ? MODE_ONE : T > 1e-15f && T < 1e15f && fabsf(top_l) < 1e15f ? MODE_FUSED : MODE_DIVIDE;
+        mode = T == 1.f ? MODE_ONE
+               : T > 1e-15f && T < 1e15f && fabsf(top_l) < 1e15f && fabsf(top) < 1e6f ? MODE_FUSED : MODE_DIVIDE;
     }
     // (max - l) / T in bins, not rounded to one; rises as l falls.  From half the
     // difference, which no two finite logits take past binary32's range.
@@ -129,11 +131,15 @@ struct Masses {
     template <int MODE>
     __device__ __forceinline__ float scaled(float l) const {
         float x = l;
-        if (MODE != MODE_ONE && !(depth(l) < NO_MASS)) return 0.f;  // (-infinity, or a quotient out of range)
         if (MODE == MODE_FUSED) {
+            if (!(depth(l) < NO_MASS)) return 0.f;  // (-infinity, or a quotient out of range)
             const float q = l * inv;
             x = fmaf(fmaf(-q, T, l), inv, q);
-        } else if (MODE == MODE_DIVIDE) x = __fdiv_rn(l, T);
+        } else if (MODE == MODE_DIVIDE) {
+            // (quotients may lie so far apart that ones of different depth are equal)
+            const float below = __fsub_rn(__fdiv_rn(l, T), top);
+            return below > -40.f ? expf(below) * UNIT : 0.f;
+        }
         return expf(__fsub_rn(x, top)) * UNIT;
     }
     // The whole number nearest to t <= 2^40 (ties to even) as hi 2^20 + lo: the

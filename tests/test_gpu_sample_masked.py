@@ -80,3 +80,37 @@ def test_temperatures_as_large_as_the_logits(T, k):
     wide = np.flatnonzero(w > 1e-4)
     got = _tokens(torch, w4, torch.tensor(x, dtype=torch.float32, device="cuda"), (w.cumsum() - w / 2)[wide], T, k, 1.0)
     assert np.array_equal(got, wide)
+
+
+@pytest.mark.parametrize("V", [40, 3000, 262144])
+@pytest.mark.parametrize("bits", [30, 100])
+@pytest.mark.parametrize("T", [0.9, 0.95, 0.6])
+@pytest.mark.parametrize("k,p", [(0, 1.0), (9, 1.0), (300, 1.0), (0, 0.5), (300, 0.5)])
+def test_quotients_whose_rounding_is_wider_than_the_exponentials(V, bits, T, k, p):
+    # logits just below a power of two, in steps of 64 and more: l / T lies above it,
+    # where numbers are twice as far apart, so tokens of different logits have the
+    # same mass and a step further they have none (whole numbers, exact)
+    torch, w4 = cuda_or_skip()
+    rng = np.random.default_rng(V)
+    step = rng.integers(0, 12, V)
+    step[:4] = 0, 1, 2, 3
+    for top in range(2 ** 24 - 2 ** 17, 2 ** 24):     # the two largest have the same quotient
+        x = ((top - step) * 2.0 ** (bits - 24)).astype(np.float32)
+        q = x / np.float32(T)
+        if q[0] == q[1]:
+            break
+    x[V // 2:] /= 2
+    q = x / np.float32(T)
+    mass = np.rint(2.0 ** 40 * np.exp((q - q.max()).astype(np.float64)))
+    order = np.argsort(-x, kind="stable")
+    w = mass[order]
+    w[k if k else V:] = 0
+    if p < 1:
+        before = np.cumsum(w) - w
+        w[before >= max(np.trunc(w.sum() * p), 1)] = 0
+    kept = np.zeros(V)
+    kept[order] = w
+    edge = kept.cumsum()
+    u = np.float32(np.linspace(0.0, 0.9999, 60))
+    want = np.searchsorted(edge, np.trunc(edge[-1] * u.astype(np.float64)), side="right")
+    assert np.array_equal(_tokens(torch, w4, torch.tensor(x, device="cuda"), u, T, k, p), want)
