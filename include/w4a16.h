@@ -571,6 +571,10 @@ int w4a16_check_device_error(void *stream);
  *      them, so the producers' waits for free stages run out while their
  *      copies are issued: each producer then waits for its own copies to
  *      land before the launch ends (W4A16_ERR_TIMEOUT as for flag 1).
+ * kv4_attention takes both: with 1 the streaming kernel issues no copy and the
+ * one for long pieces announces no item to its roles, with 2 the latter forms
+ * its operands and issues no product (the streaming kernel, whose warps copy
+ * for themselves, does not know 2).
  * The flags are a host-side setting passed to each later launch (a CUDA
  * graph keeps the flags it was captured with).  Not for production use.
  * Returns W4A16_OK, or W4A16_ERR_INVALID_ARG for an unknown flag.
