@@ -19,7 +19,7 @@
 // SM, and leaves room for two buffers of each operand.  One CTA of the pair
 // issues the products of both.  Measured on 6491 new tokens in three requests
 // with up to 6000 tokens before them, 16 heads of 256 on 8: single CTAs 455 us,
-// pairs 296 us, 1140 TFLOP/s.  What bounds it now is the softmax: 2700 cycles a
+// pairs 297 us, 1136 TFLOP/s.  What bounds it now is the softmax: 2700 cycles a
 // tile (4 x 32 keys, each 170 until the scores are there, 190 for the
 // reference, 250 for the weights), of which the exponentials are 512 per SM
 // quarter; the code is kept short (rolled loops, masks as 32-bit words),
