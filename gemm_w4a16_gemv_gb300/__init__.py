@@ -33,7 +33,9 @@ __all__ = [
     "w4a16_linear_chain", "w4a16_linear_chain_scratch_bytes", "chain_scratch", "w4a16_linear_chain_noalloc",
     "w4a16_graph_destroy", "W4A16Graph",
     "kv4_plan", "kv4_plan_buffers", "KV4Plan", "w4a16_qk_norm_rope", "kv4_append", "kv4_gather", "kv4_cache",
-    "kv4_attention", "kv4_attention_scratch", "kv4_attention_scratch_bytes", "w4a16_sample",
+    "kv4_attention", "kv4_attention_scratch", "kv4_attention_scratch_bytes",
+    "kv4_prefix_attention", "kv4_prefix_attention_scratch", "kv4_prefix_attention_scratch_bytes",
+    "kv4_bounds", "kv4_bounds_buffer", "kv4_select", "kv4_sparse_attention", "w4a16_sample",
     "library_path", "W4A16Error", "STATUS", "FMT_INT4", "FMT_FP4",
     "OUT_F32", "OUT_BF16",
 ]
@@ -91,6 +93,13 @@ SIGNATURES = {
     "kv4_attention_scratch_bytes": ([_INT, _INT, _INT], _I64),
     "kv4_attention": ([_P, _I64, _P, _I64, _INT, _P, _I64, _P, _P, _INT, _P, _I64, _INT, _INT, _INT, _F, _I64, _I64,
                        _I64, _P, _I64, _P], _INT),
+    "kv4_prefix_attention_scratch_bytes": ([_I64, _INT, _INT, _INT, _INT, _INT], _I64),
+    "kv4_prefix_attention": ([_P, _I64, _P, _I64, _INT, _P, _I64, _P, _P, _INT, _P, _P, _INT, _P, _I64, _INT, _INT, _INT,
+                              _F, _I64, _I64, _P, _I64, _P], _INT),
+    "kv4_bounds": ([_P, _I64, _INT, _P, _P, _I64, _INT, _INT, _P], _INT),
+    "kv4_select": ([_P, _I64, _P, _I64, _INT, _P, _I64, _P, _P, _INT, _I64, _INT, _INT, _INT, _INT, _INT, _INT, _P, _P,
+                    _P], _INT),
+    "kv4_sparse_attention": ([_P, _I64, _P, _I64, _INT, _P, _I64, _P, _P, _I64, _INT, _INT, _INT, _F, _P, _I64, _P], _INT),
     "w4a16_sample": ([_P, _INT, _I64, _I64, _I64, _P, _P, _P, _P, _P, _P, _P], _INT),
     "w4a16_check_device_error": ([_P], _INT),
     "w4a16_debug_inject": ([ctypes.c_uint], _INT),
@@ -772,6 +781,142 @@ def kv4_attention(q, cache, block_table, seq_lens, cu_new, scratch, out=None, sc
                  T * Hq * D, scratch, -1)
     _launch(dev, stream, lib().kv4_attention, a[0], a[1], a[2], blocks, bs, a[3], block_table.shape[1], a[4], a[5], B,
             a[6], T, Hq, Hkv, D, scale, window, sinks, max_new, a[7], scratch.numel())
+    return out
+
+
+def kv4_prefix_attention_scratch_bytes(T: int, requests: int, groups: int, Hq: int, Hkv: int, D: int) -> int:
+    """Bytes of scratch memory kv4_prefix_attention needs for up to T new
+    tokens, `requests` requests and `groups` groups."""
+    return int(lib().kv4_prefix_attention_scratch_bytes(int(T), int(requests), int(groups), int(Hq), int(Hkv), int(D)))
+
+
+def kv4_prefix_attention_scratch(T: int, requests: int, groups: int, Hq: int, Hkv: int, D: int, device=None) -> torch.Tensor:
+    """A zeroed scratch buffer for kv4_prefix_attention, for calls on one stream."""
+    return torch.zeros(max(kv4_prefix_attention_scratch_bytes(T, requests, groups, Hq, Hkv, D), 1), dtype=torch.uint8,
+                       device=device if device is not None else "cuda")
+
+
+_PREFIX_NAMES = ("q", "cache", "block_table", "seq_lens", "cu_new", "prefix_lens", "cu_groups", "out", "scratch")
+
+
+def kv4_prefix_attention(q, cache, block_table, seq_lens, cu_new, prefix_lens, cu_groups, scratch, out=None, scale=None,
+                         max_new=None, max_group=None, stream=None):
+    """kv4_attention for requests that share the first tokens of their
+    contexts: those from cu_groups[g] to cu_groups[g + 1] the first
+    prefix_lens[g], in the same pages.  What they share is attended to once for
+    a whole group.  `max_new` and `max_group`: the most new tokens any request,
+    any group has (T when None); `scratch` from kv4_prefix_attention_scratch.
+    Returns out bfloat16 [T, Hq, D]."""
+    dev = cache.device
+    T, Hq, D = q.shape
+    if out is None:
+        out = torch.empty(T, Hq, D, dtype=torch.bfloat16, device=dev)
+    scale = D ** -0.5 if scale is None else float(scale)
+    max_new = max(T, 1) if max_new is None else max_new
+    max_group = max(T, 1) if max_group is None else max_group
+    r = _extension().kv4_prefix_attention(q, cache, block_table, seq_lens, cu_new, prefix_lens, cu_groups, scratch, out,
+                                          scale, max_new, max_group, _handle(stream))
+    if r == 0:
+        return out
+    if r is not None:
+        _check(r)
+    blocks, bs, Hkv, Dc = _cache_shape(cache)
+    if Dc != D:
+        raise ValueError("q has heads of %d, the cache of %d" % (D, Dc))
+    B, N = seq_lens.numel(), prefix_lens.numel()
+    if block_table.dim() != 2 or block_table.shape[0] != B:
+        raise ValueError("block_table must be [%d, max_blocks]" % B)
+    a = _checked(dev, "rbiiiiihb", _PREFIX_NAMES, q, 0, cache, -1, block_table, -1, seq_lens, B, cu_new, B + 1,
+                 prefix_lens, N, cu_groups, N + 1, out, T * Hq * D, scratch, -1)
+    _launch(dev, stream, lib().kv4_prefix_attention, a[0], a[1], a[2], blocks, bs, a[3], block_table.shape[1], a[4], a[5], B,
+            a[6], a[7], N, a[8], T, Hq, Hkv, D, scale, max_new, max_group, a[9], scratch.numel())
+    return out
+
+
+def kv4_bounds_buffer(num_blocks: int, Hkv: int, D: int, device=None) -> torch.Tensor:
+    """Bounds of the pages of a cache, uint8 [num_blocks, Hkv, 2 D + 16], all zero."""
+    return torch.zeros(num_blocks, Hkv, 2 * D + 16, dtype=torch.uint8, device=device if device is not None else "cuda")
+
+
+def kv4_bounds(cache, slots, bounds, stream=None):
+    """The bounds of every page whose last slot is among `slots` (int64), from
+    the keys that the cache holds; call it after kv4_append with the same
+    slots.  Returns `bounds`."""
+    dev = cache.device
+    blocks, bs, Hkv, D = _cache_shape(cache)
+    r = _extension().kv4_bounds(cache, slots, bounds, _handle(stream))
+    if r == 0:
+        return bounds
+    if r is not None:
+        _check(r)
+    T = slots.numel()
+    a = _checked(dev, "blb", ("cache", "slots", "bounds"), cache, -1, slots, T, bounds, blocks * Hkv * (2 * D + 16))
+    _launch(dev, stream, lib().kv4_bounds, a[0], blocks, bs, a[1], a[2], T, Hkv, D)
+    return bounds
+
+
+_SELECT_NAMES = ("q", "bounds", "block_table", "seq_lens", "cu_new", "tables", "lens")
+
+
+def kv4_select(q, bounds, block_table, seq_lens, cu_new, block_size: int, top: int, first: int = 1, recent: int = 1,
+               tables=None, lens=None, stream=None):
+    """For every new token and key head a table of `top` pages at most: the
+    `first` first and the `recent` last ones that the token sees, and of those
+    between the ones with the highest scores by their bounds.  Returns
+    (tables int32 [T, Hkv, top], lens int32 [T]) for kv4_sparse_attention."""
+    dev = bounds.device
+    T, Hq, D = q.shape
+    blocks, Hkv, width = bounds.shape
+    if width != 2 * D + 16:
+        raise ValueError("bounds must be [num_blocks, Hkv, %d]" % (2 * D + 16))
+    if top < 1:
+        raise ValueError("top must be at least 1, got %d" % top)
+    if tables is None:
+        tables = torch.empty(T, Hkv, top, dtype=torch.int32, device=dev)
+    if lens is None:
+        lens = torch.empty(T, dtype=torch.int32, device=dev)
+    r = _extension().kv4_select(q, bounds, block_table, seq_lens, cu_new, block_size, top, first, recent, tables, lens,
+                                _handle(stream))
+    if r == 0:
+        return tables, lens
+    if r is not None:
+        _check(r)
+    B = seq_lens.numel()
+    if block_table.dim() != 2 or block_table.shape[0] != B:
+        raise ValueError("block_table must be [%d, max_blocks]" % B)
+    a = _checked(dev, "rbiiiii", _SELECT_NAMES, q, 0, bounds, -1, block_table, -1, seq_lens, B, cu_new, B + 1, tables,
+                 T * Hkv * top, lens, T)
+    _launch(dev, stream, lib().kv4_select, a[0], a[1], a[2], blocks, block_size, a[3], block_table.shape[1], a[4], a[5], B,
+            T, Hq, Hkv, D, top, first, recent, a[6], a[7])
+    return tables, lens
+
+
+_SPARSE_NAMES = ("q", "cache", "tables", "lens", "out", "scratch")
+
+
+def kv4_sparse_attention(q, cache, tables, lens, scratch, out=None, scale=None, stream=None):
+    """Attention of every new token q [T, Hq, D] over pages of its own: those
+    in its row of `tables` [T, Hkv, top] for the key head, of which it sees the
+    first lens[t] tokens (kv4_select writes both).  `scratch` from
+    kv4_attention_scratch.  Returns out bfloat16 [T, Hq, D]."""
+    dev = cache.device
+    T, Hq, D = q.shape
+    if out is None:
+        out = torch.empty(T, Hq, D, dtype=torch.bfloat16, device=dev)
+    scale = D ** -0.5 if scale is None else float(scale)
+    r = _extension().kv4_sparse_attention(q, cache, tables, lens, scratch, out, scale, _handle(stream))
+    if r == 0:
+        return out
+    if r is not None:
+        _check(r)
+    blocks, bs, Hkv, Dc = _cache_shape(cache)
+    if Dc != D:
+        raise ValueError("q has heads of %d, the cache of %d" % (D, Dc))
+    if tables.dim() != 3 or tables.shape[0] != T or tables.shape[1] != Hkv:
+        raise ValueError("tables must be [%d, %d, top]" % (T, Hkv))
+    a = _checked(dev, "rbiihb", _SPARSE_NAMES, q, 0, cache, -1, tables, -1, lens, T, out, T * Hq * D, scratch, -1)
+    _launch(dev, stream, lib().kv4_sparse_attention, a[0], a[1], a[2], blocks, bs, a[3], tables.shape[2], a[4], a[5], T, Hq,
+            Hkv, D, scale, a[6], scratch.numel())
     return out
 
 

@@ -64,6 +64,31 @@ int check_rows(const char *fn, const char *name, const void *p, int64_t stride, 
     return W4A16_OK;
 }
 
+// What the forms of attention share: a step's sizes, their limits, the scale, the
+// scratch.
+int check_batch(const char *fn, int requests, int64_t T, int Hq, int Hkv, int64_t max_blocks) {
+    if (requests < 1 || T < 0 || Hq < 1 || Hkv < 1 || max_blocks < 1)
+        return fail(W4A16_ERR_INVALID_ARG, "%s: requests=%d T=%lld Hq=%d Hkv=%d max_blocks=%lld", fn, requests,
+                    (long long)T, Hq, Hkv, (long long)max_blocks);
+    if (Hq % Hkv != 0) return fail(W4A16_ERR_INVALID_ARG, "%s: Hq=%d not a multiple of Hkv=%d", fn, Hq, Hkv);
+    return W4A16_OK;
+}
+int check_batch_limits(const char *fn, int requests, int64_t T, int Hq, int64_t max_blocks, int block_size) {
+    if (requests > 4096 || T > kMaxTokens || Hq > 1024 || max_blocks > 0x7fffffff / block_size)
+        return fail(W4A16_ERR_UNSUPPORTED, "%s: sizes too large", fn);
+    return W4A16_OK;
+}
+int check_scale(const char *fn, float scale) {
+    if (!(scale > -1e30f && scale < 1e30f))
+        return fail(W4A16_ERR_INVALID_ARG, "%s: scale=%g must be finite", fn, static_cast<double>(scale));
+    return W4A16_OK;
+}
+int check_scratch(const char *fn, int64_t bytes, int64_t need) {
+    if (bytes < need)
+        return fail(W4A16_ERR_INVALID_ARG, "%s: scratch of %lld bytes, %lld needed", fn, (long long)bytes, (long long)need);
+    return W4A16_OK;
+}
+
 // What norm and rotation share.
 int check_rope(const char *fn, int64_t T, int Hq, int Hkv, int D, const void *q_weight, const void *k_weight,
                const void *cos_sin, int64_t num_positions, int rot, const void *positions, float eps) {
@@ -274,19 +299,14 @@ int kv4_attention(const uint16_t *q, int64_t q_stride, const uint8_t *cache, int
                   int requests, uint16_t *out, int64_t T, int Hq, int Hkv, int D, float scale, int64_t window,
                   int64_t sinks, int64_t max_new, void *scratch, int64_t scratch_bytes, void *stream) {
     const char *fn = "kv4_attention";
-    if (requests < 1 || T < 0 || Hq < 1 || Hkv < 1 || max_blocks < 1)
-        return fail(W4A16_ERR_INVALID_ARG, "%s: requests=%d T=%lld Hq=%d Hkv=%d max_blocks=%lld", fn, requests,
-                    (long long)T, Hq, Hkv, (long long)max_blocks);
-    if (Hq % Hkv != 0) return fail(W4A16_ERR_INVALID_ARG, "%s: Hq=%d not a multiple of Hkv=%d", fn, Hq, Hkv);
+    if (int r = check_batch(fn, requests, T, Hq, Hkv, max_blocks)) return r;
     if (window < 0 || sinks < 0 || max_new < 1)
         return fail(W4A16_ERR_INVALID_ARG, "%s: window=%lld sinks=%lld must not be negative, max_new=%lld >= 1", fn,
                     (long long)window, (long long)sinks, (long long)max_new);
-    if (!(scale > -1e30f && scale < 1e30f))
-        return fail(W4A16_ERR_INVALID_ARG, "%s: scale=%g must be finite", fn, static_cast<double>(scale));
+    if (int r = check_scale(fn, scale)) return r;
     if (int r = check_head_dim(fn, D)) return r;
     if (int r = check_page(fn, block_size, num_blocks)) return r;
-    if (requests > 4096 || T > kMaxTokens || Hq > 1024 || max_blocks > 0x7fffffff / block_size)
-        return fail(W4A16_ERR_UNSUPPORTED, "%s: sizes too large", fn);
+    if (int r = check_batch_limits(fn, requests, T, Hq, max_blocks, block_size)) return r;
     if (T == 0) return ok();
     if (int r = check_rows(fn, "q", q, q_stride, Hq, D)) return r;
     if (int r = check_rows(fn, "out", out, static_cast<int64_t>(Hq) * D, Hq, D)) return r;
@@ -296,10 +316,7 @@ int kv4_attention(const uint16_t *q, int64_t q_stride, const uint8_t *cache, int
         !aligned(scratch, 256))
         return fail(W4A16_ERR_MISALIGNED, "%s: the cache must be 16-byte, the scratch 256-byte, the arrays 4-byte aligned",
                     fn);
-    const int64_t need = w4::kv4_attention_scratch(Hq, Hkv, D);
-    if (scratch_bytes < need)
-        return fail(W4A16_ERR_INVALID_ARG, "%s: scratch of %lld bytes, %lld needed", fn, (long long)scratch_bytes,
-                    (long long)need);
+    if (int r = check_scratch(fn, scratch_bytes, w4::kv4_attention_scratch(Hq, Hkv, D))) return r;
     w4::DeviceInfo dev;
     w4::Kv4AttnArgs a = {};
     if (int r = device_state(dev, a.status)) return r;
@@ -324,6 +341,180 @@ int kv4_attention(const uint16_t *q, int64_t q_stride, const uint8_t *cache, int
     a.bs_log2 = page_log2(block_size);
     a.scale = scale;
     return launched(w4::launch_kv4_attention(a, D, static_cast<cudaStream_t>(stream), dev), fn);
+}
+
+int kv4_bounds(const uint8_t *cache, int64_t num_blocks, int block_size, const int64_t *slots, uint8_t *bounds, int64_t T,
+               int Hkv, int D, void *stream) {
+    const char *fn = "kv4_bounds";
+    if (T < 0 || Hkv < 1)
+        return fail(W4A16_ERR_INVALID_ARG, "%s: T=%lld must not be negative, Hkv=%d >= 1", fn, (long long)T, Hkv);
+    if (int r = check_head_dim(fn, D)) return r;
+    if (int r = check_page(fn, block_size, num_blocks)) return r;
+    if (T > kMaxTokens || Hkv > 1024) return fail(W4A16_ERR_UNSUPPORTED, "%s: sizes too large", fn);
+    if (T == 0) return ok();
+    if (!cache || !slots || !bounds) return fail(W4A16_ERR_INVALID_ARG, "%s: null pointer", fn);
+    if (!aligned16(cache) || !aligned16(bounds) || !aligned(slots, 8))
+        return fail(W4A16_ERR_MISALIGNED, "%s: slots must be 8-byte, the other arrays 16-byte aligned", fn);
+    w4::DeviceInfo dev;
+    w4::Kv4BoundsArgs a;
+    if (int r = device_state(dev, a.status)) return r;
+    if (int r = check_device_ptrs(fn, dev.device, {cache, slots, bounds})) return r;
+    a.cache = cache;
+    a.slots = slots;
+    a.bounds = bounds;
+    a.T = T;
+    a.num_slots = num_blocks * block_size;
+    a.Hkv = Hkv;
+    a.bs_log2 = page_log2(block_size);
+    return launched(w4::launch_kv4_bounds(a, D, static_cast<cudaStream_t>(stream), dev), fn);
+}
+
+int kv4_select(const uint16_t *q, int64_t q_stride, const uint8_t *bounds, int64_t num_blocks, int block_size,
+               const int32_t *block_table, int64_t max_blocks, const int32_t *seq_lens, const int32_t *cu_new,
+               int requests, int64_t T, int Hq, int Hkv, int D, int top, int first, int recent, int32_t *tables,
+               int32_t *lens, void *stream) {
+    const char *fn = "kv4_select";
+    if (int r = check_batch(fn, requests, T, Hq, Hkv, max_blocks)) return r;
+    if (first < 0 || recent < 1 || top < 1 || static_cast<int64_t>(first) + recent > top)
+        return fail(W4A16_ERR_INVALID_ARG, "%s: top=%d must be at least first=%d (>= 0) and recent=%d (>= 1) together", fn, top,
+                    first, recent);
+    if (int r = check_head_dim(fn, D)) return r;
+    if (int r = check_page(fn, block_size, num_blocks)) return r;
+    if (int r = check_batch_limits(fn, requests, T, Hq, max_blocks, block_size)) return r;
+    if (max_blocks > w4::KV4_SELECT_PAGES || top > w4::KV4_SELECT_PAGES || T * Hkv > 0x7fffffff)
+        return fail(W4A16_ERR_UNSUPPORTED, "%s: max_blocks=%lld, top=%d (at most %lld each), T * Hkv at most 2^31 - 1", fn,
+                    (long long)max_blocks, top, (long long)w4::KV4_SELECT_PAGES);
+    if (T == 0) return ok();
+    if (int r = check_rows(fn, "q", q, q_stride, Hq, D)) return r;
+    if (!bounds || !block_table || !seq_lens || !cu_new || !tables || !lens)
+        return fail(W4A16_ERR_INVALID_ARG, "%s: null pointer", fn);
+    if (!aligned16(bounds) || !aligned(block_table, 4) || !aligned(seq_lens, 4) || !aligned(cu_new, 4) ||
+        !aligned(tables, 4) || !aligned(lens, 4))
+        return fail(W4A16_ERR_MISALIGNED, "%s: bounds must be 16-byte, the arrays 4-byte aligned", fn);
+    w4::DeviceInfo dev;
+    w4::Kv4SelectArgs a;
+    if (int r = device_state(dev, a.status)) return r;
+    if (int r = check_device_ptrs(fn, dev.device, {q, bounds, block_table, seq_lens, cu_new, tables, lens})) return r;
+    a.q = q;
+    a.bounds = bounds;
+    a.block_table = block_table;
+    a.seq_lens = seq_lens;
+    a.cu_new = cu_new;
+    a.tables = tables;
+    a.lens = lens;
+    a.q_stride = q_stride;
+    a.num_blocks = num_blocks;
+    a.max_blocks = max_blocks;
+    a.T = T;
+    a.requests = requests;
+    a.Hq = Hq;
+    a.Hkv = Hkv;
+    a.bs_log2 = page_log2(block_size);
+    a.top = top;
+    a.first = first;
+    a.recent = recent;
+    return launched(w4::launch_kv4_select(a, D, static_cast<cudaStream_t>(stream), dev), fn);
+}
+
+int kv4_sparse_attention(const uint16_t *q, int64_t q_stride, const uint8_t *cache, int64_t num_blocks, int block_size,
+                         const int32_t *tables, int64_t top, const int32_t *lens, uint16_t *out, int64_t T, int Hq,
+                         int Hkv, int D, float scale, void *scratch, int64_t scratch_bytes, void *stream) {
+    const char *fn = "kv4_sparse_attention";
+    if (int r = check_batch(fn, 1, T, Hq, Hkv, top)) return r;
+    if (int r = check_scale(fn, scale)) return r;
+    if (int r = check_head_dim(fn, D)) return r;
+    if (int r = check_page(fn, block_size, num_blocks)) return r;
+    if (int r = check_batch_limits(fn, 1, T, Hq, top, block_size)) return r;
+    if (T == 0) return ok();
+    if (int r = check_rows(fn, "q", q, q_stride, Hq, D)) return r;
+    if (int r = check_rows(fn, "out", out, static_cast<int64_t>(Hq) * D, Hq, D)) return r;
+    if (!cache || !tables || !lens || !scratch) return fail(W4A16_ERR_INVALID_ARG, "%s: null pointer", fn);
+    if (!aligned16(cache) || !aligned(tables, 4) || !aligned(lens, 4) || !aligned(scratch, 256))
+        return fail(W4A16_ERR_MISALIGNED, "%s: the cache must be 16-byte, the scratch 256-byte, the arrays 4-byte aligned",
+                    fn);
+    if (int r = check_scratch(fn, scratch_bytes, w4::kv4_attention_scratch(Hq, Hkv, D))) return r;
+    w4::DeviceInfo dev;
+    w4::Kv4TableArgs a = {};
+    if (int r = device_state(dev, a.status)) return r;
+    if (int r = check_device_ptrs(fn, dev.device, {q, cache, tables, lens, out, scratch})) return r;
+    a.q = q;
+    a.cache = cache;
+    a.block_table = tables;
+    a.seq_lens = lens;
+    a.out = out;
+    a.scratch = static_cast<unsigned char *>(scratch);
+    a.q_stride = q_stride;
+    a.num_blocks = num_blocks;
+    a.max_blocks = top;
+    a.T = T;
+    a.Hq = Hq;
+    a.Hkv = Hkv;
+    a.bs_log2 = page_log2(block_size);
+    a.scale = scale;
+    return launched(w4::launch_kv4_sparse(a, D, static_cast<cudaStream_t>(stream), dev), fn);
+}
+
+int64_t kv4_prefix_attention_scratch_bytes(int64_t T, int requests, int groups, int Hq, int Hkv, int D) {
+    if (T < 0 || T > kMaxTokens || requests < 1 || requests > 4096 || groups < 1 || groups > requests || Hq < 1 ||
+        Hq > 1024 || Hkv < 1 || Hq % Hkv != 0 || (D != 64 && D != 128 && D != 256))
+        return 0;
+    return w4::kv4_prefix_scratch(T, requests, groups, Hq, Hkv, D, nullptr);
+}
+
+int kv4_prefix_attention(const uint16_t *q, int64_t q_stride, const uint8_t *cache, int64_t num_blocks, int block_size,
+                         const int32_t *block_table, int64_t max_blocks, const int32_t *seq_lens,
+                         const int32_t *cu_new, int requests, const int32_t *prefix_lens, const int32_t *cu_groups,
+                         int groups, uint16_t *out, int64_t T, int Hq, int Hkv, int D, float scale, int64_t max_new,
+                         int64_t max_group, void *scratch, int64_t scratch_bytes, void *stream) {
+    const char *fn = "kv4_prefix_attention";
+    if (int r = check_batch(fn, requests, T, Hq, Hkv, max_blocks)) return r;
+    if (groups < 1 || groups > requests)
+        return fail(W4A16_ERR_INVALID_ARG, "%s: groups=%d outside 1 .. requests=%d", fn, groups, requests);
+    if (max_new < 1 || max_group < 1)
+        return fail(W4A16_ERR_INVALID_ARG, "%s: max_new=%lld and max_group=%lld must be >= 1", fn, (long long)max_new,
+                    (long long)max_group);
+    if (int r = check_scale(fn, scale)) return r;
+    if (int r = check_head_dim(fn, D)) return r;
+    if (int r = check_page(fn, block_size, num_blocks)) return r;
+    if (int r = check_batch_limits(fn, requests, T, Hq, max_blocks, block_size)) return r;
+    if (T == 0) return ok();
+    if (int r = check_rows(fn, "q", q, q_stride, Hq, D)) return r;
+    if (int r = check_rows(fn, "out", out, static_cast<int64_t>(Hq) * D, Hq, D)) return r;
+    if (!cache || !block_table || !seq_lens || !cu_new || !prefix_lens || !cu_groups || !scratch)
+        return fail(W4A16_ERR_INVALID_ARG, "%s: null pointer", fn);
+    if (!aligned16(cache) || !aligned(block_table, 4) || !aligned(seq_lens, 4) || !aligned(cu_new, 4) ||
+        !aligned(prefix_lens, 4) || !aligned(cu_groups, 4) || !aligned(scratch, 256))
+        return fail(W4A16_ERR_MISALIGNED, "%s: the cache must be 16-byte, the scratch 256-byte, the arrays 4-byte aligned",
+                    fn);
+    w4::Kv4PrefixArgs a = {};
+    a.scratch = static_cast<unsigned char *>(scratch);
+    if (int r = check_scratch(fn, scratch_bytes, w4::kv4_prefix_scratch(T, requests, groups, Hq, Hkv, D, &a))) return r;
+    w4::DeviceInfo dev;
+    if (int r = device_state(dev, a.status)) return r;
+    if (int r = check_device_ptrs(fn, dev.device,
+                                  {q, cache, block_table, seq_lens, cu_new, prefix_lens, cu_groups, out, scratch}))
+        return r;
+    a.q = q;
+    a.cache = cache;
+    a.block_table = block_table;
+    a.seq_lens = seq_lens;
+    a.cu_new = cu_new;
+    a.prefix_lens = prefix_lens;
+    a.cu_groups = cu_groups;
+    a.out = out;
+    a.q_stride = q_stride;
+    a.num_blocks = num_blocks;
+    a.max_blocks = max_blocks;
+    a.T = T;
+    a.max_new = max_new;
+    a.max_group = max_group;
+    a.requests = requests;
+    a.groups = groups;
+    a.Hq = Hq;
+    a.Hkv = Hkv;
+    a.bs_log2 = page_log2(block_size);
+    a.scale = scale;
+    return launched(w4::launch_kv4_prefix(a, D, static_cast<cudaStream_t>(stream), dev), fn);
 }
 
 int w4a16_sample(const void *logits, int dtype, int64_t row_stride, int64_t rows, int64_t vocab, const float *u,

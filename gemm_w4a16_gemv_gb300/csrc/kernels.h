@@ -177,11 +177,70 @@ struct Kv4AttnArgs {
     // zeroes the rows of no request and looks for lengths out of range
     int rows_least, rows_most, rows_above, first_launch;
     unsigned int inject;  // test-only injection flags (0 normally)
+    static constexpr bool kShared = false;  // keys of a row in several stretches
+    static constexpr bool kTail = true;     // rows that belong to no request are zeroed
 };
 constexpr int PROMPT_COUNTERS = 13056;  // byte offset in the scratch of the prompt kernel's two counters
 cudaError_t launch_kv4_prompt(const Kv4AttnArgs &a, int D, cudaStream_t st, const DeviceInfo &dev);
 int64_t kv4_attention_scratch(int Hq, int Hkv, int D);
 cudaError_t launch_kv4_attention(const Kv4AttnArgs &a, int D, cudaStream_t st, const DeviceInfo &dev);
+
+// kv4_sparse_attention: "requests" are tokens, block_table is their tables
+// [T, Hkv, max_blocks] and seq_lens the tokens in them.
+struct Kv4TableArgs : Kv4AttnArgs {
+    static constexpr bool kTail = false;
+};
+cudaError_t launch_kv4_sparse(const Kv4TableArgs &a, int D, cudaStream_t st, const DeviceInfo &dev);
+
+// A stretch of keys [from, end) of the block table's row `row`, from a multiple
+// of 16, and the new tokens that see it: all of it where base = end, else token i
+// those up to position base + i.  Its results go to places `place` and on (tokens x
+// Hq), or to the output where that is negative.
+struct alignas(16) Kv4Stretch {
+    int token, tokens, from, end, base, row;
+    int64_t place;
+};
+// kv4_prefix_attention: the groups' stretches, then the requests'; `requests`
+// counts them all.
+struct Kv4SharedArgs : Kv4AttnArgs {
+    static constexpr bool kShared = true, kTail = false;
+    const Kv4Stretch *stretches;
+    float2 *weights;  // [places] maximum (of base-2 exponents) and sum of the weights
+    float *values;    // [places, D] weighted values
+};
+// The arguments of a call besides.
+struct Kv4PrefixArgs : Kv4SharedArgs {
+    const int32_t *prefix_lens, *cu_groups;
+    Kv4Stretch *plan;     // the stretches, to be written
+    int32_t *group_of;    // [members] group whose shared stretch a request has, or -1
+    int groups, members;  // members: the call's requests
+    int64_t places, max_group;
+};
+int64_t kv4_prefix_scratch(int64_t T, int requests, int groups, int Hq, int Hkv, int D, Kv4PrefixArgs *a);
+cudaError_t launch_kv4_prefix(const Kv4PrefixArgs &a, int D, cudaStream_t st, const DeviceInfo &dev);
+
+// Bounds of pages: uint8 [num_blocks, Hkv, 2 D + 16].
+struct Kv4BoundsArgs {
+    const unsigned char *cache;
+    const int64_t *slots;
+    unsigned char *bounds;
+    unsigned int *status;
+    int64_t T, num_slots;
+    int Hkv, bs_log2;
+};
+cudaError_t launch_kv4_bounds(const Kv4BoundsArgs &a, int D, cudaStream_t st, const DeviceInfo &dev);
+
+struct Kv4SelectArgs {
+    const uint16_t *q;
+    const unsigned char *bounds;
+    const int32_t *block_table, *seq_lens, *cu_new;
+    int32_t *tables, *lens;
+    unsigned int *status;
+    int64_t q_stride, num_blocks, max_blocks, T;
+    int requests, Hq, Hkv, bs_log2, top, first, recent;
+};
+constexpr int64_t KV4_SELECT_PAGES = 49152;  // of a request: their scores lie in one SM's shared memory
+cudaError_t launch_kv4_select(const Kv4SelectArgs &a, int D, cudaStream_t st, const DeviceInfo &dev);
 
 struct SampleArgs {
     const void *logits;

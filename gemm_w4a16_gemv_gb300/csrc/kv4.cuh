@@ -50,6 +50,18 @@ __device__ __forceinline__ void check_lengths(const Kv4AttnArgs &a, int b) {
         atomicOr(a.status, kDevBadIndex);
 }
 
+// The request of token t: the last b with cu[b] <= t, or -1.  By a whole warp.
+__device__ __forceinline__ int request_of(const int32_t *cu, int requests, int64_t t, int lane) {
+    int lo = 0, hi = requests;
+    while (hi - lo > 1) {
+        const int step = (hi - lo + 31) / 32, at = lo + lane * step;
+        const unsigned below = __ballot_sync(0xffffffffu, at < hi && cu[at < hi ? at : lo] <= t);
+        lo += max(__popc(below) - 1, 0) * step;
+        hi = min(hi, lo + step);
+    }
+    return cu[lo] <= t && t < cu[lo + 1] ? lo : -1;
+}
+
 __device__ __forceinline__ float f16_lo(uint32_t w) { return __half2float(__ushort_as_half(static_cast<uint16_t>(w))); }
 __device__ __forceinline__ float f16_hi(uint32_t w) { return __half2float(__ushort_as_half(static_cast<uint16_t>(w >> 16))); }
 

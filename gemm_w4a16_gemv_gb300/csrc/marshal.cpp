@@ -29,6 +29,10 @@ decltype(&w4a16_qk_norm_rope) p_rope = nullptr;
 decltype(&kv4_append) p_append = nullptr;
 decltype(&kv4_gather) p_gather = nullptr;
 decltype(&kv4_attention) p_attention = nullptr;
+decltype(&kv4_bounds) p_bounds = nullptr;
+decltype(&kv4_select) p_select = nullptr;
+decltype(&kv4_sparse_attention) p_sparse = nullptr;
+decltype(&kv4_prefix_attention) p_prefix = nullptr;
 decltype(&w4a16_sample) p_sample = nullptr;
 
 struct Unfit {};  // an argument that the binding has to look at
@@ -222,6 +226,73 @@ int attention(PyObject *const *a) {
                        small(c.Hkv), small(c.D), scale, window, sinks, most, ps, scratch.numel(), l.stream);
 }
 
+// cache, slots, bounds, stream
+int bounds(PyObject *const *a) {
+    const Cache c(a[0]);
+    const at::Tensor &s = tensor(a[1]);
+    const int64_t T = s.numel();
+    const int64_t *slots = static_cast<int64_t *>(address(s, ScalarType::Long, c.device, T));
+    uint8_t *out = static_cast<uint8_t *>(address(tensor(a[2]), ScalarType::Byte, c.device, c.blocks * c.Hkv * (2 * c.D + 16)));
+    const Launch l(c.device, a[3]);
+    return p_bounds(c.p, c.blocks, c.bs, slots, out, T, small(c.Hkv), small(c.D), l.stream);
+}
+
+// q, bounds, block_table, seq_lens, cu_new, block_size, top, first, recent, tables, lens, stream
+int select(PyObject *const *a) {
+    const at::Tensor &x = tensor(a[1]);
+    const int device = x.get_device();
+    const Rows q(a[0], device);
+    if (x.dim() != 3 || x.size(2) != 2 * q.D + 16) throw Unfit();
+    const uint8_t *px = static_cast<uint8_t *>(address(x, ScalarType::Byte, device, -1));
+    const at::Tensor &table = tensor(a[2]), &lens = tensor(a[3]);
+    const int64_t B = lens.numel();
+    if (table.dim() != 2 || table.size(0) != B) throw Unfit();
+    const ScalarType I = ScalarType::Int;
+    const int32_t *pt = static_cast<int32_t *>(address(table, I, device, -1));
+    const int32_t *pl = static_cast<int32_t *>(address(lens, I, device, B)), *pu = address<int32_t>(a[4], I, device, B + 1);
+    const int bs = small(integer(a[5])), top = small(integer(a[6])), first = small(integer(a[7])), recent = small(integer(a[8]));
+    int32_t *to = address<int32_t>(a[9], I, device, q.T * x.size(1) * top), *n = address<int32_t>(a[10], I, device, q.T);
+    const Launch l(device, a[11]);
+    return p_select(q.p, q.stride, px, x.size(0), bs, pt, table.size(1), pl, pu, small(B), q.T, small(q.H), small(x.size(1)),
+                    small(q.D), top, first, recent, to, n, l.stream);
+}
+
+// q, cache, tables, lens, scratch, out, scale, stream
+int sparse(PyObject *const *a) {
+    const Cache c(a[1]);
+    const Rows q(a[0], c.device);
+    const at::Tensor &tables = tensor(a[2]), &scratch = tensor(a[4]);
+    if (q.D != c.D || tables.dim() != 3 || tables.size(0) != q.T || tables.size(1) != c.Hkv) throw Unfit();
+    const ScalarType I = ScalarType::Int;
+    const int32_t *pt = static_cast<int32_t *>(address(tables, I, c.device, -1)), *pl = address<int32_t>(a[3], I, c.device, q.T);
+    void *ps = address(scratch, ScalarType::Byte, c.device, -1);
+    uint16_t *out = address<uint16_t>(a[5], ScalarType::BFloat16, c.device, q.T * q.H * q.D);
+    const float scale = real(a[6]);
+    const Launch l(c.device, a[7]);
+    return p_sparse(q.p, q.stride, c.p, c.blocks, c.bs, pt, tables.size(2), pl, out, q.T, small(q.H), small(c.Hkv), small(c.D),
+                    scale, ps, scratch.numel(), l.stream);
+}
+
+// q, cache, block_table, seq_lens, cu_new, prefix_lens, cu_groups, scratch, out, scale, max_new, max_group, stream
+int prefix(PyObject *const *a) {
+    const Cache c(a[1]);
+    const Rows q(a[0], c.device);
+    const at::Tensor &table = tensor(a[2]), &lens = tensor(a[3]), &prefixes = tensor(a[5]), &scratch = tensor(a[7]);
+    const int64_t B = lens.numel(), N = prefixes.numel();
+    if (q.D != c.D || table.dim() != 2 || table.size(0) != B) throw Unfit();
+    const ScalarType I = ScalarType::Int;
+    const int32_t *pt = static_cast<int32_t *>(address(table, I, c.device, -1));
+    const int32_t *pl = static_cast<int32_t *>(address(lens, I, c.device, B)), *pu = address<int32_t>(a[4], I, c.device, B + 1);
+    const int32_t *pp = static_cast<int32_t *>(address(prefixes, I, c.device, N)), *pg = address<int32_t>(a[6], I, c.device, N + 1);
+    void *ps = address(scratch, ScalarType::Byte, c.device, -1);
+    uint16_t *out = address<uint16_t>(a[8], ScalarType::BFloat16, c.device, q.T * q.H * q.D);
+    const float scale = real(a[9]);
+    const int64_t most = integer(a[10]), widest = integer(a[11]);
+    const Launch l(c.device, a[12]);
+    return p_prefix(q.p, q.stride, c.p, c.blocks, c.bs, pt, table.size(1), pl, pu, small(B), pp, pg, small(N), out, q.T,
+                    small(q.H), small(c.Hkv), small(c.D), scale, most, widest, ps, scratch.numel(), l.stream);
+}
+
 // logits, u, temperature, top_k, top_p, min_p, out, stream
 int sample(PyObject *const *a) {
     const at::Tensor &x = tensor(a[0]);
@@ -267,8 +338,13 @@ PyObject *bind(PyObject *, PyObject *path) {
     p_append = reinterpret_cast<decltype(p_append)>(dlsym(h, "kv4_append"));
     p_gather = reinterpret_cast<decltype(p_gather)>(dlsym(h, "kv4_gather"));
     p_attention = reinterpret_cast<decltype(p_attention)>(dlsym(h, "kv4_attention"));
+    p_bounds = reinterpret_cast<decltype(p_bounds)>(dlsym(h, "kv4_bounds"));
+    p_select = reinterpret_cast<decltype(p_select)>(dlsym(h, "kv4_select"));
+    p_sparse = reinterpret_cast<decltype(p_sparse)>(dlsym(h, "kv4_sparse_attention"));
+    p_prefix = reinterpret_cast<decltype(p_prefix)>(dlsym(h, "kv4_prefix_attention"));
     p_sample = reinterpret_cast<decltype(p_sample)>(dlsym(h, "w4a16_sample"));
-    if (!p_plan || !p_rope || !p_append || !p_gather || !p_attention || !p_sample) {
+    if (!p_plan || !p_rope || !p_append || !p_gather || !p_attention || !p_bounds || !p_select || !p_sparse || !p_prefix ||
+        !p_sample) {
         p_sample = nullptr;
         PyErr_SetString(PyExc_RuntimeError, "the library lacks an entry point");
         return nullptr;
@@ -286,6 +362,10 @@ PyMethodDef methods[] = {{"bind", bind, METH_O, nullptr},
                          method<append, 14>("kv4_append"),
                          method<gather, 5>("kv4_gather"),
                          method<attention, 12>("kv4_attention"),
+                         method<bounds, 4>("kv4_bounds"),
+                         method<select, 12>("kv4_select"),
+                         method<sparse, 8>("kv4_sparse_attention"),
+                         method<prefix, 13>("kv4_prefix_attention"),
                          method<sample, 8>("w4a16_sample"),
                          {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_marshal", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};

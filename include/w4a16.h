@@ -518,6 +518,114 @@ int kv4_attention(const uint16_t *q, int64_t q_stride, const uint8_t *cache,
                   void *scratch, int64_t scratch_bytes, void *stream);
 
 /*
+ * kv4_attention for requests that share the first tokens of their contexts (a
+ * system prompt, samples of one prompt): what they share is read and multiplied
+ * once for all of a group's new tokens.  Group g is the requests cu_groups[g] <=
+ * b < cu_groups[g + 1]; the first prefix_lens[g] tokens of each of them lie in
+ * the same pages of the cache, so that the first entries of their rows of
+ * block_table agree.  The result is that of kv4_attention without a window, up to
+ * the order of its sums.
+ *   prefix_lens : int32 [groups]; how much of it is taken as shared is the
+ *                 kernel's choice: never more than the tokens that every request
+ *                 of the group with new ones had before the step
+ *   cu_groups   : int32 [groups + 1], rising; a request outside every group
+ *                 shares nothing.  Borders that fall or leave 0 .. requests and
+ *                 a negative prefix set the device status; what they say of
+ *                 sharing is left out or unspecified.
+ *   max_new, max_group : upper bounds of the new tokens of a request, of a group;
+ *                 they choose between kernels, as kv4_attention's max_new does
+ *   scratch     : at least kv4_prefix_attention_scratch_bytes(T, requests,
+ *                 groups, Hq, Hkv, D) bytes (0 where one of these is not
+ *                 supported), as kv4_attention's otherwise; a scratch for more
+ *                 tokens, requests or groups serves
+ * The other arguments are kv4_attention's, and so is what the kernels round.
+ * 1 <= groups <= requests <= 4096; T = 0 launches nothing.
+ */
+int64_t kv4_prefix_attention_scratch_bytes(int64_t T, int requests, int groups,
+                                           int Hq, int Hkv, int D);
+int kv4_prefix_attention(const uint16_t *q, int64_t q_stride,
+                         const uint8_t *cache, int64_t num_blocks,
+                         int block_size, const int32_t *block_table,
+                         int64_t max_blocks, const int32_t *seq_lens,
+                         const int32_t *cu_new, int requests,
+                         const int32_t *prefix_lens, const int32_t *cu_groups,
+                         int groups, uint16_t *out, int64_t T, int Hq, int Hkv,
+                         int D, float scale, int64_t max_new,
+                         int64_t max_group, void *scratch,
+                         int64_t scratch_bytes, void *stream);
+
+/*
+ * Bounds of the keys of a page, for kv4_select: uint8 [num_blocks, Hkv,
+ * 2 D + 16], of a page and key head D whole numbers `high` in 8 bits, D `low`,
+ * then D / 64 binary32 steps (the rest of the 16 bytes is not used).  With the
+ * largest and the smallest value v of each element over the page's tokens:
+ *   step = max |v| over 64 elements, * 65 / 8192   (one rounding in binary32)
+ *   high = ceil(max v / step),  low = floor(min v / step)   (0 where step is 0)
+ * so that every key lies between low * step and high * step (to a rounding of
+ * binary32).  The page of each slot that is the last of its page is written, from
+ * all its tokens as the cache holds them: after kv4_append with the same slots
+ * that is every page that the step filled.  Pages not yet full need no bounds:
+ * kv4_select takes a token's own page unseen.
+ *   slots : int64 [T]; negative ones are passed over, one past the cache sets
+ *           the device status
+ */
+int kv4_bounds(const uint8_t *cache, int64_t num_blocks, int block_size,
+               const int64_t *slots, uint8_t *bounds, int64_t T, int Hkv, int D,
+               void *stream);
+
+/*
+ * The pages that each new token attends to, for each key head: with the token at
+ * position p (as in kv4_attention) it sees the pages 0 .. p / block_size of its
+ * request.  Up to `top` of them all are taken; of more, the `first` first, the
+ * `recent` last (its own is one of these), and between them those with the
+ * highest scores (equal ones by lower number) until there are `top`:
+ *   u     = max_d |q_d| * 65 / 8192,  c_d = rint(q_d / u)   for a query head
+ *   dot_i = sum_d c_d (c_d > 0 ? high_d : low_d)            over the 64 of group i
+ *   score = max over the query heads of the key head of
+ *           u * (step_0 dot_0 + step_1 dot_1 + ...)
+ * dot in whole numbers, exact; the rest in binary32, each operation rounded,
+ * neighbouring terms added first.  So the score is, but for the 8 bits of q, what
+ * no q . k of the page exceeds.  A NaN in q counts as 0, an infinity as the
+ * largest finite number.  (For attention with a scale above 0.)
+ *   bounds : as kv4_bounds writes them; those of the pages before the `recent`
+ *            ones are read
+ *   tables : int32 [T, Hkv, top]: the ids of the pages taken, in the order of the
+ *            request's tokens, then -1
+ *   lens   : int32 [T]: tokens that the token sees in the pages of its table
+ *            (the same for every key head); 0 for a row of no request and where
+ *            p < 0
+ * Positions past a row of the block table set the device status and count as its
+ * last token; a block id outside [0, num_blocks) that is looked at sets it, has
+ * the lowest score and is -1 in the table.  top >= first + recent, recent >= 1;
+ * max_blocks and top <= 49152; T = 0 launches nothing.  One launch, no scratch.
+ */
+int kv4_select(const uint16_t *q, int64_t q_stride, const uint8_t *bounds,
+               int64_t num_blocks, int block_size, const int32_t *block_table,
+               int64_t max_blocks, const int32_t *seq_lens,
+               const int32_t *cu_new, int requests, int64_t T, int Hq, int Hkv,
+               int D, int top, int first, int recent, int32_t *tables,
+               int32_t *lens, void *stream);
+
+/*
+ * Attention of each new token over pages of its own:
+ *   out[t, h] = sum_j softmax_j(scale * q[t, h] . K_j) V_j,   j < lens[t]
+ * with token j in page tables[t, h / (Hq / Hkv), j / block_size] at offset
+ * j % block_size.  A row with lens[t] = 0 is written as zeros; a length below 0
+ * or past the table sets the device status and counts as the nearest; a block id
+ * outside [0, num_blocks) hides its tokens and sets it.
+ *   tables  : int32 [T, Hkv, top];  lens : int32 [T]  (kv4_select writes both)
+ *   scratch : kv4_attention_scratch_bytes(Hq, Hkv, D) bytes, as kv4_attention's
+ *             (the same array serves both, on one stream)
+ * Rounding as in kv4_attention's streaming kernel.
+ */
+int kv4_sparse_attention(const uint16_t *q, int64_t q_stride,
+                         const uint8_t *cache, int64_t num_blocks,
+                         int block_size, const int32_t *tables, int64_t top,
+                         const int32_t *lens, uint16_t *out, int64_t T, int Hq,
+                         int Hkv, int D, float scale, void *scratch,
+                         int64_t scratch_bytes, void *stream);
+
+/*
  * One token for each row of logits, from given uniform numbers.  Token i has
  * the whole-number mass
  *   m_i = rint(2^40 * exp(l_i / T - max_j(l_j / T)))     (exp in binary32)
