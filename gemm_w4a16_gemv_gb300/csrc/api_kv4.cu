@@ -9,6 +9,7 @@ using namespace w4api;
 namespace {
 
 constexpr int64_t kMaxTokens = int64_t(1) << 24;
+constexpr int64_t kMaxRows = int64_t(1) << 30;  // of kv4_prefix_attention: tokens x query heads
 
 bool aligned(const void *p, unsigned n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
 
@@ -455,8 +456,8 @@ int kv4_sparse_attention(const uint16_t *q, int64_t q_stride, const uint8_t *cac
 }
 
 int64_t kv4_prefix_attention_scratch_bytes(int64_t T, int requests, int groups, int Hq, int Hkv, int D) {
-    if (T < 0 || T > kMaxTokens || requests < 1 || requests > 4096 || groups < 1 || groups > requests || Hq < 1 ||
-        Hq > 1024 || Hkv < 1 || Hq % Hkv != 0 || (D != 64 && D != 128 && D != 256))
+    if (T < 0 || T > kMaxTokens || T * Hq > kMaxRows || requests < 1 || requests > 4096 || groups < 1 || groups > requests ||
+        Hq < 1 || Hq > 1024 || Hkv < 1 || Hq % Hkv != 0 || (D != 64 && D != 128 && D != 256))
         return 0;
     return w4::kv4_prefix_scratch(T, requests, groups, Hq, Hkv, D, nullptr);
 }
@@ -477,6 +478,7 @@ int kv4_prefix_attention(const uint16_t *q, int64_t q_stride, const uint8_t *cac
     if (int r = check_head_dim(fn, D)) return r;
     if (int r = check_page(fn, block_size, num_blocks)) return r;
     if (int r = check_batch_limits(fn, requests, T, Hq, max_blocks, block_size)) return r;
+    if (T * Hq > kMaxRows) return fail(W4A16_ERR_UNSUPPORTED, "%s: sizes too large", fn);
     if (T == 0) return ok();
     if (int r = check_rows(fn, "q", q, q_stride, Hq, D)) return r;
     if (int r = check_rows(fn, "out", out, static_cast<int64_t>(Hq) * D, Hq, D)) return r;

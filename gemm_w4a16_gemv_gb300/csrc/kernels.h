@@ -204,17 +204,32 @@ struct alignas(16) Kv4Stretch {
 // counts them all.
 struct Kv4SharedArgs : Kv4AttnArgs {
     static constexpr bool kShared = true, kTail = false;
-    const Kv4Stretch *stretches;
+    const Kv4Stretch *stretches;  // those that are streamed,
+    const Kv4Stretch *pieces;     // those of many rows, in pieces: counts[0] of them,
+    const int32_t *items_before, *counts;  // [pieces + 1] items before each
     float2 *weights;  // [places] maximum (of base-2 exponents) and sum of the weights
     float *values;    // [places, D] weighted values
+};
+cudaError_t launch_kv4_prompt(const Kv4SharedArgs &a, int D, cudaStream_t st, const DeviceInfo &dev);
+// The parts of a group's shared stretch: `parts` of them, `step` places apart.
+struct alignas(16) Kv4Share {
+    int token, parts;
+    int64_t place, step;
 };
 // The arguments of a call besides.
 struct Kv4PrefixArgs : Kv4SharedArgs {
     const int32_t *prefix_lens, *cu_groups;
-    Kv4Stretch *plan;     // the stretches, to be written
+    // the plan, to be written: of `stretches`, `pieces`, `items_before`, `counts`,
+    Kv4Stretch *plan, *cut;
+    int32_t *before, *count;
+    Kv4Share *shares;     // [groups]
     int32_t *group_of;    // [members] group whose shared stretch a request has, or -1
     int groups, members;  // members: the call's requests
+    int most_pieces;      // there is room for
     int64_t places, max_group;
+    // rows from which a shared stretch, a request goes to the tensor cores; rows of an
+    // item there; items that run at once
+    int least_shared, least_own, item_rows, workers;
 };
 int64_t kv4_prefix_scratch(int64_t T, int requests, int groups, int Hq, int Hkv, int D, Kv4PrefixArgs *a);
 cudaError_t launch_kv4_prefix(const Kv4PrefixArgs &a, int D, cudaStream_t st, const DeviceInfo &dev);

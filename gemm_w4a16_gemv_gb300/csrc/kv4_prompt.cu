@@ -302,7 +302,8 @@ __device__ __forceinline__ float factor(float f, float k) { return fmaxf(f * k, 
 __device__ __forceinline__ float pow2(int e) { return __uint_as_float(static_cast<uint32_t>(127 + e) << 23); }
 
 struct Item {
-    int b, h, tok0, r0, rows;   // rows [r0, r0 + rows) of the request; its first token
+    int b, h, tok0, r0, rows;   // rows [r0, r0 + rows) of the request; its row of the block table, its first token
+    int64_t place;              // of the rows' parts (kv4_prefix_attention), or negative
     int base;                   // position of row r is base + r / G
     int end;                    // keys at or past this are seen by no row,
     int sink, first;            // nor are those from `sink` to before `first`
@@ -324,6 +325,7 @@ __device__ __forceinline__ Item item_of(const Kv4AttnArgs &a, const int *cum, co
     const int local = index - cum[lo];
     lo = order[lo];
     it.b = lo;
+    it.place = -1;
     it.tok0 = rows_before(a, lo);
     const int n = rows_before(a, lo + 1) - it.tok0;
     const int total = n * G, blocks = (total + ITEM - 1) / ITEM;
@@ -349,6 +351,36 @@ __device__ __forceinline__ Item item_of(const Kv4AttnArgs &a, const int *cum, co
     it.low = low;
     // (rows that see nothing take one empty tile and come out as zeros)
     it.n = max(ns + max(last - low, 0), 1);
+    return it;
+}
+
+// The same of a piece of kv4_prefix_attention's: its keys from `from` on (before
+// them there may be some of the first key tile, whose cache tiles are not looked
+// at).
+template <int ITEM>
+__device__ __forceinline__ Item item_of(const Kv4SharedArgs &a, const int *cum, const int *, int index, int G) {
+    Item it;
+    int lo = 0, hi = a.counts[0];
+    while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (cum[mid] <= index) lo = mid;
+        else hi = mid;
+    }
+    const int local = index - cum[lo];
+    const Kv4Stretch s = a.pieces[lo];
+    const int total = s.tokens * G, blocks = (total + ITEM - 1) / ITEM;
+    it.b = s.row;
+    it.tok0 = s.token;
+    it.place = s.place;
+    it.h = local % a.Hkv;
+    it.r0 = (blocks - 1 - local / a.Hkv) * ITEM;
+    it.rows = min(ITEM, total - it.r0);
+    it.base = s.base;
+    it.end = max(min(s.base + (it.r0 + it.rows - 1) / G + 1, s.end), 0);
+    it.sink = it.ns = 0;
+    it.first = s.from;
+    it.low = s.from / KEYS;
+    it.n = max((it.end + KEYS - 1) / KEYS - it.low, 1);
     return it;
 }
 
@@ -384,8 +416,8 @@ __device__ __forceinline__ void form(const uint4 raw, uint32_t s2, uint32_t z102
     }
 }
 
-template <int D, bool PAIR>
-__global__ void __launch_bounds__(THREADS, 1) attn_prompt_kernel(const Kv4AttnArgs a) {
+template <class Args, int D, bool PAIR>
+__global__ void __launch_bounds__(THREADS, 1) attn_prompt_kernel(const Args a) {
     using L = PromptSmem<D, PAIR>;
     constexpr int G64 = L::G64, BUFS = L::BUFS, CTAS = PAIR ? 2 : 1, ITEM = CTAS * ROWS;
     constexpr uint32_t COL_S = D, IDESC_QK = idesc_kind_f16(ITEM, KEYS, 0u),
@@ -419,56 +451,62 @@ __global__ void __launch_bounds__(THREADS, 1) attn_prompt_kernel(const Kv4AttnAr
     pdl_launch_dependents();
     pdl_wait();
     int *const order = cum + a.requests + 1;
-    // requests by falling length (few enough to compare all pairs), then the
-    // items before each
-    for (int b = tid; b < a.requests; b += THREADS) {
-        int at = b;
-        if (a.requests <= SORT_MOST) {
-            const int mine = a.seq_lens[b];
-            at = 0;
-            for (int o = 0; o < a.requests; ++o) {
-                const int len = a.seq_lens[o];
-                at += len > mine || (len == mine && o < b);
+    if constexpr (Args::kShared) {
+        for (int i = tid; i <= a.counts[0]; i += THREADS) cum[i] = a.items_before[i];
+    } else {
+        // requests by falling length (few enough to compare all pairs), then the
+        // items before each
+        for (int b = tid; b < a.requests; b += THREADS) {
+            int at = b;
+            if (a.requests <= SORT_MOST) {
+                const int mine = a.seq_lens[b];
+                at = 0;
+                for (int o = 0; o < a.requests; ++o) {
+                    const int len = a.seq_lens[o];
+                    at += len > mine || (len == mine && o < b);
+                }
             }
+            order[at] = b;
         }
-        order[at] = b;
-    }
-    __syncthreads();
-    if (warp == 0) {
-        int at = 0;
-        for (int b0 = 0; b0 < a.requests; b0 += 32) {
-            const int i = b0 + lane;
-            int n = 0;
-            if (i < a.requests) {
-                const int b = order[i];
-                const int rows = (rows_before(a, b + 1) - rows_before(a, b)) * G;
-                n = taken(a, rows) ? (rows + ITEM - 1) / ITEM * a.Hkv : 0;
-            }
-            int in = n;
+        __syncthreads();
+        if (warp == 0) {
+            int at = 0;
+            for (int b0 = 0; b0 < a.requests; b0 += 32) {
+                const int i = b0 + lane;
+                int n = 0;
+                if (i < a.requests) {
+                    const int b = order[i];
+                    const int rows = (rows_before(a, b + 1) - rows_before(a, b)) * G;
+                    n = taken(a, rows) ? (rows + ITEM - 1) / ITEM * a.Hkv : 0;
+                }
+                int in = n;
 #pragma unroll
-            for (int o = 1; o < 32; o <<= 1) {
-                const int v = __shfl_up_sync(0xffffffffu, in, o);
-                if (lane >= o) in += v;
+                for (int o = 1; o < 32; o <<= 1) {
+                    const int v = __shfl_up_sync(0xffffffffu, in, o);
+                    if (lane >= o) in += v;
+                }
+                if (i < a.requests) cum[i + 1] = at + in;
+                at += __shfl_sync(0xffffffffu, in, 31);
             }
-            if (i < a.requests) cum[i + 1] = at + in;
-            at += __shfl_sync(0xffffffffu, in, 31);
+            if (lane == 0) cum[0] = 0;
         }
-        if (lane == 0) cum[0] = 0;
-    }
-    if (blockIdx.x == 0)
-        for (int b = tid; b < a.requests; b += THREADS) check_lengths(a, b);
-    if (a.first_launch) {  // rows that belong to no request
-        const int64_t from = static_cast<int64_t>(rows_before(a, a.requests)) * a.Hq * D / 8, to = a.T * a.Hq * D / 8;
-        for (int64_t i = from + static_cast<int64_t>(blockIdx.x) * THREADS + tid; i < to;
-             i += static_cast<int64_t>(gridDim.x) * THREADS)
-            reinterpret_cast<uint4 *>(a.out)[i] = make_uint4(0, 0, 0, 0);
+        if (blockIdx.x == 0)
+            for (int b = tid; b < a.requests; b += THREADS) check_lengths(a, b);
+        if (a.first_launch) {  // rows that belong to no request
+            const int64_t from = static_cast<int64_t>(rows_before(a, a.requests)) * a.Hq * D / 8, to = a.T * a.Hq * D / 8;
+            for (int64_t i = from + static_cast<int64_t>(blockIdx.x) * THREADS + tid; i < to;
+                 i += static_cast<int64_t>(gridDim.x) * THREADS)
+                reinterpret_cast<uint4 *>(a.out)[i] = make_uint4(0, 0, 0, 0);
+        }
     }
     tc_fence_before();
     __syncthreads();
     if (PAIR) cluster_sync();  // the other CTA's barriers are there
     tc_fence_after();
     const uint32_t tmem = bar.tmem;
-    const int items = cum[a.requests];
+    int items;
+    if constexpr (Args::kShared) items = cum[a.counts[0]];
+    else items = cum[a.requests];
     unsigned int *const counter = reinterpret_cast<unsigned int *>(a.scratch + PROMPT_COUNTERS);
     // the k-th item of this CTA or pair (items or more: there is none, or it was not announced in time)
     auto item_at = [&](int k) -> int {
@@ -618,6 +656,13 @@ __global__ void __launch_bounds__(THREADS, 1) attn_prompt_kernel(const Kv4AttnAr
             const bool on = rank * ROWS + r < cur.rows;
             const int row = cur.r0 + (on ? rank * ROWS + r : 0);
             uint16_t *const dst = a.out + (static_cast<int64_t>(cur.tok0 + row / G) * a.Hq + cur.h * G + row % G) * D;
+            float *part = nullptr;
+            if constexpr (Args::kShared)
+                if (cur.place >= 0) {
+                    const int64_t at = cur.place + static_cast<int64_t>(row / G) * a.Hq + cur.h * G + row % G;
+                    part = a.values + at * D;
+                    if (on) a.weights[at] = make_float2(M, l);
+                }
 #pragma unroll 1
             for (int c = 0; c < D / 32; ++c) {
                 uint32_t o[32];
@@ -629,6 +674,14 @@ __global__ void __launch_bounds__(THREADS, 1) attn_prompt_kernel(const Kv4AttnAr
                         uint32_t w[4];
                         const uint32_t *x = o + 8 * e;  // dimensions 0 4 1 5 2 6 3 7
                         const int at[8] = {0, 2, 4, 6, 1, 3, 5, 7};
+                        if (Args::kShared && part) {
+                            float4 *const to = reinterpret_cast<float4 *>(part + 32 * c + 8 * e);
+                            to[0] = make_float4(__uint_as_float(x[at[0]]), __uint_as_float(x[at[1]]), __uint_as_float(x[at[2]]),
+                                                __uint_as_float(x[at[3]]));
+                            to[1] = make_float4(__uint_as_float(x[at[4]]), __uint_as_float(x[at[5]]), __uint_as_float(x[at[6]]),
+                                                __uint_as_float(x[at[7]]));
+                            continue;
+                        }
 #pragma unroll
                         for (int k = 0; k < 4; ++k)
                             w[k] = pack_bf16(__uint_as_float(x[at[2 * k]]) * inv, __uint_as_float(x[at[2 * k + 1]]) * inv);
@@ -918,12 +971,13 @@ __global__ void __launch_bounds__(THREADS, 1) attn_prompt_kernel(const Kv4AttnAr
     }
 }
 
-template <int D, bool PAIR>
-cudaError_t launch(const Kv4AttnArgs &a, cudaStream_t st, const DeviceInfo &dev) {
-    const int smem = 1024 + PromptSmem<D, PAIR>::cum + (2 * a.requests + 1) * 4;
+template <int D, bool PAIR, class Args>
+cudaError_t launch(const Args &a, cudaStream_t st, const DeviceInfo &dev) {
+    // (of kv4_prefix_attention `requests` is the most pieces there can be)
+    const int smem = 1024 + PromptSmem<D, PAIR>::cum + ((Args::kShared ? 1 : 2) * a.requests + 1) * 4;
     if (smem > dev.max_smem_optin) return cudaErrorNotSupported;
     static SmemLimit limit;
-    if (cudaError_t e = limit.ensure(reinterpret_cast<const void *>(attn_prompt_kernel<D, PAIR>), dev.device, smem)) return e;
+    if (cudaError_t e = limit.ensure(reinterpret_cast<const void *>(attn_prompt_kernel<Args, D, PAIR>), dev.device, smem)) return e;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(static_cast<unsigned>(PAIR ? dev.num_sms & ~1 : dev.num_sms));
     cfg.blockDim = dim3(THREADS);
@@ -938,12 +992,18 @@ cudaError_t launch(const Kv4AttnArgs &a, cudaStream_t st, const DeviceInfo &dev)
     at[1].val.clusterDim.z = 1;
     cfg.attrs = at;
     cfg.numAttrs = PAIR ? 2 : 1;
-    return cudaLaunchKernelEx(&cfg, attn_prompt_kernel<D, PAIR>, a);
+    return cudaLaunchKernelEx(&cfg, attn_prompt_kernel<Args, D, PAIR>, a);
 }
 
 }  // namespace
 
 cudaError_t launch_kv4_prompt(const Kv4AttnArgs &a, int D, cudaStream_t st, const DeviceInfo &dev) {
+    if (D == 64) return launch<64, false>(a, st, dev);
+    if (D == 128) return launch<128, true>(a, st, dev);
+    return launch<256, true>(a, st, dev);
+}
+
+cudaError_t launch_kv4_prompt(const Kv4SharedArgs &a, int D, cudaStream_t st, const DeviceInfo &dev) {
     if (D == 64) return launch<64, false>(a, st, dev);
     if (D == 128) return launch<128, true>(a, st, dev);
     return launch<256, true>(a, st, dev);

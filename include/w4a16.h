@@ -539,7 +539,7 @@ int kv4_attention(const uint16_t *q, int64_t q_stride, const uint8_t *cache,
  *                 supported), as kv4_attention's otherwise; a scratch for more
  *                 tokens, requests or groups serves
  * The other arguments are kv4_attention's, and so is what the kernels round.
- * 1 <= groups <= requests <= 4096; T = 0 launches nothing.
+ * 1 <= groups <= requests <= 4096, T * Hq <= 2^30; T = 0 launches nothing.
  */
 int64_t kv4_prefix_attention_scratch_bytes(int64_t T, int requests, int groups,
                                            int Hq, int Hkv, int D);
