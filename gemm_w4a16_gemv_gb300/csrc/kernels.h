@@ -228,8 +228,8 @@ struct Kv4PrefixArgs : Kv4SharedArgs {
     int most_pieces;      // there is room for
     int64_t places, max_group;
     // rows from which a shared stretch, a request goes to the tensor cores; rows of an
-    // item there; items that run at once
-    int least_shared, least_own, item_rows, workers;
+    // item there; items that run at once; cost of 16 streamed rows in eighths of an item's
+    int least_shared, least_own, item_rows, workers, stream_cost;
 };
 int64_t kv4_prefix_scratch(int64_t T, int requests, int groups, int Hq, int Hkv, int D, Kv4PrefixArgs *a);
 cudaError_t launch_kv4_prefix(const Kv4PrefixArgs &a, int D, cudaStream_t st, const DeviceInfo &dev);

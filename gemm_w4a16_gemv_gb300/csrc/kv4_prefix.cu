@@ -19,202 +19,238 @@ namespace {
 
 constexpr int PLAN_THREADS = 1024;
 constexpr int JOIN_THREADS = 256;
+constexpr int64_t SMALL = 64 << 20;  // bytes of the cache that all requests can name
 constexpr int AHEAD = 4;       // parts that a thread of the join asks for together
 constexpr int KEYS = 128;      // of a key tile of the tensor cores' kernel
 constexpr int ROUNDS = 4;      // items to a worker at most, where stretches are cut
-constexpr int OVERHEAD = 4;    // cost of an item beside its key tiles, in key tiles
+constexpr int OVERHEAD = 4;    // cost of an item beside its key tiles, in key tiles,
+constexpr int PARTS = 8;       // and of the parts that it writes
 
-// Exclusive sum over the CTA's threads; `all` is the sum of all.
-__device__ __forceinline__ long long sum_before(long long v, long long &all, long long *sums) {
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    long long in = v;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-        const long long u = __shfl_up_sync(0xffffffffu, in, o);
-        if (lane >= o) in += u;
+// The stretches of a call, by one CTA.
+//
+// Sharing costs the writing and joining of parts, so a group shares only where
+// that is less than its requests' own reading: in units of an item's key tile (a
+// block of item_rows rows), a request costs an item for each such block, or
+// stream_cost / 8 for each block of 16 where it is streamed; the shared stretch the
+// same for all rows together, PARTS more for each item (its parts written and read
+// back) and OVERHEAD for each item that begins anew.
+//
+// A shared stretch of many rows is cut into pieces, so that its items (a block of
+// rows and a key head each) fill the workers: with w items a piece and t key
+// tiles, cuts of c tiles give sum w ceil(t / c) < sum w t / c + sum w items, so
+//   c = ceil(sum w t / (k workers - sum w))
+// gives at most k to a worker; of k = 1 .. ROUNDS the one with the least k (c +
+// OVERHEAD) is taken.
+//
+// Every array is read once, all elements on their way together: the kernel is a
+// chain of latencies (before the others can begin).
+struct PlanSmem {
+    int *cu, *ctx, *owner;              // [members + 1] rows before, [members] tokens before the step, the group
+    int *border, *shared, *weight;      // [groups + 1], [groups] keys that are shared, items of a piece or 0
+    long long *place, *piece;           // [groups] first place; first piece << 40 | first item
+    __device__ PlanSmem(unsigned char *p, int groups, int members) {
+        place = reinterpret_cast<long long *>(p);
+        piece = place + groups;
+        cu = reinterpret_cast<int *>(piece + groups);
+        ctx = cu + members + 1;
+        owner = ctx + members;
+        border = owner + members;
+        shared = border + groups + 1;
+        weight = shared + groups;
     }
-    __syncthreads();
-    if (lane == 31) sums[warp] = in;
-    __syncthreads();
-    long long before = in - v;
-    all = 0;
-    for (int w = 0; w < PLAN_THREADS / 32; ++w) {
-        if (w < warp) before += sums[w];
-        all += sums[w];
-    }
-    return before;
-}
+    static int bytes(int groups, int members) { return 28 * groups + 12 * members + 8; }
+};
 
-// The stretches of a call, by one CTA.  A shared stretch of many rows is cut into
-// pieces of `cut` key tiles, so that its items (a block of rows and a key head
-// each) fill the workers: of the smallest cuts that give at most one, two, ... items
-// to a worker the one with the shortest time, an item's cost beside its key tiles
-// being about OVERHEAD of them.
 __global__ void __launch_bounds__(PLAN_THREADS) plan_kernel(const Kv4PrefixArgs a) {
-    extern __shared__ int plan_smem[];
-    int *const shared = plan_smem;           // [groups] keys that the group shares
-    int *const weight = shared + a.groups;   // [groups] items of it for each piece, or 0
-    int *const owner = weight + a.groups;    // [members] the group
-    __shared__ long long sums[PLAN_THREADS / 32];
-    __shared__ unsigned long long own_items;  // of requests of many rows
-    __shared__ int longest, cuts[ROUNDS], costs[ROUNDS];
+    extern __shared__ __align__(16) unsigned char plan_smem[];
+    const PlanSmem x(plan_smem, a.groups, a.members);
+    __shared__ long long all_weight, all_tiles;  // sums of w, of w t
+    __shared__ int own_items, cut_tiles;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int G = a.Hq / a.Hkv;
     pdl_launch_dependents();
     pdl_wait();
-    const long long cap = min(static_cast<long long>(a.max_blocks) << a.bs_log2, 0x7fffff00ll);
-    if (tid == 0) longest = 0, own_items = 0;
-    for (int b = tid; b < a.members; b += PLAN_THREADS) owner[b] = -1;
-    __syncthreads();
+    const long long table = a.max_blocks << a.bs_log2, cap = min(table, 0x7fffff00ll);
+    if (tid == 0) all_weight = all_tiles = 0, own_items = 0;
+    // ---- lengths and borders; if some are out of range, nothing is shared
     bool bad = false;
-    // a warp per group: the tokens before all of its members' new ones
+    for (int i = tid; i <= a.members; i += PLAN_THREADS) {
+        const int v = a.cu_new[i];
+        bad |= v < 0 || v > a.T;
+        x.cu[i] = static_cast<int>(min(max(static_cast<long long>(v), 0ll), static_cast<long long>(a.T)));
+    }
+    for (int i = tid; i < a.members; i += PLAN_THREADS) {
+        x.ctx[i] = a.seq_lens[i];
+        x.owner[i] = -1;
+    }
+    for (int i = tid; i <= a.groups; i += PLAN_THREADS) {
+        const int v = a.cu_groups[i];
+        bad |= v < 0 || v > a.members;
+        x.border[i] = min(max(v, 0), a.members);
+    }
+    for (int i = tid; i < a.groups; i += PLAN_THREADS) x.shared[i] = a.prefix_lens[i];
+    __syncthreads();
+    bool wrong = bad;  // (a length that is too long does not speak against sharing)
+    for (int i = tid; i < a.members; i += PLAN_THREADS) {
+        const int n = x.cu[i + 1] - x.cu[i], len = x.ctx[i];
+        wrong |= n < 0;
+        bad |= n < 0 || (n > 0 && (len < 0 || len > table));
+        x.ctx[i] = max(len, -(1 << 30)) - max(n, 0);
+    }
+    for (int i = tid; i < a.groups; i += PLAN_THREADS) {
+        wrong |= x.border[i + 1] < x.border[i];
+        bad |= x.shared[i] < 0;
+    }
+    const bool sane = !__syncthreads_or(wrong);
+    if (bad || wrong) atomicOr(a.status, kDevBadIndex);
+    const int least_own = sane ? a.least_own : 0x7fffffff;
+    auto blocks = [&](int rows, int of) { return (rows + of - 1) / of; };
+    // ---- a warp per group: the tokens before all of its members' new ones
     for (int g = warp; g < a.groups; g += PLAN_THREADS / 32) {
-        const int from = a.cu_groups[g], to = a.cu_groups[g + 1], len = a.prefix_lens[g];
-        bad |= from < 0 || to < from || to > a.members || len < 0;
-        const int first = min(max(from, 0), a.members), last = min(max(to, first), a.members);
-        long long least = len;
-        int rows = 0, row = a.members;
+        const int first = x.border[g], last = sane ? x.border[g + 1] : first;
+        int least = x.shared[g], count = 0, apart = 0, begun = 0;
         for (int b = first + lane; b < last; b += 32) {
-            const int n = rows_before(a, b + 1) - rows_before(a, b);
-            if (n <= 0) continue;
-            least = min(least, static_cast<long long>(a.seq_lens[b]) - n);
-            row = min(row, b);
-            ++rows;
+            x.owner[b] = g;
+            const int rows = (x.cu[b + 1] - x.cu[b]) * G;
+            if (rows <= 0) continue;
+            least = min(least, x.ctx[b]);
+            ++count;
+            if (rows >= least_own) {
+                apart += 8 * blocks(rows, a.item_rows);
+                begun += blocks(rows, a.item_rows);
+            } else apart += a.stream_cost * blocks(rows, 16);
         }
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) least = min(least, __shfl_xor_sync(0xffffffffu, least, o));
-        rows = __reduce_add_sync(0xffffffffu, rows);
-        row = __reduce_min_sync(0xffffffffu, row);
-        const int token = rows_before(a, first), tokens = max(rows_before(a, last) - token, 0);
-        least = rows < 2 || tokens == 0 ? 0 : min(max(least, 0ll), cap) & ~15ll;  // (one request shares nothing)
-        for (int b = first + lane; b < last; b += 32) owner[b] = g;
+        least = __reduce_min_sync(0xffffffffu, least);
+        count = __reduce_add_sync(0xffffffffu, count);
+        apart = __reduce_add_sync(0xffffffffu, apart);
+        begun = __reduce_add_sync(0xffffffffu, begun);
+        const int rows = (x.cu[last] - x.cu[first]) * G;
+        int keys = count < 2 ? 0 : static_cast<int>(min(static_cast<long long>(max(least, 0)), cap)) & ~15;
+        const int tiles = (keys + KEYS - 1) / KEYS, items = blocks(rows, a.item_rows);
+        const bool many = rows >= a.least_shared;
+        const long long together = many ? 8ll * items * (tiles + PARTS + OVERHEAD) + 8ll * begun * OVERHEAD
+                                        : static_cast<long long>(a.stream_cost) * blocks(rows, 16) * (tiles + 1);
+        if (together >= static_cast<long long>(apart) * tiles) keys = 0;
         if (lane == 0) {
-            shared[g] = static_cast<int>(least);
-            const bool many = least > 0 && static_cast<long long>(tokens) * G >= a.least_shared;
-            weight[g] = many ? (tokens * G + a.item_rows - 1) / a.item_rows * a.Hkv : 0;
-            if (many) atomicMax(&longest, static_cast<int>((least + KEYS - 1) / KEYS));
-            Kv4Stretch s;
-            s.token = token;
-            s.tokens = least > 0 && !many ? tokens : 0;
-            s.from = 0;
-            s.end = s.base = static_cast<int>(least);
-            s.row = min(row, a.members - 1);
-            s.place = tokens;  // (until it has one)
-            a.plan[g] = s;
-        }
-    }
-    // requests of many rows
-    for (int b = tid; b < a.members; b += PLAN_THREADS) {
-        const int rows = max(rows_before(a, b + 1) - rows_before(a, b), 0) * G;
-        if (rows >= a.least_own) atomicAdd(&own_items, static_cast<unsigned long long>((rows + a.item_rows - 1) / a.item_rows * a.Hkv));
-    }
-    __syncthreads();
-    // (more than that only where cu_new falls somewhere)
-    const int least_own = own_items > 0 && own_items < (1ull << 30) ? a.least_own : 0x7fffffff;
-    // ---- the cut, a warp for each number of rounds
-    if (warp < ROUNDS && longest > 0) {
-        const int k = warp + 1;
-        auto items = [&](int c) -> long long {
-            long long n = 0;
-            for (int g = lane; g < a.groups; g += 32)
-                if (weight[g]) n += static_cast<long long>(weight[g]) * (((shared[g] + KEYS - 1) / KEYS + c - 1) / c);
-#pragma unroll
-            for (int o = 16; o > 0; o >>= 1) n += __shfl_xor_sync(0xffffffffu, n, o);
-            return n + static_cast<long long>(own_items);
-        };
-        int lo = 0, hi = longest;  // more items than that with lo; hi is tried last
-        while (hi - lo > 1) {
-            const int mid = (lo + hi) >> 1;
-            if (items(mid) <= static_cast<long long>(k) * a.workers) hi = mid;
-            else lo = mid;
-        }
-        const bool fits = items(hi) <= static_cast<long long>(k) * a.workers;
-        if (lane == 0) {
-            cuts[warp] = hi;
-            costs[warp] = fits ? k * (hi + OVERHEAD) : 0x7fffffff;
-        }
-    }
-    __syncthreads();
-    int cut = longest;
-    if (longest > 0) {
-        int best = 0x7fffffff;
-        for (int k = 0; k < ROUNDS; ++k)
-            if (costs[k] < best) {
-                best = costs[k];
-                cut = cuts[k];
+            x.shared[g] = keys;
+            x.weight[g] = keys > 0 && many ? items * a.Hkv : 0;
+            if (keys > 0 && many) {
+                atomicAdd(reinterpret_cast<unsigned long long *>(&all_weight), static_cast<unsigned long long>(x.weight[g]));
+                atomicAdd(reinterpret_cast<unsigned long long *>(&all_tiles), static_cast<unsigned long long>(x.weight[g]) * tiles);
             }
-    }
-    // ---- pieces: the requests' first (they differ in length), then the groups'.
-    // (pieces << 40 | items) before each
-    constexpr long long ITEMS = (1ll << 40) - 1;
-    long long at = 0, all;
-    auto put = [&](long long n, const Kv4Stretch &s) {
-        a.cut[n >> 40] = s;
-        a.before[n >> 40] = static_cast<int>(n & ITEMS);
-    };
-    if (least_own != 0x7fffffff)  // (the same for all threads)
-        for (int b0 = 0; b0 < a.members; b0 += PLAN_THREADS) {
-            const int b = b0 + tid;
-            const int rows = b < a.members ? max(rows_before(a, b + 1) - rows_before(a, b), 0) * G : 0;
-            const bool many = rows >= least_own;
-            const long long n = many ? 1ll << 40 | static_cast<long long>((rows + a.item_rows - 1) / a.item_rows * a.Hkv) : 0;
-            const long long mine = at + sum_before(n, all, sums);
-            if (many) put(mine, {rows_before(a, b), rows / G, 0, 0, 0, b, -1});  // (its keys follow below)
-            if (b < a.members) a.group_of[b] = many ? static_cast<int>(mine >> 40) : -1;
-            at += all;
         }
-    long long place = a.T * a.Hq;  // behind the requests' own
-    for (int g0 = 0; g0 < a.groups; g0 += PLAN_THREADS) {
-        const int g = g0 + tid;
-        const bool on = g < a.groups && shared[g] > 0;
-        const int tokens = on ? static_cast<int>(a.plan[g].place) : 0, tiles = on ? (shared[g] + KEYS - 1) / KEYS : 0;
-        const int parts = !on ? 0 : weight[g] ? (tiles + cut - 1) / cut : 1;
-        const long long step = static_cast<long long>(tokens) * a.Hq;
-        const long long from = place + sum_before(parts * step, all, sums);
-        place += all;
-        const bool fits = from + parts * step <= a.places;  // (not if lengths fall somewhere)
-        const long long n = on && fits && weight[g] ? static_cast<long long>(parts) << 40 | static_cast<long long>(parts) * weight[g] : 0;
-        const long long mine = at + sum_before(n, all, sums);
-        at += all;
-        const bool room = (at >> 40) <= a.most_pieces;
-        if (on) {
-            Kv4Stretch s = a.plan[g];
-            if (!fits || !room) {
-                bad = true;
-                shared[g] = 0;
-                a.plan[g].tokens = 0;
-            } else {
-                a.shares[g] = {s.token, parts, from, step};
-                s.place = from;
-                if (weight[g] == 0) a.plan[g] = s;
-                s.tokens = tokens;
-                s.base = s.end;
-                const int end = s.end;
-                for (int i = 0; weight[g] && i < parts; ++i) {
-                    s.from = i * cut * KEYS;
-                    s.end = min((i + 1) * cut * KEYS, end);
-                    s.place = from + i * step;
-                    put(mine + (static_cast<long long>(i) << 40 | static_cast<long long>(i) * weight[g]), s);
+    }
+    if (least_own != 0x7fffffff)
+        for (int b = tid; b < a.members; b += PLAN_THREADS) {
+            const int rows = (x.cu[b + 1] - x.cu[b]) * G;
+            if (rows >= least_own) atomicAdd(&own_items, blocks(rows, a.item_rows) * a.Hkv);
+        }
+    __syncthreads();
+    // ---- the cut; pieces and places in their order: requests' pieces first (they
+    // differ in length), then the groups'
+    if (warp == 0) {
+        long long cost = 0x7fffffffffffffffll;
+        int cut = 0x7fffffff;
+        const long long room = static_cast<long long>(lane + 1) * a.workers - all_weight - own_items;
+        if (lane < ROUNDS && all_weight > 0 && room > 0) {
+            cut = static_cast<int>(min((all_tiles + room - 1) / room, 0x7fffffffll));
+            cost = (lane + 1) * (static_cast<long long>(cut) + OVERHEAD);
+        }
+#pragma unroll
+        for (int o = 1; o < ROUNDS; o <<= 1) {
+            const long long other = __shfl_xor_sync(0xffffffffu, cost, o);
+            const int its = __shfl_xor_sync(0xffffffffu, cut, o);
+            if (other < cost || (other == cost && its > cut)) cost = other, cut = its;
+        }
+        cut = __shfl_sync(0xffffffffu, cut, 0);
+        if (lane == 0) cut_tiles = cut;
+        long long at = 0, place = a.T * a.Hq;  // (places of the requests' own come first)
+        auto before = [&](long long v, long long &total) {
+            long long in = v;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const long long u = __shfl_up_sync(0xffffffffu, in, o);
+                if (lane >= o) in += u;
+            }
+            const long long mine = total + in - v;
+            total += __shfl_sync(0xffffffffu, in, 31);
+            return mine;
+        };
+        if (own_items > 0)
+            for (int b0 = 0; b0 < a.members; b0 += 32) {
+                const int b = b0 + lane, rows = b < a.members ? (x.cu[b + 1] - x.cu[b]) * G : 0;
+                const bool many = rows >= least_own;
+                const long long mine = before(many ? 1ll << 40 | static_cast<long long>(blocks(rows, a.item_rows)) * a.Hkv : 0, at);
+                if (many) {
+                    a.before[mine >> 40] = static_cast<int>(mine & ((1ll << 40) - 1));
+                    a.group_of[b] = static_cast<int>(mine >> 40);  // (its piece, for now)
                 }
             }
+        for (int g0 = 0; g0 < a.groups; g0 += 32) {
+            const int g = g0 + lane;
+            const bool on = g < a.groups && x.shared[g] > 0;
+            const int tiles = on ? (x.shared[g] + KEYS - 1) / KEYS : 0, weight = on ? x.weight[g] : 0;
+            int parts = on;
+            if (weight) {
+                parts = (tiles + cut - 1) / cut;
+                const int even = (tiles + parts - 1) / parts;  // pieces of a length
+                parts = (tiles + even - 1) / even;
+            }
+            const long long step = on ? static_cast<long long>(x.cu[x.border[g + 1]] - x.cu[x.border[g]]) * a.Hq : 0;
+            const long long p = before(parts * step, place);
+            const long long n = before(weight ? static_cast<long long>(parts) << 40 | static_cast<long long>(parts) * weight : 0, at);
+            if (on) {
+                x.place[g] = p;
+                x.piece[g] = n;
+                a.shares[g] = {x.cu[x.border[g]], parts, p, step};
+            }
         }
-        if (!room) at -= all;
+        if (lane == 0) {
+            a.count[0] = static_cast<int>(at >> 40);
+            a.before[at >> 40] = static_cast<int>(at & ((1ll << 40) - 1));
+        }
     }
     __syncthreads();
-    if (tid == 0) {
-        a.count[0] = static_cast<int>(at >> 40);
-        a.before[at >> 40] = static_cast<int>(at & ITEMS);
+    // ---- the groups' stretches, a warp each
+    for (int g = warp; g < a.groups; g += PLAN_THREADS / 32) {
+        Kv4Stretch s = {};
+        const int keys = x.shared[g], weight = x.weight[g];
+        if (keys > 0) {
+            int row = a.members;  // a member with new tokens: the others' rows of the table may be old
+            for (int b = x.border[g] + lane; b < x.border[g + 1]; b += 32)
+                if (x.cu[b + 1] > x.cu[b]) row = min(row, b);
+            row = __reduce_min_sync(0xffffffffu, row);
+            s.token = x.cu[x.border[g]];
+            s.tokens = x.cu[x.border[g + 1]] - s.token;
+            s.end = s.base = keys;
+            s.row = row;
+            s.place = x.place[g];
+            if (weight) {
+                const int tiles = (keys + KEYS - 1) / KEYS, n = (tiles + cut_tiles - 1) / cut_tiles, even = (tiles + n - 1) / n;
+                const int parts = (tiles + even - 1) / even;
+                Kv4Stretch p = s;
+                for (int i = lane; i < parts; i += 32) {
+                    const int at = static_cast<int>(x.piece[g] >> 40) + i;
+                    p.from = i * even * KEYS;
+                    p.end = min((i + 1) * even * KEYS, keys);
+                    p.place = s.place + static_cast<int64_t>(i) * s.tokens * a.Hq;
+                    a.cut[at] = p;
+                    a.before[at] = static_cast<int>(x.piece[g] & ((1ll << 40) - 1)) + i * weight;
+                }
+                s.tokens = 0;
+            }
+        }
+        if (lane == 0) a.plan[g] = s;
     }
     // ---- what is left of each request
     for (int b = tid; b < a.members; b += PLAN_THREADS) {
-        check_lengths(a, b);
-        const int g = owner[b];
+        const int g = x.owner[b];
         Kv4Stretch s;
-        s.token = rows_before(a, b);
-        s.tokens = max(rows_before(a, b + 1) - s.token, 0);
-        s.from = g >= 0 ? shared[g] : 0;
+        s.token = x.cu[b];
+        s.tokens = max(x.cu[b + 1] - s.token, 0);
+        s.from = g >= 0 ? x.shared[g] : 0;
         s.end = static_cast<int>(cap);
-        s.base = a.seq_lens[b] - s.tokens;
+        s.base = x.ctx[b];
         s.row = b;
         s.place = s.from > 0 ? static_cast<int64_t>(s.token) * a.Hq : -1;
         if (s.tokens * G >= least_own) {
@@ -224,7 +260,6 @@ __global__ void __launch_bounds__(PLAN_THREADS) plan_kernel(const Kv4PrefixArgs 
         a.plan[a.groups + b] = s;
         a.group_of[b] = s.from > 0 ? g : -1;
     }
-    if (bad) atomicOr(a.status, kDevBadIndex);
 }
 
 // Four dimensions of a row a thread, JOIN_THREADS of a token's Hq D / 4 a CTA.
@@ -284,6 +319,18 @@ __global__ void __launch_bounds__(JOIN_THREADS) join_kernel(const Kv4PrefixArgs 
                    static_cast<uint32_t>(f32_to_bf16_bits(o[2])) | static_cast<uint32_t>(f32_to_bf16_bits(o[3])) << 16);
 }
 
+// Borders and prefixes out of range, where nothing else looks at them.
+__global__ void __launch_bounds__(JOIN_THREADS) check_kernel(const Kv4PrefixArgs a) {
+    pdl_launch_dependents();
+    pdl_wait();
+    bool bad = false;
+    for (int g = threadIdx.x; g < a.groups; g += JOIN_THREADS) {
+        const int from = a.cu_groups[g], to = a.cu_groups[g + 1];
+        bad |= from < 0 || to < from || to > a.requests || a.prefix_lens[g] < 0;
+    }
+    if (bad) atomicOr(a.status, kDevBadIndex);
+}
+
 cudaError_t launch(const void *kernel, Kv4PrefixArgs &a, dim3 grid, int threads, int smem, cudaStream_t st) {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = grid;
@@ -338,6 +385,11 @@ int64_t kv4_prefix_scratch(int64_t T, int requests, int groups, int Hq, int Hkv,
 cudaError_t launch_kv4_prefix(const Kv4PrefixArgs &args, int D, cudaStream_t st, const DeviceInfo &dev) {
     Kv4PrefixArgs a = args;
     const int G = a.Hq / a.Hkv;
+    // what lies in L2 after its first reading is not worth sharing
+    if ((static_cast<int64_t>(a.requests) * a.max_blocks << a.bs_log2) * a.Hkv * kv4_tile_bytes(D) / KV4_TILE <= SMALL) {
+        if (cudaError_t e = launch_kv4_attention(a, D, st, dev)) return e;
+        return launch(reinterpret_cast<const void *>(check_kernel), a, dim3(1), JOIN_THREADS, 0, st);
+    }
     a.members = a.requests;
     a.inject = dev.inject;
     a.item_rows = D == 64 ? 128 : 256;
@@ -351,7 +403,8 @@ cudaError_t launch_kv4_prefix(const Kv4PrefixArgs &args, int D, cudaStream_t st,
     const bool tensor = group > few_shared || own > few_own;
     a.least_shared = !tensor ? NONE_OF : a.groups == 1 ? 1 : static_cast<int>(few_shared) + 1;
     a.least_own = tensor && own > few_own ? static_cast<int>(few_own) + 1 : NONE_OF;
-    const int smem = (2 * a.groups + a.members) * 4;
+    a.stream_cost = D == 128 ? 4 : 6;
+    const int smem = PlanSmem::bytes(a.groups, a.members);
     static SmemLimit limit;
     if (smem > 40 * 1024)
         if (cudaError_t e = limit.ensure(reinterpret_cast<const void *>(plan_kernel), dev.device, smem)) return e;

@@ -26,16 +26,20 @@ def poisoned(blocks, Hkv, bs, D, rng):
     return c
 
 
-def grouped(torch, groups, Hq, Hkv, D, bs, seed, gap=0, spread=1.0):
+def grouped(torch, groups, Hq, Hkv, D, bs, seed, gap=0, spread=1.0, wide=True):
     """Requests in groups [(prefix, [(past, new), ...]), ...]: the first
-    prefix // bs pages of a group's requests are the same ones."""
+    prefix // bs pages of a group's requests are the same ones.  `wide`: a table
+    for so much cache that sharing is worth while by its width."""
     rng = np.random.default_rng(seed)
     ends = [p + past + n for p, members in groups for past, n in members]
     new = [n for _, members in groups for _, n in members]
     blocks = sum(-(-e // bs) for e in ends) + 3
     c = poisoned(blocks, Hkv, bs, D, rng)
     ids = list(rng.permutation(blocks))
-    table = np.full((len(ends), max(-(-e // bs) for e in ends) + 2), -1)
+    width = max(-(-e // bs) for e in ends) + 2
+    if wide:
+        width = max(width, (65 << 20) // (len(ends) * bs * Hkv * 18 * D // 16) + 1)
+    table = np.full((len(ends), width), -1)
     b, borders = 0, [0]
     for prefix, members in groups:
         lead = [ids.pop() for _ in range(prefix // bs)]

@@ -157,6 +157,32 @@ def test_captured_with_other_lengths_and_strided_rows(Hq, Hkv, D):
         _check(w4, out, host, D ** -0.5)
 
 
+@pytest.mark.parametrize("Hq,Hkv,D", [(16, 8, 256), (8, 1, 128), (4, 4, 64)])
+def test_caches_too_small_to_share(Hq, Hkv, D):
+    torch, w4 = cuda_or_skip()
+    dev, host = lh.grouped(torch, SMALL + [(32, [(0, 70), (3, 1)])], Hq, Hkv, D, 16, D, gap=1, wide=False)
+    out = torch.full_like(dev["q"], float("nan"))
+    _run(w4, dev, out=out, max_new=70, max_group=71)
+    _check(w4, out, host, D ** -0.5)
+    dev["cu_groups"][1] = 10 ** 6
+    _run(w4, dev, out=out, max_new=70, max_group=71)
+    torch.cuda.synchronize()
+    assert w4.w4a16_check_device_error() == 6
+    _check(w4, out, host, D ** -0.5)
+
+
+@pytest.mark.parametrize("groups", [1500, 40])
+def test_many_groups(groups):
+    # more groups than a warp has lanes, more stretches than a launch has workers
+    torch, w4 = cuda_or_skip()
+    rng = np.random.default_rng(groups)
+    some = [(int(rng.integers(0, 4)) * 16 if groups > 40 else int(rng.integers(1, 12)) * 16,
+             [(int(rng.integers(0, 9)), 1) for _ in range(rng.integers(1, 4 if groups > 40 else 40))]) for _ in range(groups)]
+    dev, host = lh.grouped(torch, some, 2, 1, 64, 16, groups)
+    out = _run(w4, dev, max_new=1, max_group=40)
+    _check(w4, out, host, 64 ** -0.5)
+
+
 def test_on_another_stream_beside_another_call():
     # two calls at once, each with scratch of its own
     torch, w4 = cuda_or_skip()
