@@ -789,6 +789,9 @@ __global__ void __launch_bounds__(THREADS, 1) attn_prompt_kernel(const Args a) {
                 uint2 all[2];           // of tokens 2 (lane % 8) and one more in group lane / 8, of both cache tiles
                 int n0, n1;             // tokens there are
             };
+            // (without branches: where the tokens end is looked at when the values are
+            // used.  With the loads behind a test of it a tile's ten of them waited for
+            // one another, 1400 cycles of each tile's 3900)
             auto load = [&](int i, int id) -> Tile {
                 Tile t;
                 int n = tokens(i);
@@ -796,7 +799,7 @@ __global__ void __launch_bounds__(THREADS, 1) attn_prompt_kernel(const Args a) {
                     bad = true;
                     n = 0;
                 }
-                const unsigned mine = number(i, id);
+                const unsigned mine = n > 0 ? number(i, id) : 0u;  // (nothing there: some tile)
                 t.n0 = __shfl_sync(0xffffffffu, n, 0);
                 t.n1 = __shfl_sync(0xffffffffu, n, 1);
                 const size_t o0 = static_cast<size_t>(__shfl_sync(0xffffffffu, mine, 0)) * kv4_tile_bytes(D);
@@ -804,26 +807,21 @@ __global__ void __launch_bounds__(THREADS, 1) attn_prompt_kernel(const Args a) {
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
                     const size_t o = h && !shared ? o1 : o0;
-                    const int n = h && !shared ? t.n1 : t.n0, grp = h ? g1 : g0;
+                    const int grp = h ? g1 : g0;
 #pragma unroll
                     for (int q = 0; q < HALF; ++q) {
-                        t.raw[h][q] = make_uint4(0, 0, 0, 0);
-                        t.par[h][q] = 0;
-                        if (token < n) {
-                            t.raw[h][q] = *reinterpret_cast<const uint4 *>(codes + o + (grp + q) * 512);
-                            t.par[h][q] = *reinterpret_cast<const uint32_t *>(params + o + ((grp + q) * 16 + token) * 4);
-                        }
+                        t.raw[h][q] = *reinterpret_cast<const uint4 *>(codes + o + (grp + q) * 512);
+                        t.par[h][q] = *reinterpret_cast<const uint32_t *>(params + o + ((grp + q) * 16 + token) * 4);
                     }
-                    t.all[h] = make_uint2(0, 0);
-                    if (2 * (lane & 7) < (h ? t.n1 : t.n0) && lane < 8 * G64)
-                        t.all[h] = *reinterpret_cast<const uint2 *>(params + (h ? o1 : o0) + lane * 8);
+                    t.all[h] = *reinterpret_cast<const uint2 *>(params + (h ? o1 : o0) + lane % (8 * G64) * 8);
                 }
                 return t;
             };
             // e such that every scale of a cache tile < 2^(e + 11)
             auto exponent = [&](uint2 x, int n) -> int {
-                const unsigned second = 2 * (lane & 7) + 1 < n ? x.y & 0x7fffu : 0u;  // (no stale scale past the end)
-                const unsigned bits = __reduce_max_sync(0xffffffffu, max(x.x & 0x7fffu, second));
+                // (no stale scale past the end)
+                const unsigned first = 2 * (lane & 7) < n ? x.x & 0x7fffu : 0u, second = 2 * (lane & 7) + 1 < n ? x.y & 0x7fffu : 0u;
+                const unsigned bits = __reduce_max_sync(0xffffffffu, max(first, second));
                 return bits ? static_cast<int>(__float_as_uint(f16_lo(bits)) >> 23) - 137 : -11;
             };
             Tile tile = load(0, page_of(0));
@@ -858,9 +856,11 @@ __global__ void __launch_bounds__(THREADS, 1) attn_prompt_kernel(const Args a) {
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
                     const float up = pow2(-(h && !shared ? e1 : e0));
+                    const bool there = token < (h && !shared ? tile.n1 : tile.n0);
 #pragma unroll
                     for (int q = 0; q < HALF; ++q) {
-                        const float s = f16_lo(tile.par[h][q]) * up, z = f16_hi(tile.par[h][q]);
+                        const uint32_t par = there ? tile.par[h][q] : 0u;
+                        const float s = f16_lo(par) * up, z = f16_hi(par);
                         form(tile.raw[h][q], pack_f16(s, s), pack_f16(-1024.f - z, -1024.f - z), pack_f16(-64.f - z, -64.f - z),
                              dst + buf * next_buf + h * part + q * step, x7, half);
                     }
