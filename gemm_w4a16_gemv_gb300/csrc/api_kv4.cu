@@ -382,9 +382,10 @@ int kv4_select(const uint16_t *q, int64_t q_stride, const uint8_t *bounds, int64
     if (int r = check_head_dim(fn, D)) return r;
     if (int r = check_page(fn, block_size, num_blocks)) return r;
     if (int r = check_batch_limits(fn, requests, T, Hq, max_blocks, block_size)) return r;
-    if (max_blocks > w4::KV4_SELECT_PAGES || top > w4::KV4_SELECT_PAGES || T * Hkv > 0x7fffffff)
-        return fail(W4A16_ERR_UNSUPPORTED, "%s: max_blocks=%lld, top=%d (at most %lld each), T * Hkv at most 2^31 - 1", fn,
-                    (long long)max_blocks, top, (long long)w4::KV4_SELECT_PAGES);
+    if (max_blocks > w4::KV4_SELECT_PAGES || top > w4::KV4_SELECT_PAGES || T * Hkv > 0x7fffffff / 8 || Hq / Hkv > 32)
+        return fail(W4A16_ERR_UNSUPPORTED,
+                    "%s: max_blocks=%lld, top=%d (at most %lld each), T * Hkv at most 2^28 - 1, Hq / Hkv = %d (at most 32)", fn,
+                    (long long)max_blocks, top, (long long)w4::KV4_SELECT_PAGES, Hq / Hkv);
     if (T == 0) return ok();
     if (int r = check_rows(fn, "q", q, q_stride, Hq, D)) return r;
     if (!bounds || !block_table || !seq_lens || !cu_new || !tables || !lens)

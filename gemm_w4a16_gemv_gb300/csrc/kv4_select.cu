@@ -118,7 +118,8 @@ __device__ __forceinline__ uint32_t ordered(float x) {
 }
 
 // A query head in whole numbers of 8 bits (NaN as 0, infinities as the largest
-// finite number) and their unit.  By a whole warp.
+// finite number), which bytes of them are negative, and their unit.  By a whole
+// warp.
 template <int D>
 __device__ __forceinline__ void quantise(const uint16_t *q, uint32_t *out, float &unit, int lane) {
     constexpr int WORDS = D / 4, PER = (WORDS + 31) / 32;
@@ -143,41 +144,127 @@ __device__ __forceinline__ void quantise(const uint16_t *q, uint32_t *out, float
         uint32_t word = 0;
 #pragma unroll
         for (int e = 0; e < 4; ++e) word |= (static_cast<uint32_t>(__float2int_rn(__fdiv_rn(x[k][e], by))) & 255u) << 8 * e;
-        if (lane + 32 * k < WORDS) out[lane + 32 * k] = word;
+        if (lane + 32 * k < WORDS) {
+            out[lane + 32 * k] = word;
+            out[WORDS + lane + 32 * k] = __vcmplts4(word, 0);
+        }
     }
     if (lane == 0) unit = step;
 }
 
-// Half of N sums for each of two lanes, lane ^ o the other one: those of the
-// first half where bit o of `lane` is 0.
-template <int N, class T, int M>
-__device__ __forceinline__ void fold(T (&v)[M], int o, int lane) {
-    const bool second = lane & o;
+__device__ __forceinline__ uint32_t cluster_rank() {
+    uint32_t r;
+    asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+    return r;
+}
+__device__ __forceinline__ uint32_t cluster_ctas() {
+    uint32_t r;
+    asm volatile("mov.u32 %0, %%cluster_nctaid.x;" : "=r"(r));
+    return r;
+}
+__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
+// Stores to the shared memory of the cluster's first CTA.
+__device__ __forceinline__ void store_first(uint32_t *p, uint32_t v) {
+    asm volatile("{\n\t.reg .b32 a;\n\tmapa.shared::cluster.u32 a, %0, 0;\n\tst.shared::cluster.u32 [a], %1;\n\t}" ::"r"(smem_u32(p)),
+                 "r"(v)
+                 : "memory");
+}
+
+// Key at which the `need` largest of keys[0 .. n) end, and how many of those
+// equal to it are among them; by a whole CTA.  Between the smallest and the
+// largest key a count for each of 256 steps shows the one in which they end; its
+// keys, a few as a rule, are compared with one another, and otherwise counted again
+// in 256 steps of it.
+struct Cut {
+    uint32_t key;
+    int equal;
+};
+__device__ __forceinline__ Cut find_cut(const uint32_t *keys, int n, int need, int *scratch) {
+    // scratch: [256] counts (then up to as many candidates), [WARPS] sums, the step,
+    // the rest, [2] extremes, a count, the cut
+    int *const count = scratch, *const sums = scratch + 256, *const pick = sums + WARPS;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    uint32_t low = 0xffffffffu, high = 0;
+    for (int i = tid; i < n; i += THREADS) low = min(low, keys[i]), high = max(high, keys[i]);
+    low = __reduce_min_sync(0xffffffffu, low);
+    high = __reduce_max_sync(0xffffffffu, high);
+    if (lane == 0) count[warp] = static_cast<int>(low), count[WARPS + warp] = static_cast<int>(high);
+    __syncthreads();
+    for (int w = 0; w < WARPS; ++w) {
+        low = min(low, static_cast<uint32_t>(count[w]));
+        high = max(high, static_cast<uint32_t>(count[WARPS + w]));
+    }
+    while (true) {
+        const uint32_t span = high - low;
+        const int shift = span > 255 ? 24 - __clz(span) : 0;  // (span >> shift is 8 bits)
+        __syncthreads();
+        count[tid] = 0;
+        if (tid == 0) pick[2] = 0;
+        __syncthreads();
+        for (int i = tid; i < n; i += THREADS)
+            if (keys[i] - low <= span) atomicAdd(&count[(keys[i] - low) >> shift], 1);
+        __syncthreads();
+        const int mine = count[255 - tid];  // from the top
+        int in = mine;
 #pragma unroll
-    for (int k = 0; k < N / 2; ++k) {
-        const T keep = second ? v[k + N / 2] : v[k], give = second ? v[k] : v[k + N / 2];
-        v[k] = keep + __shfl_xor_sync(0xffffffffu, give, o);
+        for (int o = 1; o < 32; o <<= 1) {
+            const int v = __shfl_up_sync(0xffffffffu, in, o);
+            if (lane >= o) in += v;
+        }
+        if (lane == 31) sums[warp] = in;
+        __syncthreads();
+        for (int w = 0; w < warp; ++w) in += sums[w];
+        if (in - mine < need && need <= in) pick[0] = 255 - tid, pick[1] = need - (in - mine), pick[3] = mine;
+        __syncthreads();
+        const int held = pick[3];
+        need = pick[1];
+        low += static_cast<uint32_t>(pick[0]) << shift;
+        if (shift == 0) return {low, need};
+        high = low + ((1u << shift) - 1u);
+        if (held > 256) continue;
+        // ---- the candidates against one another
+        uint32_t *const list = reinterpret_cast<uint32_t *>(count);
+        for (int i = tid; i < n; i += THREADS)
+            if (keys[i] - low <= high - low) list[atomicAdd(&pick[2], 1)] = keys[i];
+        __syncthreads();
+        if (tid < held) {
+            const uint32_t key = list[tid];
+            int above = 0, equal = 0;
+            for (int k = 0; k < held; ++k) above += list[k] > key, equal += list[k] == key;
+            if (above < need && need <= above + equal) pick[4] = static_cast<int>(key), pick[5] = need - above;  // (the same of equal ones)
+        }
+        __syncthreads();
+        return {static_cast<uint32_t>(pick[4]), pick[5]};
     }
 }
 
-// One CTA for a token and key head.
+// A cluster for a token and key head, its CTAs with a share of the pages each;
+// the first one then chooses.
 //
-// Score.  A warp takes 32 pages; a lane holds 16 elements, so LPP = D / 16 lanes
-// a page and PPI pages side by side, LPP times.  The sums over a page's lanes
-// are formed for all its 32 pages together: with every lane that is added, half
-// of the pages go to either side, until each lane has one page.
-template <int D, int HC>
-__global__ void __launch_bounds__(THREADS) select_kernel(const Kv4SelectArgs a) {
-    constexpr int LPP = D / 16, PPI = 32 / LPP;
-    extern __shared__ uint32_t keys[];      // of the pages between the first and the recent ones
-    __shared__ uint32_t query[HC][D / 4];   // 8 bits an element
-    __shared__ float unit[HC];
-    __shared__ int histogram[256], sums[2 * WARPS], pick[2];
+// Score.  A lane holds 16 elements of a page's bounds: D / 16 lanes a page, PPI
+// pages side by side and four (SLOTS) times as many at a time.  Each four lanes
+// have a group of 64 elements: of its sums for four pages every lane adds up one.
+// One pass over the bounds for any number of query heads.  Bound: memory, where
+// there are pages and tokens enough; about 45 instructions a query head for 4 PPI
+// pages.  16 bytes of high and of low a lane and slot are on their way at once,
+// 4 KB a warp.
+template <int D>
+__global__ void __launch_bounds__(THREADS, 3) select_kernel(const Kv4SelectArgs a) {
+    constexpr int LPP = D / 16, PPI = 32 / LPP, SLOTS = 4, BATCH = SLOTS * PPI;
+    extern __shared__ __align__(16) uint32_t keys[];  // of the pages between the first and the recent ones; then the queries
+    __shared__ int scratch[256 + WARPS + 8];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int64_t t = blockIdx.x / a.Hkv;
-    const int h = static_cast<int>(blockIdx.x % a.Hkv), G = a.Hq / a.Hkv;
+    const int ctas = static_cast<int>(cluster_ctas()), rank = static_cast<int>(cluster_rank());
+    const int64_t task = blockIdx.x / ctas, t = task / a.Hkv;
+    const int h = static_cast<int>(task % a.Hkv), G = a.Hq / a.Hkv;
+    uint32_t *const query = keys + (a.max_blocks + 3) / 4 * 4;    // [G][2][D / 4]: 8 bits an element, and which are negative
+    float *const unit = reinterpret_cast<float *>(query + G * (D / 2));  // [G]
+    cluster_arrive();  // (there, for the other CTAs' stores)
     pdl_launch_dependents();
     pdl_wait();
+    for (int g = warp; g < G; g += WARPS)
+        quantise<D>(a.q + t * a.q_stride + static_cast<int64_t>(h * G + g) * D, query + g * (D / 2), unit[g], lane);
     if (blockIdx.x == 0)
         for (int b = tid; b < a.requests; b += THREADS) {
             const int64_t from = a.cu_new[b], to = a.cu_new[b + 1], len = a.seq_lens[b];
@@ -190,9 +277,6 @@ __global__ void __launch_bounds__(THREADS) select_kernel(const Kv4SelectArgs a) 
     const int seen = p < 0 ? 0 : static_cast<int>(p >> a.bs_log2) + 1;
     const int taken = min(a.top, seen);
     int32_t *const out = a.tables + (t * a.Hkv + h) * a.top;
-    if (h == 0 && tid == 0)
-        a.lens[t] = p < 0 ? 0 : static_cast<int>(((taken - 1) << a.bs_log2) + (p & ((1 << a.bs_log2) - 1)) + 1);
-    for (int i = taken + tid; i < a.top; i += THREADS) out[i] = -1;
     const int32_t *const pages = a.block_table + (b < 0 ? 0 : b) * a.max_blocks;
     bool bad = false;
     auto id_of = [&](int page) -> int {
@@ -202,167 +286,136 @@ __global__ void __launch_bounds__(THREADS) select_kernel(const Kv4SelectArgs a) 
         return -1;
     };
     const int few = seen > a.top ? a.first : taken, late = taken - (seen > a.top ? a.recent : 0);
-    for (int i = tid; i < taken; i += THREADS)
-        if (i < few || i >= late) out[i] = id_of(i < few ? i : seen - taken + i);
     // need of n pages, from number `few` on
     const int need = late - few, n = seen - (taken - need);
+    __syncthreads();
+    cluster_wait();
     if (need > 0) {
         const int s = lane % LPP, side = lane / LPP;
-        for (int g0 = 0; g0 < G; g0 += HC) {
-            __syncthreads();
-            for (int g = warp; g < HC; g += WARPS) quantise<D>(a.q + t * a.q_stride + static_cast<int64_t>(h * G + min(g0 + g, G - 1)) * D, query[g], unit[g], lane);
-            __syncthreads();
-            uint32_t qw[HC][4], below[HC][4];
+        const int step = ctas * WARPS * BATCH;
+        // the page whose sums this lane has in the end
+        const int mine = (2 * (lane & 1) + (lane >> 1 & 1)) * PPI + side;
+        const unsigned char *const bounds = a.bounds + static_cast<int64_t>(h) * bounds_bytes(D);
+        const int64_t page_bytes = static_cast<int64_t>(a.Hkv) * bounds_bytes(D);
+        auto ids = [&](int p0) { return lane < BATCH && p0 + lane < n ? id_of(few + p0 + lane) : -1; };
+        const int first = (rank * WARPS + warp) * BATCH;
+        int id = ids(first);
+        for (int p0 = first; p0 < n; p0 += step) {
+            const int next = ids(p0 + step);  // on its way meanwhile
+            const int whose = __shfl_sync(0xffffffffu, id, mine);
+            const float unit_of = *reinterpret_cast<const float *>(bounds + max(whose, 0) * page_bytes + 2 * D + s / 4 * 4);
+            uint32_t high[SLOTS][4], low[SLOTS][4];
 #pragma unroll
-            for (int g = 0; g < HC; ++g)
-#pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    qw[g][k] = query[g][4 * s + k];
-                    below[g][k] = __vcmplts4(qw[g][k], 0);
-                }
-            for (int p0 = warp * 32; p0 < n; p0 += THREADS) {
-                const int id = p0 + lane < n ? id_of(few + p0 + lane) : -1;
-                auto row_of = [&](int slot) -> const unsigned char * {  // of the page of `slot` beside this lane, or null
-                    const int page = __shfl_sync(0xffffffffu, id, slot * PPI + side);
-                    return page < 0 ? nullptr : a.bounds + (static_cast<int64_t>(page) * a.Hkv + h) * bounds_bytes(D);
-                };
-                int dot[HC][LPP];
-#pragma unroll
-                for (int j = 0; j < LPP; ++j) {
-                    const unsigned char *const row = row_of(j);
-                    uint4 up = make_uint4(0, 0, 0, 0), down = up;
-                    if (row) {
-                        up = *reinterpret_cast<const uint4 *>(row + 16 * s);
-                        down = *reinterpret_cast<const uint4 *>(row + D + 16 * s);
-                    }
-                    const uint32_t high[4] = {up.x, up.y, up.z, up.w}, low[4] = {down.x, down.y, down.z, down.w};
-#pragma unroll
-                    for (int g = 0; g < HC; ++g) {
-                        dot[g][j] = 0;
-#pragma unroll
-                        for (int k = 0; k < 4; ++k)
-                            dot[g][j] = __dp4a(static_cast<int>((high[k] & ~below[g][k]) | (low[k] & below[g][k])),
-                                               static_cast<int>(qw[g][k]), dot[g][j]);
-                    }
-                }
-                // over the 4 lanes of a group of 64: LPP / 4 pages left, slots `slot` and on
-                const int slot = (lane & 1 ? LPP / 2 : 0) + (lane & 2 ? LPP / 4 : 0);
-                float x[HC][LPP / 4];
-#pragma unroll
-                for (int g = 0; g < HC; ++g) {
-                    fold<LPP>(dot[g], 1, lane);
-                    fold<LPP / 2>(dot[g], 2, lane);
-                }
-#pragma unroll
-                for (int j = 0; j < LPP / 4; ++j) {
-                    const unsigned char *const row = row_of(slot + j);
-                    const float step = row ? *reinterpret_cast<const float *>(row + 2 * D + s / 4 * 4) : 0.f;
-#pragma unroll
-                    for (int g = 0; g < HC; ++g) x[g][j] = __fmul_rn(static_cast<float>(dot[g][j]), step);
-                }
-                // over the groups
-                float best = -INFINITY;
-#pragma unroll
-                for (int g = 0; g < HC; ++g) {
-                    if (LPP >= 8) fold<LPP / 4>(x[g], 4, lane);
-                    if (LPP >= 16) fold<LPP / 8>(x[g], 8, lane);
-                    best = fmaxf(best, __fmul_rn(x[g][0], unit[g]));
-                }
-                const int last = slot + (LPP >= 8 && (lane & 4) ? LPP / 8 : 0) + (LPP >= 16 && (lane & 8) ? LPP / 16 : 0);
-                const int mine = last * PPI + side;
-                if (__shfl_sync(0xffffffffu, id, mine) < 0) best = -INFINITY;
-                if (p0 + mine < n) {
-                    const uint32_t key = ordered(best);
-                    keys[p0 + mine] = g0 == 0 ? key : max(key, keys[p0 + mine]);
-                }
+            for (int j = 0; j < SLOTS; ++j) {
+                const int page = __shfl_sync(0xffffffffu, id, j * PPI + side);
+                const unsigned char *const row = bounds + max(page, 0) * page_bytes;
+                const uint4 up = *reinterpret_cast<const uint4 *>(row + 16 * s), down = *reinterpret_cast<const uint4 *>(row + D + 16 * s);
+                high[j][0] = up.x, high[j][1] = up.y, high[j][2] = up.z, high[j][3] = up.w;
+                low[j][0] = down.x, low[j][1] = down.y, low[j][2] = down.z, low[j][3] = down.w;
             }
+            float best = -INFINITY;
+#pragma unroll 2
+            for (int g = 0; g < G; ++g) {
+                const uint4 c = *reinterpret_cast<const uint4 *>(query + g * (D / 2) + 4 * s);
+                const uint4 m = *reinterpret_cast<const uint4 *>(query + g * (D / 2) + D / 4 + 4 * s);
+                const uint32_t qw[4] = {c.x, c.y, c.z, c.w}, below[4] = {m.x, m.y, m.z, m.w};
+                int dot[SLOTS];
+#pragma unroll
+                for (int j = 0; j < SLOTS; ++j) {
+                    dot[j] = 0;
+#pragma unroll
+                    for (int k = 0; k < 4; ++k)
+                        dot[j] = __dp4a(static_cast<int>((high[j][k] & ~below[k]) | (low[j][k] & below[k])), static_cast<int>(qw[k]), dot[j]);
+                }
+                // (of slot 2 (lane & 1) + (lane >> 1 & 1), over the four lanes of a group)
+                const bool odd = lane & 1, upper = lane & 2;
+                const int a0 = (odd ? dot[2] : dot[0]) + __shfl_xor_sync(0xffffffffu, odd ? dot[0] : dot[2], 1);
+                const int a1 = (odd ? dot[3] : dot[1]) + __shfl_xor_sync(0xffffffffu, odd ? dot[1] : dot[3], 1);
+                const int sum = (upper ? a1 : a0) + __shfl_xor_sync(0xffffffffu, upper ? a0 : a1, 2);
+                float x = __fmul_rn(static_cast<float>(sum), unit_of);
+                if (LPP >= 8) x = __fadd_rn(x, __shfl_xor_sync(0xffffffffu, x, 4));
+                if (LPP >= 16) x = __fadd_rn(x, __shfl_xor_sync(0xffffffffu, x, 8));
+                best = fmaxf(best, __fmul_rn(x, unit[g]));
+            }
+            if (s < 4 && p0 + mine < n) store_first(keys + p0 + mine, ordered(whose < 0 ? -INFINITY : best));
+            id = next;
         }
-        // the `need` largest keys: their smallest by 8 bits at a time, and how many
-        // of those equal to it (the first ones)
-        uint32_t cut = 0, known = 0;
-        int rest = need;
-#pragma unroll 1
-        for (int shift = 24; shift >= 0; shift -= 8) {
-            histogram[tid] = 0;
-            __syncthreads();
-            for (int i = tid; i < n; i += THREADS)
-                if ((keys[i] & known) == cut) atomicAdd(&histogram[keys[i] >> shift & 255u], 1);
-            __syncthreads();
-            if (warp == 0) {  // lane l: the digits 255 - 8 l and the seven below
-                int c[8], sum = 0;
-#pragma unroll
-                for (int e = 0; e < 8; ++e) sum += c[e] = histogram[255 - 8 * lane - e];
-                int at = sum;
-#pragma unroll
-                for (int o = 1; o < 32; o <<= 1) {
-                    const int v = __shfl_up_sync(0xffffffffu, at, o);
-                    if (lane >= o) at += v;
-                }
-                at -= sum;
-#pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    if (at < rest && rest <= at + c[e]) {
-                        pick[0] = 255 - 8 * lane - e;
-                        pick[1] = rest - at;
-                    }
-                    at += c[e];
-                }
+    }
+    __syncwarp();
+    if (ctas > 1) {
+        cluster_arrive();
+        cluster_wait();
+    } else __syncthreads();
+    if (rank == 0) {
+        if (h == 0 && tid == 0)
+            a.lens[t] = p < 0 ? 0 : static_cast<int>(((taken - 1) << a.bs_log2) + (p & ((1 << a.bs_log2) - 1)) + 1);
+        for (int i = taken + tid; i < a.top; i += THREADS) out[i] = -1;
+        for (int i = tid; i < taken; i += THREADS)
+            if (i < few || i >= late) out[i] = id_of(i < few ? i : seen - taken + i);
+        if (need > 0) {
+            const Cut cut = find_cut(keys, n, need, scratch);
+            // in the order of the pages: a warp's share in a row, first counted, then
+            // written
+            int *const sums = scratch;
+            const int share = (n + THREADS - 1) / THREADS * 32, from = warp * share, upto = min(from + share, n);
+            int above = 0, equal = 0;
+            for (int i = from + lane; i - lane < upto; i += 32) {
+                const uint32_t key = i < upto ? keys[i] : 0u;
+                above += __popc(__ballot_sync(0xffffffffu, i < upto && key > cut.key));
+                equal += __popc(__ballot_sync(0xffffffffu, i < upto && key == cut.key));
             }
             __syncthreads();
-            cut |= static_cast<uint32_t>(pick[0]) << shift;
-            known |= 255u << shift;
-            rest = pick[1];
-        }
-        // in the order of the pages: thread i looks at `per` in a row
-        const int per = (n + THREADS - 1) / THREADS, from = min(tid * per, n), upto = min(from + per, n);
-        int above = 0, equal = 0;
-        for (int i = from; i < upto; ++i) {
-            above += keys[i] > cut;
-            equal += keys[i] == cut;
-        }
-        int above_in = above, equal_in = equal;
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const int v = __shfl_up_sync(0xffffffffu, above_in, o), w = __shfl_up_sync(0xffffffffu, equal_in, o);
-            if (lane >= o) above_in += v, equal_in += w;
-        }
-        if (lane == 31) sums[warp] = above_in, sums[WARPS + warp] = equal_in;
-        __syncthreads();
-        int before = above_in - above, ties = equal_in - equal;
-        for (int w = 0; w < warp; ++w) before += sums[w], ties += sums[WARPS + w];
-        for (int i = from; i < upto; ++i) {
-            const uint32_t key = keys[i];
-            if (key > cut || (key == cut && ties < rest)) out[few + before + min(ties, rest)] = id_of(few + i);
-            before += key > cut;
-            ties += key == cut;
+            if (lane == 0) sums[warp] = above, sums[WARPS + warp] = equal;
+            __syncthreads();
+            above = equal = 0;
+            for (int w = 0; w < warp; ++w) above += sums[w], equal += sums[WARPS + w];
+            const unsigned under = (1u << lane) - 1;
+            for (int i = from + lane; i - lane < upto; i += 32) {
+                const uint32_t key = i < upto ? keys[i] : 0u;
+                const unsigned more = __ballot_sync(0xffffffffu, i < upto && key > cut.key);
+                const unsigned same = __ballot_sync(0xffffffffu, i < upto && key == cut.key);
+                const int ties = equal + __popc(same & under);
+                if (i < upto && (key > cut.key || (key == cut.key && ties < cut.equal)))
+                    out[few + above + __popc(more & under) + min(ties, cut.equal)] = id_of(few + i);
+                above += __popc(more);
+                equal += __popc(same);
+            }
         }
     }
     if (bad) atomicOr(a.status, kDevBadIndex);
 }
 
-template <int D, int HC>
-cudaError_t launch_select(const Kv4SelectArgs &a, cudaStream_t st, const DeviceInfo &dev) {
-    const int smem = static_cast<int>((a.max_blocks + 1) * 4);
-    static SmemLimit limit;
-    if (smem > 40 * 1024)
-        if (cudaError_t e = limit.ensure(reinterpret_cast<const void *>(select_kernel<D, HC>), dev.device, smem)) return e;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(static_cast<unsigned>(a.T * a.Hkv));
-    cfg.blockDim = dim3(THREADS);
-    cfg.dynamicSmemBytes = static_cast<size_t>(smem);
-    cfg.stream = st;
-    cudaLaunchAttribute pdl[1];
-    pdl[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    pdl[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = pdl;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, select_kernel<D, HC>, a);
+// CTAs of a cluster: so many that the GPU has eight or more for each SM (contexts
+// are ragged), none with less than a batch of pages for each warp.
+int select_ctas(const Kv4SelectArgs &a, int D, const DeviceInfo &dev) {
+    const int64_t tasks = a.T * a.Hkv, pages = WARPS * 4 * 32 / (D / 16);
+    int ctas = 1;
+    while (ctas < 8 && tasks * ctas < 8 * dev.num_sms && a.max_blocks > pages * ctas) ctas *= 2;
+    return ctas;
 }
 
 template <int D>
 cudaError_t launch_select(const Kv4SelectArgs &a, cudaStream_t st, const DeviceInfo &dev) {
-    const int G = a.Hq / a.Hkv;
-    return G == 1 ? launch_select<D, 1>(a, st, dev) : G == 2 ? launch_select<D, 2>(a, st, dev) : launch_select<D, 4>(a, st, dev);
+    const int G = a.Hq / a.Hkv, ctas = select_ctas(a, D, dev);
+    const int smem = static_cast<int>((a.max_blocks + 3) / 4 * 16 + G * (2 * D + 4));
+    static SmemLimit limit;
+    if (smem > 40 * 1024)
+        if (cudaError_t e = limit.ensure(reinterpret_cast<const void *>(select_kernel<D>), dev.device, smem)) return e;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned>(a.T * a.Hkv * ctas));
+    cfg.blockDim = dim3(THREADS);
+    cfg.dynamicSmemBytes = static_cast<size_t>(smem);
+    cfg.stream = st;
+    cudaLaunchAttribute at[2];
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+    at[1].id = cudaLaunchAttributeClusterDimension;
+    at[1].val.clusterDim.x = static_cast<unsigned>(ctas);
+    at[1].val.clusterDim.y = 1;
+    at[1].val.clusterDim.z = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = 2;
+    return cudaLaunchKernelEx(&cfg, select_kernel<D>, a);
 }
 
 }  // namespace
