@@ -52,6 +52,8 @@ __device__ __forceinline__ void check_lengths(const Kv4AttnArgs &a, int b) {
 
 // The request of token t: the last b with cu[b] <= t, or -1.  By a whole warp.
 __device__ __forceinline__ int request_of(const int32_t *cu, int requests, int64_t t, int lane) {
+    // (number t, where every request has one new token)
+    if (t < requests && cu[t] == t && cu[t + 1] == t + 1) return static_cast<int>(t);
     int lo = 0, hi = requests;
     while (hi - lo > 1) {
         const int step = (hi - lo + 31) / 32, at = lo + lane * step;

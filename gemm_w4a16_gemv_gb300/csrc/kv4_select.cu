@@ -23,17 +23,41 @@ __host__ __device__ constexpr int bounds_bytes(int D) { return 2 * D + 16; }
 
 constexpr int BOUNDS_WARPS = 8;
 
-// A warp takes 32 slots and one key head.  A lane holds 8 elements: D / 8 lanes
-// a token, 256 / D tokens side by side.
+__device__ __forceinline__ float max3(float a, float b, float c) {
+    float d;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+    return d;
+}
+__device__ __forceinline__ float min3(float a, float b, float c) {
+    float d;
+    asm("min.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+    return d;
+}
+// v = x s + k of both halves of a pair x, s binary16.
+__device__ __forceinline__ void fma_f16(uint32_t x, uint32_t s, float k, float &lo, float &hi) {
+    asm("{\n\t.reg .b16 x0, x1, s0, s1;\n\tmov.b32 {x0, x1}, %2;\n\tmov.b32 {s0, s1}, %3;\n\t"
+        "fma.rn.f32.f16 %0, x0, s0, %4;\n\tfma.rn.f32.f16 %1, x1, s0, %4;\n\t}"
+        : "=f"(lo), "=f"(hi)
+        : "r"(x), "r"(s), "f"(k));
+}
+
+// A warp takes `slots` slots and one key head.  A lane holds 8 elements: D / 8
+// lanes a token, 256 / D tokens side by side.
+//
+// A code c masked in place under the exponent of 1024 is the binary16 number 1024 +
+// c, or in the next four bits under that of 64 the number 64 + c, so that a key is
+// one fused multiply-add, exact:
+//   (1024 + c) s - (1024 + z) s   or   (64 + c) s - (64 + z) s,
+// and two tokens enter the extremes with one comparison each way.
 template <int D>
-__global__ void __launch_bounds__(BOUNDS_WARPS * 32) bounds_kernel(const Kv4BoundsArgs a) {
-    constexpr int LANES = D / 8, SIDE = 32 / LANES, TB = kv4_tile_bytes(D);
+__global__ void __launch_bounds__(BOUNDS_WARPS * 32) bounds_kernel(const Kv4BoundsArgs a, const int slots) {
+    constexpr int LANES = D / 8, SIDE = 32 / LANES, HALF = 8 / SIDE, TB = kv4_tile_bytes(D);
     const int lane = threadIdx.x & 31, h = blockIdx.y * BOUNDS_WARPS + (threadIdx.x >> 5);
     pdl_launch_dependents();
     pdl_wait();
     if (h >= a.Hkv) return;
-    const int64_t t = static_cast<int64_t>(blockIdx.x) * 32 + lane;
-    const int64_t slot = t < a.T ? a.slots[t] : -1;
+    const int64_t t = static_cast<int64_t>(blockIdx.x) * slots + lane;
+    const int64_t slot = lane < slots && t < a.T ? a.slots[t] : -1;
     if (slot >= a.num_slots && h == 0) atomicOr(a.status, kDevBadIndex);
     const int64_t size = int64_t(1) << a.bs_log2;
     unsigned full = __ballot_sync(0xffffffffu, slot >= 0 && slot < a.num_slots && (slot & (size - 1)) == size - 1);
@@ -42,26 +66,45 @@ __global__ void __launch_bounds__(BOUNDS_WARPS * 32) bounds_kernel(const Kv4Boun
         const int64_t block = __shfl_sync(0xffffffffu, slot, __ffs(full) - 1) >> a.bs_log2;
         full &= full - 1;
         const unsigned char *tile = a.cache + ((block * a.Hkv + h) << (a.bs_log2 - 4)) * TB;
-        float high[8], low[8];
+        float high[8], low[8];  // of elements 0 4 1 5 2 6 3 7
 #pragma unroll
         for (int e = 0; e < 8; ++e) high[e] = -INFINITY, low[e] = INFINITY;
-#pragma unroll 1
-        for (int n = 0; n < 1 << (a.bs_log2 - 4); ++n, tile += TB) {
-            uint32_t codes[16 / SIDE], para[16 / SIDE];
+        // half a tile's rows at a time, the next ones on their way meanwhile
+        const int steps = 2 << (a.bs_log2 - 4);
+        uint32_t codes[HALF], para[HALF];
+        auto load = [&](int n) {
 #pragma unroll
-            for (int j = 0; j < 16 / SIDE; ++j) {
-                const int row = group * 16 + j * SIDE + side;
-                codes[j] = *reinterpret_cast<const uint32_t *>(tile + row * 32 + i % 8 * 4);
-                para[j] = *reinterpret_cast<const uint32_t *>(tile + 16 * D + row * 4);
+            for (int j = 0; j < HALF; ++j) {
+                const unsigned char *const from = tile + (n >> 1) * TB;
+                const int row = group * 16 + ((n & 1) * HALF + j) * SIDE + side;
+                codes[j] = *reinterpret_cast<const uint32_t *>(from + row * 32 + i % 8 * 4);
+                para[j] = *reinterpret_cast<const uint32_t *>(from + 16 * D + row * 4);
             }
+        };
+        load(0);
+#pragma unroll 1
+        for (int n = 0; n < steps; ++n) {
+            uint32_t w[HALF], p[HALF];
 #pragma unroll
-            for (int j = 0; j < 16 / SIDE; ++j) {
-                const float s = f16_lo(para[j]), z = f16_hi(para[j]);
+            for (int j = 0; j < HALF; ++j) w[j] = codes[j], p[j] = para[j];
+            load(min(n + 1, steps - 1));
+#pragma unroll
+            for (int j = 0; j < HALF; j += 2) {
+                float v[2][8];
+#pragma unroll
+                for (int o = 0; o < 2; ++o) {
+                    const uint32_t u = w[j + o] >> 8;
+                    const float s = f16_lo(p[j + o]), z = f16_hi(p[j + o]);
+                    const float k1024 = -(1024.f + z) * s, k64 = fmaf(960.f, s, k1024);
+                    fma_f16((w[j + o] & 0x000f000fu) | 0x64006400u, p[j + o], k1024, v[o][0], v[o][1]);
+                    fma_f16((w[j + o] & 0x00f000f0u) | 0x54005400u, p[j + o], k64, v[o][2], v[o][3]);
+                    fma_f16((u & 0x000f000fu) | 0x64006400u, p[j + o], k1024, v[o][4], v[o][5]);
+                    fma_f16((u & 0x00f000f0u) | 0x54005400u, p[j + o], k64, v[o][6], v[o][7]);
+                }
 #pragma unroll
                 for (int e = 0; e < 8; ++e) {
-                    const float v = (static_cast<float>(codes[j] >> 4 * e & 15u) - z) * s;  // exact
-                    high[e] = fmaxf(high[e], v);
-                    low[e] = fminf(low[e], v);
+                    high[e] = max3(high[e], v[0][e], v[1][e]);
+                    low[e] = min3(low[e], v[0][e], v[1][e]);
                 }
             }
         }
@@ -81,8 +124,9 @@ __global__ void __launch_bounds__(BOUNDS_WARPS * 32) bounds_kernel(const Kv4Boun
         uint32_t up[2] = {0, 0}, down[2] = {0, 0};
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
-            up[e / 4] |= (static_cast<uint32_t>(__float2int_ru(__fdiv_rn(high[e], by))) & 255u) << 8 * (e % 4);
-            down[e / 4] |= (static_cast<uint32_t>(__float2int_rd(__fdiv_rn(low[e], by))) & 255u) << 8 * (e % 4);
+            const int d = e / 2 + 4 * (e & 1);
+            up[d / 4] |= (static_cast<uint32_t>(__float2int_ru(__fdiv_rn(high[e], by))) & 255u) << 8 * (d % 4);
+            down[d / 4] |= (static_cast<uint32_t>(__float2int_rd(__fdiv_rn(low[e], by))) & 255u) << 8 * (d % 4);
         }
         unsigned char *const row = a.bounds + (block * a.Hkv + h) * bounds_bytes(D);
         if (side == 0) {
@@ -96,7 +140,10 @@ __global__ void __launch_bounds__(BOUNDS_WARPS * 32) bounds_kernel(const Kv4Boun
 template <int D>
 cudaError_t launch_bounds(const Kv4BoundsArgs &a, cudaStream_t st) {
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(static_cast<unsigned>((a.T + 31) / 32), static_cast<unsigned>((a.Hkv + BOUNDS_WARPS - 1) / BOUNDS_WARPS));
+    // few slots: few to a warp, since each may fill a page
+    const int slots = a.T <= 1024 ? 4 : 32;
+    cfg.gridDim = dim3(static_cast<unsigned>((a.T + slots - 1) / slots),
+                       static_cast<unsigned>((a.Hkv + BOUNDS_WARPS - 1) / BOUNDS_WARPS));
     cfg.blockDim = dim3(BOUNDS_WARPS * 32);
     cfg.stream = st;
     cudaLaunchAttribute pdl[1];
@@ -104,7 +151,7 @@ cudaError_t launch_bounds(const Kv4BoundsArgs &a, cudaStream_t st) {
     pdl[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = pdl;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, bounds_kernel<D>, a);
+    return cudaLaunchKernelEx(&cfg, bounds_kernel<D>, a, slots);
 }
 
 // ---------------------------------------------------------------- select
@@ -171,76 +218,106 @@ __device__ __forceinline__ void store_first(uint32_t *p, uint32_t v) {
                  : "memory");
 }
 
+// Words of shared memory of a team: keys, queries, units, scratch.
+__host__ __device__ constexpr int select_words(int width, int G, int D) {
+    return width + G * (D / 2) + (G + 3) / 4 * 4 + (256 + 2 * WARPS + 8);
+}
+
+// A team works on one token and key head: a CTA (with others of its cluster), or a
+// warp where there are tokens enough for that.
+template <bool WARP>
+struct Team {
+    static constexpr int COUNT = WARP ? 32 : THREADS;       // threads
+    __device__ static int thread() { return WARP ? threadIdx.x & 31 : threadIdx.x; }
+    __device__ static int warp() { return WARP ? 0 : threadIdx.x >> 5; }
+    __device__ static void sync() {
+        if (WARP) __syncwarp();
+        else __syncthreads();
+    }
+};
+
 // Key at which the `need` largest of keys[0 .. n) end, and how many of those
-// equal to it are among them; by a whole CTA.  Between the smallest and the
-// largest key a count for each of 256 steps shows the one in which they end; its
-// keys, a few as a rule, are compared with one another, and otherwise counted again
-// in 256 steps of it.
+// equal to it are among them.  Between the smallest and the largest key a count for
+// each of 256 steps shows the one in which they end; its keys, a few as a rule, are
+// compared with one another, and otherwise counted again in 256 steps of it.
 struct Cut {
     uint32_t key;
     int equal;
 };
+template <class T>
 __device__ __forceinline__ Cut find_cut(const uint32_t *keys, int n, int need, int *scratch) {
-    // scratch: [256] counts (then up to as many candidates), [WARPS] sums, the step,
-    // the rest, [2] extremes, a count, the cut
-    int *const count = scratch, *const sums = scratch + 256, *const pick = sums + WARPS;
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    int *const count = scratch, *const ends = scratch + 256, *const pick = ends + 2 * WARPS;
+    const int tid = T::thread(), lane = tid & 31;
     uint32_t low = 0xffffffffu, high = 0;
-    for (int i = tid; i < n; i += THREADS) low = min(low, keys[i]), high = max(high, keys[i]);
+    for (int i = tid; i < n; i += T::COUNT) low = min(low, keys[i]), high = max(high, keys[i]);
     low = __reduce_min_sync(0xffffffffu, low);
     high = __reduce_max_sync(0xffffffffu, high);
-    if (lane == 0) count[warp] = static_cast<int>(low), count[WARPS + warp] = static_cast<int>(high);
-    __syncthreads();
-    for (int w = 0; w < WARPS; ++w) {
-        low = min(low, static_cast<uint32_t>(count[w]));
-        high = max(high, static_cast<uint32_t>(count[WARPS + w]));
+    if (T::COUNT > 32) {
+        if (lane == 0) ends[T::warp()] = static_cast<int>(low), ends[WARPS + T::warp()] = static_cast<int>(high);
+        T::sync();
+        low = static_cast<uint32_t>(ends[lane % WARPS]), high = static_cast<uint32_t>(ends[WARPS + lane % WARPS]);
+        low = __reduce_min_sync(0xffffffffu, low);
+        high = __reduce_max_sync(0xffffffffu, high);
     }
     while (true) {
         const uint32_t span = high - low;
         const int shift = span > 255 ? 24 - __clz(span) : 0;  // (span >> shift is 8 bits)
-        __syncthreads();
-        count[tid] = 0;
-        if (tid == 0) pick[2] = 0;
-        __syncthreads();
-        for (int i = tid; i < n; i += THREADS)
+        for (int i = tid; i < 256; i += T::COUNT) count[i] = 0;
+        if (tid == 0) pick[0] = 0;
+        T::sync();
+        for (int i = tid; i < n; i += T::COUNT)
             if (keys[i] - low <= span) atomicAdd(&count[(keys[i] - low) >> shift], 1);
-        __syncthreads();
-        const int mine = count[255 - tid];  // from the top
-        int in = mine;
+        T::sync();
+        if (T::warp() == 0) {  // lane l: the steps 255 - 8 l and the seven below
+            int c[8], sum = 0;
 #pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const int v = __shfl_up_sync(0xffffffffu, in, o);
-            if (lane >= o) in += v;
+            for (int e = 0; e < 8; ++e) sum += c[e] = count[255 - 8 * lane - e];
+            int at = sum;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const int v = __shfl_up_sync(0xffffffffu, at, o);
+                if (lane >= o) at += v;
+            }
+            if (at - sum < need && need <= at) {
+                at -= sum;
+                int e = 0;
+#pragma unroll
+                for (int k = 0; k < 7; ++k)
+                    if (at + c[k] < need && e == k) at += c[k], e = k + 1;
+                pick[1] = 255 - 8 * lane - e;
+                pick[2] = need - at;
+                pick[3] = count[255 - 8 * lane - e];
+            }
         }
-        if (lane == 31) sums[warp] = in;
-        __syncthreads();
-        for (int w = 0; w < warp; ++w) in += sums[w];
-        if (in - mine < need && need <= in) pick[0] = 255 - tid, pick[1] = need - (in - mine), pick[3] = mine;
-        __syncthreads();
+        T::sync();
         const int held = pick[3];
-        need = pick[1];
-        low += static_cast<uint32_t>(pick[0]) << shift;
+        need = pick[2];
+        low += static_cast<uint32_t>(pick[1]) << shift;
         if (shift == 0) return {low, need};
         high = low + ((1u << shift) - 1u);
-        if (held > 256) continue;
+        if (held > 256) {
+            T::sync();
+            continue;
+        }
         // ---- the candidates against one another
         uint32_t *const list = reinterpret_cast<uint32_t *>(count);
-        for (int i = tid; i < n; i += THREADS)
-            if (keys[i] - low <= high - low) list[atomicAdd(&pick[2], 1)] = keys[i];
-        __syncthreads();
-        if (tid < held) {
-            const uint32_t key = list[tid];
+        for (int i = tid; i < n; i += T::COUNT)
+            if (keys[i] - low <= high - low) list[atomicAdd(&pick[0], 1)] = keys[i];
+        T::sync();
+        for (int j = tid; j < held; j += T::COUNT) {
+            const uint32_t key = list[j];
             int above = 0, equal = 0;
             for (int k = 0; k < held; ++k) above += list[k] > key, equal += list[k] == key;
             if (above < need && need <= above + equal) pick[4] = static_cast<int>(key), pick[5] = need - above;  // (the same of equal ones)
         }
-        __syncthreads();
+        T::sync();
         return {static_cast<uint32_t>(pick[4]), pick[5]};
     }
 }
 
-// A cluster for a token and key head, its CTAs with a share of the pages each;
-// the first one then chooses.
+// The CTAs of a cluster have a share of a token's pages each; the first one then
+// chooses.  A warp alone does both; the warps of a CTA have neighbouring tokens
+// then, which share most of their pages in L1.
 //
 // Score.  A lane holds 16 elements of a page's bounds: D / 16 lanes a page, PPI
 // pages side by side and four (SLOTS) times as many at a time.  Each four lanes
@@ -249,28 +326,35 @@ __device__ __forceinline__ Cut find_cut(const uint32_t *keys, int n, int need, i
 // there are pages and tokens enough; about 45 instructions a query head for 4 PPI
 // pages.  16 bytes of high and of low a lane and slot are on their way at once,
 // 4 KB a warp.
-template <int D>
-__global__ void __launch_bounds__(THREADS, 3) select_kernel(const Kv4SelectArgs a) {
+template <int D, bool WARP>
+__global__ void __launch_bounds__(THREADS, 4) select_kernel(const Kv4SelectArgs a) {
+    using Us = Team<WARP>;
     constexpr int LPP = D / 16, PPI = 32 / LPP, SLOTS = 4, BATCH = SLOTS * PPI;
-    extern __shared__ __align__(16) uint32_t keys[];  // of the pages between the first and the recent ones; then the queries
-    __shared__ int scratch[256 + WARPS + 8];
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int ctas = static_cast<int>(cluster_ctas()), rank = static_cast<int>(cluster_rank());
-    const int64_t task = blockIdx.x / ctas, t = task / a.Hkv;
+    extern __shared__ __align__(16) uint32_t select_smem[];
+    const int tid = Us::thread(), lane = tid & 31, warp = Us::warp();
+    const int ctas = WARP ? 1 : static_cast<int>(cluster_ctas()), rank = WARP ? 0 : static_cast<int>(cluster_rank());
+    const int64_t task = blockIdx.x / ctas;
+    const int64_t t = WARP ? task / a.Hkv * WARPS + (threadIdx.x >> 5) : task / a.Hkv;
     const int h = static_cast<int>(task % a.Hkv), G = a.Hq / a.Hkv;
-    uint32_t *const query = keys + (a.max_blocks + 3) / 4 * 4;    // [G][2][D / 4]: 8 bits an element, and which are negative
-    float *const unit = reinterpret_cast<float *>(query + G * (D / 2));  // [G]
-    cluster_arrive();  // (there, for the other CTAs' stores)
+    // of the pages between the first and the recent ones; [G][2][D / 4] the queries, 8
+    // bits an element, and which are negative; [G] their units; scratch
+    const int width = static_cast<int>((a.max_blocks + 3) / 4 * 4);
+    uint32_t *const keys = select_smem + (WARP ? (threadIdx.x >> 5) * select_words(width, G, D) : 0);
+    uint32_t *const query = keys + width;
+    float *const unit = reinterpret_cast<float *>(query + G * (D / 2));
+    int *const scratch = reinterpret_cast<int *>(unit + (G + 3) / 4 * 4);
+    if (!WARP) cluster_arrive();  // (there, for the other CTAs' stores)
     pdl_launch_dependents();
     pdl_wait();
-    for (int g = warp; g < G; g += WARPS)
-        quantise<D>(a.q + t * a.q_stride + static_cast<int64_t>(h * G + g) * D, query + g * (D / 2), unit[g], lane);
     if (blockIdx.x == 0)
-        for (int b = tid; b < a.requests; b += THREADS) {
+        for (int b = threadIdx.x; b < a.requests; b += THREADS) {
             const int64_t from = a.cu_new[b], to = a.cu_new[b + 1], len = a.seq_lens[b];
             if (from < 0 || to < from || to > a.T || (to > from && (len < 0 || len > a.max_blocks << a.bs_log2)))
                 atomicOr(a.status, kDevBadIndex);
         }
+    if (WARP && t >= a.T) return;
+    for (int g = warp; g < G; g += Us::COUNT / 32)
+        quantise<D>(a.q + t * a.q_stride + static_cast<int64_t>(h * G + g) * D, query + g * (D / 2), unit[g], lane);
     const int b = request_of(a.cu_new, a.requests, t, lane);
     const int64_t cap = a.max_blocks << a.bs_log2;
     const int64_t p = b < 0 ? -1 : min(static_cast<int64_t>(a.seq_lens[b]) - a.cu_new[b + 1] + t, cap - 1);
@@ -288,17 +372,17 @@ __global__ void __launch_bounds__(THREADS, 3) select_kernel(const Kv4SelectArgs 
     const int few = seen > a.top ? a.first : taken, late = taken - (seen > a.top ? a.recent : 0);
     // need of n pages, from number `few` on
     const int need = late - few, n = seen - (taken - need);
-    __syncthreads();
-    cluster_wait();
+    Us::sync();
+    if (!WARP) cluster_wait();
     if (need > 0) {
         const int s = lane % LPP, side = lane / LPP;
-        const int step = ctas * WARPS * BATCH;
+        const int step = ctas * (Us::COUNT / 32) * BATCH;
         // the page whose sums this lane has in the end
         const int mine = (2 * (lane & 1) + (lane >> 1 & 1)) * PPI + side;
         const unsigned char *const bounds = a.bounds + static_cast<int64_t>(h) * bounds_bytes(D);
         const int64_t page_bytes = static_cast<int64_t>(a.Hkv) * bounds_bytes(D);
         auto ids = [&](int p0) { return lane < BATCH && p0 + lane < n ? id_of(few + p0 + lane) : -1; };
-        const int first = (rank * WARPS + warp) * BATCH;
+        const int first = (rank * (Us::COUNT / 32) + warp) * BATCH;
         int id = ids(first);
         for (int p0 = first; p0 < n; p0 += step) {
             const int next = ids(p0 + step);  // on its way meanwhile
@@ -337,7 +421,11 @@ __global__ void __launch_bounds__(THREADS, 3) select_kernel(const Kv4SelectArgs 
                 if (LPP >= 16) x = __fadd_rn(x, __shfl_xor_sync(0xffffffffu, x, 8));
                 best = fmaxf(best, __fmul_rn(x, unit[g]));
             }
-            if (s < 4 && p0 + mine < n) store_first(keys + p0 + mine, ordered(whose < 0 ? -INFINITY : best));
+            if (s < 4 && p0 + mine < n) {
+                const uint32_t key = ordered(whose < 0 ? -INFINITY : best);
+                if (WARP) keys[p0 + mine] = key;
+                else store_first(keys + p0 + mine, key);
+            }
             id = next;
         }
     }
@@ -345,30 +433,32 @@ __global__ void __launch_bounds__(THREADS, 3) select_kernel(const Kv4SelectArgs 
     if (ctas > 1) {
         cluster_arrive();
         cluster_wait();
-    } else __syncthreads();
+    } else Us::sync();
     if (rank == 0) {
         if (h == 0 && tid == 0)
             a.lens[t] = p < 0 ? 0 : static_cast<int>(((taken - 1) << a.bs_log2) + (p & ((1 << a.bs_log2) - 1)) + 1);
-        for (int i = taken + tid; i < a.top; i += THREADS) out[i] = -1;
-        for (int i = tid; i < taken; i += THREADS)
+        for (int i = taken + tid; i < a.top; i += Us::COUNT) out[i] = -1;
+        for (int i = tid; i < taken; i += Us::COUNT)
             if (i < few || i >= late) out[i] = id_of(i < few ? i : seen - taken + i);
         if (need > 0) {
-            const Cut cut = find_cut(keys, n, need, scratch);
-            // in the order of the pages: a warp's share in a row, first counted, then
-            // written
-            int *const sums = scratch;
-            const int share = (n + THREADS - 1) / THREADS * 32, from = warp * share, upto = min(from + share, n);
+            const Cut cut = find_cut<Us>(keys, n, need, scratch);
+            // in the order of the pages: a warp's share in a row, counted first where
+            // there are several
+            const int share = (n + Us::COUNT - 1) / Us::COUNT * 32, from = warp * share, upto = min(from + share, n);
             int above = 0, equal = 0;
-            for (int i = from + lane; i - lane < upto; i += 32) {
-                const uint32_t key = i < upto ? keys[i] : 0u;
-                above += __popc(__ballot_sync(0xffffffffu, i < upto && key > cut.key));
-                equal += __popc(__ballot_sync(0xffffffffu, i < upto && key == cut.key));
+            if (!WARP) {
+                int *const sums = scratch;
+                for (int i = from + lane; i - lane < upto; i += 32) {
+                    const uint32_t key = i < upto ? keys[i] : 0u;
+                    above += __popc(__ballot_sync(0xffffffffu, i < upto && key > cut.key));
+                    equal += __popc(__ballot_sync(0xffffffffu, i < upto && key == cut.key));
+                }
+                Us::sync();
+                if (lane == 0) sums[warp] = above, sums[WARPS + warp] = equal;
+                Us::sync();
+                above = equal = 0;
+                for (int w = 0; w < warp; ++w) above += sums[w], equal += sums[WARPS + w];
             }
-            __syncthreads();
-            if (lane == 0) sums[warp] = above, sums[WARPS + warp] = equal;
-            __syncthreads();
-            above = equal = 0;
-            for (int w = 0; w < warp; ++w) above += sums[w], equal += sums[WARPS + w];
             const unsigned under = (1u << lane) - 1;
             for (int i = from + lane; i - lane < upto; i += 32) {
                 const uint32_t key = i < upto ? keys[i] : 0u;
@@ -394,15 +484,14 @@ int select_ctas(const Kv4SelectArgs &a, int D, const DeviceInfo &dev) {
     return ctas;
 }
 
-template <int D>
-cudaError_t launch_select(const Kv4SelectArgs &a, cudaStream_t st, const DeviceInfo &dev) {
-    const int G = a.Hq / a.Hkv, ctas = select_ctas(a, D, dev);
-    const int smem = static_cast<int>((a.max_blocks + 3) / 4 * 16 + G * (2 * D + 4));
+template <int D, bool WARP>
+cudaError_t launch_select(const Kv4SelectArgs &a, int ctas, cudaStream_t st, const DeviceInfo &dev) {
+    const int words = select_words(static_cast<int>((a.max_blocks + 3) / 4 * 4), a.Hq / a.Hkv, D), smem = (WARP ? WARPS : 1) * words * 4;
     static SmemLimit limit;
     if (smem > 40 * 1024)
-        if (cudaError_t e = limit.ensure(reinterpret_cast<const void *>(select_kernel<D>), dev.device, smem)) return e;
+        if (cudaError_t e = limit.ensure(reinterpret_cast<const void *>(select_kernel<D, WARP>), dev.device, smem)) return e;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(static_cast<unsigned>(a.T * a.Hkv * ctas));
+    cfg.gridDim = dim3(static_cast<unsigned>((WARP ? (a.T + WARPS - 1) / WARPS : a.T) * a.Hkv * ctas));
     cfg.blockDim = dim3(THREADS);
     cfg.dynamicSmemBytes = static_cast<size_t>(smem);
     cfg.stream = st;
@@ -414,8 +503,17 @@ cudaError_t launch_select(const Kv4SelectArgs &a, cudaStream_t st, const DeviceI
     at[1].val.clusterDim.y = 1;
     at[1].val.clusterDim.z = 1;
     cfg.attrs = at;
-    cfg.numAttrs = 2;
-    return cudaLaunchKernelEx(&cfg, select_kernel<D>, a);
+    cfg.numAttrs = WARP ? 1 : 2;
+    return cudaLaunchKernelEx(&cfg, select_kernel<D, WARP>, a);
+}
+
+// A warp for a token and key head where that gives each SM eight warps or more, and
+// their scores leave room for two CTAs.
+template <int D>
+cudaError_t launch_select(const Kv4SelectArgs &a, cudaStream_t st, const DeviceInfo &dev) {
+    const int words = select_words(static_cast<int>((a.max_blocks + 3) / 4 * 4), a.Hq / a.Hkv, D);
+    if (a.T * a.Hkv >= 8 * static_cast<int64_t>(dev.num_sms) && WARPS * words * 4 <= 100 * 1024) return launch_select<D, true>(a, 1, st, dev);
+    return launch_select<D, false>(a, select_ctas(a, D, dev), st, dev);
 }
 
 }  // namespace

@@ -112,6 +112,20 @@ def test_select(Hq, Hkv, D, top, first, recent):
     assert w4.w4a16_check_device_error() == 0
 
 
+@pytest.mark.parametrize("Hq,Hkv,D", [(16, 16, 128), (24, 12, 64), (18, 9, 256)])
+@pytest.mark.parametrize("top,first,recent", [(1, 0, 1), (6, 1, 2), (33, 0, 4)])
+def test_select_for_many_tokens(Hq, Hkv, D, top, first, recent):
+    # a warp for each token and head; rows of no request, scores that are equal
+    torch, w4 = cuda_or_skip()
+    ends, new = [700, 90, 30, 0, 401], [101, 1, 30, 0, 3]
+    q, raw, table, ends, cu = _batch(torch, ends, new, Hq, Hkv, D, 16, D + top, gap=5)
+    raw[table[0, 4:30]] = raw[table[0, 4]]
+    q[20] = 0
+    _same(_select(torch, w4, q, raw, table, ends, cu, 16, top, first, recent),
+          lh.select(q, raw, table, ends, cu, 16, top, first, recent))
+    assert w4.w4a16_check_device_error() == 0
+
+
 @pytest.mark.parametrize("Hq,Hkv,D,ends,bs", [(2, 1, 256, [70000], 16), (4, 1, 128, [40001, 3, 9000], 32), (2, 2, 64, [33000] * 5, 16)])
 def test_select_of_many_pages(Hq, Hkv, D, ends, bs):
     torch, w4 = cuda_or_skip()
