@@ -254,7 +254,7 @@ struct Kv4SelectArgs {
     int64_t q_stride, num_blocks, max_blocks, T;
     int requests, Hq, Hkv, bs_log2, top, first, recent;
 };
-constexpr int64_t KV4_SELECT_PAGES = 49152;  // of a request: their scores lie in one SM's shared memory
+constexpr int64_t KV4_SELECT_PAGES = 32768;  // of a request: their scores lie in one SM's shared memory
 cudaError_t launch_kv4_select(const Kv4SelectArgs &a, int D, cudaStream_t st, const DeviceInfo &dev);
 
 struct SampleArgs {

@@ -157,6 +157,7 @@ cudaError_t launch_bounds(const Kv4BoundsArgs &a, cudaStream_t st) {
 // ---------------------------------------------------------------- select
 
 constexpr int THREADS = 256, WARPS = THREADS / 32;
+constexpr int NO_PAGE = -0x7fffffff - 1;
 
 // Scores in the order of whole numbers.
 __device__ __forceinline__ uint32_t ordered(float x) {
@@ -327,14 +328,14 @@ __device__ __forceinline__ Cut find_cut(const uint32_t *keys, int n, int need, i
 // pages.  16 bytes of high and of low a lane and slot are on their way at once,
 // 4 KB a warp.
 template <int D, bool WARP>
-__global__ void __launch_bounds__(THREADS, 4) select_kernel(const Kv4SelectArgs a) {
+__global__ void __launch_bounds__(THREADS, WARP ? 2 : 3) select_kernel(const Kv4SelectArgs a) {
     using Us = Team<WARP>;
     constexpr int LPP = D / 16, PPI = 32 / LPP, SLOTS = 4, BATCH = SLOTS * PPI;
     extern __shared__ __align__(16) uint32_t select_smem[];
     const int tid = Us::thread(), lane = tid & 31, warp = Us::warp();
     const int ctas = WARP ? 1 : static_cast<int>(cluster_ctas()), rank = WARP ? 0 : static_cast<int>(cluster_rank());
     const int64_t task = blockIdx.x / ctas;
-    const int64_t t = WARP ? task / a.Hkv * WARPS + (threadIdx.x >> 5) : task / a.Hkv;
+    int64_t t = WARP ? task / a.Hkv * WARPS + (threadIdx.x >> 5) : task / a.Hkv;
     const int h = static_cast<int>(task % a.Hkv), G = a.Hq / a.Hkv;
     // of the pages between the first and the recent ones; [G][2][D / 4] the queries, 8
     // bits an element, and which are negative; [G] their units; scratch
@@ -353,6 +354,21 @@ __global__ void __launch_bounds__(THREADS, 4) select_kernel(const Kv4SelectArgs 
                 atomicOr(a.status, kDevBadIndex);
         }
     if (WARP && t >= a.T) return;
+    if (!WARP && a.requests == a.T && a.requests > 1 && a.requests <= THREADS) {
+        // a token each: those of the longest contexts first (62 -> 56 us for 64 ragged ones)
+        int *const lens = scratch;
+        if (tid < a.requests) lens[tid] = a.seq_lens[tid];
+        __syncthreads();
+        if (tid < a.requests) {
+            const int mine = lens[tid];
+            int before = 0;
+            for (int i = 0; i < a.requests; ++i) before += lens[i] > mine || (lens[i] == mine && i < tid);
+            if (before == t) lens[THREADS] = tid;
+        }
+        __syncthreads();
+        t = lens[THREADS];
+        __syncthreads();
+    }
     for (int g = warp; g < G; g += Us::COUNT / 32)
         quantise<D>(a.q + t * a.q_stride + static_cast<int64_t>(h * G + g) * D, query + g * (D / 2), unit[g], lane);
     const int b = request_of(a.cu_new, a.requests, t, lane);
@@ -381,22 +397,57 @@ __global__ void __launch_bounds__(THREADS, 4) select_kernel(const Kv4SelectArgs 
         const int mine = (2 * (lane & 1) + (lane >> 1 & 1)) * PPI + side;
         const unsigned char *const bounds = a.bounds + static_cast<int64_t>(h) * bounds_bytes(D);
         const int64_t page_bytes = static_cast<int64_t>(a.Hkv) * bounds_bytes(D);
-        auto ids = [&](int p0) { return lane < BATCH && p0 + lane < n ? id_of(few + p0 + lane) : -1; };
+        // (looked at when they are used: a test here would wait for them)
+        auto ids = [&](int p0) { return lane < BATCH && p0 + lane < n ? pages[few + p0 + lane] : NO_PAGE; };
+        auto known = [&](int id) {
+            const bool in = id >= 0 && id < a.num_blocks;
+            bad |= !in && id != NO_PAGE;
+            return in ? id : -1;
+        };
         const int first = (rank * (Us::COUNT / 32) + warp) * BATCH;
-        int id = ids(first);
-        for (int p0 = first; p0 < n; p0 += step) {
-            const int next = ids(p0 + step);  // on its way meanwhile
-            const int whose = __shfl_sync(0xffffffffu, id, mine);
-            const float unit_of = *reinterpret_cast<const float *>(bounds + max(whose, 0) * page_bytes + 2 * D + s / 4 * 4);
-            uint32_t high[SLOTS][4], low[SLOTS][4];
+        struct Rows {
+            uint4 high[SLOTS], low[SLOTS];
+            float step;  // of this lane's page and group
+            int whose;
+        };
+        auto load = [&](int id) -> Rows {
+            Rows r;
+            r.whose = __shfl_sync(0xffffffffu, id, mine);
+            r.step = *reinterpret_cast<const float *>(bounds + max(r.whose, 0) * page_bytes + 2 * D + s / 4 * 4);
 #pragma unroll
             for (int j = 0; j < SLOTS; ++j) {
                 const int page = __shfl_sync(0xffffffffu, id, j * PPI + side);
                 const unsigned char *const row = bounds + max(page, 0) * page_bytes;
-                const uint4 up = *reinterpret_cast<const uint4 *>(row + 16 * s), down = *reinterpret_cast<const uint4 *>(row + D + 16 * s);
-                high[j][0] = up.x, high[j][1] = up.y, high[j][2] = up.z, high[j][3] = up.w;
-                low[j][0] = down.x, low[j][1] = down.y, low[j][2] = down.z, low[j][3] = down.w;
+                r.high[j] = *reinterpret_cast<const uint4 *>(row + 16 * s);
+                r.low[j] = *reinterpret_cast<const uint4 *>(row + D + 16 * s);
             }
+            return r;
+        };
+        // the ids of the next pages are on their way meanwhile; to a warp alone, which
+        // has fewer others beside it on the SM, their rows too
+        int raw = ids(first);
+        Rows rows;
+        if (WARP) {
+            rows = load(known(raw));
+            raw = ids(first + step);
+        }
+        for (int p0 = first; p0 < n; p0 += step) {
+            Rows next;
+            if (WARP) {
+                next = load(known(raw));
+                raw = ids(p0 + 2 * step);
+            } else {
+                rows = load(known(raw));
+                raw = ids(p0 + step);
+            }
+            uint32_t high[SLOTS][4], low[SLOTS][4];
+#pragma unroll
+            for (int j = 0; j < SLOTS; ++j) {
+                high[j][0] = rows.high[j].x, high[j][1] = rows.high[j].y, high[j][2] = rows.high[j].z, high[j][3] = rows.high[j].w;
+                low[j][0] = rows.low[j].x, low[j][1] = rows.low[j].y, low[j][2] = rows.low[j].z, low[j][3] = rows.low[j].w;
+            }
+            const float unit_of = rows.step;
+            const int whose = rows.whose;
             float best = -INFINITY;
 #pragma unroll 2
             for (int g = 0; g < G; ++g) {
@@ -426,7 +477,7 @@ __global__ void __launch_bounds__(THREADS, 4) select_kernel(const Kv4SelectArgs 
                 if (WARP) keys[p0 + mine] = key;
                 else store_first(keys + p0 + mine, key);
             }
-            id = next;
+            if (WARP) rows = next;
         }
     }
     __syncwarp();
@@ -475,12 +526,14 @@ __global__ void __launch_bounds__(THREADS, 4) select_kernel(const Kv4SelectArgs 
     if (bad) atomicOr(a.status, kDevBadIndex);
 }
 
-// CTAs of a cluster: so many that the GPU has eight or more for each SM (contexts
-// are ragged), none with less than a batch of pages for each warp.
+// CTAs of a cluster: so many that the GPU has four or more for each SM, none with
+// less than a batch of pages for each warp.  16 query heads of 256 on 8, with 1 / 2 /
+// 4 / 8 CTAs: one request of 2048 pages 27 / 17 / 12 / 10 us, 64 of 63 to 3750 pages
+// 83 / 56 / 63 / 79 us.
 int select_ctas(const Kv4SelectArgs &a, int D, const DeviceInfo &dev) {
     const int64_t tasks = a.T * a.Hkv, pages = WARPS * 4 * 32 / (D / 16);
     int ctas = 1;
-    while (ctas < 8 && tasks * ctas < 8 * dev.num_sms && a.max_blocks > pages * ctas) ctas *= 2;
+    while (ctas < 8 && tasks * ctas < 4 * dev.num_sms && a.max_blocks > pages * ctas) ctas *= 2;
     return ctas;
 }
 
@@ -508,7 +561,8 @@ cudaError_t launch_select(const Kv4SelectArgs &a, int ctas, cudaStream_t st, con
 }
 
 // A warp for a token and key head where that gives each SM eight warps or more, and
-// their scores leave room for two CTAs.
+// their scores leave room for two CTAs: 301 tokens with 470 pages, 32 heads of 128 on
+// 8, 45 us, with CTAs 62.
 template <int D>
 cudaError_t launch_select(const Kv4SelectArgs &a, cudaStream_t st, const DeviceInfo &dev) {
     const int words = select_words(static_cast<int>((a.max_blocks + 3) / 4 * 4), a.Hq / a.Hkv, D);

@@ -597,7 +597,7 @@ int kv4_bounds(const uint8_t *cache, int64_t num_blocks, int block_size,
  * Positions past a row of the block table set the device status and count as its
  * last token; a block id outside [0, num_blocks) that is looked at sets it, has
  * the lowest score and is -1 in the table.  top >= first + recent, recent >= 1;
- * max_blocks and top <= 49152, Hq / Hkv <= 32, T * Hkv < 2^28; T = 0 launches
+ * max_blocks and top <= 32768, Hq / Hkv <= 32, T * Hkv < 2^28; T = 0 launches
  * nothing.  One launch, no scratch.
  */
 int kv4_select(const uint16_t *q, int64_t q_stride, const uint8_t *bounds,

@@ -29,8 +29,8 @@ def test_select_refusals(lib):
     _vary(call, good, GRID + ROWS + [
         ({"bounds": None}, 1), ({"bounds": A + 8}, 3), ({"table": None}, 1), ({"seq": None}, 1), ({"cu": A + 2}, 3),
         ({"tables": None}, 1), ({"lens": None}, 1), ({"lens": A + 1}, 3), ({"tables": A + 2}, 3), ({"top": 0}, 1),
-        ({"top": 2}, 1), ({"first": -1}, 1), ({"recent": 0}, 1), ({"first": 0x7fffffff}, 1), ({"top": 49153}, 2),
-        ({"maxb": 49153}, 2), ({"maxb": 0}, 1), ({"maxb": 1 << 62}, 2), ({"B": 0}, 1), ({"B": 4097}, 2)])
+        ({"top": 2}, 1), ({"first": -1}, 1), ({"recent": 0}, 1), ({"first": 0x7fffffff}, 1), ({"top": 32769}, 2),
+        ({"maxb": 32769}, 2), ({"maxb": 0}, 1), ({"maxb": 1 << 62}, 2), ({"B": 0}, 1), ({"B": 4097}, 2)])
     assert call(**dict(good, Hq=264, sq=1 << 18)) == 2      # 33 query heads to a key head
     # more CTAs than a grid has
     assert call(**dict(good, T=1 << 24, Hq=1024, Hkv=1024, sq=1 << 18)) == 2
