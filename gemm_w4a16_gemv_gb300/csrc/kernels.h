@@ -211,9 +211,10 @@ struct Kv4SharedArgs : Kv4AttnArgs {
     float *values;    // [places, D] weighted values
 };
 cudaError_t launch_kv4_prompt(const Kv4SharedArgs &a, int D, cudaStream_t st, const DeviceInfo &dev);
-// The parts of a group's shared stretch: `parts` of them, `step` places apart.
+// A shared stretch's rows: from new token `token` on, `before` rows of other
+// stretches before them; `parts` parts of each, `step` places apart.
 struct alignas(16) Kv4Share {
-    int token, parts;
+    int token, before, parts;
     int64_t place, step;
 };
 // The arguments of a call besides.
@@ -222,8 +223,8 @@ struct Kv4PrefixArgs : Kv4SharedArgs {
     // the plan, to be written: of `stretches`, `pieces`, `items_before`, `counts`,
     Kv4Stretch *plan, *cut;
     int32_t *before, *count;
-    Kv4Share *shares;     // [groups]
-    int32_t *group_of;    // [members] group whose shared stretch a request has, or -1
+    Kv4Share *shares;     // [groups] of the groups that share: count[1], with count[2] tokens
+    int32_t *piece_of;    // [members]
     int groups, members;  // members: the call's requests
     int most_pieces;      // there is room for
     int64_t places, max_group;

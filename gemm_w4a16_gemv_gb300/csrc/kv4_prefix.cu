@@ -165,6 +165,8 @@ __global__ void __launch_bounds__(PLAN_THREADS) plan_kernel(const Kv4PrefixArgs 
         cut = __shfl_sync(0xffffffffu, cut, 0);
         if (lane == 0) cut_tiles = cut;
         long long at = 0, place = a.T * a.Hq;  // (places of the requests' own come first)
+        long long joined = 0;
+        int shares = 0;
         auto before = [&](long long v, long long &total) {
             long long in = v;
 #pragma unroll
@@ -183,7 +185,7 @@ __global__ void __launch_bounds__(PLAN_THREADS) plan_kernel(const Kv4PrefixArgs 
                 const long long mine = before(many ? 1ll << 40 | static_cast<long long>(blocks(rows, a.item_rows)) * a.Hkv : 0, at);
                 if (many) {
                     a.before[mine >> 40] = static_cast<int>(mine & ((1ll << 40) - 1));
-                    a.group_of[b] = static_cast<int>(mine >> 40);  // (its piece, for now)
+                    a.piece_of[b] = static_cast<int>(mine >> 40);
                 }
             }
         for (int g0 = 0; g0 < a.groups; g0 += 32) {
@@ -197,16 +199,20 @@ __global__ void __launch_bounds__(PLAN_THREADS) plan_kernel(const Kv4PrefixArgs 
                 parts = (tiles + even - 1) / even;
             }
             const long long step = on ? static_cast<long long>(x.cu[x.border[g + 1]] - x.cu[x.border[g]]) * a.Hq : 0;
-            const long long p = before(parts * step, place);
+            const long long p = before(parts * step, place), tokens_before = before(step, joined) / a.Hq;
             const long long n = before(weight ? static_cast<long long>(parts) << 40 | static_cast<long long>(parts) * weight : 0, at);
+            const unsigned some = __ballot_sync(0xffffffffu, on);
             if (on) {
                 x.place[g] = p;
                 x.piece[g] = n;
-                a.shares[g] = {x.cu[x.border[g]], parts, p, step};
+                a.shares[shares + __popc(some & ((1u << lane) - 1))] = {x.cu[x.border[g]], static_cast<int>(tokens_before), parts, p, step};
             }
+            shares += __popc(some);
         }
         if (lane == 0) {
             a.count[0] = static_cast<int>(at >> 40);
+            a.count[1] = shares;
+            a.count[2] = static_cast<int>(joined / a.Hq);
             a.before[at >> 40] = static_cast<int>(at & ((1ll << 40) - 1));
         }
     }
@@ -254,69 +260,73 @@ __global__ void __launch_bounds__(PLAN_THREADS) plan_kernel(const Kv4PrefixArgs 
         s.row = b;
         s.place = s.from > 0 ? static_cast<int64_t>(s.token) * a.Hq : -1;
         if (s.tokens * G >= least_own) {
-            a.cut[a.group_of[b]] = s;
+            a.cut[a.piece_of[b]] = s;
             s.tokens = 0;
         }
         a.plan[a.groups + b] = s;
-        a.group_of[b] = s.from > 0 ? g : -1;
     }
 }
 
-// Four dimensions of a row a thread, JOIN_THREADS of a token's Hq D / 4 a CTA.
+// Four dimensions of a row a thread, JOIN_THREADS of a token's Hq D / 4 a CTA, which
+// goes from one token of the shared stretches to the next; and the rows of no request.
 template <int D>
 __global__ void __launch_bounds__(JOIN_THREADS) join_kernel(const Kv4PrefixArgs a) {
     const int lane = threadIdx.x & 31;
-    const int64_t t = blockIdx.x;
     const int at = blockIdx.y * JOIN_THREADS + threadIdx.x;
     pdl_launch_dependents();
     pdl_wait();
-    const int b = request_of(a.cu_new, a.members, t, lane);
-    if (at >= a.Hq * (D / 4)) return;
+    const int shares = a.counts[1], tokens = a.counts[2];
     const int head = at / (D / 4), d = at % (D / 4) * 4;
-    uint16_t *const to = a.out + (t * a.Hq + head) * D + d;
-    if (b < 0) {  // of no request
-        *reinterpret_cast<uint2 *>(to) = make_uint2(0, 0);
-        return;
-    }
-    const int g = a.group_of[b];
-    if (g < 0) return;  // written by the kernel of its only stretch
-    const Kv4Share s = a.shares[g];
-    const int64_t own = t * a.Hq + head, first = s.place + (t - s.token) * a.Hq + head;
-    float2 w = __ldcg(a.weights + own);
-    float4 v = __ldcg(reinterpret_cast<const float4 *>(a.values + own * D + d));
-    float m = w.x, l = w.y;
-    // AHEAD parts at a time, all on their way together
-    for (int i0 = 0; i0 < s.parts; i0 += AHEAD) {
-        float2 wi[AHEAD];
-        float4 vi[AHEAD];
-#pragma unroll
-        for (int i = 0; i < AHEAD; ++i) {
-            const int64_t at = first + min(i0 + i, s.parts - 1) * s.step;
-            wi[i] = __ldcg(a.weights + at);
-            vi[i] = __ldcg(reinterpret_cast<const float4 *>(a.values + at * D + d));
+    const bool on = at < a.Hq * (D / 4);
+    for (int64_t t = rows_before(a, a.members) + blockIdx.x; on && t < a.T; t += gridDim.x)
+        *reinterpret_cast<uint2 *>(a.out + (t * a.Hq + head) * D + d) = make_uint2(0, 0);
+    for (int i = blockIdx.x; i < tokens; i += gridDim.x) {
+        int lo = 0, hi = shares;  // the last with `before` <= i
+        while (hi - lo > 1) {
+            const int step = (hi - lo + 31) / 32, k = lo + lane * step;
+            const unsigned below = __ballot_sync(0xffffffffu, k < hi && a.shares[k < hi ? k : lo].before <= i);
+            lo += max(__popc(below) - 1, 0) * step;
+            hi = min(hi, lo + step);
         }
-        float up = m;
+        if (!on) continue;
+        const Kv4Share s = a.shares[lo];
+        const int64_t t = s.token + (i - s.before), own = t * a.Hq + head, first = s.place + static_cast<int64_t>(i - s.before) * a.Hq + head;
+        float2 w = __ldcg(a.weights + own);
+        float4 v = __ldcg(reinterpret_cast<const float4 *>(a.values + own * D + d));
+        float m = w.x, l = w.y;
+        // AHEAD parts at a time, all on their way together
+        for (int i0 = 0; i0 < s.parts; i0 += AHEAD) {
+            float2 wi[AHEAD];
+            float4 vi[AHEAD];
 #pragma unroll
-        for (int i = 0; i < AHEAD; ++i) up = fmaxf(up, wi[i].x);
-        const float old = ex2(m - up);
-        m = up;
-        l *= old;
-        v.x *= old, v.y *= old, v.z *= old, v.w *= old;
+            for (int k = 0; k < AHEAD; ++k) {
+                const int64_t part = first + min(i0 + k, s.parts - 1) * s.step;
+                wi[k] = __ldcg(a.weights + part);
+                vi[k] = __ldcg(reinterpret_cast<const float4 *>(a.values + part * D + d));
+            }
+            float up = m;
 #pragma unroll
-        for (int i = 0; i < AHEAD; ++i) {
-            const float f = i0 + i < s.parts ? ex2(wi[i].x - m) : 0.f;
-            l = fmaf(f, wi[i].y, l);
-            v.x = fmaf(f, vi[i].x, v.x);
-            v.y = fmaf(f, vi[i].y, v.y);
-            v.z = fmaf(f, vi[i].z, v.z);
-            v.w = fmaf(f, vi[i].w, v.w);
+            for (int k = 0; k < AHEAD; ++k) up = fmaxf(up, wi[k].x);
+            const float old = ex2(m - up);
+            m = up;
+            l *= old;
+            v.x *= old, v.y *= old, v.z *= old, v.w *= old;
+#pragma unroll
+            for (int k = 0; k < AHEAD; ++k) {
+                const float f = i0 + k < s.parts ? ex2(wi[k].x - m) : 0.f;
+                l = fmaf(f, wi[k].y, l);
+                v.x = fmaf(f, vi[k].x, v.x);
+                v.y = fmaf(f, vi[k].y, v.y);
+                v.z = fmaf(f, vi[k].z, v.z);
+                v.w = fmaf(f, vi[k].w, v.w);
+            }
         }
+        const float inv = l == 0.f ? 0.f : 1.f / l;
+        const float o[4] = {v.x * inv, v.y * inv, v.z * inv, v.w * inv};
+        *reinterpret_cast<uint2 *>(a.out + own * D + d) =
+            make_uint2(static_cast<uint32_t>(f32_to_bf16_bits(o[0])) | static_cast<uint32_t>(f32_to_bf16_bits(o[1])) << 16,
+                       static_cast<uint32_t>(f32_to_bf16_bits(o[2])) | static_cast<uint32_t>(f32_to_bf16_bits(o[3])) << 16);
     }
-    const float inv = l == 0.f ? 0.f : 1.f / l;
-    const float o[4] = {v.x * inv, v.y * inv, v.z * inv, v.w * inv};
-    *reinterpret_cast<uint2 *>(to) =
-        make_uint2(static_cast<uint32_t>(f32_to_bf16_bits(o[0])) | static_cast<uint32_t>(f32_to_bf16_bits(o[1])) << 16,
-                   static_cast<uint32_t>(f32_to_bf16_bits(o[2])) | static_cast<uint32_t>(f32_to_bf16_bits(o[3])) << 16);
 }
 
 // Borders and prefixes out of range, where nothing else looks at them.
@@ -363,8 +373,8 @@ int64_t kv4_prefix_scratch(int64_t T, int requests, int groups, int Hq, int Hkv,
     };
     const int64_t plan = take((static_cast<int64_t>(groups) + requests) * sizeof(Kv4Stretch));
     const int64_t cut = take(most_pieces * static_cast<int64_t>(sizeof(Kv4Stretch)));
-    const int64_t before = take(4 * (static_cast<int64_t>(most_pieces) + 1)), count = take(4);
-    const int64_t shares = take(groups * static_cast<int64_t>(sizeof(Kv4Share))), group_of = take(4 * static_cast<int64_t>(requests));
+    const int64_t before = take(4 * (static_cast<int64_t>(most_pieces) + 1)), count = take(12);
+    const int64_t shares = take(groups * static_cast<int64_t>(sizeof(Kv4Share))), piece_of = take(4 * static_cast<int64_t>(requests));
     const int64_t weights = take(places * sizeof(float2)), values = take(places * D * 4);
     if (a) {
         unsigned char *const p = a->scratch;
@@ -373,7 +383,7 @@ int64_t kv4_prefix_scratch(int64_t T, int requests, int groups, int Hq, int Hkv,
         a->items_before = a->before = reinterpret_cast<int32_t *>(p + before);
         a->counts = a->count = reinterpret_cast<int32_t *>(p + count);
         a->shares = reinterpret_cast<Kv4Share *>(p + shares);
-        a->group_of = reinterpret_cast<int32_t *>(p + group_of);
+        a->piece_of = reinterpret_cast<int32_t *>(p + piece_of);
         a->weights = reinterpret_cast<float2 *>(p + weights);
         a->values = reinterpret_cast<float *>(p + values);
         a->places = places;
@@ -414,7 +424,7 @@ cudaError_t launch_kv4_prefix(const Kv4PrefixArgs &args, int D, cudaStream_t st,
         s.requests = a.most_pieces;
         if (cudaError_t e = launch_kv4_prompt(s, D, st, dev)) return e;
     }
-    // the others by the form for few rows, and those with more of them by another
+    // the others; by two forms where most requests have few rows (most are decoded)
     s.requests = a.groups + a.members;
     const int64_t small = D == 256 ? 2 : D == 128 ? 4 : 8;
     int64_t most = own < few_own || !tensor ? own : few_own;
@@ -422,14 +432,16 @@ cudaError_t launch_kv4_prefix(const Kv4PrefixArgs &args, int D, cudaStream_t st,
     if (most_shared > most) most = most_shared;
     s.rows_least = 1;
     s.rows_most = NONE_OF;
-    if (most > small && G <= small) {
+    if (most > small && G <= small && (own <= small || own > few_own)) {
         s.rows_most = static_cast<int>(small);
         if (cudaError_t e = stream(s, D, small, st, dev)) return e;
         s.rows_least = s.rows_most + 1;
         s.rows_most = NONE_OF;
     }
     if (cudaError_t e = stream(s, D, most, st, dev)) return e;
-    const dim3 grid(static_cast<unsigned>(a.T), static_cast<unsigned>((a.Hq * (D / 4) + JOIN_THREADS - 1) / JOIN_THREADS));
+    const unsigned wide = static_cast<unsigned>((a.Hq * (D / 4) + JOIN_THREADS - 1) / JOIN_THREADS);
+    const unsigned rows = 8u * static_cast<unsigned>(dev.num_sms) / wide + 1;
+    const dim3 grid(a.T < rows ? static_cast<unsigned>(a.T) : rows, wide);
     const void *const join = D == 64    ? reinterpret_cast<const void *>(join_kernel<64>)
                              : D == 128 ? reinterpret_cast<const void *>(join_kernel<128>)
                                         : reinterpret_cast<const void *>(join_kernel<256>);
