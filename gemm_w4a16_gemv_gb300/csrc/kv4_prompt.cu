@@ -525,6 +525,7 @@ __global__ void __launch_bounds__(THREADS, 1) attn_prompt_kernel(const Args a) {
         const int r = tid;
         const uint32_t t_row = tmem + (static_cast<uint32_t>(warp * 32) << 16);
         int g = 0;  // key tiles so far, over all items
+        constexpr bool AHEAD = Args::kShared;  // the next scores are on their way while these are worked on
         const int window = static_cast<int>(min(a.window, int64_t(0x7fffffff)));
         const int sinks = a.window > 0 ? static_cast<int>(min(a.sinks, int64_t(0x7fffffff))) : 0;
         for (int k_item = 0;; ++k_item) {
@@ -622,11 +623,24 @@ __global__ void __launch_bounds__(THREADS, 1) attn_prompt_kernel(const Args a) {
                     }
                     tmem_st_32x32b_x16(t_s + 16 * c, w);
                 };
+                if (AHEAD) {
+                    uint32_t x1[32];
 #pragma unroll 1
-                for (int c = 0; c < 4; ++c) {
-                    if (c > 0) tmem_ld_32x32b_x32(t_s + 32 * c, x0);
-                    arrived(x0);
-                    weigh(x0, c);
+                    for (int c = 0; c < 4; c += 2) {
+                        arrived(x0);
+                        tmem_ld_32x32b_x32(t_s + 32 * c + 32, x1);
+                        weigh(x0, c);
+                        arrived(x1);
+                        if (c == 0) tmem_ld_32x32b_x32(t_s + 64, x0);
+                        weigh(x1, c + 1);
+                    }
+                } else {
+#pragma unroll 1
+                    for (int c = 0; c < 4; ++c) {
+                        if (c > 0) tmem_ld_32x32b_x32(t_s + 32 * c, x0);
+                        arrived(x0);
+                        weigh(x0, c);
+                    }
                 }
                 if (__any_sync(0xffffffffu, m != M)) {
                     l *= scaled;
