@@ -207,15 +207,18 @@ struct Kv4SharedArgs : Kv4AttnArgs {
     const Kv4Stretch *stretches;  // those that are streamed,
     const Kv4Stretch *pieces;     // those of many rows, in pieces: counts[0] of them,
     const int32_t *items_before, *counts;  // [pieces + 1] items before each
+    float *partials;  // the parts of a launch's split rows; the launch's number, 0 or 1
+    int launch;
     float2 *weights;  // [places] maximum (of base-2 exponents) and sum of the weights
     float *values;    // [places, D] weighted values
 };
 cudaError_t launch_kv4_prompt(const Kv4SharedArgs &a, int D, cudaStream_t st, const DeviceInfo &dev);
-// A shared stretch's rows: from new token `token` on, `before` rows of other
-// stretches before them; `parts` parts of each, `step` places apart.
+// Rows to be joined: of the new tokens from `token` on, with `before` tokens of
+// other such stretches before them; beside each one's own part `parts` of a shared
+// stretch, `step` places apart.
 struct alignas(16) Kv4Share {
-    int token, before, parts;
-    int64_t place, step;
+    int64_t before, place, step;
+    int token, parts;
 };
 // The arguments of a call besides.
 struct Kv4PrefixArgs : Kv4SharedArgs {
@@ -223,7 +226,9 @@ struct Kv4PrefixArgs : Kv4SharedArgs {
     // the plan, to be written: of `stretches`, `pieces`, `items_before`, `counts`,
     Kv4Stretch *plan, *cut;
     int32_t *before, *count;
-    Kv4Share *shares;     // [groups] of the groups that share: count[1], with count[2] tokens
+    Kv4Share *shares;     // [groups + members]: count[1] of them, with joined[0] tokens
+    int64_t *joined;
+    float *both_partials[2];
     int32_t *piece_of;    // [members]
     int groups, members;  // members: the call's requests
     int most_pieces;      // there is room for

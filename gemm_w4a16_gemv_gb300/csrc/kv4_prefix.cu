@@ -20,7 +20,7 @@ namespace {
 constexpr int PLAN_THREADS = 1024;
 constexpr int JOIN_THREADS = 256;
 constexpr int64_t SMALL = 64 << 20;  // bytes of the cache that all requests can name
-constexpr int AHEAD = 4;       // parts that a thread of the join asks for together
+constexpr int AHEAD = 8;       // parts that a thread of the join asks for together
 constexpr int KEYS = 128;      // of a key tile of the tensor cores' kernel
 constexpr int ROUNDS = 4;      // items to a worker at most, where stretches are cut
 constexpr int OVERHEAD = 4;    // cost of an item beside its key tiles, in key tiles,
@@ -205,14 +205,23 @@ __global__ void __launch_bounds__(PLAN_THREADS) plan_kernel(const Kv4PrefixArgs 
             if (on) {
                 x.place[g] = p;
                 x.piece[g] = n;
-                a.shares[shares + __popc(some & ((1u << lane) - 1))] = {x.cu[x.border[g]], static_cast<int>(tokens_before), parts, p, step};
+                a.shares[shares + __popc(some & ((1u << lane) - 1))] = {tokens_before, p, step, x.cu[x.border[g]], parts};
             }
+            shares += __popc(some);
+        }
+        // requests that share nothing and are streamed: some of their rows may be split
+        for (int b0 = 0; b0 < a.members; b0 += 32) {
+            const int b = b0 + lane, n = b < a.members ? x.cu[b + 1] - x.cu[b] : 0;
+            const bool on = n > 0 && n * G < least_own && (x.owner[b] < 0 || x.shared[x.owner[b]] == 0);
+            const unsigned some = __ballot_sync(0xffffffffu, on);
+            const long long tokens_before = before(on ? static_cast<long long>(n) * a.Hq : 0, joined) / a.Hq;
+            if (on) a.shares[shares + __popc(some & ((1u << lane) - 1))] = {tokens_before, 0, 0, x.cu[b], 0};
             shares += __popc(some);
         }
         if (lane == 0) {
             a.count[0] = static_cast<int>(at >> 40);
             a.count[1] = shares;
-            a.count[2] = static_cast<int>(joined / a.Hq);
+            a.joined[0] = joined / a.Hq;
             a.before[at >> 40] = static_cast<int>(at & ((1ll << 40) - 1));
         }
     }
@@ -275,12 +284,13 @@ __global__ void __launch_bounds__(JOIN_THREADS) join_kernel(const Kv4PrefixArgs 
     const int at = blockIdx.y * JOIN_THREADS + threadIdx.x;
     pdl_launch_dependents();
     pdl_wait();
-    const int shares = a.counts[1], tokens = a.counts[2];
+    const int shares = a.counts[1];
+    const int64_t tokens = *a.joined;
     const int head = at / (D / 4), d = at % (D / 4) * 4;
     const bool on = at < a.Hq * (D / 4);
     for (int64_t t = rows_before(a, a.members) + blockIdx.x; on && t < a.T; t += gridDim.x)
         *reinterpret_cast<uint2 *>(a.out + (t * a.Hq + head) * D + d) = make_uint2(0, 0);
-    for (int i = blockIdx.x; i < tokens; i += gridDim.x) {
+    for (int64_t i = blockIdx.x; i < tokens; i += gridDim.x) {
         int lo = 0, hi = shares;  // the last with `before` <= i
         while (hi - lo > 1) {
             const int step = (hi - lo + 31) / 32, k = lo + lane * step;
@@ -290,40 +300,58 @@ __global__ void __launch_bounds__(JOIN_THREADS) join_kernel(const Kv4PrefixArgs 
         }
         if (!on) continue;
         const Kv4Share s = a.shares[lo];
-        const int64_t t = s.token + (i - s.before), own = t * a.Hq + head, first = s.place + static_cast<int64_t>(i - s.before) * a.Hq + head;
-        float2 w = __ldcg(a.weights + own);
-        float4 v = __ldcg(reinterpret_cast<const float4 *>(a.values + own * D + d));
-        float m = w.x, l = w.y;
-        // AHEAD parts at a time, all on their way together
-        for (int i0 = 0; i0 < s.parts; i0 += AHEAD) {
-            float2 wi[AHEAD];
-            float4 vi[AHEAD];
+        const int64_t row = static_cast<int64_t>(s.token + (i - s.before)) * a.Hq + head;  // of the output, and place of its own part
+        const int64_t first = s.place + (i - s.before) * a.Hq + head;
+        float m = NONE, l = 0.f;
+        float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+        // n parts, given their weights and values: AHEAD at a time, all on their way together
+        auto add = [&](int n, auto weights_of, auto values_of) {
+            for (int k0 = 0; k0 < n; k0 += AHEAD) {
+                float2 w[AHEAD];
+                float4 x[AHEAD];
 #pragma unroll
-            for (int k = 0; k < AHEAD; ++k) {
-                const int64_t part = first + min(i0 + k, s.parts - 1) * s.step;
-                wi[k] = __ldcg(a.weights + part);
-                vi[k] = __ldcg(reinterpret_cast<const float4 *>(a.values + part * D + d));
+                for (int k = 0; k < AHEAD; ++k) {
+                    w[k] = __ldcg(weights_of(min(k0 + k, n - 1)));
+                    x[k] = __ldcg(reinterpret_cast<const float4 *>(values_of(min(k0 + k, n - 1))));
+                }
+                float up = m;
+#pragma unroll
+                for (int k = 0; k < AHEAD; ++k) up = fmaxf(up, w[k].x);
+                const float old = ex2(m - up);
+                m = up;
+                l *= old;
+                v.x *= old, v.y *= old, v.z *= old, v.w *= old;
+#pragma unroll
+                for (int k = 0; k < AHEAD; ++k) {
+                    const float f = k0 + k < n ? ex2(w[k].x - m) : 0.f;
+                    l = fmaf(f, w[k].y, l);
+                    v.x = fmaf(f, x[k].x, v.x);
+                    v.y = fmaf(f, x[k].y, v.y);
+                    v.z = fmaf(f, x[k].z, v.z);
+                    v.w = fmaf(f, x[k].w, v.w);
+                }
             }
-            float up = m;
-#pragma unroll
-            for (int k = 0; k < AHEAD; ++k) up = fmaxf(up, wi[k].x);
-            const float old = ex2(m - up);
-            m = up;
-            l *= old;
-            v.x *= old, v.y *= old, v.z *= old, v.w *= old;
-#pragma unroll
-            for (int k = 0; k < AHEAD; ++k) {
-                const float f = i0 + k < s.parts ? ex2(wi[k].x - m) : 0.f;
-                l = fmaf(f, wi[k].y, l);
-                v.x = fmaf(f, vi[k].x, v.x);
-                v.y = fmaf(f, vi[k].y, v.y);
-                v.z = fmaf(f, vi[k].z, v.z);
-                v.w = fmaf(f, vi[k].w, v.w);
+        };
+        // n of the arrays' parts from `at` on, or what teams left of the first one (w: what its place holds)
+        auto add_at = [&](float2 w, int64_t at, int n, int64_t step) {
+            if (w.y >= 0.f) {
+                add(n, [&](int k) { return a.weights + at + k * step; }, [&](int k) { return a.values + (at + k * step) * D + d; });
+                return;
             }
-        }
+            // (kv4_stream.cuh: of a team two places for a row block, the second where it
+            // begins)
+            const int what = __float_as_int(w.x), rows = what & 31;
+            const float *const from = a.both_partials[what >> 22] + (what >> 5 & 31) * (D + 4);
+            auto part = [&](int k) { return from + static_cast<int64_t>(2 * ((what >> 10 & 4095) + k) + (k == 0)) * rows * (D + 4); };
+            add(static_cast<int>(-w.y), [&](int k) { return reinterpret_cast<const float2 *>(part(k)); }, [&](int k) { return part(k) + 4 + d; });
+        };
+        const float2 w_own = __ldcg(a.weights + row), w_first = s.parts ? __ldcg(a.weights + first) : w_own;
+        if (w_own.y == PART_DONE) continue;
+        if (s.parts) add_at(w_first, first, s.parts, s.step);
+        add_at(w_own, row, 1, 0);
         const float inv = l == 0.f ? 0.f : 1.f / l;
         const float o[4] = {v.x * inv, v.y * inv, v.z * inv, v.w * inv};
-        *reinterpret_cast<uint2 *>(a.out + own * D + d) =
+        *reinterpret_cast<uint2 *>(a.out + row * D + d) =
             make_uint2(static_cast<uint32_t>(f32_to_bf16_bits(o[0])) | static_cast<uint32_t>(f32_to_bf16_bits(o[1])) << 16,
                        static_cast<uint32_t>(f32_to_bf16_bits(o[2])) | static_cast<uint32_t>(f32_to_bf16_bits(o[3])) << 16);
     }
@@ -373,9 +401,10 @@ int64_t kv4_prefix_scratch(int64_t T, int requests, int groups, int Hq, int Hkv,
     };
     const int64_t plan = take((static_cast<int64_t>(groups) + requests) * sizeof(Kv4Stretch));
     const int64_t cut = take(most_pieces * static_cast<int64_t>(sizeof(Kv4Stretch)));
-    const int64_t before = take(4 * (static_cast<int64_t>(most_pieces) + 1)), count = take(12);
-    const int64_t shares = take(groups * static_cast<int64_t>(sizeof(Kv4Share))), piece_of = take(4 * static_cast<int64_t>(requests));
+    const int64_t before = take(4 * (static_cast<int64_t>(most_pieces) + 1)), count = take(8);
+    const int64_t shares = take((static_cast<int64_t>(groups) + requests) * sizeof(Kv4Share)), joined = take(8), piece_of = take(4 * static_cast<int64_t>(requests));
     const int64_t weights = take(places * sizeof(float2)), values = take(places * D * 4);
+    const int64_t partials = take(kv4_attention_scratch(Hq, Hkv, D));
     if (a) {
         unsigned char *const p = a->scratch;
         a->stretches = a->plan = reinterpret_cast<Kv4Stretch *>(p + plan);
@@ -386,6 +415,9 @@ int64_t kv4_prefix_scratch(int64_t T, int requests, int groups, int Hq, int Hkv,
         a->piece_of = reinterpret_cast<int32_t *>(p + piece_of);
         a->weights = reinterpret_cast<float2 *>(p + weights);
         a->values = reinterpret_cast<float *>(p + values);
+        a->joined = reinterpret_cast<int64_t *>(p + joined);
+        a->both_partials[0] = reinterpret_cast<float *>(p + COUNTER_BYTES);
+        a->both_partials[1] = reinterpret_cast<float *>(p + partials);
         a->places = places;
         a->most_pieces = most_pieces;
     }
@@ -432,11 +464,15 @@ cudaError_t launch_kv4_prefix(const Kv4PrefixArgs &args, int D, cudaStream_t st,
     if (most_shared > most) most = most_shared;
     s.rows_least = 1;
     s.rows_most = NONE_OF;
+    s.launch = 0;
+    s.partials = a.both_partials[0];
     if (most > small && G <= small && (own <= small || own > few_own)) {
         s.rows_most = static_cast<int>(small);
         if (cudaError_t e = stream(s, D, small, st, dev)) return e;
         s.rows_least = s.rows_most + 1;
         s.rows_most = NONE_OF;
+        s.launch = 1;
+        s.partials = a.both_partials[1];
     }
     if (cudaError_t e = stream(s, D, most, st, dev)) return e;
     const unsigned wide = static_cast<unsigned>((a.Hq * (D / 4) + JOIN_THREADS - 1) / JOIN_THREADS);

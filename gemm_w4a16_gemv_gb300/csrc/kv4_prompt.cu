@@ -297,6 +297,13 @@ __device__ __forceinline__ float2 add2(float2 a, float2 b) {
         : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
     return d;
 }
+// 32 bytes, a whole sector.
+__device__ __forceinline__ void store8(float *p, uint32_t a, uint32_t b, uint32_t c, uint32_t d, uint32_t e, uint32_t f, uint32_t g,
+                                       uint32_t h) {
+    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(a), "r"(b), "r"(c), "r"(d), "r"(e), "r"(f),
+                 "r"(g), "r"(h)
+                 : "memory");
+}
 // (never zero, so that times -infinity it is no NaN)
 __device__ __forceinline__ float factor(float f, float k) { return fmaxf(f * k, 1.2e-38f); }
 __device__ __forceinline__ float pow2(int e) { return __uint_as_float(static_cast<uint32_t>(127 + e) << 23); }
@@ -689,11 +696,7 @@ __global__ void __launch_bounds__(THREADS, 1) attn_prompt_kernel(const Args a) {
                         const uint32_t *x = o + 8 * e;  // dimensions 0 4 1 5 2 6 3 7
                         const int at[8] = {0, 2, 4, 6, 1, 3, 5, 7};
                         if (Args::kShared && part) {
-                            float4 *const to = reinterpret_cast<float4 *>(part + 32 * c + 8 * e);
-                            to[0] = make_float4(__uint_as_float(x[at[0]]), __uint_as_float(x[at[1]]), __uint_as_float(x[at[2]]),
-                                                __uint_as_float(x[at[3]]));
-                            to[1] = make_float4(__uint_as_float(x[at[4]]), __uint_as_float(x[at[5]]), __uint_as_float(x[at[6]]),
-                                                __uint_as_float(x[at[7]]));
+                            store8(part + 32 * c + 8 * e, x[at[0]], x[at[1]], x[at[2]], x[at[3]], x[at[4]], x[at[5]], x[at[6]], x[at[7]]);
                             continue;
                         }
 #pragma unroll

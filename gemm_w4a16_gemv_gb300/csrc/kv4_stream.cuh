@@ -163,6 +163,15 @@ __device__ __forceinline__ const int32_t *pages_of(const Kv4SharedArgs &a, int b
     return a.block_table + static_cast<int64_t>(a.stretches[b].row) * a.max_blocks;
 }
 
+// In the place of a row's maximum and sum (never negative): its result is in the
+// output already; or row `row` of `rows` is in the parts of `count` (2 or more)
+// teams of a launch.
+constexpr float PART_DONE = -1.f;
+static_assert(MAX_TEAMS <= 1 << 12, "bits of a team");
+__device__ __forceinline__ float2 parts_of_row(int launch, int team, int row, int rows, int count) {
+    return make_float2(__int_as_float(launch << 22 | team << 10 | row << 5 | rows), -static_cast<float>(count));
+}
+
 // Rows of request b that this kernel answers: new tokens x query heads of a
 // key head, or none when the prompt kernel takes them.
 template <class A>
@@ -180,7 +189,9 @@ struct Segment {
     int base;       // position of row r is base + r / G
 };
 
-template <int R, class A>
+// EXTRA: units without a tile that a segment begins with, for what it costs beside
+// its tiles.
+template <int R, int EXTRA, class A>
 __device__ __forceinline__ void shape_segment(const A &a, int b, int r0, int G, Segment &s) {
     const int n = new_tokens(a, b);
     const int total = n * G;
@@ -206,13 +217,13 @@ __device__ __forceinline__ void shape_segment(const A &a, int b, int r0, int G, 
     s.end = static_cast<int>(end);
     s.ns = static_cast<int>(ns);
     s.low = static_cast<int>(low);
-    s.nt = static_cast<int>(nt);
+    s.nt = static_cast<int>(nt) + EXTRA;
 }
 
 // Walks the segments in order: key heads of a row block, row blocks of a
 // request, requests.  `first` is the segment's first tile relative to the
 // start of this CTA's share (negative when it began in an earlier CTA).
-template <int R>
+template <int R, int EXTRA>
 struct Cursor {
     Segment s;
     int first;
@@ -228,10 +239,11 @@ struct Cursor {
             while (b < a.requests && rows_of(a, b, G) == 0);
             if (b >= a.requests) return;  // past the last segment: not used
         }
-        shape_segment<R>(a, b, r0, G, s);
+        shape_segment<R, EXTRA>(a, b, r0, G, s);
     }
+    // (negative: none)
     __device__ __forceinline__ int tile(int u) const {
-        const int k = u - first;
+        const int k = u - first - EXTRA;
         return k < s.ns ? k : k - s.ns + s.low;
     }
 };
@@ -336,6 +348,10 @@ template <class A, int D, int NT, int W, int TEAM, bool SPLIT>
 __global__ void __launch_bounds__(W * 32, 1) attn_stream_kernel(const A a, const int depth) {
     using L = Stream<D, NT, W, TEAM, SPLIT>;
     constexpr int R = L::R, RPT = L::RPT, G64 = L::G64, SETS = L::SETS, TB = kv4_tile_bytes(D);
+    // What is left of requests behind a shared prefix may be a tile or two, and a
+    // warp with eight such segments took twice as long as one with eight tiles: a
+    // segment's queries and its end count as two tiles, or four with 16 rows.
+    constexpr int EXTRA = A::kShared && TEAM == 1 ? 2 * NT : 0;
     extern __shared__ __align__(128) unsigned char smem[];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int g = lane >> 2, t = lane & 3;
@@ -372,7 +388,7 @@ __global__ void __launch_bounds__(W * 32, 1) attn_stream_kernel(const A a, const
             long long n = 0;
             for (int r0 = 0; r0 < rows; r0 += R) {
                 Segment s;
-                shape_segment<R>(a, b, r0, G, s);
+                shape_segment<R, EXTRA>(a, b, r0, G, s);
                 n += s.nt;
             }
             cum[b + 1] = n * a.Hkv;
@@ -414,7 +430,7 @@ __global__ void __launch_bounds__(W * 32, 1) attn_stream_kernel(const A a, const
     const int mine = static_cast<int>(U * (me + 1) / C - u0);
 
     // ---- the segment of the first tile
-    Cursor<R> cur;
+    Cursor<R, EXTRA> cur;
     {
         int lo = 0, hi = a.requests;
         while (hi - lo > 1) {
@@ -425,7 +441,7 @@ __global__ void __launch_bounds__(W * 32, 1) attn_stream_kernel(const A a, const
         long long rest = u0 - cum[lo];
         int r0 = 0;
         while (true) {
-            shape_segment<R>(a, lo, r0, G, cur.s);
+            shape_segment<R, EXTRA>(a, lo, r0, G, cur.s);
             if (rest < static_cast<long long>(cur.s.nt) * a.Hkv) break;
             rest -= static_cast<long long>(cur.s.nt) * a.Hkv;
             r0 += R;
@@ -433,7 +449,7 @@ __global__ void __launch_bounds__(W * 32, 1) attn_stream_kernel(const A a, const
         cur.s.h = static_cast<int>(rest / cur.s.nt);
         cur.first = -static_cast<int>(rest - static_cast<long long>(cur.s.h) * cur.s.nt);
     }
-    Cursor<R> pre = cur;     // of the next tile to fetch
+    Cursor<R, EXTRA> pre = cur;     // of the next tile to fetch
     int pre_u = tw;          // its number in the team's share
     bool bad = false;
     const int sub_log2 = a.bs_log2 - 4;
@@ -451,6 +467,7 @@ __global__ void __launch_bounds__(W * 32, 1) attn_stream_kernel(const A a, const
             pages = pages_of(a, pre.s.b, pre.s.h);
         }
         const int tile = pre.tile(pre_u);
+        if (EXTRA > 0 && pre_u - pre.first < EXTRA) return;
         if (tile * 16 >= pre.s.end) return;
         page = pages[tile >> sub_log2];
         place = ((pre.s.h << sub_log2) + (tile & ((1 << sub_log2) - 1))) * TB;
@@ -735,7 +752,8 @@ __global__ void __launch_bounds__(W * 32, 1) attn_stream_kernel(const A a, const
         // partial results: [team][2][R][D + 4], slot 1 where the segment begins in
         // the share; of a row: maximum, sum, two unused, weighted values
         constexpr int PART = R * (D + 4);
-        float *const parts = reinterpret_cast<float *>(a.scratch + COUNTER_BYTES);
+        float *parts = reinterpret_cast<float *>(a.scratch + COUNTER_BYTES);
+        if constexpr (A::kShared) parts = a.partials;
         float *const part = parts + (static_cast<size_t>(me) * 2 + (seg_first >= 0 ? 1 : 0)) * PART;
         unsigned int *const count = reinterpret_cast<unsigned int *>(a.scratch) + c_first;
         auto row_of = [&](int r) -> uint16_t * {  // out of row r
@@ -748,7 +766,8 @@ __global__ void __launch_bounds__(W * 32, 1) attn_stream_kernel(const A a, const
         if constexpr (A::kShared) place = a.stretches[s.b].place;
         auto place_of = [&](int r) -> int64_t {
             const int row = s.r0 + r;
-            return place + static_cast<int64_t>(row / G) * a.Hq + s.h * G + row % G;
+            return (place >= 0 ? place : static_cast<int64_t>(first_token(a, s.b)) * a.Hq) + static_cast<int64_t>(row / G) * a.Hq +
+                   s.h * G + row % G;
         };
         // accumulators to their units (2^-24 for even dimensions, 2^-20 for odd
         // ones), and the sums over the keys
@@ -794,6 +813,8 @@ __global__ void __launch_bounds__(W * 32, 1) attn_stream_kernel(const A a, const
                                     w[k] = static_cast<uint32_t>(f32_to_bf16_bits(v[2 * k] * inv)) |
                                            static_cast<uint32_t>(f32_to_bf16_bits(v[2 * k + 1] * inv)) << 16;
                                 *reinterpret_cast<uint4 *>(row_of(r) + d) = make_uint4(w[0], w[1], w[2], w[3]);
+                                if constexpr (A::kShared)
+                                    if (d == 0) a.weights[place_of(r)] = make_float2(0.f, PART_DONE);
                             } else {
                                 float *const to = part + r * (D + 4);
                                 __stcg(reinterpret_cast<float4 *>(to + 4 + d), make_float4(v[0], v[1], v[2], v[3]));
@@ -857,7 +878,7 @@ __global__ void __launch_bounds__(W * 32, 1) attn_stream_kernel(const A a, const
                             }
             }
             if (!last) {
-                Cursor<R> after = cur;
+                Cursor<R, EXTRA> after = cur;
                 after.next(a, G);
                 if (tw >= TEAM - NT) build_q<L, D, SPLIT>(a, after.s, G, TEAM - 1 - tw, NT, team, par ^ 1, lane);
             }
@@ -888,15 +909,24 @@ __global__ void __launch_bounds__(W * 32, 1) attn_stream_kernel(const A a, const
                             a.values[place_of(r) * D + d] = o[e];
                             if (d == 0) a.weights[place_of(r)] = make_float2(m, l);
                         }
-                    } else if (!split) row_of(r)[d] = f32_to_bf16_bits(l == 0.f ? 0.f : o[e] / l);
-                    else {
+                    } else if (!split) {
+                        row_of(r)[d] = f32_to_bf16_bits(l == 0.f ? 0.f : o[e] / l);
+                        if constexpr (A::kShared)
+                            if (d == 0) a.weights[place_of(r)] = make_float2(0.f, PART_DONE);
+                    } else {
                         __stcg(part + r * (D + 4) + 4 + d, o[e]);
                         if (d == 0) __stcg(reinterpret_cast<float2 *>(part + r * (D + 4)), make_float2(m, l));
                     }
                 }
             }
         }
-        if (split) {
+        if constexpr (A::kShared) {
+            // the parts stay where they are; the team of the first one tells the join
+            // of them
+            if (split && seg_first >= 0)
+                for (int r = TEAM == 1 ? lane : tid; r < s.rows; r += TEAM == 1 ? 32 : W * 32)
+                    a.weights[place_of(r)] = parts_of_row(a.launch, c_first, r, R, c_last - c_first + 1);
+        } else if (split) {
             // the last team to arrive joins the parts, in the order of the teams
             __threadfence();
             team_sync();
@@ -950,13 +980,6 @@ __global__ void __launch_bounds__(W * 32, 1) attn_stream_kernel(const A a, const
                             o.w = fmaf(f, v[j].w, o.w);
                         }
                     }
-                    if constexpr (A::kShared)
-                        if (place >= 0) {
-                            const int64_t at = place_of(r);
-                            *reinterpret_cast<float4 *>(a.values + at * D + d) = o;
-                            if (d == 0) a.weights[at] = make_float2(m, l);
-                            continue;
-                        }
                     const float inv = l == 0.f ? 0.f : 1.f / l;
                     *reinterpret_cast<uint2 *>(row_of(r) + d) =
                         make_uint2(static_cast<uint32_t>(f32_to_bf16_bits(o.x * inv)) |
