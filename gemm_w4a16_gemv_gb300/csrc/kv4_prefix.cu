@@ -18,9 +18,9 @@ namespace w4 {
 namespace {
 
 constexpr int PLAN_THREADS = 1024;
-constexpr int JOIN_THREADS = 256;
+constexpr int JOIN_THREADS = 128;
 constexpr int64_t SMALL = 64 << 20;  // bytes of the cache that all requests can name
-constexpr int AHEAD = 8;       // parts that a thread of the join asks for together
+constexpr int AHEAD = 5;       // parts that a thread of the join asks for together
 constexpr int KEYS = 128;      // of a key tile of the tensor cores' kernel
 constexpr int ROUNDS = 4;      // items to a worker at most, where stretches are cut
 constexpr int OVERHEAD = 4;    // cost of an item beside its key tiles, in key tiles,
@@ -37,10 +37,10 @@ constexpr int PARTS = 8;       // and of the parts that it writes
 //
 // A shared stretch of many rows is cut into pieces, so that its items (a block of
 // rows and a key head each) fill the workers: with w items a piece and t key
-// tiles, cuts of c tiles give sum w ceil(t / c) < sum w t / c + sum w items, so
-//   c = ceil(sum w t / (k workers - sum w))
-// gives at most k to a worker; of k = 1 .. ROUNDS the one with the least k (c +
-// OVERHEAD) is taken.
+// tiles, cuts of c tiles give sum w ceil(t / c) items, at least sum w t / c and less
+// than sum w more.  Between what these two say lies the least c that gives at most k
+// items to a worker; of k = 1 .. ROUNDS the one with the least k (c + OVERHEAD) is
+// taken.
 //
 // Every array is read once, all elements on their way together: the kernel is a
 // chain of latencies (before the others can begin).
@@ -65,7 +65,7 @@ __global__ void __launch_bounds__(PLAN_THREADS) plan_kernel(const Kv4PrefixArgs 
     extern __shared__ __align__(16) unsigned char plan_smem[];
     const PlanSmem x(plan_smem, a.groups, a.members);
     __shared__ long long all_weight, all_tiles;  // sums of w, of w t
-    __shared__ int own_items, cut_tiles;
+    __shared__ int own_items, cut_tiles, cuts[ROUNDS];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int G = a.Hq / a.Hkv;
     pdl_launch_dependents();
@@ -146,23 +146,40 @@ __global__ void __launch_bounds__(PLAN_THREADS) plan_kernel(const Kv4PrefixArgs 
             if (rows >= least_own) atomicAdd(&own_items, blocks(rows, a.item_rows) * a.Hkv);
         }
     __syncthreads();
-    // ---- the cut; pieces and places in their order: requests' pieces first (they
-    // differ in length), then the groups'
+    // ---- the cut, a warp for each number of rounds
+    if (warp < ROUNDS && all_weight > 0) {
+        const long long workers = static_cast<long long>(warp + 1) * a.workers - own_items;
+        int hi = 0;  // (0: more than so many at best)
+        if (workers > all_weight) {
+            hi = static_cast<int>(min((all_tiles + workers - all_weight - 1) / (workers - all_weight), 0x7fffffffll));
+            int lo = static_cast<int>((all_tiles + workers - 1) / workers);
+            while (lo < hi && a.groups <= 256) {  // the least that gives so few
+                const int mid = (lo + hi) >> 1;
+                int items = 0;  // (2^31 are not possible: mid is at least their mean)
+                for (int g = lane; g < a.groups; g += 32)
+                    if (x.shared[g] > 0) items += x.weight[g] * (((x.shared[g] + KEYS - 1) / KEYS + mid - 1) / mid);
+                if (__reduce_add_sync(0xffffffffu, items) <= workers) hi = mid;
+                else lo = mid + 1;
+            }
+        }
+        if (lane == 0) cuts[warp] = hi;
+    }
+    bool loose = false;  // requests that share nothing and are streamed: some of their rows may be split
+    auto is_loose = [&](int b) {
+        const int n = x.cu[b + 1] - x.cu[b];
+        return n > 0 && n * G < least_own && (x.owner[b] < 0 || x.shared[x.owner[b]] == 0);
+    };
+    for (int b = tid; b < a.members; b += PLAN_THREADS) loose |= is_loose(b);
+    loose = __syncthreads_or(loose);
+    // ---- pieces and places in their order: requests' pieces first (they differ in
+    // length), then the groups'
     if (warp == 0) {
         long long cost = 0x7fffffffffffffffll;
         int cut = 0x7fffffff;
-        const long long room = static_cast<long long>(lane + 1) * a.workers - all_weight - own_items;
-        if (lane < ROUNDS && all_weight > 0 && room > 0) {
-            cut = static_cast<int>(min((all_tiles + room - 1) / room, 0x7fffffffll));
-            cost = (lane + 1) * (static_cast<long long>(cut) + OVERHEAD);
+        for (int k = 0; k < ROUNDS && all_weight > 0; ++k) {
+            const long long its = (k + 1) * (static_cast<long long>(cuts[k]) + OVERHEAD);
+            if (cuts[k] > 0 && its < cost) cost = its, cut = cuts[k];
         }
-#pragma unroll
-        for (int o = 1; o < ROUNDS; o <<= 1) {
-            const long long other = __shfl_xor_sync(0xffffffffu, cost, o);
-            const int its = __shfl_xor_sync(0xffffffffu, cut, o);
-            if (other < cost || (other == cost && its > cut)) cost = other, cut = its;
-        }
-        cut = __shfl_sync(0xffffffffu, cut, 0);
         if (lane == 0) cut_tiles = cut;
         long long at = 0, place = a.T * a.Hq;  // (places of the requests' own come first)
         long long joined = 0;
@@ -209,12 +226,11 @@ __global__ void __launch_bounds__(PLAN_THREADS) plan_kernel(const Kv4PrefixArgs 
             }
             shares += __popc(some);
         }
-        // requests that share nothing and are streamed: some of their rows may be split
-        for (int b0 = 0; b0 < a.members; b0 += 32) {
-            const int b = b0 + lane, n = b < a.members ? x.cu[b + 1] - x.cu[b] : 0;
-            const bool on = n > 0 && n * G < least_own && (x.owner[b] < 0 || x.shared[x.owner[b]] == 0);
+        for (int b0 = 0; loose && b0 < a.members; b0 += 32) {
+            const int b = b0 + lane;
+            const bool on = b < a.members && is_loose(b);
             const unsigned some = __ballot_sync(0xffffffffu, on);
-            const long long tokens_before = before(on ? static_cast<long long>(n) * a.Hq : 0, joined) / a.Hq;
+            const long long tokens_before = before(on ? static_cast<long long>(x.cu[b + 1] - x.cu[b]) * a.Hq : 0, joined) / a.Hq;
             if (on) a.shares[shares + __popc(some & ((1u << lane) - 1))] = {tokens_before, 0, 0, x.cu[b], 0};
             shares += __popc(some);
         }
@@ -279,13 +295,14 @@ __global__ void __launch_bounds__(PLAN_THREADS) plan_kernel(const Kv4PrefixArgs 
 // Four dimensions of a row a thread, JOIN_THREADS of a token's Hq D / 4 a CTA, which
 // goes from one token of the shared stretches to the next; and the rows of no request.
 template <int D>
-__global__ void __launch_bounds__(JOIN_THREADS) join_kernel(const Kv4PrefixArgs a) {
+__global__ void __launch_bounds__(JOIN_THREADS, 8) join_kernel(const Kv4PrefixArgs a) {
     const int lane = threadIdx.x & 31;
     const int at = blockIdx.y * JOIN_THREADS + threadIdx.x;
     pdl_launch_dependents();
     pdl_wait();
     const int shares = a.counts[1];
     const int64_t tokens = *a.joined;
+    const Kv4Share front = a.shares[0];  // (asked for beside their number)
     const int head = at / (D / 4), d = at % (D / 4) * 4;
     const bool on = at < a.Hq * (D / 4);
     for (int64_t t = rows_before(a, a.members) + blockIdx.x; on && t < a.T; t += gridDim.x)
@@ -299,7 +316,8 @@ __global__ void __launch_bounds__(JOIN_THREADS) join_kernel(const Kv4PrefixArgs 
             hi = min(hi, lo + step);
         }
         if (!on) continue;
-        const Kv4Share s = a.shares[lo];
+        Kv4Share s = front;
+        if (lo > 0) s = a.shares[lo];
         const int64_t row = static_cast<int64_t>(s.token + (i - s.before)) * a.Hq + head;  // of the output, and place of its own part
         const int64_t first = s.place + (i - s.before) * a.Hq + head;
         float m = NONE, l = 0.f;
