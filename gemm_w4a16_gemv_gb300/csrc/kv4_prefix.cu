@@ -357,11 +357,13 @@ __global__ void __launch_bounds__(JOIN_THREADS, 8) join_kernel(const Kv4PrefixAr
                 return;
             }
             // (kv4_stream.cuh: of a team two places for a row block, the second where it
-            // begins)
-            const int what = __float_as_int(w.x), rows = what & 31;
-            const float *const from = a.both_partials[what >> 22] + (what >> 5 & 31) * (D + 4);
-            auto part = [&](int k) { return from + static_cast<int64_t>(2 * ((what >> 10 & 4095) + k) + (k == 0)) * rows * (D + 4); };
-            add(static_cast<int>(-w.y), [&](int k) { return reinterpret_cast<const float2 *>(part(k)); }, [&](int k) { return part(k) + 4 + d; });
+            // begins; what a launch that timed out left there is no such place)
+            const int what = __float_as_int(w.x), rows = what & 31, r = what >> 5 & 31, team = what >> 10 & 4095;
+            const int count = static_cast<int>(fminf(-w.y, 4096.f));
+            if (what >> 23 != 0 || r >= rows || count < 2 || (team + count) * rows > MAX_CTAS * warp_rows(D)) return;
+            const float *const from = a.both_partials[what >> 22] + r * (D + 4);
+            auto part = [&](int k) { return from + static_cast<int64_t>(2 * (team + k) + (k == 0)) * rows * (D + 4); };
+            add(count, [&](int k) { return reinterpret_cast<const float2 *>(part(k)); }, [&](int k) { return part(k) + 4 + d; });
         };
         const float2 w_own = __ldcg(a.weights + row), w_first = s.parts ? __ldcg(a.weights + first) : w_own;
         if (w_own.y == PART_DONE) continue;

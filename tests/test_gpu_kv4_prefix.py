@@ -183,6 +183,69 @@ def test_many_groups(groups):
     _check(w4, out, host, 64 ** -0.5)
 
 
+@pytest.mark.parametrize("rows,Hq,Hkv,D", [(30, 16, 8, 256), (30, 8, 2, 128), (60, 8, 2, 64), (3, 4, 1, 128)])
+@pytest.mark.parametrize("flag", [1, 2])
+def test_waits_that_run_out(rows, Hq, Hkv, D, flag):
+    # test-only injection: no copy is issued and no item announced, or no product issued; the call
+    # ends, reports it and leaves its scratch fit
+    torch, w4 = cuda_or_skip()
+    dev, host = lh.grouped(torch, [(160, [(i % 20, 1) for i in range(rows)])], Hq, Hkv, D, 16, D)
+    scratch = lh.scratch(w4, dev)
+    kw = dict(scratch=scratch, max_new=1, max_group=rows)
+    first = _run(w4, dev, **kw)
+    _check(w4, first, host, D ** -0.5)
+    if flag == 2 and rows * Hq // Hkv <= 32:
+        return                         # streamed: its warps copy for themselves
+    w4.w4a16_debug_inject(flag)
+    try:
+        _run(w4, dev, **kw)
+        status = w4.w4a16_check_device_error()
+    finally:
+        w4.w4a16_debug_inject(0)
+    assert status == 5
+    for _ in range(3):
+        assert torch.equal(first, _run(w4, dev, **kw))
+    assert w4.w4a16_check_device_error() == 0
+
+
+@pytest.mark.parametrize("Hq,Hkv,D", [(16, 8, 256), (8, 2, 128)])
+def test_a_server_with_one_prompt_for_all(Hq, Hkv, D):
+    # the shared prompt is appended once; every request's table begins with its pages
+    torch, w4 = cuda_or_skip()
+    g = torch.Generator("cuda").manual_seed(D)
+    B, bs, pages = 20, 16, 12
+    i32 = dict(dtype=torch.int32, device="cuda")
+    width = (65 << 20) // (B * bs * Hkv * 18 * D // 16) + 1
+    blocks = pages + B * 6
+    cache = w4.kv4_cache(blocks, Hkv, bs, D)
+    rows = lambda n, h: torch.randn(n, h, D, device="cuda", generator=g).to(torch.bfloat16)
+    ids = torch.randperm(blocks, device="cuda", generator=g).to(torch.int32)
+    lead = ids[:pages]
+    slots = (lead.long()[:, None] * bs + torch.arange(bs, device="cuda")).flatten()
+    w4.kv4_append(rows(pages * bs, Hkv), rows(pages * bs, Hkv), cache, slots)
+    table = torch.full((B, width), -1, **i32)
+    table[:, :pages] = lead
+    free, ctx = ids[pages:].clone(), torch.full((B,), pages * bs, **i32)
+    prefix, groups = torch.tensor([pages * bs], **i32), torch.tensor([0, B], **i32)
+    scratch = w4.kv4_prefix_attention_scratch(3 * B, B, 1, Hq, Hkv, D)
+    plain = w4.kv4_attention_scratch(Hq, Hkv, D)
+    for step in range(6):
+        new = torch.randint(1, 4, (B,), device="cuda", generator=g, dtype=torch.int32)
+        T = int(new.sum())
+        plan = w4.kv4_plan(ctx, new, table, free, bs, num_tokens=T)
+        q = rows(T, Hq)
+        w4.kv4_append(rows(T, Hkv), rows(T, Hkv), cache, plan.slots)
+        a = w4.kv4_prefix_attention(q, cache, table, plan.seq_lens, plan.cu_new, prefix, groups, scratch, max_new=3, max_group=T)
+        b = w4.kv4_attention(q, cache, table, plan.seq_lens, plan.cu_new, plain, max_new=3)
+        c = ref.Cache(blocks, Hkv, bs, D)
+        c.raw = cache.cpu().numpy()
+        want, tol = ref.attention(q.double().cpu().numpy(), c, table.cpu().numpy(), plan.seq_lens.tolist(), plan.cu_new.cpu().numpy(),
+                                  D ** -0.5)
+        lh.check(w4, a, want, tol)
+        lh.check(w4, b, want, tol)
+        ctx, free = plan.seq_lens, free[int(plan.taken):]
+
+
 def test_on_another_stream_beside_another_call():
     # two calls at once, each with scratch of its own
     torch, w4 = cuda_or_skip()

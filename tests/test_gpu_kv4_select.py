@@ -307,3 +307,29 @@ def test_few_pages_are_all_of_attention():
     want, tol = ref.attention(*host, 128 ** -0.5)
     lh.check(w4, a, want, tol)
     assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("T,D", [(3, 256), (700, 64)])
+def test_copies_that_never_come(T, D):
+    # test-only injection, as in the waits of kv4_attention
+    torch, w4 = cuda_or_skip()
+    rng = np.random.default_rng(D)
+    c = ref.Cache(9, 2, 16, D)
+    for slot in range(9 * 16):
+        lh.fill(c, rng, slot)
+    lens = rng.integers(1, 65, T)
+    tables = _tables(rng, c, T, 4, lens)
+    i32 = dict(dtype=torch.int32, device="cuda")
+    q = torch.tensor(ref.bf16(rng.normal(0, 1, (T, 4, D))), device="cuda").to(torch.bfloat16)
+    args = (q, torch.tensor(c.raw, device="cuda"), torch.tensor(tables, **i32), torch.tensor(lens, **i32), w4.kv4_attention_scratch(4, 2, D))
+    first = w4.kv4_sparse_attention(*args)
+    w4.w4a16_debug_inject(w4.INJECT_STALL_PIPELINE)
+    try:
+        w4.kv4_sparse_attention(*args)
+        status = w4.w4a16_check_device_error()
+    finally:
+        w4.w4a16_debug_inject(0)
+    assert status == 5
+    for _ in range(3):
+        assert torch.equal(first, w4.kv4_sparse_attention(*args))
+    assert w4.w4a16_check_device_error() == 0
