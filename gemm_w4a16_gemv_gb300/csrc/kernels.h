@@ -209,6 +209,7 @@ struct Kv4SharedArgs : Kv4AttnArgs {
     const int32_t *items_before, *counts;  // [pieces + 1] items before each
     float *partials;  // the parts of a launch's split rows; the launch's number, 0 or 1
     int launch;
+    bool early;       // begins beside the kernel before it
     float2 *weights;  // [places] maximum (of base-2 exponents) and sum of the weights
     float *values;    // [places, D] weighted values
 };

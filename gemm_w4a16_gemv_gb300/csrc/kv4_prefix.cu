@@ -486,6 +486,7 @@ cudaError_t launch_kv4_prefix(const Kv4PrefixArgs &args, int D, cudaStream_t st,
     s.rows_most = NONE_OF;
     s.launch = 0;
     s.partials = a.both_partials[0];
+    s.early = tensor;
     if (most > small && G <= small && (own <= small || own > few_own)) {
         s.rows_most = static_cast<int>(small);
         if (cudaError_t e = stream(s, D, small, st, dev)) return e;
@@ -493,6 +494,7 @@ cudaError_t launch_kv4_prefix(const Kv4PrefixArgs &args, int D, cudaStream_t st,
         s.rows_most = NONE_OF;
         s.launch = 1;
         s.partials = a.both_partials[1];
+        s.early = true;
     }
     if (cudaError_t e = stream(s, D, most, st, dev)) return e;
     const unsigned wide = static_cast<unsigned>((a.Hq * (D / 4) + JOIN_THREADS - 1) / JOIN_THREADS);

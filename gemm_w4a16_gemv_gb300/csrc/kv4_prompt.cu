@@ -455,8 +455,11 @@ __global__ void __launch_bounds__(THREADS, 1) attn_prompt_kernel(const Args a) {
         fence_barrier_init();
     }
     if (warp == 12) tmem_take<PAIR>(&bar.tmem);
-    pdl_launch_dependents();
+    // (kv4_prefix_attention's next kernel does not wait for this one's results, but
+    // for what this one waits for)
+    if (!Args::kShared) pdl_launch_dependents();
     pdl_wait();
+    if (Args::kShared) pdl_launch_dependents();
     int *const order = cum + a.requests + 1;
     if constexpr (Args::kShared) {
         for (int i = tid; i <= a.counts[0]; i += THREADS) cum[i] = a.items_before[i];
@@ -560,17 +563,20 @@ __global__ void __launch_bounds__(THREADS, 1) attn_prompt_kernel(const Args a) {
                                   (window == 0 || p_hi - j0 < window || j0 + KEYS <= sinks);
                 // 32 keys at a time: scores in, weights out into the columns of scores already read (half as wide)
                 float m = M, scaled = 1.f, added = 0.f;
-                auto weigh = [&](uint32_t(&x)[32], int c) {
-                    if (!free) {
-                        // keys from .. upto of these 32 are seen, and those before `first`
-                        const int at = j0 + 32 * c;
-                        auto below = [](int n) -> uint32_t { return n >= 32 ? 0xffffffffu : n > 0 ? (1u << n) - 1 : 0u; };
-                        const uint32_t pages = (c & 2 ? held.y : held.x) >> (16 * (c & 1));
-                        uint32_t see = window == 0 ? 0xffffffffu : ~below(p - window + 1 - at) | below(sinks - at);
-                        see &= below(min(p + 1, cur.end) - at) & ((pages & 1u) * 0xffffu | (pages >> 8 & 1u) * 0xffff0000u);
+                // -infinity for the keys of chunk c that this row does not see
+                auto hide = [&](uint32_t(&x)[32], int c) {
+                    // keys from .. upto of these 32 are seen, and those before `first`
+                    const int at = j0 + 32 * c;
+                    auto below = [](int n) -> uint32_t { return n >= 32 ? 0xffffffffu : n > 0 ? (1u << n) - 1 : 0u; };
+                    const uint32_t pages = (c & 2 ? held.y : held.x) >> (16 * (c & 1));
+                    uint32_t see = window == 0 ? 0xffffffffu : ~below(p - window + 1 - at) | below(sinks - at);
+                    see &= below(min(p + 1, cur.end) - at) & ((pages & 1u) * 0xffffu | (pages >> 8 & 1u) * 0xffff0000u);
 #pragma unroll
-                        for (int e = 0; e < 32; ++e) x[e] = see >> e & 1u ? x[e] : 0xff800000u;  // -infinity
-                    }
+                    for (int e = 0; e < 32; ++e) x[e] = see >> e & 1u ? x[e] : 0xff800000u;  // -infinity
+                };
+                float4 kf4 = {}, ve4 = {}, vf4 = {};  // AHEAD: of two chunks' cache tiles, asked for before the scores are there
+                auto weigh = [&](uint32_t(&x)[32], int c) {
+                    if (!AHEAD && !free) hide(x, c);
                     float top[2];
 #pragma unroll
                     for (int q = 0; q < 2; ++q) {
@@ -582,9 +588,16 @@ __global__ void __launch_bounds__(THREADS, 1) attn_prompt_kernel(const Args a) {
                             t[e / 2 & 1] = max3(t[e / 2 & 1], __uint_as_float(y[e]), __uint_as_float(y[e + 1]));
                         top[q] = fmaxf(t[0], t[1]);
                     }
-                    const float2 kf = *reinterpret_cast<const float2 *>(meta.k_factor + 2 * c);
-                    const float2 B = *reinterpret_cast<const float2 *>(meta.v_exponent + 2 * c);
-                    const float2 vf = *reinterpret_cast<const float2 *>(meta.v_factor + 2 * c);
+                    float2 kf, B, vf;
+                    if (AHEAD) {
+                        kf = c & 1 ? make_float2(kf4.z, kf4.w) : make_float2(kf4.x, kf4.y);
+                        B = c & 1 ? make_float2(ve4.z, ve4.w) : make_float2(ve4.x, ve4.y);
+                        vf = c & 1 ? make_float2(vf4.z, vf4.w) : make_float2(vf4.x, vf4.y);
+                    } else {
+                        kf = *reinterpret_cast<const float2 *>(meta.k_factor + 2 * c);
+                        B = *reinterpret_cast<const float2 *>(meta.v_exponent + 2 * c);
+                        vf = *reinterpret_cast<const float2 *>(meta.v_factor + 2 * c);
+                    }
                     const float A[2] = {factor(Fr, kf.x), factor(Fr, kf.y)};
                     const float mx = fmaxf(fmaf(top[0], A[0], B.x), fmaf(top[1], A[1], B.y));
                     if (__any_sync(0xffffffffu, mx > m + 15.f)) {
@@ -631,15 +644,32 @@ __global__ void __launch_bounds__(THREADS, 1) attn_prompt_kernel(const Args a) {
                     tmem_st_32x32b_x16(t_s + 16 * c, w);
                 };
                 if (AHEAD) {
+                    if (!free) {  // in tensor memory, so that the loop below has no branch for it (1520 -> 1360 cycles of it alone)
+                        arrived(x0);
+#pragma unroll 1
+                        for (int c = 0; c < 4; ++c) {
+                            if (c > 0) {
+                                tmem_ld_32x32b_x32(t_s + 32 * c, x0);
+                                arrived(x0);
+                            }
+                            hide(x0, c);
+                            tmem_st_32x32b_x32(t_s + 32 * c, x0);
+                        }
+                        tmem_st_wait();
+                        tmem_ld_32x32b_x32(t_s, x0);
+                    }
                     uint32_t x1[32];
 #pragma unroll 1
                     for (int c = 0; c < 4; c += 2) {
+                        kf4 = *reinterpret_cast<const float4 *>(meta.k_factor + 2 * c);
+                        ve4 = *reinterpret_cast<const float4 *>(meta.v_exponent + 2 * c);
+                        vf4 = *reinterpret_cast<const float4 *>(meta.v_factor + 2 * c);
                         arrived(x0);
                         tmem_ld_32x32b_x32(t_s + 32 * c + 32, x1);
-                        weigh(x0, c);
+                        weigh(x0, c & 2);
                         arrived(x1);
                         if (c == 0) tmem_ld_32x32b_x32(t_s + 64, x0);
-                        weigh(x1, c + 1);
+                        weigh(x1, (c & 2) + 1);
                     }
                 } else {
 #pragma unroll 1

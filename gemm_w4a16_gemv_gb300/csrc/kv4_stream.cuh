@@ -372,7 +372,12 @@ __global__ void __launch_bounds__(W * 32, 1) attn_stream_kernel(const A a, const
         for (int i = 0; i < depth; ++i) mbar_init(&bars[i], 1);
     fence_barrier_init();
     pdl_launch_dependents();
-    pdl_wait();
+    // `early`: the kernel before this one is not what this one needs; it began when
+    // that was there.  So this one takes the SMs as they become free, and waits for
+    // the other at its end, for the sake of the kernel after both.
+    bool early = false;
+    if constexpr (A::kShared) early = a.early;
+    if (!early) pdl_wait();
 
     // ---- tiles of the requests, their running sum
     {
@@ -425,7 +430,10 @@ __global__ void __launch_bounds__(W * 32, 1) attn_stream_kernel(const A a, const
     const long long all_teams = static_cast<long long>(gridDim.x) * L::TEAMS, C = U < all_teams ? U : all_teams;
     // (neighbouring teams on different SMs: a small U fills them evenly)
     const int me = static_cast<int>(blockIdx.x) + static_cast<int>(gridDim.x) * (warp / TEAM);
-    if (me >= C) return;
+    if (me >= C) {
+        if (early) pdl_wait();
+        return;
+    }
     const long long u0 = U * me / C;
     const int mine = static_cast<int>(U * (me + 1) / C - u0);
 
@@ -998,6 +1006,7 @@ __global__ void __launch_bounds__(W * 32, 1) attn_stream_kernel(const A a, const
         } else par ^= 1;
     }
     if (__any_sync(0xffffffffu, bad) && lane == 0) atomicOr(a.status, kDevBadIndex);
+    if (early) pdl_wait();
 }
 
 template <class A, int D, int NT, int W, int TEAM, bool SPLIT>
