@@ -535,7 +535,6 @@ __global__ void __launch_bounds__(THREADS, 1) attn_prompt_kernel(const Args a) {
         const int r = tid;
         const uint32_t t_row = tmem + (static_cast<uint32_t>(warp * 32) << 16);
         int g = 0;  // key tiles so far, over all items
-        constexpr bool AHEAD = Args::kShared;  // the next scores are on their way while these are worked on
         const int window = static_cast<int>(min(a.window, int64_t(0x7fffffff)));
         const int sinks = a.window > 0 ? static_cast<int>(min(a.sinks, int64_t(0x7fffffff))) : 0;
         for (int k_item = 0;; ++k_item) {
@@ -574,9 +573,8 @@ __global__ void __launch_bounds__(THREADS, 1) attn_prompt_kernel(const Args a) {
 #pragma unroll
                     for (int e = 0; e < 32; ++e) x[e] = see >> e & 1u ? x[e] : 0xff800000u;  // -infinity
                 };
-                float4 kf4 = {}, ve4 = {}, vf4 = {};  // AHEAD: of two chunks' cache tiles, asked for before the scores are there
+                float4 kf4 = {}, ve4 = {}, vf4 = {};  // factors of two chunks' cache tiles
                 auto weigh = [&](uint32_t(&x)[32], int c) {
-                    if (!AHEAD && !free) hide(x, c);
                     float top[2];
 #pragma unroll
                     for (int q = 0; q < 2; ++q) {
@@ -588,16 +586,9 @@ __global__ void __launch_bounds__(THREADS, 1) attn_prompt_kernel(const Args a) {
                             t[e / 2 & 1] = max3(t[e / 2 & 1], __uint_as_float(y[e]), __uint_as_float(y[e + 1]));
                         top[q] = fmaxf(t[0], t[1]);
                     }
-                    float2 kf, B, vf;
-                    if (AHEAD) {
-                        kf = c & 1 ? make_float2(kf4.z, kf4.w) : make_float2(kf4.x, kf4.y);
-                        B = c & 1 ? make_float2(ve4.z, ve4.w) : make_float2(ve4.x, ve4.y);
-                        vf = c & 1 ? make_float2(vf4.z, vf4.w) : make_float2(vf4.x, vf4.y);
-                    } else {
-                        kf = *reinterpret_cast<const float2 *>(meta.k_factor + 2 * c);
-                        B = *reinterpret_cast<const float2 *>(meta.v_exponent + 2 * c);
-                        vf = *reinterpret_cast<const float2 *>(meta.v_factor + 2 * c);
-                    }
+                    const float2 kf = c & 1 ? make_float2(kf4.z, kf4.w) : make_float2(kf4.x, kf4.y);
+                    const float2 B = c & 1 ? make_float2(ve4.z, ve4.w) : make_float2(ve4.x, ve4.y);
+                    const float2 vf = c & 1 ? make_float2(vf4.z, vf4.w) : make_float2(vf4.x, vf4.y);
                     const float A[2] = {factor(Fr, kf.x), factor(Fr, kf.y)};
                     const float mx = fmaxf(fmaf(top[0], A[0], B.x), fmaf(top[1], A[1], B.y));
                     if (__any_sync(0xffffffffu, mx > m + 15.f)) {
@@ -643,41 +634,36 @@ __global__ void __launch_bounds__(THREADS, 1) attn_prompt_kernel(const Args a) {
                     }
                     tmem_st_32x32b_x16(t_s + 16 * c, w);
                 };
-                if (AHEAD) {
-                    if (!free) {  // in tensor memory, so that the loop below has no branch for it (1520 -> 1360 cycles of it alone)
-                        arrived(x0);
-#pragma unroll 1
-                        for (int c = 0; c < 4; ++c) {
-                            if (c > 0) {
-                                tmem_ld_32x32b_x32(t_s + 32 * c, x0);
-                                arrived(x0);
-                            }
-                            hide(x0, c);
-                            tmem_st_32x32b_x32(t_s + 32 * c, x0);
-                        }
-                        tmem_st_wait();
-                        tmem_ld_32x32b_x32(t_s, x0);
-                    }
-                    uint32_t x1[32];
-#pragma unroll 1
-                    for (int c = 0; c < 4; c += 2) {
-                        kf4 = *reinterpret_cast<const float4 *>(meta.k_factor + 2 * c);
-                        ve4 = *reinterpret_cast<const float4 *>(meta.v_exponent + 2 * c);
-                        vf4 = *reinterpret_cast<const float4 *>(meta.v_factor + 2 * c);
-                        arrived(x0);
-                        tmem_ld_32x32b_x32(t_s + 32 * c + 32, x1);
-                        weigh(x0, c & 2);
-                        arrived(x1);
-                        if (c == 0) tmem_ld_32x32b_x32(t_s + 64, x0);
-                        weigh(x1, (c & 2) + 1);
-                    }
-                } else {
+                if (!free) {
+                    // in tensor memory, so that the loop below has no branch for it (alone on
+                    // the SM it takes 1520 cycles a tile with one, 1360 without; the factors
+                    // asked for before the scores are there, 1290)
+                    arrived(x0);
 #pragma unroll 1
                     for (int c = 0; c < 4; ++c) {
-                        if (c > 0) tmem_ld_32x32b_x32(t_s + 32 * c, x0);
-                        arrived(x0);
-                        weigh(x0, c);
+                        if (c > 0) {
+                            tmem_ld_32x32b_x32(t_s + 32 * c, x0);
+                            arrived(x0);
+                        }
+                        hide(x0, c);
+                        tmem_st_32x32b_x32(t_s + 32 * c, x0);
                     }
+                    tmem_st_wait();
+                    tmem_ld_32x32b_x32(t_s, x0);
+                }
+                // the next scores are on their way while these are worked on
+                uint32_t x1[32];
+#pragma unroll 1
+                for (int c = 0; c < 4; c += 2) {
+                    kf4 = *reinterpret_cast<const float4 *>(meta.k_factor + 2 * c);
+                    ve4 = *reinterpret_cast<const float4 *>(meta.v_exponent + 2 * c);
+                    vf4 = *reinterpret_cast<const float4 *>(meta.v_factor + 2 * c);
+                    arrived(x0);
+                    tmem_ld_32x32b_x32(t_s + 32 * c + 32, x1);
+                    weigh(x0, c & 2);
+                    arrived(x1);
+                    if (c == 0) tmem_ld_32x32b_x32(t_s + 64, x0);
+                    weigh(x1, (c & 2) + 1);
                 }
                 if (__any_sync(0xffffffffu, m != M)) {
                     l *= scaled;
