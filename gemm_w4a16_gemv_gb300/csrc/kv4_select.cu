@@ -165,17 +165,27 @@ __device__ __forceinline__ uint32_t ordered(float x) {
     return b & 0x80000000u ? ~b : b | 0x80000000u;
 }
 
-// A query head in whole numbers of 8 bits (NaN as 0, infinities as the largest
-// finite number), which bytes of them are negative, and their unit.  By a whole
-// warp.
+// A query head's elements, four of them in each of a warp's lanes (or two times four).
 template <int D>
-__device__ __forceinline__ void quantise(const uint16_t *q, uint32_t *out, float &unit, int lane) {
-    constexpr int WORDS = D / 4, PER = (WORDS + 31) / 32;
-    float x[PER][4], most = 0.f;
+struct Query {
+    static constexpr int WORDS = D / 4, PER = (WORDS + 31) / 32;
+    uint2 raw[PER];
+};
+template <int D>
+__device__ __forceinline__ Query<D> load_query(const uint16_t *q, int lane) {
+    Query<D> r;
 #pragma unroll
-    for (int k = 0; k < PER; ++k) {
-        const int w = lane + 32 * k;
-        const uint2 raw = w < WORDS ? *reinterpret_cast<const uint2 *>(q + 4 * w) : make_uint2(0, 0);
+    for (int k = 0; k < Query<D>::PER; ++k) r.raw[k] = *reinterpret_cast<const uint2 *>(q + 4 * ((lane + 32 * k) % Query<D>::WORDS));
+    return r;
+}
+// In whole numbers of 8 bits (NaN as 0, infinities as the largest finite number);
+// their unit.  By a whole warp.
+template <int D>
+__device__ __forceinline__ float whole_numbers(const Query<D> &r, float (&x)[Query<D>::PER][4]) {
+    float most = 0.f;
+#pragma unroll
+    for (int k = 0; k < Query<D>::PER; ++k) {
+        const uint2 raw = r.raw[k];
         const uint32_t bits[4] = {raw.x << 16, raw.x & 0xffff0000u, raw.y << 16, raw.y & 0xffff0000u};
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
@@ -186,18 +196,44 @@ __device__ __forceinline__ void quantise(const uint16_t *q, uint32_t *out, float
     }
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, o));
-    const float step = most * STEP, by = step > 0.f ? step : 1.f;
+    const float unit = most * STEP, by = unit > 0.f ? unit : 1.f;
 #pragma unroll
-    for (int k = 0; k < PER; ++k) {
+    for (int k = 0; k < Query<D>::PER; ++k)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) x[k][e] = rintf(__fdiv_rn(x[k][e], by));
+    return unit;
+}
+// As bytes, and which of them are negative.
+template <int D>
+__device__ __forceinline__ void quantise(const uint16_t *q, uint32_t *out, float &unit, int lane) {
+    float x[Query<D>::PER][4];
+    const float step = whole_numbers<D>(load_query<D>(q, lane), x);
+#pragma unroll
+    for (int k = 0; k < Query<D>::PER; ++k) {
+        const int w = lane + 32 * k;
         uint32_t word = 0;
 #pragma unroll
-        for (int e = 0; e < 4; ++e) word |= (static_cast<uint32_t>(__float2int_rn(__fdiv_rn(x[k][e], by))) & 255u) << 8 * e;
-        if (lane + 32 * k < WORDS) {
-            out[lane + 32 * k] = word;
-            out[WORDS + lane + 32 * k] = __vcmplts4(word, 0);
+        for (int e = 0; e < 4; ++e) word |= (static_cast<uint32_t>(static_cast<int>(x[k][e])) & 255u) << 8 * e;
+        if (w < Query<D>::WORDS) {
+            out[w] = word;
+            out[Query<D>::WORDS + w] = __vcmplts4(word, 0);
         }
     }
     if (lane == 0) unit = step;
+}
+__device__ __forceinline__ uint32_t pair(float lo, float hi) {
+    const __half2 h = __floats2half2_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t *>(&h);
+}
+
+// Lengths and running sums of the step out of range; by the first CTA.
+__device__ __forceinline__ void check_step(const Kv4SelectArgs &a) {
+    if (blockIdx.x != 0) return;
+    for (int b = threadIdx.x; b < a.requests; b += blockDim.x) {
+        const int64_t from = a.cu_new[b], to = a.cu_new[b + 1], len = a.seq_lens[b];
+        if (from < 0 || to < from || to > a.T || (to > from && (len < 0 || len > a.max_blocks << a.bs_log2)))
+            atomicOr(a.status, kDevBadIndex);
+    }
 }
 
 __device__ __forceinline__ uint32_t cluster_rank() {
@@ -219,13 +255,7 @@ __device__ __forceinline__ void store_first(uint32_t *p, uint32_t v) {
                  : "memory");
 }
 
-// Words of shared memory of a team: keys, queries, units, scratch.
-__host__ __device__ constexpr int select_words(int width, int G, int D) {
-    return width + G * (D / 2) + (G + 3) / 4 * 4 + (256 + 2 * WARPS + 8);
-}
-
-// A team works on one token and key head: a CTA (with others of its cluster), or a
-// warp where there are tokens enough for that.
+// A team chooses for one token and key head: a CTA, or a warp.
 template <bool WARP>
 struct Team {
     static constexpr int COUNT = WARP ? 32 : THREADS;       // threads
@@ -316,45 +346,114 @@ __device__ __forceinline__ Cut find_cut(const uint32_t *keys, int n, int need, i
     }
 }
 
-// The CTAs of a cluster have a share of a token's pages each; the first one then
-// chooses.  A warp alone does both; the warps of a CTA have neighbouring tokens
-// then, which share most of their pages in L1.
+// What token t sees: its position, the pages, how many of these are taken; of them
+// the first `few` and those from number `late` on in any case, and `need` of the n
+// pages between.
+struct View {
+    const int32_t *pages;
+    int64_t p;
+    int b, seen, taken, few, late, need, n;
+};
+__device__ __forceinline__ View view_of(const Kv4SelectArgs &a, int64_t t, int lane) {
+    View v;
+    v.b = request_of(a.cu_new, a.requests, t, lane);
+    const int64_t cap = a.max_blocks << a.bs_log2;
+    v.p = v.b < 0 ? -1 : min(static_cast<int64_t>(a.seq_lens[v.b]) - a.cu_new[v.b + 1] + t, cap - 1);
+    v.seen = v.p < 0 ? 0 : static_cast<int>(v.p >> a.bs_log2) + 1;
+    v.taken = min(a.top, v.seen);
+    v.pages = a.block_table + (v.b < 0 ? 0 : v.b) * a.max_blocks;
+    v.few = v.seen > a.top ? a.first : v.taken;
+    v.late = v.taken - (v.seen > a.top ? a.recent : 0);
+    v.need = v.late - v.few;
+    v.n = v.seen - (v.taken - v.need);
+    return v;
+}
+
+// The table and the length of a token, from the keys of the pages between.
+template <class T>
+__device__ __forceinline__ void choose(const Kv4SelectArgs &a, int64_t t, int h, const View &v, const uint32_t *keys, int *scratch,
+                                       bool &bad) {
+    const int tid = T::thread(), lane = tid & 31, warp = T::warp();
+    int32_t *const out = a.tables + (t * a.Hkv + h) * a.top;
+    auto id_of = [&](int page) -> int {
+        const int id = v.pages[page];
+        if (id >= 0 && id < a.num_blocks) return id;
+        bad = true;
+        return -1;
+    };
+    if (h == 0 && tid == 0)
+        a.lens[t] = v.p < 0 ? 0 : static_cast<int>(((v.taken - 1) << a.bs_log2) + (v.p & ((1 << a.bs_log2) - 1)) + 1);
+    for (int i = v.taken + tid; i < a.top; i += T::COUNT) out[i] = -1;
+    for (int i = tid; i < v.taken; i += T::COUNT)
+        if (i < v.few || i >= v.late) out[i] = id_of(i < v.few ? i : v.seen - v.taken + i);
+    if (v.need <= 0) return;
+    const Cut cut = find_cut<T>(keys, v.n, v.need, scratch);
+    // in the order of the pages: a warp's share in a row, counted first where there
+    // are several
+    const int share = (v.n + T::COUNT - 1) / T::COUNT * 32, from = warp * share, upto = min(from + share, v.n);
+    int above = 0, equal = 0;
+    if (T::COUNT > 32) {
+        int *const sums = scratch;
+        for (int i = from + lane; i - lane < upto; i += 32) {
+            const uint32_t key = i < upto ? keys[i] : 0u;
+            above += __popc(__ballot_sync(0xffffffffu, i < upto && key > cut.key));
+            equal += __popc(__ballot_sync(0xffffffffu, i < upto && key == cut.key));
+        }
+        T::sync();
+        if (lane == 0) sums[warp] = above, sums[WARPS + warp] = equal;
+        T::sync();
+        above = equal = 0;
+        for (int w = 0; w < warp; ++w) above += sums[w], equal += sums[WARPS + w];
+    }
+    const unsigned under = (1u << lane) - 1;
+    for (int i = from + lane; i - lane < upto; i += 32) {
+        const uint32_t key = i < upto ? keys[i] : 0u;
+        const unsigned more = __ballot_sync(0xffffffffu, i < upto && key > cut.key);
+        const unsigned same = __ballot_sync(0xffffffffu, i < upto && key == cut.key);
+        const int ties = equal + __popc(same & under);
+        if (i < upto && (key > cut.key || (key == cut.key && ties < cut.equal)))
+            out[v.few + above + __popc(more & under) + min(ties, cut.equal)] = id_of(v.few + i);
+        above += __popc(more);
+        equal += __popc(same);
+    }
+}
+
+// Words of shared memory of select_kernel: keys, queries, units, scratch.
+__host__ __device__ constexpr int select_words(int width, int G, int D) {
+    return width + G * (D / 2) + (G + 3) / 4 * 4 + (256 + 2 * WARPS + 8);
+}
+
+// ---- a cluster for a token and key head: its CTAs have a share of the pages each,
+// the first one then chooses.
 //
 // Score.  A lane holds 16 elements of a page's bounds: D / 16 lanes a page, PPI
 // pages side by side and four (SLOTS) times as many at a time.  Each four lanes
 // have a group of 64 elements: of its sums for four pages every lane adds up one.
 // One pass over the bounds for any number of query heads.  Bound: memory, where
-// there are pages and tokens enough; about 45 instructions a query head for 4 PPI
-// pages.  16 bytes of high and of low a lane and slot are on their way at once,
-// 4 KB a warp.
-template <int D, bool WARP>
-__global__ void __launch_bounds__(THREADS, WARP ? 2 : 3) select_kernel(const Kv4SelectArgs a) {
-    using Us = Team<WARP>;
+// there are pages and tokens enough (64 requests of 63 to 3750 pages 57 us, 4.4 TB/s);
+// about 45 instructions a query head for 4 PPI pages.  16 bytes of high and of low a
+// lane and slot are on their way at once, 4 KB a warp.  (A ring of further rows in
+// shared memory, 72 us, or in registers, 59 us, left fewer CTAs on an SM.)
+template <int D>
+__global__ void __launch_bounds__(THREADS, 3) select_kernel(const Kv4SelectArgs a) {
+    using Us = Team<false>;
     constexpr int LPP = D / 16, PPI = 32 / LPP, SLOTS = 4, BATCH = SLOTS * PPI;
     extern __shared__ __align__(16) uint32_t select_smem[];
-    const int tid = Us::thread(), lane = tid & 31, warp = Us::warp();
-    const int ctas = WARP ? 1 : static_cast<int>(cluster_ctas()), rank = WARP ? 0 : static_cast<int>(cluster_rank());
-    const int64_t task = blockIdx.x / ctas;
-    int64_t t = WARP ? task / a.Hkv * WARPS + (threadIdx.x >> 5) : task / a.Hkv;
-    const int h = static_cast<int>(task % a.Hkv), G = a.Hq / a.Hkv;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int ctas = static_cast<int>(cluster_ctas()), rank = static_cast<int>(cluster_rank());
+    int64_t t = blockIdx.x / ctas / a.Hkv;
+    const int h = static_cast<int>(blockIdx.x / ctas % a.Hkv), G = a.Hq / a.Hkv;
     // of the pages between the first and the recent ones; [G][2][D / 4] the queries, 8
     // bits an element, and which are negative; [G] their units; scratch
     const int width = static_cast<int>((a.max_blocks + 3) / 4 * 4);
-    uint32_t *const keys = select_smem + (WARP ? (threadIdx.x >> 5) * select_words(width, G, D) : 0);
-    uint32_t *const query = keys + width;
+    uint32_t *const keys = select_smem, *const query = keys + width;
     float *const unit = reinterpret_cast<float *>(query + G * (D / 2));
     int *const scratch = reinterpret_cast<int *>(unit + (G + 3) / 4 * 4);
-    if (!WARP) cluster_arrive();  // (there, for the other CTAs' stores)
+    cluster_arrive();  // (there, for the other CTAs' stores)
     pdl_launch_dependents();
     pdl_wait();
-    if (blockIdx.x == 0)
-        for (int b = threadIdx.x; b < a.requests; b += THREADS) {
-            const int64_t from = a.cu_new[b], to = a.cu_new[b + 1], len = a.seq_lens[b];
-            if (from < 0 || to < from || to > a.T || (to > from && (len < 0 || len > a.max_blocks << a.bs_log2)))
-                atomicOr(a.status, kDevBadIndex);
-        }
-    if (WARP && t >= a.T) return;
-    if (!WARP && a.requests == a.T && a.requests > 1 && a.requests <= THREADS) {
+    check_step(a);
+    if (a.requests == a.T && a.requests > 1 && a.requests <= THREADS) {
         // a token each: those of the longest contexts first (62 -> 56 us for 64 ragged ones)
         int *const lens = scratch;
         if (tid < a.requests) lens[tid] = a.seq_lens[tid];
@@ -369,85 +468,43 @@ __global__ void __launch_bounds__(THREADS, WARP ? 2 : 3) select_kernel(const Kv4
         t = lens[THREADS];
         __syncthreads();
     }
-    for (int g = warp; g < G; g += Us::COUNT / 32)
+    for (int g = warp; g < G; g += WARPS)
         quantise<D>(a.q + t * a.q_stride + static_cast<int64_t>(h * G + g) * D, query + g * (D / 2), unit[g], lane);
-    const int b = request_of(a.cu_new, a.requests, t, lane);
-    const int64_t cap = a.max_blocks << a.bs_log2;
-    const int64_t p = b < 0 ? -1 : min(static_cast<int64_t>(a.seq_lens[b]) - a.cu_new[b + 1] + t, cap - 1);
-    const int seen = p < 0 ? 0 : static_cast<int>(p >> a.bs_log2) + 1;
-    const int taken = min(a.top, seen);
-    int32_t *const out = a.tables + (t * a.Hkv + h) * a.top;
-    const int32_t *const pages = a.block_table + (b < 0 ? 0 : b) * a.max_blocks;
+    const View v = view_of(a, t, lane);
+    const int n = v.n;
     bool bad = false;
-    auto id_of = [&](int page) -> int {
-        const int id = pages[page];
-        if (id >= 0 && id < a.num_blocks) return id;
-        bad = true;
-        return -1;
-    };
-    const int few = seen > a.top ? a.first : taken, late = taken - (seen > a.top ? a.recent : 0);
-    // need of n pages, from number `few` on
-    const int need = late - few, n = seen - (taken - need);
-    Us::sync();
-    if (!WARP) cluster_wait();
-    if (need > 0) {
+    __syncthreads();
+    cluster_wait();
+    if (v.need > 0) {
         const int s = lane % LPP, side = lane / LPP;
-        const int step = ctas * (Us::COUNT / 32) * BATCH;
+        const int step = ctas * WARPS * BATCH;
         // the page whose sums this lane has in the end
         const int mine = (2 * (lane & 1) + (lane >> 1 & 1)) * PPI + side;
         const unsigned char *const bounds = a.bounds + static_cast<int64_t>(h) * bounds_bytes(D);
         const int64_t page_bytes = static_cast<int64_t>(a.Hkv) * bounds_bytes(D);
         // (looked at when they are used: a test here would wait for them)
-        auto ids = [&](int p0) { return lane < BATCH && p0 + lane < n ? pages[few + p0 + lane] : NO_PAGE; };
+        auto ids = [&](int p0) { return lane < BATCH && p0 + lane < n ? v.pages[v.few + p0 + lane] : NO_PAGE; };
         auto known = [&](int id) {
             const bool in = id >= 0 && id < a.num_blocks;
             bad |= !in && id != NO_PAGE;
             return in ? id : -1;
         };
-        const int first = (rank * (Us::COUNT / 32) + warp) * BATCH;
-        struct Rows {
-            uint4 high[SLOTS], low[SLOTS];
-            float step;  // of this lane's page and group
-            int whose;
-        };
-        auto load = [&](int id) -> Rows {
-            Rows r;
-            r.whose = __shfl_sync(0xffffffffu, id, mine);
-            r.step = *reinterpret_cast<const float *>(bounds + max(r.whose, 0) * page_bytes + 2 * D + s / 4 * 4);
+        const int first = (rank * WARPS + warp) * BATCH;
+        int raw = ids(first);
+        for (int p0 = first; p0 < n; p0 += step) {
+            const int id = known(raw);
+            raw = ids(p0 + step);  // on its way meanwhile
+            const int whose = __shfl_sync(0xffffffffu, id, mine);
+            const float unit_of = *reinterpret_cast<const float *>(bounds + max(whose, 0) * page_bytes + 2 * D + s / 4 * 4);
+            uint32_t high[SLOTS][4], low[SLOTS][4];
 #pragma unroll
             for (int j = 0; j < SLOTS; ++j) {
                 const int page = __shfl_sync(0xffffffffu, id, j * PPI + side);
                 const unsigned char *const row = bounds + max(page, 0) * page_bytes;
-                r.high[j] = *reinterpret_cast<const uint4 *>(row + 16 * s);
-                r.low[j] = *reinterpret_cast<const uint4 *>(row + D + 16 * s);
+                const uint4 up = *reinterpret_cast<const uint4 *>(row + 16 * s), down = *reinterpret_cast<const uint4 *>(row + D + 16 * s);
+                high[j][0] = up.x, high[j][1] = up.y, high[j][2] = up.z, high[j][3] = up.w;
+                low[j][0] = down.x, low[j][1] = down.y, low[j][2] = down.z, low[j][3] = down.w;
             }
-            return r;
-        };
-        // the ids of the next pages are on their way meanwhile; to a warp alone, which
-        // has fewer others beside it on the SM, their rows too
-        int raw = ids(first);
-        Rows rows;
-        if (WARP) {
-            rows = load(known(raw));
-            raw = ids(first + step);
-        }
-        for (int p0 = first; p0 < n; p0 += step) {
-            Rows next;
-            if (WARP) {
-                next = load(known(raw));
-                raw = ids(p0 + 2 * step);
-            } else {
-                rows = load(known(raw));
-                raw = ids(p0 + step);
-            }
-            uint32_t high[SLOTS][4], low[SLOTS][4];
-#pragma unroll
-            for (int j = 0; j < SLOTS; ++j) {
-                high[j][0] = rows.high[j].x, high[j][1] = rows.high[j].y, high[j][2] = rows.high[j].z, high[j][3] = rows.high[j].w;
-                low[j][0] = rows.low[j].x, low[j][1] = rows.low[j].y, low[j][2] = rows.low[j].z, low[j][3] = rows.low[j].w;
-            }
-            const float unit_of = rows.step;
-            const int whose = rows.whose;
             float best = -INFINITY;
 #pragma unroll 2
             for (int g = 0; g < G; ++g) {
@@ -472,57 +529,209 @@ __global__ void __launch_bounds__(THREADS, WARP ? 2 : 3) select_kernel(const Kv4
                 if (LPP >= 16) x = __fadd_rn(x, __shfl_xor_sync(0xffffffffu, x, 8));
                 best = fmaxf(best, __fmul_rn(x, unit[g]));
             }
-            if (s < 4 && p0 + mine < n) {
-                const uint32_t key = ordered(whose < 0 ? -INFINITY : best);
-                if (WARP) keys[p0 + mine] = key;
-                else store_first(keys + p0 + mine, key);
-            }
-            if (WARP) rows = next;
+            if (s < 4 && p0 + mine < n) store_first(keys + p0 + mine, ordered(whose < 0 ? -INFINITY : best));
         }
     }
     __syncwarp();
     if (ctas > 1) {
         cluster_arrive();
         cluster_wait();
-    } else Us::sync();
-    if (rank == 0) {
-        if (h == 0 && tid == 0)
-            a.lens[t] = p < 0 ? 0 : static_cast<int>(((taken - 1) << a.bs_log2) + (p & ((1 << a.bs_log2) - 1)) + 1);
-        for (int i = taken + tid; i < a.top; i += Us::COUNT) out[i] = -1;
-        for (int i = tid; i < taken; i += Us::COUNT)
-            if (i < few || i >= late) out[i] = id_of(i < few ? i : seen - taken + i);
-        if (need > 0) {
-            const Cut cut = find_cut<Us>(keys, n, need, scratch);
-            // in the order of the pages: a warp's share in a row, counted first where
-            // there are several
-            const int share = (n + Us::COUNT - 1) / Us::COUNT * 32, from = warp * share, upto = min(from + share, n);
-            int above = 0, equal = 0;
-            if (!WARP) {
-                int *const sums = scratch;
-                for (int i = from + lane; i - lane < upto; i += 32) {
-                    const uint32_t key = i < upto ? keys[i] : 0u;
-                    above += __popc(__ballot_sync(0xffffffffu, i < upto && key > cut.key));
-                    equal += __popc(__ballot_sync(0xffffffffu, i < upto && key == cut.key));
+    } else __syncthreads();
+    if (rank == 0) choose<Us>(a, t, h, v, keys, scratch, bad);
+    if (bad) atomicOr(a.status, kDevBadIndex);
+}
+
+// ---- tokens of one request: a CTA for as many as fill the eight columns of a
+// product, with the 2^lg query heads of a key head (some twice where that is more than
+// there are).  Its warps take the pages in turn, 16 at a time, and then a token each to
+// choose for.
+//
+// Score.  16 pages x 8 columns by the 16-bit MMA, both operands whole numbers as
+// binary16: a byte under the exponent of 1024, minus 1152.  Sums of 64 products below
+// 2^14 are exact in binary32.  The queries' parts above 0 meet `high`, those below 0
+// `low`.  A lane's 16 bytes of a row are the operands of four products, in any order
+// of the 64 elements that is the queries' too.  Two groups of 64 of the rows are on
+// their way meanwhile.  Bound: the conversions and products beside them, and the choice
+// (301 tokens x 470 pages, 32 heads of 128 on 8, 37 us; with 8-bit products by dp4a, a
+// warp each, 45; the 8-bit MMA takes 64 cycles for what the 16-bit one does in 16).
+constexpr int COLUMNS = 8;
+
+__device__ __forceinline__ void mma_f16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+        "{%0, %1, %2, %3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+// Four whole numbers of 8 bits as binary16 pairs.
+__device__ __forceinline__ void halves(uint32_t w, uint32_t &lo, uint32_t &hi) {
+    w ^= 0x80808080u;
+    lo = __byte_perm(w, 0x64646464u, 0x4140);
+    hi = __byte_perm(w, 0x64646464u, 0x4342);
+    asm("sub.rn.f16x2 %0, %0, %1;" : "+r"(lo) : "r"(0x64806480u));
+    asm("sub.rn.f16x2 %0, %0, %1;" : "+r"(hi) : "r"(0x64806480u));
+}
+
+constexpr int PIECE_WARPS = 4;
+
+// Words of shared memory, for NB times 8 columns: keys of the tokens, queries, units,
+// what the tokens see, and of each warp scratch.
+__host__ __device__ constexpr int piece_words(int width, int lg, int D, int NB) {
+    return NB * ((width << (3 - lg)) + D * 8 + 3 * COLUMNS) + PIECE_WARPS * (256 + 2 * WARPS + 8);
+}
+
+template <int D, int NB>
+__global__ void __launch_bounds__(PIECE_WARPS * 32, NB == 1 ? 4 : 3) piece_kernel(const Kv4SelectArgs a, const int lg) {
+    using Us = Team<true>;
+    constexpr int G64 = D / 64, NEXT = G64 > 1 ? 2 : 1;  // groups on their way
+    extern __shared__ __align__(16) uint32_t select_smem[];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, q = lane & 3;
+    const int tokens = NB * (COLUMNS >> lg), G = a.Hq / a.Hkv, h = static_cast<int>(blockIdx.x % a.Hkv);
+    const int64_t t0 = static_cast<int64_t>(blockIdx.x / a.Hkv) * tokens;
+    const int here = static_cast<int>(min(static_cast<int64_t>(tokens), a.T - t0));
+    const int width = static_cast<int>((a.max_blocks + 3) / 4 * 4);
+    uint32_t *const keys = select_smem;
+    uint2 *const query = reinterpret_cast<uint2 *>(keys + NB * (width << (3 - lg)));  // [NB][G64][4 products][high, low][32 lanes]
+    float *const unit = reinterpret_cast<float *>(query + NB * D * 4);
+    int *const request = reinterpret_cast<int *>(unit + NB * COLUMNS), *const count = request + NB * COLUMNS;  // of each token: pages between
+    int *const scratch = count + NB * COLUMNS + warp * (256 + 2 * WARPS + 8);
+    pdl_launch_dependents();
+    pdl_wait();
+    check_step(a);
+    for (int c = warp; c < NB * COLUMNS; c += PIECE_WARPS) {
+        const int64_t t = t0 + min(c >> lg, here - 1);
+        const Query<D> raw = load_query<D>(a.q + t * a.q_stride + static_cast<int64_t>(h * G + (c & ((1 << lg) - 1)) % G) * D, lane);
+        float x[Query<D>::PER][4];
+        const float step = whole_numbers<D>(raw, x);
+#pragma unroll
+        for (int k = 0; k < Query<D>::PER; ++k) {
+            const int w = lane + 32 * k;  // elements 4 w and on: group w / 16, lane w / 4 % 4, product w % 4
+            if (w >= Query<D>::WORDS) continue;
+            uint2 *const to = query + c / COLUMNS * D * 4 + ((w >> 4) * 4 + (w & 3)) * 64 + c % COLUMNS * 4 + (w >> 2 & 3);
+            to[0] = make_uint2(pair(fmaxf(x[k][0], 0.f), fmaxf(x[k][1], 0.f)), pair(fmaxf(x[k][2], 0.f), fmaxf(x[k][3], 0.f)));
+            to[32] = make_uint2(pair(fminf(x[k][0], 0.f), fminf(x[k][1], 0.f)), pair(fminf(x[k][2], 0.f), fminf(x[k][3], 0.f)));
+        }
+        if (lane == 0) unit[c] = step;
+    }
+    View own;  // of this warp's first token
+    for (int i = warp; i < here; i += PIECE_WARPS) {
+        const View v = view_of(a, t0 + i, lane);
+        if (lane == 0) request[i] = v.b, count[i] = v.need > 0 ? v.n : 0;
+        if (i == warp) own = v;
+    }
+    __syncthreads();
+    bool bad = false;
+    const unsigned char *const bounds = a.bounds + static_cast<int64_t>(h) * bounds_bytes(D);
+    const int64_t page_bytes = static_cast<int64_t>(a.Hkv) * bounds_bytes(D);
+    // the token (of 8 columns) whose keys this lane writes: 2 q and the next, or one (or none)
+    const int mine = lg == 0 ? 2 * q : lg == 1 ? q : lg == 2 ? q >> 1 : 0;
+    const bool writes = lg <= 1 || (lg == 2 ? (q & 1) == 0 : q == 0);
+    for (int from = 0, upto; from < here; from = upto) {
+        // tokens of one request
+        int n = count[from];
+        for (upto = from + 1; upto < here && request[upto] == request[from]; ++upto) n = max(n, count[upto]);
+        if (n == 0) continue;
+        auto keys_of = [&](int token) { return writes && token >= from && token < upto ? count[token] : 0; };
+        int n0[NB], n1[NB];
+#pragma unroll
+        for (int b = 0; b < NB; ++b) {
+            n0[b] = keys_of(b * (COLUMNS >> lg) + mine);
+            n1[b] = lg == 0 ? keys_of(b * COLUMNS + mine + 1) : 0;
+        }
+        const int32_t *const pages = a.block_table + static_cast<int64_t>(request[from]) * a.max_blocks + a.first;
+        constexpr int STEP = 16 * PIECE_WARPS;
+        auto ids = [&](int p0) { return lane < 16 && p0 + lane < n ? pages[p0 + lane] : NO_PAGE; };
+        struct Pages {
+            const unsigned char *row[2];  // of pages g and g + 8
+            int id[2];
+        };
+        auto find = [&](int raw) {
+            const bool in = raw >= 0 && raw < a.num_blocks;
+            bad |= !in && raw != NO_PAGE;
+            Pages r;
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+                r.id[k] = __shfl_sync(0xffffffffu, in ? raw : -1, g + 8 * k);
+                r.row[k] = bounds + max(r.id[k], 0) * page_bytes;
+            }
+            return r;
+        };
+        struct Rows {
+            uint4 high[2], low[2];
+        };
+        auto load = [&](const Pages &r, int i) {
+            Rows x;
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+                x.high[k] = *reinterpret_cast<const uint4 *>(r.row[k] + 64 * i + 16 * q);
+                x.low[k] = *reinterpret_cast<const uint4 *>(r.row[k] + D + 64 * i + 16 * q);
+            }
+            return x;
+        };
+        Pages now = find(ids(16 * warp));
+        int raw = ids(16 * warp + STEP);
+        Rows ahead[NEXT];
+#pragma unroll
+        for (int k = 0; k < NEXT; ++k) ahead[k] = load(now, k);
+        for (int p0 = 16 * warp; p0 < n; p0 += STEP) {
+            const Pages next = find(raw);
+            raw = ids(p0 + 2 * STEP);
+            float steps[2][G64];
+#pragma unroll
+            for (int k = 0; k < 2; ++k)
+#pragma unroll
+                for (int i = 0; i < G64; ++i) steps[k][i] = *reinterpret_cast<const float *>(now.row[k] + 2 * D + 4 * i);
+            float sum[NB][2][4];  // of each half of the groups
+#pragma unroll
+            for (int i = 0; i < G64; ++i) {
+                const Rows x = ahead[i % NEXT];
+                ahead[i % NEXT] = i + NEXT < G64 ? load(now, i + NEXT) : load(next, i + NEXT - G64);
+                float up[NB][4] = {}, down[NB][4] = {};
+                const uint32_t high[2][4] = {{x.high[0].x, x.high[0].y, x.high[0].z, x.high[0].w}, {x.high[1].x, x.high[1].y, x.high[1].z, x.high[1].w}};
+                const uint32_t low[2][4] = {{x.low[0].x, x.low[0].y, x.low[0].z, x.low[0].w}, {x.low[1].x, x.low[1].y, x.low[1].z, x.low[1].w}};
+#pragma unroll
+                for (int s = 0; s < 4; ++s) {
+                    uint32_t a0, a1, a2, a3, b0, b1, b2, b3;
+                    halves(high[0][s], a0, a2);
+                    halves(high[1][s], a1, a3);
+                    halves(low[0][s], b0, b2);
+                    halves(low[1][s], b1, b3);
+#pragma unroll
+                    for (int b = 0; b < NB; ++b) {
+                        const uint2 above = query[b * D * 4 + (i * 4 + s) * 64 + lane], below = query[b * D * 4 + (i * 4 + s) * 64 + 32 + lane];
+                        mma_f16(up[b], a0, a1, a2, a3, above.x, above.y);
+                        mma_f16(down[b], b0, b1, b2, b3, below.x, below.y);
+                    }
                 }
-                Us::sync();
-                if (lane == 0) sums[warp] = above, sums[WARPS + warp] = equal;
-                Us::sync();
-                above = equal = 0;
-                for (int w = 0; w < warp; ++w) above += sums[w], equal += sums[WARPS + w];
+#pragma unroll
+                for (int b = 0; b < NB; ++b)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const float y = __fmul_rn(up[b][e] + down[b][e], steps[e >> 1][i]);
+                        sum[b][i >> 1][e] = i & 1 ? __fadd_rn(sum[b][i >> 1][e], y) : y;
+                    }
             }
-            const unsigned under = (1u << lane) - 1;
-            for (int i = from + lane; i - lane < upto; i += 32) {
-                const uint32_t key = i < upto ? keys[i] : 0u;
-                const unsigned more = __ballot_sync(0xffffffffu, i < upto && key > cut.key);
-                const unsigned same = __ballot_sync(0xffffffffu, i < upto && key == cut.key);
-                const int ties = equal + __popc(same & under);
-                if (i < upto && (key > cut.key || (key == cut.key && ties < cut.equal)))
-                    out[few + above + __popc(more & under) + min(ties, cut.equal)] = id_of(few + i);
-                above += __popc(more);
-                equal += __popc(same);
-            }
+#pragma unroll
+            for (int b = 0; b < NB; ++b)
+#pragma unroll
+                for (int k = 0; k < 2; ++k) {
+                    const int page = p0 + g + 8 * k;
+                    float x0 = G64 == 4 ? __fadd_rn(sum[b][0][2 * k], sum[b][1][2 * k]) : sum[b][0][2 * k];
+                    float x1 = G64 == 4 ? __fadd_rn(sum[b][0][2 * k + 1], sum[b][1][2 * k + 1]) : sum[b][0][2 * k + 1];
+                    x0 = now.id[k] < 0 ? -INFINITY : __fmul_rn(x0, unit[b * COLUMNS + 2 * q]);
+                    x1 = now.id[k] < 0 ? -INFINITY : __fmul_rn(x1, unit[b * COLUMNS + 2 * q + 1]);
+                    if (lg >= 1) x0 = fmaxf(x0, x1);
+                    if (lg >= 2) x0 = fmaxf(x0, __shfl_xor_sync(0xffffffffu, x0, 1));
+                    if (lg >= 3) x0 = fmaxf(x0, __shfl_xor_sync(0xffffffffu, x0, 2));
+                    uint32_t *const to = keys + (b * (COLUMNS >> lg) + mine) * width + page;
+                    if (page < n0[b]) *to = ordered(x0);
+                    if (page < n1[b]) to[width] = ordered(x1);
+                }
+            now = next;
         }
     }
+    __syncthreads();
+    for (int i = warp; i < here; i += PIECE_WARPS)
+        choose<Us>(a, t0 + i, h, i == warp ? own : view_of(a, t0 + i, lane), keys + i * width, scratch, bad);
     if (bad) atomicOr(a.status, kDevBadIndex);
 }
 
@@ -537,14 +746,15 @@ int select_ctas(const Kv4SelectArgs &a, int D, const DeviceInfo &dev) {
     return ctas;
 }
 
-template <int D, bool WARP>
-cudaError_t launch_select(const Kv4SelectArgs &a, int ctas, cudaStream_t st, const DeviceInfo &dev) {
-    const int words = select_words(static_cast<int>((a.max_blocks + 3) / 4 * 4), a.Hq / a.Hkv, D), smem = (WARP ? WARPS : 1) * words * 4;
+template <int D>
+cudaError_t launch_clusters(const Kv4SelectArgs &a, cudaStream_t st, const DeviceInfo &dev) {
+    const int ctas = select_ctas(a, D, dev);
+    const int smem = select_words(static_cast<int>((a.max_blocks + 3) / 4 * 4), a.Hq / a.Hkv, D) * 4;
     static SmemLimit limit;
     if (smem > 40 * 1024)
-        if (cudaError_t e = limit.ensure(reinterpret_cast<const void *>(select_kernel<D, WARP>), dev.device, smem)) return e;
+        if (cudaError_t e = limit.ensure(reinterpret_cast<const void *>(select_kernel<D>), dev.device, smem)) return e;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(static_cast<unsigned>((WARP ? (a.T + WARPS - 1) / WARPS : a.T) * a.Hkv * ctas));
+    cfg.gridDim = dim3(static_cast<unsigned>(a.T * a.Hkv * ctas));
     cfg.blockDim = dim3(THREADS);
     cfg.dynamicSmemBytes = static_cast<size_t>(smem);
     cfg.stream = st;
@@ -556,18 +766,47 @@ cudaError_t launch_select(const Kv4SelectArgs &a, int ctas, cudaStream_t st, con
     at[1].val.clusterDim.y = 1;
     at[1].val.clusterDim.z = 1;
     cfg.attrs = at;
-    cfg.numAttrs = WARP ? 1 : 2;
-    return cudaLaunchKernelEx(&cfg, select_kernel<D, WARP>, a);
+    cfg.numAttrs = 2;
+    return cudaLaunchKernelEx(&cfg, select_kernel<D>, a);
 }
 
-// A warp for a token and key head where that gives each SM eight warps or more, and
-// their scores leave room for two CTAs: 301 tokens with 470 pages, 32 heads of 128 on
-// 8, 45 us, with CTAs 62.
+template <int D, int NB>
+cudaError_t launch_piece(const Kv4SelectArgs &a, int lg, cudaStream_t st, const DeviceInfo &dev) {
+    const int smem = piece_words(static_cast<int>((a.max_blocks + 3) / 4 * 4), lg, D, NB) * 4;
+    static SmemLimit limit;
+    if (smem > 40 * 1024)
+        if (cudaError_t e = limit.ensure(reinterpret_cast<const void *>(piece_kernel<D, NB>), dev.device, smem)) return e;
+    const int64_t tokens = NB * (COLUMNS >> lg);
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned>((a.T + tokens - 1) / tokens * a.Hkv));
+    cfg.blockDim = dim3(PIECE_WARPS * 32);
+    cfg.dynamicSmemBytes = static_cast<size_t>(smem);
+    cfg.stream = st;
+    cudaLaunchAttribute pdl[1];
+    pdl[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    pdl[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = pdl;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, piece_kernel<D, NB>, a, lg);
+}
+
+// Tokens of a request together where there are four or more (on average), not too many
+// query heads and room for the scores.  470 pages, a cluster each -> together, us:
+//     new tokens                   16          40          96          301         1200
+//     32 heads of 128 on 8     11 -> 13    17 -> 17    24 -> 19    63 -> 37    230 -> 116
+//     16 heads of 256 on 8     15 -> 15    20 -> 16    28 -> 25    76 -> 29    280 -> 112
+// 16 columns a CTA where that leaves each SM 16 of them or more: 1200 tokens of 32 heads
+// 141 -> 116 us, 301 of them 37 -> 40.
 template <int D>
 cudaError_t launch_select(const Kv4SelectArgs &a, cudaStream_t st, const DeviceInfo &dev) {
-    const int words = select_words(static_cast<int>((a.max_blocks + 3) / 4 * 4), a.Hq / a.Hkv, D);
-    if (a.T * a.Hkv >= 8 * static_cast<int64_t>(dev.num_sms) && WARPS * words * 4 <= 100 * 1024) return launch_select<D, true>(a, 1, st, dev);
-    return launch_select<D, false>(a, select_ctas(a, D, dev), st, dev);
+    const int width = static_cast<int>((a.max_blocks + 3) / 4 * 4), G = a.Hq / a.Hkv;
+    const int lg = G <= 1 ? 0 : G <= 2 ? 1 : G <= 4 ? 2 : 3;
+    if (G <= COLUMNS && a.T >= 4 * static_cast<int64_t>(a.requests)) {
+        const int64_t teams = (a.T + (COLUMNS >> lg) - 1) / (COLUMNS >> lg) * a.Hkv;
+        if (teams >= 16 * dev.num_sms && piece_words(width, lg, D, 2) * 4 <= 72 * 1024) return launch_piece<D, 2>(a, lg, st, dev);
+        if (piece_words(width, lg, D, 1) * 4 <= 110 * 1024) return launch_piece<D, 1>(a, lg, st, dev);
+    }
+    return launch_clusters<D>(a, st, dev);
 }
 
 }  // namespace

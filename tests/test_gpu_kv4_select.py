@@ -112,10 +112,12 @@ def test_select(Hq, Hkv, D, top, first, recent):
     assert w4.w4a16_check_device_error() == 0
 
 
-@pytest.mark.parametrize("Hq,Hkv,D", [(16, 16, 128), (24, 12, 64), (18, 9, 256)])
+@pytest.mark.parametrize("Hq,Hkv,D", [(16, 16, 128), (24, 12, 64), (18, 9, 256), (6, 2, 128), (7, 1, 64), (8, 2, 256), (8, 1, 256),
+                                      (18, 2, 64)])
 @pytest.mark.parametrize("top,first,recent", [(1, 0, 1), (6, 1, 2), (33, 0, 4)])
 def test_select_for_many_tokens(Hq, Hkv, D, top, first, recent):
-    # a warp for each token and head; rows of no request, scores that are equal
+    # tokens of a request together (and 9 query heads, which are too many for that); rows of no
+    # request, requests that end inside such a team, scores that are equal
     torch, w4 = cuda_or_skip()
     ends, new = [700, 90, 30, 0, 401], [101, 1, 30, 0, 3]
     q, raw, table, ends, cu = _batch(torch, ends, new, Hq, Hkv, D, 16, D + top, gap=5)
@@ -124,6 +126,27 @@ def test_select_for_many_tokens(Hq, Hkv, D, top, first, recent):
     _same(_select(torch, w4, q, raw, table, ends, cu, 16, top, first, recent),
           lh.select(q, raw, table, ends, cu, 16, top, first, recent))
     assert w4.w4a16_check_device_error() == 0
+
+
+@pytest.mark.parametrize("Hq,Hkv,D", [(20, 20, 64), (30, 10, 128), (40, 20, 256)])
+def test_select_for_many_requests(Hq, Hkv, D):
+    # more requests than the order by length and a first wave of CTAs take
+    torch, w4 = cuda_or_skip()
+    rng = np.random.default_rng(D)
+    ends = [int(e) for e in rng.integers(1, 500, 130)]
+    q, raw, table, ends, cu = _batch(torch, ends, [1] * 130, Hq, Hkv, D, 16, D)
+    _same(_select(torch, w4, q, raw, table, ends, cu, 16, 9, 1, 2), lh.select(q, raw, table, ends, cu, 16, 9, 1, 2))
+
+
+def test_largest_whole_numbers():
+    # every product at its largest, of either sign: the sums are exact in both forms
+    torch, w4 = cuda_or_skip()
+    for new in (1, 30):
+        q, raw, table, ends, cu = _batch(torch, [1500], [new], 2, 1, 256, 16, new)
+        q[:] = np.where(np.random.default_rng(1).random(q.shape) < 0.5, 1.0, -1.0)
+        raw[..., :256] = np.int8(127).view(np.uint8)
+        raw[..., 256:512] = np.random.default_rng(2).integers(-127, -120, raw[..., 256:512].shape).astype(np.int8).view(np.uint8)
+        _same(_select(torch, w4, q, raw, table, ends, cu, 16, 20, 1, 1), lh.select(q, raw, table, ends, cu, 16, 20, 1, 1))
 
 
 @pytest.mark.parametrize("Hq,Hkv,D,ends,bs", [(2, 1, 256, [70000], 16), (4, 1, 128, [40001, 3, 9000], 32), (2, 2, 64, [33000] * 5, 16)])
