@@ -25,6 +25,7 @@ constexpr int KEYS = 128;      // of a key tile of the tensor cores' kernel
 constexpr int ROUNDS = 4;      // items to a worker at most, where stretches are cut
 constexpr int OVERHEAD = 4;    // cost of an item beside its key tiles, in key tiles,
 constexpr int PARTS = 8;       // and of the parts that it writes
+constexpr int WHOLE = 1 << 24; // key tiles: more than any stretch has
 
 // The stretches of a call, by one CTA.
 //
@@ -151,7 +152,7 @@ __global__ void __launch_bounds__(PLAN_THREADS) plan_kernel(const Kv4PrefixArgs 
         const long long workers = static_cast<long long>(warp + 1) * a.workers - own_items;
         int hi = 0;  // (0: more than so many at best)
         if (workers > all_weight) {
-            hi = static_cast<int>(min((all_tiles + workers - all_weight - 1) / (workers - all_weight), 0x7fffffffll));
+            hi = static_cast<int>(min((all_tiles + workers - all_weight - 1) / (workers - all_weight), static_cast<long long>(WHOLE)));
             int lo = static_cast<int>((all_tiles + workers - 1) / workers);
             while (lo < hi && a.groups <= 256) {  // the least that gives so few
                 const int mid = (lo + hi) >> 1;
@@ -175,7 +176,7 @@ __global__ void __launch_bounds__(PLAN_THREADS) plan_kernel(const Kv4PrefixArgs 
     // length), then the groups'
     if (warp == 0) {
         long long cost = 0x7fffffffffffffffll;
-        int cut = 0x7fffffff;
+        int cut = WHOLE;
         for (int k = 0; k < ROUNDS && all_weight > 0; ++k) {
             const long long its = (k + 1) * (static_cast<long long>(cuts[k]) + OVERHEAD);
             if (cuts[k] > 0 && its < cost) cost = its, cut = cuts[k];

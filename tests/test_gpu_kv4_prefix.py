@@ -183,6 +183,24 @@ def test_many_groups(groups):
     _check(w4, out, host, 64 ** -0.5)
 
 
+@pytest.mark.parametrize("requests,Hq,D", [(540, 20, 64), (270, 40, 128)])
+def test_a_prefix_of_requests_that_fill_the_gpu(requests, Hq, D):
+    # their own items are more than the cut of a shared stretch may add to: it stays whole
+    torch, w4 = cuda_or_skip()
+    dev, host = lh.grouped(torch, [(1040, [(i % 5, 1) for i in range(requests)])], Hq, 1, D, 16, D)
+    out = _run(w4, dev, max_new=1, max_group=requests)
+    _check(w4, out, host, D ** -0.5)
+
+
+@pytest.mark.parametrize("D,members", [(64, 1), (256, 2)])
+def test_most_requests_and_groups(D, members):
+    torch, w4 = cuda_or_skip()
+    some = [(16, [(j, 1) for j in range(members)]) for _ in range(4096 // members)]
+    dev, host = lh.grouped(torch, some, 2, 1, D, 16, D)
+    out = _run(w4, dev, max_new=1, max_group=members)
+    _check(w4, out, host, D ** -0.5)
+
+
 @pytest.mark.parametrize("rows,Hq,Hkv,D", [(30, 16, 8, 256), (30, 8, 2, 128), (60, 8, 2, 64), (3, 4, 1, 128)])
 @pytest.mark.parametrize("flag", [1, 2])
 def test_waits_that_run_out(rows, Hq, Hkv, D, flag):
