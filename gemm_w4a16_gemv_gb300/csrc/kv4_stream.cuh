@@ -371,13 +371,15 @@ __global__ void __launch_bounds__(W * 32, 1) attn_stream_kernel(const A a, const
     if (lane == 0)
         for (int i = 0; i < depth; ++i) mbar_init(&bars[i], 1);
     fence_barrier_init();
-    pdl_launch_dependents();
     // `early`: the kernel before this one is not what this one needs; it began when
-    // that was there.  So this one takes the SMs as they become free, and waits for
-    // the other at its end, for the sake of the kernel after both.
+    // that was there, and lets this one begin only then.  So this one takes the SMs as
+    // they become free, and waits for the other at its end, for the sake of the kernel
+    // after both.
     bool early = false;
     if constexpr (A::kShared) early = a.early;
+    if (!A::kShared) pdl_launch_dependents();
     if (!early) pdl_wait();
+    if (A::kShared) pdl_launch_dependents();
 
     // ---- tiles of the requests, their running sum
     {
