@@ -565,7 +565,8 @@ int kv4_prefix_attention(const uint16_t *q, int64_t q_stride,
  * binary32).  The page of each slot that is the last of its page is written, from
  * all its tokens as the cache holds them: after kv4_append with the same slots
  * that is every page that the step filled.  Pages not yet full need no bounds:
- * kv4_select takes a token's own page unseen.
+ * kv4_select takes a token's own page unseen.  Where a scale or zero point is not
+ * finite the bounds of its 64 elements are unspecified.
  *   slots : int64 [T]; negative ones are passed over, one past the cache sets
  *           the device status
  */
@@ -586,7 +587,8 @@ int kv4_bounds(const uint8_t *cache, int64_t num_blocks, int block_size,
  * dot in whole numbers, exact; the rest in binary32, each operation rounded,
  * neighbouring terms added first.  So the score is, but for the 8 bits of q, what
  * no q . k of the page exceeds.  A NaN in q counts as 0, an infinity as the
- * largest finite number.  (For attention with a scale above 0.)
+ * largest finite number; a query head whose score is NaN has no say, and a page
+ * with no other the lowest score.  (For attention with a scale above 0.)
  *   bounds : as kv4_bounds writes them; those of the pages before the `recent`
  *            ones are read
  *   tables : int32 [T, Hkv, top]: the ids of the pages taken, in the order of the

@@ -102,7 +102,7 @@ def scores(q, raw, ids, h):
     key head h; -inf for ids outside the cache."""
     D = q.shape[1]
     q = np.clip(np.where(np.isnan(q), F(0), q), F(-3.3895314e38), F(3.3895314e38)).astype(F)
-    with np.errstate(over="ignore"):
+    with np.errstate(over="ignore", invalid="ignore"):
         u = np.abs(q).max(-1) * F(65 / 8192)
         c = np.rint(q / np.where(u > 0, u, F(1))[:, None]).astype(np.int64)
         out = np.full(len(ids), -np.inf, F)
@@ -116,7 +116,7 @@ def scores(q, raw, ids, h):
             t = dot.astype(F) * step
             while t.shape[1] > 1:
                 t = t[:, 0::2] + t[:, 1::2]
-            out[i] = (t[:, 0] * u).max()
+            out[i] = np.fmax.reduce(t[:, 0] * u, initial=-np.inf)
     return out
 
 

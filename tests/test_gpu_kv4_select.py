@@ -356,3 +356,27 @@ def test_copies_that_never_come(T, D):
     for _ in range(3):
         assert torch.equal(first, w4.kv4_sparse_attention(*args))
     assert w4.w4a16_check_device_error() == 0
+
+
+@pytest.mark.parametrize("Hq,Hkv", [(1, 1), (8, 2)])
+@pytest.mark.parametrize("new", [1, 30])
+def test_steps_that_are_not_finite(Hq, Hkv, new):
+    # products of 0 and infinity, sums of infinities of both signs, NaN
+    torch, w4 = cuda_or_skip()
+    rng = np.random.default_rng(new)
+    q, raw, table, ends, cu = _batch(torch, [1500], [new], Hq, Hkv, 256, 16, new)
+    steps = raw[..., 512:].view(np.float32)
+    for value in (np.nan, np.inf):
+        steps[rng.random(steps.shape) < 0.1] = value
+    _same(_select(torch, w4, q, raw, table, ends, cu, 16, 20, 1, 1), lh.select(q, raw, table, ends, cu, 16, 20, 1, 1))
+
+
+@pytest.mark.parametrize("Hq,Hkv", [(1, 1), (8, 2)])
+@pytest.mark.parametrize("new", [1, 30])
+def test_scores_that_vanish(Hq, Hkv, new):
+    # zeros of either sign are equal scores
+    torch, w4 = cuda_or_skip()
+    q, raw, table, ends, cu = _batch(torch, [1500], [new], Hq, Hkv, 128, 16, new)
+    q *= 2.0 ** -110
+    raw[..., 256:].view(np.float32)[...] *= np.float32(2.0 ** -40)
+    _same(_select(torch, w4, q, raw, table, ends, cu, 16, 20, 1, 1), lh.select(q, raw, table, ends, cu, 16, 20, 1, 1))
