@@ -72,6 +72,7 @@ __global__ void __launch_bounds__(PLAN_THREADS) plan_kernel(const Kv4PrefixArgs 
     pdl_launch_dependents();
     pdl_wait();
     const long long table = a.max_blocks << a.bs_log2, cap = min(table, 0x7fffff00ll);
+    const long long most = min(cap, 0x7fffff00ll - a.T);  // keys of a shared stretch (key and row number together: 31 bits)
     if (tid == 0) all_weight = all_tiles = 0, own_items = 0;
     // ---- lengths and borders; if some are out of range, nothing is shared
     bool bad = false;
@@ -126,7 +127,7 @@ __global__ void __launch_bounds__(PLAN_THREADS) plan_kernel(const Kv4PrefixArgs 
         apart = __reduce_add_sync(0xffffffffu, apart);
         begun = __reduce_add_sync(0xffffffffu, begun);
         const int rows = (x.cu[last] - x.cu[first]) * G;
-        int keys = count < 2 ? 0 : static_cast<int>(min(static_cast<long long>(max(least, 0)), cap)) & ~15;
+        int keys = count < 2 ? 0 : static_cast<int>(min(static_cast<long long>(max(least, 0)), most)) & ~15;
         const int tiles = (keys + KEYS - 1) / KEYS, items = blocks(rows, a.item_rows);
         const bool many = rows >= a.least_shared;
         const long long together = many ? 8ll * items * (tiles + PARTS + OVERHEAD) + 8ll * begun * OVERHEAD

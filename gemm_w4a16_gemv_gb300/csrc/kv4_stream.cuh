@@ -1076,10 +1076,10 @@ cudaError_t stream(const A &a, int D, int64_t rows, cudaStream_t st, const Devic
 //     8 segments, 8000 keys, rows     16   32   64  128     (us: streamed / prompt)
 //       D = 256                       33   41   51   70  / 113 for all
 //     128 segments, 4000 keys         16   24   32   64
-//       D = 256                       74  184  185  249  / 135
-//       D = 128                       49    -   97  147  / 108
+//       D = 256                       74  184  185  249  / 128
+//       D = 128                       49    -   97  147  / 101
 //     512 segments, 1000 keys         16   24   32   48   64
-//       D = 256                      118  163  163  214  260  / 143
+//       D = 256                      118  163  163  214  260  / 139
 //       D = 128                       75    -   96  122  147  / 114
 //       D = 64                        57   65   66   83   99  / 58
 inline int64_t stream_rows(int64_t segments, int D, const DeviceInfo &dev) {
