@@ -1,6 +1,7 @@
 // Attention over the paged 4-bit cache for pieces of many new tokens, on the
 // tcgen05 tensor cores (kv4_attention in the C header; the streaming form for
-// few rows is kv4_attention.cu).
+// few rows is kv4_stream.cuh).  For kv4_prefix_attention the same kernel has pieces
+// of shared stretches of keys as its requests and leaves parts to be joined.
 //
 // An item is 128 rows (new tokens x the G query heads of one key head) of a
 // request, or 256 for a pair of CTAs; its keys are taken 128 at a time:
@@ -19,11 +20,11 @@
 // SM, and leaves room for two buffers of each operand.  One CTA of the pair
 // issues the products of both.  Measured on 6491 new tokens in three requests
 // with up to 6000 tokens before them, 16 heads of 256 on 8: single CTAs 455 us,
-// pairs 297 us, 1136 TFLOP/s.  What bounds it now is the softmax: 2700 cycles a
-// tile (4 x 32 keys, each 170 until the scores are there, 190 for the
-// reference, 250 for the weights), of which the exponentials are 512 per SM
-// quarter; the code is kept short (rolled loops, masks as 32-bit words),
-// because its three roles share the instruction cache (341 -> 298 us).
+// pairs 280 us, 1200 TFLOP/s.  A tile takes about 3700 cycles.  No stage does by
+// itself (the tensor pipe 2048; the softmax 1290 with the SM to itself, of which the
+// exponentials are 512 per SM quarter); they wait for one another, and the three roles
+// share the issue slots, 55 % of them busy, and the instruction cache: the code is
+// kept short (rolled loops, masks as 32-bit words: 341 -> 298 us).
 // (D = 64 stays with single CTAs: half of its 64 dimensions is no whole
 // swizzled row.)
 //
