@@ -15,12 +15,14 @@
 //
 // Bound: operations of the tensor cores' kernel where a group has many rows, latency
 // where it has few.  16 heads of 256 on 8: 128 requests behind 32768 tokens, 1 to 2000
-// of their own, 117 us (each for itself: 790): the plan about 6, the shared part 85, the
-// rest and the join 26; 12 prompts of 101 to 700 tokens behind 6016: 357 us, 1090
-// TFLOP/s; 4 samples behind 2048, which lie in L2, 18.6 us without sharing (40 with).
-// 32 heads of 128 on 8, 7 groups of up to 30 requests of 1 to 4 new tokens: 126 us, alone
-// the plan 8, the shared parts 72, the rest 33, the join 10 (the first two kernels of
-// these overlap a little).
+// of their own, 117 us (each for itself: 790): the plan 8; the shared part 62, of which
+// 11 until the first scores are there, 1.55 a key tile (the tensor pipe 1.0), 4 its end; the
+// rest 22; the join 5.5; the rest between the launches.  16384 more shared tokens are 18 to
+// 23 us, 80% of the tensor cores' rate.  12 prompts of 101 to 700 tokens behind 6016:
+// 360 us, 1080 TFLOP/s (nothing shared: their rows fill the items by themselves); 4
+// samples behind 2048, which lie in L2, 18.6 us without sharing (40 with).  32 heads of
+// 128 on 8, 7 groups of up to 30 requests of 1 to 4 new tokens: 125 us: the plan 8, the
+// shared parts 60 to 70, the rest 22, the join 5.
 #include "kv4_stream.cuh"
 
 namespace w4 {
@@ -34,6 +36,7 @@ constexpr int KEYS = 128;      // of a key tile of the tensor cores' kernel
 constexpr int ROUNDS = 4;      // items to a worker at most, where stretches are cut
 constexpr int OVERHEAD = 4;    // cost of an item beside its key tiles, in key tiles,
 constexpr int PARTS = 8;       // and of the parts that it writes
+constexpr int SORTED = 256;    // requests that are compared with one another
 constexpr int WHOLE = 1 << 24; // key tiles: more than any stretch has
 
 // The stretches of a call, by one CTA.
@@ -49,14 +52,21 @@ constexpr int WHOLE = 1 << 24; // key tiles: more than any stretch has
 // rows and a key head each) fill the workers: with w items a piece and t key
 // tiles, cuts of c tiles give sum w ceil(t / c) items, at least sum w t / c and less
 // than sum w more.  Between what these two say lies the least c that gives at most k
-// items to a worker; of k = 1 .. ROUNDS the one with the least k (c + OVERHEAD) is
-// taken.
+// items to a worker; of k = 1 .. ROUNDS the one is taken that ends first, after
+// k (c + OVERHEAD) or all items' cost over the workers, those of the requests' own
+// rows included, which fill what the others leave.  So items begin in the order of
+// their length: those of requests with as many key tiles as a piece has, the pieces,
+// the other requests', these by length too.  (The requests' first and as they come, and
+// as if each took as long as a piece: prompts of 101 to 700 tokens, 4 groups of 3 behind
+// 500 to 9000 tokens 255 us, now 184; 12 after 1000 to 9000 of their own behind 6016 627,
+// now 559.)
 //
 // Every array is read once, all elements on their way together: the kernel is a
 // chain of latencies (before the others can begin).
 struct PlanSmem {
     int *cu, *ctx, *owner;              // [members + 1] rows before, [members] tokens before the step, the group
     int *border, *shared, *weight;      // [groups + 1], [groups] keys that are shared, items of a piece or 0
+    int *tiles, *order;                 // [members] key tiles of those with many rows or 0; the longest first
     long long *place, *piece;           // [groups] first place; first piece << 40 | first item
     __device__ PlanSmem(unsigned char *p, int groups, int members) {
         place = reinterpret_cast<long long *>(p);
@@ -67,22 +77,24 @@ struct PlanSmem {
         border = owner + members;
         shared = border + groups + 1;
         weight = shared + groups;
+        tiles = weight + groups;
+        order = tiles + members;
     }
-    static int bytes(int groups, int members) { return 28 * groups + 12 * members + 8; }
+    static int bytes(int groups, int members) { return 28 * groups + 20 * members + 8; }
 };
 
 __global__ void __launch_bounds__(PLAN_THREADS) plan_kernel(const Kv4PrefixArgs a) {
     extern __shared__ __align__(16) unsigned char plan_smem[];
     const PlanSmem x(plan_smem, a.groups, a.members);
-    __shared__ long long all_weight, all_tiles;  // sums of w, of w t
-    __shared__ int own_items, cut_tiles, cuts[ROUNDS];
+    __shared__ long long all_weight, all_tiles, all_own;  // sums of w, of w t, of the requests' own items' cost
+    __shared__ int longest, cut_tiles, cuts[ROUNDS], counts[ROUNDS];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int G = a.Hq / a.Hkv;
     pdl_launch_dependents();
     pdl_wait();
     const long long table = a.max_blocks << a.bs_log2, cap = min(table, 0x7fffff00ll);
     const long long most = min(cap, 0x7fffff00ll - a.T);  // keys of a shared stretch (key and row number together: 31 bits)
-    if (tid == 0) all_weight = all_tiles = 0, own_items = 0;
+    if (tid == 0) all_weight = all_tiles = all_own = 0, longest = 0;
     // ---- lengths and borders; if some are out of range, nothing is shared
     bool bad = false;
     for (int i = tid; i <= a.members; i += PLAN_THREADS) {
@@ -148,19 +160,42 @@ __global__ void __launch_bounds__(PLAN_THREADS) plan_kernel(const Kv4PrefixArgs 
             if (keys > 0 && many) {
                 atomicAdd(reinterpret_cast<unsigned long long *>(&all_weight), static_cast<unsigned long long>(x.weight[g]));
                 atomicAdd(reinterpret_cast<unsigned long long *>(&all_tiles), static_cast<unsigned long long>(x.weight[g]) * tiles);
+                atomicMax(&longest, tiles);
             }
         }
     }
-    if (least_own != 0x7fffffff)
+    // key tiles of a request's own
+    auto own_tiles = [&](int b) {
+        const int g = x.owner[b];
+        const long long keys = min(static_cast<long long>(x.ctx[b]) + (x.cu[b + 1] - x.cu[b]), cap) - (g >= 0 ? x.shared[g] : 0);
+        return static_cast<int>((max(keys, 1ll) + KEYS - 1) / KEYS);
+    };
+    if (least_own != 0x7fffffff) {
+        __syncthreads();
         for (int b = tid; b < a.members; b += PLAN_THREADS) {
             const int rows = (x.cu[b + 1] - x.cu[b]) * G;
-            if (rows >= least_own) atomicAdd(&own_items, blocks(rows, a.item_rows) * a.Hkv);
+            const int tiles = rows >= least_own ? own_tiles(b) : 0;
+            x.tiles[b] = tiles;
+            if (tiles)
+                atomicAdd(reinterpret_cast<unsigned long long *>(&all_own),
+                          static_cast<unsigned long long>(blocks(rows, a.item_rows)) * a.Hkv * (tiles + OVERHEAD));
         }
+    }
     __syncthreads();
+    if (all_own > 0)
+        for (int b = tid; b < a.members; b += PLAN_THREADS) {
+            int at = b;
+            if (a.members <= SORTED) {
+                const int mine = x.tiles[b];
+                at = 0;
+                for (int o = 0; o < a.members; ++o) at += x.tiles[o] > mine || (x.tiles[o] == mine && o < b);
+            }
+            x.order[at] = b;
+        }
     // ---- the cut, a warp for each number of rounds
     if (warp < ROUNDS && all_weight > 0) {
-        const long long workers = static_cast<long long>(warp + 1) * a.workers - own_items;
-        int hi = 0;  // (0: more than so many at best)
+        const long long workers = static_cast<long long>(warp + 1) * a.workers;
+        int hi = 0, count = static_cast<int>(workers);  // (0: more than so many at best)
         if (workers > all_weight) {
             hi = static_cast<int>(min((all_tiles + workers - all_weight - 1) / (workers - all_weight), static_cast<long long>(WHOLE)));
             int lo = static_cast<int>((all_tiles + workers - 1) / workers);
@@ -169,11 +204,12 @@ __global__ void __launch_bounds__(PLAN_THREADS) plan_kernel(const Kv4PrefixArgs 
                 int items = 0;  // (2^31 are not possible: mid is at least their mean)
                 for (int g = lane; g < a.groups; g += 32)
                     if (x.shared[g] > 0) items += x.weight[g] * (((x.shared[g] + KEYS - 1) / KEYS + mid - 1) / mid);
-                if (__reduce_add_sync(0xffffffffu, items) <= workers) hi = mid;
+                items = __reduce_add_sync(0xffffffffu, items);
+                if (items <= workers) hi = mid, count = items;
                 else lo = mid + 1;
             }
         }
-        if (lane == 0) cuts[warp] = hi;
+        if (lane == 0) cuts[warp] = hi, counts[warp] = count;
     }
     bool loose = false;  // requests that share nothing and are streamed: some of their rows may be split
     auto is_loose = [&](int b) {
@@ -182,13 +218,13 @@ __global__ void __launch_bounds__(PLAN_THREADS) plan_kernel(const Kv4PrefixArgs 
     };
     for (int b = tid; b < a.members; b += PLAN_THREADS) loose |= is_loose(b);
     loose = __syncthreads_or(loose);
-    // ---- pieces and places in their order: requests' pieces first (they differ in
-    // length), then the groups'
+    // ---- pieces and places in their order
     if (warp == 0) {
         long long cost = 0x7fffffffffffffffll;
         int cut = WHOLE;
         for (int k = 0; k < ROUNDS && all_weight > 0; ++k) {
-            const long long its = (k + 1) * (static_cast<long long>(cuts[k]) + OVERHEAD);
+            const long long its = max((k + 1) * (static_cast<long long>(cuts[k]) + OVERHEAD),
+                                      (all_tiles + static_cast<long long>(counts[k]) * OVERHEAD + all_own) / a.workers);
             if (cuts[k] > 0 && its < cost) cost = its, cut = cuts[k];
         }
         if (lane == 0) cut_tiles = cut;
@@ -206,16 +242,20 @@ __global__ void __launch_bounds__(PLAN_THREADS) plan_kernel(const Kv4PrefixArgs 
             total += __shfl_sync(0xffffffffu, in, 31);
             return mine;
         };
-        if (own_items > 0)
-            for (int b0 = 0; b0 < a.members; b0 += 32) {
-                const int b = b0 + lane, rows = b < a.members ? (x.cu[b + 1] - x.cu[b]) * G : 0;
-                const bool many = rows >= least_own;
+        const int most_tiles = min(cut, longest);  // of a piece
+        auto own = [&](bool those_long) {
+            for (int b0 = 0; all_own > 0 && b0 < a.members; b0 += 32) {
+                const int b = b0 + lane < a.members ? x.order[b0 + lane] : 0, tiles = b0 + lane < a.members ? x.tiles[b] : 0;
+                const int rows = (x.cu[b + 1] - x.cu[b]) * G;
+                const bool many = tiles > 0 && (tiles >= most_tiles) == those_long;
                 const long long mine = before(many ? 1ll << 40 | static_cast<long long>(blocks(rows, a.item_rows)) * a.Hkv : 0, at);
                 if (many) {
                     a.before[mine >> 40] = static_cast<int>(mine & ((1ll << 40) - 1));
                     a.piece_of[b] = static_cast<int>(mine >> 40);
                 }
             }
+        };
+        own(true);
         for (int g0 = 0; g0 < a.groups; g0 += 32) {
             const int g = g0 + lane;
             const bool on = g < a.groups && x.shared[g] > 0;
@@ -237,6 +277,7 @@ __global__ void __launch_bounds__(PLAN_THREADS) plan_kernel(const Kv4PrefixArgs 
             }
             shares += __popc(some);
         }
+        own(false);
         for (int b0 = 0; loose && b0 < a.members; b0 += 32) {
             const int b = b0 + lane;
             const bool on = b < a.members && is_loose(b);
