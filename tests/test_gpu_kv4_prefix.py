@@ -185,11 +185,37 @@ def test_many_groups(groups):
 
 @pytest.mark.parametrize("requests,Hq,D", [(540, 20, 64), (270, 40, 128)])
 def test_a_prefix_of_requests_that_fill_the_gpu(requests, Hq, D):
-    # their own items are more than the cut of a shared stretch may add to: it stays whole
+    # their own items fill it several times over
     torch, w4 = cuda_or_skip()
     dev, host = lh.grouped(torch, [(1040, [(i % 5, 1) for i in range(requests)])], Hq, 1, D, 16, D)
     out = _run(w4, dev, max_new=1, max_group=requests)
     _check(w4, out, host, D ** -0.5)
+
+
+def test_a_prefix_with_more_items_than_pieces_may_have():
+    # it stays whole.  Against kv4_attention, each of them within the bound of kv4_helpers.attention
+    # of the exact result, with the largest |k| and |v| for every one
+    torch, w4 = cuda_or_skip()
+    n, H, D, pages = 4096, 20, 64, 20
+    i32 = dict(dtype=torch.int32, device="cuda")
+    g = torch.Generator("cuda").manual_seed(1)
+    rows = lambda m: torch.randn(m, H, D, device="cuda", generator=g).to(torch.bfloat16).clamp(-4, 4)
+    cache = w4.kv4_cache(pages + n, H, 16, D)
+    lead = torch.randperm(pages + n, device="cuda", generator=g).to(torch.int32)
+    own = lead[pages:]
+    slots = torch.cat([(lead[:pages].long()[:, None] * 16 + torch.arange(16, device="cuda")).flatten(), own.long() * 16])
+    w4.kv4_append(rows(len(slots)), rows(len(slots)), cache, slots)
+    table = torch.cat([lead[:pages].expand(n, pages), own[:, None]], 1).contiguous()
+    q, ends, cu = rows(n), torch.full((n,), 16 * pages + 1, **i32), torch.arange(n + 1, **i32)
+    one = lambda x: torch.tensor(x, **i32)
+    got = w4.kv4_prefix_attention(q, cache, table, ends, cu, one([16 * pages]), one([0, n]),
+                                  w4.kv4_prefix_attention_scratch(n, n, 1, H, H, D), max_new=1, max_group=n).double()
+    want = w4.kv4_attention(q, cache, table, ends, cu, w4.kv4_attention_scratch(H, H, D), max_new=1).double()
+    largest = 4 + 8 / 15               # a rounding of 4 bits off the values written
+    e = (2.0 ** -12 + 2.0 ** -20) * D ** -0.5 * largest * q.double().abs().sum(-1, keepdim=True)
+    tol = 2 * (2.0 ** -8 * want.abs() + (2.0 ** -11 + 2.0 ** -12 + 2.0 ** -16 + torch.expm1(2 * e)) * largest * (1 + 2.0 ** -8))
+    assert w4.w4a16_check_device_error() == 0
+    assert ((got - want).abs() <= tol).all()
 
 
 @pytest.mark.parametrize("D,members", [(64, 1), (256, 2)])
