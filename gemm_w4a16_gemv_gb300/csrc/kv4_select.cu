@@ -555,7 +555,7 @@ __global__ void __launch_bounds__(THREADS, 3) select_kernel(const Kv4SelectArgs 
 // `low`.  A lane's 16 bytes of a row are the operands of four products, in any order
 // of the 64 elements that is the queries' too.  Two groups of 64 of the rows are on
 // their way meanwhile.  Bound: the conversions and products beside them, and the choice
-// (301 tokens x 470 pages, 32 heads of 128 on 8, 37 us; with 8-bit products by dp4a, a
+// (301 tokens x 470 pages, 32 heads of 128 on 8, 30 us; with 8-bit products by dp4a, a
 // warp each, 45; the 8-bit MMA takes 64 cycles for what the 16-bit one does in 16).
 constexpr int COLUMNS = 8;
 
@@ -574,16 +574,14 @@ __device__ __forceinline__ void halves(uint32_t w, uint32_t &lo, uint32_t &hi) {
     asm("sub.rn.f16x2 %0, %0, %1;" : "+r"(hi) : "r"(0x64806480u));
 }
 
-constexpr int PIECE_WARPS = 4;
-
-// Words of shared memory, for NB times 8 columns: keys of the tokens, queries, units,
-// what the tokens see, and of each warp scratch.
-__host__ __device__ constexpr int piece_words(int width, int lg, int D, int NB) {
-    return NB * ((width << (3 - lg)) + D * 8 + 3 * COLUMNS) + PIECE_WARPS * (256 + 2 * WARPS + 8);
+// Words of shared memory, for NB times 8 columns and W warps: keys of the tokens,
+// queries, units, what the tokens see, and of each warp scratch.
+__host__ __device__ constexpr int piece_words(int width, int lg, int D, int NB, int W) {
+    return NB * ((width << (3 - lg)) + D * 8 + 3 * COLUMNS) + W * (256 + 2 * WARPS + 8);
 }
 
-template <int D, int NB>
-__global__ void __launch_bounds__(PIECE_WARPS * 32, NB == 1 ? 4 : 3) piece_kernel(const Kv4SelectArgs a, const int lg) {
+template <int D, int NB, int W>
+__global__ void __launch_bounds__(W * 32, (NB == 1 ? 16 : 12) / W) piece_kernel(const Kv4SelectArgs a, const int lg) {
     using Us = Team<true>;
     constexpr int G64 = D / 64, NEXT = G64 > 1 ? 2 : 1;  // groups on their way
     extern __shared__ __align__(16) uint32_t select_smem[];
@@ -600,7 +598,7 @@ __global__ void __launch_bounds__(PIECE_WARPS * 32, NB == 1 ? 4 : 3) piece_kerne
     pdl_launch_dependents();
     pdl_wait();
     check_step(a);
-    for (int c = warp; c < NB * COLUMNS; c += PIECE_WARPS) {
+    for (int c = warp; c < NB * COLUMNS; c += W) {
         const int64_t t = t0 + min(c >> lg, here - 1);
         const Query<D> raw = load_query<D>(a.q + t * a.q_stride + static_cast<int64_t>(h * G + (c & ((1 << lg) - 1)) % G) * D, lane);
         float x[Query<D>::PER][4];
@@ -616,7 +614,7 @@ __global__ void __launch_bounds__(PIECE_WARPS * 32, NB == 1 ? 4 : 3) piece_kerne
         if (lane == 0) unit[c] = step;
     }
     View own;  // of this warp's first token
-    for (int i = warp; i < here; i += PIECE_WARPS) {
+    for (int i = warp; i < here; i += W) {
         const View v = view_of(a, t0 + i, lane);
         if (lane == 0) request[i] = v.b, count[i] = v.need > 0 ? v.n : 0;
         if (i == warp) own = v;
@@ -641,7 +639,7 @@ __global__ void __launch_bounds__(PIECE_WARPS * 32, NB == 1 ? 4 : 3) piece_kerne
             n1[b] = lg == 0 ? keys_of(b * COLUMNS + mine + 1) : 0;
         }
         const int32_t *const pages = a.block_table + static_cast<int64_t>(request[from]) * a.max_blocks + a.first;
-        constexpr int STEP = 16 * PIECE_WARPS;
+        constexpr int STEP = 16 * W;
         auto ids = [&](int p0) { return lane < 16 && p0 + lane < n ? pages[p0 + lane] : NO_PAGE; };
         struct Pages {
             const unsigned char *row[2];  // of pages g and g + 8
@@ -734,7 +732,7 @@ __global__ void __launch_bounds__(PIECE_WARPS * 32, NB == 1 ? 4 : 3) piece_kerne
         }
     }
     __syncthreads();
-    for (int i = warp; i < here; i += PIECE_WARPS)
+    for (int i = warp; i < here; i += W)
         choose<Us>(a, t0 + i, h, i == warp ? own : view_of(a, t0 + i, lane), keys + i * width, scratch, bad);
     if (bad) atomicOr(a.status, kDevBadIndex);
 }
@@ -774,16 +772,15 @@ cudaError_t launch_clusters(const Kv4SelectArgs &a, cudaStream_t st, const Devic
     return cudaLaunchKernelEx(&cfg, select_kernel<D>, a);
 }
 
-template <int D, int NB>
-cudaError_t launch_piece(const Kv4SelectArgs &a, int lg, cudaStream_t st, const DeviceInfo &dev) {
-    const int smem = piece_words(static_cast<int>((a.max_blocks + 3) / 4 * 4), lg, D, NB) * 4;
+template <int D, int NB, int W>
+cudaError_t launch_piece(const Kv4SelectArgs &a, int lg, int smem, cudaStream_t st, const DeviceInfo &dev) {
     static SmemLimit limit;
     if (smem > 40 * 1024)
-        if (cudaError_t e = limit.ensure(reinterpret_cast<const void *>(piece_kernel<D, NB>), dev.device, smem)) return e;
+        if (cudaError_t e = limit.ensure(reinterpret_cast<const void *>(piece_kernel<D, NB, W>), dev.device, smem)) return e;
     const int64_t tokens = NB * (COLUMNS >> lg);
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(static_cast<unsigned>((a.T + tokens - 1) / tokens * a.Hkv));
-    cfg.blockDim = dim3(PIECE_WARPS * 32);
+    cfg.blockDim = dim3(W * 32);
     cfg.dynamicSmemBytes = static_cast<size_t>(smem);
     cfg.stream = st;
     cudaLaunchAttribute pdl[1];
@@ -791,24 +788,35 @@ cudaError_t launch_piece(const Kv4SelectArgs &a, int lg, cudaStream_t st, const 
     pdl[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = pdl;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, piece_kernel<D, NB>, a, lg);
+    return cudaLaunchKernelEx(&cfg, piece_kernel<D, NB, W>, a, lg);
 }
 
 // Tokens of a request together where there are four or more (on average), not too many
-// query heads and room for the scores.  470 pages, a cluster each -> together, us:
-//     new tokens                   16          40          96          301         1200
-//     32 heads of 128 on 8     11 -> 13    17 -> 17    24 -> 19    63 -> 37    230 -> 116
-//     16 heads of 256 on 8     15 -> 15    20 -> 16    28 -> 25    76 -> 29    280 -> 112
-// 16 columns a CTA where that leaves each SM 16 of them or more: 1200 tokens of 32 heads
-// 141 -> 116 us, 301 of them 37 -> 40.
+// query heads and room for the scores.
+//
+// Warps of a CTA: 8, or 4 or 2 where one wave of such CTAs takes them and one of larger
+// ones does not (so many warps score a token's pages, and one chooses); with more than that
+// 16 columns, whose conversions serve twice as many, and 4 warps, or 2 in two waves or more
+// for the few tokens of a CTA with four query heads (600 tokens: 59 | 71).  470 pages, us: a cluster for each token | 8
+// columns with 8, 4, 2 warps | 16 columns with 4, 2:
+//     new tokens                16                 96                 301                 1200
+//     32 heads of 128 on 8   11 | 12 12 16 | -   24 | 25 19 26 | -   63 | 51 37 31 | 40 38   230 | 194 142 116 | 116 109
+//     16 heads of 256 on 8   15 | 14 16 28 | -   28 | 19 26 32 | -   77 | 36 29 35 | 34 42   280 | 140 113 109 |  99 131
+//     16 heads of 64 on 16        9 15 26 | -         12 19 28 | -         22 20 29 | 28 48          85  75  72 |  67 104
 template <int D>
 cudaError_t launch_select(const Kv4SelectArgs &a, cudaStream_t st, const DeviceInfo &dev) {
     const int width = static_cast<int>((a.max_blocks + 3) / 4 * 4), G = a.Hq / a.Hkv;
     const int lg = G <= 1 ? 0 : G <= 2 ? 1 : G <= 4 ? 2 : 3;
     if (G <= COLUMNS && a.T >= 4 * static_cast<int64_t>(a.requests)) {
-        const int64_t teams = (a.T + (COLUMNS >> lg) - 1) / (COLUMNS >> lg) * a.Hkv;
-        if (teams >= 16 * dev.num_sms && piece_words(width, lg, D, 2) * 4 <= 72 * 1024) return launch_piece<D, 2>(a, lg, st, dev);
-        if (piece_words(width, lg, D, 1) * 4 <= 110 * 1024) return launch_piece<D, 1>(a, lg, st, dev);
+        const int64_t ctas = (a.T + (COLUMNS >> lg) - 1) / (COLUMNS >> lg) * a.Hkv, sms = dev.num_sms;
+        auto bytes = [&](int NB, int W) { return piece_words(width, lg, D, NB, W) * 4; };
+        // (so many CTAs that the registers allow find room)
+        auto room = [&](int NB, int W) { return bytes(NB, W) <= 220 * 1024 / ((NB == 1 ? 16 : 12) / W); };
+        if (ctas > 24 * sms && lg >= 2 && room(2, 2)) return launch_piece<D, 2, 2>(a, lg, bytes(2, 2), st, dev);
+        if (ctas > 8 * sms && room(2, 4)) return launch_piece<D, 2, 4>(a, lg, bytes(2, 4), st, dev);
+        if (ctas > 4 * sms && room(1, 2)) return launch_piece<D, 1, 2>(a, lg, bytes(1, 2), st, dev);
+        if (ctas > 2 * sms && room(1, 4)) return launch_piece<D, 1, 4>(a, lg, bytes(1, 4), st, dev);
+        if (room(1, 8)) return launch_piece<D, 1, 8>(a, lg, bytes(1, 8), st, dev);
     }
     return launch_clusters<D>(a, st, dev);
 }

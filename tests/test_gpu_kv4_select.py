@@ -128,6 +128,15 @@ def test_select_for_many_tokens(Hq, Hkv, D, top, first, recent):
     assert w4.w4a16_check_device_error() == 0
 
 
+@pytest.mark.parametrize("Hq,Hkv,D,T", [(40, 10, 64, 140), (48, 12, 256, 140), (70, 70, 64, 145), (34, 17, 256, 300), (96, 12, 128, 140),
+                                        (64, 8, 64, 470), (30, 10, 256, 750), (24, 8, 128, 960)])
+def test_select_for_so_many_tokens_that_a_wave_does_not_take_them(Hq, Hkv, D, T):
+    torch, w4 = cuda_or_skip()
+    p = _batch(torch, [T + 150, 130, 0], [T - 9, 7, 0], Hq, Hkv, D, 16, T, gap=2)
+    _same(_select(torch, w4, *p, 16, 6, 1, 1), lh.select(*p, 16, 6, 1, 1))
+    assert w4.w4a16_check_device_error() == 0
+
+
 @pytest.mark.parametrize("Hq,Hkv,D", [(20, 20, 64), (30, 10, 128), (40, 20, 256)])
 def test_select_for_many_requests(Hq, Hkv, D):
     # more requests than the order by length and a first wave of CTAs take
