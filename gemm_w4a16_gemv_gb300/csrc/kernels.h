@@ -179,6 +179,7 @@ struct Kv4AttnArgs {
     unsigned int inject;  // test-only injection flags (0 normally)
     static constexpr bool kShared = false;  // keys of a row in several stretches
     static constexpr bool kTail = true;     // rows that belong to no request are zeroed
+    static constexpr bool kEven = false;    // requests are of a length, as a rule
 };
 constexpr int PROMPT_COUNTERS = 13056;  // byte offset in the scratch of the prompt kernel's two counters
 cudaError_t launch_kv4_prompt(const Kv4AttnArgs &a, int D, cudaStream_t st, const DeviceInfo &dev);
@@ -188,7 +189,7 @@ cudaError_t launch_kv4_attention(const Kv4AttnArgs &a, int D, cudaStream_t st, c
 // kv4_sparse_attention: "requests" are tokens, block_table is their tables
 // [T, Hkv, max_blocks] and seq_lens the tokens in them.
 struct Kv4TableArgs : Kv4AttnArgs {
-    static constexpr bool kTail = false;
+    static constexpr bool kTail = false, kEven = true;
 };
 cudaError_t launch_kv4_sparse(const Kv4TableArgs &a, int D, cudaStream_t st, const DeviceInfo &dev);
 

@@ -5,7 +5,7 @@
 // token and key head is a segment, the tiles of all segments are split evenly
 // over the SMs, a tile is one bulk copy wherever its page lies.  Bound: memory,
 // as there.  Measured: 128 tokens over 2048 others each, pages of 16, 16 heads of 256
-// on 8: 104 us, 5.0 TB/s, 74% of the copy bandwidth; one such token 9.8 us (latency).
+// on 8: 104 us, 5.0 TB/s, 74% of the copy bandwidth; one such token 10.5 us (latency).
 // 301 tokens of one request, 32 heads of 128 on 8, 1088 each: 100 us, the pages in L2,
 // issue slots 65% and the ALU pipe 55% busy (the codes' logic).
 #include "kv4_stream.cuh"

@@ -190,9 +190,9 @@ struct Segment {
 };
 
 // EXTRA: units without a tile that a segment begins with, for what it costs beside
-// its tiles.
+// its tiles.  `unit`: it ends with as many as make it a multiple of that.
 template <int R, int EXTRA, class A>
-__device__ __forceinline__ void shape_segment(const A &a, int b, int r0, int G, Segment &s) {
+__device__ __forceinline__ void shape_segment(const A &a, int b, int r0, int G, int unit, Segment &s) {
     const int n = new_tokens(a, b);
     const int total = n * G;
     s.b = b;
@@ -218,6 +218,7 @@ __device__ __forceinline__ void shape_segment(const A &a, int b, int r0, int G, 
     s.ns = static_cast<int>(ns);
     s.low = static_cast<int>(low);
     s.nt = static_cast<int>(nt) + EXTRA;
+    if (unit > 1) s.nt = (s.nt + unit - 1) / unit * unit;
 }
 
 // Walks the segments in order: key heads of a row block, row blocks of a
@@ -228,7 +229,7 @@ struct Cursor {
     Segment s;
     int first;
     template <class A>
-    __device__ __forceinline__ void next(const A &a, int G) {
+    __device__ __forceinline__ void next(const A &a, int G, int unit) {
         first += s.nt;
         if (++s.h < a.Hkv) return;
         s.h = 0;
@@ -239,7 +240,7 @@ struct Cursor {
             while (b < a.requests && rows_of(a, b, G) == 0);
             if (b >= a.requests) return;  // past the last segment: not used
         }
-        shape_segment<R, EXTRA>(a, b, r0, G, s);
+        shape_segment<R, EXTRA>(a, b, r0, G, unit, s);
     }
     // (negative: none)
     __device__ __forceinline__ int tile(int u) const {
@@ -381,6 +382,54 @@ __global__ void __launch_bounds__(W * 32, 1) attn_stream_kernel(const A a, const
     if (!early) pdl_wait();
     if (A::kShared) pdl_launch_dependents();
 
+    // Where a CTA's warps are a team, a share that has the end of one segment and the
+    // start of another costs 4 to 8 us, and a part its reading by the last to arrive, 0.08
+    // (0.17 at D = 256); 16 tiles of a team about 1 (1.7).  So segments are made multiples
+    // of a unit, and a share is one unit: as many parts as the root of the mean segment's
+    // tiles x 0.75, where the two costs are least in sum; no more than there are teams.
+    // One token, 8 heads on 1, us without / with it: 8192 others (D = 128) 22 / 13.5, 4096
+    // (256) 37 / 15; three of 2240 (128) 24 / 12; 4 of 2048, 16 heads of 256 on 8, 15.5 /
+    // 12.8; one of 2048, where the shares ended with segments by chance, 9.8 / 10.5.
+    int unit = 1;
+    // (a token's tiles, of every key head and block of its rows)
+    auto tiles_of = [&](int b) -> int {
+        const int64_t len = a.seq_lens[b], cap = a.max_blocks << a.bs_log2;
+        return static_cast<int>(((len < 0 ? 0 : len < cap ? len : cap) + 15) >> 4);
+    };
+    const int blocks = (G + R - 1) / R;
+    if constexpr (TEAM > 1 && A::kEven) {
+        int most = 0;
+        float all = 0.f;
+        for (int b = a.requests > 1 ? tid : 0; b < a.requests; b += W * 32) {
+            const int n = max(tiles_of(b), 1);
+            most = max(most, n);
+            all += static_cast<float>(n);
+        }
+        if (a.requests > 1) {
+            float *const sums = reinterpret_cast<float *>(smem + L::sm);  // 2 W words, before its first use
+            most = __reduce_max_sync(0xffffffffu, most);
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1) all += __shfl_xor_sync(0xffffffffu, all, o);
+            if (lane == 0) sums[warp] = all, sums[W + warp] = __int_as_float(most);
+            __syncthreads();
+            all = lane < W ? sums[lane] : 0.f;
+            most = __reduce_max_sync(0xffffffffu, lane < W ? __float_as_int(sums[W + lane]) : 0);
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1) all += __shfl_xor_sync(0xffffffffu, all, o);
+        }
+        const int segments = a.requests * a.Hkv * blocks, teams = static_cast<int>(gridDim.x);
+        const float mean = __fdividef(all, static_cast<float>(a.requests));
+        float root;
+        asm("sqrt.approx.f32 %0, %1;" : "=f"(root) : "f"(0.75f * mean));
+        int parts = max(static_cast<int>(root), 1);
+        if (static_cast<float>(most) <= mean && segments <= teams) {  // all alike
+            parts = min(parts, teams / segments);
+            unit = (most + parts - 1) / parts;
+        } else if (2 * segments <= teams)  // (so many units at most: all / unit + segments)
+            unit = max(static_cast<int>(__fdividef(all * static_cast<float>(a.Hkv * blocks), static_cast<float>(teams - segments))) + 1,
+                       static_cast<int>(mean) / parts);
+    }
+
     // ---- tiles of the requests, their running sum
     {
         const int per = (a.requests + W * 32 - 1) / (W * 32);
@@ -391,12 +440,18 @@ __global__ void __launch_bounds__(W * 32, 1) attn_stream_kernel(const A a, const
                 asm volatile("prefetch.global.L1 [%0];" ::"l"(a.seq_lens + b));  // asked for beside cu_new
                 if (a.first_launch && blockIdx.x == 0) check_lengths(a, b);
             }
-            const int rows = rows_of(a, b, G);
             long long n = 0;
-            for (int r0 = 0; r0 < rows; r0 += R) {
-                Segment s;
-                shape_segment<R, EXTRA>(a, b, r0, G, s);
-                n += s.nt;
+            if constexpr (A::kEven) {
+                n = max(tiles_of(b), 1);
+                if (unit > 1) n = (static_cast<int>(n) + unit - 1) / unit * unit;
+                n *= blocks;
+            } else {
+                const int rows = rows_of(a, b, G);
+                for (int r0 = 0; r0 < rows; r0 += R) {
+                    Segment s;
+                    shape_segment<R, EXTRA>(a, b, r0, G, unit, s);
+                    n += s.nt;
+                }
             }
             cum[b + 1] = n * a.Hkv;
             sum += n * a.Hkv;
@@ -429,7 +484,9 @@ __global__ void __launch_bounds__(W * 32, 1) attn_stream_kernel(const A a, const
     // teams that take part: no more than there are tiles, so that none between
     // the first and the last of a shared segment is without a part of it
     const long long U = cum[a.requests];
-    const long long all_teams = static_cast<long long>(gridDim.x) * L::TEAMS, C = U < all_teams ? U : all_teams;
+    const long long all_teams = static_cast<long long>(gridDim.x) * L::TEAMS;
+    long long C = U < all_teams ? U : all_teams;
+    if (unit > 1 && U / unit < C) C = U / unit;
     // (neighbouring teams on different SMs: a small U fills them evenly)
     const int me = static_cast<int>(blockIdx.x) + static_cast<int>(gridDim.x) * (warp / TEAM);
     if (me >= C) {
@@ -451,7 +508,7 @@ __global__ void __launch_bounds__(W * 32, 1) attn_stream_kernel(const A a, const
         long long rest = u0 - cum[lo];
         int r0 = 0;
         while (true) {
-            shape_segment<R, EXTRA>(a, lo, r0, G, cur.s);
+            shape_segment<R, EXTRA>(a, lo, r0, G, unit, cur.s);
             if (rest < static_cast<long long>(cur.s.nt) * a.Hkv) break;
             rest -= static_cast<long long>(cur.s.nt) * a.Hkv;
             r0 += R;
@@ -472,7 +529,7 @@ __global__ void __launch_bounds__(W * 32, 1) attn_stream_kernel(const A a, const
         page = place = -1;
         if (pre_u >= mine) return;
         if (pre_u >= pre.first + pre.s.nt) {
-            do pre.next(a, G);
+            do pre.next(a, G, unit);
             while (pre_u >= pre.first + pre.s.nt);
             pages = pages_of(a, pre.s.b, pre.s.h);
         }
@@ -889,7 +946,7 @@ __global__ void __launch_bounds__(W * 32, 1) attn_stream_kernel(const A a, const
             }
             if (!last) {
                 Cursor<R, EXTRA> after = cur;
-                after.next(a, G);
+                after.next(a, G, unit);
                 if (tw >= TEAM - NT) build_q<L, D, SPLIT>(a, after.s, G, TEAM - 1 - tw, NT, team, par ^ 1, lane);
             }
             __syncthreads();
@@ -1000,7 +1057,7 @@ __global__ void __launch_bounds__(W * 32, 1) attn_stream_kernel(const A a, const
             }
         }
         if (last) break;
-        cur.next(a, G);
+        cur.next(a, G, unit);
         if (TEAM == 1) {
             __syncwarp();
             for (int n = 0; n < NT; ++n) build_q<L, D, SPLIT>(a, cur.s, G, n, NT, team, 0, lane);

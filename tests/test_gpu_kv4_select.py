@@ -250,6 +250,28 @@ def test_sparse_attention(Hq, Hkv, D, bs):
     assert w4.w4a16_check_device_error() == 6
 
 
+@pytest.mark.parametrize("T,Hq,Hkv,D", [(1, 8, 1, 128), (3, 8, 1, 256), (7, 24, 1, 64), (9, 20, 10, 64), (14, 28, 4, 128), (40, 8, 4, 64),
+                                        (30, 16, 8, 64)])
+@pytest.mark.parametrize("even", [True, False])
+def test_sparse_attention_with_rows_split_into_parts(T, Hq, Hkv, D, even):
+    # as many tiles for every token, or some of none and some of one beside long ones; fewer and
+    # more segments than CTAs
+    torch, w4 = cuda_or_skip()
+    rng = np.random.default_rng(T * D)
+    c = ref.Cache(40, Hkv, 16, D)
+    for slot in range(640):
+        lh.fill(c, rng, slot)
+    lens = np.full(T, 630) if even else np.where(rng.random(T) < 0.3, rng.integers(0, 3, T), rng.integers(3, 641, T))
+    tables = _tables(rng, c, T, 40, lens)
+    q = ref.bf16(rng.normal(0, 1, (T, Hq, D)))
+    i32 = dict(dtype=torch.int32, device="cuda")
+    x, raw = torch.tensor(q, device="cuda").to(torch.bfloat16), torch.tensor(c.raw, device="cuda")
+    scratch = w4.kv4_attention_scratch(Hq, Hkv, D)
+    want, tol = lh.sparse(q, c, tables, lens, D ** -0.5)
+    for _ in range(2):
+        lh.check(w4, w4.kv4_sparse_attention(x, raw, torch.tensor(tables, **i32), torch.tensor(lens, **i32), scratch), want, tol)
+
+
 def test_sparse_attention_of_more_tokens_than_a_launch_takes():
     torch, w4 = cuda_or_skip()
     rng = np.random.default_rng(8)
