@@ -179,17 +179,22 @@ struct Kv4AttnArgs {
     unsigned int inject;  // test-only injection flags (0 normally)
     static constexpr bool kShared = false;  // keys of a row in several stretches
     static constexpr bool kTail = true;     // rows that belong to no request are zeroed
-    static constexpr bool kEven = false;    // requests are of a length, as a rule
+    static constexpr bool kUnits = false;   // a share of few segments ends with its segment
 };
 constexpr int PROMPT_COUNTERS = 13056;  // byte offset in the scratch of the prompt kernel's two counters
 cudaError_t launch_kv4_prompt(const Kv4AttnArgs &a, int D, cudaStream_t st, const DeviceInfo &dev);
 int64_t kv4_attention_scratch(int Hq, int Hkv, int D);
 cudaError_t launch_kv4_attention(const Kv4AttnArgs &a, int D, cudaStream_t st, const DeviceInfo &dev);
+// The same attention with rows split otherwise: of kv4_prefix_attention over small caches.
+struct Kv4UnitArgs : Kv4AttnArgs {
+    static constexpr bool kUnits = true;
+};
+cudaError_t launch_kv4_attention(const Kv4UnitArgs &a, int D, cudaStream_t st, const DeviceInfo &dev);
 
 // kv4_sparse_attention: "requests" are tokens, block_table is their tables
 // [T, Hkv, max_blocks] and seq_lens the tokens in them.
 struct Kv4TableArgs : Kv4AttnArgs {
-    static constexpr bool kTail = false, kEven = true;
+    static constexpr bool kTail = false, kUnits = true;
 };
 cudaError_t launch_kv4_sparse(const Kv4TableArgs &a, int D, cudaStream_t st, const DeviceInfo &dev);
 

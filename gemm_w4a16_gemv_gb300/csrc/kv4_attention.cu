@@ -8,8 +8,11 @@ int64_t kv4_attention_scratch(int, int, int D) {
     return (COUNTER_BYTES + int64_t(MAX_CTAS) * 2 * warp_rows(D) * (D + 4) * 4 + 255) / 256 * 256;
 }
 
-cudaError_t launch_kv4_attention(const Kv4AttnArgs &args, int D, cudaStream_t st, const DeviceInfo &dev) {
-    Kv4AttnArgs a = args;
+namespace {
+
+template <class A>
+cudaError_t attend(const A &args, int D, cudaStream_t st, const DeviceInfo &dev) {
+    A a = args;
     const int G = a.Hq / a.Hkv;
     int64_t rows = (a.max_new < a.T ? a.max_new : a.T) * G;  // the most a request has
     const int64_t few = stream_rows(a.requests * a.Hkv, D, dev);
@@ -23,7 +26,7 @@ cudaError_t launch_kv4_attention(const Kv4AttnArgs &args, int D, cudaStream_t st
         // form for them: 64 requests, one of them a prompt, would take 201 us
         // instead of 124 in the form for 16 rows
         a.rows_above = a.requests > 1 ? static_cast<int>(few) : 0;
-        if (cudaError_t e = launch_kv4_prompt(a, D, st, dev)) return e;
+        if (cudaError_t e = launch_kv4_prompt(static_cast<const Kv4AttnArgs &>(a), D, st, dev)) return e;
         if (a.requests == 1) return cudaSuccess;
         a.first_launch = 0;
         a.rows_most = D == 256 ? 2 : D == 128 ? 4 : 8;
@@ -35,5 +38,10 @@ cudaError_t launch_kv4_attention(const Kv4AttnArgs &args, int D, cudaStream_t st
     }
     return stream(a, D, rows, st, dev);
 }
+
+}  // namespace
+
+cudaError_t launch_kv4_attention(const Kv4AttnArgs &a, int D, cudaStream_t st, const DeviceInfo &dev) { return attend(a, D, st, dev); }
+cudaError_t launch_kv4_attention(const Kv4UnitArgs &a, int D, cudaStream_t st, const DeviceInfo &dev) { return attend(a, D, st, dev); }
 
 }  // namespace w4

@@ -20,7 +20,7 @@
 // rest 22; the join 5.5; the rest between the launches.  16384 more shared tokens are 18 to
 // 23 us, 80% of the tensor cores' rate.  12 prompts of 101 to 700 tokens behind 6016:
 // 360 us, 1080 TFLOP/s (nothing shared: their rows fill the items by themselves); 4
-// samples behind 2048, which lie in L2, 18.6 us without sharing (40 with).  32 heads of
+// samples behind 2048, which lie in L2, 15.5 us without sharing (40 with).  32 heads of
 // 128 on 8, 7 groups of up to 30 requests of 1 to 4 new tokens: 125 us: the plan 8, the
 // shared parts 60 to 70, the rest 22, the join 5.
 #include "kv4_stream.cuh"
@@ -501,7 +501,7 @@ cudaError_t launch_kv4_prefix(const Kv4PrefixArgs &args, int D, cudaStream_t st,
     const int G = a.Hq / a.Hkv;
     // what lies in L2 after its first reading is not worth sharing
     if ((static_cast<int64_t>(a.requests) * a.max_blocks << a.bs_log2) * a.Hkv * kv4_tile_bytes(D) / KV4_TILE <= SMALL) {
-        if (cudaError_t e = launch_kv4_attention(a, D, st, dev)) return e;
+        if (cudaError_t e = launch_kv4_attention(Kv4UnitArgs{a}, D, st, dev)) return e;
         return launch(reinterpret_cast<const void *>(check_kernel), a, dim3(1), JOIN_THREADS, 0, st);
     }
     a.members = a.requests;

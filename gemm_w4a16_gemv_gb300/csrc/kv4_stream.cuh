@@ -389,7 +389,9 @@ __global__ void __launch_bounds__(W * 32, 1) attn_stream_kernel(const A a, const
     // tiles x 0.75, where the two costs are least in sum; no more than there are teams.
     // One token, 8 heads on 1, us without / with it: 8192 others (D = 128) 22 / 13.5, 4096
     // (256) 37 / 15; three of 2240 (128) 24 / 12; 4 of 2048, 16 heads of 256 on 8, 15.5 /
-    // 12.8; one of 2048, where the shares ended with segments by chance, 9.8 / 10.5.
+    // 12.8; one of 2048, where the shares ended with segments by chance, 9.8 / 10.5.  4
+    // requests of about 2100, one new token each, 18.4 / 15.5.  (kv4_attention itself keeps
+    // the split, and so the bits, that it had.)
     int unit = 1;
     // (a token's tiles, of every key head and block of its rows)
     auto tiles_of = [&](int b) -> int {
@@ -397,37 +399,54 @@ __global__ void __launch_bounds__(W * 32, 1) attn_stream_kernel(const A a, const
         return static_cast<int>(((len < 0 ? 0 : len < cap ? len : cap) + 15) >> 4);
     };
     const int blocks = (G + R - 1) / R;
-    if constexpr (TEAM > 1 && A::kEven) {
-        int most = 0;
+    if constexpr (TEAM > 1 && A::kUnits) {
+        int most = 0, segments = 0;
         float all = 0.f;
         for (int b = a.requests > 1 ? tid : 0; b < a.requests; b += W * 32) {
-            const int n = max(tiles_of(b), 1);
-            most = max(most, n);
-            all += static_cast<float>(n);
+            if constexpr (A::kTail) {
+                const int rows = rows_of(a, b, G);
+                for (int r0 = 0; r0 < rows; r0 += R) {
+                    Segment s;
+                    shape_segment<R, EXTRA>(a, b, r0, G, 1, s);
+                    most = max(most, s.nt);
+                    all += static_cast<float>(s.nt);
+                    ++segments;
+                }
+            } else {
+                const int n = max(tiles_of(b), 1);
+                most = max(most, n);
+                all += static_cast<float>(n * blocks);
+                segments += blocks;
+            }
         }
         if (a.requests > 1) {
-            float *const sums = reinterpret_cast<float *>(smem + L::sm);  // 2 W words, before its first use
+            float *const sums = reinterpret_cast<float *>(smem + L::sm);  // 3 W words, before its first use
+            segments = __reduce_add_sync(0xffffffffu, segments);
             most = __reduce_max_sync(0xffffffffu, most);
 #pragma unroll
             for (int o = 16; o > 0; o >>= 1) all += __shfl_xor_sync(0xffffffffu, all, o);
-            if (lane == 0) sums[warp] = all, sums[W + warp] = __int_as_float(most);
+            if (lane == 0) sums[warp] = all, sums[W + warp] = __int_as_float(most), sums[2 * W + warp] = __int_as_float(segments);
             __syncthreads();
+            segments = __reduce_add_sync(0xffffffffu, lane < W ? __float_as_int(sums[2 * W + lane]) : 0);
             all = lane < W ? sums[lane] : 0.f;
             most = __reduce_max_sync(0xffffffffu, lane < W ? __float_as_int(sums[W + lane]) : 0);
 #pragma unroll
             for (int o = 16; o > 0; o >>= 1) all += __shfl_xor_sync(0xffffffffu, all, o);
         }
-        const int segments = a.requests * a.Hkv * blocks, teams = static_cast<int>(gridDim.x);
-        const float mean = __fdividef(all, static_cast<float>(a.requests));
+        const float mean = __fdividef(all, static_cast<float>(max(segments, 1)));
+        const int teams = static_cast<int>(gridDim.x);
+        segments *= a.Hkv;
         float root;
         asm("sqrt.approx.f32 %0, %1;" : "=f"(root) : "f"(0.75f * mean));
-        int parts = max(static_cast<int>(root), 1);
-        if (static_cast<float>(most) <= mean && segments <= teams) {  // all alike
-            parts = min(parts, teams / segments);
-            unit = (most + parts - 1) / parts;
-        } else if (2 * segments <= teams)  // (so many units at most: all / unit + segments)
-            unit = max(static_cast<int>(__fdividef(all * static_cast<float>(a.Hkv * blocks), static_cast<float>(teams - segments))) + 1,
-                       static_cast<int>(mean) / parts);
+        const int parts = max(static_cast<int>(root), 1);
+        // all alike, or so few that there are some to split the longer ones
+        if (segments > 0 && segments <= teams && (static_cast<float>(most) <= mean || 2 * segments <= teams)) {
+            // two units that give no more of them than teams: by the longest segment, and as
+            // all / unit + segments are more than there can be
+            unit = (most + teams / segments - 1) / (teams / segments);
+            if (segments < teams) unit = min(unit, static_cast<int>(__fdividef(all * static_cast<float>(a.Hkv), static_cast<float>(teams - segments))) + 1);
+            unit = max(unit, (static_cast<int>(mean) + parts - 1) / parts);
+        }
     }
 
     // ---- tiles of the requests, their running sum
@@ -441,7 +460,7 @@ __global__ void __launch_bounds__(W * 32, 1) attn_stream_kernel(const A a, const
                 if (a.first_launch && blockIdx.x == 0) check_lengths(a, b);
             }
             long long n = 0;
-            if constexpr (A::kEven) {
+            if constexpr (A::kUnits && !A::kTail) {
                 n = max(tiles_of(b), 1);
                 if (unit > 1) n = (static_cast<int>(n) + unit - 1) / unit * unit;
                 n *= blocks;
@@ -1103,7 +1122,10 @@ template <int D, int NT, int W, bool SPLIT, class A>
 cudaError_t launch_teams(const A &a, int64_t rows, cudaStream_t st, const DeviceInfo &dev) {
     constexpr int R = Stream<D, NT, W, 1, SPLIT>::R;
     const int64_t segments = a.requests * a.Hkv * ((rows + R - 1) / R);
-    if (segments * TEAM_RATIO >= static_cast<int64_t>(dev.num_sms) * W) return launch_stream<A, D, NT, W, 1, SPLIT>(a, st, dev);
+    if (segments * TEAM_RATIO >= static_cast<int64_t>(dev.num_sms) * W) {
+        if constexpr (A::kUnits && A::kTail) return launch_stream<Kv4AttnArgs, D, NT, W, 1, SPLIT>(a, st, dev);
+        else return launch_stream<A, D, NT, W, 1, SPLIT>(a, st, dev);
+    }
     return launch_stream<A, D, NT, W, W, SPLIT>(a, st, dev);
 }
 
