@@ -415,7 +415,7 @@ __global__ void __launch_bounds__(W * 32, 1) attn_stream_kernel(const A a, const
             } else {
                 const int n = max(tiles_of(b), 1);
                 most = max(most, n);
-                all += static_cast<float>(n * blocks);
+                all += static_cast<float>(n) * static_cast<float>(blocks);
                 segments += blocks;
             }
         }
