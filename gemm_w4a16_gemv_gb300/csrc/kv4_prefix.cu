@@ -402,9 +402,10 @@ __global__ void __launch_bounds__(JOIN_THREADS, 8) join_kernel(const Kv4PrefixAr
                 }
             }
         };
-        // n of the arrays' parts from `at` on, or what teams left of the first one (w: what its place holds)
+        // n of the arrays' parts from `at` on, or what teams left of the first one (w: what its place
+        // holds; a sum that is NaN is a part like any other)
         auto add_at = [&](float2 w, int64_t at, int n, int64_t step) {
-            if (w.y >= 0.f) {
+            if (!(w.y < 0.f)) {
                 add(n, [&](int k) { return a.weights + at + k * step; }, [&](int k) { return a.values + (at + k * step) * D + d; });
                 return;
             }
