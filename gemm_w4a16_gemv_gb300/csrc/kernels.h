@@ -182,6 +182,7 @@ struct Kv4AttnArgs {
     static constexpr bool kUnits = false;   // a share of few segments ends with its segment
 };
 constexpr int PROMPT_COUNTERS = 13056;  // byte offset in the scratch of the prompt kernel's two counters
+constexpr int PLAN_READY = 13184;       // of a word that is 1 from the end of kv4_prefix_attention's plan to that of its join
 cudaError_t launch_kv4_prompt(const Kv4AttnArgs &a, int D, cudaStream_t st, const DeviceInfo &dev);
 int64_t kv4_attention_scratch(int Hq, int Hkv, int D);
 cudaError_t launch_kv4_attention(const Kv4AttnArgs &a, int D, cudaStream_t st, const DeviceInfo &dev);

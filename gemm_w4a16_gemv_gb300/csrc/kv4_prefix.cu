@@ -342,6 +342,9 @@ __global__ void __launch_bounds__(PLAN_THREADS) plan_kernel(const Kv4PrefixArgs 
         }
         a.plan[a.groups + b] = s;
     }
+    // for kernels that read it without waiting for this one's end
+    __syncthreads();
+    if (tid == 0) store_release(reinterpret_cast<unsigned int *>(a.scratch + PLAN_READY), 1);
 }
 
 // Four dimensions of a row a thread, JOIN_THREADS of a token's Hq D / 4 a CTA, which
@@ -352,6 +355,7 @@ __global__ void __launch_bounds__(JOIN_THREADS, 8) join_kernel(const Kv4PrefixAr
     const int at = blockIdx.y * JOIN_THREADS + threadIdx.x;
     pdl_launch_dependents();
     pdl_wait();
+    if (blockIdx.x == 0 && at == 0) *reinterpret_cast<unsigned int *>(a.scratch + PLAN_READY) = 0;  // no kernel looks at it any more
     const int shares = a.counts[1];
     const int64_t tokens = *a.joined;
     const Kv4Share front = a.shares[0];  // (asked for beside their number)

@@ -456,8 +456,8 @@ __global__ void __launch_bounds__(THREADS, 1) attn_prompt_kernel(const Args a) {
         fence_barrier_init();
     }
     if (warp == 12) tmem_take<PAIR>(&bar.tmem);
-    // (kv4_prefix_attention's next kernel does not wait for this one's results, but
-    // for what this one waits for)
+    // (kv4_prefix_attention's next kernel does not need this one's results, but the plan,
+    // which this one waits for: it begins when that is complete)
     if (!Args::kShared) pdl_launch_dependents();
     pdl_wait();
     if (Args::kShared) pdl_launch_dependents();

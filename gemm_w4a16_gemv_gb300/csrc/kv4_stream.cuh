@@ -67,8 +67,8 @@ namespace {
 constexpr int MAX_CTAS = 160;         // scratch is sized for this many
 constexpr int MAX_WARPS = 20;         // of a CTA
 constexpr int MAX_TEAMS = MAX_CTAS * MAX_WARPS;
-constexpr int COUNTER_BYTES = 13312;  // arrival counters and the prompt kernel's two
-static_assert(MAX_TEAMS * 4 <= PROMPT_COUNTERS && PROMPT_COUNTERS + 8 <= COUNTER_BYTES, "counters");
+constexpr int COUNTER_BYTES = 13312;  // arrival counters, the prompt kernel's two, the word that tells of a plan
+static_assert(MAX_TEAMS * 4 <= PROMPT_COUNTERS && PROMPT_COUNTERS + 8 <= PLAN_READY && PLAN_READY + 4 <= COUNTER_BYTES, "counters");
 // Partial results that two slots per team can need: warps x rows of an instance.
 constexpr int warp_rows(int D) { return D == 256 ? 128 : D == 128 ? 192 : 256; }
 constexpr int TEAM_RATIO = 5;         // warps to a segment up to which a warp is a team of its own
@@ -372,14 +372,25 @@ __global__ void __launch_bounds__(W * 32, 1) attn_stream_kernel(const A a, const
     if (lane == 0)
         for (int i = 0; i < depth; ++i) mbar_init(&bars[i], 1);
     fence_barrier_init();
-    // `early`: the kernel before this one is not what this one needs; it began when
-    // that was there, and lets this one begin only then.  So this one takes the SMs as
-    // they become free, and waits for the other at its end, for the sake of the kernel
-    // after both.
+    // `early`: this kernel needs nothing of the one before it, but the plan and the call's
+    // arguments as that one does, which began when the plan was complete and let this one
+    // begin only then.  So this one takes the SMs as they become free, and waits for the
+    // other at its end, for the sake of the kernel after both.  That it began is no promise
+    // that it sees what was written: that rests on the word at PLAN_READY, which the plan's
+    // CTA releases after the plan and after it has waited for all kernels before the call.
+    // A CTA that acquires it sees what that CTA saw and wrote (its bulk copies too, behind
+    // the fence); one that does not find it waits as any kernel does.  (Waiting in any case:
+    // 128 requests behind 32768 tokens 117 -> 122.5 us, 7 groups of up to 30 125 -> 130.5.)
     bool early = false;
     if constexpr (A::kShared) early = a.early;
     if (!A::kShared) pdl_launch_dependents();
     if (!early) pdl_wait();
+    else {
+        const bool there =
+            __syncthreads_or(tid == 0 && load_acquire(reinterpret_cast<const unsigned int *>(a.scratch + PLAN_READY)) != 0);
+        if (!there) pdl_wait();
+        fence_proxy_async_global();
+    }
     if (A::kShared) pdl_launch_dependents();
 
     // Where a CTA's warps are a team, a share that has the end of one segment and the

@@ -83,3 +83,24 @@ def test_a_key_that_is_no_number(name, where):
     assert torch.equal(out.isnan(), _plain(w4, x, most).isnan())
     assert out.isnan().all(-1).cpu().numpy()[~rows].all()
     _check_rows(out, want, tol, rows)
+
+
+@pytest.mark.parametrize("name", SHARED)
+def test_scratch_is_left_fit_for_the_next_call(name):
+    # counters, and the word that tells of a plan; results as from a fresh one
+    torch, w4 = cuda_or_skip()
+    groups, Hq, Hkv, D, most, widest = SHARED[name]
+    dev, host = lh.grouped(torch, groups, Hq, Hkv, D, 16, D + len(groups))
+    scratch = lh.scratch(w4, dev)
+    first = _run(w4, dev, scratch=scratch, max_new=most, max_group=widest)
+    for _ in range(20):
+        assert torch.equal(first, _run(w4, dev, scratch=scratch, max_new=most, max_group=widest))
+    torch.cuda.synchronize()
+    assert not scratch[:13312].any()
+    # behind a call of fewer tokens, whose plan and parts lie elsewhere in the scratch
+    few = dict(dev, q=dev["q"][:2].contiguous(), cu_new=dev["cu_new"].clamp(max=2))
+    _run(w4, few, scratch=scratch, max_new=most, max_group=widest)
+    torch.cuda.synchronize()
+    w4.w4a16_check_device_error()
+    assert not scratch[:13312].any()
+    assert torch.equal(first, _run(w4, dev, scratch=scratch, max_new=most, max_group=widest))
