@@ -721,7 +721,7 @@ __global__ void __launch_bounds__(W * 32, (NB == 1 ? 16 : 12) / W) piece_kernel(
                     x0 = now.id[k] < 0 ? -INFINITY : __fmul_rn(x0, unit[b * COLUMNS + 2 * q]);
                     x1 = now.id[k] < 0 ? -INFINITY : __fmul_rn(x1, unit[b * COLUMNS + 2 * q + 1]);
                     if (lg >= 1) x0 = fmaxf(x0, x1);
-                    else x0 = fmaxf(x0, -INFINITY), x1 = fmaxf(x1, -INFINITY);  // (NaN: the lowest)
+                    x0 = fmaxf(x0, -INFINITY), x1 = fmaxf(x1, -INFINITY);  // (NaN, of all heads where these are several: the lowest)
                     if (lg >= 2) x0 = fmaxf(x0, __shfl_xor_sync(0xffffffffu, x0, 1));
                     if (lg >= 3) x0 = fmaxf(x0, __shfl_xor_sync(0xffffffffu, x0, 2));
                     uint32_t *const to = keys + (b * (COLUMNS >> lg) + mine) * width + page;
