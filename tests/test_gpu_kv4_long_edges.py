@@ -104,3 +104,71 @@ def test_scratch_is_left_fit_for_the_next_call(name):
     w4.w4a16_check_device_error()
     assert not scratch[:13312].any()
     assert torch.equal(first, _run(w4, dev, scratch=scratch, max_new=most, max_group=widest))
+
+
+def _idle_and_short(torch, active, idle, Hq, Hkv, D, seed):
+    """A group whose first requests have no new tokens, and tables and lengths of theirs that are no longer
+    anything; one whose context ends inside the prefix that is said to be shared by 640 tokens."""
+    members = [(0, 0)] * idle + [(1 + i % 40, 1) for i in range(active)]
+    dev, host = lh.grouped(torch, [(640, members), (0, [(9, 1), (3, 2)])], Hq, Hkv, D, 16, seed)
+    q, c, table, ends, cu = host
+    table, ends = table.copy(), list(ends)
+    ends[idle + 1] = 422            # 421 tokens before the step: 416 are shared
+    junk = np.random.default_rng(seed).choice([-1, 10 ** 8, c.blocks, -2 ** 31], (idle, table.shape[1]))
+    i32 = dict(dtype=torch.int32, device="cuda")
+    dev["seq_lens"] = torch.tensor([10 ** 9 if b % 2 else -7 for b in range(idle)] + ends[idle:], **i32)
+    dev["block_table"][:idle] = torch.tensor(junk, **i32)
+    return dev, (q, c, table, ends, cu), idle
+
+
+@pytest.mark.parametrize("active,Hq,Hkv,D", [(12, 8, 8, 64), (6, 8, 2, 128), (7, 16, 8, 256), (50, 8, 2, 128), (40, 16, 8, 256), (90, 8, 2, 64)])
+@pytest.mark.parametrize("said", [640, 10 ** 9])
+def test_idle_requests_first_and_a_context_that_ends_inside_the_prefix(active, Hq, Hkv, D, said):
+    # few rows, streamed, and many, on the tensor cores
+    torch, w4 = cuda_or_skip()
+    dev, host, idle = _idle_and_short(torch, active, 3, Hq, Hkv, D, D + active)
+    dev["prefix_lens"][0] = said
+    if said > 640:
+        # the tables agree for ever: one context for all, and their own tokens too
+        i32 = dict(dtype=torch.int32, device="cuda")
+        q, c, table, ends, cu = host
+        rows = slice(idle, idle + active)
+        table[rows] = table[idle]
+        ends[rows] = [min(e, ends[idle]) for e in ends[rows]]
+        dev["block_table"][rows], dev["seq_lens"][rows] = torch.tensor(table[rows], **i32), torch.tensor(ends[rows], **i32)
+    want, tol = ref.attention(*host, D ** -0.5)
+    scratch = lh.scratch(w4, dev)
+    out = _run(w4, dev, scratch=scratch, max_new=2, max_group=active)
+    lh.check(w4, out, want, tol)
+    # shared it is, and read by the first request with new tokens: the others' entries are not looked at
+    dev["block_table"][idle + 1:idle + active, :416 // 16] = -1
+    assert torch.equal(out, _run(w4, dev, scratch=scratch, max_new=2, max_group=active))
+    torch.cuda.synchronize()
+    assert w4.w4a16_check_device_error() == 0
+
+
+# numbers that are out of range, and the requests that they concern
+BAD = [("cu_groups", {2: 9000}, []), ("cu_groups", {0: -3}, []), ("cu_groups", {1: 10 ** 9}, []), ("prefix_lens", {0: -5}, []),
+       ("cu_new", {-1: 70000}, [-1]), ("seq_lens", {-1: 10 ** 6}, [-1]), ("seq_lens", {0: -4}, [0]), ("seq_lens", {5: 2 ** 31 - 1}, [5])]
+
+
+@pytest.mark.parametrize("active,Hq,Hkv,D", [(12, 8, 8, 64), (6, 8, 2, 128), (50, 8, 2, 128), (40, 16, 8, 256)])
+def test_requests_beside_numbers_out_of_range(active, Hq, Hkv, D):
+    # every row of the others is right
+    torch, w4 = cuda_or_skip()
+    groups = [(320, [(1 + i % 40, 1) for i in range(active)]), (48, [(9, 1), (3, 2)])]
+    dev, host = lh.grouped(torch, groups, Hq, Hkv, D, 16, D + active)
+    want, tol = ref.attention(*host, D ** -0.5)
+    cu = host[4]
+    for name, values, concerned in BAD:
+        x = dict(dev, **{name: dev[name].clone()})
+        for i, v in values.items():
+            x[name][i] = v
+        out = _run(w4, x, max_new=2, max_group=active)
+        torch.cuda.synchronize()
+        assert w4.w4a16_check_device_error() == 6, (name, values)
+        rows = np.ones(len(want), bool)
+        for b in concerned:
+            b %= len(cu) - 1
+            rows[cu[b]:cu[b + 1]] = False
+        _check_rows(out, want, tol, rows)
