@@ -240,7 +240,7 @@ struct Kv4PrefixArgs : Kv4SharedArgs {
     int32_t *piece_of;    // [members]
     int groups, members;  // members: the call's requests
     int most_pieces;      // there is room for
-    int64_t places, max_group;
+    int64_t max_group;
     // rows from which a shared stretch, a request goes to the tensor cores; rows of an
     // item there; items that run at once; cost of 16 streamed rows in eighths of an item's
     int least_shared, least_own, item_rows, workers, stream_cost;

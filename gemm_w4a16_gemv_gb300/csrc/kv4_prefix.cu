@@ -495,7 +495,6 @@ int64_t kv4_prefix_scratch(int64_t T, int requests, int groups, int Hq, int Hkv,
         a->joined = reinterpret_cast<int64_t *>(p + joined);
         a->both_partials[0] = reinterpret_cast<float *>(p + COUNTER_BYTES);
         a->both_partials[1] = reinterpret_cast<float *>(p + partials);
-        a->places = places;
         a->most_pieces = most_pieces;
     }
     return at;
