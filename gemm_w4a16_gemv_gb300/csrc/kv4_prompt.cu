@@ -531,7 +531,7 @@ __global__ void __launch_bounds__(THREADS, 1) attn_prompt_kernel(const Args a) {
     };
     // until the products of so many key tiles are done
     auto finish = [&](int g) {
-        if (g > 0) wait_for(&bar.vfree[(g - 1) & 1], ((g - 1) >> 1) & 1, nullptr);
+        if (g > 0) wait_for(&bar.vfree[(g - 1) % 2], ((g - 1) / 2) & 1, nullptr);
     };
 
     if (warp < 4) {
@@ -673,7 +673,7 @@ __global__ void __launch_bounds__(THREADS, 1) attn_prompt_kernel(const Args a) {
                 if (__any_sync(0xffffffffu, m != M)) {
                     l *= scaled;
                     if (i > 0) {  // O holds the earlier tiles once their product is done
-                        wait_for(&bar.vfree[(g - 1) & 1], ((g - 1) >> 1) & 1, a.status);
+                        wait_for(&bar.vfree[(g - 1) % 2], ((g - 1) / 2) & 1, a.status);
                         tc_fence_after();
 #pragma unroll 1
                         for (int c = 0; c < D / 32; ++c) {
@@ -692,7 +692,7 @@ __global__ void __launch_bounds__(THREADS, 1) attn_prompt_kernel(const Args a) {
                 tc_fence_before();
                 warp_arrive<PAIR>(&bar.pfull[g & 1], lane);
             }
-            wait_for(&bar.vfree[(g - 1) & 1], ((g - 1) >> 1) & 1, a.status);
+            wait_for(&bar.vfree[(g - 1) % 2], ((g - 1) / 2) & 1, a.status);
             tc_fence_after();
             const float inv = l == 0.f ? 0.f : 1.f / l;
             const bool on = rank * ROWS + r < cur.rows;
@@ -793,7 +793,7 @@ __global__ void __launch_bounds__(THREADS, 1) attn_prompt_kernel(const Args a) {
         const int part = shared ? HALF * step : 16 * 128;           // of part 1,
         const int next_buf = is_v ? L::V_GROUPS * SUB : G64 * L::K_SUB;  // of the other buffer
         unsigned char *const dst = smem + (is_v ? L::v : L::k) + row * 128;
-        uint64_t *const full = is_v ? bar.vfull : bar.kfull;
+        uint64_t *const full = is_v ? bar.vfull : bar.kfull, *const empty = is_v ? bar.vfree : bar.kfree;
         const unsigned char *const codes = a.cache + (is_v ? 8 * D : 0) + token * 32 + half * 16;
         const unsigned char *const params = a.cache + (is_v ? 17 * D : 16 * D);
         const int shift = a.bs_log2 - 4;                  // cache tiles of a page and head
@@ -885,12 +885,12 @@ __global__ void __launch_bounds__(THREADS, 1) attn_prompt_kernel(const Args a) {
                 }
                 if (!is_v) {
                     // (that the operands of two tiles before have been used shows the same)
-                    if (gi >= BUFS) wait_for(&bar.kfree[buf], (gi / BUFS - 1) & 1, a.status);
+                    if (gi >= BUFS) wait_for(&empty[buf], (gi / BUFS - 1) & 1, a.status);
                     if (lane < 2) meta.k_factor[c] = pow2(lane ? e1 : e0);
                 }
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&bar.known[gi % METAS]);
-                if (is_v && gi >= BUFS) wait_for(&bar.vfree[(gi - BUFS) & 1], ((gi - BUFS) >> 1) & 1, a.status);
+                if (is_v && gi >= BUFS) wait_for(&empty[(gi + 2 - BUFS) % 2], ((gi + 2 - BUFS) / 2 - 1) & 1, a.status);
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
                     const float up = pow2(-(h && !shared ? e1 : e0));
@@ -938,7 +938,7 @@ __global__ void __launch_bounds__(THREADS, 1) attn_prompt_kernel(const Args a) {
             for (int k = 0; k < KEYS / 16; ++k)
                 product_tmem<PAIR>(tmem, tmem + COL_S + (gi & 1) * KEYS + 8 * k, desc_sw128_mn(vb + k * 2048, SUB), IDESC_PV,
                                    !(first && k == 0));
-            commit<PAIR>(&bar.vfree[gi & 1]);
+            commit<PAIR>(&bar.vfree[gi % 2]);
         };
         auto announce = [&](int k, int index) {
             if (lane == 0) {
