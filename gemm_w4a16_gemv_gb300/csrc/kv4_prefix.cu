@@ -17,10 +17,11 @@
 // where it has few.  16 heads of 256 on 8: 128 requests behind 32768 tokens, 1 to 2000
 // of their own, 117 us (each for itself: 790): the plan 8; the shared part 62, of which
 // 11 until the first scores are there, 1.55 a key tile (the tensor pipe 1.0), 4 its end; the
-// rest 22; the join 5.5; the rest between the launches.  16384 more shared tokens are 18 to
-// 23 us, 80% of the tensor cores' rate.  12 prompts of 101 to 700 tokens behind 6016:
-// 360 us, 1080 TFLOP/s (nothing shared: their rows fill the items by themselves); 4
-// samples behind 2048, which lie in L2, 15.5 us without sharing (40 with).  32 heads of
+// rest 22; the join 5.5; the rest between the launches.  With one token of their own, 16384
+// more shared tokens are 30 us from 16384 to 32768 and 23 beyond (1500 TFLOP/s, 79% of the
+// tensor cores' rate).  12 prompts of 101 to 700 tokens behind 6016: 362 us, 1080 TFLOP/s
+// (nothing shared: their rows fill the items by themselves); 4 samples behind 2048, which lie
+// in L2, 15.3 us without sharing, 34 with it (SMALL goes by the table's width).  32 heads of
 // 128 on 8, 7 groups of up to 30 requests of 1 to 4 new tokens: 125 us: the plan 8, the
 // shared parts 60 to 70, the rest 22, the join 5.
 #include "kv4_stream.cuh"

@@ -49,9 +49,10 @@ __device__ __forceinline__ void fma_f16(uint32_t x, uint32_t s, float k, float &
 // one fused multiply-add, exact:
 //   (1024 + c) s - (1024 + z) s   or   (64 + c) s - (64 + z) s,
 // and two tokens enter the extremes with one comparison each way.
-// Bound: instructions.  65519 tokens of 8 heads of 256, pages of 64: 29.7 us, 2.7 TB/s;
-// the ALU pipe 63% busy, issue slots 66%, the loads' latency the rest.  (16 elements a
-// lane, so that half as many instructions go to the scales: 32 us, for its registers.)
+// Bound: instructions (five a code) and the loads' latency, about half of the time each.
+// 65519 tokens of 8 heads of 256, pages of 64: 29.7 us, 2.7 TB/s; the ALU pipe 64% and the
+// issue slots 67% busy, 38% of the warps that an SM holds active.  (16 elements a lane, so
+// that half as many instructions go to the scales: 32 us, for its registers.)
 template <int D>
 __global__ void __launch_bounds__(BOUNDS_WARPS * 32) bounds_kernel(const Kv4BoundsArgs a, const int slots) {
     constexpr int LANES = D / 8, SIDE = 32 / LANES, HALF = 8 / SIDE, TB = kv4_tile_bytes(D);

@@ -534,11 +534,23 @@ int kv4_attention(const uint16_t *q, int64_t q_stride, const uint8_t *cache,
  *                 sharing is left out or unspecified.
  *   max_new, max_group : upper bounds of the new tokens of a request, of a group;
  *                 they choose between kernels, as kv4_attention's max_new does
+ *   max_blocks  : where all pages that the tables could name are 64 MB or less,
+ *                 nothing is shared (they stay in L2): a table no wider than the
+ *                 step needs is of use
  *   scratch     : at least kv4_prefix_attention_scratch_bytes(T, requests,
  *                 groups, Hq, Hkv, D) bytes (0 where one of these is not
  *                 supported), as kv4_attention's otherwise; a scratch for more
- *                 tokens, requests or groups serves
- * The other arguments are kv4_attention's, and so is what the kernels round.
+ *                 tokens, requests or groups serves.  It is large: two results
+ *                 in binary32 for each row, up to 81920 more, and twice
+ *                 kv4_attention's (174 MB for 128 tokens of 16 heads of 256 on
+ *                 8, 653 MB for 16384 of 32 of 128).
+ * The other arguments are kv4_attention's.  A row of q that is no number, or a
+ * score that is none, gives what it gives there.
+ * Rounding is that of kv4_attention's kernels, but not always of the one that
+ * the row would take there: a stretch that many rows share goes through the
+ * tensor cores, which round K and V once to binary16, also where each request
+ * has one new token and kv4_attention would take them as they are.  Which
+ * stretches these are goes by the step's lengths.
  * 1 <= groups <= requests <= 4096, T * Hq <= 2^30; T = 0 launches nothing.
  */
 int64_t kv4_prefix_attention_scratch_bytes(int64_t T, int requests, int groups,
